@@ -28,6 +28,11 @@ from ._native import (  # noqa: F401
     ss_debug_fwd_kernels,
     ss_debug_inject,
     ss_last_device_error,
+    ss_linattn_bwd,
+    ss_linattn_bwd_workspace_bytes,
+    ss_linattn_fwd,
+    ss_linattn_step,
+    ss_linattn_workspace_bytes,
     ss_scan_bwd,
     ss_scan_bwd_workspace_bytes,
     ss_scan_fwd,
@@ -38,5 +43,7 @@ from ._native import (  # noqa: F401
     ss_scan_fwd_zoh,
     ss_scan_step,
     ss_scan_workspace_bytes,
+    ss_state_load8,
+    ss_state_store8,
     ss_status_string,
 )

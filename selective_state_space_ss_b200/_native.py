@@ -25,7 +25,9 @@ EXPORTED = ("ss_scan_fwd", "ss_scan_workspace_bytes", "ss_status_string",
             "ss_last_device_error", "ss_debug_inject", "ss_scan_fwd_noalloc",
             "ss_scan_fwd_from_state", "ss_scan_step", "ss_scan_fwd_conv", "ss_scan_fwd_zoh",
             "ss_scan_bwd", "ss_scan_bwd_workspace_bytes", "ss_scan_fwd_train",
-            "ss_debug_pointwise", "ss_debug_fwd_kernels")
+            "ss_debug_pointwise", "ss_debug_fwd_kernels",
+            "ss_linattn_fwd", "ss_linattn_workspace_bytes", "ss_linattn_bwd",
+            "ss_linattn_bwd_workspace_bytes", "ss_linattn_step", "ss_state_store8", "ss_state_load8")
 
 # bytes of the library's static scratch array (SS_NOALLOC_SCRATCH_BYTES)
 SS_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -36,6 +38,12 @@ SS_NOALLOC_SCRATCH_BYTES = 4 << 20
 # pointwise functions ss_debug_pointwise evaluates (include/ss_scan_debug.h)
 (SS_PW_SOFTPLUS, SS_PW_SILU, SS_PW_SOFTPLUS2, SS_PW_SILU2, SS_PW_EXP2_NEG_FMA, SS_PW_RCP_1_2,
  SS_PW_EX2) = range(7)
+
+
+class SSHeads(ctypes.Structure):
+    """ss_heads (include/ss_linattn.h): a [batch, seqlen, heads, d] tensor with strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class SSError(RuntimeError):
@@ -96,6 +104,19 @@ def load_library():
         lib.ss_debug_pointwise.restype = ci
         lib.ss_debug_fwd_kernels.argtypes = [i64, i64, i64, ci, ci]
         lib.ss_debug_fwd_kernels.restype = ci
+        hp, cf, sz = ctypes.POINTER(SSHeads), ctypes.c_float, ctypes.c_size_t
+        sizes = [i64, i64, ci, ci, ci, ci, ci]  # batch, seqlen, heads, qk_heads, dk, dv, dtype
+        lib.ss_linattn_fwd.argtypes = [hp, hp, hp, hp, cf, vp, vp, vp, vp, *sizes, vp, sz, vp]
+        lib.ss_linattn_bwd.argtypes = [hp, hp, hp, hp, hp, cf, vp, vp, vp, vp, vp, vp, vp, vp, *sizes,
+                                       vp, sz, vp]
+        for f in (lib.ss_linattn_workspace_bytes, lib.ss_linattn_bwd_workspace_bytes):
+            f.argtypes, f.restype = sizes, sz
+        lib.ss_linattn_step.argtypes = [hp, hp, hp, hp, cf, vp, i64, vp, vp, i64, ci, ci, ci, ci, ci, vp]
+        lib.ss_state_store8.argtypes = [vp, vp, vp, i64, vp, i64, i64, ci, vp]
+        lib.ss_state_load8.argtypes = [vp, vp, i64, vp, vp, i64, i64, ci, vp]
+        for f in (lib.ss_linattn_fwd, lib.ss_linattn_bwd, lib.ss_linattn_step, lib.ss_state_store8,
+                  lib.ss_state_load8):
+            f.restype = ci
         _lib = lib
         return lib
 
@@ -416,3 +437,242 @@ def ss_scan_fwd_noalloc(u, delta, A, B, C, D=None, z=None, delta_bias=None, soft
     if st != SS_OK:
         raise SSError(st, "ss_scan_fwd_noalloc")
     return y_out, last_state_out
+
+
+# ---- linear attention with a decay per head, and the 8-bit state pool (include/ss_linattn.h)
+
+
+def _heads(name, t, device, dtype, shape):
+    """A strided [batch, seqlen, heads, d] operand (log decays: without the last axis); a
+    missing seqlen axis (the single-token step) has stride 0."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} is not {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    return SSHeads(t.data_ptr(), 0, 0, 0)
+
+
+def _heads4(name, t, device, dtype, shape):
+    h = _heads(name, t, device, dtype, shape)
+    if len(shape) == 4 and shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    h.batch_stride, h.token_stride, h.head_stride = t.stride(0), t.stride(1), t.stride(2)
+    return h
+
+
+def _heads3(name, t, device, dtype, shape):
+    h = _heads(name, t, device, dtype, shape)
+    if len(shape) == 3 and shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    h.batch_stride, h.head_stride = t.stride(0), t.stride(1)
+    return h
+
+
+def _cuda_device(name, t, what):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{what} runs on CUDA tensors only (no CPU fallback): {name}")
+    return t.device
+
+
+def _linattn_operands(what, q, k, v, log_decay):
+    device = _cuda_device("q", q, what)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and k must be [batch, L, qk_heads, dk] and v [batch, L, heads, dv]")
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"q: dtype {q.dtype} is not float32 or bfloat16")
+    batch, L, qk_heads, dk = q.shape
+    heads, dv = v.shape[2:]
+    ops = [_heads4("q", q, device, q.dtype, (batch, L, qk_heads, dk)),
+           _heads4("k", k, device, q.dtype, (batch, L, qk_heads, dk)),
+           _heads4("v", v, device, q.dtype, (batch, L, heads, dv)),
+           _heads4("log_decay", log_decay, device, q.dtype, (batch, L, heads))]
+    dt = SS_F32 if q.dtype == torch.float32 else SS_BF16
+    return device, ops, (batch, L, heads, qk_heads, dk, dv, dt)
+
+
+def _linattn_need(fn, sizes):
+    n = fn(*sizes)
+    if n == ctypes.c_size_t(-1).value:
+        _, _, heads, qk_heads, dk, dv, _ = sizes
+        unsupported = min(sizes[:6]) >= 1 and heads % qk_heads == 0 and max(dk, dv) > 128
+        raise SSError(SS_ERR_UNSUPPORTED if unsupported else SS_ERR_INVALID_ARG, fn.__name__)
+    return n
+
+
+def ss_linattn_workspace_bytes(batch, seqlen, heads, qk_heads, dk, dv, in_dtype) -> int:
+    return _linattn_need(load_library().ss_linattn_workspace_bytes,
+                         (batch, seqlen, heads, qk_heads, dk, dv, int(in_dtype)))
+
+
+def ss_linattn_bwd_workspace_bytes(batch, seqlen, heads, qk_heads, dk, dv, in_dtype) -> int:
+    return _linattn_need(load_library().ss_linattn_bwd_workspace_bytes,
+                         (batch, seqlen, heads, qk_heads, dk, dv, int(in_dtype)))
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def ss_linattn_fwd(q, k, v, log_decay, scale=1.0, initial_state=None, lengths=None, o_out=None,
+                   last_state_out=None, return_last_state=True, workspace=None, stream=None):
+    """Linear attention with one decay per head over a whole prompt:
+    S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T, o_t = scale * S_t^T q_t.
+
+    q, k: [batch, L, qk_heads, dk]; v: [batch, L, heads, dv]; log_decay: [batch, L, heads];
+    one dtype, float32 or bfloat16, strided (last axis contiguous).  heads is a multiple of
+    qk_heads; dk and dv at most 128.  initial_state: [batch, heads, dk, dv] float32.
+    lengths: [batch] int32; nothing is written to o_out behind a row's length (an o allocated
+    here is zero there).  Returns (o [batch, L, heads, dv] in the input dtype, last_state
+    [batch, heads, dk, dv] float32 or None); last_state_out may be initial_state.
+    """
+    lib = load_library()
+    device, ops, sizes = _linattn_operands("ss_linattn_fwd", q, k, v, log_decay)
+    batch, L, heads, _, dk, dv, _ = sizes
+    need = ss_linattn_workspace_bytes(*sizes)
+    _check_dev("initial_state", initial_state, device, (torch.float32,), (batch, heads, dk, dv))
+    _check_dev("lengths", lengths, device, (torch.int32,), (batch,))
+    if o_out is None:
+        make = torch.empty if lengths is None else torch.zeros
+        o_out = make((batch, L, heads, dv), dtype=q.dtype, device=device)
+    _check_dev("o_out", o_out, device, (q.dtype,), (batch, L, heads, dv))
+    if last_state_out is None and return_last_state:
+        last_state_out = torch.empty((batch, heads, dk, dv), dtype=torch.float32, device=device)
+    _check_dev("last_state_out", last_state_out, device, (torch.float32,), (batch, heads, dk, dv))
+    workspace, ws_bytes = _workspace(workspace, need, device)
+    with torch.cuda.device(device):
+        st = lib.ss_linattn_fwd(*ops, float(scale), _ptr(initial_state), _ptr(lengths), _ptr(o_out),
+                                _ptr(last_state_out), *sizes, _ptr(workspace), ws_bytes,
+                                _stream_handle(stream, device))
+    if st != SS_OK:
+        raise SSError(st, "ss_linattn_fwd")
+    return o_out, last_state_out
+
+
+def ss_linattn_bwd(q, k, v, log_decay, do, scale=1.0, initial_state=None, dlast_state=None,
+                   lengths=None, workspace=None, stream=None):
+    """Gradients of ss_linattn_fwd for an upstream do [batch, L, heads, dv] (the inputs' dtype,
+    strided) and, optionally, dlast_state [batch, heads, dk, dv] float32.
+
+    Returns a dict: dq, dk (summed over the heads that share them), dv, dlog_decay in the
+    inputs' dtype, zero behind a row's length, and dinitial_state float32 (None without
+    initial_state).
+    """
+    lib = load_library()
+    device, ops, sizes = _linattn_operands("ss_linattn_bwd", q, k, v, log_decay)
+    batch, L, heads, qk_heads, dk, dv, _ = sizes
+    need = ss_linattn_bwd_workspace_bytes(*sizes)
+    ops.append(_heads4("do", do, device, q.dtype, (batch, L, heads, dv)))
+    for name, t in (("initial_state", initial_state), ("dlast_state", dlast_state)):
+        _check_dev(name, t, device, (torch.float32,), (batch, heads, dk, dv))
+    _check_dev("lengths", lengths, device, (torch.int32,), (batch,))
+    make = torch.empty if lengths is None else torch.zeros
+    g = {"dq": make((batch, L, qk_heads, dk), dtype=q.dtype, device=device),
+         "dk": make((batch, L, qk_heads, dk), dtype=q.dtype, device=device),
+         "dv": make((batch, L, heads, dv), dtype=q.dtype, device=device),
+         "dlog_decay": make((batch, L, heads), dtype=q.dtype, device=device),
+         "dinitial_state": None if initial_state is None else torch.empty_like(initial_state)}
+    workspace, ws_bytes = _workspace(workspace, need, device)
+    with torch.cuda.device(device):
+        st = lib.ss_linattn_bwd(*ops, float(scale), _ptr(initial_state), _ptr(dlast_state),
+                                _ptr(lengths), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
+                                _ptr(g["dlog_decay"]), _ptr(g["dinitial_state"]), *sizes,
+                                _ptr(workspace), ws_bytes, _stream_handle(stream, device))
+    if st != SS_OK:
+        raise SSError(st, "ss_linattn_bwd")
+    return g
+
+
+def ss_linattn_step(state, q, k, v, log_decay, scale=1.0, slots=None, o_out=None, stream=None):
+    """One token of ss_linattn_fwd for every sequence; advances the states in place.
+
+    state: [num_slots, heads, dk, dv] float32; q, k: [batch, qk_heads, dk]; v: [batch, heads,
+    dv]; log_decay: [batch, heads] (strided).  slots: [batch] int32, the state of each row
+    (None: row b has state b); a slot outside the pool is a row of padding, whose o is not
+    written (an o allocated here is zero there), and so is a row whose slot an earlier row
+    has.  Returns o [batch, heads, dv] in the input dtype.
+    """
+    lib = load_library()
+    device = _cuda_device("state", state, "ss_linattn_step")
+    if state.dim() != 4 or q.dim() != 3 or v.dim() != 3:
+        raise ValueError("state must be [num_slots, heads, dk, dv], q and k [batch, qk_heads, dk], "
+                         "v [batch, heads, dv]")
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"q: dtype {q.dtype} is not float32 or bfloat16")
+    num_slots, heads, dk, dv = state.shape
+    batch, qk_heads, _ = q.shape
+    _check_dev("state", state, device, (torch.float32,))
+    ops = [_heads3("q", q, device, q.dtype, (batch, qk_heads, dk)),
+           _heads3("k", k, device, q.dtype, (batch, qk_heads, dk)),
+           _heads3("v", v, device, q.dtype, (batch, heads, dv)),
+           _heads3("log_decay", log_decay, device, q.dtype, (batch, heads))]
+    _check_dev("slots", slots, device, (torch.int32,), (batch,))
+    if o_out is None:
+        make = torch.empty if slots is None else torch.zeros
+        o_out = make((batch, heads, dv), dtype=q.dtype, device=device)
+    _check_dev("o_out", o_out, device, (q.dtype,), (batch, heads, dv))
+    dt = SS_F32 if q.dtype == torch.float32 else SS_BF16
+    with torch.cuda.device(device):
+        st = lib.ss_linattn_step(*ops, float(scale), _ptr(state), num_slots, _ptr(slots), _ptr(o_out),
+                                 batch, heads, qk_heads, dk, dv, dt, _stream_handle(stream, device))
+    if st != SS_OK:
+        raise SSError(st, "ss_linattn_step")
+    return o_out
+
+
+def _pool_operands(what, codes, scales, slots):
+    device = _cuda_device("codes", codes, what)
+    if codes.dim() < 2:
+        raise ValueError("codes must be [num_slots, ..., width]")
+    _check_dev("codes", codes, device, (torch.int8,))
+    _check_dev("scales", scales, device, (torch.float32,), codes.shape[:-1])
+    if slots is not None and (not isinstance(slots, torch.Tensor) or slots.dim() != 1):
+        raise ValueError("slots must be a [batch] tensor")
+    _check_dev("slots", slots, device, (torch.int32,))
+    rows = 1
+    for n in codes.shape[1:-1]:
+        rows *= n
+    return device, rows
+
+
+def ss_state_store8(state, codes, scales, slots=None, stream=None):
+    """Store states [batch, ..., width] float32 (the scan's [batch, dim, N], the attention's
+    [batch, heads, dk, dv]) into a pool in 8 bits: codes [num_slots, ..., width] int8, scales
+    [num_slots, ...] float32, one scale per row of the last axis.  slots: [batch] int32 (None:
+    row b goes to slot b); a slot outside the pool leaves that sequence out, and of several
+    with the same slot the last one is kept.
+    """
+    lib = load_library()
+    device, rows = _pool_operands("ss_state_store8", codes, scales, slots)
+    batch = state.shape[0] if slots is None else slots.shape[0]
+    _check_dev("state", state, device, (torch.float32,), (batch, *codes.shape[1:]))
+    with torch.cuda.device(device):
+        st = lib.ss_state_store8(_ptr(state), _ptr(codes), _ptr(scales), codes.shape[0], _ptr(slots),
+                                 batch, rows, codes.shape[-1], _stream_handle(stream, device))
+    if st != SS_OK:
+        raise SSError(st, "ss_state_store8")
+
+
+def ss_state_load8(codes, scales, slots=None, state_out=None, stream=None):
+    """States read back from the pool of ss_state_store8 as [batch, ..., width] float32.
+    slots: [batch] int32 (None: every slot, in order); a slot outside the pool gives a zero
+    state."""
+    lib = load_library()
+    device, rows = _pool_operands("ss_state_load8", codes, scales, slots)
+    batch = codes.shape[0] if slots is None else slots.shape[0]
+    if state_out is None:
+        state_out = torch.empty((batch, *codes.shape[1:]), dtype=torch.float32, device=device)
+    _check_dev("state_out", state_out, device, (torch.float32,), (batch, *codes.shape[1:]))
+    with torch.cuda.device(device):
+        st = lib.ss_state_load8(_ptr(codes), _ptr(scales), codes.shape[0], _ptr(slots), _ptr(state_out),
+                                batch, rows, codes.shape[-1], _stream_handle(stream, device))
+    if st != SS_OK:
+        raise SSError(st, "ss_state_load8")
+    return state_out

@@ -19,12 +19,13 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
 def sources():
-    return [os.path.join(CSRC, "ss_scan.cu")]
+    return [os.path.join(CSRC, "ss_scan.cu"), os.path.join(CSRC, "ss_linattn.cu")]
 
 
 def deps():
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + [os.path.join(ROOT, "include", "ss_scan.h"), os.path.abspath(__file__)])
+            + [os.path.join(ROOT, "include", "ss_scan.h"), os.path.join(ROOT, "include", "ss_linattn.h"),
+               os.path.abspath(__file__)])
 
 
 def source_hash(defines=()) -> str:
@@ -57,12 +58,26 @@ def build(force: bool = False, ptxas_verbose: bool = False, out: str | None = No
     if out is None and not force and not stale():
         return LIB
     tmp = target + f".tmp{os.getpid()}"
-    cmd = [NVCC, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
-           "-shared", "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp,
-           *[f"-D{d}" for d in defines], *sources()]
+    flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2"]
     if ptxas_verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
+        flags.insert(0, "-Xptxas=-v")
+    objects = []
+    try:
+        jobs = []  # the units, side by side
+        for src in sources():
+            objects.append(f"{tmp}.{os.path.splitext(os.path.basename(src))[0]}.o")
+            cmd = [NVCC, *flags, "-c", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+                   *[f"-D{d}" for d in defines], "-o", objects[-1], src]
+            jobs.append((cmd, subprocess.Popen(cmd)))
+        failed = [(job.wait(), cmd) for cmd, job in jobs]
+        for rc, cmd in failed:
+            if rc != 0:
+                raise subprocess.CalledProcessError(rc, cmd)
+        subprocess.check_call([NVCC, *flags, "-shared", "-o", tmp, *objects])
+    finally:
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(tmp, target)
     with open(target + ".src", "w") as f:
         f.write(source_hash(defines))

@@ -1,0 +1,419 @@
+// linattn_host.cuh -- host side of the linear attention: the cut into segments,
+// workspaces, launches and the argument checks
+// (host code of libssscan.so's second translation unit, ss_linattn.cu)
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "ss_linattn.h"
+#include "host_common.cuh"
+#include "linattn_pass.cuh"
+#include "linattn_step.cuh"
+#include "state_pool.cuh"
+
+namespace ssscan {
+namespace {
+
+struct LaShape {
+  int64_t batch, seqlen;
+  int heads, qk_heads, dk, dv;
+  bool bf16;
+  int64_t bh() const { return batch * heads; }
+  int64_t per_state() const { return (int64_t)dk * dv; }
+  int es() const { return bf16 ? 2 : 4; }
+};
+
+ss_status la_check_shape(const LaShape& s, int in_dtype) {
+  if (s.batch < 1 || s.seqlen < 1 || s.heads < 1 || s.qk_heads < 1 || s.dk < 1 || s.dv < 1) return SS_ERR_INVALID_ARG;
+  if (s.heads % s.qk_heads != 0) return SS_ERR_INVALID_ARG;
+  if (s.seqlen > INT_MAX - 1024 || s.batch > INT_MAX || s.batch * s.heads > (1 << 24)) return SS_ERR_INVALID_ARG;
+  if (s.dk > 128 || s.dv > 128) return SS_ERR_UNSUPPORTED;
+  if (in_dtype != SS_F32 && in_dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
+  return SS_OK;
+}
+
+bool la_check_heads(const ss_heads* x, int es) { return x && x->data && aligned(x->data, es); }
+
+LaTensor la_tensor(const ss_heads& x, int share) {
+  return LaTensor{x.data, x.batch_stride, x.token_stride, x.head_stride, share};
+}
+
+// 16-byte loads: data, every stride and the row itself whole units.
+bool la_vec(const LaTensor& x, int d, int es) {
+  const int64_t n = 16 / es;
+  return aligned(x.ptr, 16) && x.sb % n == 0 && x.st % n == 0 && x.sh % n == 0 && d % n == 0;
+}
+
+struct LaSegs {
+  int nseg, chunks;  // segments, and chunks of each
+};
+
+// How many segments a head's sequence is cut into.  One CTA fits on an SM.  Uncut,
+// batch x heads CTAs take all chunks each; cut into s, a first launch forms the
+// states of s - 1 segments (no queries, scores or outputs: about half a chunk's
+// time), a second joins them and a third runs all segments at once.  In units of a
+// chunk's time a CTA costs about 3 to start, the two extra launches about 6.
+LaSegs la_plan(const LaShape& s) {
+  const int64_t chunks = (s.seqlen + kLaChunk - 1) / kLaChunk, bh = s.bh();
+  const int64_t slots = device_sms() > 0 ? device_sms() : 148;
+  double best = 0;
+  int64_t at = 1;
+  for (int64_t n = 1; n <= 64 && n <= chunks; ++n) {
+    const int64_t per = (chunks + n - 1) / n;
+    if ((chunks + per - 1) / per != n) continue;
+    double cost = (double)((bh * n + slots - 1) / slots) * (per + 3.0);
+    if (n > 1) cost += (double)((bh * (n - 1) + slots - 1) / slots) * (0.5 * per + 3.0) + 6.0;
+    if (n == 1 || cost < best) best = cost, at = n;
+  }
+  return LaSegs{(int)at, (int)((chunks + at - 1) / at)};
+}
+
+struct LaSeg {  // a workspace's share for segments
+  float* states = nullptr;
+  double* decay = nullptr;
+};
+size_t la_seg_bytes(const LaShape& s, const LaSegs& g) {
+  if (g.nseg <= 1) return 0;
+  return align256((size_t)s.bh() * g.nseg * s.per_state() * 4) + align256((size_t)s.bh() * g.nseg * 8);
+}
+LaSeg la_seg_at(char* ws, const LaShape& s, const LaSegs& g) {
+  LaSeg r;
+  if (g.nseg <= 1) return r;
+  r.states = reinterpret_cast<float*>(ws);
+  r.decay = reinterpret_cast<double*>(ws + align256((size_t)s.bh() * g.nseg * s.per_state() * 4));
+  return r;
+}
+
+template <typename T, int KD, int VD, bool STATES>
+ss_status la_launch(const LaPassArgs& a, int64_t batch, cudaStream_t stream) {
+  using CF = LaCfg<T, KD, VD>;
+  struct Tag : CF {};
+  if (once_per_device<Tag>([] {
+        return cudaFuncSetAttribute(linattn_pass_kernel<T, KD, VD, STATES>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, CF::kSmem) == cudaSuccess;
+      }) != 1)
+    return SS_ERR_CUDA;
+  const int64_t grid = batch * a.heads * a.nseg;
+  if (grid > INT_MAX) return SS_ERR_INVALID_ARG;
+  linattn_pass_kernel<T, KD, VD, STATES><<<(unsigned)grid, CF::kThreads, CF::kSmem, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+template <typename T, bool STATES>
+ss_status la_dispatch(LaPassArgs a, int64_t batch, cudaStream_t stream) {
+  const int es = sizeof(T);
+  a.vec = la_vec(a.k, a.dk, es) && la_vec(a.v, a.dv, es) && (STATES || la_vec(a.q, a.dk, es));
+  if (a.dk <= 64) return a.dv <= 64 ? la_launch<T, 64, 64, STATES>(a, batch, stream) : la_launch<T, 64, 128, STATES>(a, batch, stream);
+  return a.dv <= 64 ? la_launch<T, 128, 64, STATES>(a, batch, stream) : la_launch<T, 128, 128, STATES>(a, batch, stream);
+}
+
+template <bool STATES>
+ss_status la_pass(const LaPassArgs& a, bool bf16, int64_t batch, cudaStream_t stream) {
+  return bf16 ? la_dispatch<__nv_bfloat16, STATES>(a, batch, stream) : la_dispatch<float, STATES>(a, batch, stream);
+}
+
+// The starting states of every segment of pass `a` (its k, v, g and directions) into seg.
+ss_status la_segment_states(LaPassArgs a, const LaShape& s, const LaSegs& g, const LaSeg& seg, const float* s0,
+                            cudaStream_t stream) {
+  a.nseg = g.nseg - 1;
+  a.seg_chunks = g.chunks;
+  a.s_in = nullptr;
+  a.s_out = seg.states;
+  a.s_out_head = (int64_t)g.nseg * s.per_state();
+  a.s_out_seg = s.per_state();
+  a.seg_decay = seg.decay;
+  const ss_status st = la_pass<true>(a, s.bf16, s.batch, stream);
+  if (st != SS_OK) return st;
+  // rows of the grid are at most 2^16 - 1: whole states of up to that many heads a launch
+  for (int64_t at = 0; at < s.bh(); at += 65535) {
+    const int64_t n = s.bh() - at < 65535 ? s.bh() - at : 65535;
+    linattn_join_kernel<<<dim3((unsigned)((s.per_state() + 255) / 256), (unsigned)n), 256, 0, stream>>>(
+        seg.states + at * g.nseg * s.per_state(), seg.decay + at * g.nseg, s0 ? s0 + at * s.per_state() : nullptr,
+        s.per_state(), g.nseg, s.per_state());
+  }
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+LaPassArgs la_base(const LaShape& s, const ss_heads* g, const int32_t* lengths, const LaSegs& segs) {
+  LaPassArgs a = {};
+  a.g = la_tensor(*g, 1);
+  a.lengths = lengths;
+  a.heads = s.heads;
+  a.seqlen = (int)s.seqlen;
+  a.nseg = segs.nseg;
+  a.seg_chunks = segs.chunks;
+  a.anchor_chunks = 1;
+  a.scale_p = a.scale_o = a.scale_w = 1.f;
+  return a;
+}
+
+// Where a pass starts: the segments' states, or the caller's.
+void la_start(LaPassArgs& a, const LaShape& s, const LaSegs& g, const LaSeg& seg, const float* s0) {
+  a.s_in = g.nseg > 1 ? seg.states : s0;
+  a.s_in_head = (int64_t)g.nseg * s.per_state();
+  a.s_in_seg = s.per_state();
+  a.s_out_head = s.per_state();
+  a.s_out_seg = 0;
+}
+
+ss_status linattn_fwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads* v, const ss_heads* g, float scale,
+                           const float* s0, const int32_t* lengths, void* o, float* last, const LaShape& s,
+                           int in_dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const ss_status shape = la_check_shape(s, in_dtype);
+  if (shape != SS_OK) return shape;
+  const int es = s.es();
+  if (!la_check_heads(q, es) || !la_check_heads(k, es) || !la_check_heads(v, es) || !la_check_heads(g, es) || !o)
+    return SS_ERR_INVALID_ARG;
+  if (!aligned(o, es) || !aligned(s0, 4) || !aligned(last, 4) || !aligned(lengths, 4)) return SS_ERR_INVALID_ARG;
+  const LaSegs segs = la_plan(s);
+  const size_t need = la_seg_bytes(s, segs);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 256))) return SS_ERR_INVALID_ARG;
+  const LaSeg seg = la_seg_at(static_cast<char*>(ws), s, segs);
+  LaPassArgs a = la_base(s, g, lengths, segs);
+  const int share = s.heads / s.qk_heads;
+  a.q = la_tensor(*q, share);
+  a.k = la_tensor(*k, share);
+  a.v = la_tensor(*v, 1);
+  a.dk = s.dk;
+  a.dv = s.dv;
+  a.sk = s.dv;
+  a.sv = 1;
+  if (segs.nseg > 1) {
+    const ss_status st = la_segment_states(a, s, segs, seg, s0, stream);
+    if (st != SS_OK) return st;
+  }
+  la_start(a, s, segs, seg, s0);
+  a.s_out = last;
+  a.out = o;
+  a.scale_p = a.scale_o = scale;
+  return la_pass<false>(a, s.bf16, s.batch, stream);
+}
+
+// ---- backward
+
+// An anchor behind every so many chunks: each costs a state's write and read, the
+// sums between two cancel over that many tokens.
+int la_anchor_chunks(const LaShape& s) { return s.bf16 ? 16 : 4; }
+
+struct LaBwdWs {
+  size_t seg = 0, dots_q = 0, dots_k = 0, anchor = 0, dump = 0, part = 0, bytes = 0;
+  int64_t anchors = 0;
+};
+LaBwdWs la_bwd_ws(const LaShape& s, const LaSegs& g) {
+  LaBwdWs w;
+  const int64_t chunks = (s.seqlen + kLaChunk - 1) / kLaChunk;
+  const int per = la_anchor_chunks(s);
+  w.anchors = (chunks + per - 1) / per;
+  size_t at = la_seg_bytes(s, g);
+  auto take = [&at](size_t n) {
+    const size_t r = at;
+    at += align256(n);
+    return r;
+  };
+  const size_t rows = (size_t)s.bh() * s.seqlen;
+  w.dots_q = take(rows * 16);
+  w.dots_k = take(rows * 16);
+  w.anchor = take((size_t)s.bh() * w.anchors * 8 * 4);
+  w.dump = take((size_t)s.bh() * w.anchors * 128 * (s.dv <= 64 ? 64 : 128) * 4);
+  w.part = take(s.heads > s.qk_heads ? rows * s.dk * 4 : 0);
+  w.bytes = at;
+  return w;
+}
+
+template <typename T>
+ss_status la_share_sum(const float* part, void* out, const int32_t* lengths, const LaShape& s, cudaStream_t stream) {
+  const int64_t total = s.batch * s.seqlen * s.qk_heads * s.dk;
+  const int64_t blocks = (total + 255) / 256;
+  linattn_share_kernel<T><<<(unsigned)(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, stream>>>(
+      part, static_cast<T*>(out), lengths, s.seqlen, total, s.heads, s.heads / s.qk_heads, s.dk);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+template <typename T>
+ss_status la_decay_grad(const LaPassArgs& a, const float* dots_q, const float* dots_k, void* dg, const LaShape& s,
+                        cudaStream_t stream) {
+  const int64_t warps = s.bh() * a.anchors;
+  linattn_decay_grad_kernel<T><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(
+      dots_q, dots_k, a.anchor, static_cast<T*>(dg), a.lengths, s.bh(), s.heads, (int)s.seqlen, a.anchors,
+      a.anchor_chunks * kLaChunk);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads* v, const ss_heads* g,
+                           const ss_heads* d_o, float scale, const float* s0, const float* dlast,
+                           const int32_t* lengths, void* dq, void* dk, void* dv, void* dg, float* ds0,
+                           const LaShape& s, int in_dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  ss_status st = la_check_shape(s, in_dtype);
+  if (st != SS_OK) return st;
+  const int es = s.es();
+  for (const ss_heads* x : {q, k, v, g, d_o})
+    if (!la_check_heads(x, es)) return SS_ERR_INVALID_ARG;
+  for (const void* x : {dq, dk, dv, dg})
+    if (!x || !aligned(x, es)) return SS_ERR_INVALID_ARG;
+  if (!aligned(s0, 4) || !aligned(dlast, 4) || !aligned(lengths, 4) || !aligned(ds0, 4)) return SS_ERR_INVALID_ARG;
+  const LaSegs segs = la_plan(s);
+  const LaBwdWs w = la_bwd_ws(s, segs);
+  if (!ws || ws_bytes < w.bytes || !aligned(ws, 256)) return SS_ERR_INVALID_ARG;
+  char* base = static_cast<char*>(ws);
+  const LaSeg seg = la_seg_at(base, s, segs);
+  const int share = s.heads / s.qk_heads;
+  const LaTensor tq = la_tensor(*q, share), tk = la_tensor(*k, share), tv = la_tensor(*v, 1), td = la_tensor(*d_o, 1);
+  float* part = reinterpret_cast<float*>(base + w.part);
+
+  // dq: a forward pass with (do, v, k); its state is S with the two indices exchanged
+  LaPassArgs a = la_base(s, g, lengths, segs);
+  a.anchor_chunks = la_anchor_chunks(s);
+  a.anchors = (int)w.anchors;
+  a.dump = reinterpret_cast<float*>(base + w.dump);
+  a.anchor = reinterpret_cast<float*>(base + w.anchor);
+  a.q = td;
+  a.k = tv;
+  a.v = tk;
+  a.dk = s.dv;
+  a.dv = s.dk;
+  a.sk = 1;
+  a.sv = s.dv;
+  if (segs.nseg > 1 && (st = la_segment_states(a, s, segs, seg, s0, stream)) != SS_OK) return st;
+  la_start(a, s, segs, seg, s0);
+  a.scale_p = a.scale_o = scale;
+  a.out = share > 1 ? part : dq;
+  a.out_f32 = share > 1;
+  a.x = tq;
+  a.dots = reinterpret_cast<float*>(base + w.dots_q);
+  if ((st = la_pass<false>(a, s.bf16, s.batch, stream)) != SS_OK) return st;
+  if (share > 1 && (st = s.bf16 ? la_share_sum<__nv_bfloat16>(part, dq, lengths, s, stream)
+                                : la_share_sum<float>(part, dq, lengths, s, stream)) != SS_OK)
+    return st;
+
+  // dk: reversed with (v, do, q); the state is R, the gradient of S
+  a.reverse = 1;
+  a.q = tv;
+  a.k = td;
+  a.v = tq;
+  a.scale_p = a.scale_w = scale;
+  a.scale_o = 1.f;
+  if (segs.nseg > 1 && (st = la_segment_states(a, s, segs, seg, dlast, stream)) != SS_OK) return st;
+  la_start(a, s, segs, seg, dlast);
+  a.out = share > 1 ? part : dk;
+  a.x = tk;
+  a.dots = reinterpret_cast<float*>(base + w.dots_k);
+  // the initial state's gradient waits for the last pass where it overwrites dlast
+  if ((st = la_pass<false>(a, s.bf16, s.batch, stream)) != SS_OK) return st;
+  if (share > 1 && (st = s.bf16 ? la_share_sum<__nv_bfloat16>(part, dk, lengths, s, stream)
+                                : la_share_sum<float>(part, dk, lengths, s, stream)) != SS_OK)
+    return st;
+  if ((st = s.bf16 ? la_decay_grad<__nv_bfloat16>(a, reinterpret_cast<float*>(base + w.dots_q), a.dots, dg, s, stream)
+                   : la_decay_grad<float>(a, reinterpret_cast<float*>(base + w.dots_q), a.dots, dg, s, stream)) != SS_OK)
+    return st;
+
+  // dv: reversed with (k, q, do)
+  a.q = tk;
+  a.k = tq;
+  a.v = td;
+  a.dk = s.dk;
+  a.dv = s.dv;
+  a.sk = s.dv;
+  a.sv = 1;
+  a.out = dv;
+  a.out_f32 = 0;
+  a.x = LaTensor{};
+  a.x.share = 1;
+  a.dots = nullptr;
+  a.dump = nullptr;
+  a.s_out = ds0;
+  return la_pass<false>(a, s.bf16, s.batch, stream);
+}
+
+// ---- single tokens
+
+template <typename T>
+ss_status la_launch_step(const LaStepArgs& a, bool vec, cudaStream_t stream) {
+  const dim3 grid((unsigned)(a.heads * ((a.dv + kLaStepCols - 1) / kLaStepCols)), (unsigned)a.batch);
+  if (vec) linattn_step_kernel<T, 4><<<grid, kLaStepThreads, 0, stream>>>(a);
+  else linattn_step_kernel<T, 1><<<grid, kLaStepThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+ss_status linattn_step_impl(const ss_heads* q, const ss_heads* k, const ss_heads* v, const ss_heads* g, float scale,
+                            float* state, int64_t num_slots, const int32_t* slots, void* o, const LaShape& s,
+                            int in_dtype, cudaStream_t stream) {
+  const ss_status shape = la_check_shape(s, in_dtype);
+  if (shape != SS_OK) return shape;
+  const int es = s.es();
+  for (const ss_heads* x : {q, k, v, g})
+    if (!la_check_heads(x, es)) return SS_ERR_INVALID_ARG;
+  if (!o || !aligned(o, es) || !state || !aligned(state, 4) || !aligned(slots, 4)) return SS_ERR_INVALID_ARG;
+  if (s.batch > 65535 || num_slots < 1 || (!slots && num_slots < s.batch)) return SS_ERR_INVALID_ARG;
+  LaStepArgs a = {};
+  const int share = s.heads / s.qk_heads;
+  a.q = la_tensor(*q, share);
+  a.k = la_tensor(*k, share);
+  a.v = la_tensor(*v, 1);
+  a.g = la_tensor(*g, 1);
+  a.state = state;
+  a.num_slots = num_slots;
+  a.slots = slots;
+  a.out = o;
+  a.batch = (int)s.batch;
+  a.heads = s.heads;
+  a.dk = s.dk;
+  a.dv = s.dv;
+  a.scale = scale;
+  const bool vec = aligned(state, 16) && s.dv % 4 == 0;
+  return s.bf16 ? la_launch_step<__nv_bfloat16>(a, vec, stream) : la_launch_step<float>(a, vec, stream);
+}
+
+// ---- the pool
+
+ss_status pool_check(const void* state, const void* codes, const void* scales, int64_t num_slots, const int32_t* slots,
+                     int64_t batch, int64_t rows, int width) {
+  if (!state || !codes || !scales || batch < 1 || rows < 1 || width < 1 || num_slots < 1) return SS_ERR_INVALID_ARG;
+  if (!aligned(state, 4) || !aligned(scales, 4) || !aligned(slots, 4)) return SS_ERR_INVALID_ARG;
+  if (batch > 65535 || (!slots && num_slots < batch)) return SS_ERR_INVALID_ARG;
+  if (width > 1024) return SS_ERR_UNSUPPORTED;
+  if (rows > (INT_MAX - 1024) / width) return SS_ERR_INVALID_ARG;
+  return SS_OK;
+}
+
+template <int LANES, int VEC, int REGS>
+ss_status pool_store(const PoolArgs& a, cudaStream_t stream) {
+  const int64_t tiles = (a.rows + kPoolThreads / LANES - 1) / (kPoolThreads / LANES);
+  state_store8_kernel<LANES, VEC, REGS><<<dim3((unsigned)tiles, (unsigned)a.batch), kPoolThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+ss_status state_store8_impl(const PoolArgs& a, cudaStream_t stream) {
+  const bool vec = a.width % 4 == 0 && aligned(a.state, 16) && aligned(a.codes, 4);
+  if (vec) {
+    if (a.width <= 16) return pool_store<4, 4, 1>(a, stream);
+    if (a.width <= 32) return pool_store<8, 4, 1>(a, stream);
+    if (a.width <= 64) return pool_store<8, 4, 2>(a, stream);
+    if (a.width <= 128) return pool_store<8, 4, 4>(a, stream);
+    if (a.width <= 256) return pool_store<16, 4, 4>(a, stream);
+    if (a.width <= 512) return pool_store<32, 4, 4>(a, stream);
+    return pool_store<32, 4, 8>(a, stream);
+  }
+  if (a.width <= 32) return pool_store<8, 1, 4>(a, stream);
+  if (a.width <= 128) return pool_store<32, 1, 4>(a, stream);
+  if (a.width <= 512) return pool_store<32, 1, 16>(a, stream);
+  return pool_store<32, 1, 32>(a, stream);
+}
+
+template <int VEC>
+ss_status pool_load(const PoolArgs& a, cudaStream_t stream) {
+  const int64_t blocks = (a.rows * a.width / VEC + kPoolThreads - 1) / kPoolThreads;
+  state_load8_kernel<VEC><<<dim3((unsigned)blocks, (unsigned)a.batch), kPoolThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+ss_status state_load8_impl(const PoolArgs& a, cudaStream_t stream) {
+  if (a.width % 16 == 0 && aligned(a.state, 16) && aligned(a.codes, 16)) return pool_load<16>(a, stream);
+  if (a.width % 4 == 0 && aligned(a.state, 16) && aligned(a.codes, 4)) return pool_load<4>(a, stream);
+  return pool_load<1>(a, stream);
+}
+
+}  // namespace
+}  // namespace ssscan

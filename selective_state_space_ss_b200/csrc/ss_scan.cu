@@ -17,6 +17,10 @@
 
 using namespace ssscan;
 
+namespace ssscan {
+bool take_linattn_error_word(unsigned int* word);  // ss_linattn.cu
+}
+
 // Scratch of ss_scan_fwd_noalloc: one file-scope device array, held by every
 // GPU that loads the library.  Host code must not use its name as an address
 // (it is a host-side stand-in); ss_scan_fwd_noalloc looks up the device
@@ -279,7 +283,7 @@ const char* ss_status_string(ss_status s) {
   switch (s) {
     case SS_OK: return "SS_OK: success";
     case SS_ERR_INVALID_ARG: return "SS_ERR_INVALID_ARG: null pointer, bad size, misalignment or small workspace";
-    case SS_ERR_UNSUPPORTED: return "SS_ERR_UNSUPPORTED: dstate must be 16, 32, 64 or 128 and dtype f32 or bf16";
+    case SS_ERR_UNSUPPORTED: return "SS_ERR_UNSUPPORTED: dtype must be f32 or bf16, dstate 16, 32, 64 or 128, dk and dv at most 128, width at most 1024";
     case SS_ERR_CUDA: return "SS_ERR_CUDA: a CUDA runtime call or launch failed";
     case SS_ERR_TIMEOUT: return "SS_ERR_TIMEOUT: a bounded wait inside a kernel gave up";
     case SS_ERR_BOUNDS: return "SS_ERR_BOUNDS: a checked build met an index outside its tensor";
@@ -290,12 +294,15 @@ const char* ss_status_string(ss_status s) {
 ss_status ss_last_device_error(cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return SS_ERR_CUDA;
   unsigned int word = 0;
+  unsigned int other = 0;  // the linear attention's kernels have a word of their own
   if (cudaMemcpyFromSymbol(&word, g_error_word, sizeof word) != cudaSuccess) return SS_ERR_CUDA;
+  if (!take_linattn_error_word(&other)) return SS_ERR_CUDA;
   if (word != 0) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof zero) != cudaSuccess) return SS_ERR_CUDA;
-    return (word & kErrBounds) ? SS_ERR_BOUNDS : SS_ERR_TIMEOUT;
   }
+  word |= other;
+  if (word != 0) return (word & kErrBounds) ? SS_ERR_BOUNDS : SS_ERR_TIMEOUT;
   return SS_OK;
 }
 
