@@ -1,0 +1,150 @@
+"""The linear attention's and the state pool's entry points without a GPU: every
+bad argument is refused on the host, before any CUDA call.  Pointers are fake
+addresses that are never followed."""
+import ctypes
+
+import pytest
+
+from selective_state_space_ss_b200 import _native as N
+from selective_state_space_ss_b200 import build as B
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return N.load_library()
+
+
+def _h(addr):
+    return N.SSHeads(addr, 64, 64, 64)
+
+
+BASE = dict(q=0x10000, k=0x20000, v=0x30000, g=0x40000, do=0x50000, s0=None, dl=None, lengths=None, o=0x60000,
+            last=None, dq=0x70000, dk_=0x80000, dv_=0x90000, dg=0xa0000, ds0=None, batch=2, L=100, heads=4, hq=2,
+            dk=64, dv=64, dt=N.SS_BF16, ws=0x1000000, wsb=1 << 40)
+
+
+def _sizes(a):
+    return a["batch"], a["L"], a["heads"], a["hq"], a["dk"], a["dv"], a["dt"]
+
+
+def _fwd(lib, **over):
+    a = {**BASE, **over}
+    ops = [None if a[n] is None else _h(a[n]) for n in ("q", "k", "v", "g")]
+    return lib.ss_linattn_fwd(*ops, 1.0, a["s0"], a["lengths"], a["o"], a["last"], *_sizes(a), a["ws"], a["wsb"], None)
+
+
+def _bwd(lib, **over):
+    a = {**BASE, **over}
+    ops = [None if a[n] is None else _h(a[n]) for n in ("q", "k", "v", "g", "do")]
+    return lib.ss_linattn_bwd(*ops, 1.0, a["s0"], a["dl"], a["lengths"], a["dq"], a["dk_"], a["dv_"], a["dg"],
+                              a["ds0"], *_sizes(a), a["ws"], a["wsb"], None)
+
+
+def _step(lib, **over):
+    a = {**BASE, "state": 0xb0000, "pool": 2, "slots": None, **over}
+    ops = [None if a[n] is None else _h(a[n]) for n in ("q", "k", "v", "g")]
+    return lib.ss_linattn_step(*ops, 1.0, a["state"], a["pool"], a["slots"], a["o"], a["batch"], a["heads"], a["hq"],
+                               a["dk"], a["dv"], a["dt"], None)
+
+
+BAD_SIZES = [(dict(batch=0), N.SS_ERR_INVALID_ARG), (dict(heads=0), N.SS_ERR_INVALID_ARG),
+             (dict(hq=3), N.SS_ERR_INVALID_ARG), (dict(hq=0), N.SS_ERR_INVALID_ARG),
+             (dict(heads=2, hq=4), N.SS_ERR_INVALID_ARG), (dict(dk=0), N.SS_ERR_INVALID_ARG),
+             (dict(dv=-1), N.SS_ERR_INVALID_ARG), (dict(dk=129), N.SS_ERR_UNSUPPORTED),
+             (dict(dv=256), N.SS_ERR_UNSUPPORTED), (dict(dt=2), N.SS_ERR_UNSUPPORTED),
+             (dict(batch=1 << 24), N.SS_ERR_INVALID_ARG), (dict(batch=1 << 40), N.SS_ERR_INVALID_ARG)]
+
+
+@pytest.mark.parametrize("over,status", BAD_SIZES + [(dict(L=0), N.SS_ERR_INVALID_ARG),
+                                                     (dict(L=1 << 31), N.SS_ERR_INVALID_ARG)])
+@pytest.mark.parametrize("call", [_fwd, _bwd], ids=["fwd", "bwd"])
+def test_sizes_and_types(lib, call, over, status):
+    assert call(lib, **over) == status
+
+
+@pytest.mark.parametrize("over,status", BAD_SIZES + [
+    (dict(state=None), N.SS_ERR_INVALID_ARG), (dict(state=0xb0002), N.SS_ERR_INVALID_ARG),
+    (dict(pool=1), N.SS_ERR_INVALID_ARG), (dict(pool=0, slots=0xc0000), N.SS_ERR_INVALID_ARG),
+    (dict(slots=0xc0002), N.SS_ERR_INVALID_ARG), (dict(batch=65536, pool=65536), N.SS_ERR_INVALID_ARG),
+    (dict(o=None), N.SS_ERR_INVALID_ARG), (dict(k=None), N.SS_ERR_INVALID_ARG)])
+def test_step_refusals(lib, over, status):
+    assert _step(lib, **over) == status
+
+
+@pytest.mark.parametrize("over", [{n: None} for n in ("q", "k", "v", "g", "o")] + [
+    dict(q=0x10001), dict(g=0x40002, dt=N.SS_F32), dict(o=0x60002, dt=N.SS_F32), dict(s0=0x1002), dict(last=0x1001),
+    dict(lengths=0x1002), dict(o=0x60001)])
+def test_fwd_pointers(lib, over):
+    assert _fwd(lib, **over) == N.SS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [{n: None} for n in ("q", "k", "v", "g", "do", "dq", "dk_", "dv_", "dg", "ws")] + [
+    dict(do=0x50001), dict(dq=0x70002, dt=N.SS_F32), dict(dl=0x1002), dict(ds0=0x1002), dict(ws=0x1000010),
+    dict(wsb=16), dict(lengths=0x1001)])
+def test_bwd_pointers(lib, over):
+    assert _bwd(lib, **over) == N.SS_ERR_INVALID_ARG
+
+
+def test_a_null_tensor_struct_data_is_refused(lib):
+    assert _fwd(lib, q=0) == N.SS_ERR_INVALID_ARG
+
+
+def test_segments_need_their_workspace(lib):
+    sizes = (1, 1 << 20, 1, 1, 64, 64, N.SS_BF16)
+    need = lib.ss_linattn_workspace_bytes(*sizes)
+    assert need > 0  # one head, a million tokens: cut into segments
+    over = dict(batch=1, L=1 << 20, heads=1, hq=1)
+    assert _fwd(lib, **over, ws=None) == N.SS_ERR_INVALID_ARG
+    assert _fwd(lib, **over, wsb=need - 1) == N.SS_ERR_INVALID_ARG
+    assert _fwd(lib, **over, ws=0x1000080) == N.SS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over,_", BAD_SIZES)
+def test_workspace_queries_reject_what_the_calls_do(lib, over, _):
+    a = {**BASE, **over}
+    bad = ctypes.c_size_t(-1).value
+    assert lib.ss_linattn_workspace_bytes(*_sizes(a)) == bad
+    assert lib.ss_linattn_bwd_workspace_bytes(*_sizes(a)) == bad
+
+
+def test_workspace_queries(lib):
+    assert lib.ss_linattn_workspace_bytes(64, 64, 16, 16, 64, 64, N.SS_BF16) == 0
+    small = lib.ss_linattn_bwd_workspace_bytes(2, 100, 4, 4, 64, 64, N.SS_BF16)
+    shared = lib.ss_linattn_bwd_workspace_bytes(2, 100, 4, 2, 64, 64, N.SS_BF16)
+    assert 0 < small < shared  # shared queries and keys add their heads' partial gradients
+    with pytest.raises(N.SSError) as e:
+        N.ss_linattn_workspace_bytes(1, 1, 1, 1, 129, 64, N.SS_BF16)
+    assert e.value.status == N.SS_ERR_UNSUPPORTED
+
+
+POOL = dict(state=0x10000, codes=0x20000, scales=0x30000, pool=4, slots=None, batch=2, rows=10, width=16)
+
+
+@pytest.mark.parametrize("over,status", [({n: None}, N.SS_ERR_INVALID_ARG) for n in ("state", "codes", "scales")] + [
+    (dict(state=0x10002), N.SS_ERR_INVALID_ARG), (dict(scales=0x30002), N.SS_ERR_INVALID_ARG),
+    (dict(slots=0x40002), N.SS_ERR_INVALID_ARG), (dict(batch=0), N.SS_ERR_INVALID_ARG),
+    (dict(rows=0), N.SS_ERR_INVALID_ARG), (dict(width=0), N.SS_ERR_INVALID_ARG),
+    (dict(width=1025), N.SS_ERR_UNSUPPORTED), (dict(pool=0, slots=0x40000), N.SS_ERR_INVALID_ARG),
+    (dict(batch=5), N.SS_ERR_INVALID_ARG), (dict(batch=65536, pool=1 << 20), N.SS_ERR_INVALID_ARG),
+    (dict(rows=1 << 31), N.SS_ERR_INVALID_ARG), (dict(rows=1 << 28, width=64), N.SS_ERR_INVALID_ARG)])
+def test_pool_refusals(lib, over, status):
+    a = {**POOL, **over}
+    assert lib.ss_state_store8(a["state"], a["codes"], a["scales"], a["pool"], a["slots"], a["batch"], a["rows"],
+                               a["width"], None) == status
+    assert lib.ss_state_load8(a["codes"], a["scales"], a["pool"], a["slots"], a["state"], a["batch"], a["rows"],
+                              a["width"], None) == status
+
+
+def test_the_binding_runs_on_cuda_tensors_only(lib):
+    x = torch.zeros(1, 4, 2, 8)
+    g = torch.zeros(1, 4, 2)
+    state = torch.zeros(1, 2, 8, 8)
+    codes, scales = torch.zeros(1, 2, 8, 8, dtype=torch.int8), torch.zeros(1, 2, 8)
+    for call in (lambda: N.ss_linattn_fwd(x, x, x, g), lambda: N.ss_linattn_bwd(x, x, x, g, x),
+                 lambda: N.ss_linattn_step(state, x[:, 0], x[:, 0], x[:, 0], g[:, 0]),
+                 lambda: N.ss_state_store8(state, codes, scales), lambda: N.ss_state_load8(codes, scales)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
