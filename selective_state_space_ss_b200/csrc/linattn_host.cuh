@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <climits>
 #include <cstdint>
@@ -48,17 +49,26 @@ bool la_vec(const LaTensor& x, int d, int es) {
 }
 
 struct LaSegs {
-  int nseg, chunks;  // segments, and chunks of each
+  int nseg, chunks;  // segments of a head, and chunks of each
+  int workers;       // > 0 (nseg 1): CTAs that share all chunks evenly
 };
 
-// How many segments a head's sequence is cut into.  One CTA fits on an SM.  Uncut,
-// batch x heads CTAs take all chunks each; cut into s, a first launch forms the
-// states of s - 1 segments (no queries, scores or outputs: about half a chunk's
+// How a pass is cut.  One CTA fits on an SM.  Uncut, batch x heads CTAs take all
+// chunks of a head each.  With more heads than SMs a last wave that is not full is
+// avoided by workers, one an SM, with an equal share of the chunks; each hands at
+// most one state on.  With fewer, a head is cut into s segments: a first launch forms
+// the states of s - 1 of them (no queries, scores or outputs: about half a chunk's
 // time), a second joins them and a third runs all segments at once.  In units of a
 // chunk's time a CTA costs about 3 to start, the two extra launches about 6.
 LaSegs la_plan(const LaShape& s) {
   const int64_t chunks = (s.seqlen + kLaChunk - 1) / kLaChunk, bh = s.bh();
   const int64_t slots = device_sms() > 0 ? device_sms() : 148;
+  if (bh > slots) {
+    const int64_t waves = (bh + slots - 1) / slots;
+    const double share = (double)bh * chunks / slots;
+    if (waves * (chunks + 3.0) > share + 8.0) return LaSegs{1, (int)chunks, (int)slots};
+    return LaSegs{1, (int)chunks, 0};
+  }
   double best = 0;
   int64_t at = 1;
   for (int64_t n = 1; n <= 64 && n <= chunks; ++n) {
@@ -68,27 +78,70 @@ LaSegs la_plan(const LaShape& s) {
     if (n > 1) cost += (double)((bh * (n - 1) + slots - 1) / slots) * (0.5 * per + 3.0) + 6.0;
     if (n == 1 || cost < best) best = cost, at = n;
   }
-  return LaSegs{(int)at, (int)((chunks + at - 1) / at)};
+  return LaSegs{(int)at, (int)((chunks + at - 1) / at), 0};
 }
 
-struct LaSeg {  // a workspace's share for segments
+struct LaSeg {  // a workspace's share for segments or workers
   float* states = nullptr;
   double* decay = nullptr;
+  float* carry = nullptr;
+  unsigned* flags = nullptr;
 };
+size_t la_carry_bytes(const LaShape& s, const LaSegs& g) {
+  // eight back warps' states, for keys or (in a gradient) values up to 64 or 128 wide
+  return align256((size_t)g.workers * 128 * (s.dk <= 64 && s.dv <= 64 ? 64 : 128) * 4);
+}
 size_t la_seg_bytes(const LaShape& s, const LaSegs& g) {
+  if (g.workers > 0) return la_carry_bytes(s, g) + align256((1 + (size_t)g.workers * 8) * 4);
   if (g.nseg <= 1) return 0;
   return align256((size_t)s.bh() * g.nseg * s.per_state() * 4) + align256((size_t)s.bh() * g.nseg * 8);
 }
 LaSeg la_seg_at(char* ws, const LaShape& s, const LaSegs& g) {
   LaSeg r;
-  if (g.nseg <= 1) return r;
-  r.states = reinterpret_cast<float*>(ws);
-  r.decay = reinterpret_cast<double*>(ws + align256((size_t)s.bh() * g.nseg * s.per_state() * 4));
+  if (g.workers > 0) {
+    r.carry = reinterpret_cast<float*>(ws);
+    r.flags = reinterpret_cast<unsigned*>(ws + la_carry_bytes(s, g));
+  } else if (g.nseg > 1) {
+    r.states = reinterpret_cast<float*>(ws);
+    r.decay = reinterpret_cast<double*>(ws + align256((size_t)s.bh() * g.nseg * s.per_state() * 4));
+  }
   return r;
 }
 
+// cuTensorMapEncodeTiled, looked up once through the runtime (no link-time libcuda).
+PFN_cuTensorMapEncodeTiled_v12000 la_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// Blocks of 64 tokens x 64 columns of one head, 128-byte swizzle, zeros out of bounds.
+bool la_map(CUtensorMap* m, const LaTensor& x, int64_t batch, int64_t seqlen, int heads, int d) {
+  const auto enc = la_map_encoder();
+  if (!enc) return false;
+  const int64_t ext[4] = {d, seqlen, heads, batch}, str[4] = {1, x.st, x.sh, x.sb};
+  cuuint64_t dims[4], strides[3];
+  for (int i = 0; i < 4; ++i) {
+    dims[i] = (cuuint64_t)ext[i];
+    if (i == 0) continue;
+    // an axis of one has any stride; a broadcast or reversed one is left to plain loads
+    const int64_t bytes = ext[i] == 1 ? 16 : str[i] * 2;
+    if (bytes <= 0 || bytes % 16 != 0 || bytes >= ((int64_t)1 << 40)) return false;
+    strides[i - 1] = (cuuint64_t)bytes;
+  }
+  const cuuint32_t box[4] = {64, kLaChunk, 1, 1}, step[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(x.ptr), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int KD, int VD, bool STATES>
-ss_status la_launch(const LaPassArgs& a, int64_t batch, cudaStream_t stream) {
+ss_status la_launch(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream) {
   using CF = LaCfg<T, KD, VD>;
   struct Tag : CF {};
   if (once_per_device<Tag>([] {
@@ -96,9 +149,12 @@ ss_status la_launch(const LaPassArgs& a, int64_t batch, cudaStream_t stream) {
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, CF::kSmem) == cudaSuccess;
       }) != 1)
     return SS_ERR_CUDA;
-  const int64_t grid = batch * a.heads * a.nseg;
+  const int64_t grid = a.workers > 0 ? a.workers : a.bh * a.nseg;
   if (grid > INT_MAX) return SS_ERR_INVALID_ARG;
-  linattn_pass_kernel<T, KD, VD, STATES><<<(unsigned)grid, CF::kThreads, CF::kSmem, stream>>>(a);
+  if (a.workers > 0 &&
+      cudaMemsetAsync(a.flags, 0, (1 + (size_t)a.workers * 8) * sizeof(unsigned), stream) != cudaSuccess)
+    return SS_ERR_CUDA;
+  linattn_pass_kernel<T, KD, VD, STATES><<<(unsigned)grid, CF::kThreads, CF::kSmem, stream>>>(a, maps);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
@@ -106,8 +162,16 @@ template <typename T, bool STATES>
 ss_status la_dispatch(LaPassArgs a, int64_t batch, cudaStream_t stream) {
   const int es = sizeof(T);
   a.vec = la_vec(a.k, a.dk, es) && la_vec(a.v, a.dv, es) && (STATES || la_vec(a.q, a.dk, es));
-  if (a.dk <= 64) return a.dv <= 64 ? la_launch<T, 64, 64, STATES>(a, batch, stream) : la_launch<T, 64, 128, STATES>(a, batch, stream);
-  return a.dv <= 64 ? la_launch<T, 128, 64, STATES>(a, batch, stream) : la_launch<T, 128, 128, STATES>(a, batch, stream);
+  a.out_vec = es == 2 && !a.out_f32 && a.out && aligned(a.out, 16) && a.dv % 8 == 0;
+  LaMaps m = {};
+  if (es == 2 && a.vec) {
+    auto map = [&](CUtensorMap* to, const LaTensor& x, int d) {
+      return la_map(to, x, batch, a.seqlen, a.heads / x.share, d);
+    };
+    a.tma = map(&m.k, a.k, a.dk) && map(&m.v, a.v, a.dv) && (STATES || map(&m.q, a.q, a.dk));
+  }
+  if (a.dk <= 64) return a.dv <= 64 ? la_launch<T, 64, 64, STATES>(a, m, stream) : la_launch<T, 64, 128, STATES>(a, m, stream);
+  return a.dv <= 64 ? la_launch<T, 128, 64, STATES>(a, m, stream) : la_launch<T, 128, 128, STATES>(a, m, stream);
 }
 
 template <bool STATES>
@@ -143,6 +207,7 @@ LaPassArgs la_base(const LaShape& s, const ss_heads* g, const int32_t* lengths, 
   a.lengths = lengths;
   a.heads = s.heads;
   a.seqlen = (int)s.seqlen;
+  a.bh = s.bh();
   a.nseg = segs.nseg;
   a.seg_chunks = segs.chunks;
   a.anchor_chunks = 1;
@@ -152,6 +217,9 @@ LaPassArgs la_base(const LaShape& s, const ss_heads* g, const int32_t* lengths, 
 
 // Where a pass starts: the segments' states, or the caller's.
 void la_start(LaPassArgs& a, const LaShape& s, const LaSegs& g, const LaSeg& seg, const float* s0) {
+  a.workers = g.workers;
+  a.carry = seg.carry;
+  a.flags = seg.flags;
   a.s_in = g.nseg > 1 ? seg.states : s0;
   a.s_in_head = (int64_t)g.nseg * s.per_state();
   a.s_in_seg = s.per_state();
@@ -238,7 +306,7 @@ ss_status la_decay_grad(const LaPassArgs& a, const float* dots_q, const float* d
   const int64_t warps = s.bh() * a.anchors;
   linattn_decay_grad_kernel<T><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(
       dots_q, dots_k, a.anchor, static_cast<T*>(dg), a.lengths, s.bh(), s.heads, (int)s.seqlen, a.anchors,
-      a.anchor_chunks * kLaChunk);
+      a.anchor_chunks * kLaChunk, s.dk <= 64);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 

@@ -32,11 +32,24 @@
 // Layout.  Scores are Q K^T with tokens in the lanes.  O and S are kept transposed
 // (value index in the lanes), so that S^T is the MMA's A operand straight from
 // tensor memory: it is written there by the threads that hold it and never goes
-// through shared memory.  M is 128 throughout; where only 64 rows mean something
-// (tokens, 64-wide values) the other lanes hold sums of whatever follows in shared
-// memory and nobody reads them.
+// through shared memory.  M is 128 there; where values are 64 wide the other lanes
+// hold sums of whatever follows in shared memory and nobody reads them.
+//
+// Roles.  Loaders (two warps) fill rings of K, V and Q tiles, one warp works out the
+// decays, one thread issues the MMAs; the front warps (four) turn scores into P and
+// keys into weighted keys one chunk ahead of the back warps (eight), which hold the
+// state: they take O and the state's increment from tensor memory, give the state
+// back as planes, and write O out while the next chunk's products run.
+//
+// Schedule.  A head's chunks depend on one another through S alone.  With fewer heads
+// than SMs the sequence is cut into segments whose starting states a first launch
+// works out (STATES).  With more, every CTA takes an equal range of the chunks of all
+// heads laid end to end; a head cut between two CTAs is begun by the first of them
+// before anything else and carried on by the second after all else, so the state
+// handed over is there when it is needed.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -69,40 +82,60 @@ struct LaPassArgs {
   void* out;            // [batch, seqlen, heads, dv] contiguous
   int out_f32;          // out is float32 whatever the inputs
   LaTensor x;           // rows to take the inner product of each output row with (ptr null: none)
-  float* dots;          // [batch * heads, seqlen, 4] partial products of x
+  float* dots;          // [batch * heads, seqlen, 4] partial products of x, one a lane quadrant
   float* dump;          // forward: where the states at anchors go; reversed: where they come from
-  float* anchor;        // reversed: [batch * heads, anchors, 8] partial products <R, S> at anchors
+  float* anchor;        // reversed: [batch * heads, anchors, 8] partial products <R, S>, one a back warp
   int anchor_chunks;    // an anchor behind every so many chunks
   int anchors;          // anchors of the longest row
   int heads, seqlen, dk, dv;
-  int nseg, seg_chunks;
+  int64_t bh;           // batch * heads
+  int nseg, seg_chunks; // segments of a head, or
+  int workers;          // > 0: CTAs that share all chunks evenly
+  float* carry;         // [workers] states handed to the next worker
+  unsigned* flags;      // [0] hands out worker numbers, then [workers][8] one a back warp; zero at launch
   int reverse;
   int vec;              // 16-byte loads apply to q, k and v
+  int out_vec;          // 16-byte stores to out
+  int tma;              // so do the tensor maps
   float scale_p, scale_o, scale_w;
+};
+
+struct LaMaps {
+  CUtensorMap q, k, v;
 };
 
 template <typename T, int KD, int VD>
 struct LaCfg {
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int NPI = kBf16 ? 1 : 3;  // planes of the inputs
-  static constexpr int NPX = kBf16 ? 2 : 3;  // planes of what is computed here
-  static constexpr int NPMAX = NPX;          // products of planes a, b with a + b < NPMAX
+  static constexpr int NPX = kBf16 ? 2 : 3;  // planes of the scores and of the state as operands
+  static constexpr int NPW = 3;              // planes of the weighted keys
   static constexpr int KB = KD / 64, VB = VD / 64;
-  static constexpr int kStages = kBf16 ? 2 : 1;
-  static constexpr int kQ = 0, kK = KB * NPI * kLaBlock, kV = 2 * kK;
-  static constexpr int kStageBytes = kV + VB * NPI * kLaBlock;
-  static constexpr int kP = kStages * kStageBytes;
+  static constexpr int RK = kBf16 ? 2 : 1, RV = RK, RQ = kBf16 ? (KB + VB == 4 ? 2 : 3) : 1;  // tiles in each ring
+  static constexpr int RW = kBf16 ? 2 : 1;   // weighted keys
+  static constexpr int RF = 4;               // decays
+  static constexpr int kTileK = KB * NPI * kLaBlock, kTileV = VB * NPI * kLaBlock, kTileW = KB * NPW * kLaBlock;
+  static constexpr int kQ = 0, kK = RQ * kTileK, kV = kK + RK * kTileK, kP = kV + RV * kTileV;
   static constexpr int kW = kP + NPX * kLaBlock;
-  static constexpr int kFac = kW + NPX * KB * kLaBlock;
-  static constexpr int kSmem = kFac + kStages * (4 * kLaChunk + 4) * 4 + 256 + 1024;
+  static constexpr int kFacFloats = 4 * kLaChunk + 4;
+  static constexpr int kFac = kW + RW * kTileW;
+  static constexpr int kStage = kFac + (RF * kFacFloats * 4 + 127) / 128 * 128;  // 1 KB a back warp
+  static constexpr int kBars = kStage + (kBf16 ? 8 * 1024 : 0);
+  static constexpr int kSmem = kBars + 512;
   // tensor memory columns
   static constexpr int cDS = 0, cSP = KD, cO1 = cSP + NPX * KD / 2, cO2 = cO1 + 64, cQK = cO2 + 64;
   static constexpr int kCols = cQK + 64 <= 256 ? 256 : 512;
   static_assert(cQK + 64 <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory");
-  static constexpr int kComputeWarps = 8, kLoadWarps = 3;
-  static constexpr int kThreads = 32 * (kComputeWarps + 1 + kLoadWarps);
+  static constexpr int kQuads = VD / 32;        // lane quadrants that hold values
+  static constexpr int kHolders = 2 * kQuads;   // back warps at work
+  static constexpr int kLoaders = 64;           // loader threads
+  static constexpr int kThreads = 512;
 };
+constexpr int kLaBackWarps = 8, kLaFrontWarps = 4;
+constexpr int kLaMmaWarp = 12, kLaLoadWarp = 13, kLaDecayWarp = 15;
+// registers a thread of the three kinds of warpgroup: 2 x 168 + 104 + 72 = 4 x 128 at launch
+constexpr int kLaBackRegs = 168, kLaFrontRegs = 104, kLaAuxRegs = 72;
 
 // Waits of one CTA: when one gives up, the others stop waiting too, and the kernel
 // runs to its end on whatever is there, inside its buffers.
@@ -134,6 +167,7 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
                                              int len, int d, bool vec, int tid, int nthreads) {
   constexpr int B = DP / 64;
   constexpr int UNITS = kLaChunk * B * 8;
+#pragma unroll 2
   for (int u = tid; u < UNITS; u += nthreads) {
     const int row = u / (B * 8), unit = u % (B * 8), col = unit * 8;
     const bool in = t0 + row < len && col < d && in_range(t0 + row, len);
@@ -171,7 +205,7 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t s[3];
-        split2<3>(f[2 * i], f[2 * i + 1], s);
+        split2<3>(pair(f[2 * i], f[2 * i + 1]), s);
         w[0][i] = s[0], w[1][i] = s[1], w[2][i] = s[2];
       }
 #pragma unroll
@@ -181,25 +215,32 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
   }
 }
 
+// 2^x, x of either sign and any size: the fraction by ex2, the integer by scaling.
+__device__ __forceinline__ float la_exp2(double x) {
+  const double n = rint(x < -1e6 ? -1e6 : x > 1e6 ? 1e6 : x);
+  return scalbnf(ex2_approx((float)(x - n)), (int)n);
+}
+
+// A lane's two log decays of a chunk, zero behind the row's end.
+template <typename T>
+__device__ __forceinline__ void la_fetch_decays(float (&x)[2], const LaPassArgs& a, int64_t b, int h, int t0, int len,
+                                                int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = t0 + 2 * lane + i;
+    x[i] = t < len && in_range(t, len) ? to_f32(*reinterpret_cast<const T*>(la_row(a.g, b, t, h, sizeof(T)))) : 0.f;
+  }
+}
+
 // A chunk's decays: running sums (base 2) as two floats, the factors of the rows and
 // of the keys, and the chunk's whole decay.  One warp, two tokens a lane.  A log
 // decay below -1400 leaves nothing in fp32 and is taken as that, so that minus
 // infinity (a reset) does not turn differences of sums into NaN.
-template <typename T>
-__device__ __forceinline__ double la_decays(float* fac, const LaPassArgs& a, int64_t b, int h, int t0, int len,
-                                            int lane, bool active) {
+__device__ __forceinline__ double la_decays(float* fac, const float (&x)[2], bool reverse, float scale_o, float scale_w,
+                                            int lane) {
   double g[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int t = t0 + 2 * lane + i;
-    float x = 0.f;
-    if (active && t < len && in_range(t, len)) {
-      const char* p = la_row(a.g, b, t, h, sizeof(T));
-      x = to_f32(*reinterpret_cast<const T*>(p));
-    }
-    x = x < -1400.f ? -1400.f : x;
-    g[i] = (double)x * 1.4426950408889634;
-  }
+  for (int i = 0; i < 2; ++i) g[i] = (double)(x[i] < -1400.f ? -1400.f : x[i]) * 1.4426950408889634;
   double sum = g[0] + g[1];
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
@@ -214,396 +255,653 @@ __device__ __forceinline__ double la_decays(float* fac, const LaPassArgs& a, int
     const float hi = (float)at[i];
     fac[r] = hi;
     fac[kLaChunk + r] = (float)(at[i] - (double)hi);
-    const float from_start = (float)exp2(at[i]), to_end = (float)exp2(total - at[i]);
-    fac[2 * kLaChunk + r] = a.reverse ? to_end : from_start;  // rows
-    fac[3 * kLaChunk + r] = a.reverse ? from_start : to_end;  // keys
+    const float from_start = la_exp2(at[i]), to_end = la_exp2(total - at[i]);
+    fac[2 * kLaChunk + r] = (reverse ? to_end : from_start) * scale_o;  // rows
+    fac[3 * kLaChunk + r] = (reverse ? from_start : to_end) * scale_w;  // keys
   }
-  if (lane == 0) fac[4 * kLaChunk] = (float)exp2(total);
+  if (lane == 0) fac[4 * kLaChunk] = la_exp2(total);
   return total;
 }
 
-// Sum over the lanes of v[i], for every i at once: lane i gets the sum of v[i].
-__device__ __forceinline__ float la_column_sums(float (&v)[32], int lane) {
+template <int N>
+struct LaWidth {
+  static constexpr int value = N;
+};
+
+// 32 values x 32 tokens of a back warp to the output, and their products with the
+// rows of x.  o[h][4 i + z]: value v0 + 16 h + 8 (z / 2) + lane / 4, token
+// t0 + 8 i + 2 (lane % 4) + z % 2.  bf16 rows go through 1 KB of shared memory, so
+// that a token's 32 values leave as 64 bytes in 16-byte stores.
+template <typename T>
+__device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2][16], char* stage, int64_t b, int64_t bh,
+                                        int h, int t0, int len, int v0, int quad, int lane) {
+  const int64_t rs = (int64_t)a.heads * a.dv;
+  const int64_t at = ((b * a.seqlen + t0) * a.heads + h) * a.dv + v0;
+  if (sizeof(T) == 2 && !a.out_f32 && a.out_vec) {
+    const uint32_t to = smem_u32(stage) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+    const int tok = lane / 4, c = lane % 4;
+    const char* from = stage + tok * 64 + ((c ^ ((tok >> 1) & 3)) << 4);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at + tok * rs + c * 8;
+    const bool mine = v0 + c * 8 < a.dv;
 #pragma unroll
-  for (int o = 16; o >= 1; o /= 2) {
-    const bool up = lane & o;
+    for (int i = 0; i < 4; i += 2) {
 #pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = up ? v[i] : v[i + o];
-      const float keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(kFullMask, send, o);
+      for (int e = 0; e < 2; ++e)
+        store_blocks_t(to + e * 512, to_bf16x2(o[0][4 * (i + e)], o[0][4 * (i + e) + 1]),
+                       to_bf16x2(o[0][4 * (i + e) + 2], o[0][4 * (i + e) + 3]),
+                       to_bf16x2(o[1][4 * (i + e)], o[1][4 * (i + e) + 1]),
+                       to_bf16x2(o[1][4 * (i + e) + 2], o[1][4 * (i + e) + 3]));
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint4 y = *reinterpret_cast<const uint4*>(from + e * 512);
+        const int t = t0 + (i + e) * 8 + tok;
+        if (mine && t < len && in_range(t, a.seqlen)) *reinterpret_cast<uint4*>(out + (i + e) * 8 * rs) = y;
+      }
+      __syncwarp();
+    }
+  } else {
+    const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
+    const int64_t mine = at + lane / 4 + 2 * (lane % 4) * rs;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int64_t row = mine + (8 * i + z) * rs;
+        if (t + 8 * i + z < len && in_range(t + 8 * i + z, a.seqlen)) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (v + 8 * u < a.dv) {
+              const float y = o[u / 2][4 * i + 2 * (u % 2) + z];
+              if (sizeof(T) == 4 || a.out_f32) static_cast<float*>(a.out)[row + 8 * u] = y;
+              else static_cast<__nv_bfloat16*>(a.out)[row + 8 * u] = __float2bfloat16_rn(y);
+            }
+        }
+      }
+  }
+  if (a.x.ptr) {
+    const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
+    const char* from = la_row(a.x, b, t, h, sizeof(T)) + (int64_t)v * sizeof(T);
+    const int64_t xs = a.x.st * (int64_t)sizeof(T);
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        float y = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (t + 8 * i + z < len && v + 8 * u < a.dv)
+            y = fmaf(o[u / 2][4 * i + 2 * (u % 2) + z],
+                     to_f32(reinterpret_cast<const T*>(from + (8 * i + z) * xs)[8 * u]), y);
+        sum[2 * i + z] = y;
+      }
+    // the lanes with the same tokens are 4, 8 and 16 apart; lane / 4 keeps token pair it
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+      for (int m = 4; m <= 16; m *= 2) sum[s] += __shfl_xor_sync(kFullMask, sum[s], m);
+    if (lane < 4) {
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int tt = t + 8 * (s / 2) + s % 2;
+        if (tt < len) a.dots[(bh * a.seqlen + tt) * 4 + quad] = sum[s];
+      }
     }
   }
-  return v[0];
+}
+
+// What one CTA works through: pieces of heads, in the order of processing.
+struct LaPiece {
+  int64_t bh;
+  int first, last;   // real chunks [first, last), whichever way they are run
+  bool from_carry;   // starts from the previous worker's state
+  bool to_carry;     // ends inside its head
+};
+struct LaWork {
+  int64_t lo, hi;    // workers: range of padded chunks
+  int n, pieces, worker;
+};
+__device__ __forceinline__ LaWork la_work(const LaPassArgs& a, int worker) {
+  LaWork w;
+  w.worker = worker;
+  w.n = (a.seqlen + kLaChunk - 1) / kLaChunk;
+  w.pieces = 1;
+  w.lo = w.hi = 0;
+  if (a.workers > 0) {
+    const int64_t total = a.bh * w.n;
+    w.lo = total * worker / a.workers;
+    w.hi = total * (worker + 1) / a.workers;
+    // heads touched: a worker's range is at least a head long
+    w.pieces = (int)((w.hi + w.n - 1) / w.n - w.lo / w.n);
+  }
+  return w;
+}
+template <bool STATES>
+__device__ __forceinline__ LaPiece la_piece(const LaPassArgs& a, const LaWork& w, int i) {
+  LaPiece p;
+  int64_t p0, p1;  // places in the order of processing, padded
+  p.from_carry = p.to_carry = false;
+  if (a.workers > 0) {
+    // the head that the next worker goes on with comes first, the one that the
+    // previous worker began comes last
+    const int64_t h0 = w.lo / w.n, c0 = w.lo % w.n, h1 = w.hi / w.n, c1 = w.hi % w.n;
+    const bool tail = c1 > 0;
+    if (tail && i == 0) {
+      p.bh = h1, p0 = 0, p1 = c1, p.to_carry = true;
+    } else {
+      const int64_t whole0 = h0 + (c0 > 0 ? 1 : 0);
+      const int64_t h = whole0 + i - (tail ? 1 : 0);
+      if (h < h1) p.bh = h, p0 = 0, p1 = w.n;
+      else p.bh = h0, p0 = c0, p1 = w.n, p.from_carry = true;
+    }
+  } else {
+    const int step = w.worker % a.nseg;
+    p.bh = w.worker / a.nseg;
+    p0 = (int64_t)step * a.seg_chunks;
+    p1 = p0 + a.seg_chunks < w.n ? p0 + a.seg_chunks : w.n;
+    if (p0 > w.n) p0 = w.n;
+  }
+  const int all = (la_length(a, p.bh / a.heads) + kLaChunk - 1) / kLaChunk;
+  int64_t f = a.reverse ? w.n - p1 : p0, l = a.reverse ? w.n - p0 : p1;
+  p.first = (int)(f < all ? f : all);
+  p.last = (int)(l < all ? l : all);
+  return p;
 }
 
 // STATES: only the states (the sequence's segments, each from zero, all at once).
 template <typename T, int KD, int VD, bool STATES>
-__global__ void __launch_bounds__(LaCfg<T, KD, VD>::kThreads, 1) linattn_pass_kernel(const __grid_constant__ LaPassArgs a) {
+__global__ void __launch_bounds__(LaCfg<T, KD, VD>::kThreads, 1)
+linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant__ LaMaps maps) {
   using CF = LaCfg<T, KD, VD>;
-  constexpr int NPI = CF::NPI, NPX = CF::NPX, ST = CF::kStages;
-  extern __shared__ char la_smem_raw[];
-  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(la_smem_raw) + 1023) & ~uintptr_t(1023));
-  float* fac_all = reinterpret_cast<float*>(smem + CF::kFac);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(fac_all + ST * (4 * kLaChunk + 4));
-  uint64_t *b_full = bars, *b_empty = bars + 2, *b_qk = bars + 4, *b_pk = bars + 5, *b_s = bars + 6, *b_ds = bars + 7;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 8);
-  volatile int* dead = reinterpret_cast<int*>(tmem_at + 1);
+  constexpr int NPI = CF::NPI, NPX = CF::NPX, NPW = CF::NPW;
+  extern __shared__ __align__(1024) char smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + CF::kBars);
+  uint64_t *full_k = bars, *empty_k = bars + 2, *full_v = bars + 4, *empty_v = bars + 6, *full_q = bars + 8,
+           *empty_q = bars + 11, *full_f = bars + 14, *empty_f = bars + 18;
+  uint64_t *b_qk = bars + 22;  // scores are there
+  uint64_t *b_pk = bars + 23;  // P and the weighted keys are there
+  uint64_t *b_ds = bars + 24;  // increment and P V are there
+  uint64_t *b_o = bars + 25;   // S Q too: the chunk's products are done
+  uint64_t *b_free = bars + 26;  // the back warps have read them
+  uint64_t *b_s = bars + 27;   // the state's planes are there
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 28);
+  int* worker_at = reinterpret_cast<int*>(tmem_at + 1);
+  volatile int* dead = worker_at + 1;
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t bh = blockIdx.x / a.nseg;
-  const int step = (int)(blockIdx.x % a.nseg);  // the segment's place in the order of processing
-  const int64_t b = bh / a.heads;
-  const int h = (int)(bh % a.heads);
-  const int len = la_length(a, b);
-  const int all_chunks = (len + kLaChunk - 1) / kLaChunk;
-  const int total_segs = STATES ? a.nseg + 1 : a.nseg;  // the last one's states are nobody's start
-  const int seg = a.reverse ? total_segs - 1 - step : step;
-  const int64_t first64 = (int64_t)seg * a.seg_chunks;
-  const int first = first64 < all_chunks ? (int)first64 : all_chunks;
-  const int last = first64 + a.seg_chunks < all_chunks ? (int)(first64 + a.seg_chunks) : all_chunks;
-  const int n_chunks = last - first;
-  auto chunk_at = [&](int n) { return a.reverse ? last - 1 - n : first + n; };
-
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&b_full[i], 32 * CF::kLoadWarps);
-      mbar_init(&b_empty[i], CF::kComputeWarps);
-    }
+    for (int i = 0; i < CF::RK; ++i) mbar_init(&full_k[i], CF::kLoaders), mbar_init(&empty_k[i], kLaFrontWarps + (STATES ? 0 : 1));
+    for (int i = 0; i < CF::RV; ++i) mbar_init(&full_v[i], CF::kLoaders), mbar_init(&empty_v[i], 1);
+    for (int i = 0; i < CF::RQ; ++i) mbar_init(&full_q[i], CF::kLoaders), mbar_init(&empty_q[i], 1);
+    for (int i = 0; i < CF::RF; ++i) mbar_init(&full_f[i], 1), mbar_init(&empty_f[i], kLaFrontWarps + CF::kHolders);
     mbar_init(b_qk, 1);
-    mbar_init(b_pk, CF::kComputeWarps);
-    mbar_init(b_s, CF::kComputeWarps);
+    mbar_init(b_pk, kLaFrontWarps);
     mbar_init(b_ds, 1);
+    mbar_init(b_o, 1);
+    mbar_init(b_free, CF::kHolders);
+    mbar_init(b_s, CF::kHolders);
     fence_mbar_init();
     *dead = 0;
+    // workers are numbered in the order in which they start, so that the one a
+    // worker may wait for is running
+    *worker_at = a.workers > 0 ? (int)atomicAdd(a.flags, 1u) : (int)blockIdx.x;
   }
-  if (warp == CF::kComputeWarps) tmem_alloc(tmem_at, CF::kCols);
+  if (warp == kLaMmaWarp) tmem_alloc(tmem_at, CF::kCols);
   tc5_fence_before();
   __syncthreads();
   tc5_fence_after();
   const uint32_t tmem = *tmem_at;
+  const LaWork work = la_work(a, *worker_at);
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
 
-  if (warp > CF::kComputeWarps) {
-    // ---- loaders
-    const int ltid = tid - 32 * (CF::kComputeWarps + 1);
-    double sum = 0.0;
-    for (int n = 0; n <= n_chunks; ++n) {
-      if (n < n_chunks) {
-        const int s = n % ST;
-        if (n >= ST) la_wait(&b_empty[s], (uint32_t)((n / ST - 1) & 1), dead);
-        const int t0 = chunk_at(n) * kLaChunk;
-        char* st = smem + s * CF::kStageBytes;
-        la_load_tile<T, KD>(st + CF::kK, a.k, b, h, t0, len, a.dk, a.vec, ltid, 32 * CF::kLoadWarps);
-        if (!STATES) la_load_tile<T, KD>(st + CF::kQ, a.q, b, h, t0, len, a.dk, a.vec, ltid, 32 * CF::kLoadWarps);
-        la_load_tile<T, VD>(st + CF::kV, a.v, b, h, t0, len, a.dv, a.vec, ltid, 32 * CF::kLoadWarps);
-        if (ltid < 32) sum += la_decays<T>(fac_all + s * (4 * kLaChunk + 4), a, b, h, t0, len, lane, true);
-        cp_async_commit();
-      }
-      // the tiles that are signalled now: with two stages the previous chunk's
-      const int m = ST == 1 ? n : n - 1;
-      if (m >= 0 && m < n_chunks) {
-        if (ST == 1 || n == n_chunks) asm volatile("cp.async.wait_group 0;\n" ::: "memory");
-        else asm volatile("cp.async.wait_group 1;\n" ::: "memory");
-        fence_proxy_async_smem();
-        mbar_arrive(&b_full[m % ST]);
-      }
-    }
-    if (STATES && ltid == 0) a.seg_decay[bh * total_segs + step] = sum;
-  } else if (warp == CF::kComputeWarps) {
-    // ---- MMA issue, one thread
-    if (lane == 0) {
+  if (warp >= kLaMmaWarp) {
+    regs_give<kLaAuxRegs>();
+    if (warp == kLaMmaWarp) {
+      // ---- MMA issue, by one thread of the warp
       const uint32_t base = smem_u32(smem);
-      auto tile = [&](int s, int what, int blocks, int plane) {
-        return base + s * CF::kStageBytes + what + plane * blocks * kLaBlock;
-      };
+      const bool leader = elect_one();
       auto scores = [&](int n) {
-        const int s = n % ST;
-        la_wait(&b_full[s], (uint32_t)((n / ST) & 1), dead);
+        la_wait(&full_k[n % CF::RK], (uint32_t)((n / CF::RK) & 1), dead);
+        la_wait(&full_q[n % CF::RQ], (uint32_t)((n / CF::RQ) & 1), dead);
         tc5_fence_after();
-        constexpr uint32_t id = mma_idesc(64, false, false);
-        bool add = false;
-        for (int pa = NPI - 1; pa >= 0; --pa)
-          for (int pb = (NPI < CF::NPMAX - pa ? NPI : CF::NPMAX - pa) - 1; pb >= 0; --pb)
+        if (leader) {
+          const uint64_t q = tile_desc(base + CF::kQ + (n % CF::RQ) * CF::kTileK, 0);
+          const uint64_t k = tile_desc(base + CF::kK + (n % CF::RK) * CF::kTileK, 0);
+          constexpr uint32_t id = mma_idesc(64, 64, false, false);
+          // the products of smaller planes first: they add up while the sum is small
 #pragma unroll
-            for (int kk = 0; kk < KD; kk += 16) {
-              const uint32_t off = (kk / 64) * kLaBlock + (kk % 64) * 2;
-              mma_ss(tmem + CF::cQK, tile_desc(tile(s, CF::kQ, CF::KB, pa) + off, 0),
-                     tile_desc(tile(s, CF::kK, CF::KB, pb) + off, 0), id, add);
-              add = true;
-            }
-        mma_commit(b_qk);
+          for (int pa = NPI - 1; pa >= 0; --pa)
+#pragma unroll
+            for (int pb = NPI - pa - 1; pb >= 0; --pb)
+#pragma unroll
+              for (int kk = 0; kk < KD; kk += 16) {
+                const uint32_t off = (kk / 64) * kLaBlock + (kk % 64) * 2;
+                mma_ss(tmem + CF::cQK, q + ((pa * CF::KB * kLaBlock + off) >> 4), k + ((pb * CF::KB * kLaBlock + off) >> 4),
+                       id, !(pa == NPI - 1 && kk == 0));
+              }
+          mma_commit(b_qk);
+          mma_commit(&empty_k[n % CF::RK]);
+        }
+        __syncwarp();
       };
-      if (!STATES && n_chunks > 0) scores(0);
-      for (int n = 0; n < n_chunks; ++n) {
-        const int s = n % ST;
+      int total = 0, scored = 0;
+      for (int i = 0; i < work.pieces; ++i) {
+        const LaPiece p = la_piece<STATES>(a, work, i);
+        total += p.last - p.first;
+      }
+      if (!STATES && total > 0) scores(scored++);
+      for (int n = 0; n < total; ++n) {
+        const uint64_t v = tile_desc(base + CF::kV + (n % CF::RV) * CF::kTileV, kLaBlock);
+        const uint64_t w = tile_desc(base + CF::kW + (n % CF::RW) * CF::kTileW, kLaBlock);
+        la_wait(b_pk, (uint32_t)(n & 1), dead);
+        tc5_fence_after();
+        if (!STATES && CF::RQ > 1 && scored < total) scores(scored++);
+        la_wait(&full_v[n % CF::RV], (uint32_t)((n / CF::RV) & 1), dead);
+        if (n > 0) la_wait(b_free, (uint32_t)((n - 1) & 1), dead);
+        tc5_fence_after();
+        if (leader) {
+          {
+            // dS^T = V^T (w . K)
+            constexpr uint32_t id = mma_idesc(128, KD, true, true);
+#pragma unroll
+            for (int pa = NPI - 1; pa >= 0; --pa)
+#pragma unroll
+              for (int pb = NPW - pa - 1; pb >= 0; --pb)
+#pragma unroll
+                for (int j = 0; j < kLaChunk; j += 16)
+                  mma_ss(tmem + CF::cDS, v + ((pa * CF::VB * kLaBlock + j * kTileRow) >> 4),
+                         w + ((pb * CF::KB * kLaBlock + j * kTileRow) >> 4), id, !(pa == NPI - 1 && pb == NPW - NPI && j == 0));
+          }
+          if (!STATES) {
+            // O1^T = V^T P^T
+            constexpr uint32_t id = mma_idesc(128, 64, true, false);
+            const uint64_t pd = tile_desc(base + CF::kP, 0);
+#pragma unroll
+            for (int pa = NPI - 1; pa >= 0; --pa)
+#pragma unroll
+              for (int pb = NPX - pa - 1; pb >= 0; --pb)
+#pragma unroll
+                for (int j = 0; j < kLaChunk; j += 16)
+                  mma_ss(tmem + CF::cO1, v + ((pa * CF::VB * kLaBlock + j * kTileRow) >> 4),
+                         pd + ((pb * kLaBlock + j * 2) >> 4), id, !(pa == NPI - 1 && pb == NPX - NPI && j == 0));
+          }
+          mma_commit(b_ds);
+          mma_commit(&empty_v[n % CF::RV]);
+        }
+        __syncwarp();
         if (!STATES) {
           // O2^T = S^T Q^T
           la_wait(b_s, (uint32_t)(n & 1), dead);
           tc5_fence_after();
-          constexpr uint32_t id = mma_idesc(64, false, false);
-          bool add = false;
-          for (int pa = NPX - 1; pa >= 0; --pa)
-            for (int pb = (NPI < CF::NPMAX - pa ? NPI : CF::NPMAX - pa) - 1; pb >= 0; --pb)
+          if (leader) {
+            const uint64_t q = tile_desc(base + CF::kQ + (n % CF::RQ) * CF::kTileK, 0);
+            constexpr uint32_t id = mma_idesc(128, 64, false, false);
 #pragma unroll
-              for (int kk = 0; kk < KD; kk += 16) {
-                const uint32_t off = (kk / 64) * kLaBlock + (kk % 64) * 2;
-                mma_ts(tmem + CF::cO2, tmem + CF::cSP + pa * (KD / 2) + kk / 2,
-                       tile_desc(tile(s, CF::kQ, CF::KB, pb) + off, 0), id, add);
-                add = true;
-              }
-        } else {
-          la_wait(&b_full[s], (uint32_t)((n / ST) & 1), dead);
+            for (int pa = NPX - 1; pa >= 0; --pa)
+#pragma unroll
+              for (int pb = (NPI < NPX - pa ? NPI : NPX - pa) - 1; pb >= 0; --pb)
+#pragma unroll
+                for (int kk = 0; kk < KD; kk += 16)
+                  mma_ts(tmem + CF::cO2, tmem + CF::cSP + pa * (KD / 2) + kk / 2,
+                         q + ((pb * CF::KB * kLaBlock + (kk / 64) * kLaBlock + (kk % 64) * 2) >> 4), id,
+                         !(pa == NPX - 1 && kk == 0));
+            mma_commit(b_o);
+            mma_commit(&empty_q[n % CF::RQ]);
+          }
+          __syncwarp();
+          // with one tile in the ring the next queries only come now
+          if (CF::RQ == 1 && scored < total) scores(scored++);
         }
-        la_wait(b_pk, (uint32_t)(n & 1), dead);
-        tc5_fence_after();
+      }
+    } else if (warp == kLaDecayWarp) {
+      // ---- decays
+      int n = 0;
+      for (int i = 0; i < work.pieces; ++i) {
+        const LaPiece p = la_piece<STATES>(a, work, i);
+        const int64_t b = p.bh / a.heads;
+        const int h = (int)(p.bh % a.heads), len = la_length(a, b);
+        double sum = 0.0;
+        auto place = [&](int c) { return (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk; };
+        float x[2], next[2];
+        if (p.first < p.last) la_fetch_decays<T>(next, a, b, h, place(p.first), len, lane);
+        for (int c = p.first; c < p.last; ++c, ++n) {
+          const int s = (int)(n % CF::RF);
+          x[0] = next[0], x[1] = next[1];
+          if (c + 1 < p.last) la_fetch_decays<T>(next, a, b, h, place(c + 1), len, lane);
+          if (n >= CF::RF) la_wait(&empty_f[s], (uint32_t)((n / CF::RF - 1) & 1), dead);
+          sum += la_decays(reinterpret_cast<float*>(smem + CF::kFac) + s * CF::kFacFloats, x, a.reverse, a.scale_o,
+                           a.scale_w, lane);
+          arrive(&full_f[s]);
+        }
+        if (STATES && lane == 0) a.seg_decay[p.bh * (a.nseg + 1) + work.worker % a.nseg] = sum;
+      }
+    } else {
+      // ---- loaders
+      const int ltid = tid - 32 * kLaLoadWarp;
+      int n = 0;
+      for (int i = 0; i < work.pieces; ++i) {
+        const LaPiece p = la_piece<STATES>(a, work, i);
+        const int b = (int)(p.bh / a.heads);
+        const int h = (int)(p.bh % a.heads), len = la_length(a, b);
+        for (int c = p.first; c < p.last; ++c, ++n) {
+          const int t0 = (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk;
+          // TMA clips at the tensor's end, not at a row's length
+          const bool by_tma = CF::kBf16 && a.tma && (t0 + kLaChunk <= len || len == a.seqlen);
+          auto tile = [&](auto width, const LaTensor& x, const CUtensorMap* map, int ring, int at, int bytes,
+                          uint64_t* full, uint64_t* empty, int d) {
+            constexpr int DP = decltype(width)::value;
+            const int s = (int)(n % ring);
+            if (n >= ring) la_wait(&empty[s], (uint32_t)((n / ring - 1) & 1), dead);
+            char* to = smem + at + s * bytes;
+            if (by_tma) {
+              if (ltid == 0) {
+                mbar_arrive_expect_tx(&full[s], DP / 64 * kLaBlock);
+                for (int j = 0; j < DP / 64; ++j)
+                  tma_load_block(to + j * kLaBlock, map, &full[s], j * 64, t0, h / x.share, b);
+              } else {
+                mbar_arrive(&full[s]);
+              }
+            } else {
+              la_load_tile<T, DP>(to, x, b, h, t0, len, d, a.vec, ltid, CF::kLoaders);
+              if (CF::kBf16 && a.vec) {
+                cp_async_commit();
+                cp_async_wait_all();
+              }
+              fence_proxy_async_smem();
+              mbar_arrive(&full[s]);
+            }
+          };
+          tile(LaWidth<KD>{}, a.k, &maps.k, CF::RK, CF::kK, CF::kTileK, full_k, empty_k, a.dk);
+          if (!STATES) tile(LaWidth<KD>{}, a.q, &maps.q, CF::RQ, CF::kQ, CF::kTileK, full_q, empty_q, a.dk);
+          tile(LaWidth<VD>{}, a.v, &maps.v, CF::RV, CF::kV, CF::kTileV, full_v, empty_v, a.dv);
+        }
+      }
+    }
+  } else if (warp >= kLaBackWarps) {
+    // ---- front: weighted keys and P, a chunk ahead of the back
+    regs_give<kLaFrontRegs>();
+    const int fw = warp - kLaBackWarps, ftid = tid - 32 * kLaBackWarps;
+    int n = 0;
+    if (!STATES) {
+      // what the mask takes away is zero once and for all
+      for (int i = ftid; i < NPX * kLaBlock / 16; i += 32 * kLaFrontWarps)
+        reinterpret_cast<uint4*>(smem + CF::kP)[i] = make_uint4(0, 0, 0, 0);
+      asm volatile("bar.sync 1, 128;\n" ::: "memory");
+    }
+    for (int i = 0; i < work.pieces; ++i) {
+      const LaPiece p = la_piece<STATES>(a, work, i);
+      for (int c = p.first; c < p.last; ++c, ++n) {
+        const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + (int)(n % CF::RF) * CF::kFacFloats;
+        la_wait(&full_f[n % CF::RF], (uint32_t)((n / CF::RF) & 1), dead);
+        la_wait(&full_k[n % CF::RK], (uint32_t)((n / CF::RK) & 1), dead);
+        if (CF::RW == 1 && n > 0) la_wait(b_ds, (uint32_t)((n - 1) & 1), dead);
         {
-          // dS^T = V^T (w . K)
-          constexpr uint32_t id = mma_idesc(KD, true, true);
-          bool add = false;
-          for (int pa = NPI - 1; pa >= 0; --pa)
-            for (int pb = (NPX < CF::NPMAX - pa ? NPX : CF::NPMAX - pa) - 1; pb >= 0; --pb)
+          // the keys weighted by their decay to the chunk's end (reversed: start)
+          const char* k = smem + CF::kK + (int)(n % CF::RK) * CF::kTileK;
+          char* w = smem + CF::kW + (int)(n % CF::RW) * CF::kTileW;
+#pragma unroll 2
+          for (int u = ftid; u < CF::KB * 512; u += 32 * kLaFrontWarps) {
+            const int row = (u % 512) / 8;
+            const float wj = fac[3 * kLaChunk + row];
+            const uint64_t ww = pair(wj, wj);
+            const int off = (u / 512) * kLaBlock + row * kTileRow + (u % 8) * 16;
+            uint32_t in[NPI][4];
 #pragma unroll
-              for (int j = 0; j < kLaChunk; j += 16) {
-                mma_ss(tmem + CF::cDS, tile_desc(tile(s, CF::kV, CF::VB, pa) + j * kTileRow, kLaBlock),
-                       tile_desc(base + CF::kW + pb * CF::KB * kLaBlock + j * kTileRow, kLaBlock), id, add);
-                add = true;
-              }
-        }
-        if (!STATES) {
-          // O1^T = V^T P^T
-          constexpr uint32_t id = mma_idesc(64, true, false);
-          bool add = false;
-          for (int pa = NPI - 1; pa >= 0; --pa)
-            for (int pb = (NPX < CF::NPMAX - pa ? NPX : CF::NPMAX - pa) - 1; pb >= 0; --pb)
+            for (int q = 0; q < NPI; ++q) {
+              const uint4 y = *reinterpret_cast<const uint4*>(k + q * CF::KB * kLaBlock + off);
+              in[q][0] = y.x, in[q][1] = y.y, in[q][2] = y.z, in[q][3] = y.w;
+            }
+            uint32_t out[NPW][4];
 #pragma unroll
-              for (int j = 0; j < kLaChunk; j += 16) {
-                mma_ss(tmem + CF::cO1, tile_desc(tile(s, CF::kV, CF::VB, pa) + j * kTileRow, kLaBlock),
-                       tile_desc(base + CF::kP + pb * kLaBlock + j * 2, 0), id, add);
-                add = true;
-              }
-        }
-        mma_commit(b_ds);
-        if (!STATES && n + 1 < n_chunks) scores(n + 1);
-      }
-    }
-    __syncwarp();
-  } else {
-    // ---- compute
-    const int quad = warp % 4, half = warp / 4;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const int vi = quad * 32 + lane;          // this thread's value index
-    const bool holds = quad * 32 < VD;        // warps whose lanes hold a state
-    constexpr int KH = KD / 2;                // its key indices: half * KH ...
-    float S[KH];
-    auto store_planes = [&]() {
+            for (int e = 0; e < 4; ++e) {
+              uint64_t y = from_bf16x2(in[NPI - 1][e]);
 #pragma unroll
-      for (int c = 0; c < KH; c += 32) {
-        uint32_t w[NPX][16];
+              for (int q = NPI - 2; q >= 0; --q) y = add2(y, from_bf16x2(in[q][e]));  // exact from the smallest
+              uint32_t sp[NPW];
+              split2<NPW>(mul2(y, ww), sp);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          uint32_t s[NPX];
-          split2<NPX>(S[c + 2 * i], S[c + 2 * i + 1], s);
+              for (int q = 0; q < NPW; ++q) out[q][e] = sp[q];
+            }
 #pragma unroll
-          for (int p = 0; p < NPX; ++p) w[p][i] = s[p];
-        }
-#pragma unroll
-        for (int p = 0; p < NPX; ++p)
-          tmem_st16(lanes + CF::cSP + p * (KD / 2) + half * (KD / 4) + c / 2, w[p]);
-      }
-      tmem_wait_st();
-    };
-    auto arrive = [&](uint64_t* bar) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-    {
-      const float* from = a.s_in && !STATES ? a.s_in + bh * a.s_in_head + step * a.s_in_seg : nullptr;
-#pragma unroll
-      for (int c = 0; c < KH; ++c) {
-        const int kk = half * KH + c;
-        S[c] = from && holds && vi < a.dv && kk < a.dk ? from[kk * a.sk + vi * a.sv] : 0.f;
-      }
-      if (!STATES) {
-        if (holds) store_planes();
-        tc5_fence_before();
-        arrive(b_s);
-      }
-    }
-    for (int n = 0; n < n_chunks; ++n) {
-      const int s = n % ST;
-      const int chunk = chunk_at(n), t0 = chunk * kLaChunk;
-      const float* fac = fac_all + s * (4 * kLaChunk + 4);
-      char* st = smem + s * CF::kStageBytes;
-      const bool anchor_here = a.dump && ((chunk + 1) % a.anchor_chunks == 0 || chunk == all_chunks - 1);
-      if (!STATES && a.reverse && anchor_here) {
-        // <R, S> behind this chunk: R is the state here, S the forward pass's
-        float sum = 0.f;
-        const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
-        if (holds) {
-          const float* from = a.dump + (an * 8 + warp) * (KH * 32);
-#pragma unroll
-          for (int c = 0; c < KH; c += 4) {
-            const float4 x = reinterpret_cast<const float4*>(from)[c / 4 * 32 + lane];
-            sum += S[c] * x.x + S[c + 1] * x.y + S[c + 2] * x.z + S[c + 3] * x.w;
+            for (int q = 0; q < NPW; ++q)
+              *reinterpret_cast<uint4*>(w + q * CF::KB * kLaBlock + off) =
+                  make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
           }
         }
-#pragma unroll
-        for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
-        if (lane == 0) a.anchor[an * 8 + warp] = sum;
-      }
-      la_wait(&b_full[s], (uint32_t)((n / ST) & 1), dead);
-      if (!STATES && quad < 2) {
-        // P = (Q K^T) . D, rows in the lanes
-        la_wait(b_qk, (uint32_t)(n & 1), dead);
-        tc5_fence_after();
-        uint32_t x[32];
-        tmem_ld32(x, lanes + CF::cQK + half * 32);
-        tmem_wait_ld(x);
-        const int row = quad * 32 + lane;
-        const float ghi = fac[row], glo = fac[kLaChunk + row];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t w[NPX][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float p[2];
+        arrive(&empty_k[n % CF::RK]);
+        // never two chunks ahead of the products that take what is made here
+        if (STATES && CF::RW > 1 && n > 0) la_wait(b_ds, (uint32_t)((n - 1) & 1), dead);
+        if (!STATES) {
+          // P = (Q K^T) . D: 16 rows a warp, two rows a thread
+          la_wait(b_qk, (uint32_t)(n & 1), dead);
+          tc5_fence_after();
+          if (CF::RW > 1 && n > 0) la_wait(b_ds, (uint32_t)((n - 1) & 1), dead);  // the last P was used
+          const int r0 = fw * 16 + lane / 4;
+          const float sign = a.reverse ? -1.f : 1.f;
+          const float h0 = fac[r0], l0 = fac[kLaChunk + r0], h1 = fac[r0 + 8], l1 = fac[kLaChunk + r0 + 8];
+          const uint64_t hh[2] = {pair(h0, h0), pair(h1, h1)}, ll[2] = {pair(l0, l0), pair(l1, l1)};
+          const uint64_t minus = pair(-1.f, -1.f), sp2 = pair(a.scale_p, a.scale_p);
+          const int c0 = 2 * (lane % 4);
+          // this lane's row address for store_blocks: blocks (rows 0-7, 8-15) x two column blocks
+          const int srow = fw * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+          // 16 columns at a time, those that the mask leaves (the others stay zero)
+          const int from = a.reverse ? fw : 0, to = a.reverse ? 4 : fw + 1;
+#pragma unroll 1
+          for (int cb = from; cb < to; ++cb) {
+            uint32_t x[8];
+            tmem_ld_rows16(x, tmem + ((uint32_t)(fw * 32) << 16) + CF::cQK + cb * 16);
+            uint64_t gh[2], gl[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int c = u * 8 + i * 2 + e, j = half * 32 + c;
-              const float d = (ghi - fac[j]) + (glo - fac[kLaChunk + j]);
-              const float y = __uint_as_float(x[c]) * a.scale_p * ex2_approx(a.reverse ? -d : d);
-              p[e] = (a.reverse ? j >= row : j <= row) ? y : 0.f;
+              gh[e] = *reinterpret_cast<const uint64_t*>(fac + cb * 16 + e * 8 + c0);
+              gl[e] = *reinterpret_cast<const uint64_t*>(fac + kLaChunk + cb * 16 + e * 8 + c0);
             }
-            uint32_t sp[NPX];
-            split2<NPX>(p[0], p[1], sp);
+            tmem_wait_ld(x);
+            uint32_t o[NPX][4];
 #pragma unroll
-            for (int q = 0; q < NPX; ++q) w[q][i] = sp[q];
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint64_t d = add2(fma2(gh[e], minus, hh[z]), fma2(gl[e], minus, ll[z]));
+                const uint64_t f = pair(ex2_approx(pair_lo(d) * sign), ex2_approx(pair_hi(d) * sign));
+                uint64_t y = mul2(mul2(pair(x[4 * e + 2 * z], x[4 * e + 2 * z + 1]), sp2), f);
+                if (cb == fw) {
+                  const int row = lane / 4 + 8 * z, col = 8 * e + c0;
+                  y = pair((a.reverse ? col >= row : col <= row) ? pair_lo(y) : 0.f,
+                           (a.reverse ? col + 1 >= row : col + 1 <= row) ? pair_hi(y) : 0.f);
+                }
+                uint32_t sp[NPX];
+                split2<NPX>(y, sp);
+#pragma unroll
+                for (int q = 0; q < NPX; ++q) o[q][e * 2 + z] = sp[q];
+              }
+#pragma unroll
+            for (int q = 0; q < NPX; ++q)
+              store_blocks(smem_u32(smem) + CF::kP + q * kLaBlock + tile_unit(srow, cb * 2 + (lane >> 4)), o[q][0], o[q][1],
+                           o[q][2], o[q][3]);
           }
-#pragma unroll
-          for (int q = 0; q < NPX; ++q)
-            *reinterpret_cast<uint4*>(smem + CF::kP + q * kLaBlock + tile_unit(row, half * 4 + u)) =
-                make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+          tc5_fence_before();
         }
-        tc5_fence_before();
-      } else {
-        // the keys weighted by their decay to the chunk's end (reversed: start)
-        const int me = STATES ? warp * 32 + lane : (half * 2 + quad - 2) * 32 + lane;
-        constexpr int NT = STATES ? 256 : 128;
-        for (int u = me; u < CF::KB * 512; u += NT) {
-          const int row = (u % 512) / 8;
-          const float wj = fac[3 * kLaChunk + row] * a.scale_w;
-          const int off = (u / 512) * kLaBlock + row * kTileRow + (u % 8) * 16;
-          uint32_t in[NPI][4];
+        fence_proxy_async_smem();
+        arrive(b_pk);
+        arrive(&empty_f[n % CF::RF]);
+      }
+    }
+  } else {
+    // ---- back: the state and the outputs
+    regs_take<kLaBackRegs>();
+    const int quad = warp % 4, half = warp / 4;
+    if (quad < CF::kQuads) {
+      const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+      const int vi = quad * 32 + lane;          // this thread's value index
+      constexpr int KH = KD / 2;                // its key indices: half * KH ...
+      uint64_t S[KH / 2];                       // in pairs
+      auto store_planes = [&]() {
 #pragma unroll
-          for (int p = 0; p < NPI; ++p) {
-            const uint4 y = *reinterpret_cast<const uint4*>(st + CF::kK + p * CF::KB * kLaBlock + off);
-            in[p][0] = y.x, in[p][1] = y.y, in[p][2] = y.z, in[p][3] = y.w;
-          }
-          uint32_t w[NPX][4];
+        for (int c = 0; c < KH; c += 32) {
+          uint32_t w[NPX][16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float lo = 0.f, hi = 0.f;
+          for (int i = 0; i < 16; ++i) {
+            uint32_t s[NPX];
+            split2<NPX>(S[c / 2 + i], s);
 #pragma unroll
-            for (int p = NPI - 1; p >= 0; --p) {  // the planes add up exactly from the smallest
-              lo += __uint_as_float(in[p][i] << 16);
-              hi += __uint_as_float(in[p][i] & 0xffff0000u);
-            }
-            uint32_t sp[NPX];
-            split2<NPX>(lo * wj, hi * wj, sp);
-#pragma unroll
-            for (int p = 0; p < NPX; ++p) w[p][i] = sp[p];
+            for (int p = 0; p < NPX; ++p) w[p][i] = s[p];
           }
 #pragma unroll
           for (int p = 0; p < NPX; ++p)
-            *reinterpret_cast<uint4*>(smem + CF::kW + p * CF::KB * kLaBlock + off) =
-                make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+            tmem_st16(lanes + CF::cSP + p * (KD / 2) + half * (KD / 4) + c / 2, w[p]);
         }
-      }
-      fence_proxy_async_smem();
-      arrive(b_pk);
-
-      la_wait(b_ds, (uint32_t)(n & 1), dead);
-      tc5_fence_after();
-      const float decay = fac[4 * kLaChunk];
-      if (!STATES && holds) {
-        uint32_t x1[32], x2[32];
-        tmem_ld32(x1, lanes + CF::cO1 + half * 32);
-        tmem_ld32(x2, lanes + CF::cO2 + half * 32);
-        tmem_wait_ld(x1);
-        tmem_wait_ld(x2);
-        float o[32];
+        tmem_wait_st();
+      };
+      int n = 0;
+      for (int i = 0; i < work.pieces; ++i) {
+        const LaPiece p = la_piece<STATES>(a, work, i);
+        const int64_t b = p.bh / a.heads, bh = p.bh;
+        const int h = (int)(bh % a.heads), len = la_length(a, b);
+        const int all_chunks = (len + kLaChunk - 1) / kLaChunk;
+        const int step = a.workers > 0 ? 0 : work.worker % a.nseg;
+        if (p.from_carry) {
+          const unsigned* flag = a.flags + 1 + (work.worker - 1) * 8 + warp;
+          if (lane == 0) {
+            unsigned there = 0;
+            for (uint32_t spin = 0; spin < kLaSpinLimit && !there && !*dead; ++spin) {
+              asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(there) : "l"(flag) : "memory");
+              if (!there) __nanosleep(64);
+            }
+            if (!there && !*dead) {
+              atomicOr(&g_error_word, kErrLookback);
+              *dead = 1;
+            }
+          }
+          __syncwarp();
+          const float4* from = reinterpret_cast<const float4*>(a.carry + ((int64_t)(work.worker - 1) * 8 + warp) * (KH * 32));
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          o[c] = fmaf(__uint_as_float(x2[c]), fac[2 * kLaChunk + half * 32 + c] * a.scale_o, __uint_as_float(x1[c]));
-        const int tb = t0 + half * 32;
-        if (vi < a.dv) {
-          const int64_t rs = (int64_t)a.heads * a.dv;
-          const int64_t at = ((b * a.seqlen + tb) * a.heads + h) * a.dv + vi;
-          if (sizeof(T) == 4 || a.out_f32) {
-            float* to = static_cast<float*>(a.out) + at;
+          for (int c = 0; c < KH; c += 4) {
+            const float4 x = __ldcg(from + c / 4 * 32 + lane);
+            S[c / 2] = pair(x.x, x.y), S[c / 2 + 1] = pair(x.z, x.w);
+          }
+        } else {
+          const float* from = a.s_in && !STATES ? a.s_in + bh * a.s_in_head + step * a.s_in_seg : nullptr;
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (tb + c < len && in_range(tb + c, a.seqlen)) to[c * rs] = o[c];
-          } else {
-            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at;
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (tb + c < len && in_range(tb + c, a.seqlen)) to[c * rs] = __float2bfloat16_rn(o[c]);
+          for (int c = 0; c < KH; c += 2) {
+            const int kk = half * KH + c;
+            const bool in = from && vi < a.dv;
+            S[c / 2] = pair(in && kk < a.dk ? from[kk * a.sk + vi * a.sv] : 0.f,
+                            in && kk + 1 < a.dk ? from[(kk + 1) * a.sk + vi * a.sv] : 0.f);
           }
         }
-        if (a.x.ptr) {
-          const char* from = la_row(a.x, b, tb, h, sizeof(T)) + (int64_t)vi * sizeof(T);
-          const int64_t rs = a.x.st * (int64_t)sizeof(T);
+        // every MMA that read the planes before is done (b_o of the last chunk)
+        auto give_state = [&]() {
+          store_planes();
+          tc5_fence_before();
+          arrive(b_s);
+        };
+        if (!STATES && p.first < p.last) give_state();
+        for (int cc = p.first; cc < p.last; ++cc, ++n) {
+          const int chunk = a.reverse ? p.last - 1 - (cc - p.first) : cc, t0 = chunk * kLaChunk;
+          const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + (int)(n % CF::RF) * CF::kFacFloats;
+          const bool anchor_here = a.dump && ((chunk + 1) % a.anchor_chunks == 0 || chunk == all_chunks - 1);
+          if (!STATES && a.reverse && anchor_here) {
+            // <R, S> behind this chunk: R is the state here, S the forward pass's
+            float sum = 0.f;
+            const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
+            const float* from = a.dump + (an * 8 + warp) * (KH * 32);
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            o[c] = vi < a.dv && tb + c < len ? o[c] * to_f32(*reinterpret_cast<const T*>(from + c * rs)) : 0.f;
-          const float sum = la_column_sums(o, lane);
-          if (tb + lane < len) a.dots[(bh * a.seqlen + tb + lane) * 4 + quad] = sum;
+            for (int c = 0; c < KH; c += 4) {
+              const float4 x = reinterpret_cast<const float4*>(from)[c / 4 * 32 + lane];
+              sum += pair_lo(S[c / 2]) * x.x + pair_hi(S[c / 2]) * x.y + pair_lo(S[c / 2 + 1]) * x.z + pair_hi(S[c / 2 + 1]) * x.w;
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
+            if (lane == 0) a.anchor[an * 8 + warp] = sum;
+          }
+          la_wait(&full_f[n % CF::RF], (uint32_t)((n / CF::RF) & 1), dead);
+          const float decay = fac[4 * kLaChunk];
+          la_wait(STATES ? b_ds : b_o, (uint32_t)(n & 1), dead);
+          tc5_fence_after();
+          float o[2][16];
+          if (!STATES) {
+            uint32_t x1[2][16], x2[2][16];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              tmem_ld_rows16(x1[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO1 + half * 32);
+              tmem_ld_rows16(x2[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO2 + half * 32);
+            }
+            uint64_t f[4];
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4)
+              f[i4] = *reinterpret_cast<const uint64_t*>(fac + 2 * kLaChunk + half * 32 + i4 * 8 + 2 * (lane % 4));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              tmem_wait_ld(x1[e]);
+              tmem_wait_ld(x2[e]);
+#pragma unroll
+              for (int i2 = 0; i2 < 8; ++i2) {
+                const uint64_t y = fma2(pair(x2[e][2 * i2], x2[e][2 * i2 + 1]), f[i2 / 2], pair(x1[e][2 * i2], x1[e][2 * i2 + 1]));
+                o[e][2 * i2] = pair_lo(y);
+                o[e][2 * i2 + 1] = pair_hi(y);
+              }
+            }
+          }
+          const uint64_t decay2 = pair(decay, decay);
+#pragma unroll
+          for (int c = 0; c < KH; c += 32) {
+            uint32_t x[32];
+            tmem_ld32(x, lanes + CF::cDS + half * KH + c);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) S[c / 2 + e] = fma2(S[c / 2 + e], decay2, pair(x[2 * e], x[2 * e + 1]));
+          }
+          tc5_fence_before();
+          arrive(b_free);
+          arrive(&empty_f[n % CF::RF]);
+          if (!STATES && cc + 1 < p.last) give_state();
+          if (!STATES)
+            la_emit<T>(a, o, smem + CF::kStage + warp * 1024, b, bh, h, t0 + half * 32, len, quad * 32, quad, lane);
+          if (!STATES && !a.reverse && anchor_here) {
+            const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
+            float* to = a.dump + (an * 8 + warp) * (KH * 32);
+#pragma unroll
+            for (int c = 0; c < KH; c += 4)
+              reinterpret_cast<float4*>(to)[c / 4 * 32 + lane] =
+                  make_float4(pair_lo(S[c / 2]), pair_hi(S[c / 2]), pair_lo(S[c / 2 + 1]), pair_hi(S[c / 2 + 1]));
+          }
         }
-      } else if (!STATES && a.x.ptr && t0 + half * 32 + lane < len) {
-        a.dots[(bh * a.seqlen + t0 + half * 32 + lane) * 4 + quad] = 0.f;
-      }
-      if (holds) {
+        if (p.to_carry) {
+          float4* to = reinterpret_cast<float4*>(a.carry + ((int64_t)work.worker * 8 + warp) * (KH * 32));
 #pragma unroll
-        for (int c = 0; c < KH; c += 32) {
-          uint32_t x[32];
-          tmem_ld32(x, lanes + CF::cDS + half * KH + c);
-          tmem_wait_ld(x);
+          for (int c = 0; c < KH; c += 4) 
+            __stcg(to + c / 4 * 32 + lane,
+                   make_float4(pair_lo(S[c / 2]), pair_hi(S[c / 2]), pair_lo(S[c / 2 + 1]), pair_hi(S[c / 2 + 1])));
+          __threadfence();
+          __syncwarp();
+          if (lane == 0)
+            asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(a.flags + 1 + work.worker * 8 + warp), "r"(1u) : "memory");
+        } else if (a.s_out && (STATES || step == a.nseg - 1) && vi < a.dv) {
+          float* to = a.s_out + bh * a.s_out_head + step * a.s_out_seg;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) S[c + i] = fmaf(S[c + i], decay, __uint_as_float(x[i]));
+          for (int c = 0; c < KH; ++c) {
+            const int kk = half * KH + c;
+            if (kk < a.dk) to[kk * a.sk + vi * a.sv] = c % 2 ? pair_hi(S[c / 2]) : pair_lo(S[c / 2]);
+          }
         }
-        if (!STATES && n + 1 < n_chunks) store_planes();
-      }
-      tc5_fence_before();
-      arrive(&b_empty[s]);
-      if (!STATES) arrive(b_s);
-      if (!STATES && !a.reverse && anchor_here && holds) {
-        const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
-        float* to = a.dump + (an * 8 + warp) * (KH * 32);
-#pragma unroll
-        for (int c = 0; c < KH; c += 4)
-          reinterpret_cast<float4*>(to)[c / 4 * 32 + lane] = make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
-      }
-    }
-    if (a.s_out && (STATES || step == a.nseg - 1) && holds && vi < a.dv) {
-      float* to = a.s_out + bh * a.s_out_head + step * a.s_out_seg;
-#pragma unroll
-      for (int c = 0; c < KH; ++c) {
-        const int kk = half * KH + c;
-        if (kk < a.dk) to[kk * a.sk + vi * a.sv] = S[c];
       }
     }
   }
-  // every MMA was waited for (b_ds of the last chunk) unless a wait gave up: then
-  // this one, bounded too, stands between the MMAs in flight and the end
+  // every MMA was waited for (the last chunk's) unless a wait gave up: then this
+  // commit, waited for with a limit too, stands between those in flight and the end
   tc5_fence_before();
   __syncthreads();
   tc5_fence_after();
-  if (warp == CF::kComputeWarps) {
+  if (warp == kLaMmaWarp) {
     if (*dead) {
       if (lane == 0) {
         mma_commit(b_qk);
-        for (int i = 0; i < 1024 && !mbar_try_wait(b_qk, 0); ++i) {}
+        for (int i = 0; i < 4096 && !mbar_try_wait(b_qk, 0); ++i) {}
       }
       __syncwarp();
     }
@@ -650,11 +948,12 @@ __global__ void linattn_share_kernel(const float* part, T* out, const int* lengt
 // dg_t = sum_{s = t..e} (q_s . dq_s - k_s . dk_s) + <R_e, S_e>, e the next anchor at or
 // behind t, R_e what the later tokens send back to the state S_e.  Each anchor's
 // sums start anew, so that what cancels in the differences is no longer than the
-// stretch between two.  One warp a stretch, from its end; sums in fp64.
+// stretch between two.  One warp a stretch, from its end; sums in fp64.  Keys of at
+// most 64 fill two lane quadrants of the partial products, wider ones four.
 template <typename T>
 __global__ void linattn_decay_grad_kernel(const float* dots_q, const float* dots_k, const float* anchor, T* out,
                                           const int* lengths, int64_t bhs, int heads, int seqlen, int anchors,
-                                          int anchor_tokens) {
+                                          int anchor_tokens, bool two_quads) {
   const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
   const int lane = threadIdx.x % 32;
   const int64_t bh = w / anchors;
@@ -668,14 +967,16 @@ __global__ void linattn_decay_grad_kernel(const float* dots_q, const float* dots
   if (begin >= len) return;
   const int end = begin + anchor_tokens < len ? (int)(begin + anchor_tokens) : len;
   double carry = 0.0;
-  for (int i = 0; i < 8; ++i) carry += anchor[(bh * anchors + an) * 8 + i];
+  for (int i = 0; i < 8; ++i)
+    if (!two_quads || i % 4 < 2) carry += anchor[(bh * anchors + an) * 8 + i];
   for (int hi = end; hi > begin; hi -= 32) {
     const int t = hi - 1 - lane;  // lane 0 the latest
     double x = 0.0;
     if (t >= begin) {
       const float4 q = reinterpret_cast<const float4*>(dots_q)[bh * seqlen + t];
       const float4 k = reinterpret_cast<const float4*>(dots_k)[bh * seqlen + t];
-      x = ((double)q.x + q.y + q.z + q.w) - ((double)k.x + k.y + k.z + k.w);
+      x = ((double)q.x + q.y) - ((double)k.x + k.y);
+      if (!two_quads) x += ((double)q.z + q.w) - ((double)k.z + k.w);
     }
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
