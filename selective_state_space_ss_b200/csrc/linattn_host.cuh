@@ -149,7 +149,7 @@ ss_status la_launch(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, CF::kSmem) == cudaSuccess;
       }) != 1)
     return SS_ERR_CUDA;
-  const int64_t grid = a.workers > 0 ? a.workers : a.bh * a.nseg;
+  const int64_t grid = a.workers > 0 ? a.workers : (int64_t)a.bh * a.nseg;
   if (grid > INT_MAX) return SS_ERR_INVALID_ARG;
   if (a.workers > 0 &&
       cudaMemsetAsync(a.flags, 0, (1 + (size_t)a.workers * 8) * sizeof(unsigned), stream) != cudaSuccess)
@@ -207,7 +207,7 @@ LaPassArgs la_base(const LaShape& s, const ss_heads* g, const int32_t* lengths, 
   a.lengths = lengths;
   a.heads = s.heads;
   a.seqlen = (int)s.seqlen;
-  a.bh = s.bh();
+  a.bh = (int)s.bh();
   a.nseg = segs.nseg;
   a.seg_chunks = segs.chunks;
   a.anchor_chunks = 1;

@@ -88,7 +88,7 @@ struct LaPassArgs {
   int anchor_chunks;    // an anchor behind every so many chunks
   int anchors;          // anchors of the longest row
   int heads, seqlen, dk, dv;
-  int64_t bh;           // batch * heads
+  int bh;               // batch * heads
   int nseg, seg_chunks; // segments of a head, or
   int workers;          // > 0: CTAs that share all chunks evenly
   float* carry;         // [workers] states handed to the next worker
@@ -111,9 +111,11 @@ struct LaCfg {
   static constexpr int NPX = kBf16 ? 2 : 3;  // planes of the scores and of the state as operands
   static constexpr int NPW = 3;              // planes of the weighted keys
   static constexpr int KB = KD / 64, VB = VD / 64;
-  static constexpr int RK = kBf16 ? 2 : 1, RV = RK, RQ = kBf16 ? (KB + VB == 4 ? 2 : 3) : 1;  // tiles in each ring
+  static constexpr int RK = kBf16 ? 2 : 1, RV = RK, RQ = kBf16 ? (KB == 2 ? 2 : 4) : 1;  // tiles in each ring
   static constexpr int RW = kBf16 ? 2 : 1;   // weighted keys
   static constexpr int RF = 4;               // decays
+  static constexpr int kRing = 4;
+  static_assert(RK <= kRing && RV <= kRing && RQ <= kRing && RF <= kRing, "barriers of a ring");
   static constexpr int kTileK = KB * NPI * kLaBlock, kTileV = VB * NPI * kLaBlock, kTileW = KB * NPW * kLaBlock;
   static constexpr int kQ = 0, kK = RQ * kTileK, kV = kK + RK * kTileK, kP = kV + RV * kTileV;
   static constexpr int kW = kP + NPX * kLaBlock;
@@ -121,7 +123,7 @@ struct LaCfg {
   static constexpr int kFac = kW + RW * kTileW;
   static constexpr int kStage = kFac + (RF * kFacFloats * 4 + 127) / 128 * 128;  // 1 KB a back warp
   static constexpr int kBars = kStage + (kBf16 ? 8 * 1024 : 0);
-  static constexpr int kSmem = kBars + 512;
+  static constexpr int kSmem = kBars + (8 * kRing + 6) * 8 + 16;
   // tensor memory columns
   static constexpr int cDS = 0, cSP = KD, cO1 = cSP + NPX * KD / 2, cO2 = cO1 + 64, cQK = cO2 + 64;
   static constexpr int kCols = cQK + 64 <= 256 ? 256 : 512;
@@ -140,7 +142,7 @@ constexpr int kLaBackRegs = 168, kLaFrontRegs = 104, kLaAuxRegs = 72;
 // Waits of one CTA: when one gives up, the others stop waiting too, and the kernel
 // runs to its end on whatever is there, inside its buffers.
 __device__ __forceinline__ void la_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return;
+#pragma unroll 1
   for (uint32_t i = 0; i < kLaSpinLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return;
     if (*dead) return;
@@ -167,7 +169,7 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
                                              int len, int d, bool vec, int tid, int nthreads) {
   constexpr int B = DP / 64;
   constexpr int UNITS = kLaChunk * B * 8;
-#pragma unroll 2
+#pragma unroll 1
   for (int u = tid; u < UNITS; u += nthreads) {
     const int row = u / (B * 8), unit = u % (B * 8), col = unit * 8;
     const bool in = t0 + row < len && col < d && in_range(t0 + row, len);
@@ -215,10 +217,13 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
   }
 }
 
-// 2^x, x of either sign and any size: the fraction by ex2, the integer by scaling.
+// 2^x, x of either sign and any size: the fraction by ex2, the integer through the
+// exponent; what is below the normal numbers is zero, as ex2 has it elsewhere.
 __device__ __forceinline__ float la_exp2(double x) {
-  const double n = rint(x < -1e6 ? -1e6 : x > 1e6 ? 1e6 : x);
-  return scalbnf(ex2_approx((float)(x - n)), (int)n);
+  const float n = rintf((float)x);
+  const float y = ex2_approx((float)(x - (double)n));
+  const float z = y * __int_as_float(((int)n + 127) << 23);
+  return n < -125.f ? 0.f : n > 127.f ? __int_as_float(0x7f800000) : z;
 }
 
 // A lane's two log decays of a chunk, zero behind the row's end.
@@ -351,61 +356,77 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
   }
 }
 
+// The products of planes pa < PA of one operand and pb < PB of the other whose
+// weight counts, the smaller ones first: they add up while the sum is small.  STEPS
+// MMAs each, given the planes' places (in descriptor units: blocks of a plane, or
+// `a_cols` columns).  Kept a loop: the kernel's roles together have to stay in the
+// instruction cache.
+template <int PA, int PB, int STEPS, typename F>
+__device__ __forceinline__ void la_products(int a_blocks, int b_blocks, F&& mma, int a_cols = 0) {
+  constexpr int P = PA > PB ? PA : PB;
+  bool add = false;
+#pragma unroll 1
+  for (int pa = PA - 1; pa >= 0; --pa)
+#pragma unroll 1
+    for (int pb = (P - pa < PB ? P - pa : PB) - 1; pb >= 0; --pb)
+#pragma unroll 1
+      for (int i = 0; i < STEPS; ++i) {
+        mma(pa * (a_blocks * (kLaBlock >> 4) + a_cols), pb * b_blocks * (kLaBlock >> 4), i, add);
+        add = true;
+      }
+}
+
 // What one CTA works through: pieces of heads, in the order of processing.
 struct LaPiece {
-  int64_t bh;
+  int bh, b, h, len;
   int first, last;   // real chunks [first, last), whichever way they are run
   bool from_carry;   // starts from the previous worker's state
   bool to_carry;     // ends inside its head
 };
 struct LaWork {
-  int64_t lo, hi;    // workers: range of padded chunks
-  int n, pieces, worker;
+  int worker, n, pieces;   // chunks of a whole head
+  int h0, c0, h1, c1;      // from chunk c0 of head h0 to before chunk c1 of head h1
 };
 __device__ __forceinline__ LaWork la_work(const LaPassArgs& a, int worker) {
   LaWork w;
   w.worker = worker;
   w.n = (a.seqlen + kLaChunk - 1) / kLaChunk;
-  w.pieces = 1;
-  w.lo = w.hi = 0;
   if (a.workers > 0) {
-    const int64_t total = a.bh * w.n;
-    w.lo = total * worker / a.workers;
-    w.hi = total * (worker + 1) / a.workers;
-    // heads touched: a worker's range is at least a head long
-    w.pieces = (int)((w.hi + w.n - 1) / w.n - w.lo / w.n);
+    const int64_t total = (int64_t)a.bh * w.n, lo = total * worker / a.workers, hi = total * (worker + 1) / a.workers;
+    w.h0 = (int)(lo / w.n), w.c0 = (int)(lo - (int64_t)w.h0 * w.n);
+    w.h1 = (int)(hi / w.n), w.c1 = (int)(hi - (int64_t)w.h1 * w.n);
+    w.pieces = w.h1 - w.h0 + (w.c1 > 0);  // a range is at least a head long
+  } else {
+    w.h0 = w.h1 = worker / a.nseg;
+    const int step = worker - w.h0 * a.nseg;
+    const int64_t p0 = (int64_t)step * a.seg_chunks, p1 = p0 + a.seg_chunks;
+    w.c0 = (int)(p0 < w.n ? p0 : w.n);
+    w.c1 = (int)(p1 < w.n ? p1 : w.n);
+    w.pieces = 1;
   }
   return w;
 }
-template <bool STATES>
 __device__ __forceinline__ LaPiece la_piece(const LaPassArgs& a, const LaWork& w, int i) {
   LaPiece p;
-  int64_t p0, p1;  // places in the order of processing, padded
+  int p0 = 0, p1 = w.n;  // places in the order of processing, padded
   p.from_carry = p.to_carry = false;
   if (a.workers > 0) {
     // the head that the next worker goes on with comes first, the one that the
     // previous worker began comes last
-    const int64_t h0 = w.lo / w.n, c0 = w.lo % w.n, h1 = w.hi / w.n, c1 = w.hi % w.n;
-    const bool tail = c1 > 0;
-    if (tail && i == 0) {
-      p.bh = h1, p0 = 0, p1 = c1, p.to_carry = true;
-    } else {
-      const int64_t whole0 = h0 + (c0 > 0 ? 1 : 0);
-      const int64_t h = whole0 + i - (tail ? 1 : 0);
-      if (h < h1) p.bh = h, p0 = 0, p1 = w.n;
-      else p.bh = h0, p0 = c0, p1 = w.n, p.from_carry = true;
-    }
+    const int tail = w.c1 > 0;
+    p.bh = w.h0 + (w.c0 > 0) + i - tail;
+    if (tail && i == 0) p.bh = w.h1, p1 = w.c1, p.to_carry = true;
+    else if (p.bh >= w.h1) p.bh = w.h0, p0 = w.c0, p.from_carry = true;
   } else {
-    const int step = w.worker % a.nseg;
-    p.bh = w.worker / a.nseg;
-    p0 = (int64_t)step * a.seg_chunks;
-    p1 = p0 + a.seg_chunks < w.n ? p0 + a.seg_chunks : w.n;
-    if (p0 > w.n) p0 = w.n;
+    p.bh = w.h0, p0 = w.c0, p1 = w.c1;
   }
-  const int all = (la_length(a, p.bh / a.heads) + kLaChunk - 1) / kLaChunk;
-  int64_t f = a.reverse ? w.n - p1 : p0, l = a.reverse ? w.n - p0 : p1;
-  p.first = (int)(f < all ? f : all);
-  p.last = (int)(l < all ? l : all);
+  p.b = p.bh / a.heads;
+  p.h = p.bh - p.b * a.heads;
+  p.len = la_length(a, p.b);
+  const int all = (p.len + kLaChunk - 1) / kLaChunk;
+  const int f = a.reverse ? w.n - p1 : p0, l = a.reverse ? w.n - p0 : p1;
+  p.first = f < all ? f : all;
+  p.last = l < all ? l : all;
   return p;
 }
 
@@ -417,23 +438,25 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   constexpr int NPI = CF::NPI, NPX = CF::NPX, NPW = CF::NPW;
   extern __shared__ __align__(1024) char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + CF::kBars);
-  uint64_t *full_k = bars, *empty_k = bars + 2, *full_v = bars + 4, *empty_v = bars + 6, *full_q = bars + 8,
-           *empty_q = bars + 11, *full_f = bars + 14, *empty_f = bars + 18;
-  uint64_t *b_qk = bars + 22;  // scores are there
-  uint64_t *b_pk = bars + 23;  // P and the weighted keys are there
-  uint64_t *b_ds = bars + 24;  // increment and P V are there
-  uint64_t *b_o = bars + 25;   // S Q too: the chunk's products are done
-  uint64_t *b_free = bars + 26;  // the back warps have read them
-  uint64_t *b_s = bars + 27;   // the state's planes are there
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 28);
+  // a ring's barriers: CF::kRing slots each, whatever its length
+  uint64_t *full_k = bars, *empty_k = full_k + CF::kRing, *full_v = empty_k + CF::kRing, *empty_v = full_v + CF::kRing,
+           *full_q = empty_v + CF::kRing, *empty_q = full_q + CF::kRing, *full_f = empty_q + CF::kRing,
+           *empty_f = full_f + CF::kRing, *single = empty_f + CF::kRing;
+  uint64_t *b_qk = single;        // scores are there
+  uint64_t *b_pk = single + 1;    // P and the weighted keys are there
+  uint64_t *b_ds = single + 2;    // increment and P V are there
+  uint64_t *b_o = single + 3;     // S Q too: the chunk's products are done
+  uint64_t *b_free = single + 4;  // the back warps have read them
+  uint64_t *b_s = single + 5;     // the state's planes are there
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(single + 6);
   int* worker_at = reinterpret_cast<int*>(tmem_at + 1);
   volatile int* dead = worker_at + 1;
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
-    for (int i = 0; i < CF::RK; ++i) mbar_init(&full_k[i], CF::kLoaders), mbar_init(&empty_k[i], kLaFrontWarps + (STATES ? 0 : 1));
-    for (int i = 0; i < CF::RV; ++i) mbar_init(&full_v[i], CF::kLoaders), mbar_init(&empty_v[i], 1);
-    for (int i = 0; i < CF::RQ; ++i) mbar_init(&full_q[i], CF::kLoaders), mbar_init(&empty_q[i], 1);
+    for (int i = 0; i < CF::RK; ++i) mbar_init(&full_k[i], 1), mbar_init(&empty_k[i], kLaFrontWarps + (STATES ? 0 : 1));
+    for (int i = 0; i < CF::RV; ++i) mbar_init(&full_v[i], 1), mbar_init(&empty_v[i], 1);
+    for (int i = 0; i < CF::RQ; ++i) mbar_init(&full_q[i], 1), mbar_init(&empty_q[i], 1);
     for (int i = 0; i < CF::RF; ++i) mbar_init(&full_f[i], 1), mbar_init(&empty_f[i], kLaFrontWarps + CF::kHolders);
     mbar_init(b_qk, 1);
     mbar_init(b_pk, kLaFrontWarps);
@@ -471,18 +494,10 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         if (leader) {
           const uint64_t q = tile_desc(base + CF::kQ + (n % CF::RQ) * CF::kTileK, 0);
           const uint64_t k = tile_desc(base + CF::kK + (n % CF::RK) * CF::kTileK, 0);
-          constexpr uint32_t id = mma_idesc(64, 64, false, false);
-          // the products of smaller planes first: they add up while the sum is small
-#pragma unroll
-          for (int pa = NPI - 1; pa >= 0; --pa)
-#pragma unroll
-            for (int pb = NPI - pa - 1; pb >= 0; --pb)
-#pragma unroll
-              for (int kk = 0; kk < KD; kk += 16) {
-                const uint32_t off = (kk / 64) * kLaBlock + (kk % 64) * 2;
-                mma_ss(tmem + CF::cQK, q + ((pa * CF::KB * kLaBlock + off) >> 4), k + ((pb * CF::KB * kLaBlock + off) >> 4),
-                       id, !(pa == NPI - 1 && kk == 0));
-              }
+          la_products<NPI, NPI, KD / 16>(CF::KB, CF::KB, [&](int pa, int pb, int i, bool add) {
+            const int off = (i / 4) * (kLaBlock >> 4) + (i % 4) * 2;
+            mma_ss(tmem + CF::cQK, q + pa + off, k + pb + off, mma_idesc(64, 64, false, false), add);
+          });
           mma_commit(b_qk);
           mma_commit(&empty_k[n % CF::RK]);
         }
@@ -490,7 +505,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
       };
       int total = 0, scored = 0;
       for (int i = 0; i < work.pieces; ++i) {
-        const LaPiece p = la_piece<STATES>(a, work, i);
+        const LaPiece p = la_piece(a, work, i);
         total += p.last - p.first;
       }
       if (!STATES && total > 0) scores(scored++);
@@ -504,30 +519,17 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         if (n > 0) la_wait(b_free, (uint32_t)((n - 1) & 1), dead);
         tc5_fence_after();
         if (leader) {
-          {
-            // dS^T = V^T (w . K)
-            constexpr uint32_t id = mma_idesc(128, KD, true, true);
-#pragma unroll
-            for (int pa = NPI - 1; pa >= 0; --pa)
-#pragma unroll
-              for (int pb = NPW - pa - 1; pb >= 0; --pb)
-#pragma unroll
-                for (int j = 0; j < kLaChunk; j += 16)
-                  mma_ss(tmem + CF::cDS, v + ((pa * CF::VB * kLaBlock + j * kTileRow) >> 4),
-                         w + ((pb * CF::KB * kLaBlock + j * kTileRow) >> 4), id, !(pa == NPI - 1 && pb == NPW - NPI && j == 0));
-          }
+          // dS^T = V^T (w . K)
+          la_products<NPI, NPW, kLaChunk / 16>(CF::VB, CF::KB, [&](int pa, int pb, int i, bool add) {
+            const int off = i * (16 * kTileRow >> 4);
+            mma_ss(tmem + CF::cDS, v + pa + off, w + pb + off, mma_idesc(128, KD, true, true), add);
+          });
           if (!STATES) {
             // O1^T = V^T P^T
-            constexpr uint32_t id = mma_idesc(128, 64, true, false);
             const uint64_t pd = tile_desc(base + CF::kP, 0);
-#pragma unroll
-            for (int pa = NPI - 1; pa >= 0; --pa)
-#pragma unroll
-              for (int pb = NPX - pa - 1; pb >= 0; --pb)
-#pragma unroll
-                for (int j = 0; j < kLaChunk; j += 16)
-                  mma_ss(tmem + CF::cO1, v + ((pa * CF::VB * kLaBlock + j * kTileRow) >> 4),
-                         pd + ((pb * kLaBlock + j * 2) >> 4), id, !(pa == NPI - 1 && pb == NPX - NPI && j == 0));
+            la_products<NPI, NPX, kLaChunk / 16>(CF::VB, 1, [&](int pa, int pb, int i, bool add) {
+              mma_ss(tmem + CF::cO1, v + pa + i * (16 * kTileRow >> 4), pd + pb + i * 2, mma_idesc(128, 64, true, false), add);
+            });
           }
           mma_commit(b_ds);
           mma_commit(&empty_v[n % CF::RV]);
@@ -539,16 +541,10 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           tc5_fence_after();
           if (leader) {
             const uint64_t q = tile_desc(base + CF::kQ + (n % CF::RQ) * CF::kTileK, 0);
-            constexpr uint32_t id = mma_idesc(128, 64, false, false);
-#pragma unroll
-            for (int pa = NPX - 1; pa >= 0; --pa)
-#pragma unroll
-              for (int pb = (NPI < NPX - pa ? NPI : NPX - pa) - 1; pb >= 0; --pb)
-#pragma unroll
-                for (int kk = 0; kk < KD; kk += 16)
-                  mma_ts(tmem + CF::cO2, tmem + CF::cSP + pa * (KD / 2) + kk / 2,
-                         q + ((pb * CF::KB * kLaBlock + (kk / 64) * kLaBlock + (kk % 64) * 2) >> 4), id,
-                         !(pa == NPX - 1 && kk == 0));
+            la_products<NPX, NPI, KD / 16>(0, CF::KB, [&](int pa, int pb, int i, bool add) {
+              mma_ts(tmem + CF::cO2, tmem + CF::cSP + pa + i * 8, q + pb + (i / 4) * (kLaBlock >> 4) + (i % 4) * 2,
+                     mma_idesc(128, 64, false, false), add);
+            }, KD / 2);
             mma_commit(b_o);
             mma_commit(&empty_q[n % CF::RQ]);
           }
@@ -561,58 +557,57 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
       // ---- decays
       int n = 0;
       for (int i = 0; i < work.pieces; ++i) {
-        const LaPiece p = la_piece<STATES>(a, work, i);
-        const int64_t b = p.bh / a.heads;
-        const int h = (int)(p.bh % a.heads), len = la_length(a, b);
+        const LaPiece p = la_piece(a, work, i);
         double sum = 0.0;
         auto place = [&](int c) { return (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk; };
         float x[2], next[2];
-        if (p.first < p.last) la_fetch_decays<T>(next, a, b, h, place(p.first), len, lane);
+        if (p.first < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(p.first), p.len, lane);
         for (int c = p.first; c < p.last; ++c, ++n) {
           const int s = (int)(n % CF::RF);
           x[0] = next[0], x[1] = next[1];
-          if (c + 1 < p.last) la_fetch_decays<T>(next, a, b, h, place(c + 1), len, lane);
+          if (c + 1 < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(c + 1), p.len, lane);
           if (n >= CF::RF) la_wait(&empty_f[s], (uint32_t)((n / CF::RF - 1) & 1), dead);
           sum += la_decays(reinterpret_cast<float*>(smem + CF::kFac) + s * CF::kFacFloats, x, a.reverse, a.scale_o,
                            a.scale_w, lane);
           arrive(&full_f[s]);
         }
-        if (STATES && lane == 0) a.seg_decay[p.bh * (a.nseg + 1) + work.worker % a.nseg] = sum;
+        if (STATES && lane == 0) a.seg_decay[(int64_t)p.bh * (a.nseg + 1) + work.worker % a.nseg] = sum;
       }
     } else {
-      // ---- loaders
+      // ---- loaders: one thread by TMA, or all of them
       const int ltid = tid - 32 * kLaLoadWarp;
       int n = 0;
       for (int i = 0; i < work.pieces; ++i) {
-        const LaPiece p = la_piece<STATES>(a, work, i);
-        const int b = (int)(p.bh / a.heads);
-        const int h = (int)(p.bh % a.heads), len = la_length(a, b);
+        const LaPiece p = la_piece(a, work, i);
         for (int c = p.first; c < p.last; ++c, ++n) {
           const int t0 = (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk;
           // TMA clips at the tensor's end, not at a row's length
-          const bool by_tma = CF::kBf16 && a.tma && (t0 + kLaChunk <= len || len == a.seqlen);
+          const bool by_tma = CF::kBf16 && a.tma && (t0 + kLaChunk <= p.len || p.len == a.seqlen);
           auto tile = [&](auto width, const LaTensor& x, const CUtensorMap* map, int ring, int at, int bytes,
                           uint64_t* full, uint64_t* empty, int d) {
             constexpr int DP = decltype(width)::value;
-            const int s = (int)(n % ring);
-            if (n >= ring) la_wait(&empty[s], (uint32_t)((n / ring - 1) & 1), dead);
+            const int s = n % ring;
             char* to = smem + at + s * bytes;
+            if (ltid == 0 && n >= ring) la_wait(&empty[s], (uint32_t)((n / ring - 1) & 1), dead);
             if (by_tma) {
               if (ltid == 0) {
                 mbar_arrive_expect_tx(&full[s], DP / 64 * kLaBlock);
+#pragma unroll 1
                 for (int j = 0; j < DP / 64; ++j)
-                  tma_load_block(to + j * kLaBlock, map, &full[s], j * 64, t0, h / x.share, b);
-              } else {
-                mbar_arrive(&full[s]);
+                  tma_load_block(to + j * kLaBlock, map, &full[s], j * 64, t0, p.h / x.share, p.b);
               }
             } else {
-              la_load_tile<T, DP>(to, x, b, h, t0, len, d, a.vec, ltid, CF::kLoaders);
+              __syncwarp();
+              asm volatile("bar.sync 2, 64;\n" ::: "memory");
+              la_load_tile<T, DP>(to, x, p.b, p.h, t0, p.len, d, a.vec, ltid, CF::kLoaders);
               if (CF::kBf16 && a.vec) {
                 cp_async_commit();
                 cp_async_wait_all();
               }
               fence_proxy_async_smem();
-              mbar_arrive(&full[s]);
+              __syncwarp();
+              asm volatile("bar.sync 2, 64;\n" ::: "memory");
+              if (ltid == 0) mbar_arrive(&full[s]);
             }
           };
           tile(LaWidth<KD>{}, a.k, &maps.k, CF::RK, CF::kK, CF::kTileK, full_k, empty_k, a.dk);
@@ -633,7 +628,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
       asm volatile("bar.sync 1, 128;\n" ::: "memory");
     }
     for (int i = 0; i < work.pieces; ++i) {
-      const LaPiece p = la_piece<STATES>(a, work, i);
+      const LaPiece p = la_piece(a, work, i);
       for (int c = p.first; c < p.last; ++c, ++n) {
         const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + (int)(n % CF::RF) * CF::kFacFloats;
         la_wait(&full_f[n % CF::RF], (uint32_t)((n / CF::RF) & 1), dead);
@@ -643,7 +638,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           // the keys weighted by their decay to the chunk's end (reversed: start)
           const char* k = smem + CF::kK + (int)(n % CF::RK) * CF::kTileK;
           char* w = smem + CF::kW + (int)(n % CF::RW) * CF::kTileW;
-#pragma unroll 2
+#pragma unroll 1
           for (int u = ftid; u < CF::KB * 512; u += 32 * kLaFrontWarps) {
             const int row = (u % 512) / 8;
             const float wj = fac[3 * kLaChunk + row];
@@ -759,9 +754,9 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
       };
       int n = 0;
       for (int i = 0; i < work.pieces; ++i) {
-        const LaPiece p = la_piece<STATES>(a, work, i);
-        const int64_t b = p.bh / a.heads, bh = p.bh;
-        const int h = (int)(bh % a.heads), len = la_length(a, b);
+        const LaPiece p = la_piece(a, work, i);
+        const int64_t bh = p.bh;
+        const int b = p.b, h = p.h, len = p.len;
         const int all_chunks = (len + kLaChunk - 1) / kLaChunk;
         const int step = a.workers > 0 ? 0 : work.worker % a.nseg;
         if (p.from_carry) {
@@ -785,13 +780,13 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             S[c / 2] = pair(x.x, x.y), S[c / 2 + 1] = pair(x.z, x.w);
           }
         } else {
-          const float* from = a.s_in && !STATES ? a.s_in + bh * a.s_in_head + step * a.s_in_seg : nullptr;
+          const bool in = a.s_in && !STATES && vi < a.dv;
+          const float* from = a.s_in + bh * a.s_in_head + step * a.s_in_seg + half * KH * a.sk + vi * a.sv;
 #pragma unroll
           for (int c = 0; c < KH; c += 2) {
             const int kk = half * KH + c;
-            const bool in = from && vi < a.dv;
-            S[c / 2] = pair(in && kk < a.dk ? from[kk * a.sk + vi * a.sv] : 0.f,
-                            in && kk + 1 < a.dk ? from[(kk + 1) * a.sk + vi * a.sv] : 0.f);
+            S[c / 2] = pair(in && kk < a.dk ? from[0] : 0.f, in && kk + 1 < a.dk ? from[a.sk] : 0.f);
+            from += 2 * a.sk;
           }
         }
         // every MMA that read the planes before is done (b_o of the last chunk)
@@ -882,11 +877,11 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           if (lane == 0)
             asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(a.flags + 1 + work.worker * 8 + warp), "r"(1u) : "memory");
         } else if (a.s_out && (STATES || step == a.nseg - 1) && vi < a.dv) {
-          float* to = a.s_out + bh * a.s_out_head + step * a.s_out_seg;
+          float* to = a.s_out + bh * a.s_out_head + step * a.s_out_seg + half * KH * a.sk + vi * a.sv;
 #pragma unroll
           for (int c = 0; c < KH; ++c) {
-            const int kk = half * KH + c;
-            if (kk < a.dk) to[kk * a.sk + vi * a.sv] = c % 2 ? pair_hi(S[c / 2]) : pair_lo(S[c / 2]);
+            if (half * KH + c < a.dk) *to = c % 2 ? pair_hi(S[c / 2]) : pair_lo(S[c / 2]);
+            to += a.sk;
           }
         }
       }
