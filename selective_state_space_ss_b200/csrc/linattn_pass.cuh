@@ -27,7 +27,7 @@
 // takes two planes, 16 bits, a relative error of about 1e-6 at every product; fp32
 // inputs and everything behind them take three planes, 24 bits, and the six
 // products of planes whose weight reaches that far.  The state itself stays fp32 in
-// registers.  Running sums of the decays are fp64, kept as two floats.
+// registers.  Running sums of the decays are whole numbers of 2^-32.
 //
 // Layout.  Scores are Q K^T with tokens in the lanes.  O and S are kept transposed
 // (value index in the lanes), so that S^T is the MMA's A operand straight from
@@ -111,23 +111,26 @@ struct LaCfg {
   static constexpr int NPX = kBf16 ? 2 : 3;  // planes of the scores and of the state as operands
   static constexpr int NPW = 3;              // planes of the weighted keys
   static constexpr int KB = KD / 64, VB = VD / 64;
-  static constexpr int RK = kBf16 ? 2 : 1, RV = RK, RQ = kBf16 ? (KB == 2 ? 2 : 4) : 1;  // tiles in each ring
-  static constexpr int RW = kBf16 ? 2 : 1;   // weighted keys
+  // Tiles in each ring.  A key tile lives until its chunk's increment is formed (the
+  // weighted keys' first planes replace it in place), a query tile until S Q is.
+  static constexpr int RK = kBf16 ? 3 : 2, RQ = kBf16 ? 3 : 1, RV = kBf16 ? (KB == 2 && VB == 2 ? 2 : 3) : 1;
+  static constexpr int RW = 2;               // the weighted keys' further planes
   static constexpr int RF = 4;               // decays
   static constexpr int kRing = 4;
   static_assert(RK <= kRing && RV <= kRing && RQ <= kRing && RF <= kRing, "barriers of a ring");
-  static constexpr int kTileK = KB * NPI * kLaBlock, kTileV = VB * NPI * kLaBlock, kTileW = KB * NPW * kLaBlock;
+  static constexpr int kTileK = KB * NPI * kLaBlock, kTileV = VB * NPI * kLaBlock, kTileW = KB * (NPW - NPI) * kLaBlock;
   static constexpr int kQ = 0, kK = RQ * kTileK, kV = kK + RK * kTileK, kP = kV + RV * kTileV;
   static constexpr int kW = kP + NPX * kLaBlock;
   static constexpr int kFacFloats = 4 * kLaChunk + 4;
   static constexpr int kFac = kW + RW * kTileW;
   static constexpr int kStage = kFac + (RF * kFacFloats * 4 + 127) / 128 * 128;  // 1 KB a back warp
   static constexpr int kBars = kStage + (kBf16 ? 8 * 1024 : 0);
-  static constexpr int kSmem = kBars + (8 * kRing + 6) * 8 + 16;
+  static constexpr int kSmem = kBars + (8 * kRing + 8) * 8 + 16;
   // tensor memory columns
   static constexpr int cDS = 0, cSP = KD, cO1 = cSP + NPX * KD / 2, cO2 = cO1 + 64, cQK = cO2 + 64;
-  static constexpr int kCols = cQK + 64 <= 256 ? 256 : 512;
-  static_assert(cQK + 64 <= 512, "tensor memory");
+  static constexpr int kAhead = kBf16 ? 2 : 1;  // chunks that scores run ahead, one place for each
+  static constexpr int kCols = cQK + 64 * kAhead <= 256 ? 256 : 512;
+  static_assert(cQK + 64 * kAhead <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr int kQuads = VD / 32;        // lane quadrants that hold values
   static constexpr int kHolders = 2 * kQuads;   // back warps at work
@@ -217,54 +220,63 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
   }
 }
 
-// 2^x, x of either sign and any size: the fraction by ex2, the integer through the
-// exponent; what is below the normal numbers is zero, as ex2 has it elsewhere.
-__device__ __forceinline__ float la_exp2(double x) {
-  const float n = rintf((float)x);
-  const float y = ex2_approx((float)(x - (double)n));
-  const float z = y * __int_as_float(((int)n + 127) << 23);
-  return n < -125.f ? 0.f : n > 127.f ? __int_as_float(0x7f800000) : z;
-}
-
-// A lane's two log decays of a chunk, zero behind the row's end.
+// A lane's two log decays of a chunk as they are stored, zero behind the row's end.
 template <typename T>
-__device__ __forceinline__ void la_fetch_decays(float (&x)[2], const LaPassArgs& a, int64_t b, int h, int t0, int len,
-                                                int lane) {
+__device__ __forceinline__ void la_fetch_decays(T (&x)[2], const LaPassArgs& a, int b, int h, int t0, int len, int lane) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = t0 + 2 * lane + i;
-    x[i] = t < len && in_range(t, len) ? to_f32(*reinterpret_cast<const T*>(la_row(a.g, b, t, h, sizeof(T)))) : 0.f;
+    x[i] = zero_elem<T>();
+    if (t < len && in_range(t, len)) x[i] = *reinterpret_cast<const T*>(la_row(a.g, b, t, h, sizeof(T)));
   }
 }
 
-// A chunk's decays: running sums (base 2) as two floats, the factors of the rows and
-// of the keys, and the chunk's whole decay.  One warp, two tokens a lane.  A log
-// decay below -1400 leaves nothing in fp32 and is taken as that, so that minus
-// infinity (a reset) does not turn differences of sums into NaN.
-__device__ __forceinline__ double la_decays(float* fac, const float (&x)[2], bool reverse, float scale_o, float scale_w,
-                                            int lane) {
-  double g[2];
+// 2^x of a number with 32 bits behind the point: the fraction by ex2, the integer
+// through the exponent; what is below the normal numbers is zero, as ex2 has it.
+__device__ __forceinline__ float la_exp2(int64_t x) {
+  const int n = (int)(x >> 32);
+  const float y = ex2_approx((float)(uint32_t)x * 0x1p-32f);  // 1 to 2
+  const float z = y * __int_as_float((n + 127) << 23);
+  return n < -126 ? 0.f : n > 127 ? __int_as_float(0x7f800000) : z;
+}
+
+// A chunk's decays: running sums, base 2, as integer and fraction, the factors of the
+// rows and of the keys, and the chunk's whole decay, which is returned.  One warp, two
+// tokens a lane.  The sums are whole numbers of 2^-32, so differences of large sums
+// lose nothing.  A log decay beyond +-1400 leaves nothing, or too much, in fp32 and is
+// taken as that: minus infinity (a reset) is a number like any other here.
+__device__ __forceinline__ int64_t la_decays(float* fac, float x0, float x1, bool reverse, float scale_o, float scale_w,
+                                             int lane) {
+  const float x[2] = {x0, x1};
+  int64_t g[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) g[i] = (double)(x[i] < -1400.f ? -1400.f : x[i]) * 1.4426950408889634;
-  double sum = g[0] + g[1];
+  for (int i = 0; i < 2; ++i)
+    g[i] = __double2ll_rn((double)fminf(fmaxf(x[i], -1400.f), 1400.f) * (1.4426950408889634 * 4294967296.0));
+  int64_t sum = g[0] + g[1];
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
-    const double up = __shfl_up_sync(kFullMask, sum, o);
+    const int64_t up = __shfl_up_sync(kFullMask, sum, o);
     if (lane >= o) sum += up;
   }
-  const double total = __shfl_sync(kFullMask, sum, 31);
-  const double at[2] = {sum - g[1], sum};
+  const int64_t total = __shfl_sync(kFullMask, sum, 31);
+  const int64_t at[2] = {sum - g[1], sum};
+  // a NaN among them is not to vanish
+  const float bad = __any_sync(kFullMask, x0 != x0 || x1 != x1) ? __int_as_float(0x7fffffff) : 1.f;
+  float2 hi, lo, rows, keys;
+  float* out[4] = {&hi.x, &lo.x, &rows.x, &keys.x};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = 2 * lane + i;
-    const float hi = (float)at[i];
-    fac[r] = hi;
-    fac[kLaChunk + r] = (float)(at[i] - (double)hi);
     const float from_start = la_exp2(at[i]), to_end = la_exp2(total - at[i]);
-    fac[2 * kLaChunk + r] = (reverse ? to_end : from_start) * scale_o;  // rows
-    fac[3 * kLaChunk + r] = (reverse ? from_start : to_end) * scale_w;  // keys
+    out[0][i] = (float)(int)(at[i] >> 32);
+    out[1][i] = (float)(uint32_t)at[i] * 0x1p-32f * bad;
+    out[2][i] = (reverse ? to_end : from_start) * scale_o * bad;
+    out[3][i] = (reverse ? from_start : to_end) * scale_w * bad;
   }
-  if (lane == 0) fac[4 * kLaChunk] = la_exp2(total);
+  reinterpret_cast<float2*>(fac)[lane] = hi;
+  reinterpret_cast<float2*>(fac + kLaChunk)[lane] = lo;
+  reinterpret_cast<float2*>(fac + 2 * kLaChunk)[lane] = rows;
+  reinterpret_cast<float2*>(fac + 3 * kLaChunk)[lane] = keys;
+  if (lane == 0) fac[4 * kLaChunk] = la_exp2(total) * bad;
   return total;
 }
 
@@ -359,8 +371,8 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
 // The products of planes pa < PA of one operand and pb < PB of the other whose
 // weight counts, the smaller ones first: they add up while the sum is small.  STEPS
 // MMAs each, given the planes' places (in descriptor units: blocks of a plane, or
-// `a_cols` columns).  Kept a loop: the kernel's roles together have to stay in the
-// instruction cache.
+// `a_cols` columns).  The loop over planes stays one: the roles together have to fit
+// the instruction cache.
 template <int PA, int PB, int STEPS, typename F>
 __device__ __forceinline__ void la_products(int a_blocks, int b_blocks, F&& mma, int a_cols = 0) {
   constexpr int P = PA > PB ? PA : PB;
@@ -368,12 +380,12 @@ __device__ __forceinline__ void la_products(int a_blocks, int b_blocks, F&& mma,
 #pragma unroll 1
   for (int pa = PA - 1; pa >= 0; --pa)
 #pragma unroll 1
-    for (int pb = (P - pa < PB ? P - pa : PB) - 1; pb >= 0; --pb)
-#pragma unroll 1
-      for (int i = 0; i < STEPS; ++i) {
-        mma(pa * (a_blocks * (kLaBlock >> 4) + a_cols), pb * b_blocks * (kLaBlock >> 4), i, add);
-        add = true;
-      }
+    for (int pb = (P - pa < PB ? P - pa : PB) - 1; pb >= 0; --pb) {
+      const int at_a = pa * (a_blocks * (kLaBlock >> 4) + a_cols), at_b = pb * b_blocks * (kLaBlock >> 4);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) mma(at_a, at_b, i, add || i > 0);
+      add = true;
+    }
 }
 
 // What one CTA works through: pieces of heads, in the order of processing.
@@ -442,23 +454,24 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   uint64_t *full_k = bars, *empty_k = full_k + CF::kRing, *full_v = empty_k + CF::kRing, *empty_v = full_v + CF::kRing,
            *full_q = empty_v + CF::kRing, *empty_q = full_q + CF::kRing, *full_f = empty_q + CF::kRing,
            *empty_f = full_f + CF::kRing, *single = empty_f + CF::kRing;
-  uint64_t *b_qk = single;        // scores are there
+  uint64_t *b_qk = single + 6;    // scores are there, one for each place
   uint64_t *b_pk = single + 1;    // P and the weighted keys are there
   uint64_t *b_ds = single + 2;    // increment and P V are there
   uint64_t *b_o = single + 3;     // S Q too: the chunk's products are done
   uint64_t *b_free = single + 4;  // the back warps have read them
   uint64_t *b_s = single + 5;     // the state's planes are there
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(single + 6);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(single + 8);
   int* worker_at = reinterpret_cast<int*>(tmem_at + 1);
   volatile int* dead = worker_at + 1;
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
-    for (int i = 0; i < CF::RK; ++i) mbar_init(&full_k[i], 1), mbar_init(&empty_k[i], kLaFrontWarps + (STATES ? 0 : 1));
+    for (int i = 0; i < CF::RK; ++i) mbar_init(&full_k[i], 1), mbar_init(&empty_k[i], 1);
     for (int i = 0; i < CF::RV; ++i) mbar_init(&full_v[i], 1), mbar_init(&empty_v[i], 1);
     for (int i = 0; i < CF::RQ; ++i) mbar_init(&full_q[i], 1), mbar_init(&empty_q[i], 1);
     for (int i = 0; i < CF::RF; ++i) mbar_init(&full_f[i], 1), mbar_init(&empty_f[i], kLaFrontWarps + CF::kHolders);
-    mbar_init(b_qk, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&b_qk[i], 1);
+    mbar_init(single, 1);
     mbar_init(b_pk, kLaFrontWarps);
     mbar_init(b_ds, 1);
     mbar_init(b_o, 1);
@@ -496,10 +509,9 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           const uint64_t k = tile_desc(base + CF::kK + (n % CF::RK) * CF::kTileK, 0);
           la_products<NPI, NPI, KD / 16>(CF::KB, CF::KB, [&](int pa, int pb, int i, bool add) {
             const int off = (i / 4) * (kLaBlock >> 4) + (i % 4) * 2;
-            mma_ss(tmem + CF::cQK, q + pa + off, k + pb + off, mma_idesc(64, 64, false, false), add);
+            mma_ss(tmem + CF::cQK + (n % CF::kAhead) * 64, q + pa + off, k + pb + off, mma_idesc(64, 64, false, false), add);
           });
-          mma_commit(b_qk);
-          mma_commit(&empty_k[n % CF::RK]);
+          mma_commit(&b_qk[n % CF::kAhead]);
         }
         __syncwarp();
       };
@@ -508,13 +520,16 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         const LaPiece p = la_piece(a, work, i);
         total += p.last - p.first;
       }
-      if (!STATES && total > 0) scores(scored++);
+      if (!STATES)
+        while (scored < CF::kAhead && scored < total) scores(scored++);
       for (int n = 0; n < total; ++n) {
         const uint64_t v = tile_desc(base + CF::kV + (n % CF::RV) * CF::kTileV, kLaBlock);
-        const uint64_t w = tile_desc(base + CF::kW + (n % CF::RW) * CF::kTileW, kLaBlock);
+        // planes of the weighted keys: in the key tile's place, then in a ring of their own
+        const uint64_t w0 = tile_desc(base + CF::kK + (n % CF::RK) * CF::kTileK, kLaBlock);
+        const uint64_t w1 = tile_desc(base + CF::kW + (n % CF::RW) * CF::kTileW, kLaBlock) -
+                            (uint64_t)(NPI * CF::KB * (kLaBlock >> 4));
         la_wait(b_pk, (uint32_t)(n & 1), dead);
         tc5_fence_after();
-        if (!STATES && CF::RQ > 1 && scored < total) scores(scored++);
         la_wait(&full_v[n % CF::RV], (uint32_t)((n / CF::RV) & 1), dead);
         if (n > 0) la_wait(b_free, (uint32_t)((n - 1) & 1), dead);
         tc5_fence_after();
@@ -522,7 +537,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           // dS^T = V^T (w . K)
           la_products<NPI, NPW, kLaChunk / 16>(CF::VB, CF::KB, [&](int pa, int pb, int i, bool add) {
             const int off = i * (16 * kTileRow >> 4);
-            mma_ss(tmem + CF::cDS, v + pa + off, w + pb + off, mma_idesc(128, KD, true, true), add);
+            mma_ss(tmem + CF::cDS, v + pa + off, (pb < NPI * CF::KB * (kLaBlock >> 4) ? w0 : w1) + pb + off,
+                   mma_idesc(128, KD, true, true), add);
           });
           if (!STATES) {
             // O1^T = V^T P^T
@@ -533,6 +549,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
           mma_commit(b_ds);
           mma_commit(&empty_v[n % CF::RV]);
+          mma_commit(&empty_k[n % CF::RK]);
         }
         __syncwarp();
         if (!STATES) {
@@ -549,8 +566,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             mma_commit(&empty_q[n % CF::RQ]);
           }
           __syncwarp();
-          // with one tile in the ring the next queries only come now
-          if (CF::RQ == 1 && scored < total) scores(scored++);
+          // last, so that no tile is waited for while the chunk's own products could run
+          if (scored < total) scores(scored++);
         }
       }
     } else if (warp == kLaDecayWarp) {
@@ -560,15 +577,16 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         const LaPiece p = la_piece(a, work, i);
         double sum = 0.0;
         auto place = [&](int c) { return (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk; };
-        float x[2], next[2];
+        T next[2];
         if (p.first < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(p.first), p.len, lane);
         for (int c = p.first; c < p.last; ++c, ++n) {
           const int s = (int)(n % CF::RF);
-          x[0] = next[0], x[1] = next[1];
+          const float x0 = to_f32(next[0]), x1 = to_f32(next[1]);
           if (c + 1 < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(c + 1), p.len, lane);
           if (n >= CF::RF) la_wait(&empty_f[s], (uint32_t)((n / CF::RF - 1) & 1), dead);
-          sum += la_decays(reinterpret_cast<float*>(smem + CF::kFac) + s * CF::kFacFloats, x, a.reverse, a.scale_o,
-                           a.scale_w, lane);
+          const int64_t whole = la_decays(reinterpret_cast<float*>(smem + CF::kFac) + s * CF::kFacFloats, x0, x1,
+                                          a.reverse, a.scale_o, a.scale_w, lane);
+          if (STATES) sum += (double)whole * 0x1p-32;
           arrive(&full_f[s]);
         }
         if (STATES && lane == 0) a.seg_decay[(int64_t)p.bh * (a.nseg + 1) + work.worker % a.nseg] = sum;
@@ -621,6 +639,16 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
     regs_give<kLaFrontRegs>();
     const int fw = warp - kLaBackWarps, ftid = tid - 32 * kLaBackWarps;
     int n = 0;
+    // Shares of the 32 or 16 steps of a key tile.  A warp's rows of P have one to four
+    // blocks of 16 columns under the mask (reversed: four to one), each about as much
+    // work as one and a half steps of 128-wide keys: the others' shares make up for it.
+    const int at = STATES ? 0 : a.reverse ? 4 - fw : fw;
+    const auto share = [&](int i) {
+      return STATES ? i * CF::KB * 4 : CF::KB == 2 ? (i == 0 ? 0 : i == 1 ? 11 : i == 2 ? 20 : i == 3 ? 27 : 32)
+                                                   : (i == 0 ? 0 : i == 1 ? 7 : i == 2 ? 12 : i == 3 ? 15 : 16);
+    };
+    const int w_from = STATES ? share(fw) : a.reverse ? share(at - 1) : share(at);
+    const int w_to = STATES ? share(fw + 1) : a.reverse ? share(at) : share(at + 1);
     if (!STATES) {
       // what the mask takes away is zero once and for all
       for (int i = ftid; i < NPX * kLaBlock / 16; i += 32 * kLaFrontWarps)
@@ -633,13 +661,13 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + (int)(n % CF::RF) * CF::kFacFloats;
         la_wait(&full_f[n % CF::RF], (uint32_t)((n / CF::RF) & 1), dead);
         la_wait(&full_k[n % CF::RK], (uint32_t)((n / CF::RK) & 1), dead);
-        if (CF::RW == 1 && n > 0) la_wait(b_ds, (uint32_t)((n - 1) & 1), dead);
+        if (!STATES) la_wait(&b_qk[n % CF::kAhead], (uint32_t)((n / CF::kAhead) & 1), dead);  // the keys as they are were used
         {
           // the keys weighted by their decay to the chunk's end (reversed: start)
-          const char* k = smem + CF::kK + (int)(n % CF::RK) * CF::kTileK;
-          char* w = smem + CF::kW + (int)(n % CF::RW) * CF::kTileW;
-#pragma unroll 1
-          for (int u = ftid; u < CF::KB * 512; u += 32 * kLaFrontWarps) {
+          char* k = smem + CF::kK + (n % CF::RK) * CF::kTileK;
+          char* w = smem + CF::kW + (n % CF::RW) * CF::kTileW;
+#pragma unroll 2
+          for (int u = w_from * 32 + lane; u < w_to * 32; u += 32) {
             const int row = (u % 512) / 8;
             const float wj = fac[3 * kLaChunk + row];
             const uint64_t ww = pair(wj, wj);
@@ -663,18 +691,16 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             }
 #pragma unroll
             for (int q = 0; q < NPW; ++q)
-              *reinterpret_cast<uint4*>(w + q * CF::KB * kLaBlock + off) =
+              *reinterpret_cast<uint4*>((q < NPI ? k + q * CF::KB * kLaBlock : w + (q - NPI) * CF::KB * kLaBlock) + off) =
                   make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
           }
         }
-        arrive(&empty_k[n % CF::RK]);
-        // never two chunks ahead of the products that take what is made here
-        if (STATES && CF::RW > 1 && n > 0) la_wait(b_ds, (uint32_t)((n - 1) & 1), dead);
+        // the last chunk's products are done: P may be overwritten, and what is made here
+        // is never two chunks ahead
+        if (n > 0) la_wait(b_ds, (uint32_t)((n - 1) & 1), dead);
         if (!STATES) {
           // P = (Q K^T) . D: 16 rows a warp, two rows a thread
-          la_wait(b_qk, (uint32_t)(n & 1), dead);
           tc5_fence_after();
-          if (CF::RW > 1 && n > 0) la_wait(b_ds, (uint32_t)((n - 1) & 1), dead);  // the last P was used
           const int r0 = fw * 16 + lane / 4;
           const float sign = a.reverse ? -1.f : 1.f;
           const float h0 = fac[r0], l0 = fac[kLaChunk + r0], h1 = fac[r0 + 8], l1 = fac[kLaChunk + r0 + 8];
@@ -688,7 +714,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
 #pragma unroll 1
           for (int cb = from; cb < to; ++cb) {
             uint32_t x[8];
-            tmem_ld_rows16(x, tmem + ((uint32_t)(fw * 32) << 16) + CF::cQK + cb * 16);
+            tmem_ld_rows16(x, tmem + ((uint32_t)(fw * 32) << 16) + CF::cQK + (n % CF::kAhead) * 64 + cb * 16);
             uint64_t gh[2], gl[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -895,8 +921,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   if (warp == kLaMmaWarp) {
     if (*dead) {
       if (lane == 0) {
-        mma_commit(b_qk);
-        for (int i = 0; i < 4096 && !mbar_try_wait(b_qk, 0); ++i) {}
+        mma_commit(single);  // not used otherwise
+        for (int i = 0; i < 4096 && !mbar_try_wait(single, 0); ++i) {}
       }
       __syncwarp();
     }
