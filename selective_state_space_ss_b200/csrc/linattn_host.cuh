@@ -88,11 +88,11 @@ struct LaSeg {  // a workspace's share for segments or workers
   unsigned* flags = nullptr;
 };
 size_t la_carry_bytes(const LaShape& s, const LaSegs& g) {
-  // eight back warps' states, for keys or (in a gradient) values up to 64 or 128 wide
+  // sixteen back warps' states, for keys or (in a gradient) values up to 64 or 128 wide
   return align256((size_t)g.workers * 128 * (s.dk <= 64 && s.dv <= 64 ? 64 : 128) * 4);
 }
 size_t la_seg_bytes(const LaShape& s, const LaSegs& g) {
-  if (g.workers > 0) return la_carry_bytes(s, g) + align256((1 + (size_t)g.workers * 8) * 4);
+  if (g.workers > 0) return la_carry_bytes(s, g) + align256((1 + (size_t)g.workers * 16) * 4);
   if (g.nseg <= 1) return 0;
   return align256((size_t)s.bh() * g.nseg * s.per_state() * 4) + align256((size_t)s.bh() * g.nseg * 8);
 }
@@ -152,7 +152,7 @@ ss_status la_launch(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream
   const int64_t grid = a.workers > 0 ? a.workers : (int64_t)a.bh * a.nseg;
   if (grid > INT_MAX) return SS_ERR_INVALID_ARG;
   if (a.workers > 0 &&
-      cudaMemsetAsync(a.flags, 0, (1 + (size_t)a.workers * 8) * sizeof(unsigned), stream) != cudaSuccess)
+      cudaMemsetAsync(a.flags, 0, (1 + (size_t)a.workers * 16) * sizeof(unsigned), stream) != cudaSuccess)
     return SS_ERR_CUDA;
   linattn_pass_kernel<T, KD, VD, STATES><<<(unsigned)grid, CF::kThreads, CF::kSmem, stream>>>(a, maps);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
@@ -284,7 +284,7 @@ LaBwdWs la_bwd_ws(const LaShape& s, const LaSegs& g) {
   const size_t rows = (size_t)s.bh() * s.seqlen;
   w.dots_q = take(rows * 16);
   w.dots_k = take(rows * 16);
-  w.anchor = take((size_t)s.bh() * w.anchors * 8 * 4);
+  w.anchor = take((size_t)s.bh() * w.anchors * 16 * 4);
   w.dump = take((size_t)s.bh() * w.anchors * 128 * (s.dv <= 64 ? 64 : 128) * 4);
   w.part = take(s.heads > s.qk_heads ? rows * s.dk * 4 : 0);
   w.bytes = at;

@@ -36,8 +36,8 @@
 // hold sums of whatever follows in shared memory and nobody reads them.
 //
 // Roles.  Loaders (two warps) fill rings of K, V and Q tiles, one warp works out the
-// decays, one thread issues the MMAs; the front warps (four) turn scores into P and
-// keys into weighted keys one chunk ahead of the back warps (eight), which hold the
+// decays, one thread issues the MMAs; the front warps (eight) turn scores into P and
+// keys into weighted keys one chunk ahead of the back warps (sixteen), which hold the
 // state: they take O and the state's increment from tensor memory, give the state
 // back as planes, and write O out while the next chunk's products run.
 //
@@ -60,7 +60,8 @@ namespace ssscan {
 
 constexpr int kLaChunk = 64;
 constexpr int kLaBlock = kLaChunk * kTileRow;  // bytes of one plane's 64 x 64 block
-constexpr uint32_t kLaSpinLimit = 1u << 20;
+constexpr uint32_t kLaSpinLimit = 1u << 9;        // polls of a barrier: a few seconds
+constexpr uint32_t kLaCarrySpinLimit = 1u << 24;  // of the previous worker's flag: likewise
 
 // A [batch, seqlen, heads, d] tensor, last axis contiguous, strides in elements;
 // `share` consecutive heads of the pass read one of its heads.
@@ -84,7 +85,7 @@ struct LaPassArgs {
   LaTensor x;           // rows to take the inner product of each output row with (ptr null: none)
   float* dots;          // [batch * heads, seqlen, 4] partial products of x, one a lane quadrant
   float* dump;          // forward: where the states at anchors go; reversed: where they come from
-  float* anchor;        // reversed: [batch * heads, anchors, 8] partial products <R, S>, one a back warp
+  float* anchor;        // reversed: [batch * heads, anchors, 16] partial products <R, S>, one a back warp
   int anchor_chunks;    // an anchor behind every so many chunks
   int anchors;          // anchors of the longest row
   int heads, seqlen, dk, dv;
@@ -92,7 +93,7 @@ struct LaPassArgs {
   int nseg, seg_chunks; // segments of a head, or
   int workers;          // > 0: CTAs that share all chunks evenly
   float* carry;         // [workers] states handed to the next worker
-  unsigned* flags;      // [0] hands out worker numbers, then [workers][8] one a back warp; zero at launch
+  unsigned* flags;      // [0] hands out worker numbers, then [workers][16] one a back warp; zero at launch
   int reverse;
   int vec;              // 16-byte loads apply to q, k and v
   int out_vec;          // 16-byte stores to out
@@ -123,8 +124,8 @@ struct LaCfg {
   static constexpr int kW = kP + NPX * kLaBlock;
   static constexpr int kFacFloats = 4 * kLaChunk + 4;
   static constexpr int kFac = kW + RW * kTileW;
-  static constexpr int kStage = kFac + (RF * kFacFloats * 4 + 127) / 128 * 128;  // 1 KB a back warp
-  static constexpr int kBars = kStage + (kBf16 ? 8 * 1024 : 0);
+  static constexpr int kStage = kFac + (RF * kFacFloats * 4 + 127) / 128 * 128;  // 512 bytes a back warp
+  static constexpr int kBars = kStage + (kBf16 ? 16 * 512 : 0);
   static constexpr int kSmem = kBars + (8 * kRing + 8) * 8 + 16;
   // tensor memory columns
   static constexpr int cDS = 0, cSP = KD, cO1 = cSP + NPX * KD / 2, cO2 = cO1 + 64, cQK = cO2 + 64;
@@ -133,22 +134,28 @@ struct LaCfg {
   static_assert(cQK + 64 * kAhead <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr int kQuads = VD / 32;        // lane quadrants that hold values
-  static constexpr int kHolders = 2 * kQuads;   // back warps at work
+  static constexpr int kHolders = 4 * kQuads;   // back warps at work
   static constexpr int kLoaders = 64;           // loader threads
-  static constexpr int kThreads = 512;
+  static constexpr int kThreads = 896;
 };
-constexpr int kLaBackWarps = 8, kLaFrontWarps = 4;
-constexpr int kLaMmaWarp = 12, kLaLoadWarp = 13, kLaDecayWarp = 15;
-// registers a thread of the three kinds of warpgroup: 2 x 168 + 104 + 72 = 4 x 128 at launch
-constexpr int kLaBackRegs = 168, kLaFrontRegs = 104, kLaAuxRegs = 72;
+constexpr int kLaBackWarps = 16, kLaFrontWarps = 8;
+constexpr int kLaMmaWarp = 24, kLaLoadWarp = 25, kLaDecayWarp = 27;
+// registers a thread of the three kinds of warpgroup: 4 x 88 + 2 x 56 + 40 = 7 x 72 at launch
+constexpr int kLaBackRegs = 88, kLaFrontRegs = 56, kLaAuxRegs = 40;
 
 // Waits of one CTA: when one gives up, the others stop waiting too, and the kernel
-// runs to its end on whatever is there, inside its buffers.
+// runs to its end on whatever is there, inside its buffers.  A poll may suspend the
+// thread for up to 10 ms, so that those that wait leave the issue slots to the others.
 __device__ __forceinline__ void la_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
 #pragma unroll 1
   for (uint32_t i = 0; i < kLaSpinLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return;
-    if (*dead) return;
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(10000000)
+        : "memory");
+    if (ok || *dead) return;
   }
   atomicOr(&g_error_word, kErrTmaWait);
   *dead = 1;
@@ -285,12 +292,12 @@ struct LaWidth {
   static constexpr int value = N;
 };
 
-// 32 values x 32 tokens of a back warp to the output, and their products with the
+// 32 values x 16 tokens of a back warp to the output, and their products with the
 // rows of x.  o[h][4 i + z]: value v0 + 16 h + 8 (z / 2) + lane / 4, token
-// t0 + 8 i + 2 (lane % 4) + z % 2.  bf16 rows go through 1 KB of shared memory, so
-// that a token's 32 values leave as 64 bytes in 16-byte stores.
+// t0 + 8 i + 2 (lane % 4) + z % 2.  bf16 rows go through 512 bytes of shared memory, 8
+// tokens at a time, so that a token's 32 values leave as 64 bytes in 16-byte stores.
 template <typename T>
-__device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2][16], char* stage, int64_t b, int64_t bh,
+__device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2][8], char* stage, int64_t b, int64_t bh,
                                         int h, int t0, int len, int v0, int quad, int lane) {
   const int64_t rs = (int64_t)a.heads * a.dv;
   const int64_t at = ((b * a.seqlen + t0) * a.heads + h) * a.dv + v0;
@@ -301,27 +308,20 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at + tok * rs + c * 8;
     const bool mine = v0 + c * 8 < a.dv;
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        store_blocks_t(to + e * 512, to_bf16x2(o[0][4 * (i + e)], o[0][4 * (i + e) + 1]),
-                       to_bf16x2(o[0][4 * (i + e) + 2], o[0][4 * (i + e) + 3]),
-                       to_bf16x2(o[1][4 * (i + e)], o[1][4 * (i + e) + 1]),
-                       to_bf16x2(o[1][4 * (i + e) + 2], o[1][4 * (i + e) + 3]));
+    for (int i = 0; i < 2; ++i) {
+      store_blocks_t(to, to_bf16x2(o[0][4 * i], o[0][4 * i + 1]), to_bf16x2(o[0][4 * i + 2], o[0][4 * i + 3]),
+                     to_bf16x2(o[1][4 * i], o[1][4 * i + 1]), to_bf16x2(o[1][4 * i + 2], o[1][4 * i + 3]));
       __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint4 y = *reinterpret_cast<const uint4*>(from + e * 512);
-        const int t = t0 + (i + e) * 8 + tok;
-        if (mine && t < len && in_range(t, a.seqlen)) *reinterpret_cast<uint4*>(out + (i + e) * 8 * rs) = y;
-      }
+      const uint4 y = *reinterpret_cast<const uint4*>(from);
+      const int t = t0 + i * 8 + tok;
+      if (mine && t < len && in_range(t, a.seqlen)) *reinterpret_cast<uint4*>(out + i * 8 * rs) = y;
       __syncwarp();
     }
   } else {
     const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
     const int64_t mine = at + lane / 4 + 2 * (lane % 4) * rs;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         const int64_t row = mine + (8 * i + z) * rs;
@@ -340,9 +340,9 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
     const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
     const char* from = la_row(a.x, b, t, h, sizeof(T)) + (int64_t)v * sizeof(T);
     const int64_t xs = a.x.st * (int64_t)sizeof(T);
-    float sum[8];
+    float sum[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         float y = 0.f;
@@ -353,14 +353,14 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
                      to_f32(reinterpret_cast<const T*>(from + (8 * i + z) * xs)[8 * u]), y);
         sum[2 * i + z] = y;
       }
-    // the lanes with the same tokens are 4, 8 and 16 apart; lane / 4 keeps token pair it
+    // the lanes with the same tokens are 4, 8 and 16 apart
 #pragma unroll
-    for (int s = 0; s < 8; ++s)
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int m = 4; m <= 16; m *= 2) sum[s] += __shfl_xor_sync(kFullMask, sum[s], m);
     if (lane < 4) {
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
+      for (int s = 0; s < 4; ++s) {
         const int tt = t + 8 * (s / 2) + s % 2;
         if (tt < len) a.dots[(bh * a.seqlen + tt) * 4 + quad] = sum[s];
       }
@@ -637,23 +637,23 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   } else if (warp >= kLaBackWarps) {
     // ---- front: weighted keys and P, a chunk ahead of the back
     regs_give<kLaFrontRegs>();
-    const int fw = warp - kLaBackWarps, ftid = tid - 32 * kLaBackWarps;
+    // 16 rows of P for each pair of warps, side 0 with every other block of columns
+    const int fw = warp % 4, side = (warp - kLaBackWarps) / 4, ftid = tid - 32 * kLaBackWarps;
     int n = 0;
-    // Shares of the 32 or 16 steps of a key tile.  A warp's rows of P have one to four
-    // blocks of 16 columns under the mask (reversed: four to one), each about as much
-    // work as one and a half steps of 128-wide keys: the others' shares make up for it.
-    const int at = STATES ? 0 : a.reverse ? 4 - fw : fw;
-    const auto share = [&](int i) {
-      return STATES ? i * CF::KB * 4 : CF::KB == 2 ? (i == 0 ? 0 : i == 1 ? 11 : i == 2 ? 20 : i == 3 ? 27 : 32)
-                                                   : (i == 0 ? 0 : i == 1 ? 7 : i == 2 ? 12 : i == 3 ? 15 : 16);
-    };
-    const int w_from = STATES ? share(fw) : a.reverse ? share(at - 1) : share(at);
-    const int w_to = STATES ? share(fw + 1) : a.reverse ? share(at) : share(at + 1);
+    // Shares of the 32 or 16 steps of a key tile.  A warp's rows of P have none to two
+    // blocks of 16 columns under the mask, each about as much work as one and a half
+    // steps: where they have fewer, the share of the steps is larger.  Byte i is where
+    // the share of the i-th warp begins, in the order of rows (reversed: from the last).
+    const int at = 2 * (a.reverse ? 3 - fw : fw) + side;
+    const uint64_t begins = STATES ? (CF::KB == 2 ? 0x1c1814100c080400ull : 0x0e0c0a0806040200ull)
+                                   : (CF::KB == 2 ? 0x1d1a16130f0a0400ull : 0x0f0e0c0b09060200ull);
+    const int w_from = (int)(begins >> (8 * at)) & 0xff;
+    const int w_to = at == 7 ? CF::KB * 16 : (int)(begins >> (8 * at + 8)) & 0xff;
     if (!STATES) {
       // what the mask takes away is zero once and for all
       for (int i = ftid; i < NPX * kLaBlock / 16; i += 32 * kLaFrontWarps)
         reinterpret_cast<uint4*>(smem + CF::kP)[i] = make_uint4(0, 0, 0, 0);
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");
     }
     for (int i = 0; i < work.pieces; ++i) {
       const LaPiece p = la_piece(a, work, i);
@@ -712,7 +712,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           // 16 columns at a time, those that the mask leaves (the others stay zero)
           const int from = a.reverse ? fw : 0, to = a.reverse ? 4 : fw + 1;
 #pragma unroll 1
-          for (int cb = from; cb < to; ++cb) {
+          for (int cb = from + side; cb < to; cb += 2) {
             uint32_t x[8];
             tmem_ld_rows16(x, tmem + ((uint32_t)(fw * 32) << 16) + CF::cQK + (n % CF::kAhead) * 64 + cb * 16);
             uint64_t gh[2], gl[2];
@@ -755,26 +755,25 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   } else {
     // ---- back: the state and the outputs
     regs_take<kLaBackRegs>();
-    const int quad = warp % 4, half = warp / 4;
+    const int quad = warp % 4, part = warp / 4;  // value lanes; a quarter of the keys and tokens
     if (quad < CF::kQuads) {
       const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
       const int vi = quad * 32 + lane;          // this thread's value index
-      constexpr int KH = KD / 2;                // its key indices: half * KH ...
+      constexpr int KH = KD / 4;                // its key indices: part * KH ...
       uint64_t S[KH / 2];                       // in pairs
       auto store_planes = [&]() {
 #pragma unroll
-        for (int c = 0; c < KH; c += 32) {
-          uint32_t w[NPX][16];
+        for (int c = 0; c < KH / 2; c += 8) {
+          uint32_t w[NPX][8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 8; ++i) {
             uint32_t s[NPX];
-            split2<NPX>(S[c / 2 + i], s);
+            split2<NPX>(S[c + i], s);
 #pragma unroll
             for (int p = 0; p < NPX; ++p) w[p][i] = s[p];
           }
 #pragma unroll
-          for (int p = 0; p < NPX; ++p)
-            tmem_st16(lanes + CF::cSP + p * (KD / 2) + half * (KD / 4) + c / 2, w[p]);
+          for (int p = 0; p < NPX; ++p) tmem_st(lanes + CF::cSP + p * (KD / 2) + part * (KH / 2) + c, w[p]);
         }
         tmem_wait_st();
       };
@@ -786,10 +785,10 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         const int all_chunks = (len + kLaChunk - 1) / kLaChunk;
         const int step = a.workers > 0 ? 0 : work.worker % a.nseg;
         if (p.from_carry) {
-          const unsigned* flag = a.flags + 1 + (work.worker - 1) * 8 + warp;
+          const unsigned* flag = a.flags + 1 + (work.worker - 1) * 16 + warp;
           if (lane == 0) {
             unsigned there = 0;
-            for (uint32_t spin = 0; spin < kLaSpinLimit && !there && !*dead; ++spin) {
+            for (uint32_t spin = 0; spin < kLaCarrySpinLimit && !there && !*dead; ++spin) {
               asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(there) : "l"(flag) : "memory");
               if (!there) __nanosleep(64);
             }
@@ -799,7 +798,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             }
           }
           __syncwarp();
-          const float4* from = reinterpret_cast<const float4*>(a.carry + ((int64_t)(work.worker - 1) * 8 + warp) * (KH * 32));
+          const float4* from = reinterpret_cast<const float4*>(a.carry + ((int64_t)(work.worker - 1) * 16 + warp) * (KH * 32));
 #pragma unroll
           for (int c = 0; c < KH; c += 4) {
             const float4 x = __ldcg(from + c / 4 * 32 + lane);
@@ -807,10 +806,10 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
         } else {
           const bool in = a.s_in && !STATES && vi < a.dv;
-          const float* from = a.s_in + bh * a.s_in_head + step * a.s_in_seg + half * KH * a.sk + vi * a.sv;
+          const float* from = a.s_in + bh * a.s_in_head + step * a.s_in_seg + part * KH * a.sk + vi * a.sv;
 #pragma unroll
           for (int c = 0; c < KH; c += 2) {
-            const int kk = half * KH + c;
+            const int kk = part * KH + c;
             S[c / 2] = pair(in && kk < a.dk ? from[0] : 0.f, in && kk + 1 < a.dk ? from[a.sk] : 0.f);
             from += 2 * a.sk;
           }
@@ -830,7 +829,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             // <R, S> behind this chunk: R is the state here, S the forward pass's
             float sum = 0.f;
             const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
-            const float* from = a.dump + (an * 8 + warp) * (KH * 32);
+            const float* from = a.dump + (an * 16 + warp) * (KH * 32);
 #pragma unroll
             for (int c = 0; c < KH; c += 4) {
               const float4 x = reinterpret_cast<const float4*>(from)[c / 4 * 32 + lane];
@@ -838,54 +837,50 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             }
 #pragma unroll
             for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
-            if (lane == 0) a.anchor[an * 8 + warp] = sum;
+            if (lane == 0) a.anchor[an * 16 + warp] = sum;
           }
           la_wait(&full_f[n % CF::RF], (uint32_t)((n / CF::RF) & 1), dead);
           const float decay = fac[4 * kLaChunk];
           la_wait(STATES ? b_ds : b_o, (uint32_t)(n & 1), dead);
           tc5_fence_after();
-          float o[2][16];
+          float o[2][8];
+          uint32_t x[KH];
           if (!STATES) {
-            uint32_t x1[2][16], x2[2][16];
+            uint32_t x1[2][8], x2[2][8];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              tmem_ld_rows16(x1[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO1 + half * 32);
-              tmem_ld_rows16(x2[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO2 + half * 32);
+              tmem_ld_rows16(x1[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO1 + part * 16);
+              tmem_ld_rows16(x2[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO2 + part * 16);
             }
-            uint64_t f[4];
+            tmem_ld(x, lanes + CF::cDS + part * KH);
+            float2 f[2];
 #pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4)
-              f[i4] = *reinterpret_cast<const uint64_t*>(fac + 2 * kLaChunk + half * 32 + i4 * 8 + 2 * (lane % 4));
+            for (int i2 = 0; i2 < 2; ++i2)
+              f[i2] = *reinterpret_cast<const float2*>(fac + 2 * kLaChunk + part * 16 + i2 * 8 + 2 * (lane % 4));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               tmem_wait_ld(x1[e]);
               tmem_wait_ld(x2[e]);
 #pragma unroll
-              for (int i2 = 0; i2 < 8; ++i2) {
-                const uint64_t y = fma2(pair(x2[e][2 * i2], x2[e][2 * i2 + 1]), f[i2 / 2], pair(x1[e][2 * i2], x1[e][2 * i2 + 1]));
-                o[e][2 * i2] = pair_lo(y);
-                o[e][2 * i2 + 1] = pair_hi(y);
-              }
+              for (int i2 = 0; i2 < 8; ++i2)
+                o[e][i2] = fmaf(__uint_as_float(x2[e][i2]), i2 % 2 ? f[i2 / 4].y : f[i2 / 4].x, __uint_as_float(x1[e][i2]));
             }
+          } else {
+            tmem_ld(x, lanes + CF::cDS + part * KH);
           }
           const uint64_t decay2 = pair(decay, decay);
+          tmem_wait_ld(x);
 #pragma unroll
-          for (int c = 0; c < KH; c += 32) {
-            uint32_t x[32];
-            tmem_ld32(x, lanes + CF::cDS + half * KH + c);
-            tmem_wait_ld(x);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) S[c / 2 + e] = fma2(S[c / 2 + e], decay2, pair(x[2 * e], x[2 * e + 1]));
-          }
+          for (int e = 0; e < KH / 2; ++e) S[e] = fma2(S[e], decay2, pair(x[2 * e], x[2 * e + 1]));
           tc5_fence_before();
           arrive(b_free);
           arrive(&empty_f[n % CF::RF]);
           if (!STATES && cc + 1 < p.last) give_state();
           if (!STATES)
-            la_emit<T>(a, o, smem + CF::kStage + warp * 1024, b, bh, h, t0 + half * 32, len, quad * 32, quad, lane);
+            la_emit<T>(a, o, smem + CF::kStage + warp * 512, b, bh, h, t0 + part * 16, len, quad * 32, quad, lane);
           if (!STATES && !a.reverse && anchor_here) {
             const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
-            float* to = a.dump + (an * 8 + warp) * (KH * 32);
+            float* to = a.dump + (an * 16 + warp) * (KH * 32);
 #pragma unroll
             for (int c = 0; c < KH; c += 4)
               reinterpret_cast<float4*>(to)[c / 4 * 32 + lane] =
@@ -893,7 +888,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
         }
         if (p.to_carry) {
-          float4* to = reinterpret_cast<float4*>(a.carry + ((int64_t)work.worker * 8 + warp) * (KH * 32));
+          float4* to = reinterpret_cast<float4*>(a.carry + ((int64_t)work.worker * 16 + warp) * (KH * 32));
 #pragma unroll
           for (int c = 0; c < KH; c += 4) 
             __stcg(to + c / 4 * 32 + lane,
@@ -901,12 +896,12 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           __threadfence();
           __syncwarp();
           if (lane == 0)
-            asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(a.flags + 1 + work.worker * 8 + warp), "r"(1u) : "memory");
+            asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(a.flags + 1 + work.worker * 16 + warp), "r"(1u) : "memory");
         } else if (a.s_out && (STATES || step == a.nseg - 1) && vi < a.dv) {
-          float* to = a.s_out + bh * a.s_out_head + step * a.s_out_seg + half * KH * a.sk + vi * a.sv;
+          float* to = a.s_out + bh * a.s_out_head + step * a.s_out_seg + part * KH * a.sk + vi * a.sv;
 #pragma unroll
           for (int c = 0; c < KH; ++c) {
-            if (half * KH + c < a.dk) *to = c % 2 ? pair_hi(S[c / 2]) : pair_lo(S[c / 2]);
+            if (part * KH + c < a.dk) *to = c % 2 ? pair_hi(S[c / 2]) : pair_lo(S[c / 2]);
             to += a.sk;
           }
         }
@@ -988,8 +983,8 @@ __global__ void linattn_decay_grad_kernel(const float* dots_q, const float* dots
   if (begin >= len) return;
   const int end = begin + anchor_tokens < len ? (int)(begin + anchor_tokens) : len;
   double carry = 0.0;
-  for (int i = 0; i < 8; ++i)
-    if (!two_quads || i % 4 < 2) carry += anchor[(bh * anchors + an) * 8 + i];
+  for (int i = 0; i < 16; ++i)
+    if (!two_quads || i % 4 < 2) carry += anchor[(bh * anchors + an) * 16 + i];
   for (int hi = end; hi > begin; hi -= 32) {
     const int t = hi - 1 - lane;  // lane 0 the latest
     double x = 0.0;
