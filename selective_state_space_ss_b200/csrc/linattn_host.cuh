@@ -30,7 +30,8 @@ struct LaShape {
 ss_status la_check_shape(const LaShape& s, int in_dtype) {
   if (s.batch < 1 || s.seqlen < 1 || s.heads < 1 || s.qk_heads < 1 || s.dk < 1 || s.dv < 1) return SS_ERR_INVALID_ARG;
   if (s.heads % s.qk_heads != 0) return SS_ERR_INVALID_ARG;
-  if (s.seqlen > INT_MAX - 1024 || s.batch > INT_MAX || s.batch * s.heads > (1 << 24)) return SS_ERR_INVALID_ARG;
+  if (s.seqlen > INT_MAX - 1024 || s.batch > INT_MAX || s.heads > 65536 || s.batch * s.heads > (1 << 24))
+    return SS_ERR_INVALID_ARG;
   if (s.dk > 128 || s.dv > 128) return SS_ERR_UNSUPPORTED;
   if (in_dtype != SS_F32 && in_dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
   return SS_OK;
@@ -140,12 +141,12 @@ bool la_map(CUtensorMap* m, const LaTensor& x, int64_t batch, int64_t seqlen, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int KD, int VD, bool STATES>
+template <typename T, int KD, int VD, LaMode MODE>
 ss_status la_launch(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream) {
   using CF = LaCfg<T, KD, VD>;
   struct Tag : CF {};
   if (once_per_device<Tag>([] {
-        return cudaFuncSetAttribute(linattn_pass_kernel<T, KD, VD, STATES>,
+        return cudaFuncSetAttribute(linattn_pass_kernel<T, KD, VD, MODE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, CF::kSmem) == cudaSuccess;
       }) != 1)
     return SS_ERR_CUDA;
@@ -154,29 +155,30 @@ ss_status la_launch(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream
   if (a.workers > 0 &&
       cudaMemsetAsync(a.flags, 0, (1 + (size_t)a.workers * 16) * sizeof(unsigned), stream) != cudaSuccess)
     return SS_ERR_CUDA;
-  linattn_pass_kernel<T, KD, VD, STATES><<<(unsigned)grid, CF::kThreads, CF::kSmem, stream>>>(a, maps);
+  linattn_pass_kernel<T, KD, VD, MODE><<<(unsigned)grid, CF::kThreads, CF::kSmem, stream>>>(a, maps);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
-template <typename T, bool STATES>
+template <typename T, LaMode MODE>
 ss_status la_dispatch(LaPassArgs a, int64_t batch, cudaStream_t stream) {
   const int es = sizeof(T);
-  a.vec = la_vec(a.k, a.dk, es) && la_vec(a.v, a.dv, es) && (STATES || la_vec(a.q, a.dk, es));
+  a.vec = la_vec(a.k, a.dk, es) && la_vec(a.v, a.dv, es) && (MODE == kLaStates || la_vec(a.q, a.dk, es));
   a.out_vec = es == 2 && !a.out_f32 && a.out && aligned(a.out, 16) && a.dv % 8 == 0;
+  a.x_vec = es == 2 && a.x.ptr && la_vec(a.x, a.dv, es);
   LaMaps m = {};
   if (es == 2 && a.vec) {
     auto map = [&](CUtensorMap* to, const LaTensor& x, int d) {
       return la_map(to, x, batch, a.seqlen, a.heads / x.share, d);
     };
-    a.tma = map(&m.k, a.k, a.dk) && map(&m.v, a.v, a.dv) && (STATES || map(&m.q, a.q, a.dk));
+    a.tma = map(&m.k, a.k, a.dk) && map(&m.v, a.v, a.dv) && (MODE == kLaStates || map(&m.q, a.q, a.dk));
   }
-  if (a.dk <= 64) return a.dv <= 64 ? la_launch<T, 64, 64, STATES>(a, m, stream) : la_launch<T, 64, 128, STATES>(a, m, stream);
-  return a.dv <= 64 ? la_launch<T, 128, 64, STATES>(a, m, stream) : la_launch<T, 128, 128, STATES>(a, m, stream);
+  if (a.dk <= 64) return a.dv <= 64 ? la_launch<T, 64, 64, MODE>(a, m, stream) : la_launch<T, 64, 128, MODE>(a, m, stream);
+  return a.dv <= 64 ? la_launch<T, 128, 64, MODE>(a, m, stream) : la_launch<T, 128, 128, MODE>(a, m, stream);
 }
 
-template <bool STATES>
+template <LaMode MODE>
 ss_status la_pass(const LaPassArgs& a, bool bf16, int64_t batch, cudaStream_t stream) {
-  return bf16 ? la_dispatch<__nv_bfloat16, STATES>(a, batch, stream) : la_dispatch<float, STATES>(a, batch, stream);
+  return bf16 ? la_dispatch<__nv_bfloat16, MODE>(a, batch, stream) : la_dispatch<float, MODE>(a, batch, stream);
 }
 
 // The starting states of every segment of pass `a` (its k, v, g and directions) into seg.
@@ -189,7 +191,7 @@ ss_status la_segment_states(LaPassArgs a, const LaShape& s, const LaSegs& g, con
   a.s_out_head = (int64_t)g.nseg * s.per_state();
   a.s_out_seg = s.per_state();
   a.seg_decay = seg.decay;
-  const ss_status st = la_pass<true>(a, s.bf16, s.batch, stream);
+  const ss_status st = la_pass<kLaStates>(a, s.bf16, s.batch, stream);
   if (st != SS_OK) return st;
   // rows of the grid are at most 2^16 - 1: whole states of up to that many heads a launch
   for (int64_t at = 0; at < s.bh(); at += 65535) {
@@ -257,7 +259,7 @@ ss_status linattn_fwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   a.s_out = last;
   a.out = o;
   a.scale_p = a.scale_o = scale;
-  return la_pass<false>(a, s.bf16, s.batch, stream);
+  return la_pass<kLaOutputs>(a, s.bf16, s.batch, stream);
 }
 
 // ---- backward
@@ -351,7 +353,7 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   a.out_f32 = share > 1;
   a.x = tq;
   a.dots = reinterpret_cast<float*>(base + w.dots_q);
-  if ((st = la_pass<false>(a, s.bf16, s.batch, stream)) != SS_OK) return st;
+  if ((st = la_pass<kLaProducts>(a, s.bf16, s.batch, stream)) != SS_OK) return st;
   if (share > 1 && (st = s.bf16 ? la_share_sum<__nv_bfloat16>(part, dq, lengths, s, stream)
                                 : la_share_sum<float>(part, dq, lengths, s, stream)) != SS_OK)
     return st;
@@ -369,7 +371,7 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   a.x = tk;
   a.dots = reinterpret_cast<float*>(base + w.dots_k);
   // the initial state's gradient waits for the last pass where it overwrites dlast
-  if ((st = la_pass<false>(a, s.bf16, s.batch, stream)) != SS_OK) return st;
+  if ((st = la_pass<kLaProducts>(a, s.bf16, s.batch, stream)) != SS_OK) return st;
   if (share > 1 && (st = s.bf16 ? la_share_sum<__nv_bfloat16>(part, dk, lengths, s, stream)
                                 : la_share_sum<float>(part, dk, lengths, s, stream)) != SS_OK)
     return st;
@@ -392,7 +394,7 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   a.dots = nullptr;
   a.dump = nullptr;
   a.s_out = ds0;
-  return la_pass<false>(a, s.bf16, s.batch, stream);
+  return la_pass<kLaOutputs>(a, s.bf16, s.batch, stream);
 }
 
 // ---- single tokens

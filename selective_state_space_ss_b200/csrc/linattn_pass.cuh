@@ -96,7 +96,7 @@ struct LaPassArgs {
   unsigned* flags;      // [0] hands out worker numbers, then [workers][16] one a back warp; zero at launch
   int reverse;
   int vec;              // 16-byte loads apply to q, k and v
-  int out_vec;          // 16-byte stores to out
+  int out_vec, x_vec;   // 16-byte stores to out, loads of x
   int tma;              // so do the tensor maps
   float scale_p, scale_o, scale_w;
 };
@@ -110,23 +110,22 @@ struct LaCfg {
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int NPI = kBf16 ? 1 : 3;  // planes of the inputs
   static constexpr int NPX = kBf16 ? 2 : 3;  // planes of the scores and of the state as operands
-  static constexpr int NPW = 3;              // planes of the weighted keys
+  static constexpr int NPW = kBf16 ? 4 : 3;  // planes of the weighted keys
   static constexpr int KB = KD / 64, VB = VD / 64;
   // Tiles in each ring.  A key tile lives until its chunk's increment is formed (the
   // weighted keys' first planes replace it in place), a query tile until S Q is.
   static constexpr int RK = kBf16 ? 3 : 2, RQ = kBf16 ? 3 : 1, RV = kBf16 ? (KB == 2 && VB == 2 ? 2 : 3) : 1;
-  static constexpr int RW = 2;               // the weighted keys' further planes
   static constexpr int RF = 4;               // decays
   static constexpr int kRing = 4;
   static_assert(RK <= kRing && RV <= kRing && RQ <= kRing && RF <= kRing, "barriers of a ring");
   static constexpr int kTileK = KB * NPI * kLaBlock, kTileV = VB * NPI * kLaBlock, kTileW = KB * (NPW - NPI) * kLaBlock;
   static constexpr int kQ = 0, kK = RQ * kTileK, kV = kK + RK * kTileK, kP = kV + RV * kTileV;
   static constexpr int kW = kP + NPX * kLaBlock;
-  static constexpr int kFacFloats = 4 * kLaChunk + 4;
-  static constexpr int kFac = kW + RW * kTileW;
+  static constexpr int kFacFloats = (kBf16 ? 6 : 4) * kLaChunk + 4;
+  static constexpr int kFac = kW + kTileW;
   static constexpr int kStage = kFac + (RF * kFacFloats * 4 + 127) / 128 * 128;  // 512 bytes a back warp
   static constexpr int kBars = kStage + (kBf16 ? 16 * 512 : 0);
-  static constexpr int kSmem = kBars + (8 * kRing + 8) * 8 + 16;
+  static constexpr int kSmem = kBars + 10 * kRing * 8 + 16;
   // tensor memory columns
   static constexpr int cDS = 0, cSP = KD, cO1 = cSP + NPX * KD / 2, cO2 = cO1 + 64, cQK = cO2 + 64;
   static constexpr int kAhead = kBf16 ? 2 : 1;  // chunks that scores run ahead, one place for each
@@ -146,20 +145,44 @@ constexpr int kLaBackRegs = 88, kLaFrontRegs = 56, kLaAuxRegs = 40;
 // Waits of one CTA: when one gives up, the others stop waiting too, and the kernel
 // runs to its end on whatever is there, inside its buffers.  A poll may suspend the
 // thread for up to 10 ms, so that those that wait leave the issue slots to the others.
-__device__ __forceinline__ void la_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+__device__ __forceinline__ void la_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
 #pragma unroll 1
   for (uint32_t i = 0; i < kLaSpinLimit; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(10000000)
+        : "r"(bar), "r"(parity), "r"(10000000)
         : "memory");
-    if (ok || *dead) return;
+    if (ok) return;
+    if (*dead) return;
   }
   atomicOr(&g_error_word, kErrTmaWait);
   *dead = 1;
 }
+__device__ __forceinline__ void la_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void la_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void la_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// A place in a ring of R and how often it came round: full barriers complete phase
+// `turn`, empty ones are waited for from the second turn on.
+template <int R>
+struct LaRing {
+  int i = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == R) i = 0, ++turn;
+  }
+  __device__ __forceinline__ uint32_t full() const { return turn & 1; }
+  __device__ __forceinline__ bool used() const { return turn > 0; }
+  __device__ __forceinline__ uint32_t empty() const { return (turn - 1) & 1; }
+};
 
 __device__ __forceinline__ int la_length(const LaPassArgs& a, int64_t b) {
   if (!a.lengths) return a.seqlen;
@@ -247,11 +270,13 @@ __device__ __forceinline__ float la_exp2(int64_t x) {
   return n < -126 ? 0.f : n > 127 ? __int_as_float(0x7f800000) : z;
 }
 
-// A chunk's decays: running sums, base 2, as integer and fraction, the factors of the
-// rows and of the keys, and the chunk's whole decay, which is returned.  One warp, two
-// tokens a lane.  The sums are whole numbers of 2^-32, so differences of large sums
-// lose nothing.  A log decay beyond +-1400 leaves nothing, or too much, in fp32 and is
-// taken as that: minus infinity (a reset) is a number like any other here.
+// A chunk's decays: running sums, base 2, as integer and fraction (64 floats each), the
+// factors of the rows, those of the keys (for bf16 keys as three bf16 planes, each twice
+// in a word), and the chunk's whole decay, which is returned.  One warp, two tokens a
+// lane.  The sums are whole numbers of 2^-32, so differences of large sums lose nothing.
+// A log decay beyond +-1400 leaves nothing, or too much, in fp32 and is taken as that:
+// minus infinity (a reset) is a number like any other here.
+template <bool BF16>
 __device__ __forceinline__ int64_t la_decays(float* fac, float x0, float x1, bool reverse, float scale_o, float scale_w,
                                              int lane) {
   const float x[2] = {x0, x1};
@@ -269,21 +294,30 @@ __device__ __forceinline__ int64_t la_decays(float* fac, float x0, float x1, boo
   const int64_t at[2] = {sum - g[1], sum};
   // a NaN among them is not to vanish
   const float bad = __any_sync(kFullMask, x0 != x0 || x1 != x1) ? __int_as_float(0x7fffffff) : 1.f;
-  float2 hi, lo, rows, keys;
-  float* out[4] = {&hi.x, &lo.x, &rows.x, &keys.x};
+  float hi[2], lo[2], rows[2], keys[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float from_start = la_exp2(at[i]), to_end = la_exp2(total - at[i]);
-    out[0][i] = (float)(int)(at[i] >> 32);
-    out[1][i] = (float)(uint32_t)at[i] * 0x1p-32f * bad;
-    out[2][i] = (reverse ? to_end : from_start) * scale_o * bad;
-    out[3][i] = (reverse ? from_start : to_end) * scale_w * bad;
+    hi[i] = (float)(int)(at[i] >> 32);
+    lo[i] = (float)(uint32_t)at[i] * 0x1p-32f * bad;
+    rows[i] = (reverse ? to_end : from_start) * scale_o * bad;
+    keys[i] = (reverse ? from_start : to_end) * scale_w * bad;
   }
-  reinterpret_cast<float2*>(fac)[lane] = hi;
-  reinterpret_cast<float2*>(fac + kLaChunk)[lane] = lo;
-  reinterpret_cast<float2*>(fac + 2 * kLaChunk)[lane] = rows;
-  reinterpret_cast<float2*>(fac + 3 * kLaChunk)[lane] = keys;
-  if (lane == 0) fac[4 * kLaChunk] = la_exp2(total) * bad;
+  float2* out = reinterpret_cast<float2*>(fac) + lane;
+  out[0] = make_float2(hi[0], hi[1]);
+  out[32] = make_float2(lo[0], lo[1]);
+  out[64] = make_float2(rows[0], rows[1]);
+  if constexpr (BF16) {
+    uint32_t p0[3], p1[3];
+    split2<3>(pair(keys[0], keys[0]), p0);
+    split2<3>(pair(keys[1], keys[1]), p1);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) reinterpret_cast<uint2*>(fac)[96 + 32 * i + lane] = make_uint2(p0[i], p1[i]);
+    if (lane == 0) fac[6 * kLaChunk] = la_exp2(total) * bad;
+  } else {
+    out[96] = make_float2(keys[0], keys[1]);
+    if (lane == 0) fac[4 * kLaChunk] = la_exp2(total) * bad;
+  }
   return total;
 }
 
@@ -292,100 +326,65 @@ struct LaWidth {
   static constexpr int value = N;
 };
 
-// 32 values x 16 tokens of a back warp to the output, and their products with the
-// rows of x.  o[h][4 i + z]: value v0 + 16 h + 8 (z / 2) + lane / 4, token
-// t0 + 8 i + 2 (lane % 4) + z % 2.  bf16 rows go through 512 bytes of shared memory, 8
-// tokens at a time, so that a token's 32 values leave as 64 bytes in 16-byte stores.
+// 32 values x 16 tokens of a back warp, o[h][4 i + z]: value v0 + 16 h + 8 (z / 2) +
+// lane / 4, token t0 + 8 i + 2 (lane % 4) + z % 2.  To the output element by element: fp32
+// (32 bytes a token together) and rows that are not whole 16-byte units.
 template <typename T>
-__device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2][8], char* stage, int64_t b, int64_t bh,
-                                        int h, int t0, int len, int v0, int quad, int lane) {
+__device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2][8], int64_t b, int h, int t0, int len,
+                                        int v0, int lane) {
   const int64_t rs = (int64_t)a.heads * a.dv;
-  const int64_t at = ((b * a.seqlen + t0) * a.heads + h) * a.dv + v0;
-  if (sizeof(T) == 2 && !a.out_f32 && a.out_vec) {
-    const uint32_t to = smem_u32(stage) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
-    const int tok = lane / 4, c = lane % 4;
-    const char* from = stage + tok * 64 + ((c ^ ((tok >> 1) & 3)) << 4);
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at + tok * rs + c * 8;
-    const bool mine = v0 + c * 8 < a.dv;
+  const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
+  const int64_t mine = ((b * a.seqlen + t) * a.heads + h) * a.dv + v;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      store_blocks_t(to, to_bf16x2(o[0][4 * i], o[0][4 * i + 1]), to_bf16x2(o[0][4 * i + 2], o[0][4 * i + 3]),
-                     to_bf16x2(o[1][4 * i], o[1][4 * i + 1]), to_bf16x2(o[1][4 * i + 2], o[1][4 * i + 3]));
-      __syncwarp();
-      const uint4 y = *reinterpret_cast<const uint4*>(from);
-      const int t = t0 + i * 8 + tok;
-      if (mine && t < len && in_range(t, a.seqlen)) *reinterpret_cast<uint4*>(out + i * 8 * rs) = y;
-      __syncwarp();
-    }
-  } else {
-    const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
-    const int64_t mine = at + lane / 4 + 2 * (lane % 4) * rs;
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int64_t row = mine + (8 * i + z) * rs;
-        if (t + 8 * i + z < len && in_range(t + 8 * i + z, a.seqlen)) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (v + 8 * u < a.dv) {
-              const float y = o[u / 2][4 * i + 2 * (u % 2) + z];
-              if (sizeof(T) == 4 || a.out_f32) static_cast<float*>(a.out)[row + 8 * u] = y;
-              else static_cast<__nv_bfloat16*>(a.out)[row + 8 * u] = __float2bfloat16_rn(y);
-            }
-        }
-      }
-  }
-  if (a.x.ptr) {
-    const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
-    const char* from = la_row(a.x, b, t, h, sizeof(T)) + (int64_t)v * sizeof(T);
-    const int64_t xs = a.x.st * (int64_t)sizeof(T);
-    float sum[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        float y = 0.f;
+    for (int z = 0; z < 2; ++z) {
+      const int64_t row = mine + (8 * i + z) * rs;
+      if (t + 8 * i + z < len && in_range(t + 8 * i + z, a.seqlen)) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (t + 8 * i + z < len && v + 8 * u < a.dv)
-            y = fmaf(o[u / 2][4 * i + 2 * (u % 2) + z],
-                     to_f32(reinterpret_cast<const T*>(from + (8 * i + z) * xs)[8 * u]), y);
-        sum[2 * i + z] = y;
-      }
-    // the lanes with the same tokens are 4, 8 and 16 apart
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int m = 4; m <= 16; m *= 2) sum[s] += __shfl_xor_sync(kFullMask, sum[s], m);
-    if (lane < 4) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int tt = t + 8 * (s / 2) + s % 2;
-        if (tt < len) a.dots[(bh * a.seqlen + tt) * 4 + quad] = sum[s];
+          if (v + 8 * u < a.dv) {
+            const float y = o[u / 2][4 * i + 2 * (u % 2) + z];
+            if (sizeof(T) == 4 || a.out_f32) static_cast<float*>(a.out)[row + 8 * u] = y;
+            else static_cast<__nv_bfloat16*>(a.out)[row + 8 * u] = __float2bfloat16_rn(y);
+          }
       }
     }
-  }
+}
+
+// The same values' products with the rows of x, element by element.
+template <typename T>
+__device__ __forceinline__ void la_dots(float (&sum)[4], const LaPassArgs& a, const float (&o)[2][8], int64_t b, int h,
+                                        int t0, int len, int v0, int lane) {
+  const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
+  const char* from = la_row(a.x, b, t, h, sizeof(T)) + (int64_t)v * sizeof(T);
+  const int64_t xs = a.x.st * (int64_t)sizeof(T);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      float y = 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (t + 8 * i + z < len && v + 8 * u < a.dv)
+          y = fmaf(o[u / 2][4 * i + 2 * (u % 2) + z], to_f32(reinterpret_cast<const T*>(from + (8 * i + z) * xs)[8 * u]), y);
+      sum[2 * i + z] = y;
+    }
 }
 
 // The products of planes pa < PA of one operand and pb < PB of the other whose
-// weight counts, the smaller ones first: they add up while the sum is small.  STEPS
-// MMAs each, given the planes' places (in descriptor units: blocks of a plane, or
-// `a_cols` columns).  The loop over planes stays one: the roles together have to fit
-// the instruction cache.
+// weight counts, the smaller ones first: they add up while the sum is small.  STEPS MMAs
+// each, told the planes, the step and whether they add.
 template <int PA, int PB, int STEPS, typename F>
-__device__ __forceinline__ void la_products(int a_blocks, int b_blocks, F&& mma, int a_cols = 0) {
+__device__ __forceinline__ void la_products(F&& mma) {
   constexpr int P = PA > PB ? PA : PB;
-  bool add = false;
-#pragma unroll 1
-  for (int pa = PA - 1; pa >= 0; --pa)
-#pragma unroll 1
-    for (int pb = (P - pa < PB ? P - pa : PB) - 1; pb >= 0; --pb) {
-      const int at_a = pa * (a_blocks * (kLaBlock >> 4) + a_cols), at_b = pb * b_blocks * (kLaBlock >> 4);
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) mma(at_a, at_b, i, add || i > 0);
-      add = true;
-    }
+  for (int pa = PA - 1; pa >= 0; --pa)
+#pragma unroll
+    for (int pb = (P - pa < PB ? P - pa : PB) - 1; pb >= 0; --pb)
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+        mma(pa, pb, i, !(pa == PA - 1 && pb == (P - pa < PB ? P - pa : PB) - 1 && i == 0));
 }
 
 // What one CTA works through: pieces of heads, in the order of processing.
@@ -442,41 +441,56 @@ __device__ __forceinline__ LaPiece la_piece(const LaPassArgs& a, const LaWork& w
   return p;
 }
 
-// STATES: only the states (the sequence's segments, each from zero, all at once).
-template <typename T, int KD, int VD, bool STATES>
+// What a launch does: outputs and states; the states alone (the sequence's segments, each
+// from zero, all at once); outputs and states with the products that a decay's gradient
+// is made of (of each output row with x, of states at anchors).
+enum LaMode { kLaOutputs, kLaStates, kLaProducts };
+
+template <typename T, int KD, int VD, LaMode MODE>
 __global__ void __launch_bounds__(LaCfg<T, KD, VD>::kThreads, 1)
 linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant__ LaMaps maps) {
   using CF = LaCfg<T, KD, VD>;
   constexpr int NPI = CF::NPI, NPX = CF::NPX, NPW = CF::NPW;
+  constexpr bool STATES = MODE == kLaStates, DOTS = MODE == kLaProducts;
   extern __shared__ __align__(1024) char smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + CF::kBars);
-  // a ring's barriers: CF::kRing slots each, whatever its length
-  uint64_t *full_k = bars, *empty_k = full_k + CF::kRing, *full_v = empty_k + CF::kRing, *empty_v = full_v + CF::kRing,
-           *full_q = empty_v + CF::kRing, *empty_q = full_q + CF::kRing, *full_f = empty_q + CF::kRing,
-           *empty_f = full_f + CF::kRing, *single = empty_f + CF::kRing;
-  uint64_t *b_qk = single + 6;    // scores are there, one for each place
-  uint64_t *b_pk = single + 1;    // P and the weighted keys are there
-  uint64_t *b_ds = single + 2;    // increment and P V are there
-  uint64_t *b_o = single + 3;     // S Q too: the chunk's products are done
-  uint64_t *b_free = single + 4;  // the back warps have read them
-  uint64_t *b_s = single + 5;     // the state's planes are there
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(single + 8);
+  // barriers: CF::kRing places for each ring, whatever its length
+  const uint32_t base = smem_u32(smem), bars = base + CF::kBars;
+  const auto ring_bar = [&](int which, int i) { return bars + (uint32_t)(which * CF::kRing + i) * 8; };
+  const auto full_k = [&](int i) { return ring_bar(0, i); };
+  const auto empty_k = [&](int i) { return ring_bar(1, i); };
+  const auto full_v = [&](int i) { return ring_bar(2, i); };
+  const auto empty_v = [&](int i) { return ring_bar(3, i); };
+  const auto full_q = [&](int i) { return ring_bar(4, i); };
+  const auto empty_q = [&](int i) { return ring_bar(5, i); };
+  const auto full_f = [&](int i) { return ring_bar(6, i); };
+  const auto empty_f = [&](int i) { return ring_bar(7, i); };
+  const auto b_qk = [&](int i) { return ring_bar(8, i); };  // scores are there, one for each place
+  const uint32_t b_pk = ring_bar(8, 2);    // P and the weighted keys are there
+  const uint32_t b_ds = ring_bar(8, 3);    // increment and P V are there
+  const uint32_t b_o = ring_bar(9, 0);     // S Q too: the chunk's products are done
+  const uint32_t b_free = ring_bar(9, 1);  // the back warps have read them
+  const uint32_t b_s = ring_bar(9, 2);     // the state's planes are there
+  const uint32_t b_end = ring_bar(9, 3);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + 10 * CF::kRing * 8);
   int* worker_at = reinterpret_cast<int*>(tmem_at + 1);
   volatile int* dead = worker_at + 1;
 
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  // one value for a warp, known as such: what follows from it stays off the vector registers
+  const auto same = [](uint32_t x) { return __shfl_sync(kFullMask, x, 0); };
+  const int tid = threadIdx.x, warp = (int)same(tid / 32), lane = tid % 32;
   if (tid == 0) {
-    for (int i = 0; i < CF::RK; ++i) mbar_init(&full_k[i], 1), mbar_init(&empty_k[i], 1);
-    for (int i = 0; i < CF::RV; ++i) mbar_init(&full_v[i], 1), mbar_init(&empty_v[i], 1);
-    for (int i = 0; i < CF::RQ; ++i) mbar_init(&full_q[i], 1), mbar_init(&empty_q[i], 1);
-    for (int i = 0; i < CF::RF; ++i) mbar_init(&full_f[i], 1), mbar_init(&empty_f[i], kLaFrontWarps + CF::kHolders);
-    for (int i = 0; i < 2; ++i) mbar_init(&b_qk[i], 1);
-    mbar_init(single, 1);
-    mbar_init(b_pk, kLaFrontWarps);
-    mbar_init(b_ds, 1);
-    mbar_init(b_o, 1);
-    mbar_init(b_free, CF::kHolders);
-    mbar_init(b_s, CF::kHolders);
+    for (int i = 0; i < CF::kRing; ++i) {
+      for (int w = 0; w < 7; ++w) la_init(ring_bar(w, i), 1);
+      la_init(empty_f(i), kLaFrontWarps + CF::kHolders);
+    }
+    la_init(b_qk(0), 1);
+    la_init(b_qk(1), 1);
+    la_init(b_pk, kLaFrontWarps);
+    la_init(b_ds, 1);
+    la_init(b_o, 1);
+    la_init(b_free, CF::kHolders);
+    la_init(b_s, CF::kHolders);
+    la_init(b_end, 1);
     fence_mbar_init();
     *dead = 0;
     // workers are numbered in the order in which they start, so that the one a
@@ -487,137 +501,143 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   tc5_fence_before();
   __syncthreads();
   tc5_fence_after();
-  const uint32_t tmem = *tmem_at;
-  const LaWork work = la_work(a, *worker_at);
-  auto arrive = [&](uint64_t* bar) {
+  const uint32_t tmem = same(*tmem_at);
+  const LaWork work = la_work(a, (int)same(*worker_at));
+  auto arrive = [&](uint32_t bar) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
+    if (lane == 0) la_arrive(bar);
   };
 
   if (warp >= kLaMmaWarp) {
     regs_give<kLaAuxRegs>();
     if (warp == kLaMmaWarp) {
       // ---- MMA issue, by one thread of the warp
-      const uint32_t base = smem_u32(smem);
+      constexpr int kUnits = kLaBlock >> 4;  // a block in descriptor units
       const bool leader = elect_one();
-      auto scores = [&](int n) {
-        la_wait(&full_k[n % CF::RK], (uint32_t)((n / CF::RK) & 1), dead);
-        la_wait(&full_q[n % CF::RQ], (uint32_t)((n / CF::RQ) & 1), dead);
-        tc5_fence_after();
-        if (leader) {
-          const uint64_t q = tile_desc(base + CF::kQ + (n % CF::RQ) * CF::kTileK, 0);
-          const uint64_t k = tile_desc(base + CF::kK + (n % CF::RK) * CF::kTileK, 0);
-          la_products<NPI, NPI, KD / 16>(CF::KB, CF::KB, [&](int pa, int pb, int i, bool add) {
-            const int off = (i / 4) * (kLaBlock >> 4) + (i % 4) * 2;
-            mma_ss(tmem + CF::cQK + (n % CF::kAhead) * 64, q + pa + off, k + pb + off, mma_idesc(64, 64, false, false), add);
-          });
-          mma_commit(&b_qk[n % CF::kAhead]);
-        }
-        __syncwarp();
-      };
+      LaRing<CF::RK> rk, sk;  // of the chunk at hand, and of the one whose scores come next
+      LaRing<CF::RQ> rq, sq;
+      LaRing<CF::RV> rv;
       int total = 0, scored = 0;
       for (int i = 0; i < work.pieces; ++i) {
         const LaPiece p = la_piece(a, work, i);
         total += p.last - p.first;
       }
-      if (!STATES)
-        while (scored < CF::kAhead && scored < total) scores(scored++);
-      for (int n = 0; n < total; ++n) {
-        const uint64_t v = tile_desc(base + CF::kV + (n % CF::RV) * CF::kTileV, kLaBlock);
-        // planes of the weighted keys: in the key tile's place, then in a ring of their own
-        const uint64_t w0 = tile_desc(base + CF::kK + (n % CF::RK) * CF::kTileK, kLaBlock);
-        const uint64_t w1 = tile_desc(base + CF::kW + (n % CF::RW) * CF::kTileW, kLaBlock) -
-                            (uint64_t)(NPI * CF::KB * (kLaBlock >> 4));
-        la_wait(b_pk, (uint32_t)(n & 1), dead);
+      auto scores = [&]() {
+        la_wait(full_k(sk.i), sk.full(), dead);
+        la_wait(full_q(sq.i), sq.full(), dead);
         tc5_fence_after();
-        la_wait(&full_v[n % CF::RV], (uint32_t)((n / CF::RV) & 1), dead);
-        if (n > 0) la_wait(b_free, (uint32_t)((n - 1) & 1), dead);
+        const int place = scored % CF::kAhead;
+        if (leader) {
+          const uint32_t q = tile_desc(base + CF::kQ + sq.i * CF::kTileK, 0);
+          const uint32_t k = tile_desc(base + CF::kK + sk.i * CF::kTileK, 0);
+          la_products<NPI, NPI, KD / 16>([&](int pa, int pb, int i, bool add) {
+            const int off = (i / 4) * kUnits + (i % 4) * 2;
+            mma_ss(tmem + CF::cQK + place * 64, q + pa * CF::KB * kUnits + off, k + pb * CF::KB * kUnits + off,
+                   mma_idesc(64, 64, false, false), add);
+          });
+          mma_commit(b_qk(place));
+        }
+        __syncwarp();
+        sk.next(), sq.next(), ++scored;
+      };
+      if (!STATES)
+        while (scored < CF::kAhead && scored < total) scores();
+      for (int n = 0; n < total; ++n) {
+        const uint32_t v = tile_desc(base + CF::kV + rv.i * CF::kTileV, kLaBlock);
+        // planes of the weighted keys: in the key tile's place, then in one of their own
+        const uint32_t w0 = tile_desc(base + CF::kK + rk.i * CF::kTileK, kLaBlock);
+        const uint32_t w1 = tile_desc(base + CF::kW, kLaBlock);
+        la_wait(b_pk, n & 1, dead);
+        la_wait(full_v(rv.i), rv.full(), dead);
+        if (n > 0) la_wait(b_free, (n - 1) & 1, dead);
         tc5_fence_after();
         if (leader) {
           // dS^T = V^T (w . K)
-          la_products<NPI, NPW, kLaChunk / 16>(CF::VB, CF::KB, [&](int pa, int pb, int i, bool add) {
+          la_products<NPI, NPW, kLaChunk / 16>([&](int pa, int pb, int i, bool add) {
             const int off = i * (16 * kTileRow >> 4);
-            mma_ss(tmem + CF::cDS, v + pa + off, (pb < NPI * CF::KB * (kLaBlock >> 4) ? w0 : w1) + pb + off,
-                   mma_idesc(128, KD, true, true), add);
+            const uint32_t w = pb < NPI ? w0 + pb * CF::KB * kUnits : w1 + (pb - NPI) * CF::KB * kUnits;
+            mma_ss(tmem + CF::cDS, v + pa * CF::VB * kUnits + off, w + off, mma_idesc(128, KD, true, true), add);
           });
           if (!STATES) {
             // O1^T = V^T P^T
-            const uint64_t pd = tile_desc(base + CF::kP, 0);
-            la_products<NPI, NPX, kLaChunk / 16>(CF::VB, 1, [&](int pa, int pb, int i, bool add) {
-              mma_ss(tmem + CF::cO1, v + pa + i * (16 * kTileRow >> 4), pd + pb + i * 2, mma_idesc(128, 64, true, false), add);
+            const uint32_t pd = tile_desc(base + CF::kP, 0);
+            la_products<NPI, NPX, kLaChunk / 16>([&](int pa, int pb, int i, bool add) {
+              mma_ss(tmem + CF::cO1, v + pa * CF::VB * kUnits + i * (16 * kTileRow >> 4), pd + pb * kUnits + i * 2,
+                     mma_idesc(128, 64, true, false), add);
             });
           }
           mma_commit(b_ds);
-          mma_commit(&empty_v[n % CF::RV]);
-          mma_commit(&empty_k[n % CF::RK]);
+          mma_commit(empty_v(rv.i));
+          mma_commit(empty_k(rk.i));
         }
         __syncwarp();
         if (!STATES) {
           // O2^T = S^T Q^T
-          la_wait(b_s, (uint32_t)(n & 1), dead);
+          la_wait(b_s, n & 1, dead);
           tc5_fence_after();
           if (leader) {
-            const uint64_t q = tile_desc(base + CF::kQ + (n % CF::RQ) * CF::kTileK, 0);
-            la_products<NPX, NPI, KD / 16>(0, CF::KB, [&](int pa, int pb, int i, bool add) {
-              mma_ts(tmem + CF::cO2, tmem + CF::cSP + pa + i * 8, q + pb + (i / 4) * (kLaBlock >> 4) + (i % 4) * 2,
-                     mma_idesc(128, 64, false, false), add);
-            }, KD / 2);
+            const uint32_t q = tile_desc(base + CF::kQ + rq.i * CF::kTileK, 0);
+            la_products<NPX, NPI, KD / 16>([&](int pa, int pb, int i, bool add) {
+              mma_ts(tmem + CF::cO2, tmem + CF::cSP + pa * (KD / 2) + i * 8,
+                     q + (pb * CF::KB + i / 4) * kUnits + (i % 4) * 2, mma_idesc(128, 64, false, false), add);
+            });
             mma_commit(b_o);
-            mma_commit(&empty_q[n % CF::RQ]);
+            mma_commit(empty_q(rq.i));
           }
           __syncwarp();
           // last, so that no tile is waited for while the chunk's own products could run
-          if (scored < total) scores(scored++);
+          if (scored < total) scores();
         }
+        rk.next(), rq.next(), rv.next();
       }
     } else if (warp == kLaDecayWarp) {
       // ---- decays
-      int n = 0;
+      LaRing<CF::RF> rf;
       for (int i = 0; i < work.pieces; ++i) {
         const LaPiece p = la_piece(a, work, i);
         double sum = 0.0;
         auto place = [&](int c) { return (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk; };
         T next[2];
         if (p.first < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(p.first), p.len, lane);
-        for (int c = p.first; c < p.last; ++c, ++n) {
-          const int s = (int)(n % CF::RF);
+        for (int c = p.first; c < p.last; ++c) {
           const float x0 = to_f32(next[0]), x1 = to_f32(next[1]);
           if (c + 1 < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(c + 1), p.len, lane);
-          if (n >= CF::RF) la_wait(&empty_f[s], (uint32_t)((n / CF::RF - 1) & 1), dead);
-          const int64_t whole = la_decays(reinterpret_cast<float*>(smem + CF::kFac) + s * CF::kFacFloats, x0, x1,
-                                          a.reverse, a.scale_o, a.scale_w, lane);
+          if (rf.used()) la_wait(empty_f(rf.i), rf.empty(), dead);
+          const int64_t whole = la_decays<CF::kBf16>(reinterpret_cast<float*>(smem + CF::kFac) + rf.i * CF::kFacFloats, x0,
+                                                     x1, a.reverse, a.scale_o, a.scale_w, lane);
           if (STATES) sum += (double)whole * 0x1p-32;
-          arrive(&full_f[s]);
+          arrive(full_f(rf.i));
+          rf.next();
         }
         if (STATES && lane == 0) a.seg_decay[(int64_t)p.bh * (a.nseg + 1) + work.worker % a.nseg] = sum;
       }
     } else {
       // ---- loaders: one thread by TMA, or all of them
       const int ltid = tid - 32 * kLaLoadWarp;
-      int n = 0;
+      LaRing<CF::RK> rk;
+      LaRing<CF::RQ> rq;
+      LaRing<CF::RV> rv;
       for (int i = 0; i < work.pieces; ++i) {
         const LaPiece p = la_piece(a, work, i);
-        for (int c = p.first; c < p.last; ++c, ++n) {
+        const int hk = p.h / a.k.share, hq = p.h / a.q.share, hv = p.h / a.v.share;
+        for (int c = p.first; c < p.last; ++c) {
           const int t0 = (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk;
           // TMA clips at the tensor's end, not at a row's length
           const bool by_tma = CF::kBf16 && a.tma && (t0 + kLaChunk <= p.len || p.len == a.seqlen);
-          auto tile = [&](auto width, const LaTensor& x, const CUtensorMap* map, int ring, int at, int bytes,
-                          uint64_t* full, uint64_t* empty, int d) {
+          auto tile = [&](auto width, const LaTensor& x, const CUtensorMap* map, int hx, int at, bool wait, uint32_t turn,
+                          uint32_t full, uint32_t empty, int d) {
             constexpr int DP = decltype(width)::value;
-            const int s = n % ring;
-            char* to = smem + at + s * bytes;
-            if (ltid == 0 && n >= ring) la_wait(&empty[s], (uint32_t)((n / ring - 1) & 1), dead);
+            if (ltid == 0 && wait) la_wait(empty, turn, dead);
             if (by_tma) {
               if (ltid == 0) {
-                mbar_arrive_expect_tx(&full[s], DP / 64 * kLaBlock);
-#pragma unroll 1
-                for (int j = 0; j < DP / 64; ++j)
-                  tma_load_block(to + j * kLaBlock, map, &full[s], j * 64, t0, p.h / x.share, p.b);
+                la_expect(full, DP / 64 * kLaBlock);
+#pragma unroll
+                for (int j = 0; j < DP / 64; ++j) tma_load_block(base + at + j * kLaBlock, map, full, j * 64, t0, hx, p.b);
               }
             } else {
               __syncwarp();
               asm volatile("bar.sync 2, 64;\n" ::: "memory");
-              la_load_tile<T, DP>(to, x, p.b, p.h, t0, p.len, d, a.vec, ltid, CF::kLoaders);
+              la_load_tile<T, DP>(smem + at, x, p.b, p.h, t0, p.len, d, a.vec, ltid, CF::kLoaders);
               if (CF::kBf16 && a.vec) {
                 cp_async_commit();
                 cp_async_wait_all();
@@ -625,12 +645,17 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
               fence_proxy_async_smem();
               __syncwarp();
               asm volatile("bar.sync 2, 64;\n" ::: "memory");
-              if (ltid == 0) mbar_arrive(&full[s]);
+              if (ltid == 0) la_arrive(full);
             }
           };
-          tile(LaWidth<KD>{}, a.k, &maps.k, CF::RK, CF::kK, CF::kTileK, full_k, empty_k, a.dk);
-          if (!STATES) tile(LaWidth<KD>{}, a.q, &maps.q, CF::RQ, CF::kQ, CF::kTileK, full_q, empty_q, a.dk);
-          tile(LaWidth<VD>{}, a.v, &maps.v, CF::RV, CF::kV, CF::kTileV, full_v, empty_v, a.dv);
+          tile(LaWidth<KD>{}, a.k, &maps.k, hk, CF::kK + rk.i * CF::kTileK, rk.used(), rk.empty(), full_k(rk.i),
+               empty_k(rk.i), a.dk);
+          if (!STATES)
+            tile(LaWidth<KD>{}, a.q, &maps.q, hq, CF::kQ + rq.i * CF::kTileK, rq.used(), rq.empty(), full_q(rq.i),
+                 empty_q(rq.i), a.dk);
+          tile(LaWidth<VD>{}, a.v, &maps.v, hv, CF::kV + rv.i * CF::kTileV, rv.used(), rv.empty(), full_v(rv.i),
+               empty_v(rv.i), a.dv);
+          rk.next(), rq.next(), rv.next();
         }
       }
     }
@@ -655,49 +680,59 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         reinterpret_cast<uint4*>(smem + CF::kP)[i] = make_uint4(0, 0, 0, 0);
       asm volatile("bar.sync 1, 256;\n" ::: "memory");
     }
+    LaRing<CF::RF> rf;
+    LaRing<CF::RK> rk;
     for (int i = 0; i < work.pieces; ++i) {
       const LaPiece p = la_piece(a, work, i);
       for (int c = p.first; c < p.last; ++c, ++n) {
-        const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + (int)(n % CF::RF) * CF::kFacFloats;
-        la_wait(&full_f[n % CF::RF], (uint32_t)((n / CF::RF) & 1), dead);
-        la_wait(&full_k[n % CF::RK], (uint32_t)((n / CF::RK) & 1), dead);
-        if (!STATES) la_wait(&b_qk[n % CF::kAhead], (uint32_t)((n / CF::kAhead) & 1), dead);  // the keys as they are were used
-        {
-          // the keys weighted by their decay to the chunk's end (reversed: start)
-          char* k = smem + CF::kK + (n % CF::RK) * CF::kTileK;
-          char* w = smem + CF::kW + (n % CF::RW) * CF::kTileW;
+        const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + rf.i * CF::kFacFloats;
+        char* k = smem + CF::kK + rk.i * CF::kTileK;
+        la_wait(full_f(rf.i), rf.full(), dead);
+        la_wait(full_k(rk.i), rk.full(), dead);
+        // the keys as they are were used, and what was made here for the last chunk too
+        if (!STATES) la_wait(b_qk(n % CF::kAhead), (n / CF::kAhead) & 1, dead);
+        if (n > 0) la_wait(b_ds, (n - 1) & 1, dead);
+        // the keys weighted by their decay to the chunk's end (reversed: start)
 #pragma unroll 2
-          for (int u = w_from * 32 + lane; u < w_to * 32; u += 32) {
-            const int row = (u % 512) / 8;
-            const float wj = fac[3 * kLaChunk + row];
-            const uint64_t ww = pair(wj, wj);
-            const int off = (u / 512) * kLaBlock + row * kTileRow + (u % 8) * 16;
-            uint32_t in[NPI][4];
+        for (int u = w_from * 32 + lane; u < w_to * 32; u += 32) {
+          const int row = (u % 512) / 8;
+          const int off = (u / 512) * kLaBlock + row * kTileRow + (u % 8) * 16;
+          uint32_t in[NPI][4], out[NPW][4];
 #pragma unroll
-            for (int q = 0; q < NPI; ++q) {
-              const uint4 y = *reinterpret_cast<const uint4*>(k + q * CF::KB * kLaBlock + off);
-              in[q][0] = y.x, in[q][1] = y.y, in[q][2] = y.z, in[q][3] = y.w;
+          for (int q = 0; q < NPI; ++q) {
+            const uint4 y = *reinterpret_cast<const uint4*>(k + q * CF::KB * kLaBlock + off);
+            in[q][0] = y.x, in[q][1] = y.y, in[q][2] = y.z, in[q][3] = y.w;
+          }
+          if constexpr (CF::kBf16) {
+            // k (w0 + w1 + w2): a product of two bf16 is a bf16 and the bf16 that is left,
+            // exactly, so four planes hold 24 bits without leaving bf16 arithmetic
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(fac) + 3 * kLaChunk + row;
+            const uint32_t w0 = w[0], w1 = w[kLaChunk], w2 = w[2 * kLaChunk];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              out[0][e] = mul_bf16x2(in[0][e], w0);
+              out[1][e] = fma_bf16x2(in[0][e], w0, neg_bf16x2(out[0][e]));
+              out[2][e] = mul_bf16x2(in[0][e], w1);
+              out[3][e] = fma_bf16x2(in[0][e], w2, fma_bf16x2(in[0][e], w1, neg_bf16x2(out[2][e])));
             }
-            uint32_t out[NPW][4];
+          } else {
+            const float wj = fac[3 * kLaChunk + row];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint64_t y = from_bf16x2(in[NPI - 1][e]);
 #pragma unroll
               for (int q = NPI - 2; q >= 0; --q) y = add2(y, from_bf16x2(in[q][e]));  // exact from the smallest
               uint32_t sp[NPW];
-              split2<NPW>(mul2(y, ww), sp);
+              split2<NPW>(mul2(y, pair(wj, wj)), sp);
 #pragma unroll
               for (int q = 0; q < NPW; ++q) out[q][e] = sp[q];
             }
-#pragma unroll
-            for (int q = 0; q < NPW; ++q)
-              *reinterpret_cast<uint4*>((q < NPI ? k + q * CF::KB * kLaBlock : w + (q - NPI) * CF::KB * kLaBlock) + off) =
-                  make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
           }
+#pragma unroll
+          for (int q = 0; q < NPW; ++q)
+            *reinterpret_cast<uint4*>((q < NPI ? k + q * CF::KB * kLaBlock : smem + CF::kW + (q - NPI) * CF::KB * kLaBlock) +
+                                      off) = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
         }
-        // the last chunk's products are done: P may be overwritten, and what is made here
-        // is never two chunks ahead
-        if (n > 0) la_wait(b_ds, (uint32_t)((n - 1) & 1), dead);
         if (!STATES) {
           // P = (Q K^T) . D: 16 rows a warp, two rows a thread
           tc5_fence_after();
@@ -749,7 +784,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         }
         fence_proxy_async_smem();
         arrive(b_pk);
-        arrive(&empty_f[n % CF::RF]);
+        arrive(empty_f(rf.i));
+        rf.next(), rk.next();
       }
     }
   } else {
@@ -777,6 +813,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         }
         tmem_wait_st();
       };
+      LaRing<CF::RF> rf;
       int n = 0;
       for (int i = 0; i < work.pieces; ++i) {
         const LaPiece p = la_piece(a, work, i);
@@ -784,6 +821,14 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         const int b = p.b, h = p.h, len = p.len;
         const int all_chunks = (len + kLaChunk - 1) / kLaChunk;
         const int step = a.workers > 0 ? 0 : work.worker % a.nseg;
+        // 16-byte rows: this lane's part of token lane / 4, in memory and in the stage
+        const int tok = lane / 4, c8 = quad * 32 + (lane % 4) * 8;
+        char* stage = smem + CF::kStage + warp * 512;
+        char* mine = stage + tok * 64 + (((lane % 4) ^ ((tok >> 1) & 3)) << 4);
+        const uint32_t blocks = smem_u32(stage) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+        const int rs = a.heads * a.dv * 2;
+        const bool fast = CF::kBf16 && a.out_vec, fast_x = DOTS && CF::kBf16 && a.x_vec;
+        char* out = static_cast<char*>(a.out) + ((int64_t)b * a.seqlen + tok) * rs + (h * a.dv + c8) * 2;
         if (p.from_carry) {
           const unsigned* flag = a.flags + 1 + (work.worker - 1) * 16 + warp;
           if (lane == 0) {
@@ -823,9 +868,19 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         if (!STATES && p.first < p.last) give_state();
         for (int cc = p.first; cc < p.last; ++cc, ++n) {
           const int chunk = a.reverse ? p.last - 1 - (cc - p.first) : cc, t0 = chunk * kLaChunk;
-          const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + (int)(n % CF::RF) * CF::kFacFloats;
-          const bool anchor_here = a.dump && ((chunk + 1) % a.anchor_chunks == 0 || chunk == all_chunks - 1);
-          if (!STATES && a.reverse && anchor_here) {
+          const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + rf.i * CF::kFacFloats;
+          const int tw = t0 + part * 16;  // this warp's tokens
+          uint4 xrow[2];
+          if (fast_x) {
+            const char* xp = la_row(a.x, b, tw + tok, h, 2) + c8 * 2;
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+              xrow[i2] = make_uint4(0, 0, 0, 0);
+              if (tw + i2 * 8 + tok < len && c8 < a.dv) xrow[i2] = *reinterpret_cast<const uint4*>(xp + i2 * 16 * a.x.st);
+            }
+          }
+          const bool anchor_here = DOTS && ((chunk + 1) % a.anchor_chunks == 0 || chunk == all_chunks - 1);
+          if (DOTS && a.reverse && anchor_here) {
             // <R, S> behind this chunk: R is the state here, S the forward pass's
             float sum = 0.f;
             const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
@@ -839,24 +894,22 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
             if (lane == 0) a.anchor[an * 16 + warp] = sum;
           }
-          la_wait(&full_f[n % CF::RF], (uint32_t)((n / CF::RF) & 1), dead);
-          const float decay = fac[4 * kLaChunk];
-          la_wait(STATES ? b_ds : b_o, (uint32_t)(n & 1), dead);
+          la_wait(full_f(rf.i), rf.full(), dead);
+          const float decay = fac[CF::kFacFloats - 4];
+          la_wait(STATES ? b_ds : b_o, n & 1, dead);
           tc5_fence_after();
           float o[2][8];
-          uint32_t x[KH];
           if (!STATES) {
+            float2 f[2];
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2)
+              f[i2] = *reinterpret_cast<const float2*>(fac + 2 * kLaChunk + part * 16 + i2 * 8 + 2 * (lane % 4));
             uint32_t x1[2][8], x2[2][8];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               tmem_ld_rows16(x1[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO1 + part * 16);
               tmem_ld_rows16(x2[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO2 + part * 16);
             }
-            tmem_ld(x, lanes + CF::cDS + part * KH);
-            float2 f[2];
-#pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2)
-              f[i2] = *reinterpret_cast<const float2*>(fac + 2 * kLaChunk + part * 16 + i2 * 8 + 2 * (lane % 4));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               tmem_wait_ld(x1[e]);
@@ -865,20 +918,72 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
               for (int i2 = 0; i2 < 8; ++i2)
                 o[e][i2] = fmaf(__uint_as_float(x2[e][i2]), i2 % 2 ? f[i2 / 4].y : f[i2 / 4].x, __uint_as_float(x1[e][i2]));
             }
-          } else {
-            tmem_ld(x, lanes + CF::cDS + part * KH);
           }
           const uint64_t decay2 = pair(decay, decay);
-          tmem_wait_ld(x);
+          // 16 key indices at a time: the state, the outputs and more would not fit the registers
 #pragma unroll
-          for (int e = 0; e < KH / 2; ++e) S[e] = fma2(S[e], decay2, pair(x[2 * e], x[2 * e + 1]));
+          for (int c = 0; c < KH; c += 16) {
+            uint32_t x[16];
+            tmem_ld(x, lanes + CF::cDS + part * KH + c);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) S[c / 2 + e] = fma2(S[c / 2 + e], decay2, pair(x[2 * e], x[2 * e + 1]));
+          }
           tc5_fence_before();
           arrive(b_free);
-          arrive(&empty_f[n % CF::RF]);
+          arrive(empty_f(rf.i));
+          rf.next();
           if (!STATES && cc + 1 < p.last) give_state();
-          if (!STATES)
-            la_emit<T>(a, o, smem + CF::kStage + warp * 512, b, bh, h, t0 + part * 16, len, quad * 32, quad, lane);
-          if (!STATES && !a.reverse && anchor_here) {
+          if (!STATES && CF::kBf16 && fast) {
+            // bf16 rows leave through 512 bytes of shared memory, 8 tokens at a time, as 64
+            // bytes of a token together
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+              store_blocks_t(blocks, to_bf16x2(o[0][4 * i2], o[0][4 * i2 + 1]), to_bf16x2(o[0][4 * i2 + 2], o[0][4 * i2 + 3]),
+                             to_bf16x2(o[1][4 * i2], o[1][4 * i2 + 1]), to_bf16x2(o[1][4 * i2 + 2], o[1][4 * i2 + 3]));
+              __syncwarp();
+              const uint4 y = *reinterpret_cast<const uint4*>(mine);
+              const int t = tw + i2 * 8;
+              if (c8 < a.dv && t + tok < len && in_range(t + tok, a.seqlen)) *reinterpret_cast<uint4*>(out + (int64_t)t * rs) = y;
+              __syncwarp();
+            }
+          } else if (!STATES) {
+            la_emit<T>(a, o, b, h, tw, len, quad * 32, lane);
+          }
+          if (DOTS) {
+            float sum[4];
+            if (fast_x) {
+              // the rows of x the other way through the stage, into the order of o
+#pragma unroll
+              for (int i2 = 0; i2 < 2; ++i2) {
+                *reinterpret_cast<uint4*>(mine) = xrow[i2];
+                __syncwarp();
+                uint32_t x4[4];
+                load_blocks_t(blocks, x4);
+                __syncwarp();
+                uint64_t y = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  y = fma2(pair(o[u / 2][4 * i2 + 2 * (u % 2)], o[u / 2][4 * i2 + 2 * (u % 2) + 1]), from_bf16x2(x4[u]), y);
+                sum[2 * i2] = pair_lo(y), sum[2 * i2 + 1] = pair_hi(y);
+              }
+            } else {
+              la_dots<T>(sum, a, o, b, h, tw, len, quad * 32, lane);
+            }
+            // the lanes with the same tokens are 4, 8 and 16 apart
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int m = 4; m <= 16; m *= 2) sum[e] += __shfl_xor_sync(kFullMask, sum[e], m);
+            if (lane < 4) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int t = tw + 2 * lane + 8 * (e / 2) + e % 2;
+                if (t < len) a.dots[(bh * a.seqlen + t) * 4 + quad] = sum[e];
+              }
+            }
+          }
+          if (DOTS && !a.reverse && anchor_here) {
             const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
             float* to = a.dump + (an * 16 + warp) * (KH * 32);
 #pragma unroll
@@ -916,8 +1021,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   if (warp == kLaMmaWarp) {
     if (*dead) {
       if (lane == 0) {
-        mma_commit(single);  // not used otherwise
-        for (int i = 0; i < 4096 && !mbar_try_wait(single, 0); ++i) {}
+        mma_commit(b_end);
+        la_wait(b_end, 0, dead);
       }
       __syncwarp();
     }

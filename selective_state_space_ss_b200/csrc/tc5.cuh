@@ -22,12 +22,11 @@ __device__ __forceinline__ uint32_t tile_unit(uint32_t row, uint32_t unit) {
   return row * kTileRow + ((unit ^ (row & 7u)) << 4);
 }
 
-// Shared-memory descriptor, 128-byte swizzle: `sbo` bytes between 8-row groups;
-// `lbo` bytes between blocks of 64 columns (read for MN-major operands only).
-__device__ __forceinline__ uint64_t tile_desc(uint32_t smem_addr, uint32_t lbo) {
-  return (uint64_t)((smem_addr >> 4) & 0x3fffu) | ((uint64_t)(lbo >> 4) << 16) |
-         ((uint64_t)(kTileGroup >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory descriptor, 128-byte swizzle: the low word has the address and, for
+// MN-major operands, the bytes between blocks of 64 columns (both in 16 bytes); the high
+// word the bytes between 8-row groups, the version and the swizzle, always the same.
+__device__ __forceinline__ uint32_t tile_desc(uint32_t smem_addr, uint32_t lbo) { return (smem_addr >> 4) | (lbo >> 4) << 16; }
+constexpr uint32_t kTileDescHigh = (kTileGroup >> 4) | (1u << 14) | (2u << 29);
 
 // Instruction descriptor of a bf16 x bf16 -> fp32 MMA.
 __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool a_mn_major, bool b_mn_major) {
@@ -36,27 +35,25 @@ __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool a_mn_major, 
 }
 
 // D[tmem] (+)= A[shared] B[shared]; issued by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
-      "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"((uint32_t)add), "n"(kTileDescHigh)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[shared]: A's row is the lane, two summed values per 32-bit column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b),
-      "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"((uint32_t)add), "n"(kTileDescHigh)
       : "memory");
 }
 
 // One arrival on `bar` when every MMA that this thread issued before is done.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(
-                   smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
 // Tensor memory, by a whole warp: `cols` a power of two from 32.
@@ -177,6 +174,19 @@ __device__ __forceinline__ uint32_t to_bf16x2(float a, float b) {
 // Two bf16 as floats.
 __device__ __forceinline__ uint64_t from_bf16x2(uint32_t h) { return pair(h << 16, h & 0xffff0000u); }
 
+// Arithmetic on two bf16 at once, each result rounded once.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t neg_bf16x2(uint32_t a) { return a ^ 0x80008000u; }
+
 // Two floats as bf16 planes: plane 0 the nearest bf16, each further plane the
 // nearest bf16 of what is left, so that p planes hold 8 p bits of the value.
 // Packed as the MMA wants them: the first value in the low half.
@@ -195,6 +205,15 @@ __device__ __forceinline__ void split2(uint64_t x, uint32_t (&out)[PLANES]) {
 __device__ __forceinline__ void store_blocks(uint32_t row_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(row_addr), "r"(a), "r"(b),
                "r"(c), "r"(d)
+               : "memory");
+}
+
+// Four 8 x 8 blocks from shared memory, each transposed: a thread gets two neighbours
+// of column lane / 4 of each.
+__device__ __forceinline__ void load_blocks_t(uint32_t row_addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(row_addr)
                : "memory");
 }
 
@@ -219,30 +238,13 @@ template <int N>
 __device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 
 // One 64 x 64 block of a [batch, seqlen, heads, d] tensor by TMA (no multicast).
-__device__ __forceinline__ void tma_load_block(void* smem_dst, const void* tmap, uint64_t* bar, int32_t d, int32_t t,
+__device__ __forceinline__ void tma_load_block(uint32_t smem_dst, const void* tmap, uint32_t bar, int32_t d, int32_t t,
                                                int32_t h, int32_t b) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];\n" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(d), "r"(t), "r"(h), "r"(b)
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];\n" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(d), "r"(t), "r"(h), "r"(b)
       : "memory");
-}
-
-// Two floats as bf16 planes: plane 0 the nearest bf16, each further plane the
-// nearest bf16 of what is left, so that p planes hold 8 p bits of the value.
-// Packed as the MMA wants them: the first value in the low half.
-template <int PLANES>
-__device__ __forceinline__ void split2(float a, float b, uint32_t (&out)[PLANES]) {
-#pragma unroll
-  for (int p = 0; p < PLANES; ++p) {
-    uint32_t h;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
-    out[p] = h;
-    if (p + 1 < PLANES) {
-      a -= __uint_as_float(h << 16);
-      b -= __uint_as_float(h & 0xffff0000u);
-    }
-  }
 }
 
 }  // namespace ssscan
