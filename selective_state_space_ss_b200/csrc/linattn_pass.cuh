@@ -115,17 +115,18 @@ struct LaCfg {
   // Tiles in each ring.  A key tile lives until its chunk's increment is formed (the
   // weighted keys' first planes replace it in place), a query tile until S Q is.
   static constexpr int RK = kBf16 ? 3 : 2, RQ = kBf16 ? 3 : 1, RV = kBf16 ? (KB == 2 && VB == 2 ? 2 : 3) : 1;
+  static constexpr int RP = kBf16 ? 2 : 1;   // P
   static constexpr int RF = 4;               // decays
   static constexpr int kRing = 4;
   static_assert(RK <= kRing && RV <= kRing && RQ <= kRing && RF <= kRing, "barriers of a ring");
   static constexpr int kTileK = KB * NPI * kLaBlock, kTileV = VB * NPI * kLaBlock, kTileW = KB * (NPW - NPI) * kLaBlock;
   static constexpr int kQ = 0, kK = RQ * kTileK, kV = kK + RK * kTileK, kP = kV + RV * kTileV;
-  static constexpr int kW = kP + NPX * kLaBlock;
+  static constexpr int kW = kP + RP * NPX * kLaBlock;
   static constexpr int kFacFloats = (kBf16 ? 6 : 4) * kLaChunk + 4;
   static constexpr int kFac = kW + kTileW;
   static constexpr int kStage = kFac + (RF * kFacFloats * 4 + 127) / 128 * 128;  // 512 bytes a back warp
   static constexpr int kBars = kStage + (kBf16 ? 16 * 512 : 0);
-  static constexpr int kSmem = kBars + 10 * kRing * 8 + 16;
+  static constexpr int kSmem = kBars + 11 * kRing * 8 + 16;
   // tensor memory columns
   static constexpr int cDS = 0, cSP = KD, cO1 = cSP + NPX * KD / 2, cO2 = cO1 + 64, cQK = cO2 + 64;
   static constexpr int kAhead = kBf16 ? 2 : 1;  // chunks that scores run ahead, one place for each
@@ -465,13 +466,14 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   const auto full_f = [&](int i) { return ring_bar(6, i); };
   const auto empty_f = [&](int i) { return ring_bar(7, i); };
   const auto b_qk = [&](int i) { return ring_bar(8, i); };  // scores are there, one for each place
-  const uint32_t b_pk = ring_bar(8, 2);    // P and the weighted keys are there
-  const uint32_t b_ds = ring_bar(8, 3);    // increment and P V are there
+  const auto b_p = [&](int i) { return ring_bar(8, 2 + i); };  // P is there
+  const uint32_t b_w = ring_bar(10, 0);    // the weighted keys are there
+  const uint32_t b_ds = ring_bar(10, 1);   // increment and P V are there
   const uint32_t b_o = ring_bar(9, 0);     // S Q too: the chunk's products are done
   const uint32_t b_free = ring_bar(9, 1);  // the back warps have read them
   const uint32_t b_s = ring_bar(9, 2);     // the state's planes are there
   const uint32_t b_end = ring_bar(9, 3);
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + 10 * CF::kRing * 8);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + 11 * CF::kRing * 8);
   int* worker_at = reinterpret_cast<int*>(tmem_at + 1);
   volatile int* dead = worker_at + 1;
 
@@ -485,7 +487,9 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
     }
     la_init(b_qk(0), 1);
     la_init(b_qk(1), 1);
-    la_init(b_pk, kLaFrontWarps);
+    la_init(b_p(0), kLaFrontWarps);
+    la_init(b_p(1), kLaFrontWarps);
+    la_init(b_w, kLaFrontWarps);
     la_init(b_ds, 1);
     la_init(b_o, 1);
     la_init(b_free, CF::kHolders);
@@ -547,9 +551,22 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         // planes of the weighted keys: in the key tile's place, then in one of their own
         const uint32_t w0 = tile_desc(base + CF::kK + rk.i * CF::kTileK, kLaBlock);
         const uint32_t w1 = tile_desc(base + CF::kW, kLaBlock);
-        la_wait(b_pk, n & 1, dead);
         la_wait(full_v(rv.i), rv.full(), dead);
         if (n > 0) la_wait(b_free, (n - 1) & 1, dead);
+        if (!STATES) {
+          // O1^T = V^T P^T
+          la_wait(b_p(n % CF::RP), (n / CF::RP) & 1, dead);
+          tc5_fence_after();
+          if (leader) {
+            const uint32_t pd = tile_desc(base + CF::kP + (n % CF::RP) * NPX * kLaBlock, 0);
+            la_products<NPI, NPX, kLaChunk / 16>([&](int pa, int pb, int i, bool add) {
+              mma_ss(tmem + CF::cO1, v + pa * CF::VB * kUnits + i * (16 * kTileRow >> 4), pd + pb * kUnits + i * 2,
+                     mma_idesc(128, 64, true, false), add);
+            });
+          }
+          __syncwarp();
+        }
+        la_wait(b_w, n & 1, dead);
         tc5_fence_after();
         if (leader) {
           // dS^T = V^T (w . K)
@@ -558,14 +575,6 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             const uint32_t w = pb < NPI ? w0 + pb * CF::KB * kUnits : w1 + (pb - NPI) * CF::KB * kUnits;
             mma_ss(tmem + CF::cDS, v + pa * CF::VB * kUnits + off, w + off, mma_idesc(128, KD, true, true), add);
           });
-          if (!STATES) {
-            // O1^T = V^T P^T
-            const uint32_t pd = tile_desc(base + CF::kP, 0);
-            la_products<NPI, NPX, kLaChunk / 16>([&](int pa, int pb, int i, bool add) {
-              mma_ss(tmem + CF::cO1, v + pa * CF::VB * kUnits + i * (16 * kTileRow >> 4), pd + pb * kUnits + i * 2,
-                     mma_idesc(128, 64, true, false), add);
-            });
-          }
           mma_commit(b_ds);
           mma_commit(empty_v(rv.i));
           mma_commit(empty_k(rk.i));
@@ -676,7 +685,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
     const int w_to = at == 7 ? CF::KB * 16 : (int)(begins >> (8 * at + 8)) & 0xff;
     if (!STATES) {
       // what the mask takes away is zero once and for all
-      for (int i = ftid; i < NPX * kLaBlock / 16; i += 32 * kLaFrontWarps)
+      for (int i = ftid; i < CF::RP * NPX * kLaBlock / 16; i += 32 * kLaFrontWarps)
         reinterpret_cast<uint4*>(smem + CF::kP)[i] = make_uint4(0, 0, 0, 0);
       asm volatile("bar.sync 1, 256;\n" ::: "memory");
     }
@@ -689,8 +698,61 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         char* k = smem + CF::kK + rk.i * CF::kTileK;
         la_wait(full_f(rf.i), rf.full(), dead);
         la_wait(full_k(rk.i), rk.full(), dead);
-        // the keys as they are were used, and what was made here for the last chunk too
-        if (!STATES) la_wait(b_qk(n % CF::kAhead), (n / CF::kAhead) & 1, dead);
+        if (!STATES) {
+          // P = (Q K^T) . D: 16 rows a warp, two rows a thread
+          la_wait(b_qk(n % CF::kAhead), (n / CF::kAhead) & 1, dead);
+          if (CF::RP == 1 && n > 0) la_wait(b_ds, (n - 1) & 1, dead);  // the last P was used
+          tc5_fence_after();
+          const uint32_t p_to = base + CF::kP + (n % CF::RP) * NPX * kLaBlock;
+          const int r0 = fw * 16 + lane / 4;
+          const float sign = a.reverse ? -1.f : 1.f;
+          const float h0 = fac[r0], l0 = fac[kLaChunk + r0], h1 = fac[r0 + 8], l1 = fac[kLaChunk + r0 + 8];
+          const uint64_t hh[2] = {pair(h0, h0), pair(h1, h1)}, ll[2] = {pair(l0, l0), pair(l1, l1)};
+          const uint64_t minus = pair(-1.f, -1.f), sp2 = pair(a.scale_p, a.scale_p);
+          const int c0 = 2 * (lane % 4);
+          // this lane's row address for store_blocks: blocks (rows 0-7, 8-15) x two column blocks
+          const int srow = fw * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+          // 16 columns at a time, those that the mask leaves (the others stay zero)
+          const int from = a.reverse ? fw : 0, to = a.reverse ? 4 : fw + 1;
+#pragma unroll 1
+          for (int cb = from + side; cb < to; cb += 2) {
+            uint32_t x[8];
+            tmem_ld_rows16(x, tmem + ((uint32_t)(fw * 32) << 16) + CF::cQK + (n % CF::kAhead) * 64 + cb * 16);
+            uint64_t gh[2], gl[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              gh[e] = *reinterpret_cast<const uint64_t*>(fac + cb * 16 + e * 8 + c0);
+              gl[e] = *reinterpret_cast<const uint64_t*>(fac + kLaChunk + cb * 16 + e * 8 + c0);
+            }
+            tmem_wait_ld(x);
+            uint32_t o[NPX][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint64_t d = add2(fma2(gh[e], minus, hh[z]), fma2(gl[e], minus, ll[z]));
+                const uint64_t f = pair(ex2_approx(pair_lo(d) * sign), ex2_approx(pair_hi(d) * sign));
+                uint64_t y = mul2(mul2(pair(x[4 * e + 2 * z], x[4 * e + 2 * z + 1]), sp2), f);
+                if (cb == fw) {
+                  const int row = lane / 4 + 8 * z, col = 8 * e + c0;
+                  y = pair((a.reverse ? col >= row : col <= row) ? pair_lo(y) : 0.f,
+                           (a.reverse ? col + 1 >= row : col + 1 <= row) ? pair_hi(y) : 0.f);
+                }
+                uint32_t sp[NPX];
+                split2<NPX>(y, sp);
+#pragma unroll
+                for (int q = 0; q < NPX; ++q) o[q][e * 2 + z] = sp[q];
+              }
+#pragma unroll
+            for (int q = 0; q < NPX; ++q)
+              store_blocks(p_to + q * kLaBlock + tile_unit(srow, cb * 2 + (lane >> 4)), o[q][0], o[q][1],
+                           o[q][2], o[q][3]);
+          }
+          tc5_fence_before();
+          fence_proxy_async_smem();
+          arrive(b_p(n % CF::RP));
+        }
+        // the last chunk's weighted keys were used (and this chunk's keys as they are: b_qk)
         if (n > 0) la_wait(b_ds, (n - 1) & 1, dead);
         // the keys weighted by their decay to the chunk's end (reversed: start)
 #pragma unroll 2
@@ -733,57 +795,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             *reinterpret_cast<uint4*>((q < NPI ? k + q * CF::KB * kLaBlock : smem + CF::kW + (q - NPI) * CF::KB * kLaBlock) +
                                       off) = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
         }
-        if (!STATES) {
-          // P = (Q K^T) . D: 16 rows a warp, two rows a thread
-          tc5_fence_after();
-          const int r0 = fw * 16 + lane / 4;
-          const float sign = a.reverse ? -1.f : 1.f;
-          const float h0 = fac[r0], l0 = fac[kLaChunk + r0], h1 = fac[r0 + 8], l1 = fac[kLaChunk + r0 + 8];
-          const uint64_t hh[2] = {pair(h0, h0), pair(h1, h1)}, ll[2] = {pair(l0, l0), pair(l1, l1)};
-          const uint64_t minus = pair(-1.f, -1.f), sp2 = pair(a.scale_p, a.scale_p);
-          const int c0 = 2 * (lane % 4);
-          // this lane's row address for store_blocks: blocks (rows 0-7, 8-15) x two column blocks
-          const int srow = fw * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-          // 16 columns at a time, those that the mask leaves (the others stay zero)
-          const int from = a.reverse ? fw : 0, to = a.reverse ? 4 : fw + 1;
-#pragma unroll 1
-          for (int cb = from + side; cb < to; cb += 2) {
-            uint32_t x[8];
-            tmem_ld_rows16(x, tmem + ((uint32_t)(fw * 32) << 16) + CF::cQK + (n % CF::kAhead) * 64 + cb * 16);
-            uint64_t gh[2], gl[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              gh[e] = *reinterpret_cast<const uint64_t*>(fac + cb * 16 + e * 8 + c0);
-              gl[e] = *reinterpret_cast<const uint64_t*>(fac + kLaChunk + cb * 16 + e * 8 + c0);
-            }
-            tmem_wait_ld(x);
-            uint32_t o[NPX][4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const uint64_t d = add2(fma2(gh[e], minus, hh[z]), fma2(gl[e], minus, ll[z]));
-                const uint64_t f = pair(ex2_approx(pair_lo(d) * sign), ex2_approx(pair_hi(d) * sign));
-                uint64_t y = mul2(mul2(pair(x[4 * e + 2 * z], x[4 * e + 2 * z + 1]), sp2), f);
-                if (cb == fw) {
-                  const int row = lane / 4 + 8 * z, col = 8 * e + c0;
-                  y = pair((a.reverse ? col >= row : col <= row) ? pair_lo(y) : 0.f,
-                           (a.reverse ? col + 1 >= row : col + 1 <= row) ? pair_hi(y) : 0.f);
-                }
-                uint32_t sp[NPX];
-                split2<NPX>(y, sp);
-#pragma unroll
-                for (int q = 0; q < NPX; ++q) o[q][e * 2 + z] = sp[q];
-              }
-#pragma unroll
-            for (int q = 0; q < NPX; ++q)
-              store_blocks(smem_u32(smem) + CF::kP + q * kLaBlock + tile_unit(srow, cb * 2 + (lane >> 4)), o[q][0], o[q][1],
-                           o[q][2], o[q][3]);
-          }
-          tc5_fence_before();
-        }
         fence_proxy_async_smem();
-        arrive(b_pk);
+        arrive(b_w);
         arrive(empty_f(rf.i));
         rf.next(), rk.next();
       }
