@@ -7,6 +7,8 @@ the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 import threading
 
@@ -442,83 +444,136 @@ def ss_scan_fwd_noalloc(u, delta, A, B, C, D=None, z=None, delta_bias=None, soft
 # ---- linear attention with a decay per head, and the 8-bit state pool (include/ss_linattn.h)
 
 
-def _heads(name, t, device, dtype, shape):
-    """A strided [batch, seqlen, heads, d] operand (log decays: without the last axis); a
-    missing seqlen axis (the single-token step) has stride 0."""
+# These calls are short next to what Python costs, so every operand is looked at once,
+# plainly, and what is wrong with it is worked out only when something is.
+
+
+def _wrong(name, t, device, dtype, shape):
     if not isinstance(t, torch.Tensor) or t.device != device:
         raise ValueError(f"{name} must be a tensor on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype} is not {dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    return SSHeads(t.data_ptr(), 0, 0, 0)
+    raise ValueError(f"{name}: the last axis must be contiguous" if len(shape) > 2
+                     else f"{name} must be contiguous")
 
 
 def _heads4(name, t, device, dtype, shape):
-    h = _heads(name, t, device, dtype, shape)
-    if len(shape) == 4 and shape[3] > 1 and t.stride(3) != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    h.batch_stride, h.token_stride, h.head_stride = t.stride(0), t.stride(1), t.stride(2)
-    return h
+    """A strided [batch, seqlen, heads, d] operand, or [batch, seqlen, heads] (log decays)."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or t.device != device:
+        _wrong(name, t, device, dtype, shape)
+    st = t.stride()
+    if len(st) == 4 and st[3] != 1 and shape[3] > 1:
+        _wrong(name, t, device, dtype, shape)
+    return SSHeads(t.data_ptr(), st[0], st[1], st[2])
 
 
 def _heads3(name, t, device, dtype, shape):
-    h = _heads(name, t, device, dtype, shape)
-    if len(shape) == 3 and shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    h.batch_stride, h.head_stride = t.stride(0), t.stride(1)
-    return h
+    """The same for a single token: [batch, heads, d] or [batch, heads]."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or t.device != device:
+        _wrong(name, t, device, dtype, shape)
+    st = t.stride()
+    if len(st) == 3 and st[2] != 1 and shape[2] > 1:
+        _wrong(name, t, device, dtype, shape)
+    return SSHeads(t.data_ptr(), st[0], 0, st[1])
+
+
+def _dense(name, t, device, dtype, shape):
+    """Address of a contiguous operand, None of a missing one."""
+    if t is None:
+        return None
+    if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or t.device != device
+            or not t.is_contiguous()):
+        _check_dev(name, t, device, (dtype,), shape)
+    return t.data_ptr()
 
 
 def _cuda_device(name, t, what):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} runs on CUDA tensors only (no CPU fallback): {name}")
     return t.device
 
 
+_FLOATS = {torch.float32: SS_F32, torch.bfloat16: SS_BF16}
+
+
+def _in_dtype(q):
+    dt = _FLOATS.get(q.dtype)
+    if dt is None:
+        raise ValueError(f"q: dtype {q.dtype} is not float32 or bfloat16")
+    return dt
+
+
+def _call(fn, where, device, stream, *args):
+    """fn(*args, stream) with the operands' device current."""
+    index = device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = _stream_handle(stream, device)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != SS_OK:
+        raise SSError(st, where)
+
+
 def _linattn_operands(what, q, k, v, log_decay):
     device = _cuda_device("q", q, what)
-    if q.dim() != 4 or v.dim() != 4:
+    if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
         raise ValueError("q and k must be [batch, L, qk_heads, dk] and v [batch, L, heads, dv]")
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"q: dtype {q.dtype} is not float32 or bfloat16")
-    batch, L, qk_heads, dk = q.shape
+    dt, dtype = _in_dtype(q), q.dtype
+    shape = q.shape
+    batch, L, qk_heads, dk = shape
     heads, dv = v.shape[2:]
-    ops = [_heads4("q", q, device, q.dtype, (batch, L, qk_heads, dk)),
-           _heads4("k", k, device, q.dtype, (batch, L, qk_heads, dk)),
-           _heads4("v", v, device, q.dtype, (batch, L, heads, dv)),
-           _heads4("log_decay", log_decay, device, q.dtype, (batch, L, heads))]
-    dt = SS_F32 if q.dtype == torch.float32 else SS_BF16
+    ops = [_heads4("q", q, device, dtype, shape), _heads4("k", k, device, dtype, shape),
+           _heads4("v", v, device, dtype, (batch, L, heads, dv)),
+           _heads4("log_decay", log_decay, device, dtype, (batch, L, heads))]
     return device, ops, (batch, L, heads, qk_heads, dk, dv, dt)
 
 
-def _linattn_need(fn, sizes):
-    n = fn(*sizes)
+@functools.lru_cache(maxsize=1024)
+def _linattn_need(backward, device, batch, seqlen, heads, qk_heads, dk, dv, in_dtype):
+    """Workspace bytes on the device of that number (they follow from the sizes and its SMs)."""
+    lib = load_library()
+    fn = lib.ss_linattn_bwd_workspace_bytes if backward else lib.ss_linattn_workspace_bytes
+    sizes = (batch, seqlen, heads, qk_heads, dk, dv, in_dtype)
+    if device is None or device == torch.cuda.current_device():
+        n = fn(*sizes)
+    else:
+        with torch.cuda.device(device):
+            n = fn(*sizes)
     if n == ctypes.c_size_t(-1).value:
-        _, _, heads, qk_heads, dk, dv, _ = sizes
         unsupported = min(sizes[:6]) >= 1 and heads % qk_heads == 0 and max(dk, dv) > 128
         raise SSError(SS_ERR_UNSUPPORTED if unsupported else SS_ERR_INVALID_ARG, fn.__name__)
     return n
 
 
+def _current_device():
+    return torch.cuda.current_device() if torch.cuda.is_available() else None
+
+
 def ss_linattn_workspace_bytes(batch, seqlen, heads, qk_heads, dk, dv, in_dtype) -> int:
-    return _linattn_need(load_library().ss_linattn_workspace_bytes,
-                         (batch, seqlen, heads, qk_heads, dk, dv, int(in_dtype)))
+    return _linattn_need(False, _current_device(), batch, seqlen, heads, qk_heads, dk, dv, int(in_dtype))
 
 
 def ss_linattn_bwd_workspace_bytes(batch, seqlen, heads, qk_heads, dk, dv, in_dtype) -> int:
-    return _linattn_need(load_library().ss_linattn_bwd_workspace_bytes,
-                         (batch, seqlen, heads, qk_heads, dk, dv, int(in_dtype)))
+    return _linattn_need(True, _current_device(), batch, seqlen, heads, qk_heads, dk, dv, int(in_dtype))
 
 
 def _workspace(workspace, need, device):
+    """(tensor to keep until the launch, its address, its bytes)"""
     if workspace is None:
         if need == 0:
-            return None, 0
+            return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def ss_linattn_fwd(q, k, v, log_decay, scale=1.0, initial_state=None, lengths=None, o_out=None,
@@ -533,26 +588,21 @@ def ss_linattn_fwd(q, k, v, log_decay, scale=1.0, initial_state=None, lengths=No
     here is zero there).  Returns (o [batch, L, heads, dv] in the input dtype, last_state
     [batch, heads, dk, dv] float32 or None); last_state_out may be initial_state.
     """
-    lib = load_library()
+    lib = _lib or load_library()
     device, ops, sizes = _linattn_operands("ss_linattn_fwd", q, k, v, log_decay)
     batch, L, heads, _, dk, dv, _ = sizes
-    need = ss_linattn_workspace_bytes(*sizes)
-    _check_dev("initial_state", initial_state, device, (torch.float32,), (batch, heads, dk, dv))
-    _check_dev("lengths", lengths, device, (torch.int32,), (batch,))
+    need = _linattn_need(False, device.index, *sizes)
+    f32, shape = torch.float32, (batch, heads, dk, dv)
     if o_out is None:
-        make = torch.empty if lengths is None else torch.zeros
-        o_out = make((batch, L, heads, dv), dtype=q.dtype, device=device)
-    _check_dev("o_out", o_out, device, (q.dtype,), (batch, L, heads, dv))
+        o_out = (q.new_empty if lengths is None else q.new_zeros)((batch, L, heads, dv))
     if last_state_out is None and return_last_state:
-        last_state_out = torch.empty((batch, heads, dk, dv), dtype=torch.float32, device=device)
-    _check_dev("last_state_out", last_state_out, device, (torch.float32,), (batch, heads, dk, dv))
-    workspace, ws_bytes = _workspace(workspace, need, device)
-    with torch.cuda.device(device):
-        st = lib.ss_linattn_fwd(*ops, float(scale), _ptr(initial_state), _ptr(lengths), _ptr(o_out),
-                                _ptr(last_state_out), *sizes, _ptr(workspace), ws_bytes,
-                                _stream_handle(stream, device))
-    if st != SS_OK:
-        raise SSError(st, "ss_linattn_fwd")
+        last_state_out = torch.empty(shape, dtype=f32, device=device)
+    keep, ws, ws_bytes = _workspace(workspace, need, device)
+    _call(lib.ss_linattn_fwd, "ss_linattn_fwd", device, stream, *ops, scale,
+          _dense("initial_state", initial_state, device, f32, shape),
+          _dense("lengths", lengths, device, torch.int32, (batch,)),
+          _dense("o_out", o_out, device, q.dtype, (batch, L, heads, dv)),
+          _dense("last_state_out", last_state_out, device, f32, shape), *sizes, ws, ws_bytes)
     return o_out, last_state_out
 
 
@@ -565,28 +615,22 @@ def ss_linattn_bwd(q, k, v, log_decay, do, scale=1.0, initial_state=None, dlast_
     inputs' dtype, zero behind a row's length, and dinitial_state float32 (None without
     initial_state).
     """
-    lib = load_library()
+    lib = _lib or load_library()
     device, ops, sizes = _linattn_operands("ss_linattn_bwd", q, k, v, log_decay)
     batch, L, heads, qk_heads, dk, dv, _ = sizes
-    need = ss_linattn_bwd_workspace_bytes(*sizes)
-    ops.append(_heads4("do", do, device, q.dtype, (batch, L, heads, dv)))
-    for name, t in (("initial_state", initial_state), ("dlast_state", dlast_state)):
-        _check_dev(name, t, device, (torch.float32,), (batch, heads, dk, dv))
-    _check_dev("lengths", lengths, device, (torch.int32,), (batch,))
-    make = torch.empty if lengths is None else torch.zeros
-    g = {"dq": make((batch, L, qk_heads, dk), dtype=q.dtype, device=device),
-         "dk": make((batch, L, qk_heads, dk), dtype=q.dtype, device=device),
-         "dv": make((batch, L, heads, dv), dtype=q.dtype, device=device),
-         "dlog_decay": make((batch, L, heads), dtype=q.dtype, device=device),
+    need = _linattn_need(True, device.index, *sizes)
+    f32, shape, dtype = torch.float32, (batch, heads, dk, dv), q.dtype
+    ops.append(_heads4("do", do, device, dtype, (batch, L, heads, dv)))
+    states = (_dense("initial_state", initial_state, device, f32, shape),
+              _dense("dlast_state", dlast_state, device, f32, shape),
+              _dense("lengths", lengths, device, torch.int32, (batch,)))
+    make = q.new_empty if lengths is None else q.new_zeros
+    g = {"dq": make((batch, L, qk_heads, dk)), "dk": make((batch, L, qk_heads, dk)),
+         "dv": make((batch, L, heads, dv)), "dlog_decay": make((batch, L, heads)),
          "dinitial_state": None if initial_state is None else torch.empty_like(initial_state)}
-    workspace, ws_bytes = _workspace(workspace, need, device)
-    with torch.cuda.device(device):
-        st = lib.ss_linattn_bwd(*ops, float(scale), _ptr(initial_state), _ptr(dlast_state),
-                                _ptr(lengths), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
-                                _ptr(g["dlog_decay"]), _ptr(g["dinitial_state"]), *sizes,
-                                _ptr(workspace), ws_bytes, _stream_handle(stream, device))
-    if st != SS_OK:
-        raise SSError(st, "ss_linattn_bwd")
+    keep, ws, ws_bytes = _workspace(workspace, need, device)
+    _call(lib.ss_linattn_bwd, "ss_linattn_bwd", device, stream, *ops, scale, *states,
+          *[_ptr(t) for t in g.values()], *sizes, ws, ws_bytes)
     return g
 
 
@@ -599,47 +643,42 @@ def ss_linattn_step(state, q, k, v, log_decay, scale=1.0, slots=None, o_out=None
     written (an o allocated here is zero there), and so is a row whose slot an earlier row
     has.  Returns o [batch, heads, dv] in the input dtype.
     """
-    lib = load_library()
+    lib = _lib or load_library()
     device = _cuda_device("state", state, "ss_linattn_step")
-    if state.dim() != 4 or q.dim() != 3 or v.dim() != 3:
+    if state.dim() != 4 or _cuda_device("q", q, "ss_linattn_step") != device or q.dim() != 3:
         raise ValueError("state must be [num_slots, heads, dk, dv], q and k [batch, qk_heads, dk], "
-                         "v [batch, heads, dv]")
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"q: dtype {q.dtype} is not float32 or bfloat16")
-    num_slots, heads, dk, dv = state.shape
-    batch, qk_heads, _ = q.shape
-    _check_dev("state", state, device, (torch.float32,))
-    ops = [_heads3("q", q, device, q.dtype, (batch, qk_heads, dk)),
-           _heads3("k", k, device, q.dtype, (batch, qk_heads, dk)),
-           _heads3("v", v, device, q.dtype, (batch, heads, dv)),
-           _heads3("log_decay", log_decay, device, q.dtype, (batch, heads))]
-    _check_dev("slots", slots, device, (torch.int32,), (batch,))
+                         "v [batch, heads, dv], on one device")
+    dt, dtype = _in_dtype(q), q.dtype
+    pool, shape = state.shape, q.shape
+    num_slots, heads, dk, dv = pool
+    batch, qk_heads, width = shape
+    if width != dk:
+        raise ValueError(f"q: {width} values a head, the states have {dk}")
+    out = (batch, heads, dv)
     if o_out is None:
-        make = torch.empty if slots is None else torch.zeros
-        o_out = make((batch, heads, dv), dtype=q.dtype, device=device)
-    _check_dev("o_out", o_out, device, (q.dtype,), (batch, heads, dv))
-    dt = SS_F32 if q.dtype == torch.float32 else SS_BF16
-    with torch.cuda.device(device):
-        st = lib.ss_linattn_step(*ops, float(scale), _ptr(state), num_slots, _ptr(slots), _ptr(o_out),
-                                 batch, heads, qk_heads, dk, dv, dt, _stream_handle(stream, device))
-    if st != SS_OK:
-        raise SSError(st, "ss_linattn_step")
+        o_out = (q.new_empty if slots is None else q.new_zeros)(out)
+    _call(lib.ss_linattn_step, "ss_linattn_step", device, stream,
+          _heads3("q", q, device, dtype, shape), _heads3("k", k, device, dtype, shape),
+          _heads3("v", v, device, dtype, out), _heads3("log_decay", log_decay, device, dtype, (batch, heads)),
+          scale, _dense("state", state, device, torch.float32, pool), num_slots,
+          _dense("slots", slots, device, torch.int32, (batch,)), _dense("o_out", o_out, device, dtype, out),
+          batch, heads, qk_heads, dk, dv, dt)
     return o_out
 
 
 def _pool_operands(what, codes, scales, slots):
+    """(device, batch, shape of a state, arguments that follow the state's)"""
     device = _cuda_device("codes", codes, what)
-    if codes.dim() < 2:
+    shape = codes.shape
+    if len(shape) < 2:
         raise ValueError("codes must be [num_slots, ..., width]")
-    _check_dev("codes", codes, device, (torch.int8,))
-    _check_dev("scales", scales, device, (torch.float32,), codes.shape[:-1])
     if slots is not None and (not isinstance(slots, torch.Tensor) or slots.dim() != 1):
         raise ValueError("slots must be a [batch] tensor")
-    _check_dev("slots", slots, device, (torch.int32,))
-    rows = 1
-    for n in codes.shape[1:-1]:
-        rows *= n
-    return device, rows
+    batch = None if slots is None else slots.shape[0]
+    ptrs = (_dense("codes", codes, device, torch.int8, shape),
+            _dense("scales", scales, device, torch.float32, shape[:-1]),
+            shape[0], _dense("slots", slots, device, torch.int32, (batch,)))
+    return device, batch, shape[1:], ptrs
 
 
 def ss_state_store8(state, codes, scales, slots=None, stream=None):
@@ -649,30 +688,27 @@ def ss_state_store8(state, codes, scales, slots=None, stream=None):
     row b goes to slot b); a slot outside the pool leaves that sequence out, and of several
     with the same slot the last one is kept.
     """
-    lib = load_library()
-    device, rows = _pool_operands("ss_state_store8", codes, scales, slots)
-    batch = state.shape[0] if slots is None else slots.shape[0]
-    _check_dev("state", state, device, (torch.float32,), (batch, *codes.shape[1:]))
-    with torch.cuda.device(device):
-        st = lib.ss_state_store8(_ptr(state), _ptr(codes), _ptr(scales), codes.shape[0], _ptr(slots),
-                                 batch, rows, codes.shape[-1], _stream_handle(stream, device))
-    if st != SS_OK:
-        raise SSError(st, "ss_state_store8")
+    lib = _lib or load_library()
+    device, batch, shape, ptrs = _pool_operands("ss_state_store8", codes, scales, slots)
+    if batch is None:
+        batch = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() else 0
+    _call(lib.ss_state_store8, "ss_state_store8", device, stream,
+          _dense("state", state, device, torch.float32, (batch, *shape)), *ptrs, batch,
+          math.prod(shape[:-1]), shape[-1])
 
 
 def ss_state_load8(codes, scales, slots=None, state_out=None, stream=None):
     """States read back from the pool of ss_state_store8 as [batch, ..., width] float32.
     slots: [batch] int32 (None: every slot, in order); a slot outside the pool gives a zero
     state."""
-    lib = load_library()
-    device, rows = _pool_operands("ss_state_load8", codes, scales, slots)
-    batch = codes.shape[0] if slots is None else slots.shape[0]
+    lib = _lib or load_library()
+    device, batch, shape, ptrs = _pool_operands("ss_state_load8", codes, scales, slots)
+    if batch is None:
+        batch = codes.shape[0]
+    whole = (batch, *shape)
     if state_out is None:
-        state_out = torch.empty((batch, *codes.shape[1:]), dtype=torch.float32, device=device)
-    _check_dev("state_out", state_out, device, (torch.float32,), (batch, *codes.shape[1:]))
-    with torch.cuda.device(device):
-        st = lib.ss_state_load8(_ptr(codes), _ptr(scales), codes.shape[0], _ptr(slots), _ptr(state_out),
-                                batch, rows, codes.shape[-1], _stream_handle(stream, device))
-    if st != SS_OK:
-        raise SSError(st, "ss_state_load8")
+        state_out = scales.new_empty(whole)
+    _call(lib.ss_state_load8, "ss_state_load8", device, stream, *ptrs,
+          _dense("state_out", state_out, device, torch.float32, whole), batch,
+          math.prod(shape[:-1]), shape[-1])
     return state_out

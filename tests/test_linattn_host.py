@@ -111,7 +111,7 @@ def test_workspace_queries_reject_what_the_calls_do(lib, over, _):
 
 
 def test_workspace_queries(lib):
-    assert lib.ss_linattn_workspace_bytes(64, 64, 16, 16, 64, 64, N.SS_BF16) == 0
+    assert lib.ss_linattn_workspace_bytes(2, 64, 16, 16, 64, 64, N.SS_BF16) == 0  # a chunk each: nothing to cut
     small = lib.ss_linattn_bwd_workspace_bytes(2, 100, 4, 4, 64, 64, N.SS_BF16)
     shared = lib.ss_linattn_bwd_workspace_bytes(2, 100, 4, 2, 64, 64, N.SS_BF16)
     assert 0 < small < shared  # shared queries and keys add their heads' partial gradients
