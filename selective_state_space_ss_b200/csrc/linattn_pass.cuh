@@ -126,7 +126,7 @@ struct LaCfg {
   static constexpr int kFac = kW + kTileW;
   static constexpr int kStage = kFac + (RF * kFacFloats * 4 + 127) / 128 * 128;  // 512 bytes a back warp
   static constexpr int kBars = kStage + (kBf16 ? 16 * 512 : 0);
-  static constexpr int kSmem = kBars + 11 * kRing * 8 + 16;
+  static constexpr int kSmem = kBars + 12 * kRing * 8 + 16;
   // tensor memory columns
   static constexpr int cDS = 0, cSP = KD, cO1 = cSP + NPX * KD / 2, cO2 = cO1 + 64, cQK = cO2 + 64;
   static constexpr int kAhead = kBf16 ? 2 : 1;  // chunks that scores run ahead, one place for each
@@ -135,11 +135,16 @@ struct LaCfg {
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr int kQuads = VD / 32;        // lane quadrants that hold values
   static constexpr int kHolders = 4 * kQuads;   // back warps at work
-  static constexpr int kLoaders = 64;           // loader threads
+  // Two warps issue MMAs: one the state's increments, the other scores and outputs, so
+  // that neither chain of hand-overs waits in the other's.  (fp32 has one query tile and
+  // one place for scores, so all in one order, and more loading to do: there the second
+  // warp loads.)
+  static constexpr bool kTwoIssuers = kBf16;
+  static constexpr int kLoaders = kTwoIssuers ? 32 : 64;  // loader threads
   static constexpr int kThreads = 896;
 };
 constexpr int kLaBackWarps = 16, kLaFrontWarps = 8;
-constexpr int kLaMmaWarp = 24, kLaLoadWarp = 25, kLaDecayWarp = 27;
+constexpr int kLaMmaWarp = 24, kLaLoadWarp = 25, kLaMmaOrLoadWarp = 26, kLaDecayWarp = 27;
 // registers a thread of the three kinds of warpgroup: 4 x 88 + 2 x 56 + 40 = 7 x 72 at launch
 constexpr int kLaBackRegs = 88, kLaFrontRegs = 56, kLaAuxRegs = 40;
 
@@ -467,13 +472,15 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   const auto empty_f = [&](int i) { return ring_bar(7, i); };
   const auto b_qk = [&](int i) { return ring_bar(8, i); };  // scores are there, one for each place
   const auto b_p = [&](int i) { return ring_bar(8, 2 + i); };  // P is there
-  const uint32_t b_w = ring_bar(10, 0);    // the weighted keys are there
-  const uint32_t b_ds = ring_bar(10, 1);   // increment and P V are there
-  const uint32_t b_o = ring_bar(9, 0);     // S Q too: the chunk's products are done
-  const uint32_t b_free = ring_bar(9, 1);  // the back warps have read them
-  const uint32_t b_s = ring_bar(9, 2);     // the state's planes are there
+  const auto b_w = [&](int i) { return ring_bar(11, i); };  // half of the weighted keys is there
+  const uint32_t b_half = ring_bar(10, 0); // the first half of them was used
+  const uint32_t b_ds = ring_bar(10, 1);   // the state's increment is there
+  const auto b_p_free = [&](int i) { return ring_bar(10, 2 + i); };  // P was used
+  const uint32_t b_o = ring_bar(9, 0);     // P V and S Q are there
+  const uint32_t b_free = ring_bar(9, 1);  // the back warps have read the increment
+  const uint32_t b_s = ring_bar(9, 2);     // the state's planes are there, and the outputs before were read
   const uint32_t b_end = ring_bar(9, 3);
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + 11 * CF::kRing * 8);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + 12 * CF::kRing * 8);
   int* worker_at = reinterpret_cast<int*>(tmem_at + 1);
   volatile int* dead = worker_at + 1;
 
@@ -482,14 +489,20 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   const int tid = threadIdx.x, warp = (int)same(tid / 32), lane = tid % 32;
   if (tid == 0) {
     for (int i = 0; i < CF::kRing; ++i) {
-      for (int w = 0; w < 7; ++w) la_init(ring_bar(w, i), 1);
+      for (int w = 0; w < 7; ++w)
+        if (STATES || w != 3) la_init(ring_bar(w, i), 1);
       la_init(empty_f(i), kLaFrontWarps + CF::kHolders);
+      if (!STATES) la_init(empty_v(i), 2);
     }
     la_init(b_qk(0), 1);
     la_init(b_qk(1), 1);
     la_init(b_p(0), kLaFrontWarps);
     la_init(b_p(1), kLaFrontWarps);
-    la_init(b_w, kLaFrontWarps);
+    la_init(b_w(0), kLaFrontWarps);
+    la_init(b_w(1), kLaFrontWarps);
+    la_init(b_half, 1);
+    la_init(b_p_free(0), 1);
+    la_init(b_p_free(1), 1);
     la_init(b_ds, 1);
     la_init(b_o, 1);
     la_init(b_free, CF::kHolders);
@@ -514,10 +527,11 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
 
   if (warp >= kLaMmaWarp) {
     regs_give<kLaAuxRegs>();
-    if (warp == kLaMmaWarp) {
-      // ---- MMA issue, by one thread of the warp
+    if (warp == kLaMmaWarp || (CF::kTwoIssuers && warp == kLaMmaOrLoadWarp)) {
+      // ---- MMA issue, by one thread of a warp
       constexpr int kUnits = kLaBlock >> 4;  // a block in descriptor units
       const bool leader = elect_one();
+      const bool states = warp == kLaMmaWarp, outputs = !STATES && (!CF::kTwoIssuers || !states);
       LaRing<CF::RK> rk, sk;  // of the chunk at hand, and of the one whose scores come next
       LaRing<CF::RQ> rq, sq;
       LaRing<CF::RV> rv;
@@ -544,53 +558,64 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         __syncwarp();
         sk.next(), sq.next(), ++scored;
       };
-      if (!STATES)
+      if (outputs)
         while (scored < CF::kAhead && scored < total) scores();
       for (int n = 0; n < total; ++n) {
         const uint32_t v = tile_desc(base + CF::kV + rv.i * CF::kTileV, kLaBlock);
-        // planes of the weighted keys: in the key tile's place, then in one of their own
-        const uint32_t w0 = tile_desc(base + CF::kK + rk.i * CF::kTileK, kLaBlock);
-        const uint32_t w1 = tile_desc(base + CF::kW, kLaBlock);
         la_wait(full_v(rv.i), rv.full(), dead);
-        if (n > 0) la_wait(b_free, (n - 1) & 1, dead);
-        if (!STATES) {
-          // O1^T = V^T P^T
-          la_wait(b_p(n % CF::RP), (n / CF::RP) & 1, dead);
+        if (states) {
+          // planes of the weighted keys: in the key tile's place, then in one of their own
+          const uint32_t w0 = tile_desc(base + CF::kK + rk.i * CF::kTileK, kLaBlock);
+          const uint32_t w1 = tile_desc(base + CF::kW, kLaBlock);
+          if (n > 0) la_wait(b_free, (n - 1) & 1, dead);
+          // dS^T = V^T (w . K), 32 tokens at a time: the front makes the next chunk's first
+          // half while the second is at work
+          const auto half = [&](int first) {
+            la_products<NPI, NPW, kLaChunk / 32>([&](int pa, int pb, int i, bool add) {
+              const int off = (first + i) * (16 * kTileRow >> 4);
+              const uint32_t w = pb < NPI ? w0 + pb * CF::KB * kUnits : w1 + (pb - NPI) * CF::KB * kUnits;
+              mma_ss(tmem + CF::cDS, v + pa * CF::VB * kUnits + off, w + off, mma_idesc(128, KD, true, true),
+                     add || first > 0);
+            });
+          };
+          la_wait(b_w(0), n & 1, dead);
           tc5_fence_after();
           if (leader) {
-            const uint32_t pd = tile_desc(base + CF::kP + (n % CF::RP) * NPX * kLaBlock, 0);
+            half(0);
+            mma_commit(b_half);
+          }
+          __syncwarp();
+          la_wait(b_w(1), n & 1, dead);
+          tc5_fence_after();
+          if (leader) {
+            half(2);
+            mma_commit(b_ds);
+            mma_commit(empty_v(rv.i));
+            mma_commit(empty_k(rk.i));
+          }
+          __syncwarp();
+        }
+        if (outputs) {
+          const int place = n % CF::RP;
+          la_wait(b_p(place), (n / CF::RP) & 1, dead);
+          la_wait(b_s, n & 1, dead);  // and the last chunk's outputs were read
+          tc5_fence_after();
+          if (leader) {
+            // O1^T = V^T P^T
+            const uint32_t pd = tile_desc(base + CF::kP + place * NPX * kLaBlock, 0);
             la_products<NPI, NPX, kLaChunk / 16>([&](int pa, int pb, int i, bool add) {
               mma_ss(tmem + CF::cO1, v + pa * CF::VB * kUnits + i * (16 * kTileRow >> 4), pd + pb * kUnits + i * 2,
                      mma_idesc(128, 64, true, false), add);
             });
-          }
-          __syncwarp();
-        }
-        la_wait(b_w, n & 1, dead);
-        tc5_fence_after();
-        if (leader) {
-          // dS^T = V^T (w . K)
-          la_products<NPI, NPW, kLaChunk / 16>([&](int pa, int pb, int i, bool add) {
-            const int off = i * (16 * kTileRow >> 4);
-            const uint32_t w = pb < NPI ? w0 + pb * CF::KB * kUnits : w1 + (pb - NPI) * CF::KB * kUnits;
-            mma_ss(tmem + CF::cDS, v + pa * CF::VB * kUnits + off, w + off, mma_idesc(128, KD, true, true), add);
-          });
-          mma_commit(b_ds);
-          mma_commit(empty_v(rv.i));
-          mma_commit(empty_k(rk.i));
-        }
-        __syncwarp();
-        if (!STATES) {
-          // O2^T = S^T Q^T
-          la_wait(b_s, n & 1, dead);
-          tc5_fence_after();
-          if (leader) {
+            // O2^T = S^T Q^T
             const uint32_t q = tile_desc(base + CF::kQ + rq.i * CF::kTileK, 0);
             la_products<NPX, NPI, KD / 16>([&](int pa, int pb, int i, bool add) {
               mma_ts(tmem + CF::cO2, tmem + CF::cSP + pa * (KD / 2) + i * 8,
                      q + (pb * CF::KB + i / 4) * kUnits + (i % 4) * 2, mma_idesc(128, 64, false, false), add);
             });
             mma_commit(b_o);
+            mma_commit(b_p_free(place));
+            mma_commit(empty_v(rv.i));
             mma_commit(empty_q(rq.i));
           }
           __syncwarp();
@@ -645,7 +670,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
               }
             } else {
               __syncwarp();
-              asm volatile("bar.sync 2, 64;\n" ::: "memory");
+              if (CF::kLoaders > 32) asm volatile("bar.sync 2, 64;\n" ::: "memory");
               la_load_tile<T, DP>(smem + at, x, p.b, p.h, t0, p.len, d, a.vec, ltid, CF::kLoaders);
               if (CF::kBf16 && a.vec) {
                 cp_async_commit();
@@ -653,7 +678,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
               }
               fence_proxy_async_smem();
               __syncwarp();
-              asm volatile("bar.sync 2, 64;\n" ::: "memory");
+              if (CF::kLoaders > 32) asm volatile("bar.sync 2, 64;\n" ::: "memory");
               if (ltid == 0) la_arrive(full);
             }
           };
@@ -672,17 +697,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
     // ---- front: weighted keys and P, a chunk ahead of the back
     regs_give<kLaFrontRegs>();
     // 16 rows of P for each pair of warps, side 0 with every other block of columns
-    const int fw = warp % 4, side = (warp - kLaBackWarps) / 4, ftid = tid - 32 * kLaBackWarps;
+    const int fw = warp % 4, front = warp - kLaBackWarps, side = front / 4, ftid = tid - 32 * kLaBackWarps;
     int n = 0;
-    // Shares of the 32 or 16 steps of a key tile.  A warp's rows of P have none to two
-    // blocks of 16 columns under the mask, each about as much work as one and a half
-    // steps: where they have fewer, the share of the steps is larger.  Byte i is where
-    // the share of the i-th warp begins, in the order of rows (reversed: from the last).
-    const int at = 2 * (a.reverse ? 3 - fw : fw) + side;
-    const uint64_t begins = STATES ? (CF::KB == 2 ? 0x1c1814100c080400ull : 0x0e0c0a0806040200ull)
-                                   : (CF::KB == 2 ? 0x1d1a16130f0a0400ull : 0x0f0e0c0b09060200ull);
-    const int w_from = (int)(begins >> (8 * at)) & 0xff;
-    const int w_to = at == 7 ? CF::KB * 16 : (int)(begins >> (8 * at + 8)) & 0xff;
     if (!STATES) {
       // what the mask takes away is zero once and for all
       for (int i = ftid; i < CF::RP * NPX * kLaBlock / 16; i += 32 * kLaFrontWarps)
@@ -698,10 +714,58 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         char* k = smem + CF::kK + rk.i * CF::kTileK;
         la_wait(full_f(rf.i), rf.full(), dead);
         la_wait(full_k(rk.i), rk.full(), dead);
+        // the keys weighted by their decay to the chunk's end (reversed: start), 32 tokens at
+        // a time, each half when the last chunk's was used (and these keys as they are: b_qk)
+        if (!STATES) la_wait(b_qk(n % CF::kAhead), (n / CF::kAhead) & 1, dead);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (n > 0) la_wait(half ? b_ds : b_half, (n - 1) & 1, dead);
+#pragma unroll
+          for (int st = front; st < CF::KB * 8; st += kLaFrontWarps) {
+            const int row = half * 32 + (st % 8) * 4 + lane / 8;
+            const int off = (st / 8) * kLaBlock + row * kTileRow + (lane % 8) * 16;
+            uint32_t in[NPI][4], out[NPW][4];
+#pragma unroll
+            for (int q = 0; q < NPI; ++q) {
+              const uint4 y = *reinterpret_cast<const uint4*>(k + q * CF::KB * kLaBlock + off);
+              in[q][0] = y.x, in[q][1] = y.y, in[q][2] = y.z, in[q][3] = y.w;
+            }
+            if constexpr (CF::kBf16) {
+              // k (w0 + w1 + w2): a product of two bf16 is a bf16 and the bf16 that is left,
+              // exactly, so four planes hold 24 bits without leaving bf16 arithmetic
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(fac) + 3 * kLaChunk + row;
+              const uint32_t w0 = w[0], w1 = w[kLaChunk], w2 = w[2 * kLaChunk];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                out[0][e] = mul_bf16x2(in[0][e], w0);
+                out[1][e] = fma_bf16x2(in[0][e], w0, neg_bf16x2(out[0][e]));
+                out[2][e] = mul_bf16x2(in[0][e], w1);
+                out[3][e] = fma_bf16x2(in[0][e], w2, fma_bf16x2(in[0][e], w1, neg_bf16x2(out[2][e])));
+              }
+            } else {
+              const float wj = fac[3 * kLaChunk + row];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint64_t y = from_bf16x2(in[NPI - 1][e]);
+#pragma unroll
+                for (int q = NPI - 2; q >= 0; --q) y = add2(y, from_bf16x2(in[q][e]));  // exact from the smallest
+                uint32_t sp[NPW];
+                split2<NPW>(mul2(y, pair(wj, wj)), sp);
+#pragma unroll
+                for (int q = 0; q < NPW; ++q) out[q][e] = sp[q];
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < NPW; ++q)
+              *reinterpret_cast<uint4*>((q < NPI ? k + q * CF::KB * kLaBlock : smem + CF::kW + (q - NPI) * CF::KB * kLaBlock) +
+                                        off) = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
+          }
+          fence_proxy_async_smem();
+          arrive(b_w(half));
+        }
         if (!STATES) {
           // P = (Q K^T) . D: 16 rows a warp, two rows a thread
-          la_wait(b_qk(n % CF::kAhead), (n / CF::kAhead) & 1, dead);
-          if (CF::RP == 1 && n > 0) la_wait(b_ds, (n - 1) & 1, dead);  // the last P was used
+          if (n >= CF::RP) la_wait(b_p_free(n % CF::RP), (n / CF::RP - 1) & 1, dead);
           tc5_fence_after();
           const uint32_t p_to = base + CF::kP + (n % CF::RP) * NPX * kLaBlock;
           const int r0 = fw * 16 + lane / 4;
@@ -752,51 +816,6 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           fence_proxy_async_smem();
           arrive(b_p(n % CF::RP));
         }
-        // the last chunk's weighted keys were used (and this chunk's keys as they are: b_qk)
-        if (n > 0) la_wait(b_ds, (n - 1) & 1, dead);
-        // the keys weighted by their decay to the chunk's end (reversed: start)
-#pragma unroll 2
-        for (int u = w_from * 32 + lane; u < w_to * 32; u += 32) {
-          const int row = (u % 512) / 8;
-          const int off = (u / 512) * kLaBlock + row * kTileRow + (u % 8) * 16;
-          uint32_t in[NPI][4], out[NPW][4];
-#pragma unroll
-          for (int q = 0; q < NPI; ++q) {
-            const uint4 y = *reinterpret_cast<const uint4*>(k + q * CF::KB * kLaBlock + off);
-            in[q][0] = y.x, in[q][1] = y.y, in[q][2] = y.z, in[q][3] = y.w;
-          }
-          if constexpr (CF::kBf16) {
-            // k (w0 + w1 + w2): a product of two bf16 is a bf16 and the bf16 that is left,
-            // exactly, so four planes hold 24 bits without leaving bf16 arithmetic
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(fac) + 3 * kLaChunk + row;
-            const uint32_t w0 = w[0], w1 = w[kLaChunk], w2 = w[2 * kLaChunk];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              out[0][e] = mul_bf16x2(in[0][e], w0);
-              out[1][e] = fma_bf16x2(in[0][e], w0, neg_bf16x2(out[0][e]));
-              out[2][e] = mul_bf16x2(in[0][e], w1);
-              out[3][e] = fma_bf16x2(in[0][e], w2, fma_bf16x2(in[0][e], w1, neg_bf16x2(out[2][e])));
-            }
-          } else {
-            const float wj = fac[3 * kLaChunk + row];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint64_t y = from_bf16x2(in[NPI - 1][e]);
-#pragma unroll
-              for (int q = NPI - 2; q >= 0; --q) y = add2(y, from_bf16x2(in[q][e]));  // exact from the smallest
-              uint32_t sp[NPW];
-              split2<NPW>(mul2(y, pair(wj, wj)), sp);
-#pragma unroll
-              for (int q = 0; q < NPW; ++q) out[q][e] = sp[q];
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < NPW; ++q)
-            *reinterpret_cast<uint4*>((q < NPI ? k + q * CF::KB * kLaBlock : smem + CF::kW + (q - NPI) * CF::KB * kLaBlock) +
-                                      off) = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
-        }
-        fence_proxy_async_smem();
-        arrive(b_w);
         arrive(empty_f(rf.i));
         rf.next(), rk.next();
       }
@@ -909,29 +928,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
           la_wait(full_f(rf.i), rf.full(), dead);
           const float decay = fac[CF::kFacFloats - 4];
-          la_wait(STATES ? b_ds : b_o, n & 1, dead);
+          la_wait(b_ds, n & 1, dead);
           tc5_fence_after();
-          float o[2][8];
-          if (!STATES) {
-            float2 f[2];
-#pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2)
-              f[i2] = *reinterpret_cast<const float2*>(fac + 2 * kLaChunk + part * 16 + i2 * 8 + 2 * (lane % 4));
-            uint32_t x1[2][8], x2[2][8];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              tmem_ld_rows16(x1[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO1 + part * 16);
-              tmem_ld_rows16(x2[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO2 + part * 16);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              tmem_wait_ld(x1[e]);
-              tmem_wait_ld(x2[e]);
-#pragma unroll
-              for (int i2 = 0; i2 < 8; ++i2)
-                o[e][i2] = fmaf(__uint_as_float(x2[e][i2]), i2 % 2 ? f[i2 / 4].y : f[i2 / 4].x, __uint_as_float(x1[e][i2]));
-            }
-          }
           const uint64_t decay2 = pair(decay, decay);
           // 16 key indices at a time: the state, the outputs and more would not fit the registers
 #pragma unroll
@@ -944,9 +942,32 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
           tc5_fence_before();
           arrive(b_free);
+          float o[2][8];
+          if (!STATES) {
+            la_wait(b_o, n & 1, dead);
+            tc5_fence_after();
+            uint32_t x1[2][8], x2[2][8];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              tmem_ld_rows16(x1[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO1 + part * 16);
+              tmem_ld_rows16(x2[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO2 + part * 16);
+            }
+            float2 f[2];
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2)
+              f[i2] = *reinterpret_cast<const float2*>(fac + 2 * kLaChunk + part * 16 + i2 * 8 + 2 * (lane % 4));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              tmem_wait_ld(x1[e]);
+              tmem_wait_ld(x2[e]);
+#pragma unroll
+              for (int i2 = 0; i2 < 8; ++i2)
+                o[e][i2] = fmaf(__uint_as_float(x2[e][i2]), i2 % 2 ? f[i2 / 4].y : f[i2 / 4].x, __uint_as_float(x1[e][i2]));
+            }
+            if (cc + 1 < p.last) give_state();
+          }
           arrive(empty_f(rf.i));
           rf.next();
-          if (!STATES && cc + 1 < p.last) give_state();
           if (!STATES && CF::kBf16 && fast) {
             // bf16 rows leave through 512 bytes of shared memory, 8 tokens at a time, as 64
             // bytes of a token together
