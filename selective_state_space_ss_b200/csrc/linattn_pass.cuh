@@ -142,11 +142,13 @@ struct LaCfg {
   static constexpr bool kTwoIssuers = kBf16;
   static constexpr int kLoaders = kTwoIssuers ? 32 : 64;  // loader threads
   static constexpr int kThreads = 896;
+  // Registers a thread of the three kinds of warpgroup: 4 x 88 + 2 x 56 + 40 (fp32, with
+  // all its loads through registers: 4 x 88 + 2 x 48 + 56) = 7 x 72 at launch.
+  static constexpr int kBackRegs = 88, kFrontRegs = kBf16 ? 56 : 48, kAuxRegs = kBf16 ? 40 : 56;
+  static_assert(4 * kBackRegs + 2 * kFrontRegs + kAuxRegs == 7 * 72, "registers of a block");
 };
 constexpr int kLaBackWarps = 16, kLaFrontWarps = 8;
 constexpr int kLaMmaWarp = 24, kLaLoadWarp = 25, kLaMmaOrLoadWarp = 26, kLaDecayWarp = 27;
-// registers a thread of the three kinds of warpgroup: 4 x 88 + 2 x 56 + 40 = 7 x 72 at launch
-constexpr int kLaBackRegs = 88, kLaFrontRegs = 56, kLaAuxRegs = 40;
 
 // Waits of one CTA: when one gives up, the others stop waiting too, and the kernel
 // runs to its end on whatever is there, inside its buffers.  A poll may suspend the
@@ -202,56 +204,70 @@ __device__ __forceinline__ const char* la_row(const LaTensor& x, int64_t b, int6
 
 // One tile of 64 tokens into shared memory: rows from `len` on and columns from `d`
 // on are zero.  bf16 with 16-byte rows: asynchronous copies (the caller waits);
-// everything else through registers.
+// everything else through registers, up to four units at a time, the rows `ahead` tokens on
+// (the next chunk's) asked for in L2 meanwhile.
+template <typename T>
+__device__ __forceinline__ void la_fetch_unit(float (&f)[8], const char* from, bool in, int col, int d, bool vec) {
+  const T* p = reinterpret_cast<const T*>(from);
+  if (sizeof(T) == 4 && vec) {
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 f0 = in ? reinterpret_cast<const float4*>(p)[0] : z;
+    const float4 f1 = in && col + 4 < d ? reinterpret_cast<const float4*>(p)[1] : z;
+    f[0] = f0.x, f[1] = f0.y, f[2] = f0.z, f[3] = f0.w, f[4] = f1.x, f[5] = f1.y, f[6] = f1.z, f[7] = f1.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = in && col + i < d ? to_f32(p[i]) : 0.f;
+  }
+}
 template <typename T, int DP>
-__device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64_t b, int h, int t0,
-                                             int len, int d, bool vec, int tid, int nthreads) {
-  constexpr int B = DP / 64;
+__device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64_t b, int h, int t0, int len, int d,
+                                             bool vec, int ahead, int tid, int nthreads) {
+  constexpr int B = DP / 64, PLANES = sizeof(T) == 2 ? 1 : 3, E = sizeof(T) == 2 ? 1 : 4;
   constexpr int UNITS = kLaChunk * B * 8;
+  const char* base = la_row(x, b, 0, h, sizeof(T));
+  const int64_t step = x.st * (int64_t)sizeof(T);
+  if (sizeof(T) == 2 && vec) {
 #pragma unroll 1
-  for (int u = tid; u < UNITS; u += nthreads) {
-    const int row = u / (B * 8), unit = u % (B * 8), col = unit * 8;
-    const bool in = t0 + row < len && col < d && in_range(t0 + row, len);
-    char* to = dst + (unit / 8) * kLaBlock + tile_unit(row, unit % 8);
-    const char* from = la_row(x, b, in ? t0 + row : 0, h, sizeof(T)) + (in ? col : 0) * (int)sizeof(T);
-    if constexpr (sizeof(T) == 2) {
-      if (vec) {
-        const uint32_t bytes = in ? 16 : 0;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(to)), "l"(from), "r"(bytes)
-                     : "memory");
-      } else {
-        uint32_t w[4];
+    for (int u = tid; u < UNITS; u += nthreads) {
+      const int row = u / (B * 8), unit = u % (B * 8), col = unit * 8;
+      const bool in = t0 + row < len && col < d && in_range(t0 + row, len);
+      const char* from = base + (in ? (t0 + row) * step + col * 2 : 0);
+      const uint32_t bytes = in ? 16 : 0;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                       smem_u32(dst + (unit / 8) * kLaBlock + tile_unit(row, unit % 8))),
+                   "l"(from), "r"(bytes)
+                   : "memory");
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int u = tid; u < UNITS; u += E * nthreads) {
+    float f[E][8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint16_t* p = reinterpret_cast<const uint16_t*>(from) + 2 * i;
-          const uint32_t lo = in && col + 2 * i < d ? p[0] : 0;
-          const uint32_t hi = in && col + 2 * i + 1 < d ? p[1] : 0;
-          w[i] = lo | hi << 16;
-        }
-        *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-      float f[8];
-      const float* p = reinterpret_cast<const float*>(from);
-      if (vec) {
-        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 f0 = in ? reinterpret_cast<const float4*>(p)[0] : z;
-        const float4 f1 = in && col + 4 < d ? reinterpret_cast<const float4*>(p)[1] : z;
-        f[0] = f0.x, f[1] = f0.y, f[2] = f0.z, f[3] = f0.w, f[4] = f1.x, f[5] = f1.y, f[6] = f1.z, f[7] = f1.w;
-      } else {
+    for (int e = 0; e < E; ++e) {
+      const int v = u + e * nthreads, row = v / (B * 8), col = v % (B * 8) * 8;
+      const bool in = t0 + row < len && col < d && in_range(t0 + row, len);
+      const char* from = base + (in ? (t0 + row) * step + col * (int)sizeof(T) : 0);
+      la_fetch_unit<T>(f[e], from, in, col, d, vec);
+      const int next = t0 + row + ahead;
+      if (in && next >= 0 && next < len)
+        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(from + ahead * step));
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = in && col + i < d ? p[i] : 0.f;
-      }
-      uint32_t w[3][4];
+    for (int e = 0; e < E; ++e) {
+      const int v = u + e * nthreads, row = v / (B * 8), unit = v % (B * 8);
+      char* to = dst + (unit / 8) * kLaBlock + tile_unit(row, unit % 8);
+      uint32_t w[PLANES][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t s[3];
-        split2<3>(pair(f[2 * i], f[2 * i + 1]), s);
-        w[0][i] = s[0], w[1][i] = s[1], w[2][i] = s[2];
+        uint32_t s[PLANES];
+        split2<PLANES>(pair(f[e][2 * i], f[e][2 * i + 1]), s);
+#pragma unroll
+        for (int p = 0; p < PLANES; ++p) w[p][i] = s[p];
       }
 #pragma unroll
-      for (int p3 = 0; p3 < 3; ++p3)
-        *reinterpret_cast<uint4*>(to + p3 * B * kLaBlock) = make_uint4(w[p3][0], w[p3][1], w[p3][2], w[p3][3]);
+      for (int p = 0; p < PLANES; ++p)
+        *reinterpret_cast<uint4*>(to + p * B * kLaBlock) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
     }
   }
 }
@@ -526,7 +542,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   };
 
   if (warp >= kLaMmaWarp) {
-    regs_give<kLaAuxRegs>();
+    regs_give<CF::kAuxRegs>();
     if (warp == kLaMmaWarp || (CF::kTwoIssuers && warp == kLaMmaOrLoadWarp)) {
       // ---- MMA issue, by one thread of a warp
       constexpr int kUnits = kLaBlock >> 4;  // a block in descriptor units
@@ -671,7 +687,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             } else {
               __syncwarp();
               if (CF::kLoaders > 32) asm volatile("bar.sync 2, 64;\n" ::: "memory");
-              la_load_tile<T, DP>(smem + at, x, p.b, p.h, t0, p.len, d, a.vec, ltid, CF::kLoaders);
+              la_load_tile<T, DP>(smem + at, x, p.b, p.h, t0, p.len, d, a.vec, a.reverse ? -kLaChunk : kLaChunk, ltid,
+                                  CF::kLoaders);
               if (CF::kBf16 && a.vec) {
                 cp_async_commit();
                 cp_async_wait_all();
@@ -695,7 +712,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
     }
   } else if (warp >= kLaBackWarps) {
     // ---- front: weighted keys and P, a chunk ahead of the back
-    regs_give<kLaFrontRegs>();
+    regs_give<CF::kFrontRegs>();
     // 16 rows of P for each pair of warps, side 0 with every other block of columns
     const int fw = warp % 4, front = warp - kLaBackWarps, side = front / 4, ftid = tid - 32 * kLaBackWarps;
     int n = 0;
@@ -822,7 +839,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
     }
   } else {
     // ---- back: the state and the outputs
-    regs_take<kLaBackRegs>();
+    regs_take<CF::kBackRegs>();
     const int quad = warp % 4, part = warp / 4;  // value lanes; a quarter of the keys and tokens
     if (quad < CF::kQuads) {
       const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
