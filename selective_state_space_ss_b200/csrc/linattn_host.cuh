@@ -305,9 +305,10 @@ ss_status la_share_sum(const float* part, void* out, const int32_t* lengths, con
 template <typename T>
 ss_status la_decay_grad(const LaPassArgs& a, const float* dots_q, const float* dots_k, void* dg, const LaShape& s,
                         cudaStream_t stream) {
-  const int64_t warps = s.bh() * a.anchors;
-  linattn_decay_grad_kernel<T><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(
-      dots_q, dots_k, a.anchor, static_cast<T*>(dg), a.lengths, s.bh(), s.heads, (int)s.seqlen, a.anchors,
+  const int64_t blocks = s.bh() * a.anchors;
+  if (blocks > INT_MAX) return SS_ERR_INVALID_ARG;
+  linattn_decay_grad_kernel<T><<<(unsigned)blocks, kLaGradThreads, 0, stream>>>(
+      dots_q, dots_k, a.anchor, static_cast<T*>(dg), a.lengths, s.heads, (int)s.seqlen, a.anchors,
       a.anchor_chunks * kLaChunk, s.dk <= 64);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }

@@ -866,8 +866,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
       int n = 0;
       for (int i = 0; i < work.pieces; ++i) {
         const LaPiece p = la_piece(a, work, i);
-        const int64_t bh = p.bh;
-        const int b = p.b, h = p.h, len = p.len;
+        const int bh = p.bh, b = p.b, h = p.h, len = p.len;
         const int all_chunks = (len + kLaChunk - 1) / kLaChunk;
         const int step = a.workers > 0 ? 0 : work.worker % a.nseg;
         // 16-byte rows: this lane's part of token lane / 4, in memory and in the stage
@@ -900,7 +899,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
         } else {
           const bool in = a.s_in && !STATES && vi < a.dv;
-          const float* from = a.s_in + bh * a.s_in_head + step * a.s_in_seg + part * KH * a.sk + vi * a.sv;
+          const float* from = a.s_in + (int64_t)bh * a.s_in_head + step * a.s_in_seg + part * KH * a.sk + vi * a.sv;
 #pragma unroll
           for (int c = 0; c < KH; c += 2) {
             const int kk = part * KH + c;
@@ -919,20 +918,11 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           const int chunk = a.reverse ? p.last - 1 - (cc - p.first) : cc, t0 = chunk * kLaChunk;
           const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + rf.i * CF::kFacFloats;
           const int tw = t0 + part * 16;  // this warp's tokens
-          uint4 xrow[2];
-          if (fast_x) {
-            const char* xp = la_row(a.x, b, tw + tok, h, 2) + c8 * 2;
-#pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2) {
-              xrow[i2] = make_uint4(0, 0, 0, 0);
-              if (tw + i2 * 8 + tok < len && c8 < a.dv) xrow[i2] = *reinterpret_cast<const uint4*>(xp + i2 * 16 * a.x.st);
-            }
-          }
           const bool anchor_here = DOTS && ((chunk + 1) % a.anchor_chunks == 0 || chunk == all_chunks - 1);
           if (DOTS && a.reverse && anchor_here) {
             // <R, S> behind this chunk: R is the state here, S the forward pass's
             float sum = 0.f;
-            const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
+            const int64_t an = (int64_t)bh * a.anchors + chunk / a.anchor_chunks;
             const float* from = a.dump + (an * 16 + warp) * (KH * 32);
 #pragma unroll
             for (int c = 0; c < KH; c += 4) {
@@ -1004,7 +994,21 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           if (DOTS) {
             float sum[4];
             if (fast_x) {
-              // the rows of x the other way through the stage, into the order of o
+              // the rows of x the other way through the stage, into the order of o; the next
+              // chunk's are asked for in L2
+              const char* xp = la_row(a.x, b, tw + tok, h, 2) + c8 * 2;
+              const int64_t xs = 16 * a.x.st;
+              uint4 xrow[2];
+#pragma unroll
+              for (int i2 = 0; i2 < 2; ++i2) {
+                xrow[i2] = make_uint4(0, 0, 0, 0);
+                if (tw + i2 * 8 + tok < len && c8 < a.dv) xrow[i2] = *reinterpret_cast<const uint4*>(xp + i2 * xs);
+              }
+              const int ahead = a.reverse ? -8 : 8;  // in steps of 8 tokens
+              if (cc + 1 < p.last && c8 < a.dv && tw + ahead * 8 + 8 + tok < len) {
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(xp + ahead * xs));
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(xp + (ahead + 1) * xs));
+              }
 #pragma unroll
               for (int i2 = 0; i2 < 2; ++i2) {
                 *reinterpret_cast<uint4*>(mine) = xrow[i2];
@@ -1030,12 +1034,12 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int t = tw + 2 * lane + 8 * (e / 2) + e % 2;
-                if (t < len) a.dots[(bh * a.seqlen + t) * 4 + quad] = sum[e];
+                if (t < len) a.dots[((int64_t)bh * a.seqlen + t) * 4 + quad] = sum[e];
               }
             }
           }
           if (DOTS && !a.reverse && anchor_here) {
-            const int64_t an = bh * a.anchors + chunk / a.anchor_chunks;
+            const int64_t an = (int64_t)bh * a.anchors + chunk / a.anchor_chunks;
             float* to = a.dump + (an * 16 + warp) * (KH * 32);
 #pragma unroll
             for (int c = 0; c < KH; c += 4)
@@ -1054,7 +1058,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           if (lane == 0)
             asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(a.flags + 1 + work.worker * 16 + warp), "r"(1u) : "memory");
         } else if (a.s_out && (STATES || step == a.nseg - 1) && vi < a.dv) {
-          float* to = a.s_out + bh * a.s_out_head + step * a.s_out_seg + part * KH * a.sk + vi * a.sv;
+          float* to = a.s_out + (int64_t)bh * a.s_out_head + step * a.s_out_seg + part * KH * a.sk + vi * a.sv;
 #pragma unroll
           for (int c = 0; c < KH; ++c) {
             if (part * KH + c < a.dk) *to = c % 2 ? pair_hi(S[c / 2]) : pair_lo(S[c / 2]);
@@ -1120,49 +1124,58 @@ __global__ void linattn_share_kernel(const float* part, T* out, const int* lengt
 // dg_t = sum_{s = t..e} (q_s . dq_s - k_s . dk_s) + <R_e, S_e>, e the next anchor at or
 // behind t, R_e what the later tokens send back to the state S_e.  Each anchor's
 // sums start anew, so that what cancels in the differences is no longer than the
-// stretch between two.  One warp a stretch, from its end; sums in fp64.  Keys of at
-// most 64 fill two lane quadrants of the partial products, wider ones four.
+// stretch between two.  One block a stretch, the same number of tokens a thread; sums
+// in fp64.  Keys of at most 64 fill two lane quadrants of the partial products, wider
+// ones four.
+constexpr int kLaGradThreads = 256;
 template <typename T>
-__global__ void linattn_decay_grad_kernel(const float* dots_q, const float* dots_k, const float* anchor, T* out,
-                                          const int* lengths, int64_t bhs, int heads, int seqlen, int anchors,
-                                          int anchor_tokens, bool two_quads) {
-  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
-  const int lane = threadIdx.x % 32;
-  const int64_t bh = w / anchors;
-  const int an = (int)(w % anchors);
-  if (bh >= bhs) return;
-  const int64_t b = bh / heads;
-  const int h = (int)(bh % heads);
+__global__ void __launch_bounds__(kLaGradThreads)
+linattn_decay_grad_kernel(const float* dots_q, const float* dots_k, const float* anchor, T* out, const int* lengths,
+                          int heads, int seqlen, int anchors, int anchor_tokens, bool two_quads) {
+  __shared__ double warp_sum[kLaGradThreads / 32];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int bh = blockIdx.x / anchors, an = blockIdx.x % anchors;
+  const int b = bh / heads, h = bh % heads;
   int len = lengths ? lengths[b] : seqlen;
   len = len < 0 ? 0 : len < seqlen ? len : seqlen;
   const int64_t begin = (int64_t)an * anchor_tokens;
   if (begin >= len) return;
   const int end = begin + anchor_tokens < len ? (int)(begin + anchor_tokens) : len;
-  double carry = 0.0;
-  for (int i = 0; i < 16; ++i)
-    if (!two_quads || i % 4 < 2) carry += anchor[(bh * anchors + an) * 16 + i];
-  for (int hi = end; hi > begin; hi -= 32) {
-    const int t = hi - 1 - lane;  // lane 0 the latest
-    double x = 0.0;
-    if (t >= begin) {
-      const float4 q = reinterpret_cast<const float4*>(dots_q)[bh * seqlen + t];
-      const float4 k = reinterpret_cast<const float4*>(dots_k)[bh * seqlen + t];
-      x = ((double)q.x + q.y) - ((double)k.x + k.y);
-      if (!two_quads) x += ((double)q.z + q.w) - ((double)k.z + k.w);
-    }
+  // thread 0 has the latest tokens; each goes back from its own latest
+  const int per = (anchor_tokens + kLaGradThreads - 1) / kLaGradThreads;
+  const int last = end - 1 - tid * per;
+  const float4* rq = reinterpret_cast<const float4*>(dots_q) + (int64_t)bh * seqlen;
+  const float4* rk = reinterpret_cast<const float4*>(dots_k) + (int64_t)bh * seqlen;
+  auto term = [&](int t) {
+    const float4 q = rq[t], k = rk[t];
+    double x = ((double)q.x + q.y) - ((double)k.x + k.y);
+    if (!two_quads) x += ((double)q.z + q.w) - ((double)k.z + k.w);
+    return x;
+  };
+  double mine = 0.0;
+#pragma unroll 4
+  for (int i = 0; i < per; ++i)
+    if (last - i >= begin) mine += term(last - i);
+  double upto = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const double up = __shfl_up_sync(kFullMask, x, o);
-      if (lane >= o) x += up;
-    }
-    x += carry;
-    if (t >= begin) {
-      const float y = (float)x;
-      T* to = out + (b * seqlen + t) * heads + h;
-      if constexpr (sizeof(T) == 2) *to = __float2bfloat16_rn(y);
-      else *to = y;
-    }
-    carry = __shfl_sync(kFullMask, x, 31);
+  for (int o = 1; o < 32; o *= 2) {
+    const double up = __shfl_up_sync(kFullMask, upto, o);
+    if (lane >= o) upto += up;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  double x = upto - mine;
+  for (int i = 0; i < warp; ++i) x += warp_sum[i];
+  for (int i = 0; i < 16; ++i)
+    if (!two_quads || i % 4 < 2) x += anchor[((int64_t)bh * anchors + an) * 16 + i];
+#pragma unroll 4
+  for (int i = 0; i < per; ++i) {
+    const int t = last - i;
+    if (t < begin) break;
+    x += term(t);
+    T* to = out + ((int64_t)b * seqlen + t) * heads + h;
+    if constexpr (sizeof(T) == 2) *to = __float2bfloat16_rn((float)x);
+    else *to = (float)x;
   }
 }
 
