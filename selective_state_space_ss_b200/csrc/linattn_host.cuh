@@ -58,16 +58,19 @@ struct LaSegs {
 // chunks of a head each.  With more heads than SMs a last wave that is not full is
 // avoided by workers, one an SM, with an equal share of the chunks; each hands at
 // most one state on.  With fewer, a head is cut into s segments: a first launch forms
-// the states of s - 1 of them (no queries, scores or outputs: about half a chunk's
-// time), a second joins them and a third runs all segments at once.  In units of a
-// chunk's time a CTA costs about 3 to start, the two extra launches about 6.
+// the states of s - 1 of them (no queries, scores or outputs: 0.7 of a chunk's time,
+// measured with 64 x 64 heads, 1.46 us to 2.08), a second joins them and a third runs
+// all segments at once.  A CTA costs about 10 us to start, the two extra launches about
+// as much: in units of a chunk's time 4 where a chunk takes 2.5 us (bf16), 1.3 where it
+// takes 8 (fp32).
 LaSegs la_plan(const LaShape& s) {
   const int64_t chunks = (s.seqlen + kLaChunk - 1) / kLaChunk, bh = s.bh();
   const int64_t slots = device_sms() > 0 ? device_sms() : 148;
+  const double start = s.bf16 ? 4.0 : 1.3, extra = start;
   if (bh > slots) {
     const int64_t waves = (bh + slots - 1) / slots;
     const double share = (double)bh * chunks / slots;
-    if (waves * (chunks + 3.0) > share + 8.0) return LaSegs{1, (int)chunks, (int)slots};
+    if (waves * (chunks + start) > share + 2 * start) return LaSegs{1, (int)chunks, (int)slots};
     return LaSegs{1, (int)chunks, 0};
   }
   double best = 0;
@@ -75,8 +78,8 @@ LaSegs la_plan(const LaShape& s) {
   for (int64_t n = 1; n <= 64 && n <= chunks; ++n) {
     const int64_t per = (chunks + n - 1) / n;
     if ((chunks + per - 1) / per != n) continue;
-    double cost = (double)((bh * n + slots - 1) / slots) * (per + 3.0);
-    if (n > 1) cost += (double)((bh * (n - 1) + slots - 1) / slots) * (0.5 * per + 3.0) + 6.0;
+    double cost = (double)((bh * n + slots - 1) / slots) * (per + start);
+    if (n > 1) cost += (double)((bh * (n - 1) + slots - 1) / slots) * (0.7 * per + start) + extra;
     if (n == 1 || cost < best) best = cost, at = n;
   }
   return LaSegs{(int)at, (int)((chunks + at - 1) / at), 0};
@@ -475,7 +478,7 @@ ss_status state_store8_impl(const PoolArgs& a, cudaStream_t stream) {
 
 template <int VEC>
 ss_status pool_load(const PoolArgs& a, cudaStream_t stream) {
-  const int64_t blocks = (a.rows * a.width / VEC + kPoolThreads - 1) / kPoolThreads;
+  const int64_t per = 4 * kPoolThreads, blocks = (a.rows * a.width / VEC + per - 1) / per;
   state_load8_kernel<VEC><<<dim3((unsigned)blocks, (unsigned)a.batch), kPoolThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
