@@ -476,17 +476,26 @@ ss_status state_store8_impl(const PoolArgs& a, cudaStream_t stream) {
   return pool_store<32, 1, 32>(a, stream);
 }
 
-template <int VEC>
+template <int LANES, int REGS, int ROWS>
 ss_status pool_load(const PoolArgs& a, cudaStream_t stream) {
-  const int64_t per = 4 * kPoolThreads, blocks = (a.rows * a.width / VEC + per - 1) / per;
-  state_load8_kernel<VEC><<<dim3((unsigned)blocks, (unsigned)a.batch), kPoolThreads, 0, stream>>>(a);
+  const int64_t per = kPoolThreads / LANES * ROWS, blocks = (a.rows + per - 1) / per;
+  state_load8_kernel<LANES, REGS, ROWS><<<dim3((unsigned)blocks, (unsigned)a.batch), kPoolThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 ss_status state_load8_impl(const PoolArgs& a, cudaStream_t stream) {
-  if (a.width % 16 == 0 && aligned(a.state, 16) && aligned(a.codes, 16)) return pool_load<16>(a, stream);
-  if (a.width % 4 == 0 && aligned(a.state, 16) && aligned(a.codes, 4)) return pool_load<4>(a, stream);
-  return pool_load<1>(a, stream);
+  if (a.width % 4 == 0 && aligned(a.state, 16) && aligned(a.codes, 4)) {
+    if (a.width <= 16) return pool_load<4, 1, 8>(a, stream);
+    if (a.width <= 32) return pool_load<8, 1, 8>(a, stream);
+    if (a.width <= 64) return pool_load<16, 1, 8>(a, stream);
+    if (a.width <= 128) return pool_load<32, 1, 8>(a, stream);
+    if (a.width <= 256) return pool_load<32, 2, 4>(a, stream);
+    if (a.width <= 512) return pool_load<32, 4, 2>(a, stream);
+    return pool_load<32, 8, 1>(a, stream);
+  }
+  const int64_t blocks = (a.rows * a.width + kPoolThreads - 1) / kPoolThreads;
+  state_load8_plain_kernel<<<dim3((unsigned)blocks, (unsigned)a.batch), kPoolThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 }  // namespace

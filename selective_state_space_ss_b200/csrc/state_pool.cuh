@@ -20,23 +20,26 @@ struct PoolArgs {
   int width;
 };
 
-// x / scale to the nearest integer, ties to even, of the exact quotient.  The fp32
-// product lands within one of it; the remainder x - n scale is exact (both terms
-// are multiples of the smaller one's last place and it has fewer than 24 bits), so
-// comparing it with half a scale corrects the step.
-__device__ __forceinline__ int pool_code(float x, float scale, float inv) {
-  float n = rintf(x * inv);
-  const float r = fmaf(-n, scale, x), half = 0.5f * scale;
-  const bool odd = ((int)n & 1) != 0;
-  if (r > half || (r == half && odd)) n += 1.f;
-  else if (r < -half || (r == -half && odd)) n -= 1.f;
-  return (int)n;
+// x / scale to the nearest integer, ties to even, of the exact quotient, |x / scale| at
+// most 127: the low byte of the result (it is 1.5 * 2^23 more than the code, so that its
+// last bits are the code's).  The fp32 product lands within one of it; the remainder
+// x - n scale is exact (both terms are multiples of the smaller one's last place and it
+// has fewer than 24 bits), and where it is not below half a scale it says what is nearer.
+__device__ __forceinline__ uint32_t pool_code(float x, float scale, float half, float inv) {
+  float t = fmaf(x, inv, 12582912.f);
+  const float n = t - 12582912.f, r = fmaf(-n, scale, x);
+  if (fabsf(r) >= half) {
+    const bool odd = ((int)n & 1) != 0;
+    if (r > half || (r == half && odd)) t += 1.f;
+    else if (r < -half || (r == -half && odd)) t -= 1.f;
+  }
+  return __float_as_uint(t);
 }
 
-// The row's scale from its largest magnitude (NaN where the row is not finite).
-__device__ __forceinline__ float pool_scale(float top, bool finite) {
-  const float s = top * (1.f / 127.f);
-  return !finite ? __int_as_float(0x7fffffff) : s < 1.17549435e-38f ? 0.f : s;
+// The row's scale from its largest magnitude's bits (NaN where the row is not finite).
+__device__ __forceinline__ float pool_scale(uint32_t top) {
+  const float s = __uint_as_float(top) * (1.f / 127.f);
+  return top >= 0x7f800000u ? __int_as_float(0x7fffffff) : s < 1.17549435e-38f ? 0.f : s;
 }
 
 // The pool slot of sequence b, or -1: outside the pool, or (KEEP_LAST) one that a
@@ -62,8 +65,7 @@ __global__ void __launch_bounds__(kPoolThreads) state_store8_kernel(const __grid
   const int64_t row = (int64_t)blockIdx.x * (kPoolThreads / LANES) + threadIdx.x / LANES;
   const bool in = row < a.rows;
   const float* from = a.state + ((int64_t)b * a.rows + (in ? row : 0)) * a.width;
-  float x[REGS][VEC], top = 0.f;
-  bool finite = true;
+  float x[REGS][VEC];
 #pragma unroll
   for (int i = 0; i < REGS; ++i) {
     const int c = (i * LANES + lane) * VEC;
@@ -76,20 +78,14 @@ __global__ void __launch_bounds__(kPoolThreads) state_store8_kernel(const __grid
   }
   const int64_t slot = pool_slot<true>(a, b);
   if (slot < 0) return;
+  uint32_t top = 0;  // magnitudes as bits: those of infinity and NaN are the largest
 #pragma unroll
   for (int i = 0; i < REGS; ++i)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float m = fabsf(x[i][e]);
-      finite = finite && m <= 3.402823466e38f;
-      top = fmaxf(top, m);
-    }
+    for (int e = 0; e < VEC; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7fffffffu);
 #pragma unroll
-  for (int o = LANES / 2; o >= 1; o /= 2) {
-    top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-    finite = __shfl_xor_sync(kFullMask, (int)finite, o) && finite;
-  }
-  const float scale = pool_scale(top, finite);
+  for (int o = LANES / 2; o >= 1; o /= 2) top = max(top, __shfl_xor_sync(kFullMask, top, o));
+  const float scale = pool_scale(top), half = 0.5f * scale;
   const bool some = scale > 0.f;
   const float inv = some ? __frcp_rn(scale) : 0.f;
   if (!in) return;
@@ -98,65 +94,63 @@ __global__ void __launch_bounds__(kPoolThreads) state_store8_kernel(const __grid
   for (int i = 0; i < REGS; ++i) {
     const int c = (i * LANES + lane) * VEC;
     if (c >= a.width) continue;
-    int n[VEC];
+    uint32_t n[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) n[e] = some ? pool_code(x[i][e], scale, inv) : 0;
+    for (int e = 0; e < VEC; ++e) n[e] = some ? pool_code(x[i][e], scale, half, inv) : 0;
     if constexpr (VEC == 4)
-      *reinterpret_cast<char4*>(to + c) = make_char4((signed char)n[0], (signed char)n[1], (signed char)n[2], (signed char)n[3]);
+      *reinterpret_cast<uint32_t*>(to + c) = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
     else
       to[c] = (int8_t)n[0];
   }
   if (lane == 0) a.scales[slot * a.rows + row] = scale;
 }
 
-// VEC codes an access (16, 4 or 1; width a multiple of it), four accesses a thread at
-// once: the pool's latency comes twice, slot and codes, so more is kept in flight.
-template <int VEC>
+// LANES lanes a row, 4 codes an access, REGS accesses a lane and ROWS rows at once:
+// LANES * 4 * REGS >= width.  A warp's stores are 512 bytes together.
+template <int LANES, int REGS, int ROWS>
 __global__ void __launch_bounds__(kPoolThreads) state_load8_kernel(const __grid_constant__ PoolArgs a) {
-  constexpr int W = VEC == 1 ? 1 : VEC / 4, E = 4;
+  constexpr int PER = kPoolThreads / LANES;
+  const int b = blockIdx.y, lane = threadIdx.x % LANES;
+  const int64_t slot = pool_slot<false>(a, b);
+  const int64_t row0 = (int64_t)blockIdx.x * (PER * ROWS) + threadIdx.x / LANES;
+  uint32_t w[ROWS][REGS];
+  float scale[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int64_t row = row0 + r * PER;
+    const bool in = slot >= 0 && row < a.rows;
+    scale[r] = in ? a.scales[slot * a.rows + row] : 0.f;
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) {
+      const int c = (i * LANES + lane) * 4;
+      w[r][i] = in && c < a.width ? __ldcs(reinterpret_cast<const uint32_t*>(a.codes + (slot * a.rows + row) * a.width + c)) : 0;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int64_t row = row0 + r * PER;
+    if (row >= a.rows) continue;
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) {
+      const int c = (i * LANES + lane) * 4;
+      if (c >= a.width) continue;
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(w[r][i] >> (8 * e)) * scale[r];
+      __stcs(reinterpret_cast<float4*>(a.state + ((int64_t)b * a.rows + row) * a.width + c), make_float4(f[0], f[1], f[2], f[3]));
+    }
+  }
+}
+
+// Any width and alignment, code by code.
+__global__ void __launch_bounds__(kPoolThreads) state_load8_plain_kernel(const __grid_constant__ PoolArgs a) {
   const int b = blockIdx.y;
   const int64_t slot = pool_slot<false>(a, b);
-  const uint32_t n = (uint32_t)(a.rows * a.width / VEC), per_row = (uint32_t)(a.width / VEC);
-  const int8_t* codes = a.codes + slot * a.rows * a.width;
-  const float* scales = a.scales + slot * a.rows;
-  float* out = a.state + (int64_t)b * a.rows * a.width;
-  const uint32_t i0 = blockIdx.x * (kPoolThreads * E) + threadIdx.x;
-  uint32_t w[E][W];
-  float scale[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint32_t i = i0 + e * kPoolThreads;
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[e][j] = 0;
-    scale[e] = 0.f;
-    if (slot >= 0 && i < n) {
-      scale[e] = scales[i / per_row];
-      if constexpr (VEC == 16) {
-        const uint4 y = __ldcs(reinterpret_cast<const uint4*>(codes) + i);
-        w[e][0] = y.x, w[e][1] = y.y, w[e][2] = y.z, w[e][3] = y.w;
-      } else if constexpr (VEC == 4) {
-        w[e][0] = reinterpret_cast<const uint32_t*>(codes)[i];
-      } else {
-        w[e][0] = (uint8_t)codes[i];
-      }
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint32_t i = i0 + e * kPoolThreads;
-    if (i >= n) continue;
-    if constexpr (VEC == 1) {
-      out[i] = (float)(int8_t)w[e][0] * scale[e];
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        float f[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) f[c] = (float)(int8_t)(w[e][j] >> (8 * c)) * scale[e];
-        __stcs(reinterpret_cast<float4*>(out) + (int64_t)i * W + j, make_float4(f[0], f[1], f[2], f[3]));
-      }
-    }
-  }
+  const uint32_t n = (uint32_t)(a.rows * a.width), i = blockIdx.x * kPoolThreads + threadIdx.x;
+  if (i >= n) return;
+  float y = 0.f;
+  if (slot >= 0) y = (float)a.codes[slot * a.rows * a.width + i] * a.scales[slot * a.rows + i / (uint32_t)a.width];
+  a.state[(int64_t)b * a.rows * a.width + i] = y;
 }
 
 }  // namespace ssscan
