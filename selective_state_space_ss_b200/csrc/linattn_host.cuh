@@ -146,7 +146,7 @@ bool la_map(CUtensorMap* m, const LaTensor& x, int64_t batch, int64_t seqlen, in
 
 template <typename T, int KD, int VD, LaMode MODE>
 ss_status la_launch(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream) {
-  using CF = LaCfg<T, KD, VD>;
+  using CF = LaCfg<T, KD, VD, MODE>;
   struct Tag : CF {};
   if (once_per_device<Tag>([] {
         return cudaFuncSetAttribute(linattn_pass_kernel<T, KD, VD, MODE>,

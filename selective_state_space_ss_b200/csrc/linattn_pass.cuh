@@ -105,7 +105,12 @@ struct LaMaps {
   CUtensorMap q, k, v;
 };
 
-template <typename T, int KD, int VD>
+// What a launch does: outputs and states; the states alone (the sequence's segments, each
+// from zero, all at once); outputs and states with the products that a decay's gradient
+// is made of (of each output row with x, of states at anchors).
+enum LaMode { kLaOutputs, kLaStates, kLaProducts };
+
+template <typename T, int KD, int VD, LaMode MODE = kLaOutputs>
 struct LaCfg {
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int NPI = kBf16 ? 1 : 3;  // planes of the inputs
@@ -116,6 +121,9 @@ struct LaCfg {
   // weighted keys' first planes replace it in place), a query tile until S Q is.
   static constexpr int RK = kBf16 ? 3 : 2, RQ = kBf16 ? 3 : 1, RV = kBf16 ? (KB == 2 && VB == 2 ? 2 : 3) : 1;
   static constexpr int RP = kBf16 ? 2 : 1;   // P
+  // The weighted keys' further planes: two places, or one that is filled and used in halves.
+  // (fp32 has all three planes in the key tile.)
+  static constexpr int RW = kBf16 && KB == 2 ? 1 : 2;
   static constexpr int RF = 4;               // decays
   static constexpr int kRing = 4;
   static_assert(RK <= kRing && RV <= kRing && RQ <= kRing && RF <= kRing, "barriers of a ring");
@@ -123,15 +131,19 @@ struct LaCfg {
   static constexpr int kQ = 0, kK = RQ * kTileK, kV = kK + RK * kTileK, kP = kV + RV * kTileV;
   static constexpr int kW = kP + RP * NPX * kLaBlock;
   static constexpr int kFacFloats = (kBf16 ? 6 : 4) * kLaChunk + 4;
-  static constexpr int kFac = kW + kTileW;
+  static constexpr int kFac = kW + RW * kTileW;
   static constexpr int kStage = kFac + (RF * kFacFloats * 4 + 127) / 128 * 128;  // 512 bytes a back warp
   static constexpr int kBars = kStage + (kBf16 ? 16 * 512 : 0);
   static constexpr int kSmem = kBars + 12 * kRing * 8 + 16;
   // tensor memory columns
-  static constexpr int cDS = 0, cSP = KD, cO1 = cSP + NPX * KD / 2, cO2 = cO1 + 64, cQK = cO2 + 64;
+  // (two increments where there is room: the next one need not wait until the back has
+  // read the last)
+  static constexpr int ND = KD == 64 || MODE == kLaStates ? 2 : 1;
+  static constexpr int cDS = 0, cSP = ND * KD, cO1 = cSP + NPX * KD / 2, cO2 = cO1 + 64, cQK = cO2 + 64;
   static constexpr int kAhead = kBf16 ? 2 : 1;  // chunks that scores run ahead, one place for each
-  static constexpr int kCols = cQK + 64 * kAhead <= 256 ? 256 : 512;
-  static_assert(cQK + 64 * kAhead <= 512, "tensor memory");
+  static constexpr int kUsed = MODE == kLaStates ? ND * KD : cQK + 64 * kAhead;
+  static constexpr int kCols = kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr int kQuads = VD / 32;        // lane quadrants that hold values
   static constexpr int kHolders = 4 * kQuads;   // back warps at work
@@ -273,13 +285,18 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
 }
 
 // A lane's two log decays of a chunk as they are stored, zero behind the row's end.
+// Those of `ahead` tokens on are asked for in L2: a chunk may take less than a load.
 template <typename T>
-__device__ __forceinline__ void la_fetch_decays(T (&x)[2], const LaPassArgs& a, int b, int h, int t0, int len, int lane) {
+__device__ __forceinline__ void la_fetch_decays(T (&x)[2], const LaPassArgs& a, int b, int h, int t0, int len, int ahead,
+                                                int lane) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = t0 + 2 * lane + i;
     x[i] = zero_elem<T>();
-    if (t < len && in_range(t, len)) x[i] = *reinterpret_cast<const T*>(la_row(a.g, b, t, h, sizeof(T)));
+    const char* from = la_row(a.g, b, t, h, sizeof(T));
+    if (t < len && in_range(t, len)) x[i] = *reinterpret_cast<const T*>(from);
+    if (t + ahead >= 0 && t + ahead < len)
+      asm volatile("prefetch.global.L2 [%0];\n" ::"l"(from + ahead * a.g.st * (int64_t)sizeof(T)));
   }
 }
 
@@ -463,15 +480,10 @@ __device__ __forceinline__ LaPiece la_piece(const LaPassArgs& a, const LaWork& w
   return p;
 }
 
-// What a launch does: outputs and states; the states alone (the sequence's segments, each
-// from zero, all at once); outputs and states with the products that a decay's gradient
-// is made of (of each output row with x, of states at anchors).
-enum LaMode { kLaOutputs, kLaStates, kLaProducts };
-
 template <typename T, int KD, int VD, LaMode MODE>
-__global__ void __launch_bounds__(LaCfg<T, KD, VD>::kThreads, 1)
+__global__ void __launch_bounds__(LaCfg<T, KD, VD, MODE>::kThreads, 1)
 linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant__ LaMaps maps) {
-  using CF = LaCfg<T, KD, VD>;
+  using CF = LaCfg<T, KD, VD, MODE>;
   constexpr int NPI = CF::NPI, NPX = CF::NPX, NPW = CF::NPW;
   constexpr bool STATES = MODE == kLaStates, DOTS = MODE == kLaProducts;
   extern __shared__ __align__(1024) char smem[];
@@ -490,10 +502,10 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
   const auto b_p = [&](int i) { return ring_bar(8, 2 + i); };  // P is there
   const auto b_w = [&](int i) { return ring_bar(11, i); };  // half of the weighted keys is there
   const uint32_t b_half = ring_bar(10, 0); // the first half of them was used
-  const uint32_t b_ds = ring_bar(10, 1);   // the state's increment is there
+  const auto b_ds = [&](int i) { return ring_bar(11, 2 + i); };  // the state's increment is there
   const auto b_p_free = [&](int i) { return ring_bar(10, 2 + i); };  // P was used
   const uint32_t b_o = ring_bar(9, 0);     // P V and S Q are there
-  const uint32_t b_free = ring_bar(9, 1);  // the back warps have read the increment
+  const auto b_free = [&](int i) { return ring_bar(i ? 10 : 9, 1); };  // the back warps have read the increment
   const uint32_t b_s = ring_bar(9, 2);     // the state's planes are there, and the outputs before were read
   const uint32_t b_end = ring_bar(9, 3);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + 12 * CF::kRing * 8);
@@ -519,9 +531,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
     la_init(b_half, 1);
     la_init(b_p_free(0), 1);
     la_init(b_p_free(1), 1);
-    la_init(b_ds, 1);
+    for (int i = 0; i < 2; ++i) la_init(b_ds(i), 1), la_init(b_free(i), CF::kHolders);
     la_init(b_o, 1);
-    la_init(b_free, CF::kHolders);
     la_init(b_s, CF::kHolders);
     la_init(b_end, 1);
     fence_mbar_init();
@@ -582,30 +593,34 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         if (states) {
           // planes of the weighted keys: in the key tile's place, then in one of their own
           const uint32_t w0 = tile_desc(base + CF::kK + rk.i * CF::kTileK, kLaBlock);
-          const uint32_t w1 = tile_desc(base + CF::kW, kLaBlock);
-          if (n > 0) la_wait(b_free, (n - 1) & 1, dead);
-          // dS^T = V^T (w . K), 32 tokens at a time: the front makes the next chunk's first
-          // half while the second is at work
-          const auto half = [&](int first) {
-            la_products<NPI, NPW, kLaChunk / 32>([&](int pa, int pb, int i, bool add) {
+          const uint32_t w1 = tile_desc(base + CF::kW + (n % CF::RW) * CF::kTileW, kLaBlock);
+          const int inc = n % CF::ND;
+          if (n >= CF::ND) la_wait(b_free(inc), (n / CF::ND - 1) & 1, dead);
+          // dS^T = V^T (w . K), with one place for the keys 32 tokens at a time: the front makes
+          // the next chunk's first half while the second is at work
+          const auto tokens = [&](auto steps, int first) {
+            la_products<NPI, NPW, decltype(steps)::value>([&](int pa, int pb, int i, bool add) {
               const int off = (first + i) * (16 * kTileRow >> 4);
               const uint32_t w = pb < NPI ? w0 + pb * CF::KB * kUnits : w1 + (pb - NPI) * CF::KB * kUnits;
-              mma_ss(tmem + CF::cDS, v + pa * CF::VB * kUnits + off, w + off, mma_idesc(128, KD, true, true),
+              mma_ss(tmem + CF::cDS + inc * KD, v + pa * CF::VB * kUnits + off, w + off, mma_idesc(128, KD, true, true),
                      add || first > 0);
             });
           };
-          la_wait(b_w(0), n & 1, dead);
+          la_wait(b_w(CF::RW == 2 ? n % 2 : 0), (CF::RW == 2 ? n / 2 : n) & 1, dead);
           tc5_fence_after();
-          if (leader) {
-            half(0);
-            mma_commit(b_half);
+          if (CF::RW == 1) {
+            if (leader) {
+              tokens(LaWidth<kLaChunk / 32>{}, 0);
+              mma_commit(b_half);
+            }
+            __syncwarp();
+            la_wait(b_w(1), n & 1, dead);
+            tc5_fence_after();
           }
-          __syncwarp();
-          la_wait(b_w(1), n & 1, dead);
-          tc5_fence_after();
           if (leader) {
-            half(2);
-            mma_commit(b_ds);
+            if (CF::RW == 1) tokens(LaWidth<kLaChunk / 32>{}, 2);
+            else tokens(LaWidth<kLaChunk / 16>{}, 0);
+            mma_commit(b_ds(inc));
             mma_commit(empty_v(rv.i));
             mma_commit(empty_k(rk.i));
           }
@@ -648,10 +663,11 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         double sum = 0.0;
         auto place = [&](int c) { return (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk; };
         T next[2];
-        if (p.first < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(p.first), p.len, lane);
+        const int ahead = (a.reverse ? -4 : 4) * kLaChunk;
+        if (p.first < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(p.first), p.len, ahead, lane);
         for (int c = p.first; c < p.last; ++c) {
           const float x0 = to_f32(next[0]), x1 = to_f32(next[1]);
-          if (c + 1 < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(c + 1), p.len, lane);
+          if (c + 1 < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(c + 1), p.len, ahead, lane);
           if (rf.used()) la_wait(empty_f(rf.i), rf.empty(), dead);
           const int64_t whole = la_decays<CF::kBf16>(reinterpret_cast<float*>(smem + CF::kFac) + rf.i * CF::kFacFloats, x0,
                                                      x1, a.reverse, a.scale_o, a.scale_w, lane);
@@ -731,12 +747,19 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         char* k = smem + CF::kK + rk.i * CF::kTileK;
         la_wait(full_f(rf.i), rf.full(), dead);
         la_wait(full_k(rk.i), rk.full(), dead);
-        // the keys weighted by their decay to the chunk's end (reversed: start), 32 tokens at
-        // a time, each half when the last chunk's was used (and these keys as they are: b_qk)
+        // the keys weighted by their decay to the chunk's end (reversed: start): in the place
+        // of the chunk before last, or half by half in that of the last (and when these keys
+        // as they are were used: b_qk).  (With one increment a barrier tells only the last
+        // chunk's, so that is waited for.)
         if (!STATES) la_wait(b_qk(n % CF::kAhead), (n / CF::kAhead) & 1, dead);
-#pragma unroll 1
+        if (CF::RW == 2 && n >= CF::ND) la_wait(b_ds(n % CF::ND), (n / CF::ND - 1) & 1, dead);
+        char* wk = smem + CF::kW + (n % CF::RW) * CF::kTileW;
+#pragma unroll CF::RW
         for (int half = 0; half < 2; ++half) {
-          if (n > 0) la_wait(half ? b_ds : b_half, (n - 1) & 1, dead);
+          if (CF::RW == 1 && n > 0) {
+            if (half) la_wait(b_ds((n - 1) % CF::ND), ((n - 1) / CF::ND) & 1, dead);
+            else la_wait(b_half, (n - 1) & 1, dead);
+          }
 #pragma unroll
           for (int st = front; st < CF::KB * 8; st += kLaFrontWarps) {
             const int row = half * 32 + (st % 8) * 4 + lane / 8;
@@ -774,11 +797,17 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             }
 #pragma unroll
             for (int q = 0; q < NPW; ++q)
-              *reinterpret_cast<uint4*>((q < NPI ? k + q * CF::KB * kLaBlock : smem + CF::kW + (q - NPI) * CF::KB * kLaBlock) +
+              *reinterpret_cast<uint4*>((q < NPI ? k + q * CF::KB * kLaBlock : wk + (q - NPI) * CF::KB * kLaBlock) +
                                         off) = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
           }
+          if (CF::RW == 1) {
+            fence_proxy_async_smem();
+            arrive(b_w(half));
+          }
+        }
+        if (CF::RW == 2) {
           fence_proxy_async_smem();
-          arrive(b_w(half));
+          arrive(b_w(n % 2));
         }
         if (!STATES) {
           // P = (Q K^T) . D: 16 rows a warp, two rows a thread
@@ -935,20 +964,21 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
           la_wait(full_f(rf.i), rf.full(), dead);
           const float decay = fac[CF::kFacFloats - 4];
-          la_wait(b_ds, n & 1, dead);
+          const int inc = n % CF::ND;
+          la_wait(b_ds(inc), (n / CF::ND) & 1, dead);
           tc5_fence_after();
           const uint64_t decay2 = pair(decay, decay);
           // 16 key indices at a time: the state, the outputs and more would not fit the registers
 #pragma unroll
           for (int c = 0; c < KH; c += 16) {
             uint32_t x[16];
-            tmem_ld(x, lanes + CF::cDS + part * KH + c);
+            tmem_ld(x, lanes + CF::cDS + inc * KD + part * KH + c);
             tmem_wait_ld(x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) S[c / 2 + e] = fma2(S[c / 2 + e], decay2, pair(x[2 * e], x[2 * e + 1]));
           }
           tc5_fence_before();
-          arrive(b_free);
+          arrive(b_free(inc));
           float o[2][8];
           if (!STATES) {
             la_wait(b_o, n & 1, dead);
@@ -1095,10 +1125,21 @@ __global__ void linattn_join_kernel(float* states, const double* seg_decay, cons
   if (i >= per_state) return;
   float s = s0 ? s0[bh * s0_head + i] : 0.f;
   float* at = states + bh * nseg * per_state + i;
-  for (int n = 0; n < nseg; ++n) {
-    const float local = n + 1 < nseg ? at[n * per_state] : 0.f;
-    at[n * per_state] = s;
-    if (n + 1 < nseg) s = fmaf(s, (float)exp2(seg_decay[bh * nseg + n]), local);
+  const double* decay = seg_decay + bh * nseg;
+  for (int n = 0; n < nseg; n += 8) {
+    float local[8], a[8];  // eight segments asked for at once: only the sums are a chain
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool more = n + e + 1 < nseg;
+      local[e] = more ? at[(n + e) * per_state] : 0.f;
+      a[e] = more ? (float)exp2(decay[n + e]) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (n + e < nseg) {
+        at[(n + e) * per_state] = s;
+        s = fmaf(s, a[e], local[e]);
+      }
   }
 }
 
