@@ -15,10 +15,14 @@
  * allocated, nothing synchronised; calls are asynchronous on `stream` and may be
  * captured into a CUDA graph; the stream belongs to the current device, and so do
  * the buffers; arguments are checked on the host before any launch and a rejected
- * call launches nothing.  Values must be finite: a NaN or an infinity in q, k or v
- * spreads over its head of its batch row from the 64-token chunk that holds it
- * (a reversed gradient: to the chunks before it as well), the chunk's earlier
- * tokens included, and stays out of every other head and row.
+ * call launches nothing.  Values must be finite (fp32: below 3.38e38): a NaN or an
+ * infinity in q, k or v spreads over the heads of its batch row that read it, from
+ * the 64-token chunk that holds it on (gradients: to the chunks before it as well),
+ * the chunk's earlier tokens included, and stays out of every other head and row.
+ * fp32 inputs are multiplied as three bf16 parts, so below about 1e-33 their last
+ * bits are lost.  Outputs must not overlap inputs or one another, but where it says
+ * so.  A kernel whose waits give up (ss_last_device_error: SS_ERR_TIMEOUT) leaves
+ * its outputs unspecified.
  */
 #ifndef SS_LINATTN_H_
 #define SS_LINATTN_H_
@@ -61,10 +65,12 @@ typedef struct {
  *                it is to a matrix product, and is rounded once, at the end
  *  last_state_out[batch, heads, dk, dv] float32, nullable; it may be the buffer of
  *                initial_state (then advanced in place); no other overlap
- *  1 <= dk, dv <= 128 (others: SS_ERR_UNSUPPORTED); heads a multiple of qk_heads
+ *  1 <= dk, dv <= 128 (others: SS_ERR_UNSUPPORTED); heads a multiple of qk_heads and
+ *                at most 65536, batch * heads at most 2^24, seqlen below 2^31 - 1024
  *  workspace     ss_linattn_workspace_bytes(...) bytes, 256-byte aligned (null
  *                when 0): states of the segments that a long sequence with few
- *                heads is cut into.  Contents on entry do not matter; calls in
+ *                heads is cut into, or those that CTAs hand on where there are more
+ *                heads than SMs.  Contents on entry do not matter; calls in
  *                flight at once, replays of captured ones among them, must not
  *                share one
  *

@@ -725,6 +725,19 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           rk.next(), rq.next(), rv.next();
         }
       }
+      // where a wait gave up, copies may be in flight still: they are waited for, with a limit
+      if (*dead && ltid == 0) {
+        const auto land = [&](auto& ring, int count, const auto& full) {
+          for (int i = 0; i < count; ++i) {
+            const uint32_t fills = ring.turn + (i < ring.i ? 1 : 0);
+            if (fills > 0) la_wait(full(i), (fills - 1) & 1, dead);
+          }
+        };
+        land(rk, CF::RK, full_k);
+        if (!STATES) land(rq, CF::RQ, full_q);
+        land(rv, CF::RV, full_v);
+      }
+      __syncwarp();
     }
   } else if (warp >= kLaBackWarps) {
     // ---- front: weighted keys and P, a chunk ahead of the back

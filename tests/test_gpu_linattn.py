@@ -107,6 +107,74 @@ def test_fwd_segments(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_more_heads_than_sms(dtype, ragged):
+    """180 heads: every SM takes an equal range of all chunks, heads are cut between two."""
+    x, r = make(3, 200, 60, 20, 32, 48, dtype)
+    assert ss.ss_linattn_workspace_bytes(3, 200, 60, 20, 32, 48, ss.SS_BF16 if dtype == BF16 else ss.SS_F32) > 0
+    lengths = torch.tensor([200, 64, 131], dtype=torch.int32, device="cuda") if ragged else None
+    o, last = fwd(x, lengths=lengths)
+    assert ss.ss_last_device_error() == ss.SS_OK
+    check_fwd(x, o, last, lengths=lengths)
+    do, dlast = r(3, 200, 60, 48).to(dtype), r(3, 60, 32, 48)
+    got = bwd(x, do, dlast, lengths=lengths)
+    assert ss.ss_last_device_error() == ss.SS_OK
+    check_bwd(x, do, dlast, got, 1.0, lengths)
+
+
+def test_offsets_beyond_32_bits():
+    """Tokens 8.4 million elements apart: the last ones lie beyond 2^31 elements."""
+    step, L = 8_400_000, 300
+    base = torch.empty(step * L, dtype=BF16, device="cuda")
+    x, r = make(1, L, 2, 2, 64, 64, BF16)
+    at = 0
+    for n in ("q", "k", "v"):
+        view = base[at:].as_strided((1, L, 2, 64), (0, step, 64, 1))
+        view.copy_(x[n])
+        x[n], at = view, at + 128
+    far = base[at:].as_strided((1, L, 2), (0, step, 1))
+    far.copy_(x["g"])
+    x["g"] = far
+    o, last = fwd(x)
+    check_fwd(x, o, last)
+    do = base[at + 8:].as_strided((1, L, 2, 64), (0, step, 64, 1))
+    do.copy_(r(1, L, 2, 64))
+    check_bwd(x, do, None, bwd(x, do), 1.0)
+
+
+def test_two_calls_at_once():
+    """Two streams, each with more heads than SMs, on workspaces of their own."""
+    xs = [make(2, 400, 90, 90, 64, 64, BF16, seed=s)[0] for s in (1, 2)]
+    want = [fwd(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(4):
+        got = []
+        for x, st in zip(xs, streams):
+            with torch.cuda.stream(st):
+                got.append(fwd(x))
+        torch.cuda.synchronize()
+        for (o, last), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(last, wl)
+    assert ss.ss_last_device_error() == ss.SS_OK
+
+
+def test_a_nan_stays_in_its_head_and_row():
+    x, _ = make(2, 200, 4, 2, 64, 64, BF16)
+    clean, last_clean = fwd(x)
+    for n, h in (("v", 1), ("k", 1), ("q", 1)):
+        bad = {m: t if t is None else t.clone() for m, t in x.items()}
+        bad[n][1, 70, h] = float("nan")
+        heads = [1] if n == "v" else [2, 3]  # heads 2 and 3 read shared head 1
+        o, last = fwd(bad)
+        others = [h2 for h2 in range(4) if h2 not in heads]
+        assert torch.equal(o[0], clean[0]) and torch.equal(last[0], last_clean[0])
+        assert torch.equal(o[1][:, others], clean[1][:, others]) and torch.equal(last[1, others], last_clean[1, others])
+        assert torch.equal(o[1, :64], clean[1, :64])  # the chunk before
+        assert o[1, 70][heads].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_fwd_lengths_and_rows_behind(dtype):
     x, _ = make(6, 150, 2, 1, 64, 64, dtype)
     lengths = torch.tensor([0, 1, 64, 150, 900, -3], dtype=torch.int32, device="cuda")
