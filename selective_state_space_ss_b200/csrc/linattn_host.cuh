@@ -269,7 +269,7 @@ ss_status linattn_fwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
 
 // An anchor behind every so many chunks: each costs a state's write and read, the
 // sums between two cancel over that many tokens.
-int la_anchor_chunks(const LaShape& s) { return s.bf16 ? 16 : 4; }
+int la_anchor_chunks(const LaShape& s) { return s.bf16 ? 16 : 2; }
 
 struct LaBwdWs {
   size_t seg = 0, dots_q = 0, dots_k = 0, anchor = 0, dump = 0, part = 0, bytes = 0;
@@ -296,13 +296,25 @@ LaBwdWs la_bwd_ws(const LaShape& s, const LaSegs& g) {
   return w;
 }
 
+template <typename T, int VEC, typename I>
+ss_status la_launch_share(const float* part, void* out, const int32_t* lengths, const LaShape& s, int64_t total,
+                          cudaStream_t stream) {
+  const int64_t blocks = (total + 255) / 256;
+  if (blocks > INT_MAX) return SS_ERR_INVALID_ARG;
+  linattn_share_kernel<T, VEC, I><<<(unsigned)blocks, 256, 0, stream>>>(
+      part, static_cast<T*>(out), lengths, (I)s.seqlen, (I)total, s.heads, s.heads / s.qk_heads, s.dk);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
 template <typename T>
 ss_status la_share_sum(const float* part, void* out, const int32_t* lengths, const LaShape& s, cudaStream_t stream) {
-  const int64_t total = s.batch * s.seqlen * s.qk_heads * s.dk;
-  const int64_t blocks = (total + 255) / 256;
-  linattn_share_kernel<T><<<(unsigned)(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, stream>>>(
-      part, static_cast<T*>(out), lengths, s.seqlen, total, s.heads, s.heads / s.qk_heads, s.dk);
-  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+  const bool vec = s.dk % 4 == 0 && aligned(out, 4 * sizeof(T));
+  const int64_t total = s.batch * s.seqlen * s.qk_heads * (vec ? s.dk / 4 : s.dk);
+  const bool small = s.batch * s.seqlen * s.qk_heads * s.dk < INT_MAX;  // 32-bit divisions
+  if (vec) return small ? la_launch_share<T, 4, uint32_t>(part, out, lengths, s, total, stream)
+                        : la_launch_share<T, 4, uint64_t>(part, out, lengths, s, total, stream);
+  return small ? la_launch_share<T, 1, uint32_t>(part, out, lengths, s, total, stream)
+               : la_launch_share<T, 1, uint64_t>(part, out, lengths, s, total, stream);
 }
 
 template <typename T>

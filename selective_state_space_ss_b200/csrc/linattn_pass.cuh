@@ -374,6 +374,18 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
   const int64_t rs = (int64_t)a.heads * a.dv;
   const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
   const int64_t mine = ((b * a.seqlen + t) * a.heads + h) * a.dv + v;
+  if ((sizeof(T) == 4 || a.out_f32) && t0 + 16 <= len && v0 + 32 <= a.dv) {  // all there
+    float* to = static_cast<float*>(a.out) + mine;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        float* row = to + (8 * i + z) * rs;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) row[8 * u] = o[u / 2][4 * i + 2 * (u % 2) + z];
+      }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -961,7 +973,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + rf.i * CF::kFacFloats;
           const int tw = t0 + part * 16;  // this warp's tokens
           const bool anchor_here = DOTS && ((chunk + 1) % a.anchor_chunks == 0 || chunk == all_chunks - 1);
-          if (DOTS && a.reverse && anchor_here) {
+          if (DOTS && __builtin_expect(a.reverse && anchor_here, 0)) {
             // <R, S> behind this chunk: R is the state here, S the forward pass's
             float sum = 0.f;
             const int64_t an = (int64_t)bh * a.anchors + chunk / a.anchor_chunks;
@@ -1018,7 +1030,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
           arrive(empty_f(rf.i));
           rf.next();
-          if (!STATES && CF::kBf16 && fast) {
+          if (!STATES && CF::kBf16 && __builtin_expect(fast, 1)) {
             // bf16 rows leave through 512 bytes of shared memory, 8 tokens at a time, as 64
             // bytes of a token together
 #pragma unroll
@@ -1036,7 +1048,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
           if (DOTS) {
             float sum[4];
-            if (fast_x) {
+            if (__builtin_expect(fast_x, CF::kBf16)) {
               // the rows of x the other way through the stage, into the order of o; the next
               // chunk's are asked for in L2
               const char* xp = la_row(a.x, b, tw + tok, h, 2) + c8 * 2;
@@ -1081,7 +1093,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
               }
             }
           }
-          if (DOTS && !a.reverse && anchor_here) {
+          if (DOTS && __builtin_expect(!a.reverse && anchor_here, 0)) {
             const int64_t an = (int64_t)bh * a.anchors + chunk / a.anchor_chunks;
             float* to = a.dump + (an * 16 + warp) * (KH * 32);
 #pragma unroll
@@ -1157,22 +1169,41 @@ __global__ void linattn_join_kernel(float* states, const double* seg_decay, cons
 }
 
 // Gradients of shared heads: float partials [rows, heads, d] summed over the `share`
-// heads that read one, in order.
-template <typename T>
-__global__ void linattn_share_kernel(const float* part, T* out, const int* lengths, int64_t seqlen, int64_t total,
-                                     int heads, int share, int d) {
-  const int groups = heads / share;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int c = (int)(i % d);
-    const int gr = (int)(i / d % groups);
-    const int64_t row = i / d / groups;
-    if (lengths && row % seqlen >= lengths[row / seqlen]) continue;
-    const float* p = part + (row * heads + (int64_t)gr * share) * d + c;
-    float s = 0.f;
-    for (int j = 0; j < share; ++j) s += p[(int64_t)j * d];
-    if constexpr (sizeof(T) == 2) out[i] = __float2bfloat16_rn(s);
-    else out[i] = s;
+// heads that read one, in order.  VEC values a thread, an index of type I.
+template <typename T, int VEC, typename I>
+__global__ void __launch_bounds__(256)
+linattn_share_kernel(const float* part, T* out, const int* lengths, I seqlen, I total, int heads, int share, int d) {
+  const I groups = (I)(heads / share), units = (I)(d / VEC);
+  const I i = (I)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const I at = i / units, c = i - at * units, row = at / groups, gr = at - row * groups;
+  if (lengths) {
+    const I b = row / seqlen;
+    const int len = lengths[b];
+    if ((int64_t)(row - b * seqlen) >= len) return;
   }
+  const float* p = part + ((int64_t)row * heads + (int64_t)gr * share) * d + (int64_t)c * VEC;
+  T* to = out + ((int64_t)row * groups + gr) * d + (int64_t)c * VEC;
+  float s[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) s[e] = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < share; ++j) {
+    if constexpr (VEC == 4) {
+      const float4 y = __ldcs(reinterpret_cast<const float4*>(p + (int64_t)j * d));
+      s[0] += y.x, s[1] += y.y, s[2] += y.z, s[3] += y.w;
+    } else {
+      s[0] += p[(int64_t)j * d];
+    }
+  }
+  if constexpr (sizeof(T) == 2 && VEC == 4)
+    *reinterpret_cast<uint2*>(to) = make_uint2(to_bf16x2(s[0], s[1]), to_bf16x2(s[2], s[3]));
+  else if constexpr (VEC == 4)
+    *reinterpret_cast<float4*>(to) = make_float4(s[0], s[1], s[2], s[3]);
+  else if constexpr (sizeof(T) == 2)
+    *to = __float2bfloat16_rn(s[0]);
+  else
+    *to = s[0];
 }
 
 // dg_t = sum_{s = t..e} (q_s . dq_s - k_s . dk_s) + <R_e, S_e>, e the next anchor at or
