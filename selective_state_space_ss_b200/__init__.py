@@ -1,7 +1,8 @@
-"""B200-native S6 selective scan: the fused forward, its backward and the recurrent step.
+"""B200-native S6 selective scan: the fused forward, its backward and the recurrent step;
+the same recurrence with one decay per head (linear attention); an 8-bit pool for states.
 
 The compute lives in libssscan.so (hand-written sm_100a CUDA, C ABI in
-include/ss_scan.h); this package is its Python binding plus the seeded input
+include/ss_scan.h and include/ss_linattn.h); this package is its Python binding plus the seeded input
 generator (``selective_state_space_ss_b200.inputs``).  The library is loaded
 lazily on the first call, and a missing library raises: there is no CPU path.
 """

@@ -21,13 +21,16 @@
 // k and k for v, a forward pass gives dq; (v, do, q) and (k, q, do) reversed give
 // dk and dv.  So one kernel serves all four.
 //
-// Precision.  The tensor core multiplies bf16 and adds in fp32.  A value that is
-// not bf16 already is split into bf16 planes (split2): bf16 inputs stay as they
-// are, what is computed here (the masked products P, the weighted keys, the state)
-// takes two planes, 16 bits, a relative error of about 1e-6 at every product; fp32
-// inputs and everything behind them take three planes, 24 bits, and the six
-// products of planes whose weight reaches that far.  The state itself stays fp32 in
-// registers.  Running sums of the decays are whole numbers of 2^-32.
+// Precision.  The tensor core multiplies bf16 and adds in fp32.  A value that is not bf16
+// already is split into bf16 planes.  bf16 inputs stay as they are; scores times decays
+// (P) and the state, whose products end in a bf16 output, take two planes, 16 bits; the
+// weighted keys, whose products add up in the fp32 state, take four: a product of two
+// bf16 is a bf16 and a bf16 that is left over, exactly, so they are formed in bf16
+// arithmetic (two planes left the state 2.4e-6 off, four 1e-7).  fp32 inputs and
+// everything behind them take three planes, 24 bits, and the six products of planes whose
+// weight reaches that far.  Products of smaller planes are added first, while the sum is
+// small (in the other order fp32 outputs were 2e-6 off, in this one 2e-7).  The state
+// itself stays fp32 in registers.  Running sums of the decays are whole numbers of 2^-32.
 //
 // Layout.  Scores are Q K^T with tokens in the lanes.  O and S are kept transposed
 // (value index in the lanes), so that S^T is the MMA's A operand straight from
@@ -35,11 +38,23 @@
 // through shared memory.  M is 128 there; where values are 64 wide the other lanes
 // hold sums of whatever follows in shared memory and nobody reads them.
 //
-// Roles.  Loaders (two warps) fill rings of K, V and Q tiles, one warp works out the
-// decays, one thread issues the MMAs; the front warps (eight) turn scores into P and
-// keys into weighted keys one chunk ahead of the back warps (sixteen), which hold the
-// state: they take O and the state's increment from tensor memory, give the state
-// back as planes, and write O out while the next chunk's products run.
+// Roles.  One thread loads K, V and Q tiles into rings by TMA (a warp or two where TMA
+// does not apply), one warp works out the decays, one thread of a warp issues the state's
+// increments and one of another the scores and outputs; the front warps (eight) turn
+// keys into weighted keys and scores into P a chunk ahead of the back warps (sixteen),
+// which hold the state: they add the increment, give the state back as planes, take O
+// from tensor memory and write it out while the next chunk's products run.
+//
+// What bounds it, and what the steps gave (bf16, B4 L8192, 40 heads of 128 x 128: 1.36 GB,
+// 207 us at the copy rate of 6.55 TB/s).  Four loader warps and eight that did all the
+// rest in turn: 2.32 ms.  The roles apart, TMA: 1.03.  Fewer instructions, code that fits
+// the instruction cache (spin loops not unrolled, product loops short): 0.50.  Products
+// issued from warp-uniform descriptors, sixteen and eight warps, hand-overs of their own
+// for P and the weighted keys: 0.41 to 0.46 (2.9 to 3.3 TB/s, 44 to 51% of the copy
+// rate), 2.5 us a chunk and SM of 64 tokens.  ncu: 11 thousand warp instructions a chunk,
+// issue slots 60% busy, tensor pipe 43%, DRAM 40%: it is bound by the work around the
+// products (splitting, weighting, moving) and its hand-overs, not by a single unit.
+// With 64 x 64 heads a chunk takes 1.65 us, half of its data, for the same hand-overs.
 //
 // Schedule.  A head's chunks depend on one another through S alone.  With fewer heads
 // than SMs the sequence is cut into segments whose starting states a first launch

@@ -1,5 +1,9 @@
 // state_pool.cuh -- states in 8 bits: each row of `width` values as int8 steps of a
 // scale of its own.  Bound by memory: 4 bytes in and 1 out a value, or the other way.
+// 64 sequences of 5120 rows of 128, written and read back (422 MB): 72 us, 5.9 TB/s, 90%
+// of the copy rate (store 39 us, load 34).  Codes through conversions, with ties looked at
+// for every value, kept the store at 63 us and the arithmetic at 72%; a thread's 64 bytes
+// of output in a row kept the load at 51.
 #pragma once
 
 #include <stdint.h>
