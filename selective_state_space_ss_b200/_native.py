@@ -593,16 +593,21 @@ def ss_linattn_fwd(q, k, v, log_decay, scale=1.0, initial_state=None, lengths=No
     batch, L, heads, _, dk, dv, _ = sizes
     need = _linattn_need(False, device.index, *sizes)
     f32, shape = torch.float32, (batch, heads, dk, dv)
+    states = _dense("initial_state", initial_state, device, f32, shape)
+    rows = _dense("lengths", lengths, device, torch.int32, (batch,))
     if o_out is None:
         o_out = (q.new_empty if lengths is None else q.new_zeros)((batch, L, heads, dv))
+        o_ptr = o_out.data_ptr()
+    else:
+        o_ptr = _dense("o_out", o_out, device, q.dtype, (batch, L, heads, dv))
     if last_state_out is None and return_last_state:
-        last_state_out = torch.empty(shape, dtype=f32, device=device)
+        last_state_out = q.new_empty(shape, dtype=f32)
+        last_ptr = last_state_out.data_ptr()
+    else:
+        last_ptr = _dense("last_state_out", last_state_out, device, f32, shape)
     keep, ws, ws_bytes = _workspace(workspace, need, device)
-    _call(lib.ss_linattn_fwd, "ss_linattn_fwd", device, stream, *ops, scale,
-          _dense("initial_state", initial_state, device, f32, shape),
-          _dense("lengths", lengths, device, torch.int32, (batch,)),
-          _dense("o_out", o_out, device, q.dtype, (batch, L, heads, dv)),
-          _dense("last_state_out", last_state_out, device, f32, shape), *sizes, ws, ws_bytes)
+    _call(lib.ss_linattn_fwd, "ss_linattn_fwd", device, stream, *ops, scale, states, rows, o_ptr,
+          last_ptr, *sizes, ws, ws_bytes)
     return o_out, last_state_out
 
 
@@ -657,12 +662,14 @@ def ss_linattn_step(state, q, k, v, log_decay, scale=1.0, slots=None, o_out=None
     out = (batch, heads, dv)
     if o_out is None:
         o_out = (q.new_empty if slots is None else q.new_zeros)(out)
+        o_ptr = o_out.data_ptr()
+    else:
+        o_ptr = _dense("o_out", o_out, device, dtype, out)
     _call(lib.ss_linattn_step, "ss_linattn_step", device, stream,
           _heads3("q", q, device, dtype, shape), _heads3("k", k, device, dtype, shape),
           _heads3("v", v, device, dtype, out), _heads3("log_decay", log_decay, device, dtype, (batch, heads)),
           scale, _dense("state", state, device, torch.float32, pool), num_slots,
-          _dense("slots", slots, device, torch.int32, (batch,)), _dense("o_out", o_out, device, dtype, out),
-          batch, heads, qk_heads, dk, dv, dt)
+          _dense("slots", slots, device, torch.int32, (batch,)), o_ptr, batch, heads, qk_heads, dk, dv, dt)
     return o_out
 
 
@@ -708,7 +715,9 @@ def ss_state_load8(codes, scales, slots=None, state_out=None, stream=None):
     whole = (batch, *shape)
     if state_out is None:
         state_out = scales.new_empty(whole)
-    _call(lib.ss_state_load8, "ss_state_load8", device, stream, *ptrs,
-          _dense("state_out", state_out, device, torch.float32, whole), batch,
+        out = state_out.data_ptr()
+    else:
+        out = _dense("state_out", state_out, device, torch.float32, whole)
+    _call(lib.ss_state_load8, "ss_state_load8", device, stream, *ptrs, out, batch,
           math.prod(shape[:-1]), shape[-1])
     return state_out
