@@ -144,12 +144,12 @@ bool la_map(CUtensorMap* m, const LaTensor& x, int64_t batch, int64_t seqlen, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int KD, int VD, LaMode MODE>
-ss_status la_launch(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream) {
+template <typename T, int KD, int VD, LaMode MODE, bool FAST>
+ss_status la_launch_as(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream) {
   using CF = LaCfg<T, KD, VD, MODE>;
   struct Tag : CF {};
   if (once_per_device<Tag>([] {
-        return cudaFuncSetAttribute(linattn_pass_kernel<T, KD, VD, MODE>,
+        return cudaFuncSetAttribute(linattn_pass_kernel<T, KD, VD, MODE, FAST>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, CF::kSmem) == cudaSuccess;
       }) != 1)
     return SS_ERR_CUDA;
@@ -158,8 +158,18 @@ ss_status la_launch(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream
   if (a.workers > 0 &&
       cudaMemsetAsync(a.flags, 0, (1 + (size_t)a.workers * 16) * sizeof(unsigned), stream) != cudaSuccess)
     return SS_ERR_CUDA;
-  linattn_pass_kernel<T, KD, VD, MODE><<<(unsigned)grid, CF::kThreads, CF::kSmem, stream>>>(a, maps);
+  linattn_pass_kernel<T, KD, VD, MODE, FAST><<<(unsigned)grid, CF::kThreads, CF::kSmem, stream>>>(a, maps);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+template <typename T, int KD, int VD, LaMode MODE>
+ss_status la_launch(const LaPassArgs& a, const LaMaps& maps, cudaStream_t stream) {
+  if constexpr (sizeof(T) == 2) {
+    const bool stores = MODE == kLaStates || a.out_vec || (MODE == kLaProducts && a.out_f32);
+    if (a.tma && !a.lengths && stores && (MODE != kLaProducts || a.x_vec))
+      return la_launch_as<T, KD, VD, MODE, true>(a, maps, stream);
+  }
+  return la_launch_as<T, KD, VD, MODE, false>(a, maps, stream);
 }
 
 template <typename T, LaMode MODE>

@@ -170,8 +170,9 @@ struct LaCfg {
   static constexpr int kLoaders = kTwoIssuers ? 32 : 64;  // loader threads
   static constexpr int kThreads = 896;
   // Registers a thread of the three kinds of warpgroup: 4 x 88 + 2 x 56 + 40 (fp32, with
-  // all its loads through registers: 4 x 88 + 2 x 48 + 56) = 7 x 72 at launch.
-  static constexpr int kBackRegs = 88, kFrontRegs = kBf16 ? 56 : 48, kAuxRegs = kBf16 ? 40 : 56;
+  // all its loads through registers: 4 x 80 + 2 x 56 + 72, 8% faster with 128 x 128
+  // heads) = 7 x 72 at launch.
+  static constexpr int kBackRegs = kBf16 ? 88 : 80, kFrontRegs = 56, kAuxRegs = kBf16 ? 40 : 72;
   static_assert(4 * kBackRegs + 2 * kFrontRegs + kAuxRegs == 7 * 72, "registers of a block");
 };
 constexpr int kLaBackWarps = 16, kLaFrontWarps = 8;
@@ -382,14 +383,15 @@ struct LaWidth {
 
 // 32 values x 16 tokens of a back warp, o[h][4 i + z]: value v0 + 16 h + 8 (z / 2) +
 // lane / 4, token t0 + 8 i + 2 (lane % 4) + z % 2.  To the output element by element: fp32
-// (32 bytes a token together) and rows that are not whole 16-byte units.
-template <typename T>
+// (32 bytes a token together) and, but for F32_ONLY, rows that are not whole 16-byte
+// units.
+template <typename T, bool F32_ONLY>
 __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2][8], int64_t b, int h, int t0, int len,
                                         int v0, int lane) {
   const int64_t rs = (int64_t)a.heads * a.dv;
   const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
   const int64_t mine = ((b * a.seqlen + t) * a.heads + h) * a.dv + v;
-  if ((sizeof(T) == 4 || a.out_f32) && t0 + 16 <= len && v0 + 32 <= a.dv) {  // all there
+  if ((F32_ONLY || sizeof(T) == 4 || a.out_f32) && t0 + 16 <= len && v0 + 32 <= a.dv) {  // all there
     float* to = static_cast<float*>(a.out) + mine;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -411,7 +413,7 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
         for (int u = 0; u < 4; ++u)
           if (v + 8 * u < a.dv) {
             const float y = o[u / 2][4 * i + 2 * (u % 2) + z];
-            if (sizeof(T) == 4 || a.out_f32) static_cast<float*>(a.out)[row + 8 * u] = y;
+            if (F32_ONLY || sizeof(T) == 4 || a.out_f32) static_cast<float*>(a.out)[row + 8 * u] = y;
             else static_cast<__nv_bfloat16*>(a.out)[row + 8 * u] = __float2bfloat16_rn(y);
           }
       }
@@ -507,7 +509,10 @@ __device__ __forceinline__ LaPiece la_piece(const LaPassArgs& a, const LaWork& w
   return p;
 }
 
-template <typename T, int KD, int VD, LaMode MODE>
+// FAST: bf16 with 16-byte rows everywhere and no lengths, without the code for the rest
+// (720 instructions of plain loads alone; B4 L8192 H40 128 x 128 took 4% longer with it,
+// for the instruction cache).
+template <typename T, int KD, int VD, LaMode MODE, bool FAST>
 __global__ void __launch_bounds__(LaCfg<T, KD, VD, MODE>::kThreads, 1)
 linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant__ LaMaps maps) {
   using CF = LaCfg<T, KD, VD, MODE>;
@@ -716,7 +721,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         for (int c = p.first; c < p.last; ++c) {
           const int t0 = (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk;
           // TMA clips at the tensor's end, not at a row's length
-          const bool by_tma = CF::kBf16 && a.tma && (t0 + kLaChunk <= p.len || p.len == a.seqlen);
+          const bool by_tma = FAST || (CF::kBf16 && a.tma && (t0 + kLaChunk <= p.len || p.len == a.seqlen));
           auto tile = [&](auto width, const LaTensor& x, const CUtensorMap* map, int hx, int at, bool wait, uint32_t turn,
                           uint32_t full, uint32_t empty, int d) {
             constexpr int DP = decltype(width)::value;
@@ -727,7 +732,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
 #pragma unroll
                 for (int j = 0; j < DP / 64; ++j) tma_load_block(base + at + j * kLaBlock, map, full, j * 64, t0, hx, p.b);
               }
-            } else {
+            } else if constexpr (!FAST) {
               __syncwarp();
               if (CF::kLoaders > 32) asm volatile("bar.sync 2, 64;\n" ::: "memory");
               la_load_tile<T, DP>(smem + at, x, p.b, p.h, t0, p.len, d, a.vec, a.reverse ? -kLaChunk : kLaChunk, ltid,
@@ -944,7 +949,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         char* mine = stage + tok * 64 + (((lane % 4) ^ ((tok >> 1) & 3)) << 4);
         const uint32_t blocks = smem_u32(stage) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
         const int rs = a.heads * a.dv * 2;
-        const bool fast = CF::kBf16 && a.out_vec, fast_x = DOTS && CF::kBf16 && a.x_vec;
+        const bool fast = FAST && MODE == kLaOutputs ? true : CF::kBf16 && a.out_vec;
+        const bool fast_x = DOTS && CF::kBf16 && (FAST || a.x_vec);
         char* out = static_cast<char*>(a.out) + ((int64_t)b * a.seqlen + tok) * rs + (h * a.dv + c8) * 2;
         if (p.from_carry) {
           const unsigned* flag = a.flags + 1 + (work.worker - 1) * 16 + warp;
@@ -1058,8 +1064,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
               if (c8 < a.dv && t + tok < len && in_range(t + tok, a.seqlen)) *reinterpret_cast<uint4*>(out + (int64_t)t * rs) = y;
               __syncwarp();
             }
-          } else if (!STATES) {
-            la_emit<T>(a, o, b, h, tw, len, quad * 32, lane);
+          } else if constexpr (!STATES && !(FAST && MODE == kLaOutputs)) {
+            la_emit<T, FAST>(a, o, b, h, tw, len, quad * 32, lane);
           }
           if (DOTS) {
             float sum[4];
@@ -1092,7 +1098,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
                   y = fma2(pair(o[u / 2][4 * i2 + 2 * (u % 2)], o[u / 2][4 * i2 + 2 * (u % 2) + 1]), from_bf16x2(x4[u]), y);
                 sum[2 * i2] = pair_lo(y), sum[2 * i2 + 1] = pair_hi(y);
               }
-            } else {
+            } else if constexpr (!FAST) {
               la_dots<T>(sum, a, o, b, h, tw, len, quad * 32, lane);
             }
             // the lanes with the same tokens are 4, 8 and 16 apart
