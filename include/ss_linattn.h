@@ -106,7 +106,10 @@ size_t ss_linattn_workspace_bytes(int64_t batch, int64_t seqlen, int heads,
  * dlog_decay [batch, seqlen, heads]: in_dtype, contiguous, required; as in the
  * forward nothing is written behind a row's length.  dinitial_state [batch, heads,
  * dk, dv] float32, nullable; it may be the buffer of dlast_state.  (A decay that was
- * broadcast over time gets its gradient token by token.)  Sums are in a fixed
+ * broadcast over time gets its gradient token by token.)  dg_t is formed from
+ * differences of q . dq and k . dk summed over up to 1024 tokens (fp32: 128), so it is
+ * good relative to those sums; where exp(g_t) leaves nearly nothing, its own size is
+ * far below them.  It is exactly zero at t = 1 without an initial state.  Sums are in a fixed
  * order: the same call gives the same bits.  workspace:
  * ss_linattn_bwd_workspace_bytes(...) bytes, 256-byte aligned.
  */

@@ -328,13 +328,13 @@ ss_status la_share_sum(const float* part, void* out, const int32_t* lengths, con
 }
 
 template <typename T>
-ss_status la_decay_grad(const LaPassArgs& a, const float* dots_q, const float* dots_k, void* dg, const LaShape& s,
-                        cudaStream_t stream) {
+ss_status la_decay_grad(const LaPassArgs& a, const float* dots_q, const float* dots_k, bool from_zero, void* dg,
+                        const LaShape& s, cudaStream_t stream) {
   const int64_t blocks = s.bh() * a.anchors;
   if (blocks > INT_MAX) return SS_ERR_INVALID_ARG;
   linattn_decay_grad_kernel<T><<<(unsigned)blocks, kLaGradThreads, 0, stream>>>(
       dots_q, dots_k, a.anchor, static_cast<T*>(dg), a.lengths, s.heads, (int)s.seqlen, a.anchors,
-      a.anchor_chunks * kLaChunk, s.dk <= 64);
+      a.anchor_chunks * kLaChunk, s.dk <= 64, from_zero);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
@@ -401,8 +401,8 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   if (share > 1 && (st = s.bf16 ? la_share_sum<__nv_bfloat16>(part, dk, lengths, s, stream)
                                 : la_share_sum<float>(part, dk, lengths, s, stream)) != SS_OK)
     return st;
-  if ((st = s.bf16 ? la_decay_grad<__nv_bfloat16>(a, reinterpret_cast<float*>(base + w.dots_q), a.dots, dg, s, stream)
-                   : la_decay_grad<float>(a, reinterpret_cast<float*>(base + w.dots_q), a.dots, dg, s, stream)) != SS_OK)
+  if ((st = s.bf16 ? la_decay_grad<__nv_bfloat16>(a, reinterpret_cast<float*>(base + w.dots_q), a.dots, !s0, dg, s, stream)
+                   : la_decay_grad<float>(a, reinterpret_cast<float*>(base + w.dots_q), a.dots, !s0, dg, s, stream)) != SS_OK)
     return st;
 
   // dv: reversed with (k, q, do)

@@ -1232,12 +1232,13 @@ linattn_share_kernel(const float* part, T* out, const int* lengths, I seqlen, I 
 // sums start anew, so that what cancels in the differences is no longer than the
 // stretch between two.  One block a stretch, the same number of tokens a thread; sums
 // in fp64.  Keys of at most 64 fill two lane quadrants of the partial products, wider
-// ones four.
+// ones four.  The first token's gradient is zero where the states start from zero: its
+// terms cancel, and their roundings are not left in the place of it.
 constexpr int kLaGradThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kLaGradThreads)
 linattn_decay_grad_kernel(const float* dots_q, const float* dots_k, const float* anchor, T* out, const int* lengths,
-                          int heads, int seqlen, int anchors, int anchor_tokens, bool two_quads) {
+                          int heads, int seqlen, int anchors, int anchor_tokens, bool two_quads, bool from_zero) {
   __shared__ double warp_sum[kLaGradThreads / 32];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int bh = blockIdx.x / anchors, an = blockIdx.x % anchors;
@@ -1279,6 +1280,7 @@ linattn_decay_grad_kernel(const float* dots_q, const float* dots_k, const float*
     const int t = last - i;
     if (t < begin) break;
     x += term(t);
+    if (from_zero && t == 0) x = 0.0;
     T* to = out + ((int64_t)b * seqlen + t) * heads + h;
     if constexpr (sizeof(T) == 2) *to = __float2bfloat16_rn((float)x);
     else *to = (float)x;

@@ -330,6 +330,18 @@ def test_bwd_extreme_decays(kind):
     check_bwd(x, do, None, got, 1.0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_bwd_first_decay_acts_on_nothing(dtype):
+    """Without an initial state the first token's decay has no effect: its gradient is zero, not rounding."""
+    x, r = make(3, 70, 2, 2, 64, 64, dtype, state=False)
+    do = r(3, 70, 2, 64).to(dtype)
+    lengths = torch.tensor([70, 1, 66], dtype=torch.int32, device="cuda")
+    got = bwd(x, do, r(3, 2, 64, 64), lengths=lengths)
+    assert not got["dlog_decay"][:, 0].any() and got["dlog_decay"][0, 1:].all()
+    one = {n: t if t is None else t[:, :1] for n, t in x.items()}
+    assert not bwd(one, do[:, :1])["dlog_decay"].any()
+
+
 def test_bwd_initial_gradient_in_the_last_states_buffer():
     """Through the C ABI: dinitial_state may overwrite dlast_state."""
     import ctypes
