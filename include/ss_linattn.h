@@ -106,12 +106,13 @@ size_t ss_linattn_workspace_bytes(int64_t batch, int64_t seqlen, int heads,
  * dlog_decay [batch, seqlen, heads]: in_dtype, contiguous, required; as in the
  * forward nothing is written behind a row's length.  dinitial_state [batch, heads,
  * dk, dv] float32, nullable; it may be the buffer of dlast_state.  (A decay that was
- * broadcast over time gets its gradient token by token.)  dg_t is formed from
- * differences of q . dq and k . dk summed over up to 1024 tokens (fp32: 128), so it is
- * good relative to those sums; where exp(g_t) leaves nearly nothing, its own size is
- * far below them.  It is exactly zero at t = 1 without an initial state.  Sums are in a fixed
+ * broadcast over time gets its gradient token by token.)  dg_t is a sum of terms that
+ * each hold exp(g_t), none of which cancels another's larger part: it is good relative
+ * to their size, however much the decay leaves, and exactly zero where that is nothing
+ * (minus infinity) and at t = 1 without an initial state.  Sums are in a fixed
  * order: the same call gives the same bits.  workspace:
- * ss_linattn_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ * ss_linattn_bwd_workspace_bytes(...) bytes, 256-byte aligned, most of it a state (dk
+ * and dv made up to 64 or 128, float32) for every 64 tokens of every head.
  */
 ss_status ss_linattn_bwd(const ss_heads* q, const ss_heads* k, const ss_heads* v,
                          const ss_heads* log_decay, const ss_heads* d_o, float scale,

@@ -11,6 +11,7 @@
 
 #include "ss_linattn.h"
 #include "host_common.cuh"
+#include "linattn_decay_grad.cuh"
 #include "linattn_pass.cuh"
 #include "linattn_step.cuh"
 #include "state_pool.cuh"
@@ -36,6 +37,8 @@ ss_status la_check_shape(const LaShape& s, int in_dtype) {
   if (in_dtype != SS_F32 && in_dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
   return SS_OK;
 }
+
+int la_chunks(const LaShape& s) { return (int)((s.seqlen + kLaChunk - 1) / kLaChunk); }
 
 bool la_check_heads(const ss_heads* x, int es) { return x && x->data && aligned(x->data, es); }
 
@@ -225,7 +228,7 @@ LaPassArgs la_base(const LaShape& s, const ss_heads* g, const int32_t* lengths, 
   a.bh = (int)s.bh();
   a.nseg = segs.nseg;
   a.seg_chunks = segs.chunks;
-  a.anchor_chunks = 1;
+  a.chunks = la_chunks(s);
   a.scale_p = a.scale_o = a.scale_w = 1.f;
   return a;
 }
@@ -277,30 +280,23 @@ ss_status linattn_fwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
 
 // ---- backward
 
-// An anchor behind every so many chunks: each costs a state's write and read, the
-// sums between two cancel over that many tokens.
-int la_anchor_chunks(const LaShape& s) { return s.bf16 ? 16 : 2; }
-
 struct LaBwdWs {
-  size_t seg = 0, dots_q = 0, dots_k = 0, anchor = 0, dump = 0, part = 0, bytes = 0;
-  int64_t anchors = 0;
+  size_t dots_q = 0, dots_k = 0, flow = 0, dump = 0, part = 0, bytes = 0;
 };
 LaBwdWs la_bwd_ws(const LaShape& s, const LaSegs& g) {
   LaBwdWs w;
-  const int64_t chunks = (s.seqlen + kLaChunk - 1) / kLaChunk;
-  const int per = la_anchor_chunks(s);
-  w.anchors = (chunks + per - 1) / per;
   size_t at = la_seg_bytes(s, g);
   auto take = [&at](size_t n) {
     const size_t r = at;
     at += align256(n);
     return r;
   };
-  const size_t rows = (size_t)s.bh() * s.seqlen;
+  const size_t rows = (size_t)s.bh() * s.seqlen, chunks = (size_t)s.bh() * la_chunks(s);
   w.dots_q = take(rows * 16);
   w.dots_k = take(rows * 16);
-  w.anchor = take((size_t)s.bh() * w.anchors * 16 * 4);
-  w.dump = take((size_t)s.bh() * w.anchors * 128 * (s.dv <= 64 ? 64 : 128) * 4);
+  w.flow = take(chunks * 16 * 4);
+  // a state for every chunk, as the warps hold it
+  w.dump = take(chunks * (s.dk <= 64 ? 64 : 128) * (s.dv <= 64 ? 64 : 128) * 4);
   w.part = take(s.heads > s.qk_heads ? rows * s.dk * 4 : 0);
   w.bytes = at;
   return w;
@@ -327,15 +323,24 @@ ss_status la_share_sum(const float* part, void* out, const int32_t* lengths, con
                : la_launch_share<T, 1, uint64_t>(part, out, lengths, s, total, stream);
 }
 
-template <typename T>
-ss_status la_decay_grad(const LaPassArgs& a, const float* dots_q, const float* dots_k, bool from_zero, void* dg,
-                        const LaShape& s, cudaStream_t stream) {
-  const int64_t blocks = s.bh() * a.anchors;
-  if (blocks > INT_MAX) return SS_ERR_INVALID_ARG;
-  linattn_decay_grad_kernel<T><<<(unsigned)blocks, kLaGradThreads, 0, stream>>>(
-      dots_q, dots_k, a.anchor, static_cast<T*>(dg), a.lengths, s.heads, (int)s.seqlen, a.anchors,
-      a.anchor_chunks * kLaChunk, s.dk <= 64, from_zero);
+template <typename T, bool VEC>
+ss_status la_launch_decay_grad(const LaGradArgs& a, const LaShape& s, cudaStream_t stream) {
+  struct Tag {};
+  if (once_per_device<Tag>([] {
+        return cudaFuncSetAttribute(linattn_decay_grad_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    la_grad_smem(128, 128, sizeof(T))) == cudaSuccess;
+      }) != 1)
+    return SS_ERR_CUDA;
+  linattn_decay_grad_kernel<T, VEC>
+      <<<(unsigned)(s.bh() * a.chunks), kLaGradThreads, la_grad_smem(s.dk, s.dv, sizeof(T)), stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+template <typename T>
+ss_status la_decay_grad(const LaGradArgs& a, const LaShape& s, cudaStream_t stream) {
+  const int es = sizeof(T);
+  const bool vec = la_vec(a.q, s.dk, es) && la_vec(a.k, s.dk, es) && la_vec(a.v, s.dv, es) && la_vec(a.d, s.dv, es);
+  return vec ? la_launch_decay_grad<T, true>(a, s, stream) : la_launch_decay_grad<T, false>(a, s, stream);
 }
 
 ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads* v, const ss_heads* g,
@@ -350,6 +355,7 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   for (const void* x : {dq, dk, dv, dg})
     if (!x || !aligned(x, es)) return SS_ERR_INVALID_ARG;
   if (!aligned(s0, 4) || !aligned(dlast, 4) || !aligned(lengths, 4) || !aligned(ds0, 4)) return SS_ERR_INVALID_ARG;
+  if (s.bh() * la_chunks(s) > INT_MAX) return SS_ERR_INVALID_ARG;  // one block each; their gradients alone are 256 GB
   const LaSegs segs = la_plan(s);
   const LaBwdWs w = la_bwd_ws(s, segs);
   if (!ws || ws_bytes < w.bytes || !aligned(ws, 256)) return SS_ERR_INVALID_ARG;
@@ -361,10 +367,8 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
 
   // dq: a forward pass with (do, v, k); its state is S with the two indices exchanged
   LaPassArgs a = la_base(s, g, lengths, segs);
-  a.anchor_chunks = la_anchor_chunks(s);
-  a.anchors = (int)w.anchors;
   a.dump = reinterpret_cast<float*>(base + w.dump);
-  a.anchor = reinterpret_cast<float*>(base + w.anchor);
+  a.flow = reinterpret_cast<float*>(base + w.flow);
   a.q = td;
   a.k = tv;
   a.v = tk;
@@ -401,9 +405,16 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   if (share > 1 && (st = s.bf16 ? la_share_sum<__nv_bfloat16>(part, dk, lengths, s, stream)
                                 : la_share_sum<float>(part, dk, lengths, s, stream)) != SS_OK)
     return st;
-  if ((st = s.bf16 ? la_decay_grad<__nv_bfloat16>(a, reinterpret_cast<float*>(base + w.dots_q), a.dots, !s0, dg, s, stream)
-                   : la_decay_grad<float>(a, reinterpret_cast<float*>(base + w.dots_q), a.dots, !s0, dg, s, stream)) != SS_OK)
-    return st;
+  LaGradArgs dec = {};
+  dec.q = tq, dec.k = tk, dec.v = tv, dec.d = td, dec.g = a.g;
+  dec.lengths = lengths;
+  dec.dots_q = reinterpret_cast<float*>(base + w.dots_q);
+  dec.dots_k = a.dots;
+  dec.flow = a.flow;
+  dec.out = dg;
+  dec.heads = s.heads, dec.seqlen = a.seqlen, dec.dk = s.dk, dec.dv = s.dv, dec.chunks = a.chunks;
+  dec.scale = scale;
+  if ((st = s.bf16 ? la_decay_grad<__nv_bfloat16>(dec, s, stream) : la_decay_grad<float>(dec, s, stream)) != SS_OK) return st;
 
   // dv: reversed with (k, q, do)
   a.q = tk;

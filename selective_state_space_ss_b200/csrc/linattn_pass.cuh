@@ -97,12 +97,11 @@ struct LaPassArgs {
   double* seg_decay;    // states-only: each segment's sum of g (base 2)
   void* out;            // [batch, seqlen, heads, dv] contiguous
   int out_f32;          // out is float32 whatever the inputs
-  LaTensor x;           // rows to take the inner product of each output row with (ptr null: none)
+  LaTensor x;           // rows to take the inner product of with each output row's part from the state
   float* dots;          // [batch * heads, seqlen, 4] partial products of x, one a lane quadrant
-  float* dump;          // forward: where the states at anchors go; reversed: where they come from
-  float* anchor;        // reversed: [batch * heads, anchors, 16] partial products <R, S>, one a back warp
-  int anchor_chunks;    // an anchor behind every so many chunks
-  int anchors;          // anchors of the longest row
+  float* dump;          // the states before each chunk: forward writes them, reversed reads them
+  float* flow;          // reversed: [batch * heads, chunks, 16] partial products <R, S>, one a back warp
+  int chunks;           // of a whole row
   int heads, seqlen, dk, dv;
   int bh;               // batch * heads
   int nseg, seg_chunks; // segments of a head, or
@@ -122,7 +121,8 @@ struct LaMaps {
 
 // What a launch does: outputs and states; the states alone (the sequence's segments, each
 // from zero, all at once); outputs and states with the products that a decay's gradient
-// is made of (of each output row with x, of states at anchors).
+// is made of (of x with what each output row has from the state, of the two passes' states
+// at every chunk).
 enum LaMode { kLaOutputs, kLaStates, kLaProducts };
 
 template <typename T, int KD, int VD, LaMode MODE = kLaOutputs>
@@ -303,16 +303,16 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
 // A lane's two log decays of a chunk as they are stored, zero behind the row's end.
 // Those of `ahead` tokens on are asked for in L2: a chunk may take less than a load.
 template <typename T>
-__device__ __forceinline__ void la_fetch_decays(T (&x)[2], const LaPassArgs& a, int b, int h, int t0, int len, int ahead,
+__device__ __forceinline__ void la_fetch_decays(T (&x)[2], const LaTensor& g, int b, int h, int t0, int len, int ahead,
                                                 int lane) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = t0 + 2 * lane + i;
     x[i] = zero_elem<T>();
-    const char* from = la_row(a.g, b, t, h, sizeof(T));
+    const char* from = la_row(g, b, t, h, sizeof(T));
     if (t < len && in_range(t, len)) x[i] = *reinterpret_cast<const T*>(from);
-    if (t + ahead >= 0 && t + ahead < len)
-      asm volatile("prefetch.global.L2 [%0];\n" ::"l"(from + ahead * a.g.st * (int64_t)sizeof(T)));
+    if (ahead != 0 && t + ahead >= 0 && t + ahead < len)
+      asm volatile("prefetch.global.L2 [%0];\n" ::"l"(from + ahead * g.st * (int64_t)sizeof(T)));
   }
 }
 
@@ -325,15 +325,11 @@ __device__ __forceinline__ float la_exp2(int64_t x) {
   return n < -126 ? 0.f : n > 127 ? __int_as_float(0x7f800000) : z;
 }
 
-// A chunk's decays: running sums, base 2, as integer and fraction (64 floats each), the
-// factors of the rows, those of the keys (for bf16 keys as three bf16 planes, each twice
-// in a word), and the chunk's whole decay, which is returned.  One warp, two tokens a
-// lane.  The sums are whole numbers of 2^-32, so differences of large sums lose nothing.
-// A log decay beyond +-1400 leaves nothing, or too much, in fp32 and is taken as that:
-// minus infinity (a reset) is a number like any other here.
-template <bool BF16>
-__device__ __forceinline__ int64_t la_decays(float* fac, float x0, float x1, bool reverse, float scale_o, float scale_w,
-                                             int lane) {
+// Running sums of a chunk's decays, base 2, two tokens a lane of a warp, and the whole.
+// They are whole numbers of 2^-32, so differences of large sums lose nothing.  A log decay
+// beyond +-1400 leaves nothing, or too much, in fp32 and is taken as that: minus infinity
+// (a reset) is a number like any other here.
+__device__ __forceinline__ void la_decay_sums(int64_t (&at)[2], int64_t& total, float x0, float x1, int lane) {
   const float x[2] = {x0, x1};
   int64_t g[2];
 #pragma unroll
@@ -345,8 +341,18 @@ __device__ __forceinline__ int64_t la_decays(float* fac, float x0, float x1, boo
     const int64_t up = __shfl_up_sync(kFullMask, sum, o);
     if (lane >= o) sum += up;
   }
-  const int64_t total = __shfl_sync(kFullMask, sum, 31);
-  const int64_t at[2] = {sum - g[1], sum};
+  total = __shfl_sync(kFullMask, sum, 31);
+  at[0] = sum - g[1], at[1] = sum;
+}
+
+// A chunk's decays: running sums, base 2, as integer and fraction (64 floats each), the
+// factors of the rows, those of the keys (for bf16 keys as three bf16 planes, each twice
+// in a word), and the chunk's whole decay, which is returned.  One warp.
+template <bool BF16>
+__device__ __forceinline__ int64_t la_decays(float* fac, float x0, float x1, bool reverse, float scale_o, float scale_w,
+                                             int lane) {
+  int64_t at[2], total;
+  la_decay_sums(at, total, x0, x1, lane);
   // a NaN among them is not to vanish
   const float bad = __any_sync(kFullMask, x0 != x0 || x1 != x1) ? __int_as_float(0x7fffffff) : 1.f;
   float hi[2], lo[2], rows[2], keys[2];
@@ -696,10 +702,10 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         auto place = [&](int c) { return (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk; };
         T next[2];
         const int ahead = (a.reverse ? -4 : 4) * kLaChunk;
-        if (p.first < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(p.first), p.len, ahead, lane);
+        if (p.first < p.last) la_fetch_decays<T>(next, a.g, p.b, p.h, place(p.first), p.len, ahead, lane);
         for (int c = p.first; c < p.last; ++c) {
           const float x0 = to_f32(next[0]), x1 = to_f32(next[1]);
-          if (c + 1 < p.last) la_fetch_decays<T>(next, a, p.b, p.h, place(c + 1), p.len, ahead, lane);
+          if (c + 1 < p.last) la_fetch_decays<T>(next, a.g, p.b, p.h, place(c + 1), p.len, ahead, lane);
           if (rf.used()) la_wait(empty_f(rf.i), rf.empty(), dead);
           const int64_t whole = la_decays<CF::kBf16>(reinterpret_cast<float*>(smem + CF::kFac) + rf.i * CF::kFacFloats, x0,
                                                      x1, a.reverse, a.scale_o, a.scale_w, lane);
@@ -941,7 +947,6 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
       for (int i = 0; i < work.pieces; ++i) {
         const LaPiece p = la_piece(a, work, i);
         const int bh = p.bh, b = p.b, h = p.h, len = p.len;
-        const int all_chunks = (len + kLaChunk - 1) / kLaChunk;
         const int step = a.workers > 0 ? 0 : work.worker % a.nseg;
         // 16-byte rows: this lane's part of token lane / 4, in memory and in the stage
         const int tok = lane / 4, c8 = quad * 32 + (lane % 4) * 8;
@@ -993,20 +998,27 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           const int chunk = a.reverse ? p.last - 1 - (cc - p.first) : cc, t0 = chunk * kLaChunk;
           const float* fac = reinterpret_cast<const float*>(smem + CF::kFac) + rf.i * CF::kFacFloats;
           const int tw = t0 + part * 16;  // this warp's tokens
-          const bool anchor_here = DOTS && ((chunk + 1) % a.anchor_chunks == 0 || chunk == all_chunks - 1);
-          if (DOTS && __builtin_expect(a.reverse && anchor_here, 0)) {
-            // <R, S> behind this chunk: R is the state here, S the forward pass's
-            float sum = 0.f;
-            const int64_t an = (int64_t)bh * a.anchors + chunk / a.anchor_chunks;
-            const float* from = a.dump + (an * 16 + warp) * (KH * 32);
+          if constexpr (DOTS) {
+            // the state before the chunk: S, left by the forward pass, or R, met with it there
+            const int64_t at = (int64_t)bh * a.chunks + chunk;
+            float4* kept = reinterpret_cast<float4*>(a.dump) + (at * CF::kHolders + part * CF::kQuads + quad) * (KH * 8) + lane;
+            if (!a.reverse) {
 #pragma unroll
-            for (int c = 0; c < KH; c += 4) {
-              const float4 x = reinterpret_cast<const float4*>(from)[c / 4 * 32 + lane];
-              sum += pair_lo(S[c / 2]) * x.x + pair_hi(S[c / 2]) * x.y + pair_lo(S[c / 2 + 1]) * x.z + pair_hi(S[c / 2 + 1]) * x.w;
+              for (int c = 0; c < KH; c += 4)
+                __stcs(kept + c / 4 * 32, make_float4(pair_lo(S[c / 2]), pair_hi(S[c / 2]), pair_lo(S[c / 2 + 1]), pair_hi(S[c / 2 + 1])));
+            } else {
+              if (cc + 1 < p.last && lane < KH)  // the next chunk's, 128 bytes a lane
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(kept - lane - CF::kHolders * (KH * 8) + lane * 8));
+              float sum = 0.f;
+#pragma unroll
+              for (int c = 0; c < KH; c += 4) {
+                const float4 x = __ldcs(kept + c / 4 * 32);
+                sum += pair_lo(S[c / 2]) * x.x + pair_hi(S[c / 2]) * x.y + pair_lo(S[c / 2 + 1]) * x.z + pair_hi(S[c / 2 + 1]) * x.w;
+              }
+#pragma unroll
+              for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
+              if (lane == 0) a.flow[at * 16 + part * CF::kQuads + quad] = sum;
             }
-#pragma unroll
-            for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
-            if (lane == 0) a.anchor[an * 16 + warp] = sum;
           }
           la_wait(full_f(rf.i), rf.full(), dead);
           const float decay = fac[CF::kFacFloats - 4];
@@ -1025,27 +1037,82 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           }
           tc5_fence_before();
           arrive(b_free(inc));
-          float o[2][8];
+          float o[2][8], sum[4];
           if (!STATES) {
-            la_wait(b_o, n & 1, dead);
-            tc5_fence_after();
-            uint32_t x1[2][8], x2[2][8];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              tmem_ld_rows16(x1[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO1 + part * 16);
-              tmem_ld_rows16(x2[e], lanes + ((uint32_t)(e * 16) << 16) + CF::cO2 + part * 16);
-            }
             float2 f[2];
 #pragma unroll
             for (int i2 = 0; i2 < 2; ++i2)
               f[i2] = *reinterpret_cast<const float2*>(fac + 2 * kLaChunk + part * 16 + i2 * 8 + 2 * (lane % 4));
+            const auto read = [&](uint32_t (&y)[2][8], int column) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              tmem_wait_ld(x1[e]);
-              tmem_wait_ld(x2[e]);
+              for (int e = 0; e < 2; ++e) tmem_ld_rows16(y[e], lanes + ((uint32_t)(e * 16) << 16) + column + part * 16);
+            };
+            uint32_t x1[2][8], x2[2][8];
+            if constexpr (DOTS) {
+              // the part from the state first: its products with the rows of x
+              uint4 xrow[2];
+              const char* xp = la_row(a.x, b, tw + tok, h, sizeof(T)) + c8 * (int)sizeof(T);
+              const int64_t xs = 8 * (int64_t)sizeof(T) * a.x.st;
+              if (fast_x) {
 #pragma unroll
-              for (int i2 = 0; i2 < 8; ++i2)
-                o[e][i2] = fmaf(__uint_as_float(x2[e][i2]), i2 % 2 ? f[i2 / 4].y : f[i2 / 4].x, __uint_as_float(x1[e][i2]));
+                for (int i2 = 0; i2 < 2; ++i2) {
+                  xrow[i2] = make_uint4(0, 0, 0, 0);
+                  if (tw + i2 * 8 + tok < len && c8 < a.dv) xrow[i2] = *reinterpret_cast<const uint4*>(xp + i2 * xs);
+                }
+                // the next chunk's rows are asked for in L2
+                const int ahead = a.reverse ? -8 : 8;  // in steps of 8 tokens
+                if (cc + 1 < p.last && c8 < a.dv && tw + ahead * 8 + 8 + tok < len) {
+                  asm volatile("prefetch.global.L2 [%0];\n" ::"l"(xp + ahead * xs));
+                  asm volatile("prefetch.global.L2 [%0];\n" ::"l"(xp + (ahead + 1) * xs));
+                }
+              }
+              la_wait(b_o, n & 1, dead);
+              tc5_fence_after();
+              read(x2, CF::cO2);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                tmem_wait_ld(x2[e]);
+#pragma unroll
+                for (int i2 = 0; i2 < 8; ++i2) o[e][i2] = __uint_as_float(x2[e][i2]) * (i2 % 2 ? f[i2 / 4].y : f[i2 / 4].x);
+              }
+              if (__builtin_expect(fast_x, CF::kBf16)) {
+                // through the stage into the order of o
+#pragma unroll
+                for (int i2 = 0; i2 < 2; ++i2) {
+                  *reinterpret_cast<uint4*>(mine) = xrow[i2];
+                  __syncwarp();
+                  uint32_t x4[4];
+                  load_blocks_t(blocks, x4);
+                  __syncwarp();
+                  uint64_t y = 0;
+#pragma unroll
+                  for (int u = 0; u < 4; ++u)
+                    y = fma2(pair(o[u / 2][4 * i2 + 2 * (u % 2)], o[u / 2][4 * i2 + 2 * (u % 2) + 1]), from_bf16x2(x4[u]), y);
+                  sum[2 * i2] = pair_lo(y), sum[2 * i2 + 1] = pair_hi(y);
+                }
+              } else if constexpr (!FAST) {
+                la_dots<T>(sum, a, o, b, h, tw, len, quad * 32, lane);
+              }
+              read(x1, CF::cO1);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                tmem_wait_ld(x1[e]);
+#pragma unroll
+                for (int i2 = 0; i2 < 8; ++i2) o[e][i2] += __uint_as_float(x1[e][i2]);
+              }
+            } else {
+              la_wait(b_o, n & 1, dead);
+              tc5_fence_after();
+              read(x1, CF::cO1);
+              read(x2, CF::cO2);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                tmem_wait_ld(x1[e]);
+                tmem_wait_ld(x2[e]);
+#pragma unroll
+                for (int i2 = 0; i2 < 8; ++i2)
+                  o[e][i2] = fmaf(__uint_as_float(x2[e][i2]), i2 % 2 ? f[i2 / 4].y : f[i2 / 4].x, __uint_as_float(x1[e][i2]));
+              }
             }
             if (cc + 1 < p.last) give_state();
           }
@@ -1068,39 +1135,6 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             la_emit<T, FAST>(a, o, b, h, tw, len, quad * 32, lane);
           }
           if (DOTS) {
-            float sum[4];
-            if (__builtin_expect(fast_x, CF::kBf16)) {
-              // the rows of x the other way through the stage, into the order of o; the next
-              // chunk's are asked for in L2
-              const char* xp = la_row(a.x, b, tw + tok, h, 2) + c8 * 2;
-              const int64_t xs = 16 * a.x.st;
-              uint4 xrow[2];
-#pragma unroll
-              for (int i2 = 0; i2 < 2; ++i2) {
-                xrow[i2] = make_uint4(0, 0, 0, 0);
-                if (tw + i2 * 8 + tok < len && c8 < a.dv) xrow[i2] = *reinterpret_cast<const uint4*>(xp + i2 * xs);
-              }
-              const int ahead = a.reverse ? -8 : 8;  // in steps of 8 tokens
-              if (cc + 1 < p.last && c8 < a.dv && tw + ahead * 8 + 8 + tok < len) {
-                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(xp + ahead * xs));
-                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(xp + (ahead + 1) * xs));
-              }
-#pragma unroll
-              for (int i2 = 0; i2 < 2; ++i2) {
-                *reinterpret_cast<uint4*>(mine) = xrow[i2];
-                __syncwarp();
-                uint32_t x4[4];
-                load_blocks_t(blocks, x4);
-                __syncwarp();
-                uint64_t y = 0;
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  y = fma2(pair(o[u / 2][4 * i2 + 2 * (u % 2)], o[u / 2][4 * i2 + 2 * (u % 2) + 1]), from_bf16x2(x4[u]), y);
-                sum[2 * i2] = pair_lo(y), sum[2 * i2 + 1] = pair_hi(y);
-              }
-            } else if constexpr (!FAST) {
-              la_dots<T>(sum, a, o, b, h, tw, len, quad * 32, lane);
-            }
             // the lanes with the same tokens are 4, 8 and 16 apart
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -1113,14 +1147,6 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
                 if (t < len) a.dots[((int64_t)bh * a.seqlen + t) * 4 + quad] = sum[e];
               }
             }
-          }
-          if (DOTS && __builtin_expect(!a.reverse && anchor_here, 0)) {
-            const int64_t an = (int64_t)bh * a.anchors + chunk / a.anchor_chunks;
-            float* to = a.dump + (an * 16 + warp) * (KH * 32);
-#pragma unroll
-            for (int c = 0; c < KH; c += 4)
-              reinterpret_cast<float4*>(to)[c / 4 * 32 + lane] =
-                  make_float4(pair_lo(S[c / 2]), pair_hi(S[c / 2]), pair_lo(S[c / 2 + 1]), pair_hi(S[c / 2 + 1]));
           }
         }
         if (p.to_carry) {
@@ -1225,66 +1251,6 @@ linattn_share_kernel(const float* part, T* out, const int* lengths, I seqlen, I 
     *to = __float2bfloat16_rn(s[0]);
   else
     *to = s[0];
-}
-
-// dg_t = sum_{s = t..e} (q_s . dq_s - k_s . dk_s) + <R_e, S_e>, e the next anchor at or
-// behind t, R_e what the later tokens send back to the state S_e.  Each anchor's
-// sums start anew, so that what cancels in the differences is no longer than the
-// stretch between two.  One block a stretch, the same number of tokens a thread; sums
-// in fp64.  Keys of at most 64 fill two lane quadrants of the partial products, wider
-// ones four.  The first token's gradient is zero where the states start from zero: its
-// terms cancel, and their roundings are not left in the place of it.
-constexpr int kLaGradThreads = 256;
-template <typename T>
-__global__ void __launch_bounds__(kLaGradThreads)
-linattn_decay_grad_kernel(const float* dots_q, const float* dots_k, const float* anchor, T* out, const int* lengths,
-                          int heads, int seqlen, int anchors, int anchor_tokens, bool two_quads, bool from_zero) {
-  __shared__ double warp_sum[kLaGradThreads / 32];
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int bh = blockIdx.x / anchors, an = blockIdx.x % anchors;
-  const int b = bh / heads, h = bh % heads;
-  int len = lengths ? lengths[b] : seqlen;
-  len = len < 0 ? 0 : len < seqlen ? len : seqlen;
-  const int64_t begin = (int64_t)an * anchor_tokens;
-  if (begin >= len) return;
-  const int end = begin + anchor_tokens < len ? (int)(begin + anchor_tokens) : len;
-  // thread 0 has the latest tokens; each goes back from its own latest
-  const int per = (anchor_tokens + kLaGradThreads - 1) / kLaGradThreads;
-  const int last = end - 1 - tid * per;
-  const float4* rq = reinterpret_cast<const float4*>(dots_q) + (int64_t)bh * seqlen;
-  const float4* rk = reinterpret_cast<const float4*>(dots_k) + (int64_t)bh * seqlen;
-  auto term = [&](int t) {
-    const float4 q = rq[t], k = rk[t];
-    double x = ((double)q.x + q.y) - ((double)k.x + k.y);
-    if (!two_quads) x += ((double)q.z + q.w) - ((double)k.z + k.w);
-    return x;
-  };
-  double mine = 0.0;
-#pragma unroll 4
-  for (int i = 0; i < per; ++i)
-    if (last - i >= begin) mine += term(last - i);
-  double upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const double up = __shfl_up_sync(kFullMask, upto, o);
-    if (lane >= o) upto += up;
-  }
-  if (lane == 31) warp_sum[warp] = upto;
-  __syncthreads();
-  double x = upto - mine;
-  for (int i = 0; i < warp; ++i) x += warp_sum[i];
-  for (int i = 0; i < 16; ++i)
-    if (!two_quads || i % 4 < 2) x += anchor[((int64_t)bh * anchors + an) * 16 + i];
-#pragma unroll 4
-  for (int i = 0; i < per; ++i) {
-    const int t = last - i;
-    if (t < begin) break;
-    x += term(t);
-    if (from_zero && t == 0) x = 0.0;
-    T* to = out + ((int64_t)b * seqlen + t) * heads + h;
-    if constexpr (sizeof(T) == 2) *to = __float2bfloat16_rn((float)x);
-    else *to = (float)x;
-  }
 }
 
 }  // namespace ssscan

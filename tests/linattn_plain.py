@@ -61,3 +61,29 @@ def backward(q, k, v, g, do, scale=1.0, s0=None, dlast=None, lengths=None):
     share = (qk_heads, heads // qk_heads)
     return {"dq": dq.unflatten(2, share).sum(3), "dk": dk.unflatten(2, share).sum(3), "dv": dv, "dlog_decay": dg,
             "dinitial_state": r, "dq_h": dq, "dk_h": dk}
+
+
+def decay_grad_bound(q, k, v, g, do, scale=1.0, s0=None, dlast=None, lengths=None):
+    """(dlog_decay in 64 bits, what it may be off by before it is rounded).
+
+    dg_t is a plain sum of products q do k v e^{sum of g}, without a difference that
+    cancels.  A product is formed of a few rounded factors: the score or the state (planes
+    of 16 bits for bf16 inputs, 24 for fp32) twice 2^-16 or 2^-24, an exponential good to
+    2^-22 twice, and fp32 multiplications; in all below u = 2^-14 (bf16) or 2^-19 (fp32)
+    with the fp32 sums' share.  Inputs of random signs have roundings of random signs, so
+    the sum is off by about u times the root of the sum of squared products, and eight
+    times that is hardly ever passed.  That sum is the same gradient over squared inputs.
+    """
+    u = 2.0 ** -14 if q.dtype == torch.bfloat16 else 2.0 ** -19
+    sq = lambda t: None if t is None else t.double() ** 2  # noqa: E731
+    ref = backward(q, k, v, g, do, scale, s0, dlast, lengths)["dlog_decay"]
+    squares = backward(sq(q), sq(k), sq(v), 2 * g.double(), sq(do), scale ** 2, sq(s0), sq(dlast), lengths)["dlog_decay"]
+    return ref, 8 * u * squares.sqrt()
+
+
+def decay_grad_wrong(got, ref, slack, dtype):
+    """How many elements of a decay's gradient are further off than the bound and one rounding to `dtype`."""
+    half = torch.finfo(dtype).eps / 2
+    over = (got.double() - ref).abs() - (1 + half) * slack - half * ref.abs()
+    # an exponential below the smallest normal number is zero, whatever up to 2^16 it multiplies
+    return int((~(over <= 2.0 ** -110)).sum())

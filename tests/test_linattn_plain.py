@@ -61,3 +61,23 @@ def test_gradients_are_differences(lengths):
         got = float((grads[of] * along).sum())
         # central differences: eps^2 times third derivatives of order one to a hundred
         assert abs(diff - got) <= 1e-7 * max(1.0, abs(got)), name
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("decay", [0.05, 2.0])
+def test_the_decay_gradients_bound_rejects_mistakes(dtype, decay):
+    """A flow through one border of 64 tokens left out, a wrong sign, a zero, a bf16 sum: none passes."""
+    gen = torch.Generator().manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    L, d = 400, 16
+    q, k, v, do = (r(1, L, 1, d).to(dtype) for _ in range(4))
+    g, s0 = (-decay * r(1, L, 1).abs()).to(dtype), r(1, 1, d, d)
+    ref, slack = P.decay_grad_bound(q, k, v, g, do, 0.25, s0)
+    assert P.decay_grad_wrong(ref.to(dtype), ref, slack, dtype) == 0
+    assert P.decay_grad_wrong(0 * ref, ref, slack, dtype) > 0.9 * L
+    assert P.decay_grad_wrong(-ref, ref, slack, dtype) > 0.9 * L
+    lost = ref.clone()
+    lost[:, 128:192] -= P.backward(q, k, v, g, do, 0.25, s0)["dlog_decay"][:, 192:193]  # the flow at one border
+    assert P.decay_grad_wrong(lost.to(dtype), ref, slack, dtype) > 32
+    if dtype == torch.float32:
+        assert P.decay_grad_wrong(ref.bfloat16(), ref, slack, dtype) > 0.5 * L
