@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import math
 import os
 import threading
@@ -140,6 +141,45 @@ def _stream_handle(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_its_stream(fn):
+    """`stream` of a call: a torch stream or a raw handle on the operands' device; None, the
+    current one.
+
+    The call runs with that stream current, so that its fills, its launches and the
+    allocator's reuse of its workspace keep the stream's order; what it allocates and
+    returns is marked as used by the caller's current stream too (which has to wait for
+    the other before it reads, as ever).
+    """
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        args, kwargs = args[:at], {n: x for n, x in kwargs.items() if n != "stream"}
+        given = [x for x in (*args, *kwargs.values()) if isinstance(x, torch.Tensor)]
+        device = next((x.device for x in given if x.is_cuda), None)
+        if device is None:
+            return fn(*args, **kwargs)  # refuses them
+        handle = _stream_handle(stream, device)
+        if handle == torch._C._cuda_getCurrentRawStream(device.index):
+            return fn(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(handle, device=device)
+        if stream.device != device:
+            raise ValueError(f"stream must be one of {device}")
+        before = torch.cuda.current_stream(device)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kwargs)
+        for x in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+            if isinstance(x, torch.Tensor) and not any(x is y for y in given):
+                x.record_stream(before)
+        return out
+
+    return call
+
+
 def ss_last_device_error(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device error status."""
     return load_library().ss_last_device_error(_stream_handle(stream, None))
@@ -160,6 +200,7 @@ def ss_debug_fwd_kernels(batch: int, dim: int, seqlen: int, dstate: int, in_dtyp
     return n
 
 
+@_on_its_stream
 def ss_debug_pointwise(fn: int, x, stream=None):
     """Evaluate one of the kernels' pointwise functions on a CUDA float32 tensor
     (test hook, include/ss_scan_debug.h); returns a new tensor."""
@@ -257,6 +298,7 @@ def _fwd_call(name, initial_state, u, delta, A, B, C, D, z, delta_bias, softplus
     return y_out, last_state_out
 
 
+@_on_its_stream
 def ss_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
                 y_out=None, last_state_out=None, return_last_state=True,
                 workspace=None, stream=None):
@@ -272,6 +314,7 @@ def ss_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=Tru
                      last_state_out, return_last_state, workspace, stream)
 
 
+@_on_its_stream
 def ss_scan_fwd_from_state(initial_state, u, delta, A, B, C, D=None, z=None, delta_bias=None,
                            softplus=True, y_out=None, last_state_out=None,
                            return_last_state=True, workspace=None, stream=None):
@@ -282,6 +325,7 @@ def ss_scan_fwd_from_state(initial_state, u, delta, A, B, C, D=None, z=None, del
                      stream)
 
 
+@_on_its_stream
 def ss_scan_fwd_zoh(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
                     y_out=None, last_state_out=None, return_last_state=True, workspace=None,
                     stream=None):
@@ -290,6 +334,7 @@ def ss_scan_fwd_zoh(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus
                      last_state_out, return_last_state, workspace, stream)
 
 
+@_on_its_stream
 def ss_scan_fwd_conv(x, conv_weight, delta, A, B, C, D=None, z=None, delta_bias=None,
                      conv_bias=None, softplus=True, y_out=None, last_state_out=None,
                      return_last_state=True, workspace=None, stream=None):
@@ -309,6 +354,7 @@ def ss_scan_bwd_workspace_bytes(batch: int, dim: int, seqlen: int, dstate: int) 
     return n
 
 
+@_on_its_stream
 def ss_scan_fwd_train(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
                       y_out=None, last_state_out=None, checkpoints=None, return_last_state=True,
                       workspace=None, stream=None):
@@ -327,6 +373,7 @@ def ss_scan_fwd_train(u, delta, A, B, C, D=None, z=None, delta_bias=None, softpl
     return y, h, checkpoints
 
 
+@_on_its_stream
 def ss_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, softplus=True,
                 dlast_state=None, checkpoints=None, workspace=None, stream=None):
     """Gradients of ss_scan_fwd for an upstream dy [batch, dim, L] float32.
@@ -364,6 +411,7 @@ def ss_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, softplus
     return g
 
 
+@_on_its_stream
 def ss_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
                  y_out=None, stream=None):
     """One recurrent (decode) step; advances state [batch, dim, N] float32 in place.
@@ -401,6 +449,7 @@ def ss_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, soft
     return y_out
 
 
+@_on_its_stream
 def ss_scan_fwd_noalloc(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
                         y_out=None, last_state_out=None, stream=None):
     """ss_scan_fwd without a workspace: the library's static scratch array is used.
@@ -505,13 +554,10 @@ def _in_dtype(q):
     return dt
 
 
-def _call(fn, where, device, stream, *args):
-    """fn(*args, stream) with the operands' device current."""
+def _call(fn, where, device, *args):
+    """fn(*args, the device's current stream) with the operands' device current."""
     index = device.index
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        handle = _stream_handle(stream, device)
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         st = fn(*args, handle)
     else:
@@ -576,6 +622,7 @@ def _workspace(workspace, need, device):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+@_on_its_stream
 def ss_linattn_fwd(q, k, v, log_decay, scale=1.0, initial_state=None, lengths=None, o_out=None,
                    last_state_out=None, return_last_state=True, workspace=None, stream=None):
     """Linear attention with one decay per head over a whole prompt:
@@ -606,11 +653,12 @@ def ss_linattn_fwd(q, k, v, log_decay, scale=1.0, initial_state=None, lengths=No
     else:
         last_ptr = _dense("last_state_out", last_state_out, device, f32, shape)
     keep, ws, ws_bytes = _workspace(workspace, need, device)
-    _call(lib.ss_linattn_fwd, "ss_linattn_fwd", device, stream, *ops, scale, states, rows, o_ptr,
+    _call(lib.ss_linattn_fwd, "ss_linattn_fwd", device, *ops, scale, states, rows, o_ptr,
           last_ptr, *sizes, ws, ws_bytes)
     return o_out, last_state_out
 
 
+@_on_its_stream
 def ss_linattn_bwd(q, k, v, log_decay, do, scale=1.0, initial_state=None, dlast_state=None,
                    lengths=None, workspace=None, stream=None):
     """Gradients of ss_linattn_fwd for an upstream do [batch, L, heads, dv] (the inputs' dtype,
@@ -634,11 +682,12 @@ def ss_linattn_bwd(q, k, v, log_decay, do, scale=1.0, initial_state=None, dlast_
          "dv": make((batch, L, heads, dv)), "dlog_decay": make((batch, L, heads)),
          "dinitial_state": None if initial_state is None else torch.empty_like(initial_state)}
     keep, ws, ws_bytes = _workspace(workspace, need, device)
-    _call(lib.ss_linattn_bwd, "ss_linattn_bwd", device, stream, *ops, scale, *states,
+    _call(lib.ss_linattn_bwd, "ss_linattn_bwd", device, *ops, scale, *states,
           *[_ptr(t) for t in g.values()], *sizes, ws, ws_bytes)
     return g
 
 
+@_on_its_stream
 def ss_linattn_step(state, q, k, v, log_decay, scale=1.0, slots=None, o_out=None, stream=None):
     """One token of ss_linattn_fwd for every sequence; advances the states in place.
 
@@ -665,7 +714,7 @@ def ss_linattn_step(state, q, k, v, log_decay, scale=1.0, slots=None, o_out=None
         o_ptr = o_out.data_ptr()
     else:
         o_ptr = _dense("o_out", o_out, device, dtype, out)
-    _call(lib.ss_linattn_step, "ss_linattn_step", device, stream,
+    _call(lib.ss_linattn_step, "ss_linattn_step", device,
           _heads3("q", q, device, dtype, shape), _heads3("k", k, device, dtype, shape),
           _heads3("v", v, device, dtype, out), _heads3("log_decay", log_decay, device, dtype, (batch, heads)),
           scale, _dense("state", state, device, torch.float32, pool), num_slots,
@@ -688,6 +737,7 @@ def _pool_operands(what, codes, scales, slots):
     return device, batch, shape[1:], ptrs
 
 
+@_on_its_stream
 def ss_state_store8(state, codes, scales, slots=None, stream=None):
     """Store states [batch, ..., width] float32 (the scan's [batch, dim, N], the attention's
     [batch, heads, dk, dv]) into a pool in 8 bits: codes [num_slots, ..., width] int8, scales
@@ -699,11 +749,12 @@ def ss_state_store8(state, codes, scales, slots=None, stream=None):
     device, batch, shape, ptrs = _pool_operands("ss_state_store8", codes, scales, slots)
     if batch is None:
         batch = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() else 0
-    _call(lib.ss_state_store8, "ss_state_store8", device, stream,
+    _call(lib.ss_state_store8, "ss_state_store8", device,
           _dense("state", state, device, torch.float32, (batch, *shape)), *ptrs, batch,
           math.prod(shape[:-1]), shape[-1])
 
 
+@_on_its_stream
 def ss_state_load8(codes, scales, slots=None, state_out=None, stream=None):
     """States read back from the pool of ss_state_store8 as [batch, ..., width] float32.
     slots: [batch] int32 (None: every slot, in order); a slot outside the pool gives a zero
@@ -718,6 +769,6 @@ def ss_state_load8(codes, scales, slots=None, state_out=None, stream=None):
         out = state_out.data_ptr()
     else:
         out = _dense("state_out", state_out, device, torch.float32, whole)
-    _call(lib.ss_state_load8, "ss_state_load8", device, stream, *ptrs, out, batch,
+    _call(lib.ss_state_load8, "ss_state_load8", device, *ptrs, out, batch,
           math.prod(shape[:-1]), shape[-1])
     return state_out

@@ -148,3 +148,51 @@ def test_the_binding_runs_on_cuda_tensors_only(lib):
                  lambda: N.ss_state_store8(state, codes, scales), lambda: N.ss_state_load8(codes, scales)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_a_call_runs_with_its_stream_current(monkeypatch):
+    """The `stream` of a call is the current one while it allocates, fills and launches (shown with stand-ins)."""
+    import contextlib
+
+    import selective_state_space_ss_b200 as ss
+
+    log, now = [], ["main"]
+
+    class Stream:
+        def __init__(self, name):
+            self.cuda_stream, self.device = name, "gpu"
+
+    @contextlib.contextmanager
+    def entered(s):
+        old, now[0] = now[0], s.cuda_stream
+        yield
+        now[0] = old
+
+    class T(torch.Tensor):
+        is_cuda, device = True, type("D", (), {"index": 0, "__eq__": lambda a, b: b == "gpu" or a is b, "__hash__": None})()
+
+        def record_stream(self, s):
+            log.append(("used on", s.cuda_stream))
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", entered)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: Stream(now[0]))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: now[0], raising=False)
+    make = lambda: torch.zeros(1).as_subclass(T)  # noqa: E731
+
+    @N._on_its_stream
+    def f(x, out=None, stream=None):
+        assert stream is None
+        log.append(("runs on", now[0]))
+        return (make() if out is None else out, None)
+
+    given = make()
+    f(make())
+    f(make(), stream=Stream("side"))
+    f(make(), given, Stream("side"))
+    f(make(), stream=Stream("main"))
+    assert log == [("runs on", "main"), ("runs on", "side"), ("used on", "main"), ("runs on", "side"), ("runs on", "main")]
+    for name in dir(ss):  # every public call that takes one
+        fn = getattr(ss, name)
+        if callable(fn) and name.startswith("ss_") and name != "ss_last_device_error" and "stream" in getattr(fn, "__code__", f.__code__).co_varnames:
+            assert hasattr(fn, "__wrapped__"), name
