@@ -75,8 +75,12 @@ namespace ssscan {
 
 constexpr int kLaChunk = 64;
 constexpr int kLaBlock = kLaChunk * kTileRow;  // bytes of one plane's 64 x 64 block
-constexpr uint32_t kLaSpinLimit = 1u << 9;        // polls of a barrier: a few seconds
-constexpr uint32_t kLaCarrySpinLimit = 1u << 24;  // of the previous worker's flag: likewise
+// Polls before a wait gives up, a second or so.  A poll of a barrier suspends the thread
+// for as long as the hardware likes, 3 to 4 us whatever longer time it is given; a poll of
+// the previous worker's flag takes about as many tenths.  (512 polls of the first gave up
+// after 2 ms, which a worker may well wait for a state where the rows between are short.)
+constexpr uint32_t kLaSpinLimit = 1u << 18;
+constexpr uint32_t kLaCarrySpinLimit = 1u << 21;
 
 // A [batch, seqlen, heads, d] tensor, last axis contiguous, strides in elements;
 // `share` consecutive heads of the pass read one of its heads.
@@ -179,8 +183,8 @@ constexpr int kLaBackWarps = 16, kLaFrontWarps = 8;
 constexpr int kLaMmaWarp = 24, kLaLoadWarp = 25, kLaMmaOrLoadWarp = 26, kLaDecayWarp = 27;
 
 // Waits of one CTA: when one gives up, the others stop waiting too, and the kernel
-// runs to its end on whatever is there, inside its buffers.  A poll may suspend the
-// thread for up to 10 ms, so that those that wait leave the issue slots to the others.
+// runs to its end on whatever is there, inside its buffers.  A poll suspends the
+// thread, so that those that wait leave the issue slots to the others.
 __device__ __forceinline__ void la_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
 #pragma unroll 1
   for (uint32_t i = 0; i < kLaSpinLimit; ++i) {
