@@ -2,8 +2,8 @@
  * ss_scan_debug.h -- test hooks of libssscan.so.  Not for production use.
  *
  * Each setting is picked up by the NEXT ss_scan_fwd (SS_DEBUG_STEP_SIMPLE:
- * ss_scan_step) call in the process and
- * then cleared (ss_scan_workspace_bytes honours a pending worker count, so a
+ * ss_scan_step; SS_DEBUG_LINATTN_...: ss_linattn_fwd or ss_linattn_bwd) call in the
+ * process and then cleared (ss_scan_workspace_bytes honours a pending worker count, so a
  * test can size the workspace for it).  They exist so that tests can drive the
  * load-balanced schedule and its bounded carry waits on small problems:
  *
@@ -25,6 +25,12 @@
  *                           of chunks; 1: none), so the carry-in correction
  *                           runs on problems small enough to check in full.
  *                           Ignored by the training forward.
+ *   SS_DEBUG_LINATTN_SPIN_LIMIT, SS_DEBUG_LINATTN_SKIP_PUBLISH  the same two for the
+ *                           next ss_linattn_fwd or ss_linattn_bwd (all its launches) where
+ *                           there are more heads than SMs.
+ *   SS_DEBUG_LINATTN_SKIP_LOAD  value = a chunk of 64 tokens whose values are never
+ *                           loaded in that call: waits for them run out after a
+ *                           second or so.
  *   SS_DEBUG_CLEAR          value ignored: drop every pending setting.
  *
  * Returns SS_OK, or SS_ERR_INVALID_ARG for an unknown `what`.  Host-only,
@@ -45,7 +51,10 @@ enum {
   SS_DEBUG_SKIP_PUBLISH = 2,
   SS_DEBUG_SPIN_LIMIT = 3,
   SS_DEBUG_STEP_SIMPLE = 4,
-  SS_DEBUG_FORCE_SEGMENTS = 5
+  SS_DEBUG_FORCE_SEGMENTS = 5,
+  SS_DEBUG_LINATTN_SPIN_LIMIT = 6,
+  SS_DEBUG_LINATTN_SKIP_PUBLISH = 7,
+  SS_DEBUG_LINATTN_SKIP_LOAD = 8
 };
 
 ss_status ss_debug_inject(int what, long long value);

@@ -11,6 +11,9 @@ from ._native import (  # noqa: F401
     SS_DEBUG_CLEAR,
     SS_DEBUG_FORCE_SEGMENTS,
     SS_DEBUG_FORCE_WORKERS,
+    SS_DEBUG_LINATTN_SKIP_LOAD,
+    SS_DEBUG_LINATTN_SKIP_PUBLISH,
+    SS_DEBUG_LINATTN_SPIN_LIMIT,
     SS_DEBUG_SKIP_PUBLISH,
     SS_DEBUG_SPIN_LIMIT,
     SS_DEBUG_STEP_SIMPLE,

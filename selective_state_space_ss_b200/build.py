@@ -24,8 +24,7 @@ def sources():
 
 def deps():
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + [os.path.join(ROOT, "include", "ss_scan.h"), os.path.join(ROOT, "include", "ss_linattn.h"),
-               os.path.abspath(__file__)])
+            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
 
 
 def source_hash(defines=()) -> str:

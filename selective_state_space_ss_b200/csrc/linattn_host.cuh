@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -219,8 +220,17 @@ ss_status la_segment_states(LaPassArgs a, const LaShape& s, const LaSegs& g, con
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
+// Test hooks (ss_scan_debug.h): consumed by the next forward or backward call.
+std::atomic<long long> g_dbg_la_spin_limit{0};
+std::atomic<long long> g_dbg_la_skip_publish{-1};
+std::atomic<long long> g_dbg_la_skip_load{-1};
+
 LaPassArgs la_base(const LaShape& s, const ss_heads* g, const int32_t* lengths, const LaSegs& segs) {
   LaPassArgs a = {};
+  const long long spin = g_dbg_la_spin_limit.exchange(0);
+  a.carry_spin_limit = spin > 0 ? (uint32_t)spin : kLaCarrySpinLimit;
+  a.skip_publish = (int)g_dbg_la_skip_publish.exchange(-1);
+  a.skip_load = (int)g_dbg_la_skip_load.exchange(-1);
   a.g = la_tensor(*g, 1);
   a.lengths = lengths;
   a.heads = s.heads;

@@ -79,6 +79,7 @@ constexpr int kLaBlock = kLaChunk * kTileRow;  // bytes of one plane's 64 x 64 b
 // for as long as the hardware likes, 3 to 4 us whatever longer time it is given; a poll of
 // the previous worker's flag takes about as many tenths.  (512 polls of the first gave up
 // after 2 ms, which a worker may well wait for a state where the rows between are short.)
+// As a launch's argument the first limit cost 2 to 4%.
 constexpr uint32_t kLaSpinLimit = 1u << 18;
 constexpr uint32_t kLaCarrySpinLimit = 1u << 21;
 
@@ -117,6 +118,9 @@ struct LaPassArgs {
   int out_vec, x_vec;   // 16-byte stores to out, loads of x
   int tma;              // so do the tensor maps
   float scale_p, scale_o, scale_w;
+  uint32_t carry_spin_limit;  // polls before a wait for another worker's state gives up
+  int skip_publish;     // test hooks: a worker that hands nothing on,
+  int skip_load;        // a chunk whose values no CTA loads (-1: none)
 };
 
 struct LaMaps {
@@ -185,20 +189,31 @@ constexpr int kLaMmaWarp = 24, kLaLoadWarp = 25, kLaMmaOrLoadWarp = 26, kLaDecay
 // Waits of one CTA: when one gives up, the others stop waiting too, and the kernel
 // runs to its end on whatever is there, inside its buffers.  A poll suspends the
 // thread, so that those that wait leave the issue slots to the others.
-__device__ __forceinline__ void la_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+__device__ __forceinline__ bool la_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(10000000)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
 #pragma unroll 1
   for (uint32_t i = 0; i < kLaSpinLimit; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(10000000)
-        : "memory");
-    if (ok) return;
-    if (*dead) return;
+    if (la_poll(bar, parity)) return true;
+    if (*dead) return false;
   }
   atomicOr(&g_error_word, kErrTmaWait);
   *dead = 1;
+  return false;
+}
+// Whatever else gave up: for copies and products of one's own that are in flight.
+__device__ __forceinline__ void la_wait_own(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kLaSpinLimit; ++i)
+    if (la_poll(bar, parity)) return;
+  atomicOr(&g_error_word, kErrTmaWait);
 }
 __device__ __forceinline__ void la_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
@@ -576,7 +591,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
     for (int i = 0; i < 2; ++i) la_init(b_ds(i), 1), la_init(b_free(i), CF::kHolders);
     la_init(b_o, 1);
     la_init(b_s, CF::kHolders);
-    la_init(b_end, 1);
+    la_init(b_end, CF::kTwoIssuers ? 2 : 1);
     fence_mbar_init();
     *dead = 0;
     // workers are numbered in the order in which they start, so that the one a
@@ -697,6 +712,9 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         }
         rk.next(), rq.next(), rv.next();
       }
+      // whoever issued products says when they are done: one waits for it below if a wait gave up
+      if (leader) mma_commit(b_end);
+      __syncwarp();
     } else if (warp == kLaDecayWarp) {
       // ---- decays
       LaRing<CF::RF> rf;
@@ -725,6 +743,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
       LaRing<CF::RK> rk;
       LaRing<CF::RQ> rq;
       LaRing<CF::RV> rv;
+      bool gone = false;  // (TMA) a place was not free in time: no further copies
       for (int i = 0; i < work.pieces; ++i) {
         const LaPiece p = la_piece(a, work, i);
         const int hk = p.h / a.k.share, hq = p.h / a.q.share, hv = p.h / a.v.share;
@@ -732,12 +751,15 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           const int t0 = (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk;
           // TMA clips at the tensor's end, not at a row's length
           const bool by_tma = FAST || (CF::kBf16 && a.tma && (t0 + kLaChunk <= p.len || p.len == a.seqlen));
-          auto tile = [&](auto width, const LaTensor& x, const CUtensorMap* map, int hx, int at, bool wait, uint32_t turn,
-                          uint32_t full, uint32_t empty, int d) {
+          auto tile = [&](auto width, const LaTensor& x, const CUtensorMap* map, int hx, int at, auto& ring, uint32_t full,
+                          uint32_t empty, int d) {
             constexpr int DP = decltype(width)::value;
-            if (ltid == 0 && wait) la_wait(empty, turn, dead);
+            if (ltid == 0 && !gone && ring.used()) {
+              const bool free = la_wait(empty, ring.empty(), dead);
+              if (CF::kBf16) gone = !free;
+            }
             if (by_tma) {
-              if (ltid == 0) {
+              if (ltid == 0 && !gone) {
                 la_expect(full, DP / 64 * kLaBlock);
 #pragma unroll
                 for (int j = 0; j < DP / 64; ++j) tma_load_block(base + at + j * kLaBlock, map, full, j * 64, t0, hx, p.b);
@@ -754,25 +776,25 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
               fence_proxy_async_smem();
               __syncwarp();
               if (CF::kLoaders > 32) asm volatile("bar.sync 2, 64;\n" ::: "memory");
-              if (ltid == 0) la_arrive(full);
+              if (ltid == 0 && !gone) la_arrive(full);
             }
+            if (!gone) ring.next();
           };
-          tile(LaWidth<KD>{}, a.k, &maps.k, hk, CF::kK + rk.i * CF::kTileK, rk.used(), rk.empty(), full_k(rk.i),
-               empty_k(rk.i), a.dk);
+          tile(LaWidth<KD>{}, a.k, &maps.k, hk, CF::kK + rk.i * CF::kTileK, rk, full_k(rk.i), empty_k(rk.i), a.dk);
           if (!STATES)
-            tile(LaWidth<KD>{}, a.q, &maps.q, hq, CF::kQ + rq.i * CF::kTileK, rq.used(), rq.empty(), full_q(rq.i),
-                 empty_q(rq.i), a.dk);
-          tile(LaWidth<VD>{}, a.v, &maps.v, hv, CF::kV + rv.i * CF::kTileV, rv.used(), rv.empty(), full_v(rv.i),
-               empty_v(rv.i), a.dv);
-          rk.next(), rq.next(), rv.next();
+            tile(LaWidth<KD>{}, a.q, &maps.q, hq, CF::kQ + rq.i * CF::kTileK, rq, full_q(rq.i), empty_q(rq.i), a.dk);
+          if (c != a.skip_load)
+            tile(LaWidth<VD>{}, a.v, &maps.v, hv, CF::kV + rv.i * CF::kTileV, rv, full_v(rv.i), empty_v(rv.i), a.dv);
         }
       }
-      // where a wait gave up, copies may be in flight still: they are waited for, with a limit
-      if (*dead && ltid == 0) {
+      // the last copies into each place land before the end, also where those that they are
+      // for have given up, or give up yet
+      if (CF::kBf16 && ltid == 0) {
         const auto land = [&](auto& ring, int count, const auto& full) {
+#pragma unroll 1
           for (int i = 0; i < count; ++i) {
             const uint32_t fills = ring.turn + (i < ring.i ? 1 : 0);
-            if (fills > 0) la_wait(full(i), (fills - 1) & 1, dead);
+            if (fills > 0) la_wait_own(full(i), (fills - 1) & 1);
           }
         };
         land(rk, CF::RK, full_k);
@@ -965,7 +987,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           const unsigned* flag = a.flags + 1 + (work.worker - 1) * 16 + warp;
           if (lane == 0) {
             unsigned there = 0;
-            for (uint32_t spin = 0; spin < kLaCarrySpinLimit && !there && !*dead; ++spin) {
+            for (uint32_t spin = 0; spin < a.carry_spin_limit && !there && !*dead; ++spin) {
               asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(there) : "l"(flag) : "memory");
               if (!there) __nanosleep(64);
             }
@@ -1161,7 +1183,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
                    make_float4(pair_lo(S[c / 2]), pair_hi(S[c / 2]), pair_lo(S[c / 2 + 1]), pair_hi(S[c / 2 + 1])));
           __threadfence();
           __syncwarp();
-          if (lane == 0)
+          if (lane == 0 && work.worker != a.skip_publish)
             asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(a.flags + 1 + work.worker * 16 + warp), "r"(1u) : "memory");
         } else if (a.s_out && (STATES || step == a.nseg - 1) && vi < a.dv) {
           float* to = a.s_out + (int64_t)bh * a.s_out_head + step * a.s_out_seg + part * KH * a.sk + vi * a.sv;
@@ -1174,17 +1196,14 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
       }
     }
   }
-  // every MMA was waited for (the last chunk's) unless a wait gave up: then this
-  // commit, waited for with a limit too, stands between those in flight and the end
+  // every MMA was waited for (the last chunk's) unless a wait gave up: then the issuers'
+  // last commits, waited for with a limit too, stand between those in flight and the end
   tc5_fence_before();
   __syncthreads();
   tc5_fence_after();
   if (warp == kLaMmaWarp) {
     if (*dead) {
-      if (lane == 0) {
-        mma_commit(b_end);
-        la_wait(b_end, 0, dead);
-      }
+      if (lane == 0) la_wait_own(b_end, 0);
       __syncwarp();
     }
     tmem_free(tmem, CF::kCols);

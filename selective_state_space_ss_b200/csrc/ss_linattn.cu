@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "ss_linattn.h"
+#include "ss_scan_debug.h"
 #include "linattn_host.cuh"
 
 using namespace ssscan;
@@ -19,6 +20,18 @@ bool take_linattn_error_word(unsigned int* word) {
   if (*word == 0) return true;
   const unsigned int zero = 0;
   return cudaMemcpyToSymbol(g_error_word, &zero, sizeof zero) == cudaSuccess;
+}
+
+// ss_debug_inject's settings of this unit.
+void set_linattn_debug(int what, long long value) {
+  if (what == SS_DEBUG_LINATTN_SPIN_LIMIT) g_dbg_la_spin_limit.store(value);
+  if (what == SS_DEBUG_LINATTN_SKIP_PUBLISH) g_dbg_la_skip_publish.store(value);
+  if (what == SS_DEBUG_LINATTN_SKIP_LOAD) g_dbg_la_skip_load.store(value);
+  if (what == SS_DEBUG_CLEAR) {
+    g_dbg_la_spin_limit.store(0);
+    g_dbg_la_skip_publish.store(-1);
+    g_dbg_la_skip_load.store(-1);
+  }
 }
 
 }  // namespace ssscan

@@ -18,7 +18,9 @@
 using namespace ssscan;
 
 namespace ssscan {
-bool take_linattn_error_word(unsigned int* word);  // ss_linattn.cu
+// ss_linattn.cu
+bool take_linattn_error_word(unsigned int* word);
+void set_linattn_debug(int what, long long value);
 }
 
 // Scratch of ss_scan_fwd_noalloc: one file-scope device array, held by every
@@ -258,7 +260,13 @@ ss_status ss_debug_inject(int what, long long value) {
     case SS_DEBUG_SPIN_LIMIT: g_dbg_spin_limit.store(value); return SS_OK;
     case SS_DEBUG_STEP_SIMPLE: g_dbg_step_simple.store(value); return SS_OK;
     case SS_DEBUG_FORCE_SEGMENTS: g_dbg_segments.store(value); return SS_OK;
+    case SS_DEBUG_LINATTN_SPIN_LIMIT:
+    case SS_DEBUG_LINATTN_SKIP_PUBLISH:
+    case SS_DEBUG_LINATTN_SKIP_LOAD:
+      set_linattn_debug(what, value);
+      return SS_OK;
     case SS_DEBUG_CLEAR:
+      set_linattn_debug(what, 0);
       g_dbg_segments.store(0);
       g_dbg_step_simple.store(0);
       g_dbg_workers.store(0);

@@ -196,3 +196,10 @@ def test_a_call_runs_with_its_stream_current(monkeypatch):
         fn = getattr(ss, name)
         if callable(fn) and name.startswith("ss_") and name != "ss_last_device_error" and "stream" in getattr(fn, "__code__", f.__code__).co_varnames:
             assert hasattr(fn, "__wrapped__"), name
+
+
+def test_the_waits_hooks_are_known(lib):
+    for what in (N.SS_DEBUG_LINATTN_SPIN_LIMIT, N.SS_DEBUG_LINATTN_SKIP_PUBLISH, N.SS_DEBUG_LINATTN_SKIP_LOAD):
+        assert lib.ss_debug_inject(what, 3) == N.SS_OK
+    assert lib.ss_debug_inject(N.SS_DEBUG_CLEAR, 0) == N.SS_OK
+    assert lib.ss_debug_inject(N.SS_DEBUG_LINATTN_SKIP_LOAD + 1, 0) == N.SS_ERR_INVALID_ARG
