@@ -81,3 +81,20 @@ def test_the_decay_gradients_bound_rejects_mistakes(dtype, decay):
     assert P.decay_grad_wrong(lost.to(dtype), ref, slack, dtype) > 32
     if dtype == torch.float32:
         assert P.decay_grad_wrong(ref.bfloat16(), ref, slack, dtype) > 0.5 * L
+
+
+def test_what_bounds_the_state_of_bf16_prompts():
+    """Keys weighted by their decay and kept as bf16 planes: two leave the state more than 2^-20 off, three do not."""
+    gen = torch.Generator().manual_seed(1)
+    L, d = 64, 64
+    k, v = (torch.randn(L, d, generator=gen).bfloat16().double() for _ in range(2))
+    w = torch.exp(torch.cumsum(-0.1 * torch.rand(L, generator=gen).double(), 0)).flip(0)
+    ref = (k * w[:, None]).mT @ v
+    off = []
+    for planes in (2, 3):
+        kept, rest = torch.zeros_like(k), k * w[:, None]
+        for _ in range(planes):
+            p = rest.bfloat16().double()
+            kept, rest = kept + p, rest - p
+        off.append(float((kept.mT @ v - ref).norm() / ref.norm()))
+    assert off[0] > 2.0 ** -20 > 16 * off[1]
