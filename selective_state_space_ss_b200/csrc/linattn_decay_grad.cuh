@@ -73,7 +73,8 @@ __device__ __forceinline__ void la_grad_tile(char* to, const LaTensor& x, int64_
 #pragma unroll
     for (int row = row0; row < row0 + kLaChunk; row += kLaGradThreads / 8) {
       const int col = unit * N;
-      const bool in = t0 + row < len && col < d;
+      const bool in = t0 + row < len && col < d &&
+                      la_inside(x, base + row * step + col * (int)sizeof(T), d - col < N ? d - col : N, sizeof(T));
       const char* from = base + (in ? row * step + col * (int)sizeof(T) : 0);
       char* at = to + la_grad_unit(row, unit, bytes);
       if constexpr (VEC) {
@@ -188,12 +189,13 @@ __global__ void __launch_bounds__(kLaGradThreads) linattn_decay_grad_kernel(cons
   if (warp == 0) {  // it has the fewest products
     T g[2];
     la_fetch_decays<T>(g, a.g, b, h, t0, len, 0, lane);
-    float all = lane < (a.dk <= 64 ? 8 : 16) ? a.flow[(bh * a.chunks + chunk) * 16 + lane] : 0.f;
+    const int64_t rows = (int64_t)gridDim.x / a.chunks, at16 = (bh * a.chunks + chunk) * 16 + lane;  // batch x heads
+    float all = lane < (a.dk <= 64 ? 8 : 16) && in_range(at16, rows * a.chunks * 16) ? a.flow[at16] : 0.f;
     float s[2][2];  // a and b of two tokens
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = t0 + 2 * lane + i;
-      const bool in = t < len && in_range(t, a.seqlen);
+      const bool in = t < len && in_range(bh * a.seqlen + t, rows * a.seqlen);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {  // two quadrants hold keys of at most 64, four wider ones
         const float4 y = in ? reinterpret_cast<const float4*>(e ? a.dots_k : a.dots_q)[bh * a.seqlen + t]
@@ -277,13 +279,13 @@ __global__ void __launch_bounds__(kLaGradThreads) linattn_decay_grad_kernel(cons
   *reinterpret_cast<float2*>(part[warp] + lane / 4 * 8 + c * 2) = make_float2(p[0][0], p[0][1]);
   __syncthreads();
   const int t = t0 + (int)threadIdx.x;
-  if (threadIdx.x < kLaChunk && t < len && in_range(t, a.seqlen)) {
+  const int64_t to = ((int64_t)b * a.seqlen + t) * a.heads + h;
+  if (threadIdx.x < kLaChunk && t < len && in_range(to, (int64_t)gridDim.x / a.chunks * a.seqlen)) {
     float s = rest[threadIdx.x];
 #pragma unroll
     for (int w = 0; w < 4; ++w) s += part[w][threadIdx.x];
-    T* to = static_cast<T*>(a.out) + ((int64_t)b * a.seqlen + t) * a.heads + h;
-    if constexpr (sizeof(T) == 2) *to = __float2bfloat16_rn(s);
-    else *to = s;
+    if constexpr (sizeof(T) == 2) static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(s);
+    else static_cast<float*>(a.out)[to] = s;
   }
 }
 

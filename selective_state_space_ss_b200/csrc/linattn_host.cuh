@@ -43,8 +43,16 @@ int la_chunks(const LaShape& s) { return (int)((s.seqlen + kLaChunk - 1) / kLaCh
 
 bool la_check_heads(const ss_heads* x, int es) { return x && x->data && aligned(x->data, es); }
 
-LaTensor la_tensor(const ss_heads& x, int share) {
-  return LaTensor{x.data, x.batch_stride, x.token_stride, x.head_stride, share};
+// `heads` heads of d values as the pass has them, every `share` of them one of the tensor's.
+LaTensor la_tensor(const ss_heads& x, const LaShape& s, int share, int d) {
+  LaTensor t{x.data, x.batch_stride, x.token_stride, x.head_stride, share};
+#ifdef SS_BOUNDS_CHECK
+  int64_t hi = d - 1;
+  const int64_t ends[3] = {(s.batch - 1) * t.sb, (s.seqlen - 1) * t.st, (s.heads / share - 1) * t.sh};
+  for (int64_t e : ends) (e < 0 ? t.lo : hi) += e;
+  t.n = hi - t.lo + 1;
+#endif
+  return t;
 }
 
 // 16-byte loads: data, every stride and the row itself whole units.
@@ -231,7 +239,7 @@ LaPassArgs la_base(const LaShape& s, const ss_heads* g, const int32_t* lengths, 
   a.carry_spin_limit = spin > 0 ? (uint32_t)spin : kLaCarrySpinLimit;
   a.skip_publish = (int)g_dbg_la_skip_publish.exchange(-1);
   a.skip_load = (int)g_dbg_la_skip_load.exchange(-1);
-  a.g = la_tensor(*g, 1);
+  a.g = la_tensor(*g, s, 1, 1);
   a.lengths = lengths;
   a.heads = s.heads;
   a.seqlen = (int)s.seqlen;
@@ -270,9 +278,9 @@ ss_status linattn_fwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   const LaSeg seg = la_seg_at(static_cast<char*>(ws), s, segs);
   LaPassArgs a = la_base(s, g, lengths, segs);
   const int share = s.heads / s.qk_heads;
-  a.q = la_tensor(*q, share);
-  a.k = la_tensor(*k, share);
-  a.v = la_tensor(*v, 1);
+  a.q = la_tensor(*q, s, share, s.dk);
+  a.k = la_tensor(*k, s, share, s.dk);
+  a.v = la_tensor(*v, s, 1, s.dv);
   a.dk = s.dk;
   a.dv = s.dv;
   a.sk = s.dv;
@@ -372,7 +380,8 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   char* base = static_cast<char*>(ws);
   const LaSeg seg = la_seg_at(base, s, segs);
   const int share = s.heads / s.qk_heads;
-  const LaTensor tq = la_tensor(*q, share), tk = la_tensor(*k, share), tv = la_tensor(*v, 1), td = la_tensor(*d_o, 1);
+  const LaTensor tq = la_tensor(*q, s, share, s.dk), tk = la_tensor(*k, s, share, s.dk), tv = la_tensor(*v, s, 1, s.dv),
+                 td = la_tensor(*d_o, s, 1, s.dv);
   float* part = reinterpret_cast<float*>(base + w.part);
 
   // dq: a forward pass with (do, v, k); its state is S with the two indices exchanged
@@ -466,10 +475,10 @@ ss_status linattn_step_impl(const ss_heads* q, const ss_heads* k, const ss_heads
   if (s.batch > 65535 || num_slots < 1 || (!slots && num_slots < s.batch)) return SS_ERR_INVALID_ARG;
   LaStepArgs a = {};
   const int share = s.heads / s.qk_heads;
-  a.q = la_tensor(*q, share);
-  a.k = la_tensor(*k, share);
-  a.v = la_tensor(*v, 1);
-  a.g = la_tensor(*g, 1);
+  a.q = la_tensor(*q, s, share, s.dk);
+  a.k = la_tensor(*k, s, share, s.dk);
+  a.v = la_tensor(*v, s, 1, s.dv);
+  a.g = la_tensor(*g, s, 1, 1);
   a.state = state;
   a.num_slots = num_slots;
   a.slots = slots;

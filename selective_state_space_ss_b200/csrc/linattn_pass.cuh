@@ -89,6 +89,9 @@ struct LaTensor {
   const void* ptr;
   int64_t sb, st, sh;
   int share;
+#ifdef SS_BOUNDS_CHECK
+  int64_t lo, n;  // its elements: n of them from offset lo on
+#endif
 };
 
 struct LaPassArgs {
@@ -249,6 +252,15 @@ __device__ __forceinline__ const char* la_row(const LaTensor& x, int64_t b, int6
   return static_cast<const char*>(x.ptr) + (b * x.sb + t * x.st + (int64_t)(h / x.share) * x.sh) * es;
 }
 
+// Checked builds: whether `count` elements at `from` are the tensor's.
+__device__ __forceinline__ bool la_inside(const LaTensor& x, const char* from, int count, int es) {
+#ifdef SS_BOUNDS_CHECK
+  return in_range((from - static_cast<const char*>(x.ptr)) / es - x.lo, count, x.n);
+#else
+  return true;
+#endif
+}
+
 // One tile of 64 tokens into shared memory: rows from `len` on and columns from `d`
 // on are zero.  bf16 with 16-byte rows: asynchronous copies (the caller waits);
 // everything else through registers, up to four units at a time, the rows `ahead` tokens on
@@ -277,7 +289,7 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
 #pragma unroll 1
     for (int u = tid; u < UNITS; u += nthreads) {
       const int row = u / (B * 8), unit = u % (B * 8), col = unit * 8;
-      const bool in = t0 + row < len && col < d && in_range(t0 + row, len);
+      const bool in = t0 + row < len && col < d && la_inside(x, base + (t0 + row) * step + col * 2, 8, 2);
       const char* from = base + (in ? (t0 + row) * step + col * 2 : 0);
       const uint32_t bytes = in ? 16 : 0;
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
@@ -293,7 +305,8 @@ __device__ __forceinline__ void la_load_tile(char* dst, const LaTensor& x, int64
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int v = u + e * nthreads, row = v / (B * 8), col = v % (B * 8) * 8;
-      const bool in = t0 + row < len && col < d && in_range(t0 + row, len);
+      const bool in = t0 + row < len && col < d &&
+                      la_inside(x, base + (t0 + row) * step + col * (int)sizeof(T), d - col < 8 ? d - col : 8, sizeof(T));
       const char* from = base + (in ? (t0 + row) * step + col * (int)sizeof(T) : 0);
       la_fetch_unit<T>(f[e], from, in, col, d, vec);
       const int next = t0 + row + ahead;
@@ -329,7 +342,7 @@ __device__ __forceinline__ void la_fetch_decays(T (&x)[2], const LaTensor& g, in
     const int t = t0 + 2 * lane + i;
     x[i] = zero_elem<T>();
     const char* from = la_row(g, b, t, h, sizeof(T));
-    if (t < len && in_range(t, len)) x[i] = *reinterpret_cast<const T*>(from);
+    if (t < len && la_inside(g, from, 1, sizeof(T))) x[i] = *reinterpret_cast<const T*>(from);
     if (ahead != 0 && t + ahead >= 0 && t + ahead < len)
       asm volatile("prefetch.global.L2 [%0];\n" ::"l"(from + ahead * g.st * (int64_t)sizeof(T)));
   }
@@ -415,7 +428,7 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
                                         int v0, int lane) {
   const int64_t rs = (int64_t)a.heads * a.dv;
   const int v = v0 + lane / 4, t = t0 + 2 * (lane % 4);
-  const int64_t mine = ((b * a.seqlen + t) * a.heads + h) * a.dv + v;
+  const int64_t mine = ((b * a.seqlen + t) * a.heads + h) * a.dv + v, all = (int64_t)a.bh * a.seqlen * a.dv;
   if ((F32_ONLY || sizeof(T) == 4 || a.out_f32) && t0 + 16 <= len && v0 + 32 <= a.dv) {  // all there
     float* to = static_cast<float*>(a.out) + mine;
 #pragma unroll
@@ -424,7 +437,8 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
       for (int z = 0; z < 2; ++z) {
         float* row = to + (8 * i + z) * rs;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) row[8 * u] = o[u / 2][4 * i + 2 * (u % 2) + z];
+        for (int u = 0; u < 4; ++u)
+          if (in_range(row + 8 * u - static_cast<float*>(a.out), all)) row[8 * u] = o[u / 2][4 * i + 2 * (u % 2) + z];
       }
     return;
   }
@@ -433,10 +447,10 @@ __device__ __forceinline__ void la_emit(const LaPassArgs& a, const float (&o)[2]
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
       const int64_t row = mine + (8 * i + z) * rs;
-      if (t + 8 * i + z < len && in_range(t + 8 * i + z, a.seqlen)) {
+      if (t + 8 * i + z < len) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (v + 8 * u < a.dv) {
+          if (v + 8 * u < a.dv && in_range(row + 8 * u, all)) {
             const float y = o[u / 2][4 * i + 2 * (u % 2) + z];
             if (F32_ONLY || sizeof(T) == 4 || a.out_f32) static_cast<float*>(a.out)[row + 8 * u] = y;
             else static_cast<__nv_bfloat16*>(a.out)[row + 8 * u] = __float2bfloat16_rn(y);
@@ -459,7 +473,8 @@ __device__ __forceinline__ void la_dots(float (&sum)[4], const LaPassArgs& a, co
       float y = 0.f;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (t + 8 * i + z < len && v + 8 * u < a.dv)
+        if (t + 8 * i + z < len && v + 8 * u < a.dv &&
+            la_inside(a.x, from + (8 * i + z) * xs + 8 * u * (int)sizeof(T), 1, sizeof(T)))
           y = fmaf(o[u / 2][4 * i + 2 * (u % 2) + z], to_f32(reinterpret_cast<const T*>(from + (8 * i + z) * xs)[8 * u]), y);
       sum[2 * i + z] = y;
     }
@@ -735,7 +750,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           arrive(full_f(rf.i));
           rf.next();
         }
-        if (STATES && lane == 0) a.seg_decay[(int64_t)p.bh * (a.nseg + 1) + work.worker % a.nseg] = sum;
+        const int64_t at = (int64_t)p.bh * (a.nseg + 1) + work.worker % a.nseg;
+        if (STATES && lane == 0 && in_range(at, (int64_t)a.bh * (a.nseg + 1))) a.seg_decay[at] = sum;
       }
     } else {
       // ---- loaders: one thread by TMA, or all of them
@@ -982,10 +998,14 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
         const int rs = a.heads * a.dv * 2;
         const bool fast = FAST && MODE == kLaOutputs ? true : CF::kBf16 && a.out_vec;
         const bool fast_x = DOTS && CF::kBf16 && (FAST || a.x_vec);
+        // floats handed on by all workers, elements of the outputs
+        const int64_t carried = (int64_t)a.workers * 128 * (a.dk <= 64 && a.dv <= 64 ? 64 : 128);
+        const int64_t all = (int64_t)a.bh * a.seqlen * a.dv;
         char* out = static_cast<char*>(a.out) + ((int64_t)b * a.seqlen + tok) * rs + (h * a.dv + c8) * 2;
         if (p.from_carry) {
-          const unsigned* flag = a.flags + 1 + (work.worker - 1) * 16 + warp;
-          if (lane == 0) {
+          const int at = (work.worker - 1) * 16 + warp;  // of the flags, and of the states handed on
+          const unsigned* flag = a.flags + 1 + at;
+          if (lane == 0 && in_range(at, a.workers * 16)) {
             unsigned there = 0;
             for (uint32_t spin = 0; spin < a.carry_spin_limit && !there && !*dead; ++spin) {
               asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(there) : "l"(flag) : "memory");
@@ -997,10 +1017,11 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             }
           }
           __syncwarp();
-          const float4* from = reinterpret_cast<const float4*>(a.carry + ((int64_t)(work.worker - 1) * 16 + warp) * (KH * 32));
+          const float4* from = reinterpret_cast<const float4*>(a.carry + (int64_t)at * (KH * 32));
 #pragma unroll
           for (int c = 0; c < KH; c += 4) {
-            const float4 x = __ldcg(from + c / 4 * 32 + lane);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in_range((int64_t)at * (KH * 32) + (c / 4 * 32 + lane) * 4, 4, carried)) x = __ldcg(from + c / 4 * 32 + lane);
             S[c / 2] = pair(x.x, x.y), S[c / 2 + 1] = pair(x.z, x.w);
           }
         } else {
@@ -1009,7 +1030,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
 #pragma unroll
           for (int c = 0; c < KH; c += 2) {
             const int kk = part * KH + c;
-            S[c / 2] = pair(in && kk < a.dk ? from[0] : 0.f, in && kk + 1 < a.dk ? from[a.sk] : 0.f);
+            S[c / 2] = pair(in && kk < a.dk && in_range(from - a.s_in, a.bh * a.s_in_head) ? from[0] : 0.f,
+                            in && kk + 1 < a.dk && in_range(from + a.sk - a.s_in, a.bh * a.s_in_head) ? from[a.sk] : 0.f);
             from += 2 * a.sk;
           }
         }
@@ -1028,22 +1050,29 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
             // the state before the chunk: S, left by the forward pass, or R, met with it there
             const int64_t at = (int64_t)bh * a.chunks + chunk;
             float4* kept = reinterpret_cast<float4*>(a.dump) + (at * CF::kHolders + part * CF::kQuads + quad) * (KH * 8) + lane;
+            const int64_t all_kept = (int64_t)a.bh * a.chunks * CF::kHolders * (KH * 8);
+            const auto there = [&](const float4* p) { return in_range(p - reinterpret_cast<float4*>(a.dump), all_kept); };
             if (!a.reverse) {
 #pragma unroll
               for (int c = 0; c < KH; c += 4)
-                __stcs(kept + c / 4 * 32, make_float4(pair_lo(S[c / 2]), pair_hi(S[c / 2]), pair_lo(S[c / 2 + 1]), pair_hi(S[c / 2 + 1])));
+                if (there(kept + c / 4 * 32))
+                  __stcs(kept + c / 4 * 32,
+                         make_float4(pair_lo(S[c / 2]), pair_hi(S[c / 2]), pair_lo(S[c / 2 + 1]), pair_hi(S[c / 2 + 1])));
             } else {
               if (cc + 1 < p.last && lane < KH)  // the next chunk's, 128 bytes a lane
                 asm volatile("prefetch.global.L2 [%0];\n" ::"l"(kept - lane - CF::kHolders * (KH * 8) + lane * 8));
               float sum = 0.f;
 #pragma unroll
               for (int c = 0; c < KH; c += 4) {
-                const float4 x = __ldcs(kept + c / 4 * 32);
-                sum += pair_lo(S[c / 2]) * x.x + pair_hi(S[c / 2]) * x.y + pair_lo(S[c / 2 + 1]) * x.z + pair_hi(S[c / 2 + 1]) * x.w;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (there(kept + c / 4 * 32)) x = __ldcs(kept + c / 4 * 32);
+                sum += pair_lo(S[c / 2]) * x.x + pair_hi(S[c / 2]) * x.y + pair_lo(S[c / 2 + 1]) * x.z +
+                       pair_hi(S[c / 2 + 1]) * x.w;
               }
 #pragma unroll
               for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
-              if (lane == 0) a.flow[at * 16 + part * CF::kQuads + quad] = sum;
+              const int64_t mine_at = at * 16 + part * CF::kQuads + quad;
+              if (lane == 0 && in_range(mine_at, (int64_t)a.bh * a.chunks * 16)) a.flow[mine_at] = sum;
             }
           }
           la_wait(full_f(rf.i), rf.full(), dead);
@@ -1083,7 +1112,8 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
 #pragma unroll
                 for (int i2 = 0; i2 < 2; ++i2) {
                   xrow[i2] = make_uint4(0, 0, 0, 0);
-                  if (tw + i2 * 8 + tok < len && c8 < a.dv) xrow[i2] = *reinterpret_cast<const uint4*>(xp + i2 * xs);
+                  if (tw + i2 * 8 + tok < len && c8 < a.dv && la_inside(a.x, xp + i2 * xs, 8, sizeof(T)))
+                    xrow[i2] = *reinterpret_cast<const uint4*>(xp + i2 * xs);
                 }
                 // the next chunk's rows are asked for in L2
                 const int ahead = a.reverse ? -8 : 8;  // in steps of 8 tokens
@@ -1154,7 +1184,9 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
               __syncwarp();
               const uint4 y = *reinterpret_cast<const uint4*>(mine);
               const int t = tw + i2 * 8;
-              if (c8 < a.dv && t + tok < len && in_range(t + tok, a.seqlen)) *reinterpret_cast<uint4*>(out + (int64_t)t * rs) = y;
+              char* to = out + (int64_t)t * rs;
+              if (c8 < a.dv && t + tok < len && in_range((to - static_cast<char*>(a.out)) / 2, 8, all))
+                *reinterpret_cast<uint4*>(to) = y;
               __syncwarp();
             }
           } else if constexpr (!STATES && !(FAST && MODE == kLaOutputs)) {
@@ -1170,26 +1202,29 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int t = tw + 2 * lane + 8 * (e / 2) + e % 2;
-                if (t < len) a.dots[((int64_t)bh * a.seqlen + t) * 4 + quad] = sum[e];
+                const int64_t at = ((int64_t)bh * a.seqlen + t) * 4 + quad;
+                if (t < len && in_range(at, (int64_t)a.bh * a.seqlen * 4)) a.dots[at] = sum[e];
               }
             }
           }
         }
         if (p.to_carry) {
-          float4* to = reinterpret_cast<float4*>(a.carry + ((int64_t)work.worker * 16 + warp) * (KH * 32));
+          const int at = work.worker * 16 + warp;
+          float4* to = reinterpret_cast<float4*>(a.carry + (int64_t)at * (KH * 32));
 #pragma unroll
-          for (int c = 0; c < KH; c += 4) 
-            __stcg(to + c / 4 * 32 + lane,
+          for (int c = 0; c < KH; c += 4)
+            if (in_range((int64_t)at * (KH * 32) + (c / 4 * 32 + lane) * 4, 4, carried)) __stcg(to + c / 4 * 32 + lane,
                    make_float4(pair_lo(S[c / 2]), pair_hi(S[c / 2]), pair_lo(S[c / 2 + 1]), pair_hi(S[c / 2 + 1])));
           __threadfence();
           __syncwarp();
-          if (lane == 0 && work.worker != a.skip_publish)
-            asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(a.flags + 1 + work.worker * 16 + warp), "r"(1u) : "memory");
+          if (lane == 0 && work.worker != a.skip_publish && in_range(at, a.workers * 16))
+            asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(a.flags + 1 + at), "r"(1u) : "memory");
         } else if (a.s_out && (STATES || step == a.nseg - 1) && vi < a.dv) {
           float* to = a.s_out + (int64_t)bh * a.s_out_head + step * a.s_out_seg + part * KH * a.sk + vi * a.sv;
 #pragma unroll
           for (int c = 0; c < KH; ++c) {
-            if (part * KH + c < a.dk) *to = c % 2 ? pair_hi(S[c / 2]) : pair_lo(S[c / 2]);
+            if (part * KH + c < a.dk && in_range(to - a.s_out, a.bh * a.s_out_head))
+              *to = c % 2 ? pair_hi(S[c / 2]) : pair_lo(S[c / 2]);
             to += a.sk;
           }
         }
@@ -1220,19 +1255,20 @@ __global__ void linattn_join_kernel(float* states, const double* seg_decay, cons
   if (i >= per_state) return;
   float s = s0 ? s0[bh * s0_head + i] : 0.f;
   float* at = states + bh * nseg * per_state + i;
+  const int64_t all = (int64_t)gridDim.y * nseg;  // states, and decays
   const double* decay = seg_decay + bh * nseg;
   for (int n = 0; n < nseg; n += 8) {
     float local[8], a[8];  // eight segments asked for at once: only the sums are a chain
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const bool more = n + e + 1 < nseg;
-      local[e] = more ? at[(n + e) * per_state] : 0.f;
-      a[e] = more ? (float)exp2(decay[n + e]) : 0.f;
+      local[e] = more && in_range(at + (n + e) * per_state - states, all * per_state) ? at[(n + e) * per_state] : 0.f;
+      a[e] = more && in_range(decay + n + e - seg_decay, all) ? (float)exp2(decay[n + e]) : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (n + e < nseg) {
-        at[(n + e) * per_state] = s;
+        if (in_range(at + (n + e) * per_state - states, all * per_state)) at[(n + e) * per_state] = s;
         s = fmaf(s, a[e], local[e]);
       }
   }
@@ -1254,6 +1290,8 @@ linattn_share_kernel(const float* part, T* out, const int* lengths, I seqlen, I 
   }
   const float* p = part + ((int64_t)row * heads + (int64_t)gr * share) * d + (int64_t)c * VEC;
   T* to = out + ((int64_t)row * groups + gr) * d + (int64_t)c * VEC;
+  const int64_t all = (int64_t)(total / units) * d;  // elements of the sums
+  if (!in_range(to - out, VEC, all) || !in_range(p - part, (int64_t)(share - 1) * d + VEC, all * share)) return;
   float s[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) s[e] = 0.f;

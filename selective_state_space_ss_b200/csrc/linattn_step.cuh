@@ -55,11 +55,12 @@ __global__ void __launch_bounds__(kLaStepThreads) linattn_step_kernel(const __gr
   const int c = (tid % TPR) * VEC, r0 = tid / TPR;
   const bool mine = v0 + c < a.dv;
   float* st = a.state + ((slot * a.heads + h) * a.dk) * a.dv + v0 + c;
+  const int64_t all = a.num_slots * a.heads * a.dk * a.dv;
   float x[IT][VEC];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int r = r0 + i * ROWS;
-    if (mine && r < a.dk) {
+    if (mine && r < a.dk && in_range(st + (int64_t)r * a.dv - a.state, VEC, all)) {
       if constexpr (VEC == 4) {
         const float4 y = __ldcs(reinterpret_cast<const float4*>(st + (int64_t)r * a.dv));
         x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
@@ -69,14 +70,17 @@ __global__ void __launch_bounds__(kLaStepThreads) linattn_step_kernel(const __gr
     }
   }
   if (tid < a.dk) {
-    sq[tid] = to_f32(*reinterpret_cast<const T*>(la_row(a.q, b, 0, h, sizeof(T)) + tid * sizeof(T)));
-    sk[tid] = to_f32(*reinterpret_cast<const T*>(la_row(a.k, b, 0, h, sizeof(T)) + tid * sizeof(T)));
+    const char* qk[2] = {la_row(a.q, b, 0, h, sizeof(T)) + tid * sizeof(T), la_row(a.k, b, 0, h, sizeof(T)) + tid * sizeof(T)};
+    if (la_inside(a.q, qk[0], 1, sizeof(T))) sq[tid] = to_f32(*reinterpret_cast<const T*>(qk[0]));
+    if (la_inside(a.k, qk[1], 1, sizeof(T))) sk[tid] = to_f32(*reinterpret_cast<const T*>(qk[1]));
   }
-  const float decay = expf(to_f32(*reinterpret_cast<const T*>(la_row(a.g, b, 0, h, sizeof(T)))));
+  const char* g = la_row(a.g, b, 0, h, sizeof(T));
+  const float decay = la_inside(a.g, g, 1, sizeof(T)) ? expf(to_f32(*reinterpret_cast<const T*>(g))) : 0.f;
   float vv[VEC], o[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    vv[e] = mine ? to_f32(*reinterpret_cast<const T*>(la_row(a.v, b, 0, h, sizeof(T)) + (v0 + c + e) * sizeof(T))) : 0.f;
+    const char* v = la_row(a.v, b, 0, h, sizeof(T)) + (v0 + c + e) * sizeof(T);
+    vv[e] = mine && la_inside(a.v, v, 1, sizeof(T)) ? to_f32(*reinterpret_cast<const T*>(v)) : 0.f;
     o[e] = 0.f;
   }
   __syncthreads();
@@ -90,6 +94,7 @@ __global__ void __launch_bounds__(kLaStepThreads) linattn_step_kernel(const __gr
         x[i][e] = fmaf(x[i][e], decay, k * vv[e]);
         o[e] = fmaf(q, x[i][e], o[e]);
       }
+      if (!in_range(st + (int64_t)r * a.dv - a.state, VEC, all)) continue;
       if constexpr (VEC == 4)
         __stcs(reinterpret_cast<float4*>(st + (int64_t)r * a.dv), make_float4(x[i][0], x[i][1], x[i][2], x[i][3]));
       else
@@ -104,6 +109,7 @@ __global__ void __launch_bounds__(kLaStepThreads) linattn_step_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) s += part[i][tid];
     const int64_t at = ((int64_t)b * a.heads + h) * a.dv + v0 + tid;
+    if (!in_range(at, (int64_t)a.batch * a.heads * a.dv)) return;
     if constexpr (sizeof(T) == 2) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(s * a.scale);
     else static_cast<float*>(a.out)[at] = s * a.scale;
   }

@@ -69,15 +69,17 @@ __global__ void __launch_bounds__(kPoolThreads) state_store8_kernel(const __grid
   const int64_t row = (int64_t)blockIdx.x * (kPoolThreads / LANES) + threadIdx.x / LANES;
   const bool in = row < a.rows;
   const float* from = a.state + ((int64_t)b * a.rows + (in ? row : 0)) * a.width;
+  const int64_t states = a.batch * a.rows * a.width, kept = a.num_slots * a.rows;  // values, and rows of the pool
   float x[REGS][VEC];
 #pragma unroll
   for (int i = 0; i < REGS; ++i) {
     const int c = (i * LANES + lane) * VEC;
     if constexpr (VEC == 4) {
-      const float4 y = in && c < a.width ? __ldcs(reinterpret_cast<const float4*>(from + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const bool there = in && c < a.width && in_range(from + c - a.state, 4, states);
+      const float4 y = there ? __ldcs(reinterpret_cast<const float4*>(from + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
       x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
     } else {
-      x[i][0] = in && c < a.width ? from[c] : 0.f;
+      x[i][0] = in && c < a.width && in_range(from + c - a.state, states) ? from[c] : 0.f;
     }
   }
   const int64_t slot = pool_slot<true>(a, b);
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kPoolThreads) state_store8_kernel(const __grid
 #pragma unroll
   for (int i = 0; i < REGS; ++i) {
     const int c = (i * LANES + lane) * VEC;
-    if (c >= a.width) continue;
+    if (c >= a.width || !in_range(to + c - a.codes, VEC, kept * a.width)) continue;
     uint32_t n[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) n[e] = some ? pool_code(x[i][e], scale, half, inv) : 0;
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kPoolThreads) state_store8_kernel(const __grid
     else
       to[c] = (int8_t)n[0];
   }
-  if (lane == 0) a.scales[slot * a.rows + row] = scale;
+  if (lane == 0 && in_range(slot * a.rows + row, kept)) a.scales[slot * a.rows + row] = scale;
 }
 
 // LANES lanes a row, 4 codes an access, REGS accesses a lane and ROWS rows at once:
@@ -117,17 +119,20 @@ __global__ void __launch_bounds__(kPoolThreads) state_load8_kernel(const __grid_
   const int b = blockIdx.y, lane = threadIdx.x % LANES;
   const int64_t slot = pool_slot<false>(a, b);
   const int64_t row0 = (int64_t)blockIdx.x * (PER * ROWS) + threadIdx.x / LANES;
+  const int64_t states = a.batch * a.rows * a.width, kept = a.num_slots * a.rows;  // values, and rows of the pool
   uint32_t w[ROWS][REGS];
   float scale[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     const int64_t row = row0 + r * PER;
-    const bool in = slot >= 0 && row < a.rows;
+    const bool in = slot >= 0 && row < a.rows && in_range(slot * a.rows + row, kept);
     scale[r] = in ? a.scales[slot * a.rows + row] : 0.f;
 #pragma unroll
     for (int i = 0; i < REGS; ++i) {
       const int c = (i * LANES + lane) * 4;
-      w[r][i] = in && c < a.width ? __ldcs(reinterpret_cast<const uint32_t*>(a.codes + (slot * a.rows + row) * a.width + c)) : 0;
+      const int64_t at = (slot * a.rows + row) * a.width + c;
+      const bool there = in && c < a.width && in_range(at, 4, kept * a.width);
+      w[r][i] = there ? __ldcs(reinterpret_cast<const uint32_t*>(a.codes + at)) : 0;
     }
   }
 #pragma unroll
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kPoolThreads) state_load8_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < REGS; ++i) {
       const int c = (i * LANES + lane) * 4;
-      if (c >= a.width) continue;
+      if (c >= a.width || !in_range(((int64_t)b * a.rows + row) * a.width + c, 4, states)) continue;
       float f[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(w[r][i] >> (8 * e)) * scale[r];
@@ -153,8 +158,11 @@ __global__ void __launch_bounds__(kPoolThreads) state_load8_plain_kernel(const _
   const uint32_t n = (uint32_t)(a.rows * a.width), i = blockIdx.x * kPoolThreads + threadIdx.x;
   if (i >= n) return;
   float y = 0.f;
-  if (slot >= 0) y = (float)a.codes[slot * a.rows * a.width + i] * a.scales[slot * a.rows + i / (uint32_t)a.width];
-  a.state[(int64_t)b * a.rows * a.width + i] = y;
+  const int64_t code = slot * a.rows * a.width + i, row = slot * a.rows + i / (uint32_t)a.width;
+  const int64_t to = (int64_t)b * a.rows * a.width + i;
+  if (slot >= 0 && in_range(code, a.num_slots * a.rows * a.width) && in_range(row, a.num_slots * a.rows))
+    y = (float)a.codes[code] * a.scales[row];
+  if (in_range(to, a.batch * a.rows * a.width)) a.state[to] = y;
 }
 
 }  // namespace ssscan
