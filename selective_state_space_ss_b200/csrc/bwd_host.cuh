@@ -1,6 +1,6 @@
 // bwd_host.cuh -- host side of the backward: checkpoint sizes and the launch
 // behind ss_scan_bwd
-// (host code of libssscan.so; the library is one translation unit, ss_scan.cu)
+// (host code of libssscan.so's first translation unit, ss_scan.cu)
 #pragma once
 
 #include <cuda_runtime.h>
@@ -10,6 +10,7 @@
 
 #include "ss_scan.h"
 #include "host_common.cuh"
+#include "scan_hooks.cuh"
 #include "scan_bwd.cuh"
 
 namespace ssscan {

@@ -1,7 +1,7 @@
 // fwd_host.cuh -- host side of the forward scan: TMA descriptors, the
 // schedule plan (balanced workers or sequence segments), launches and the
 // argument checks behind ss_scan_fwd and its variants
-// (host code of libssscan.so; the library is one translation unit, ss_scan.cu)
+// (host code of libssscan.so's first translation unit, ss_scan.cu)
 #pragma once
 
 #include <cuda_runtime.h>
@@ -15,6 +15,7 @@
 
 #include "ss_scan.h"
 #include "host_common.cuh"
+#include "scan_hooks.cuh"
 #include "scan_fwd_chunked.cuh"
 #include "scan_fix.cuh"
 

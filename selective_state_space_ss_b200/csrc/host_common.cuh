@@ -1,6 +1,6 @@
-// host_common.cuh -- host helpers shared by every entry point: alignment,
-// per-device lookups done once, and the test-hook settings
-// (host code of libssscan.so; the library is one translation unit, ss_scan.cu)
+// host_common.cuh -- host helpers shared by every entry point: alignment and
+// per-device lookups done once
+// (host code of both translation units of libssscan.so, a copy in each)
 #pragma once
 
 #include <cuda_runtime.h>
@@ -13,13 +13,6 @@ namespace ssscan {
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Test hooks (ss_scan_debug.h): consumed by the next ss_scan_fwd call.
-std::atomic<long long> g_dbg_workers{0};
-std::atomic<long long> g_dbg_skip_publish{-1};
-std::atomic<long long> g_dbg_spin_limit{0};
-std::atomic<long long> g_dbg_step_simple{0};
-std::atomic<long long> g_dbg_segments{0};
 
 // Per-device answers that never change, looked up once (every launch plans its
 // schedule, and every workspace query plans all kernel variants).
@@ -54,8 +47,6 @@ int once_per_device(F setup) {
   }
   return v;
 }
-
-bool supported_dstate(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
 
 }  // namespace
 }  // namespace ssscan

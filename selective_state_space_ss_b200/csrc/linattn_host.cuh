@@ -218,13 +218,9 @@ ss_status la_segment_states(LaPassArgs a, const LaShape& s, const LaSegs& g, con
   a.seg_decay = seg.decay;
   const ss_status st = la_pass<kLaStates>(a, s.bf16, s.batch, stream);
   if (st != SS_OK) return st;
-  // rows of the grid are at most 2^16 - 1: whole states of up to that many heads a launch
-  for (int64_t at = 0; at < s.bh(); at += 65535) {
-    const int64_t n = s.bh() - at < 65535 ? s.bh() - at : 65535;
-    linattn_join_kernel<<<dim3((unsigned)((s.per_state() + 255) / 256), (unsigned)n), 256, 0, stream>>>(
-        seg.states + at * g.nseg * s.per_state(), seg.decay + at * g.nseg, s0 ? s0 + at * s.per_state() : nullptr,
-        s.per_state(), g.nseg, s.per_state());
-  }
+  // (segments are cut where there are no more heads than SMs, so they fit the grid's rows)
+  linattn_join_kernel<<<dim3((unsigned)((s.per_state() + 255) / 256), (unsigned)s.bh()), 256, 0, stream>>>(
+      seg.states, seg.decay, s0, g.nseg, s.per_state());
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 

@@ -1248,12 +1248,12 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
 // Segments joined: the state before each segment from the one before the first and
 // what each adds, s <- e^{G} s + local, every element on its own.  `states` [bh][nseg]
 // of dk x dv holds the local states and gets the starting ones.
-__global__ void linattn_join_kernel(float* states, const double* seg_decay, const float* s0, int64_t s0_head,
-                                    int nseg, int64_t per_state) {
+__global__ void linattn_join_kernel(float* states, const double* seg_decay, const float* s0, int nseg,
+                                    int64_t per_state) {
   const int64_t bh = blockIdx.y;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= per_state) return;
-  float s = s0 ? s0[bh * s0_head + i] : 0.f;
+  float s = s0 ? s0[bh * per_state + i] : 0.f;
   float* at = states + bh * nseg * per_state + i;
   const int64_t all = (int64_t)gridDim.y * nseg;  // states, and decays
   const double* decay = seg_decay + bh * nseg;

@@ -45,8 +45,8 @@ namespace ssscan {
 // ------------------------------------------------------------ mbarrier/TMA ---
 
 // Device error word: a kernel that gives up a bounded wait sets a bit here
-// instead of trapping; ss_last_device_error reads and clears it.  (The library
-// is a single translation unit, so the definition lives in this header.)
+// instead of trapping; ss_last_device_error reads and clears it.  (Each of the
+// library's two translation units has one of its own; both are read.)
 __device__ unsigned int g_error_word = 0;
 constexpr unsigned kErrTmaWait = 1u;     // a TMA completion wait timed out
 constexpr unsigned kErrLookback = 2u;    // an inter-CTA carry wait timed out

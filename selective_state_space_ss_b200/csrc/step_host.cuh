@@ -1,6 +1,6 @@
 // step_host.cuh -- host side of the recurrent decode step: kernel choice and
 // launch behind ss_scan_step
-// (host code of libssscan.so; the library is one translation unit, ss_scan.cu)
+// (host code of libssscan.so's first translation unit, ss_scan.cu)
 #pragma once
 
 #include <cuda_runtime.h>
@@ -11,6 +11,7 @@
 
 #include "ss_scan.h"
 #include "host_common.cuh"
+#include "scan_hooks.cuh"
 #include "scan_step.cuh"
 
 namespace ssscan {
