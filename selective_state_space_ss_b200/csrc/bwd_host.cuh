@@ -10,7 +10,6 @@
 
 #include "ss_scan.h"
 #include "host_common.cuh"
-#include "scan_hooks.cuh"
 #include "scan_bwd.cuh"
 
 namespace ssscan {

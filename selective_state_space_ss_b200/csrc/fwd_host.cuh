@@ -15,7 +15,6 @@
 
 #include "ss_scan.h"
 #include "host_common.cuh"
-#include "scan_hooks.cuh"
 #include "scan_fwd_chunked.cuh"
 #include "scan_fix.cuh"
 

@@ -1,6 +1,7 @@
-// host_common.cuh -- host helpers shared by every entry point: alignment and
-// per-device lookups done once
-// (host code of both translation units of libssscan.so, a copy in each)
+// host_common.cuh -- host helpers shared by every entry point: alignment,
+// per-device lookups done once, and the scan's test-hook settings
+// (host code of both translation units of libssscan.so; the scan's hooks are set and
+// read in ss_scan.cu alone, the other unit's 40 bytes of them never)
 #pragma once
 
 #include <cuda_runtime.h>
@@ -13,6 +14,13 @@ namespace ssscan {
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Test hooks (ss_scan_debug.h): consumed by the next ss_scan_fwd call.
+std::atomic<long long> g_dbg_workers{0};
+std::atomic<long long> g_dbg_skip_publish{-1};
+std::atomic<long long> g_dbg_spin_limit{0};
+std::atomic<long long> g_dbg_step_simple{0};
+std::atomic<long long> g_dbg_segments{0};
 
 // Per-device answers that never change, looked up once (every launch plans its
 // schedule, and every workspace query plans all kernel variants).
@@ -47,6 +55,8 @@ int once_per_device(F setup) {
   }
   return v;
 }
+
+bool supported_dstate(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
 
 }  // namespace
 }  // namespace ssscan

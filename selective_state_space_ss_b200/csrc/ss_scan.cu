@@ -10,7 +10,6 @@
 #include "ss_scan.h"
 #include "ss_scan_debug.h"
 #include "host_common.cuh"
-#include "scan_hooks.cuh"
 #include "fwd_host.cuh"
 #include "step_host.cuh"
 #include "bwd_host.cuh"

@@ -11,7 +11,6 @@
 
 #include "ss_scan.h"
 #include "host_common.cuh"
-#include "scan_hooks.cuh"
 #include "scan_step.cuh"
 
 namespace ssscan {
