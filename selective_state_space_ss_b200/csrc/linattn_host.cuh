@@ -70,11 +70,11 @@ struct LaSegs {
 // chunks of a head each.  With more heads than SMs a last wave that is not full is
 // avoided by workers, one an SM, with an equal share of the chunks; each hands at
 // most one state on.  With fewer, a head is cut into s segments: a first launch forms
-// the states of s - 1 of them (no queries, scores or outputs: 0.7 of a chunk's time,
-// measured with 64 x 64 heads, 1.46 us to 2.08), a second joins them and a third runs
-// all segments at once.  A CTA costs about 10 us to start, the two extra launches about
-// as much: in units of a chunk's time 4 where a chunk takes 2.5 us (bf16), 1.3 where it
-// takes 8 (fp32).
+// the states of s - 1 of them (no queries, scores or outputs: 0.53 to 0.67 of a chunk's
+// time, 0.98 us of 1.62 with 64 x 64 bf16 heads, 1.26 of 2.34 with 128 x 128, 4.5 of 7.5
+// and 8.8 of 15.4 in fp32), a second joins them and a third runs all segments at once.
+// A CTA costs 7 to 13 us to start, the two extra launches about as much: in units of a
+// chunk's time 4 (bf16) or 1.3 (fp32).
 LaSegs la_plan(const LaShape& s) {
   const int64_t chunks = (s.seqlen + kLaChunk - 1) / kLaChunk, bh = s.bh();
   const int64_t slots = device_sms() > 0 ? device_sms() : 148;
@@ -91,7 +91,7 @@ LaSegs la_plan(const LaShape& s) {
     const int64_t per = (chunks + n - 1) / n;
     if ((chunks + per - 1) / per != n) continue;
     double cost = (double)((bh * n + slots - 1) / slots) * (per + start);
-    if (n > 1) cost += (double)((bh * (n - 1) + slots - 1) / slots) * (0.7 * per + start) + extra;
+    if (n > 1) cost += (double)((bh * (n - 1) + slots - 1) / slots) * (0.6 * per + start) + extra;
     if (n == 1 || cost < best) best = cost, at = n;
   }
   return LaSegs{(int)at, (int)((chunks + at - 1) / at), 0};
