@@ -25,9 +25,10 @@
 // products of pairs by the warps' own matrix instructions, 16 rows i a warp.  The order of
 // the summed index is free, so a lane takes whole 16-byte units of a row.  The 64 x 64
 // results stay in registers, 32 columns at a time, where prefix sums along j and plain
-// sums along i >= t give the pairs.  Bound by a block's latencies (6144 chunks of 64 x 64
-// bf16 heads, 133 MB: 60 us, 2.2 TB/s; 2080 of 128 x 128, 134 MB: 40 us, 3.4 TB/s); with
-// products column after column, each waiting for the one before, it was 87 and 52.
+// sums along i >= t give the pairs.  Bound by instructions and latencies (6144 chunks of
+// 64 x 64 bf16 heads, 133 MB: 54 us, 2.5 TB/s, issue slots 70% busy; 2080 of 128 x 128,
+// 134 MB: 40 us, 3.4 TB/s); with products column after column, each waiting for the one
+// before, it was 87 and 52.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -55,30 +56,27 @@ __host__ __device__ constexpr int la_grad_row(int d, int es) { return (d + 31) /
 __host__ __device__ constexpr int la_grad_smem(int dk, int dv, int es) {
   return 2 * kLaChunk * (la_grad_row(dk, es) + la_grad_row(dv, es));
 }
-// A 16-byte unit's place: rows of whole 128 bytes have their halves exchanged in turn, so
-// that four units of two neighbouring rows are in different banks.
-__device__ __forceinline__ int la_grad_unit(int row, int unit, int bytes) {
-  return row * bytes + ((unit * 16) ^ (bytes % 128 == 0 ? (row & 1) * 64 : 0));
-}
+// Rows of whole 128 bytes have their halves exchanged in turn, so that four 16-byte units
+// of two neighbouring rows are in different banks: the bit of a unit's offset to turn.
+__device__ __forceinline__ int la_grad_turn(int row, int bytes) { return bytes % 128 == 0 ? (row & 1) * 64 : 0; }
 
-// The tile at t0; zeros behind the row's end and its last column.
+// The tile at t0; zeros behind the row's end and its last column.  Eight lanes a row.
 template <typename T, bool VEC>
 __device__ __forceinline__ void la_grad_tile(char* to, const LaTensor& x, int64_t b, int h, int t0, int len, int d) {
-  constexpr int N = 16 / sizeof(T);  // elements of a unit
+  constexpr int N = 16 / sizeof(T), STEP = kLaGradThreads / 8;  // elements of a unit, rows at once
   const int bytes = la_grad_row(d, sizeof(T)), row0 = threadIdx.x / 8;
-  const char* base = la_row(x, b, t0, h, sizeof(T));
-  const int64_t step = x.st * (int64_t)sizeof(T);
+  const int64_t step = STEP * x.st * (int64_t)sizeof(T);
 #pragma unroll 1
-  for (int unit = threadIdx.x % 8; unit * 16 < bytes; unit += 8)
+  for (int unit = threadIdx.x % 8; unit * 16 < bytes; unit += 8) {
+    const char* from = la_row(x, b, t0 + row0, h, sizeof(T)) + unit * 16;
+    char* at = to + row0 * bytes + (unit * 16 ^ la_grad_turn(row0, bytes));
+    const int col = unit * N;
 #pragma unroll
-    for (int row = row0; row < row0 + kLaChunk; row += kLaGradThreads / 8) {
-      const int col = unit * N;
-      const bool in = t0 + row < len && col < d &&
-                      la_inside(x, base + row * step + col * (int)sizeof(T), d - col < N ? d - col : N, sizeof(T));
-      const char* from = base + (in ? row * step + col * (int)sizeof(T) : 0);
-      char* at = to + la_grad_unit(row, unit, bytes);
+    for (int row = 0; row < kLaChunk; row += STEP, from += step, at += STEP * bytes) {
+      const bool in = t0 + row0 + row < len && col < d && la_inside(x, from, d - col < N ? d - col : N, sizeof(T));
       if constexpr (VEC) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(at)), "l"(from), "r"(in ? 16 : 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(at)),
+                     "l"(in ? from : static_cast<const char*>(x.ptr)), "r"(in ? 16 : 0)
                      : "memory");
       } else {
         T e[N];
@@ -88,18 +86,20 @@ __device__ __forceinline__ void la_grad_tile(char* to, const LaTensor& x, int64_
         for (int i = 0; i < N; ++i) reinterpret_cast<T*>(at)[i] = e[i];
       }
     }
+  }
 }
 
-// A lane's eight elements of 32 columns, as bf16 planes.
+// A lane's eight elements of 32 columns, as bf16 planes: of unit c, and in fp32 of that 64
+// bytes further on (`turn`: the other way round).
 template <typename T, int PLANES>
-__device__ __forceinline__ void la_grad_load(uint32_t (&p)[PLANES][4], const char* tile, int row, int k, int c, int bytes) {
+__device__ __forceinline__ void la_grad_load(uint32_t (&p)[PLANES][4], const char* from, int turn) {
   if constexpr (sizeof(T) == 2) {
-    const uint4 y = *reinterpret_cast<const uint4*>(tile + la_grad_unit(row, k / 8 + c, bytes));
+    const uint4 y = *reinterpret_cast<const uint4*>(from);
     p[0][0] = y.x, p[0][1] = y.y, p[0][2] = y.z, p[0][3] = y.w;
   } else {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float4 y = *reinterpret_cast<const float4*>(tile + la_grad_unit(row, k / 4 + c + 4 * e, bytes));
+      const float4 y = *reinterpret_cast<const float4*>(from + (64 * e ^ turn));
       uint32_t s[2][PLANES];
       split2<PLANES>(pair(y.x, y.y), s[0]);
       split2<PLANES>(pair(y.z, y.w), s[1]);
@@ -125,7 +125,9 @@ template <typename T>
 __device__ __forceinline__ void la_grad_products(float (&c)[4][4], const char* x, const char* y, int n0, int d, int warp,
                                                  int lane) {
   constexpr int PLANES = sizeof(T) == 2 ? 1 : 3;
-  const int r = lane / 4, col = lane % 4, bytes = la_grad_row(d, sizeof(T));
+  const int r = lane / 4, bytes = la_grad_row(d, sizeof(T)), turn = la_grad_turn(r, bytes);
+  const char* xr = x + (warp * 16 + r) * bytes + lane % 4 * 16;
+  const char* yr = y + (n0 * 8 + r) * bytes + lane % 4 * 16;
   float small[PLANES > 1 ? 4 : 1][4];
 #pragma unroll
   for (int n = 0; n < 4; ++n)
@@ -134,10 +136,11 @@ __device__ __forceinline__ void la_grad_products(float (&c)[4][4], const char* x
 #pragma unroll 1
   for (int k = 0; k < d; k += 32) {
     uint32_t lo[PLANES][4], hi[PLANES][4], z[4][PLANES][4];
-    la_grad_load<T, PLANES>(lo, x, warp * 16 + r, k, col, bytes);
-    la_grad_load<T, PLANES>(hi, x, warp * 16 + r + 8, k, col, bytes);
+    const int at = sizeof(T) == 2 ? k * 2 ^ turn : k * 4;
+    la_grad_load<T, PLANES>(lo, xr + at, turn);
+    la_grad_load<T, PLANES>(hi, xr + 8 * bytes + at, turn);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) la_grad_load<T, PLANES>(z[n], y, (n0 + n) * 8 + r, k, col, bytes);
+    for (int n = 0; n < 4; ++n) la_grad_load<T, PLANES>(z[n], yr + n * 8 * bytes + at, turn);
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
       if constexpr (PLANES > 1) {
