@@ -26,7 +26,11 @@
 // (P) and the state, whose products end in a bf16 output, take two planes, 16 bits; the
 // weighted keys, whose products add up in the fp32 state, take four: a product of two
 // bf16 is a bf16 and a bf16 that is left over, exactly, so they are formed in bf16
-// arithmetic (two planes left the state 2.4e-6 off, four 1e-7).  fp32 inputs and
+// arithmetic (two planes left the state 2.4e-6 off, four 1e-7).  With P and the state in
+// two planes the last place of a bf16 output differs from that of a 32-bit evaluation
+// in about one of 400, 9e-5 of the norm next to the rounding's own 1.7e-3; three gave 3e-5
+// and took 6% longer with 64 x 64 heads, 34% with 128 x 128 (B4 L8192 H40, 438 -> 587 us:
+// tensor memory then has one place for scores).  fp32 inputs and
 // everything behind them take three planes, 24 bits, and the six products of planes whose
 // weight reaches that far.  Products of smaller planes are added first, while the sum is
 // small (in the other order fp32 outputs were 2e-6 off, in this one 2e-7).  The state
@@ -51,10 +55,13 @@
 // the instruction cache (spin loops not unrolled, product loops short): 0.50.  Products
 // issued from warp-uniform descriptors, sixteen and eight warps, hand-overs of their own
 // for P and the weighted keys: 0.41 to 0.46 (2.9 to 3.3 TB/s, 44 to 51% of the copy
-// rate), 2.5 us a chunk and SM of 64 tokens.  ncu: 11 thousand warp instructions a chunk,
-// issue slots 60% busy, tensor pipe 43%, DRAM 40%: it is bound by the work around the
-// products (splitting, weighting, moving) and its hand-overs, not by a single unit.
-// With 64 x 64 heads a chunk takes 1.65 us, half of its data, for the same hand-overs.
+// rate), 2.3 to 2.5 us a chunk and SM of 64 tokens.  ncu: 11 thousand warp instructions a
+// chunk, issue slots 60% busy, tensor pipe 43%, DRAM 40%: it is bound by the work around
+// the products (splitting, weighting, moving) and its hand-overs, not by a single unit.
+// With 64 x 64 heads a chunk takes 1.6 us, half of its data, for the same hand-overs; with
+// 128 x 64 2.1 us, tensor pipe 51%, issue slots 50%.  fp32: 7.5 us (64 x 64) to 15
+// (128 x 128), issue slots 22% and tensor pipe 22% busy: the warps wait for tiles that two
+// loader warps split.
 //
 // Schedule.  A head's chunks depend on one another through S alone.  With fewer heads
 // than SMs the sequence is cut into segments whose starting states a first launch
