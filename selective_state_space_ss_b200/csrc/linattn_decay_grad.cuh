@@ -212,8 +212,9 @@ __global__ void __launch_bounds__(kLaGradThreads) linattn_decay_grad_kernel(cons
     const float bad = __any_sync(kFullMask, x0 != x0 || x1 != x1) ? __int_as_float(0x7fffffff) : 1.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      fac[2 * lane + i] = (float)(int)(at[i] >> 32);
-      fac[kLaChunk + 2 * lane + i] = (float)(uint32_t)at[i] * 0x1p-32f * bad;
+      const int64_t x = la_fixed32(at[i]);
+      fac[2 * lane + i] = (float)(int)(x >> 32);
+      fac[kLaChunk + 2 * lane + i] = (float)(uint32_t)x * 0x1p-32f * bad;
     }
     // a from its token on, b before its token
     float from = s[0][0] + s[0][1], upto = s[1][0] + s[1][1];
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kLaGradThreads) linattn_decay_grad_kernel(cons
     const float earlier = __shfl_up_sync(kFullMask, upto, 1);  // b before them
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2) all += __shfl_xor_sync(kFullMask, all, o);
-    all *= la_exp2(total) * bad;
+    all *= la_exp2(la_fixed32(total)) * bad;
     const float b0 = lane ? earlier : 0.f, a1 = s[0][1] + (lane < 31 ? later : 0.f);
     rest[2 * lane] = all + b0 + (s[0][0] + a1);
     rest[2 * lane + 1] = all + (b0 + s[1][0]) + a1;

@@ -34,7 +34,7 @@
 // everything behind them take three planes, 24 bits, and the six products of planes whose
 // weight reaches that far.  Products of smaller planes are added first, while the sum is
 // small (in the other order fp32 outputs were 2e-6 off, in this one 2e-7).  The state
-// itself stays fp32 in registers.  Running sums of the decays are whole numbers of 2^-32.
+// itself stays fp32 in registers.  Running sums of the decays are whole numbers of 2^-44.
 //
 // Layout.  Scores are Q K^T with tokens in the lanes.  O and S are kept transposed
 // (value index in the lanes), so that S^T is the MMA's A operand straight from
@@ -364,16 +364,21 @@ __device__ __forceinline__ float la_exp2(int64_t x) {
   return n < -126 ? 0.f : n > 127 ? __int_as_float(0x7f800000) : z;
 }
 
+// Of a sum of decays (below), what la_exp2 takes.
+__device__ __forceinline__ int64_t la_fixed32(int64_t x) { return x >> 12; }
+
 // Running sums of a chunk's decays, base 2, two tokens a lane of a warp, and the whole.
-// They are whole numbers of 2^-32, so differences of large sums lose nothing.  A log decay
+// They are whole numbers of 2^-44 (64 tokens of at most 2020 fit 61 bits), so differences of
+// large sums lose nothing, nor do the sums of tens of thousands of slow decays.  A log decay
 // beyond +-1400 leaves nothing, or too much, in fp32 and is taken as that: minus infinity
 // (a reset) is a number like any other here.
+constexpr int kLaDecayBits = 44;
 __device__ __forceinline__ void la_decay_sums(int64_t (&at)[2], int64_t& total, float x0, float x1, int lane) {
   const float x[2] = {x0, x1};
   int64_t g[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    g[i] = __double2ll_rn((double)fminf(fmaxf(x[i], -1400.f), 1400.f) * (1.4426950408889634 * 4294967296.0));
+    g[i] = __double2ll_rn((double)fminf(fmaxf(x[i], -1400.f), 1400.f) * (1.4426950408889634 * (double)(INT64_C(1) << kLaDecayBits)));
   int64_t sum = g[0] + g[1];
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
@@ -384,40 +389,67 @@ __device__ __forceinline__ void la_decay_sums(int64_t (&at)[2], int64_t& total, 
   at[0] = sum - g[1], at[1] = sum;
 }
 
+// The factor that the state passes a chunk with, from the sum of its decays.  Near 1 what
+// rounding leaves out of it, `left` (a natural logarithm), goes into the next chunk's: with
+// slow decays the state passes hundreds of equal factors, whose equal roundings would add
+// up (to 8e-6 of the state after 256 chunks of log decays of -1e-6).  e^t - 1 by its series,
+// |t| < 0.35: the first term left out is 2e-8 of it.
+__device__ __forceinline__ float la_exp2_chunk(int64_t x, float& left) {
+  if (x <= -(INT64_C(1) << (kLaDecayBits - 1)) || x >= (INT64_C(1) << (kLaDecayBits - 1))) {
+    left = 0.f;
+    return la_exp2(la_fixed32(x));
+  }
+  const float t = fmaf((float)x, (float)(0.6931471805599453 / (INT64_C(1) << kLaDecayBits)), left);
+  float e = fmaf(t, 1.f / 5040, 1.f / 720);
+  e = fmaf(t, e, 1.f / 120);
+  e = fmaf(t, e, 1.f / 24);
+  e = fmaf(t, e, 1.f / 6);
+  e = fmaf(t, e, 0.5f);
+  e = fmaf(t * t, e, t);
+  const float y = 1.f + e;
+  left = (e - (y - 1.f)) * rcp_approx(y);
+  return y;
+}
+
 // A chunk's decays: running sums, base 2, as integer and fraction (64 floats each), the
 // factors of the rows, those of the keys (for bf16 keys as three bf16 planes, each twice
-// in a word), and the chunk's whole decay, which is returned.  One warp.
-template <bool BF16>
-__device__ __forceinline__ int64_t la_decays(float* fac, float x0, float x1, bool reverse, float scale_o, float scale_w,
-                                             int lane) {
+// in a word), and the chunk's whole decay, whose sum is returned.  ROWS false (the states
+// alone): the last two.  One warp.
+template <bool BF16, bool ROWS>
+__device__ __forceinline__ int64_t la_decays(float* fac, float& left, float x0, float x1, bool reverse, float scale_o,
+                                             float scale_w, int lane) {
   int64_t at[2], total;
   la_decay_sums(at, total, x0, x1, lane);
   // a NaN among them is not to vanish
   const float bad = __any_sync(kFullMask, x0 != x0 || x1 != x1) ? __int_as_float(0x7fffffff) : 1.f;
-  float hi[2], lo[2], rows[2], keys[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float from_start = la_exp2(at[i]), to_end = la_exp2(total - at[i]);
-    hi[i] = (float)(int)(at[i] >> 32);
-    lo[i] = (float)(uint32_t)at[i] * 0x1p-32f * bad;
-    rows[i] = (reverse ? to_end : from_start) * scale_o * bad;
-    keys[i] = (reverse ? from_start : to_end) * scale_w * bad;
-  }
   float2* out = reinterpret_cast<float2*>(fac) + lane;
-  out[0] = make_float2(hi[0], hi[1]);
-  out[32] = make_float2(lo[0], lo[1]);
-  out[64] = make_float2(rows[0], rows[1]);
+  float keys[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) keys[i] = la_exp2(la_fixed32(reverse ? at[i] : total - at[i])) * scale_w * bad;
+  if constexpr (ROWS) {
+    float hi[2], lo[2], rows[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t x = la_fixed32(at[i]);
+      hi[i] = (float)(int)(x >> 32);
+      lo[i] = (float)(uint32_t)x * 0x1p-32f * bad;
+      rows[i] = la_exp2(reverse ? la_fixed32(total - at[i]) : x) * scale_o * bad;
+    }
+    out[0] = make_float2(hi[0], hi[1]);
+    out[32] = make_float2(lo[0], lo[1]);
+    out[64] = make_float2(rows[0], rows[1]);
+  }
   if constexpr (BF16) {
     uint32_t p0[3], p1[3];
     split2<3>(pair(keys[0], keys[0]), p0);
     split2<3>(pair(keys[1], keys[1]), p1);
 #pragma unroll
     for (int i = 0; i < 3; ++i) reinterpret_cast<uint2*>(fac)[96 + 32 * i + lane] = make_uint2(p0[i], p1[i]);
-    if (lane == 0) fac[6 * kLaChunk] = la_exp2(total) * bad;
   } else {
     out[96] = make_float2(keys[0], keys[1]);
-    if (lane == 0) fac[4 * kLaChunk] = la_exp2(total) * bad;
   }
+  const float whole = la_exp2_chunk(total, left) * bad;
+  if (lane == 0) fac[(BF16 ? 6 : 4) * kLaChunk] = whole;
   return total;
 }
 
@@ -743,6 +775,7 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
       for (int i = 0; i < work.pieces; ++i) {
         const LaPiece p = la_piece(a, work, i);
         double sum = 0.0;
+        float left = 0.f;
         auto place = [&](int c) { return (a.reverse ? p.last - 1 - (c - p.first) : c) * kLaChunk; };
         T next[2];
         const int ahead = (a.reverse ? -4 : 4) * kLaChunk;
@@ -751,9 +784,9 @@ linattn_pass_kernel(const __grid_constant__ LaPassArgs a, const __grid_constant_
           const float x0 = to_f32(next[0]), x1 = to_f32(next[1]);
           if (c + 1 < p.last) la_fetch_decays<T>(next, a.g, p.b, p.h, place(c + 1), p.len, ahead, lane);
           if (rf.used()) la_wait(empty_f(rf.i), rf.empty(), dead);
-          const int64_t whole = la_decays<CF::kBf16>(reinterpret_cast<float*>(smem + CF::kFac) + rf.i * CF::kFacFloats, x0,
-                                                     x1, a.reverse, a.scale_o, a.scale_w, lane);
-          if (STATES) sum += (double)whole * 0x1p-32;
+          const int64_t whole = la_decays<CF::kBf16, !STATES>(reinterpret_cast<float*>(smem + CF::kFac) + rf.i * CF::kFacFloats,
+                                                              left, x0, x1, a.reverse, a.scale_o, a.scale_w, lane);
+          if (STATES) sum += (double)whole * (1.0 / (INT64_C(1) << kLaDecayBits));
           arrive(full_f(rf.i));
           rf.next();
         }
@@ -1260,23 +1293,24 @@ __global__ void linattn_join_kernel(float* states, const double* seg_decay, cons
   const int64_t bh = blockIdx.y;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= per_state) return;
-  float s = s0 ? s0[bh * per_state + i] : 0.f;
+  double s = s0 ? s0[bh * per_state + i] : 0.f;  // equal factors' roundings would add up
   float* at = states + bh * nseg * per_state + i;
   const int64_t all = (int64_t)gridDim.y * nseg;  // states, and decays
   const double* decay = seg_decay + bh * nseg;
   for (int n = 0; n < nseg; n += 8) {
-    float local[8], a[8];  // eight segments asked for at once: only the sums are a chain
+    float local[8];
+    double a[8];  // eight segments asked for at once: only the sums are a chain
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const bool more = n + e + 1 < nseg;
       local[e] = more && in_range(at + (n + e) * per_state - states, all * per_state) ? at[(n + e) * per_state] : 0.f;
-      a[e] = more && in_range(decay + n + e - seg_decay, all) ? (float)exp2(decay[n + e]) : 0.f;
+      a[e] = more && in_range(decay + n + e - seg_decay, all) ? exp2(decay[n + e]) : 0.0;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (n + e < nseg) {
-        if (in_range(at + (n + e) * per_state - states, all * per_state)) at[(n + e) * per_state] = s;
-        s = fmaf(s, a[e], local[e]);
+        if (in_range(at + (n + e) * per_state - states, all * per_state)) at[(n + e) * per_state] = (float)s;
+        s = fma(s, a[e], (double)local[e]);
       }
   }
 }
