@@ -147,8 +147,9 @@ def _on_its_stream(fn):
     current one.
 
     The call runs with that stream current, so that its fills, its launches and the
-    allocator's reuse of its workspace keep the stream's order; what it allocates and
-    returns is marked as used by the caller's current stream too (which has to wait for
+    allocator's reuse of its workspace keep the stream's order.  What it is given is marked
+    as used by that stream, so that a temporary may be dropped right after the call; what it
+    allocates and returns as used by the caller's current stream too (which has to wait for
     the other before it reads, as ever).
     """
     at = list(inspect.signature(fn).parameters).index("stream")
@@ -173,6 +174,9 @@ def _on_its_stream(fn):
         before = torch.cuda.current_stream(device)
         with torch.cuda.stream(stream):
             out = fn(*args, **kwargs)
+        for x in given:
+            if x.is_cuda:
+                x.record_stream(stream)
         for x in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
             if isinstance(x, torch.Tensor) and not any(x is y for y in given):
                 x.record_stream(before)

@@ -116,6 +116,28 @@ def test_an_output_freed_while_the_current_stream_reads_it():
     assert torch.equal(copy, want)
 
 
+@pytest.mark.parametrize("name", ["linattn", "scan"])
+def test_an_operand_dropped_right_after_the_call(name):
+    """A temporary of the caller, with the given stream still busy: the current stream's next tensors do not take its place."""
+    ops = linattn(L=1000)[0] if name == "linattn" else scan(L=2000)
+    fn = ss.ss_linattn_fwd if name == "linattn" else ss.ss_scan_fwd
+    want = tensors(fn(*ops))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    temporary = [x.clone() for x in ops]
+    sizes = [x.numel() * x.element_size() for x in ops]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(LONG)
+    got = tensors(fn(*temporary, stream=side))
+    del temporary
+    junk = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes * 2]
+    torch.cuda.synchronize()
+    assert len(junk) and ss.ss_last_device_error() == ss.SS_OK
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_refusals():
     ops, _, _ = linattn()
     with pytest.raises(ValueError):

@@ -191,7 +191,9 @@ def test_a_call_runs_with_its_stream_current(monkeypatch):
     f(make(), stream=Stream("side"))
     f(make(), given, Stream("side"))
     f(make(), stream=Stream("main"))
-    assert log == [("runs on", "main"), ("runs on", "side"), ("used on", "main"), ("runs on", "side"), ("runs on", "main")]
+    side = ("used on", "side")
+    assert log == [("runs on", "main"), ("runs on", "side"), side, ("used on", "main"), ("runs on", "side"), side, side,
+                   ("runs on", "main")]
     for name in dir(ss):  # every public call that takes one
         fn = getattr(ss, name)
         if callable(fn) and name.startswith("ss_") and name != "ss_last_device_error" and "stream" in getattr(fn, "__code__", f.__code__).co_varnames:
