@@ -294,6 +294,13 @@ ss_status linattn_fwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
 
 // ---- backward
 
+ss_status la_check_bwd_shape(const LaShape& s, int in_dtype) {
+  const ss_status st = la_check_shape(s, in_dtype);
+  if (st != SS_OK) return st;
+  // a block of the decays' gradient each (the gradients of so many alone are 256 GB)
+  return s.bh() * la_chunks(s) > INT_MAX ? SS_ERR_INVALID_ARG : SS_OK;
+}
+
 struct LaBwdWs {
   size_t dots_q = 0, dots_k = 0, flow = 0, dump = 0, part = 0, bytes = 0;
 };
@@ -361,7 +368,7 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
                            const ss_heads* d_o, float scale, const float* s0, const float* dlast,
                            const int32_t* lengths, void* dq, void* dk, void* dv, void* dg, float* ds0,
                            const LaShape& s, int in_dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
-  ss_status st = la_check_shape(s, in_dtype);
+  ss_status st = la_check_bwd_shape(s, in_dtype);
   if (st != SS_OK) return st;
   const int es = s.es();
   for (const ss_heads* x : {q, k, v, g, d_o})
@@ -369,7 +376,6 @@ ss_status linattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   for (const void* x : {dq, dk, dv, dg})
     if (!x || !aligned(x, es)) return SS_ERR_INVALID_ARG;
   if (!aligned(s0, 4) || !aligned(dlast, 4) || !aligned(lengths, 4) || !aligned(ds0, 4)) return SS_ERR_INVALID_ARG;
-  if (s.bh() * la_chunks(s) > INT_MAX) return SS_ERR_INVALID_ARG;  // one block each; their gradients alone are 256 GB
   const LaSegs segs = la_plan(s);
   const LaBwdWs w = la_bwd_ws(s, segs);
   if (!ws || ws_bytes < w.bytes || !aligned(ws, 256)) return SS_ERR_INVALID_ARG;

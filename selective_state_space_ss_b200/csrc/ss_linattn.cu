@@ -67,7 +67,7 @@ ss_status ss_linattn_bwd(const ss_heads* q, const ss_heads* k, const ss_heads* v
 size_t ss_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int qk_heads, int dk, int dv,
                                       ss_dtype in_dtype) {
   const LaShape s{batch, seqlen, heads, qk_heads, dk, dv, in_dtype == SS_BF16};
-  if (la_check_shape(s, in_dtype) != SS_OK) return (size_t)-1;
+  if (la_check_bwd_shape(s, in_dtype) != SS_OK) return (size_t)-1;
   return la_bwd_ws(s, la_plan(s)).bytes;
 }
 

@@ -205,3 +205,12 @@ def test_the_waits_hooks_are_known(lib):
         assert lib.ss_debug_inject(what, 3) == N.SS_OK
     assert lib.ss_debug_inject(N.SS_DEBUG_CLEAR, 0) == N.SS_OK
     assert lib.ss_debug_inject(N.SS_DEBUG_LINATTN_SKIP_LOAD + 1, 0) == N.SS_ERR_INVALID_ARG
+
+
+def test_a_backward_of_too_many_chunks_has_no_workspace(lib):
+    """As for every size that the call rejects; the forward has one."""
+    sizes = (1, 2**31 - 1025, 65536, 1, 8, 8, N.SS_BF16)
+    none = ctypes.c_size_t(-1).value
+    assert lib.ss_linattn_bwd_workspace_bytes(*sizes) == none
+    assert lib.ss_linattn_workspace_bytes(*sizes) != none
+    assert lib.ss_linattn_bwd_workspace_bytes(1, 2**31 - 1025, 8, 1, 8, 8, N.SS_BF16) != none
