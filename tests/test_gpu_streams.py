@@ -138,6 +138,28 @@ def test_an_operand_dropped_right_after_the_call(name):
         assert torch.equal(a, b)
 
 
+def test_a_branch_of_a_captured_graph():
+    """Inside a capture, on a stream that was forked from the captured one and joins it again."""
+    ops, do, _ = linattn(heads=90)
+    lengths = torch.tensor([300, 77], dtype=torch.int32, device="cuda")
+    want = [*tensors(ss.ss_linattn_fwd(*ops, lengths=lengths)), *tensors(ss.ss_linattn_bwd(*ops, do, lengths=lengths))]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        got = tensors(ss.ss_linattn_fwd(*ops, lengths=lengths, stream=side))
+        got += tensors(ss.ss_linattn_bwd(*[x.clone() for x in ops], do, lengths=lengths))
+        main.wait_stream(side)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert ss.ss_last_device_error() == ss.SS_OK and len(got) == len(want)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_refusals():
     ops, _, _ = linattn()
     with pytest.raises(ValueError):
