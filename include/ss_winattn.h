@@ -1,0 +1,197 @@
+/*
+ * ss_winattn.h -- C ABI of libssscan.so: attention over a window with a few first
+ * tokens that stay visible (sinks), its paged cache, and the rotation of positions.
+ *
+ * The layers that stand between the recurrent ones of ss_scan.h and ss_linattn.h in a
+ * hybrid model: like a state, a window is of bounded size.  With the tokens of a row
+ * numbered from 0, token t sees token j where
+ *
+ *   j <= t   and   (t - j < window  or  j < sinks)
+ *
+ * and, over the tokens that it sees,
+ *
+ *   s_tj = scale q_t . k_j,   lse_t = log sum_j exp(s_tj),
+ *   o_t  = sum_j exp(s_tj - lse_t) v_j
+ *
+ * A window of seqlen or more is plain causal attention.
+ *
+ * The conventions of ss_scan.h and the strided operands (ss_heads) of ss_linattn.h
+ * hold: device pointers, caller-owned; nothing is allocated, nothing synchronised;
+ * calls are asynchronous on `stream` and may be captured into a CUDA graph; the stream
+ * belongs to the current device, and so do the buffers; arguments are checked on the
+ * host before any launch and a rejected call launches nothing.  in_dtype is float32 or
+ * bfloat16 for every operand and output but lse.  Outputs must not overlap inputs or
+ * one another, but where it says so.  Any element alignment and any strides (0
+ * repeats); bfloat16 operands of 16-byte aligned data and strides and a d that is a
+ * multiple of 8 go through the tensor cores.
+ *
+ * Softmax statistics and all sums are fp32, in a fixed order: the same call gives the
+ * same bits.  For bfloat16 operands the probabilities, and in the backward pass their
+ * gradients, are rounded to bfloat16 as operands of the next product.
+ *
+ * Values of tokens that a row holds must be finite: a NaN or an infinity among them
+ * may spread over its row's and its heads' results, to tokens that do not see it as
+ * well.  What lies behind a row's length, in the cache's tokens that no query sees and
+ * in pages that no row has is never used.  A kernel whose waits give up
+ * (ss_last_device_error: SS_ERR_TIMEOUT) leaves its outputs unspecified.
+ */
+#ifndef SS_WINATTN_H_
+#define SS_WINATTN_H_
+
+#include "ss_linattn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * ss_winattn_fwd -- a whole prompt.
+ *
+ *  q             [batch, seqlen, heads, d]; head h of them reads head
+ *                h / (heads / kv_heads) of the keys and values
+ *  k, v          [batch, seqlen, kv_heads, d]
+ *  window        >= 1, the token itself included
+ *  sinks         >= 0
+ *  scale         > 0 and finite (d^-1/2)
+ *  lengths       [batch] int32, nullable: row b has lengths[b] tokens, taken into
+ *                0 .. seqlen.  Nothing behind them is used, and o_out and lse_out
+ *                keep what they hold there
+ *  o_out         [batch, seqlen, heads, d] in_dtype, contiguous
+ *  lse_out       [batch, heads, seqlen] float32, nullable; ss_winattn_bwd takes it
+ *  1 <= d <= 128 (others: SS_ERR_UNSUPPORTED); heads a multiple of kv_heads and at
+ *                most 65536, batch * heads at most 2^24, seqlen below 2^31 - 1024,
+ *                and at most 2^31 - 1 blocks of 64 tokens of all rows and heads
+ *
+ * No workspace.
+ */
+ss_status ss_winattn_fwd(const ss_heads* q, const ss_heads* k, const ss_heads* v,
+                         int64_t window, int64_t sinks, float scale,
+                         const int32_t* lengths, void* o_out, float* lse_out,
+                         int64_t batch, int64_t seqlen, int heads, int kv_heads, int d,
+                         ss_dtype in_dtype, cudaStream_t stream);
+
+/*
+ * ss_winattn_bwd -- the gradients of ss_winattn_fwd for an upstream gradient d_o
+ * [batch, seqlen, heads, d] of o, with its o (strided) and lse.  With p_tj =
+ * exp(s_tj - lse_t):
+ *
+ *   dv_j  = sum_t p_tj do_t                      (and over the heads that share j)
+ *   ds_tj = p_tj (do_t . v_j - do_t . o_t)
+ *   dq_t  = scale sum_j ds_tj k_j
+ *   dk_j  = scale sum_t ds_tj q_t                (and over the heads that share j)
+ *
+ * dq [batch, seqlen, heads, d], dk_out, dv_out [batch, seqlen, kv_heads, d]:
+ * in_dtype, contiguous, required; nothing is written behind a row's length.
+ * workspace: ss_winattn_bwd_workspace_bytes(...) bytes, 256-byte aligned.  Contents on
+ * entry do not matter; calls in flight at once, replays of captured ones among them,
+ * must not share one.
+ */
+ss_status ss_winattn_bwd(const ss_heads* q, const ss_heads* k, const ss_heads* v,
+                         const ss_heads* o, const float* lse, const ss_heads* d_o,
+                         int64_t window, int64_t sinks, float scale,
+                         const int32_t* lengths, void* dq, void* dk_out, void* dv_out,
+                         int64_t batch, int64_t seqlen, int heads, int kv_heads, int d,
+                         ss_dtype in_dtype, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
+
+/* Bytes of workspace ss_winattn_bwd needs; (size_t)-1 for sizes that it would reject. */
+size_t ss_winattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads,
+                                      int kv_heads, int d, int64_t window,
+                                      int64_t sinks, ss_dtype in_dtype);
+
+/*
+ * A cache of keys and values in pages: k and v are [num_pages, page_size, kv_heads, d]
+ * with the strides of ss_heads (batch_stride: from page to page, token_stride: from
+ * token to token in a page), so pages of [kv_heads, page_size, d] do as well.  Token t
+ * of row b lies in page table[b * max_pages + t / page_size], at t % page_size.  A
+ * table entry outside 0 .. num_pages - 1 is no page: tokens there are not seen and not
+ * written.  Entries of pages that hold no token a call sees or writes are not followed:
+ * pages that a window has left behind may be given back.
+ */
+typedef struct {
+  ss_heads k, v;
+  int64_t num_pages;
+  int page_size;         /* >= 1 */
+  const int32_t* table;  /* [batch, max_pages] int32 */
+  int max_pages;         /* >= 1; max_pages * page_size below 2^31 - 1024 */
+} ss_pages;
+
+/*
+ * ss_winattn_step -- the newest tokens of every sequence over the cache that holds
+ * them and all before.
+ *
+ *  q        [batch, tokens, heads, d]: row b's tokens lengths[b] - tokens ..
+ *           lengths[b] - 1 (one in plain decoding; several drafted ones, or a short
+ *           turn, see one another as in the prompt)
+ *  lengths  [batch] int32: tokens in row b's cache, taken into 0 .. max_pages *
+ *           page_size
+ *  o_out    [batch, tokens, heads, d] in_dtype, contiguous: zero for a query that
+ *           sees nothing (a row of length 0, one of fewer than `tokens` tokens in its
+ *           missing places)
+ *
+ * Sizes as ss_winattn_fwd, batch * kv_heads at most 65535, tokens * heads / kv_heads
+ * below 2^19.  No workspace.
+ */
+ss_status ss_winattn_step(const ss_heads* q, const ss_pages* pages,
+                          const int32_t* lengths, int64_t window, int64_t sinks,
+                          float scale, void* o_out, int64_t batch, int64_t tokens,
+                          int heads, int kv_heads, int d, ss_dtype in_dtype,
+                          cudaStream_t stream);
+
+/*
+ * The rotation of positions: of each head's first 2 * half values, pair i is turned by
+ * the angle position * inv_freq[i], worked out in 64 bits,
+ *
+ *   (x, y) -> (x cos a - y sin a, x sin a + y cos a)
+ *
+ * with x and y the values i and half + i, or 2 i and 2 i + 1 (interleaved != 0); the
+ * values from 2 * half on stay as they are.
+ */
+typedef struct {
+  const float* inv_freq;  /* [half] float32; nullable with half 0 (no rotation) */
+  int half;               /* 0 .. d / 2 */
+  int interleaved;
+} ss_rotation;
+
+/*
+ * ss_kv_append -- new tokens' keys and values into the cache, the keys rotated on the
+ * way, and the tokens' queries rotated.
+ *
+ *  k, v     [batch, tokens, kv_heads, d]: row b's token t goes to position starts[b] + t
+ *  q        [batch, tokens, heads, d], nullable (with q_out); heads is then ignored
+ *  starts   [batch] int32: tokens that row b's cache holds before.  A negative one
+ *           marks a row of padding: its tokens stay out of the cache
+ *  counts   [batch] int32, nullable: row b has counts[b] new tokens, taken into 0 ..
+ *           tokens; nothing behind them is read or written
+ *  q_out    [batch, tokens, heads, d] in_dtype, contiguous: the rotated queries
+ *  k_out    [batch, tokens, kv_heads, d] in_dtype, contiguous, nullable: the rotated
+ *           keys as they are in the cache, for a prompt's attention over itself
+ *
+ * q_out may be the buffer of q, k_out that of k (contiguous, then turned in place).
+ * A position beyond max_pages * page_size, or in no page, is left out of the cache
+ * (q_out and k_out have it).  No two tokens may have the same place.  Values are turned
+ * in fp32 and rounded once; v is copied.  1 <= d <= 1024, the other sizes as
+ * ss_winattn_fwd (heads a multiple of kv_heads).
+ */
+ss_status ss_kv_append(const ss_heads* k, const ss_heads* v, const ss_heads* q,
+                       const ss_pages* pages, const int32_t* starts,
+                       const int32_t* counts, const ss_rotation* rotation, void* q_out,
+                       void* k_out, int64_t batch, int64_t tokens, int heads,
+                       int kv_heads, int d, ss_dtype in_dtype, cudaStream_t stream);
+
+/*
+ * ss_rotate -- the same rotation by itself, of queries and, nullable (with k_out),
+ * keys, where no cache is involved (training); inverse != 0 turns back, which is the
+ * rotation's gradient.  Row b's token t has position starts[b] + t (starts nullable:
+ * t); the rest as in ss_kv_append, in place among it.
+ */
+ss_status ss_rotate(const ss_heads* q, const ss_heads* k, const int32_t* starts,
+                    const int32_t* counts, const ss_rotation* rotation, int inverse,
+                    void* q_out, void* k_out, int64_t batch, int64_t tokens, int heads,
+                    int kv_heads, int d, ss_dtype in_dtype, cudaStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SS_WINATTN_H_ */

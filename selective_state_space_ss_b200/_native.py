@@ -30,7 +30,9 @@ EXPORTED = ("ss_scan_fwd", "ss_scan_workspace_bytes", "ss_status_string",
             "ss_scan_bwd", "ss_scan_bwd_workspace_bytes", "ss_scan_fwd_train",
             "ss_debug_pointwise", "ss_debug_fwd_kernels",
             "ss_linattn_fwd", "ss_linattn_workspace_bytes", "ss_linattn_bwd",
-            "ss_linattn_bwd_workspace_bytes", "ss_linattn_step", "ss_state_store8", "ss_state_load8")
+            "ss_linattn_bwd_workspace_bytes", "ss_linattn_step", "ss_state_store8", "ss_state_load8",
+            "ss_winattn_fwd", "ss_winattn_bwd", "ss_winattn_bwd_workspace_bytes", "ss_winattn_step",
+            "ss_kv_append", "ss_rotate")
 
 # bytes of the library's static scratch array (SS_NOALLOC_SCRATCH_BYTES)
 SS_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -48,6 +50,17 @@ class SSHeads(ctypes.Structure):
     """ss_heads (include/ss_linattn.h): a [batch, seqlen, heads, d] tensor with strides."""
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class SSPages(ctypes.Structure):
+    """ss_pages (include/ss_winattn.h): a paged cache of keys and values."""
+    _fields_ = [("k", SSHeads), ("v", SSHeads), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("table", ctypes.c_void_p), ("max_pages", ctypes.c_int)]
+
+
+class SSRotation(ctypes.Structure):
+    """ss_rotation (include/ss_winattn.h)."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("half", ctypes.c_int), ("interleaved", ctypes.c_int)]
 
 
 class SSError(RuntimeError):
@@ -118,8 +131,18 @@ def load_library():
         lib.ss_linattn_step.argtypes = [hp, hp, hp, hp, cf, vp, i64, vp, vp, i64, ci, ci, ci, ci, ci, vp]
         lib.ss_state_store8.argtypes = [vp, vp, vp, i64, vp, i64, i64, ci, vp]
         lib.ss_state_load8.argtypes = [vp, vp, i64, vp, vp, i64, i64, ci, vp]
+        heads = [i64, i64, ci, ci, ci, ci]  # batch, seqlen or tokens, heads, kv_heads, d, dtype
+        pp, rp = ctypes.POINTER(SSPages), ctypes.POINTER(SSRotation)
+        lib.ss_winattn_fwd.argtypes = [hp, hp, hp, i64, i64, cf, vp, vp, vp, *heads, vp]
+        lib.ss_winattn_bwd.argtypes = [hp, hp, hp, hp, vp, hp, i64, i64, cf, vp, vp, vp, vp, *heads, vp, sz, vp]
+        lib.ss_winattn_bwd_workspace_bytes.argtypes = [i64, i64, ci, ci, ci, i64, i64, ci]
+        lib.ss_winattn_bwd_workspace_bytes.restype = sz
+        lib.ss_winattn_step.argtypes = [hp, pp, vp, i64, i64, cf, vp, *heads, vp]
+        lib.ss_kv_append.argtypes = [hp, hp, hp, pp, vp, vp, rp, vp, vp, *heads, vp]
+        lib.ss_rotate.argtypes = [hp, hp, vp, vp, rp, ci, vp, vp, *heads, vp]
         for f in (lib.ss_linattn_fwd, lib.ss_linattn_bwd, lib.ss_linattn_step, lib.ss_state_store8,
-                  lib.ss_state_load8):
+                  lib.ss_state_load8, lib.ss_winattn_fwd, lib.ss_winattn_bwd, lib.ss_winattn_step,
+                  lib.ss_kv_append, lib.ss_rotate):
             f.restype = ci
         _lib = lib
         return lib
@@ -777,3 +800,227 @@ def ss_state_load8(codes, scales, slots=None, state_out=None, stream=None):
     _call(lib.ss_state_load8, "ss_state_load8", device, *ptrs, out, batch,
           math.prod(shape[:-1]), shape[-1])
     return state_out
+
+
+# ---- attention over a window with sinks, its paged cache, the rotation (include/ss_winattn.h)
+
+
+def _winattn_operands(what, q, k, v):
+    device = _cuda_device("q", q, what)
+    if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("q must be [batch, L, heads, d], k and v [batch, L, kv_heads, d]")
+    dt, dtype, shape = _in_dtype(q), q.dtype, q.shape
+    batch, L, heads, d = shape
+    kv = (batch, L, k.shape[2], d)
+    ops = [_heads4("q", q, device, dtype, shape), _heads4("k", k, device, dtype, kv),
+           _heads4("v", v, device, dtype, kv)]
+    return device, ops, (batch, L, heads, kv[2], d, dt)
+
+
+def _count(name, n):
+    """A window or a number of sinks as the C ABI takes it."""
+    n = int(n)
+    if not 0 <= n < 1 << 62:
+        raise ValueError(f"{name}: {n} is out of range")
+    return n
+
+
+@_on_its_stream
+def ss_winattn_fwd(q, k, v, window, sinks=0, scale=None, lengths=None, o_out=None, lse_out=None, return_lse=True,
+                   stream=None):
+    """Attention over a window with sinks, over a whole prompt: token t sees the tokens j <= t
+    with t - j < window or j < sinks; o_t = sum_j softmax_j(scale * q_t . k_j) v_j.
+
+    q: [batch, L, heads, d]; k, v: [batch, L, kv_heads, d]; one dtype, float32 or bfloat16,
+    strided (last axis contiguous); heads a multiple of kv_heads, d at most 128.  scale: d ** -0.5
+    when not given.  lengths: [batch] int32; nothing is written to o_out and lse_out behind a
+    row's length (what is allocated here is zero there).  Returns (o [batch, L, heads, d] in the
+    input dtype, lse [batch, heads, L] float32 for ss_winattn_bwd, or None).
+    """
+    lib = _lib or load_library()
+    device, ops, sizes = _winattn_operands("ss_winattn_fwd", q, k, v)
+    batch, L, heads, _, d, _ = sizes
+    rows = _dense("lengths", lengths, device, torch.int32, (batch,))
+    make = q.new_empty if lengths is None else q.new_zeros
+    if o_out is None:
+        o_out = make(q.shape)
+        o_ptr = o_out.data_ptr()
+    else:
+        o_ptr = _dense("o_out", o_out, device, q.dtype, q.shape)
+    if lse_out is None and return_lse:
+        lse_out = make((batch, heads, L), dtype=torch.float32)
+        lse_ptr = lse_out.data_ptr()
+    else:
+        lse_ptr = _dense("lse_out", lse_out, device, torch.float32, (batch, heads, L))
+    _call(lib.ss_winattn_fwd, "ss_winattn_fwd", device, *ops, _count("window", window), _count("sinks", sinks),
+          d ** -0.5 if scale is None else scale, rows, o_ptr, lse_ptr, *sizes)
+    return o_out, lse_out
+
+
+@functools.lru_cache(maxsize=1024)
+def ss_winattn_bwd_workspace_bytes(batch, seqlen, heads, kv_heads, d, window, sinks, in_dtype) -> int:
+    n = load_library().ss_winattn_bwd_workspace_bytes(batch, seqlen, heads, kv_heads, d, _count("window", window),
+                                                      _count("sinks", sinks), int(in_dtype))
+    if n == ctypes.c_size_t(-1).value:
+        unsupported = min(batch, seqlen, heads, kv_heads) >= 1 and heads % kv_heads == 0 and d > 128
+        raise SSError(SS_ERR_UNSUPPORTED if unsupported else SS_ERR_INVALID_ARG, "ss_winattn_bwd_workspace_bytes")
+    return n
+
+
+@_on_its_stream
+def ss_winattn_bwd(q, k, v, o, lse, do, window, sinks=0, scale=None, lengths=None, workspace=None, stream=None):
+    """Gradients of ss_winattn_fwd for an upstream do [batch, L, heads, d] (the inputs' dtype,
+    strided), from its inputs, its o (strided) and its lse.
+
+    Returns a dict: dq, dk, dv (the latter two summed over the heads that share them) in the
+    inputs' dtype, zero behind a row's length.
+    """
+    lib = _lib or load_library()
+    device, ops, sizes = _winattn_operands("ss_winattn_bwd", q, k, v)
+    batch, L, heads, kv_heads, d, dt = sizes
+    window, sinks = _count("window", window), _count("sinks", sinks)
+    need = ss_winattn_bwd_workspace_bytes(batch, L, heads, kv_heads, d, window, sinks, dt)
+    o_op = _heads4("o", o, device, q.dtype, q.shape)
+    if lse is None:
+        raise ValueError("lse: the forward's, a float32 tensor")
+    lse_ptr = _dense("lse", lse, device, torch.float32, (batch, heads, L))
+    do_op = _heads4("do", do, device, q.dtype, q.shape)
+    rows = _dense("lengths", lengths, device, torch.int32, (batch,))
+    make = q.new_empty if lengths is None else q.new_zeros
+    g = {"dq": make(q.shape), "dk": make(k.shape), "dv": make(k.shape)}
+    keep, ws, ws_bytes = _workspace(workspace, need, device)
+    _call(lib.ss_winattn_bwd, "ss_winattn_bwd", device, *ops, o_op, lse_ptr, do_op, window, sinks,
+          d ** -0.5 if scale is None else scale, rows, *[t.data_ptr() for t in g.values()], *sizes, ws, ws_bytes)
+    return g
+
+
+def _pages(device, dtype, kv_heads, d, batch, k_pages, v_pages, page_table):
+    shape = getattr(k_pages, "shape", ())
+    if len(shape) != 4 or shape[2:] != (kv_heads, d):
+        raise ValueError(f"k_pages and v_pages must be [num_pages, page_size, {kv_heads}, {d}]")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    table = page_table.shape
+    return SSPages(_heads4("k_pages", k_pages, device, dtype, shape), _heads4("v_pages", v_pages, device, dtype, shape),
+                   shape[0], shape[1], _dense("page_table", page_table, device, torch.int32, (batch, table[1])), table[1])
+
+
+@_on_its_stream
+def ss_winattn_step(q, k_pages, v_pages, page_table, lengths, window, sinks=0, scale=None, o_out=None, stream=None):
+    """The newest tokens of every sequence over its paged cache, which holds them already
+    (ss_kv_append) and all before.
+
+    q: [batch, tokens, heads, d], the last `tokens` tokens of each row (one in plain decoding);
+    k_pages, v_pages: [num_pages, page_size, kv_heads, d] (strided); page_table: [batch,
+    max_pages] int32, the pages of each row's tokens in order (entries that no visible token lies
+    in are not followed); lengths: [batch] int32, tokens in each row's cache.  Returns o [batch,
+    tokens, heads, d], zero for a query that sees nothing (a row of length 0).
+    """
+    lib = _lib or load_library()
+    device = _cuda_device("q", q, "ss_winattn_step")
+    if q.dim() != 4 or not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("q must be [batch, tokens, heads, d], k_pages and v_pages [num_pages, page_size, kv_heads, d]")
+    dt, dtype, shape = _in_dtype(q), q.dtype, q.shape
+    batch, tokens, heads, d = shape
+    kv_heads = k_pages.shape[2]
+    pages = _pages(device, dtype, kv_heads, d, batch, k_pages, v_pages, page_table)
+    if lengths is None:
+        raise ValueError("lengths must be a [batch] int32 tensor")
+    if o_out is None:
+        o_out = q.new_empty(shape)
+        o_ptr = o_out.data_ptr()
+    else:
+        o_ptr = _dense("o_out", o_out, device, dtype, shape)
+    _call(lib.ss_winattn_step, "ss_winattn_step", device, _heads4("q", q, device, dtype, shape), pages,
+          _dense("lengths", lengths, device, torch.int32, (batch,)), _count("window", window), _count("sinks", sinks),
+          d ** -0.5 if scale is None else scale, o_ptr, batch, tokens, heads, kv_heads, d, dt)
+    return o_out
+
+
+def _rotation(device, inv_freq, interleaved):
+    if inv_freq is None:
+        return SSRotation(None, 0, 0)
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a [rotated / 2] float32 tensor")
+    n = inv_freq.shape[0]
+    return SSRotation(_dense("inv_freq", inv_freq, device, torch.float32, (n,)) if n else None, n, int(bool(interleaved)))
+
+
+def _rotated(name, out, x, device, partial):
+    """Output of a rotation: the one given, or a new one (zero where tokens may be left out)."""
+    if out is None:
+        out = (x.new_zeros if partial else x.new_empty)(x.shape)
+        return out, out.data_ptr()
+    return out, _dense(name, out, device, x.dtype, x.shape)
+
+
+@_on_its_stream
+def ss_kv_append(k, v, k_pages, v_pages, page_table, starts, inv_freq=None, q=None, counts=None, interleaved=False,
+                 q_out=None, k_out=None, return_k=False, stream=None):
+    """New tokens' keys and values into a paged cache, the keys rotated by their positions on the
+    way, and the same tokens' queries rotated.
+
+    k, v: [batch, tokens, kv_heads, d], q: [batch, tokens, heads, d] (strided); row b's token t
+    has position starts[b] + t ([batch] int32; rows of a negative start stay out of the cache).  counts:
+    [batch] int32, new tokens of each row (None: all).  inv_freq: [rotated / 2] float32, the
+    angle of a pair per position (None: no rotation); pairs are (i, i + rotated / 2), or
+    (2 i, 2 i + 1) with interleaved.  Returns (q rotated or None without q, k rotated as the
+    cache has it with return_k or k_out, else None); q_out may be q itself, k_out k.
+    """
+    lib = _lib or load_library()
+    device = _cuda_device("k", k, "ss_kv_append")
+    if k.dim() != 4:
+        raise ValueError("k and v must be [batch, tokens, kv_heads, d]")
+    dt, dtype, shape = _in_dtype(k), k.dtype, k.shape
+    batch, tokens, kv_heads, d = shape
+    pages = _pages(device, dtype, kv_heads, d, batch, k_pages, v_pages, page_table)
+    if starts is None:
+        raise ValueError("starts must be a [batch] int32 tensor")
+    rows = (_dense("starts", starts, device, torch.int32, (batch,)), _dense("counts", counts, device, torch.int32, (batch,)))
+    heads, q_op, q_ptr, k_ptr = kv_heads, None, None, None
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("q must be [batch, tokens, heads, d]")
+        heads = q.shape[2]
+        q_op = _heads4("q", q, device, dtype, (batch, tokens, heads, d))
+        q_out, q_ptr = _rotated("q_out", q_out, q, device, counts is not None)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if return_k or k_out is not None:
+        k_out, k_ptr = _rotated("k_out", k_out, k, device, counts is not None)
+    _call(lib.ss_kv_append, "ss_kv_append", device, _heads4("k", k, device, dtype, shape), _heads4("v", v, device, dtype, shape),
+          q_op, pages, *rows, _rotation(device, inv_freq, interleaved), q_ptr, k_ptr, batch, tokens, heads, kv_heads, d, dt)
+    return q_out, k_out
+
+
+@_on_its_stream
+def ss_rotate(q, inv_freq, k=None, starts=None, counts=None, interleaved=False, inverse=False, q_out=None, k_out=None,
+              stream=None):
+    """Heads' values rotated by their positions, as ss_kv_append does, without a cache; inverse
+    turns back, which is the gradient.
+
+    q: [batch, L, heads, d]; k: [batch, L, kv_heads, d] (strided); inv_freq: [rotated / 2]
+    float32; row b's token t has position starts[b] + t ([batch] int32; None: t); counts:
+    [batch] int32, tokens of each row.  Returns (q rotated, k rotated or None); q_out may be q
+    itself, k_out k.
+    """
+    lib = _lib or load_library()
+    device = _cuda_device("q", q, "ss_rotate")
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, L, heads, d]")
+    dt, dtype, shape = _in_dtype(q), q.dtype, q.shape
+    batch, L, heads, d = shape
+    q_op, k_op, k_ptr, kv_heads = _heads4("q", q, device, dtype, shape), None, None, heads
+    rows = (_dense("starts", starts, device, torch.int32, (batch,)), _dense("counts", counts, device, torch.int32, (batch,)))
+    q_out, q_ptr = _rotated("q_out", q_out, q, device, counts is not None)
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be [batch, L, kv_heads, d]")
+        kv_heads = k.shape[2]
+        k_op = _heads4("k", k, device, dtype, (batch, L, kv_heads, d))
+        k_out, k_ptr = _rotated("k_out", k_out, k, device, counts is not None)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _call(lib.ss_rotate, "ss_rotate", device, q_op, k_op, *rows, _rotation(device, inv_freq, interleaved),
+          int(bool(inverse)), q_ptr, k_ptr, batch, L, heads, kv_heads, d, dt)
+    return q_out, k_out

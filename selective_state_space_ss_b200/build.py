@@ -19,7 +19,7 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
 def sources():
-    return [os.path.join(CSRC, "ss_scan.cu"), os.path.join(CSRC, "ss_linattn.cu")]
+    return [os.path.join(CSRC, f) for f in ("ss_scan.cu", "ss_linattn.cu", "ss_winattn.cu")]
 
 
 def deps():

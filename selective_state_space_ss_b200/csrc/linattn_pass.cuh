@@ -75,31 +75,17 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "heads.cuh"
 #include "scan_common.cuh"
 #include "tc5.cuh"
+#include "waits.cuh"
 
 namespace ssscan {
 
 constexpr int kLaChunk = 64;
 constexpr int kLaBlock = kLaChunk * kTileRow;  // bytes of one plane's 64 x 64 block
-// Polls before a wait gives up, a second or so.  A poll of a barrier suspends the thread
-// for as long as the hardware likes, 3 to 4 us whatever longer time it is given; a poll of
-// the previous worker's flag takes about as many tenths.  (512 polls of the first gave up
-// after 2 ms, which a worker may well wait for a state where the rows between are short.)
-// As a launch's argument the first limit cost 2 to 4%.
-constexpr uint32_t kLaSpinLimit = 1u << 18;
+// Polls before a wait for another worker's state gives up (waits.cuh).
 constexpr uint32_t kLaCarrySpinLimit = 1u << 21;
-
-// A [batch, seqlen, heads, d] tensor, last axis contiguous, strides in elements;
-// `share` consecutive heads of the pass read one of its heads.
-struct LaTensor {
-  const void* ptr;
-  int64_t sb, st, sh;
-  int share;
-#ifdef SS_BOUNDS_CHECK
-  int64_t lo, n;  // its elements: n of them from offset lo on
-#endif
-};
 
 struct LaPassArgs {
   LaTensor q, k, v;
@@ -196,76 +182,10 @@ struct LaCfg {
 constexpr int kLaBackWarps = 16, kLaFrontWarps = 8;
 constexpr int kLaMmaWarp = 24, kLaLoadWarp = 25, kLaMmaOrLoadWarp = 26, kLaDecayWarp = 27;
 
-// Waits of one CTA: when one gives up, the others stop waiting too, and the kernel
-// runs to its end on whatever is there, inside its buffers.  A poll suspends the
-// thread, so that those that wait leave the issue slots to the others.
-__device__ __forceinline__ bool la_poll(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(10000000)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kLaSpinLimit; ++i) {
-    if (la_poll(bar, parity)) return true;
-    if (*dead) return false;
-  }
-  atomicOr(&g_error_word, kErrTmaWait);
-  *dead = 1;
-  return false;
-}
-// Whatever else gave up: for copies and products of one's own that are in flight.
-__device__ __forceinline__ void la_wait_own(uint32_t bar, uint32_t parity) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kLaSpinLimit; ++i)
-    if (la_poll(bar, parity)) return;
-  atomicOr(&g_error_word, kErrTmaWait);
-}
-__device__ __forceinline__ void la_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void la_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void la_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-// A place in a ring of R and how often it came round: full barriers complete phase
-// `turn`, empty ones are waited for from the second turn on.
-template <int R>
-struct LaRing {
-  int i = 0;
-  uint32_t turn = 0;
-  __device__ __forceinline__ void next() {
-    if (++i == R) i = 0, ++turn;
-  }
-  __device__ __forceinline__ uint32_t full() const { return turn & 1; }
-  __device__ __forceinline__ bool used() const { return turn > 0; }
-  __device__ __forceinline__ uint32_t empty() const { return (turn - 1) & 1; }
-};
-
 __device__ __forceinline__ int la_length(const LaPassArgs& a, int64_t b) {
   if (!a.lengths) return a.seqlen;
   const int n = a.lengths[b];
   return n < 0 ? 0 : n < a.seqlen ? n : a.seqlen;
-}
-
-__device__ __forceinline__ const char* la_row(const LaTensor& x, int64_t b, int64_t t, int h, int es) {
-  return static_cast<const char*>(x.ptr) + (b * x.sb + t * x.st + (int64_t)(h / x.share) * x.sh) * es;
-}
-
-// Checked builds: whether `count` elements at `from` are the tensor's.
-__device__ __forceinline__ bool la_inside(const LaTensor& x, const char* from, int count, int es) {
-#ifdef SS_BOUNDS_CHECK
-  return in_range((from - static_cast<const char*>(x.ptr)) / es - x.lo, count, x.n);
-#else
-  return true;
-#endif
 }
 
 // One tile of 64 tokens into shared memory: rows from `len` on and columns from `d`

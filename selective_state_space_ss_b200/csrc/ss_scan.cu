@@ -21,6 +21,8 @@ namespace ssscan {
 // ss_linattn.cu
 bool take_linattn_error_word(unsigned int* word);
 void set_linattn_debug(int what, long long value);
+// ss_winattn.cu's
+bool take_winattn_error_word(unsigned int* word);
 }
 
 // Scratch of ss_scan_fwd_noalloc: one file-scope device array, held by every
@@ -302,14 +304,14 @@ const char* ss_status_string(ss_status s) {
 ss_status ss_last_device_error(cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return SS_ERR_CUDA;
   unsigned int word = 0;
-  unsigned int other = 0;  // the linear attention's kernels have a word of their own
+  unsigned int other = 0, third = 0;  // the linear attention's kernels have a word of their own, the window's too
   if (cudaMemcpyFromSymbol(&word, g_error_word, sizeof word) != cudaSuccess) return SS_ERR_CUDA;
-  if (!take_linattn_error_word(&other)) return SS_ERR_CUDA;
+  if (!take_linattn_error_word(&other) || !take_winattn_error_word(&third)) return SS_ERR_CUDA;
   if (word != 0) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof zero) != cudaSuccess) return SS_ERR_CUDA;
   }
-  word |= other;
+  word |= other | third;
   if (word != 0) return (word & kErrBounds) ? SS_ERR_BOUNDS : SS_ERR_TIMEOUT;
   return SS_OK;
 }

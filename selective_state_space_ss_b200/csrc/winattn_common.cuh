@@ -1,0 +1,80 @@
+// winattn_common.cuh -- what the window attention's kernels share: arguments, which
+// token sees which, and the tiles that a block of tokens has to look at.
+#pragma once
+
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "heads.cuh"
+#include "scan_common.cuh"
+
+namespace ssscan {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct WaArgs {
+  LaTensor q, k, v;    // share: heads / kv_heads for k and v, numbered by the queries' heads
+  const int* lengths;  // [batch] or null
+  void* out;           // [batch, seqlen, heads, d] contiguous
+  float* lse;          // [batch, heads, seqlen], nullable in the forward
+  int64_t window;
+  int sinks, seqlen, heads, share, d, batch;  // share: heads that read one head of keys
+  float scale;
+  // backward
+  LaTensor o, g;       // the forward's result and its gradient
+  float* delta;        // [batch, heads, seqlen]: do . o
+  void *dk, *dv;       // [batch, seqlen, kv_heads, d] contiguous
+  float* part;         // partial dk, dv of the tiles that hold sinks (WaSplit)
+  int sink_tiles, pieces, piece_tiles;  // WaSplit
+};
+
+__device__ __forceinline__ int wa_length(const int* lengths, int64_t b, int most) {
+  if (!lengths) return most;
+  const int n = lengths[b];
+  return n < 0 ? 0 : n < most ? n : most;
+}
+
+// Whether the token at `row` sees that at `col`.
+__device__ __forceinline__ bool wa_sees(int row, int col, int64_t window, int sinks) {
+  return col <= row && (row - col < window || col < sinks);
+}
+
+// The key tiles of N tokens that rows r0 .. r1 - 1 (r1 > r0) see any of: first those of the
+// sinks that the window does not reach, then the window's.
+template <int N>
+struct WaKeyTiles {
+  int sink, first, count;
+  __device__ __forceinline__ WaKeyTiles(int r0, int r1, int64_t window, int sinks) {
+    const int64_t from = (int64_t)r0 + 1 - window;
+    first = from > 0 ? (int)(from / N) : 0;
+    const int s = (sinks + N - 1) / N;
+    sink = s < first ? s : first;
+    count = sink + (r1 - 1) / N - first + 1;
+  }
+  __device__ __forceinline__ int at(int i) const { return i < sink ? i : first + i - sink; }
+};
+
+// Whether all of rows r0 .. r1 - 1 see all of the columns c0 .. c1 - 1.
+__device__ __forceinline__ bool wa_all_seen(int r0, int r1, int c0, int c1, int64_t window, int sinks) {
+  return c1 - 1 <= r0 && (r1 - 1 - c0 < window || c1 <= sinks);
+}
+
+// The queries that a key tile c0 .. c1 - 1 meets, in tiles of N tokens.  Those that see it
+// through the window are `near`: first .. near - 1.  A tile that holds sinks is met by all
+// queries behind as well; these are cut into pieces, each a block of its own, so that no
+// block has much more to do than the others, and the pieces' sums are added up afterwards,
+// in their order.
+template <int N>
+struct WaQueryTiles {
+  int first, near, last;  // last: behind the last tile that sees any of the keys
+  __device__ __forceinline__ WaQueryTiles(int c0, int c1, int len, int64_t window, int sinks) {
+    const int all = (len + N - 1) / N;
+    const int64_t end = ((int64_t)c1 + window - 2) / N + 1;  // the last key is seen by c1 - 1 + window - 1
+    first = c0 / N;
+    near = end < all ? (int)end : all;
+    last = c0 < sinks ? all : near;
+    if (c0 >= len) first = near = last = 0;
+  }
+};
+
+}  // namespace ssscan

@@ -1,0 +1,386 @@
+// winattn_fma.cuh -- the window attention in fp32 arithmetic (ss_winattn_fwd and
+// ss_winattn_bwd for float32 operands, and for bfloat16 ones whose rows are not whole
+// 16-byte units).
+//
+// A block takes 64 queries (or, for the keys' gradients, 64 keys) of one head and walks
+// the tiles of 64 keys (queries) that they meet; every product is a 64 x 64 x d or
+// 64 x d x 64 one in registers, 4 x 4 or 4 x d/16 values a thread, from tiles in shared
+// memory.  The forward keeps the running maximum and sum of the softmax; the backward
+// works the probabilities out again from the saved normaliser.
+#pragma once
+
+#include "winattn_common.cuh"
+
+namespace ssscan {
+
+constexpr int kWfTile = 64, kWfThreads = 256;
+
+// Shared memory, in floats: rows of DP + 4 so that a quarter-warp's rows lie in different banks.
+template <int DP>
+struct WfCfg {
+  static constexpr int kRow = DP + 4, kScoreRow = kWfTile + 4;
+  static constexpr int kTile = kWfTile * kRow, kScores = kWfTile * kScoreRow;
+  static constexpr int kFwd = 2 * kTile + kScores, kDq = 4 * kTile + kScores, kDkv = 4 * kTile + 2 * kScores;
+};
+
+// A tile of 64 tokens from t0 on into fp32 rows; what is behind `len` or d is zero.
+template <typename T, int DP>
+__device__ __forceinline__ void wf_load(float* to, const LaTensor& x, int64_t b, int h, int t0, int len, int d) {
+  constexpr int kRow = WfCfg<DP>::kRow;
+  const bool vec = sizeof(T) == 4 && d % 4 == 0 && reinterpret_cast<uintptr_t>(x.ptr) % 16 == 0 && x.sb % 4 == 0 &&
+                   x.st % 4 == 0 && x.sh % 4 == 0;
+  for (int u = threadIdx.x; u < kWfTile * (DP / 4); u += kWfThreads) {
+    const int row = u / (DP / 4), col = u % (DP / 4) * 4;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t0 + row < len && col < d) {
+      const char* from = la_row(x, b, t0 + row, h, sizeof(T)) + col * sizeof(T);
+      if (la_inside(x, from, d - col < 4 ? d - col : 4, sizeof(T))) {
+        const T* p = reinterpret_cast<const T*>(from);
+        if (vec) {
+          y = *reinterpret_cast<const float4*>(from);
+        } else {
+          y.x = to_f32(p[0]);
+          if (col + 1 < d) y.y = to_f32(p[1]);
+          if (col + 2 < d) y.z = to_f32(p[2]);
+          if (col + 3 < d) y.w = to_f32(p[3]);
+        }
+      }
+    }
+    *reinterpret_cast<float4*>(to + row * kRow + col) = y;
+  }
+}
+
+// s[i][j] = <a row 4 ty + i, b row tx + 16 j>
+template <int DP>
+__device__ __forceinline__ void wf_scores(float (&s)[4][4], const float* a, const float* b, int ty, int tx) {
+  constexpr int kRow = WfCfg<DP>::kRow;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < DP; k += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (4 * ty + i) * kRow + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * kRow + k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
+        s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
+        s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
+        s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+      }
+  }
+}
+
+// acc[i] += sum_j w[4 ty + i][j] x row j (TRANSPOSED: w[j][4 ty + i]), columns 4 tx + 64 c
+template <int DP, bool TRANSPOSED>
+__device__ __forceinline__ void wf_accumulate(float (&acc)[4][DP / 16], const float* w, const float* x, int ty, int tx) {
+  constexpr int kRow = WfCfg<DP>::kRow, kW = WfCfg<DP>::kScoreRow;
+#pragma unroll 2
+  for (int j = 0; j < kWfTile; j += 4) {
+    float p[4][4];  // [i][j]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 y = *reinterpret_cast<const float4*>(TRANSPOSED ? w + (j + i) * kW + 4 * ty : w + (4 * ty + i) * kW + j);
+      if (TRANSPOSED) p[0][i] = y.x, p[1][i] = y.y, p[2][i] = y.z, p[3][i] = y.w;
+      else p[i][0] = y.x, p[i][1] = y.y, p[i][2] = y.z, p[i][3] = y.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) {
+        const float4 y = *reinterpret_cast<const float4*>(x + (j + k) * kRow + 4 * tx + 64 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i][4 * c] = fmaf(p[i][k], y.x, acc[i][4 * c]);
+          acc[i][4 * c + 1] = fmaf(p[i][k], y.y, acc[i][4 * c + 1]);
+          acc[i][4 * c + 2] = fmaf(p[i][k], y.z, acc[i][4 * c + 2]);
+          acc[i][4 * c + 3] = fmaf(p[i][k], y.w, acc[i][4 * c + 3]);
+        }
+      }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T wf_round(float x);
+template <>
+__device__ __forceinline__ float wf_round<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 wf_round<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Row r of [.., heads, d] output from this thread's columns.
+template <typename T, int DP>
+__device__ __forceinline__ void wf_store(T* row, const float (&acc)[DP / 16], float by, int d, int tx) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (4 * tx + 64 * c + e < d) row[4 * tx + 64 * c + e] = wf_round<T>(acc[4 * c + e] * by);
+}
+
+__device__ __forceinline__ float wf_max16(float x) {
+#pragma unroll
+  for (int o = 1; o < 16; o *= 2) x = fmaxf(x, __shfl_xor_sync(kFullMask, x, o));
+  return x;
+}
+__device__ __forceinline__ float wf_sum16(float x) {
+#pragma unroll
+  for (int o = 1; o < 16; o *= 2) x += __shfl_xor_sync(kFullMask, x, o);
+  return x;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kWfThreads) winattn_fma_fwd_kernel(const __grid_constant__ WaArgs a) {
+  using CF = WfCfg<DP>;
+  extern __shared__ __align__(16) float wf_smem[];
+  float *q = wf_smem, *kv = q + CF::kTile, *p = kv + CF::kTile;
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const int bh_all = a.batch * a.heads, bh = blockIdx.x % bh_all, b = bh / a.heads, h = bh % a.heads;
+  const int tiles = gridDim.x / bh_all, r0 = (tiles - 1 - (int)(blockIdx.x / bh_all)) * kWfTile;  // long rows first
+  const int len = wa_length(a.lengths, b, a.seqlen);
+  if (r0 >= len) return;
+  const int r1 = r0 + kWfTile < len ? r0 + kWfTile : len;
+  wf_load<T, DP>(q, a.q, b, h, r0, len, a.d);
+  const float by = a.scale * kLog2e;  // exponents are of base 2
+  float acc[4][DP / 16] = {}, top[4], sum[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top[i] = -CUDART_INF_F, sum[i] = 0.f;
+  const WaKeyTiles<kWfTile> keys(r0, r1, a.window, a.sinks);
+  for (int n = 0; n < keys.count; ++n) {
+    const int c0 = keys.at(n) * kWfTile;
+    __syncthreads();
+    wf_load<T, DP>(kv, a.k, b, h, c0, len, a.d);
+    __syncthreads();
+    float s[4][4];
+    wf_scores<DP>(s, q, kv, ty, tx);
+    const bool all = wa_all_seen(r0, r1, c0, c0 + kWfTile, a.window, a.sinks);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float most = -CUDART_INF_F;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = all || wa_sees(r0 + 4 * ty + i, c0 + tx + 16 * j, a.window, a.sinks) ? s[i][j] * by : -CUDART_INF_F;
+        most = fmaxf(most, s[i][j]);
+      }
+      most = fmaxf(top[i], wf_max16(most));
+      // a row that has seen nothing yet: exponents from 0, so that nothing is exp(-inf - -inf)
+      const float from = most == -CUDART_INF_F ? 0.f : most;
+      const float fade = exp2f(top[i] - from);
+      float add = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = exp2f(s[i][j] - from);
+        add += s[i][j];
+        p[(4 * ty + i) * CF::kScoreRow + tx + 16 * j] = s[i][j];
+      }
+      top[i] = most;
+      sum[i] = sum[i] * fade + wf_sum16(add);
+#pragma unroll
+      for (int c = 0; c < DP / 16; ++c) acc[i][c] *= fade;
+    }
+    __syncthreads();
+    wf_load<T, DP>(kv, a.v, b, h, c0, len, a.d);
+    __syncthreads();
+    wf_accumulate<DP, false>(acc, p, kv, ty, tx);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = r0 + 4 * ty + i;
+    if (t >= len) continue;
+    const int64_t at = (((int64_t)b * a.seqlen + t) * a.heads + h) * a.d, all = (int64_t)bh_all * a.seqlen;
+    if (in_range(at, a.d, all * a.d)) wf_store<T, DP>(static_cast<T*>(a.out) + at, acc[i], 1.f / sum[i], a.d, tx);
+    const int64_t l = (int64_t)bh * a.seqlen + t;
+    if (a.lse && tx == 0 && in_range(l, all)) a.lse[l] = (top[i] + log2f(sum[i])) * kLn2;
+  }
+}
+
+// p = exp(s - lse) of a tile's scores, and ds = p (dp - delta); both zero where nothing is seen.
+__device__ __forceinline__ void wf_probabilities(float (&s)[4][4], float (&dp)[4][4], const WaArgs& a, int64_t bh, int r0,
+                                                 int c0, int len, int ty, int tx) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = r0 + 4 * ty + i;
+    const bool real = t < len && in_range(bh * a.seqlen + t, (int64_t)a.batch * a.heads * a.seqlen);
+    const float lse = real ? a.lse[bh * a.seqlen + t] * kLog2e : 0.f, delta = real ? a.delta[bh * a.seqlen + t] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool seen = real && wa_sees(t, c0 + tx + 16 * j, a.window, a.sinks);
+      s[i][j] = seen ? exp2f(s[i][j] * (a.scale * kLog2e) - lse) : 0.f;
+      dp[i][j] = seen ? s[i][j] * (dp[i][j] - delta) : 0.f;
+    }
+  }
+}
+
+template <int DP>
+__device__ __forceinline__ void wf_put_scores(float* to, const float (&s)[4][4], int ty, int tx) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) to[(4 * ty + i) * WfCfg<DP>::kScoreRow + tx + 16 * j] = s[i][j];
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kWfThreads) winattn_fma_dq_kernel(const __grid_constant__ WaArgs a) {
+  using CF = WfCfg<DP>;
+  extern __shared__ __align__(16) float wf_smem[];
+  float *q = wf_smem, *g = q + CF::kTile, *k = g + CF::kTile, *v = k + CF::kTile, *ds = v + CF::kTile;
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const int bh_all = a.batch * a.heads, bh = blockIdx.x % bh_all, b = bh / a.heads, h = bh % a.heads;
+  const int tiles = gridDim.x / bh_all, r0 = (tiles - 1 - (int)(blockIdx.x / bh_all)) * kWfTile;
+  const int len = wa_length(a.lengths, b, a.seqlen);
+  if (r0 >= len) return;
+  const int r1 = r0 + kWfTile < len ? r0 + kWfTile : len;
+  wf_load<T, DP>(q, a.q, b, h, r0, len, a.d);
+  wf_load<T, DP>(g, a.g, b, h, r0, len, a.d);
+  float acc[4][DP / 16] = {};
+  const WaKeyTiles<kWfTile> keys(r0, r1, a.window, a.sinks);
+  for (int n = 0; n < keys.count; ++n) {
+    const int c0 = keys.at(n) * kWfTile;
+    __syncthreads();
+    wf_load<T, DP>(k, a.k, b, h, c0, len, a.d);
+    wf_load<T, DP>(v, a.v, b, h, c0, len, a.d);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    wf_scores<DP>(s, q, k, ty, tx);
+    wf_scores<DP>(dp, g, v, ty, tx);
+    wf_probabilities(s, dp, a, bh, r0, c0, len, ty, tx);
+    wf_put_scores<DP>(ds, dp, ty, tx);
+    __syncthreads();
+    wf_accumulate<DP, false>(acc, ds, k, ty, tx);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = r0 + 4 * ty + i;
+    const int64_t at = (((int64_t)b * a.seqlen + t) * a.heads + h) * a.d;
+    if (t < len && in_range(at, a.d, (int64_t)bh_all * a.seqlen * a.d))
+      wf_store<T, DP>(static_cast<T*>(a.out) + at, acc[i], a.scale, a.d, tx);
+  }
+}
+
+// Where a block of the keys' gradients stands: its key tile, the query tiles that it takes,
+// and whether it leaves a partial sum.
+template <int N>
+struct WaKeyBlock {
+  int tile, from, to, piece;
+  bool partial;
+  __device__ __forceinline__ WaKeyBlock(const WaArgs& a, int item, int len) {
+    const int pieces = a.sink_tiles * a.pieces;  // the sinks' pieces come first, they are as long as any
+    partial = true;
+    if (item < pieces) {
+      tile = item / a.pieces;
+      piece = 1 + item % a.pieces;
+    } else {
+      tile = item - pieces;
+      piece = 0;
+      partial = a.pieces > 0 && tile < a.sink_tiles;
+    }
+    const int c0 = tile * N, c1 = c0 + N < len ? c0 + N : len;
+    const WaQueryTiles<N> queries(c0, c1, len, a.window, a.sinks);
+    from = queries.first;
+    to = a.pieces > 0 ? queries.near : queries.last;
+    if (piece > 0) {
+      const int64_t at = (int64_t)queries.near + (int64_t)(piece - 1) * a.piece_tiles, end = at + a.piece_tiles;
+      from = at < queries.last ? (int)at : queries.last;
+      to = end < queries.last ? (int)end : queries.last;
+    }
+  }
+};
+// Element offset of a partial sum: dk, then dv, of [N, d] each.
+template <int N>
+__device__ __forceinline__ int64_t wa_part(const WaArgs& a, int64_t bh_kv, int tile, int piece) {
+  return ((bh_kv * a.sink_tiles + tile) * (1 + a.pieces) + piece) * 2 * N * a.d;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kWfThreads) winattn_fma_dkv_kernel(const __grid_constant__ WaArgs a) {
+  using CF = WfCfg<DP>;
+  extern __shared__ __align__(16) float wf_smem[];
+  float *k = wf_smem, *v = k + CF::kTile, *q = v + CF::kTile, *g = q + CF::kTile;
+  float *p = g + CF::kTile, *ds = p + CF::kScores;
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const int kv_heads = a.heads / a.share, bh_all = a.batch * kv_heads;
+  const int bh = blockIdx.x % bh_all, b = bh / kv_heads, hk = bh % kv_heads;
+  const int len = wa_length(a.lengths, b, a.seqlen);
+  const WaKeyBlock<kWfTile> w(a, blockIdx.x / bh_all, len);
+  const int c0 = w.tile * kWfTile;
+  if (c0 >= len) return;
+  wf_load<T, DP>(k, a.k, b, hk * a.share, c0, len, a.d);
+  wf_load<T, DP>(v, a.v, b, hk * a.share, c0, len, a.d);
+  float dk[4][DP / 16] = {}, dv[4][DP / 16] = {};
+  for (int h = hk * a.share; h < (hk + 1) * a.share; ++h)
+    for (int n = w.from; n < w.to; ++n) {
+      const int r0 = n * kWfTile;
+      __syncthreads();
+      wf_load<T, DP>(q, a.q, b, h, r0, len, a.d);
+      wf_load<T, DP>(g, a.g, b, h, r0, len, a.d);
+      __syncthreads();
+      float s[4][4], dp[4][4];
+      wf_scores<DP>(s, q, k, ty, tx);
+      wf_scores<DP>(dp, g, v, ty, tx);
+      wf_probabilities(s, dp, a, (int64_t)b * a.heads + h, r0, c0, len, ty, tx);
+      wf_put_scores<DP>(p, s, ty, tx);
+      wf_put_scores<DP>(ds, dp, ty, tx);
+      __syncthreads();
+      wf_accumulate<DP, true>(dv, p, g, ty, tx);
+      wf_accumulate<DP, true>(dk, ds, q, ty, tx);
+    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = 4 * ty + i, t = c0 + j;
+    if (t >= len) continue;
+    if (w.partial) {
+      const int64_t at = wa_part<kWfTile>(a, bh, w.tile, w.piece) + (int64_t)j * a.d;
+      wf_store<float, DP>(a.part + at, dk[i], a.scale, a.d, tx);
+      wf_store<float, DP>(a.part + at + kWfTile * a.d, dv[i], 1.f, a.d, tx);
+      continue;
+    }
+    const int64_t at = (((int64_t)b * a.seqlen + t) * kv_heads + hk) * a.d;
+    if (!in_range(at, a.d, (int64_t)bh_all * a.seqlen * a.d)) continue;
+    wf_store<T, DP>(static_cast<T*>(a.dk) + at, dk[i], a.scale, a.d, tx);
+    wf_store<T, DP>(static_cast<T*>(a.dv) + at, dv[i], 1.f, a.d, tx);
+  }
+}
+
+// delta = do . o of every row, a warp each.
+template <typename T>
+__global__ void __launch_bounds__(256) winattn_delta_kernel(const __grid_constant__ WaArgs a) {
+  const int lane = threadIdx.x % 32;
+  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32, all = (int64_t)a.batch * a.heads * a.seqlen;
+  if (row >= all) return;
+  const int h = (int)(row % a.heads);
+  const int64_t bt = row / a.heads, t = bt % a.seqlen, b = bt / a.seqlen;
+  if (t >= wa_length(a.lengths, b, a.seqlen)) return;
+  const char *o = la_row(a.o, b, t, h, sizeof(T)), *g = la_row(a.g, b, t, h, sizeof(T));
+  float sum = 0.f;
+  if (la_inside(a.o, o, a.d, sizeof(T)) && la_inside(a.g, g, a.d, sizeof(T)))
+    for (int i = lane; i < a.d; i += 32)
+      sum = fmaf(to_f32(reinterpret_cast<const T*>(o)[i]), to_f32(reinterpret_cast<const T*>(g)[i]), sum);
+#pragma unroll
+  for (int o2 = 16; o2 > 0; o2 /= 2) sum += __shfl_xor_sync(kFullMask, sum, o2);
+  const int64_t at = (b * a.heads + h) * a.seqlen + t;
+  if (lane == 0 && in_range(at, all)) a.delta[at] = sum;
+}
+
+// The sinks' partial gradients added up, N tokens a tile.
+template <typename T, int N>
+__global__ void __launch_bounds__(256) winattn_sinks_kernel(const __grid_constant__ WaArgs a) {
+  const int kv_heads = a.heads / a.share;
+  const int64_t bh = blockIdx.y, b = bh / kv_heads, hk = bh % kv_heads;
+  const int i = blockIdx.x * 256 + threadIdx.x;  // of [sink_tiles, 2, N, d]
+  if (i >= a.sink_tiles * 2 * N * a.d) return;
+  const int tile = i / (2 * N * a.d), rest = i % (2 * N * a.d), j = rest % (N * a.d) / a.d, c = rest % a.d;
+  const int64_t t = (int64_t)tile * N + j;
+  if (t >= wa_length(a.lengths, b, a.seqlen)) return;
+  float sum = 0.f;
+  for (int piece = 0; piece <= a.pieces; ++piece) sum += a.part[wa_part<N>(a, bh, tile, piece) + rest];
+  const int64_t at = ((b * a.seqlen + t) * kv_heads + hk) * a.d + c;
+  if (in_range(at, (int64_t)a.batch * kv_heads * a.seqlen * a.d))
+    static_cast<T*>(rest < N * a.d ? a.dk : a.dv)[at] = wf_round<T>(sum);
+}
+
+}  // namespace ssscan

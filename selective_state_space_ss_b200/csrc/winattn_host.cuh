@@ -1,0 +1,375 @@
+// winattn_host.cuh -- host side of the window attention, its paged cache and the rotation:
+// argument checks, plans and launches
+// (host code of libssscan.so's third translation unit, ss_winattn.cu)
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "ss_winattn.h"
+#include "host_common.cuh"
+#include "rotate.cuh"
+#include "winattn_fma.cuh"
+#include "winattn_step.cuh"
+
+namespace ssscan {
+namespace {
+
+struct WaShape {
+  int64_t batch, seqlen;
+  int heads, kv_heads, d;
+  int dtype;
+  int64_t window, sinks;
+  int share() const { return heads / kv_heads; }
+  int es() const { return dtype == SS_BF16 ? 2 : 4; }
+};
+
+constexpr int64_t kWaMostTokens = INT_MAX - 1024;
+
+ss_status wa_check_shape(const WaShape& s, int most_d) {
+  if (s.batch < 1 || s.seqlen < 1 || s.heads < 1 || s.kv_heads < 1 || s.d < 1) return SS_ERR_INVALID_ARG;
+  if (s.heads % s.kv_heads != 0 || s.seqlen > kWaMostTokens || s.batch > (1 << 24) || s.heads > 65536 ||
+      s.batch * s.heads > (1 << 24))
+    return SS_ERR_INVALID_ARG;
+  if (s.window < 1 || s.sinks < 0) return SS_ERR_INVALID_ARG;
+  if (s.d > most_d) return SS_ERR_UNSUPPORTED;
+  if (s.dtype != SS_F32 && s.dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
+  return SS_OK;
+}
+
+// The same mask in numbers that fit the kernels: with as many sinks as tokens all is seen.
+WaShape wa_normal(WaShape s, int64_t tokens) {
+  if (s.window > tokens || s.sinks >= tokens) s.window = tokens;
+  if (s.window >= tokens) s.sinks = 0;
+  return s;
+}
+
+bool wa_check_heads(const ss_heads* x, int es) { return x && x->data && aligned(x->data, es); }
+
+// batch x seqlen x heads heads of d values, every `share` of the kernel's one of the tensor's.
+LaTensor wa_tensor(const ss_heads& x, int64_t batch, int64_t seqlen, int heads, int d, int share) {
+  LaTensor t{x.data, x.batch_stride, x.token_stride, x.head_stride, share};
+#ifdef SS_BOUNDS_CHECK
+  int64_t hi = d - 1;
+  const int64_t ends[3] = {(batch - 1) * t.sb, (seqlen - 1) * t.st, (heads - 1) * t.sh};
+  for (int64_t e : ends) (e < 0 ? t.lo : hi) += e;
+  t.n = hi - t.lo + 1;
+#endif
+  return t;
+}
+
+template <typename K>
+bool wa_set_smem(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+ss_status wa_launched() { return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA; }
+
+// Blocks of `tile` tokens of every row and head; 0 where they are more than a grid has.
+unsigned wa_grid(int64_t tiles, int64_t bh) { return tiles * bh > INT_MAX ? 0 : (unsigned)(tiles * bh); }
+
+// The keys' gradients of the tiles that hold sinks, cut into pieces (WaQueryTiles): every
+// piece about as long as what a tile meets through its window, but not more than 64 pieces
+// of all of them (their sums take workspace).
+struct WaSplit {
+  int sink_tiles = 0, pieces = 0, piece_tiles = 0;
+};
+WaSplit wa_split(const WaShape& s, int tile) {
+  WaSplit r;
+  const int64_t all = (s.seqlen + tile - 1) / tile, near = (s.window + tile - 2) / tile + 1;
+  if (s.sinks == 0 || all <= 2 * near) return r;
+  const int64_t tiles = (s.sinks + tile - 1) / tile;
+  const int64_t most = 64 / tiles > 1 ? 64 / tiles : 1;
+  int64_t each = near > 8 ? near : 8;
+  if (each * most < all) each = (all + most - 1) / most;
+  r.sink_tiles = (int)(tiles < all ? tiles : all);
+  r.piece_tiles = (int)each;
+  r.pieces = (int)((all + each - 1) / each);
+  return r;
+}
+struct WaBwdWs {
+  size_t delta = 0, part = 0, bytes = 0;
+};
+WaBwdWs wa_bwd_ws(const WaShape& s, const WaSplit& split, int tile) {
+  WaBwdWs w;
+  w.part = align256((size_t)s.batch * s.heads * s.seqlen * 4);
+  const size_t parts = (size_t)s.batch * s.kv_heads * split.sink_tiles * (1 + split.pieces) * 2 * tile * s.d * 4;
+  w.bytes = w.part + (split.pieces > 0 ? align256(parts) : 0);
+  return w;
+}
+
+WaArgs wa_base(const WaShape& s, const ss_heads* q, const ss_heads* k, const ss_heads* v, float scale,
+               const int32_t* lengths) {
+  WaArgs a = {};
+  a.q = wa_tensor(*q, s.batch, s.seqlen, s.heads, s.d, 1);
+  a.k = wa_tensor(*k, s.batch, s.seqlen, s.kv_heads, s.d, s.share());
+  a.v = wa_tensor(*v, s.batch, s.seqlen, s.kv_heads, s.d, s.share());
+  a.lengths = lengths;
+  a.window = s.window;
+  a.sinks = (int)s.sinks;
+  a.seqlen = (int)s.seqlen;
+  a.heads = s.heads;
+  a.share = s.share();
+  a.d = s.d;
+  a.batch = (int)s.batch;
+  a.scale = scale;
+  return a;
+}
+
+template <typename T, int DP>
+ss_status wa_fma_fwd(const WaArgs& a, cudaStream_t stream) {
+  constexpr int kSmem = WfCfg<DP>::kFwd * 4;
+  struct Tag : WfCfg<DP> { T x; };
+  if (once_per_device<Tag>([] { return wa_set_smem(winattn_fma_fwd_kernel<T, DP>, kSmem); }) != 1) return SS_ERR_CUDA;
+  const unsigned grid = wa_grid((a.seqlen + kWfTile - 1) / kWfTile, (int64_t)a.batch * a.heads);
+  winattn_fma_fwd_kernel<T, DP><<<grid, kWfThreads, kSmem, stream>>>(a);
+  return wa_launched();
+}
+
+// The grid of every launch fits (64 tokens the smallest tile of any).
+ss_status wa_check_grid(const WaShape& s) {
+  return wa_grid((s.seqlen + kWfTile - 1) / kWfTile + 128, s.batch * s.heads) ? SS_OK : SS_ERR_INVALID_ARG;
+}
+
+ss_status winattn_fwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads* v, float scale,
+                           const int32_t* lengths, void* o, float* lse, const WaShape& given, cudaStream_t stream) {
+  ss_status st = wa_check_shape(given, 128);
+  if (st == SS_OK) st = wa_check_grid(given);
+  if (st != SS_OK) return st;
+  const int es = given.es();
+  if (!wa_check_heads(q, es) || !wa_check_heads(k, es) || !wa_check_heads(v, es) || !o) return SS_ERR_INVALID_ARG;
+  if (!aligned(o, es) || !aligned(lse, 4) || !aligned(lengths, 4)) return SS_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return SS_ERR_INVALID_ARG;
+  const WaShape s = wa_normal(given, given.seqlen);
+  WaArgs a = wa_base(s, q, k, v, scale, lengths);
+  a.out = o;
+  a.lse = lse;
+  if (s.dtype == SS_BF16)
+    return s.d <= 64 ? wa_fma_fwd<__nv_bfloat16, 64>(a, stream) : wa_fma_fwd<__nv_bfloat16, 128>(a, stream);
+  return s.d <= 64 ? wa_fma_fwd<float, 64>(a, stream) : wa_fma_fwd<float, 128>(a, stream);
+}
+
+template <typename T>
+ss_status wa_delta(const WaArgs& a, cudaStream_t stream) {
+  const int64_t blocks = ((int64_t)a.batch * a.heads * a.seqlen + 7) / 8;
+  winattn_delta_kernel<T><<<(unsigned)blocks, 256, 0, stream>>>(a);
+  return wa_launched();
+}
+
+template <typename T, int N>
+ss_status wa_sinks(const WaArgs& a, cudaStream_t stream) {
+  if (a.pieces == 0) return SS_OK;
+  const int64_t n = (int64_t)a.sink_tiles * 2 * N * a.d;
+  winattn_sinks_kernel<T, N><<<dim3((unsigned)((n + 255) / 256), (unsigned)(a.batch * (a.heads / a.share))), 256, 0, stream>>>(a);
+  return wa_launched();
+}
+
+template <typename T, int DP>
+ss_status wa_fma_bwd(WaArgs a, void* dq, cudaStream_t stream) {
+  using CF = WfCfg<DP>;
+  struct Tag : CF { T x; };
+  if (once_per_device<Tag>([] {
+        return wa_set_smem(winattn_fma_dq_kernel<T, DP>, CF::kDq * 4) &&
+               wa_set_smem(winattn_fma_dkv_kernel<T, DP>, CF::kDkv * 4);
+      }) != 1)
+    return SS_ERR_CUDA;
+  ss_status st = wa_delta<T>(a, stream);
+  if (st != SS_OK) return st;
+  const int64_t tiles = (a.seqlen + kWfTile - 1) / kWfTile;
+  a.out = dq;
+  winattn_fma_dq_kernel<T, DP><<<wa_grid(tiles, (int64_t)a.batch * a.heads), kWfThreads, CF::kDq * 4, stream>>>(a);
+  st = wa_launched();
+  if (st != SS_OK) return st;
+  const unsigned grid = wa_grid(tiles + a.sink_tiles * a.pieces, (int64_t)a.batch * (a.heads / a.share));
+  winattn_fma_dkv_kernel<T, DP><<<grid, kWfThreads, CF::kDkv * 4, stream>>>(a);
+  st = wa_launched();
+  return st != SS_OK ? st : wa_sinks<T, kWfTile>(a, stream);
+}
+
+ss_status wa_check_bwd_shape(const WaShape& s) {
+  const ss_status st = wa_check_shape(s, 128);
+  if (st != SS_OK) return st;
+  if (s.batch * s.kv_heads > 65535) return SS_ERR_INVALID_ARG;  // the sinks' sums have a grid row each
+  if ((s.batch * s.heads * s.seqlen + 7) / 8 > INT_MAX) return SS_ERR_INVALID_ARG;
+  return wa_check_grid(s);
+}
+
+// Tokens of a tile of the backward pass.
+int wa_bwd_tile(const WaShape&) { return kWfTile; }
+
+size_t winattn_bwd_bytes(const WaShape& given) {
+  if (wa_check_bwd_shape(given) != SS_OK) return (size_t)-1;
+  const WaShape s = wa_normal(given, given.seqlen);
+  return wa_bwd_ws(s, wa_split(s, wa_bwd_tile(s)), wa_bwd_tile(s)).bytes;
+}
+
+ss_status winattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads* v, const ss_heads* o,
+                           const float* lse, const ss_heads* g, float scale, const int32_t* lengths, void* dq,
+                           void* dk, void* dv, const WaShape& given, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const ss_status shape = wa_check_bwd_shape(given);
+  if (shape != SS_OK) return shape;
+  const int es = given.es();
+  for (const ss_heads* x : {q, k, v, o, g})
+    if (!wa_check_heads(x, es)) return SS_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)dq, (const void*)dk, (const void*)dv})
+    if (!x || !aligned(x, es)) return SS_ERR_INVALID_ARG;
+  if (!lse || !aligned(lse, 4) || !aligned(lengths, 4)) return SS_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return SS_ERR_INVALID_ARG;
+  const WaShape s = wa_normal(given, given.seqlen);
+  const int tile = wa_bwd_tile(s);
+  const WaSplit split = wa_split(s, tile);
+  const WaBwdWs w = wa_bwd_ws(s, split, tile);
+  if (!ws || ws_bytes < w.bytes || !aligned(ws, 256)) return SS_ERR_INVALID_ARG;
+  WaArgs a = wa_base(s, q, k, v, scale, lengths);
+  a.o = wa_tensor(*o, s.batch, s.seqlen, s.heads, s.d, 1);
+  a.g = wa_tensor(*g, s.batch, s.seqlen, s.heads, s.d, 1);
+  a.lse = const_cast<float*>(lse);
+  a.delta = static_cast<float*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part);
+  a.sink_tiles = split.sink_tiles, a.pieces = split.pieces, a.piece_tiles = split.piece_tiles;
+  a.dk = dk;
+  a.dv = dv;
+  if (s.dtype == SS_BF16)
+    return s.d <= 64 ? wa_fma_bwd<__nv_bfloat16, 64>(a, dq, stream) : wa_fma_bwd<__nv_bfloat16, 128>(a, dq, stream);
+  return s.d <= 64 ? wa_fma_bwd<float, 64>(a, dq, stream) : wa_fma_bwd<float, 128>(a, dq, stream);
+}
+
+// ---- the cache
+
+bool wa_check_pages(const ss_pages* p, int es) {
+  return p && wa_check_heads(&p->k, es) && wa_check_heads(&p->v, es) && p->num_pages >= 1 && p->num_pages <= INT_MAX &&
+         p->page_size >= 1 && p->max_pages >= 1 && (int64_t)p->max_pages * p->page_size <= kWaMostTokens && p->table &&
+         aligned(p->table, 4);
+}
+WaPages wa_pages(const ss_pages& p, int kv_heads, int d) {
+  WaPages r;
+  r.k = wa_tensor(p.k, p.num_pages, p.page_size, kv_heads, d, 1);
+  r.v = wa_tensor(p.v, p.num_pages, p.page_size, kv_heads, d, 1);
+  r.num_pages = p.num_pages;
+  r.table = p.table;
+  r.page_size = p.page_size;
+  r.max_pages = p.max_pages;
+  return r;
+}
+
+template <typename T, int DP>
+ss_status wa_step_fma(const WaStepArgs& a, int parts, cudaStream_t stream) {
+  constexpr int kSmem = WsFmaCfg<DP>::kFloats * 4;
+  struct Tag : WsFmaCfg<DP> { T x; };
+  if (once_per_device<Tag>([] { return wa_set_smem(winattn_step_fma_kernel<T, DP>, kSmem); }) != 1) return SS_ERR_CUDA;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)parts, (unsigned)a.row_tiles, (unsigned)(a.batch * (a.heads / a.share)));
+  c.blockDim = dim3(kWsThreads);
+  c.dynamicSmemBytes = kSmem;
+  c.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)parts, 1, 1};
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, winattn_step_fma_kernel<T, DP>, a) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+ss_status winattn_step_impl(const ss_heads* q, const ss_pages* pages, const int32_t* lengths, float scale, void* o,
+                            const WaShape& given, cudaStream_t stream) {
+  const ss_status shape = wa_check_shape(given, 128);
+  if (shape != SS_OK) return shape;
+  const int es = given.es();
+  if (given.batch * given.kv_heads > 65535 || given.seqlen * given.share() >= (1 << 19)) return SS_ERR_INVALID_ARG;
+  if (!wa_check_heads(q, es) || !wa_check_pages(pages, es) || !lengths || !aligned(lengths, 4) || !o || !aligned(o, es))
+    return SS_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return SS_ERR_INVALID_ARG;
+  const int64_t room = (int64_t)pages->max_pages * pages->page_size;
+  const WaShape s = wa_normal(given, room);
+  WaStepArgs a = {};
+  a.q = wa_tensor(*q, s.batch, s.seqlen, s.heads, s.d, 1);
+  a.pages = wa_pages(*pages, s.kv_heads, s.d);
+  a.lengths = lengths;
+  a.out = o;
+  a.window = s.window;
+  a.sinks = (int)s.sinks;
+  a.tokens = (int)s.seqlen;
+  a.heads = s.heads;
+  a.share = s.share();
+  a.d = s.d;
+  a.batch = (int)s.batch;
+  a.scale = scale;
+  a.row_tiles = (int)((s.seqlen * a.share + kWsRows - 1) / kWsRows);
+  // a walk is cut while blocks are fewer than SMs twice over and its parts have two chunks or more
+  const int64_t seen = s.window + s.sinks + s.seqlen - 1, chunks = ((seen < room ? seen : room) + kWsChunk - 1) / kWsChunk;
+  const int64_t blocks = s.batch * s.kv_heads * a.row_tiles, sms = device_sms() > 0 ? device_sms() : 148;
+  int parts = 1;
+  while (parts < 8 && blocks * parts < 2 * sms && chunks >= 4 * parts) parts *= 2;
+  if (s.dtype == SS_BF16)
+    return s.d <= 64 ? wa_step_fma<__nv_bfloat16, 64>(a, parts, stream) : wa_step_fma<__nv_bfloat16, 128>(a, parts, stream);
+  return s.d <= 64 ? wa_step_fma<float, 64>(a, parts, stream) : wa_step_fma<float, 128>(a, parts, stream);
+}
+
+// ---- the rotation
+
+template <typename T, int VEC>
+ss_status rot_launch(const RotArgs& a, cudaStream_t stream) {
+  const int64_t grid = a.batch * a.blocks;
+  if (grid > INT_MAX) return SS_ERR_INVALID_ARG;
+  rotate_kernel<T, VEC><<<(unsigned)grid, kRotThreads, (size_t)a.block_tokens * a.half * 8, stream>>>(a);
+  return wa_launched();
+}
+
+// 16-byte accesses: data and every stride whole units.
+bool rot_vec(const LaTensor& x, int es) {
+  const int64_t n = 16 / es;
+  return !x.ptr || (aligned(x.ptr, 16) && x.sb % n == 0 && x.st % n == 0 && x.sh % n == 0);
+}
+
+ss_status rotate_impl(const ss_heads* k, const ss_heads* v, const ss_heads* q, const ss_pages* pages,
+                      const int32_t* starts, const int32_t* counts, const ss_rotation* rotation, int inverse,
+                      void* q_out, void* k_out, const WaShape& s, cudaStream_t stream) {
+  const ss_status shape = wa_check_shape(s, 1024);
+  if (shape != SS_OK) return shape;
+  const int es = s.es();
+  if ((q && !wa_check_heads(q, es)) || (k && !wa_check_heads(k, es)) || (v && !wa_check_heads(v, es)))
+    return SS_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (!k && k_out) || (!pages && k && !k_out)) return SS_ERR_INVALID_ARG;
+  if (!aligned(q_out, es) || !aligned(k_out, es) || !aligned(starts, 4) || !aligned(counts, 4)) return SS_ERR_INVALID_ARG;
+  if (!rotation || rotation->half < 0 || rotation->half > s.d / 2) return SS_ERR_INVALID_ARG;
+  if (rotation->half > 0 && (!rotation->inv_freq || !aligned(rotation->inv_freq, 4))) return SS_ERR_INVALID_ARG;
+  if (pages && (!wa_check_pages(pages, es) || !starts || !k || !v)) return SS_ERR_INVALID_ARG;
+  RotArgs a = {};
+  if (q) a.q = wa_tensor(*q, s.batch, s.seqlen, s.heads, s.d, 1);
+  if (k) a.k = wa_tensor(*k, s.batch, s.seqlen, s.kv_heads, s.d, 1);
+  if (v) a.v = wa_tensor(*v, s.batch, s.seqlen, s.kv_heads, s.d, 1);
+  if (pages) a.pages = wa_pages(*pages, s.kv_heads, s.d);
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.starts = starts;
+  a.counts = counts;
+  a.inv_freq = rotation->inv_freq;
+  a.half = rotation->half;
+  a.interleaved = rotation->interleaved != 0;
+  a.inverse = inverse;
+  a.batch = s.batch;
+  a.tokens = (int)s.seqlen;
+  a.heads = q ? s.heads : 0;
+  a.kv_heads = k ? s.kv_heads : 0;
+  a.d = s.d;
+  const int n = 16 / es;
+  const bool vec = s.d % n == 0 && (a.interleaved || a.half % n == 0) && rot_vec(a.q, es) && rot_vec(a.k, es) &&
+                   rot_vec(a.v, es) && aligned(q_out, 16) && aligned(k_out, 16) &&
+                   (!pages || (rot_vec(a.pages.k, es) && rot_vec(a.pages.v, es)));
+  // about 2048 items a block, and at most 32 KB of sines and cosines
+  const int64_t items = (int64_t)(a.heads + a.kv_heads * (v ? 2 : 1)) * ((s.d / (vec ? n : 1) + 1) / 2);
+  int64_t tokens = 2048 / items;
+  tokens = tokens < 1 ? 1 : tokens > 16 ? 16 : tokens;
+  if (tokens * a.half > 4096) tokens = 4096 / a.half;
+  a.block_tokens = (int)(tokens < s.seqlen ? tokens : s.seqlen);
+  a.blocks = (int)((s.seqlen + a.block_tokens - 1) / a.block_tokens);
+  if (items * a.block_tokens > INT_MAX) return SS_ERR_INVALID_ARG;
+  if (es == 2) return vec ? rot_launch<__nv_bfloat16, 8>(a, stream) : rot_launch<__nv_bfloat16, 1>(a, stream);
+  return vec ? rot_launch<float, 4>(a, stream) : rot_launch<float, 1>(a, stream);
+}
+
+}  // namespace
+}  // namespace ssscan
