@@ -20,6 +20,7 @@ struct WaArgs {
   int64_t window;
   int sinks, seqlen, heads, share, d, batch;  // share: heads that read one head of keys
   float scale;
+  int items;           // tensor cores: 256 queries of a head each, shared by the blocks
   // backward
   LaTensor o, g;       // the forward's result and its gradient
   float* delta;        // [batch, heads, seqlen]: do . o
@@ -44,6 +45,7 @@ __device__ __forceinline__ bool wa_sees(int row, int col, int64_t window, int si
 template <int N>
 struct WaKeyTiles {
   int sink, first, count;
+  WaKeyTiles() = default;
   __device__ __forceinline__ WaKeyTiles(int r0, int r1, int64_t window, int sinks) {
     const int64_t from = (int64_t)r0 + 1 - window;
     first = from > 0 ? (int)(from / N) : 0;

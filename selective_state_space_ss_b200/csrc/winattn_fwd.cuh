@@ -1,0 +1,465 @@
+// winattn_fwd.cuh -- the window attention's forward on the tensor cores (bf16, rows of whole
+// 16-byte units).
+//
+// A block takes 256 queries of a head as two tiles of 128, A and B, and walks the tiles of
+// 128 keys that either sees.  For each: S = Q K^T into tensor memory; the tile's warpgroup, a
+// row a thread, takes S from there, applies the mask, and gives the probabilities P back in
+// bf16 in S's place, whence they are an operand of O += P V, whose sum stays in tensor memory
+// too.  While A's softmax is at work the tensor core has B's products, and the other way
+// round.
+//
+// Softmax.  exp(scale (s - m)) as a power of two, one fma and one ex2.  The running maximum m
+// is raised, and O brought down by the factor, only when a row's scores pass it by more than
+// 8 binary orders: in between P is above 1, at most 2^8, which bf16 and fp32 hold as well as
+// what is below 1, and O need not be touched.  The normaliser sums the fp32 values; P itself
+// is rounded to bf16 once, 2^-9 of each term on average, random in sign, next to the output's
+// own rounding.
+//
+// Roles: two warpgroups of softmax, a warp that loads (TMA, 128 x 64 blocks), one that issues
+// products.  S of the next tile is issued behind P V of this one, so that what a warpgroup
+// waits for (its next S) also tells that its last O is complete and may be scaled.  A block
+// stays on its SM and goes on with the next queries while the last O is written out.
+#pragma once
+
+#include <cuda.h>
+
+#include "tc5.cuh"
+#include "waits.cuh"
+#include "winattn_common.cuh"
+
+namespace ssscan {
+
+constexpr int kWtRows = 128;                          // tokens of a tile
+constexpr uint32_t kWtBlock = kWtRows * kTileRow;     // bytes of its 64 columns
+
+struct WaMaps {
+  CUtensorMap q, k, v, g;
+};
+
+// 32 consecutive columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23,"
+      " %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+// Waits for this warp's loads; the values pass through, so that no use of them moves before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23,"
+      " %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Whether any of rows r0 .. r1 - 1 sees any of the columns c0 .. c1 - 1.
+__device__ __forceinline__ bool wa_any_seen(int r0, int r1, int c0, int c1, int64_t window, int sinks) {
+  return r1 > r0 && c0 < r1 && (r0 - (c1 - 1) < window || c0 < sinks);
+}
+
+// Columns of a key tile that are worked on: all, or of the sinks' last tile 32 where they suffice.
+__device__ __forceinline__ int wa_columns(int i, const WaKeyTiles<kWtRows>& keys, int sinks) {
+  return i < keys.sink && sinks - keys.at(i) * kWtRows <= 32 ? 32 : kWtRows;
+}
+template <int N>
+struct WtWidth {
+  static constexpr int value = N;
+};
+
+// One tile of `blocks` x 64 columns by TMA into `to`, completing on `bar`.
+template <int DP>
+__device__ __forceinline__ void wt_load(uint32_t to, const CUtensorMap* map, uint32_t bar, int t0, int h, int b) {
+  la_expect(bar, DP / 64 * kWtBlock);
+#pragma unroll
+  for (int j = 0; j < DP / 64; ++j) tma_load_block(to + j * kWtBlock, map, bar, j * 64, t0, h, b);
+}
+// Rows from `row` on of a tile in shared memory made zero (garbage behind a row's end may be
+// NaN, which zero probabilities do not take out of a product), by a warp.
+template <int DP>
+__device__ __forceinline__ void wt_clear(char* tile, int row, int lane) {
+  for (int i = row * 8 + lane; i < kWtRows * 8; i += 32)
+#pragma unroll
+    for (int j = 0; j < DP / 64; ++j) reinterpret_cast<uint4*>(tile + j * kWtBlock)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <int DP>
+struct WtFwdCfg {
+  static constexpr int kTile = DP / 64 * (int)kWtBlock;
+  static constexpr int kRing = DP == 64 ? 8 : 4;  // places for tiles of K and V in turn
+  static constexpr int kStage = 32 * (int)kTileRow;  // a softmax warp's 32 rows of 64 output columns
+  static constexpr int kQ = 0, kKv = 2 * kTile, kOut = kKv + kRing * kTile, kBars = kOut + 8 * kStage;
+  static constexpr int kNumBars = 2 * kRing + 16;
+  static constexpr int kSmem = kBars + kNumBars * 8 + 16;
+  static constexpr int cS = 0, cO = 2 * kWtRows;  // tensor memory: S (and P) of A and B, then O
+  static constexpr int kThreads = 384;
+  // Registers a thread: 2 x 208 + 88 = 3 x 168 at launch.
+  static constexpr int kSoftmaxRegs = 208, kAuxRegs = 88;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+constexpr int kWtLoadWarp = 8, kWtMmaWarp = 9;
+
+// What a block does at a time: 256 queries of a head, as A (r0 .. mid - 1) and B (mid ..
+// end - 1, maybe none), and the key tiles that any of them sees.
+struct WtItem {
+  int b, h, r0, mid, end, len;
+  WaKeyTiles<kWtRows> keys;
+  __device__ __forceinline__ int from(int x) const { return x ? mid : r0; }
+  __device__ __forceinline__ int to(int x) const { return x ? end : mid; }
+  __device__ __forceinline__ bool needs(int x, int i, const WaArgs& a) const {
+    const int c0 = keys.at(i) * kWtRows;
+    return wa_any_seen(from(x), to(x), c0, c0 + kWtRows, a.window, a.sinks);
+  }
+  // the last of the tiles that A or B needs (there may be a gap between the sinks and the window)
+  __device__ __forceinline__ int last(int x) const {
+    return x ? (end > mid ? keys.count - 1 : -2) : keys.sink + (mid - 1) / kWtRows - keys.first;
+  }
+};
+// Item `n`, long rows first; false where the row has ended before.
+__device__ __forceinline__ bool wt_item(WtItem& w, const WaArgs& a, int n) {
+  const int bh_all = a.batch * a.heads, bh = n % bh_all;
+  w.b = bh / a.heads;
+  w.h = bh - w.b * a.heads;
+  w.r0 = (a.items / bh_all - 1 - n / bh_all) * 2 * kWtRows;
+  w.len = wa_length(a.lengths, w.b, a.seqlen);
+  if (w.r0 >= w.len) return false;
+  w.end = w.len - w.r0 > 2 * kWtRows ? w.r0 + 2 * kWtRows : w.len;
+  w.mid = w.end - w.r0 > kWtRows ? w.r0 + kWtRows : w.end;
+  w.keys = WaKeyTiles<kWtRows>(w.r0, w.end, a.window, a.sinks);
+  return true;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(WtFwdCfg<DP>::kThreads, 1)
+winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMaps maps) {
+  using CF = WtFwdCfg<DP>;
+  extern __shared__ __align__(1024) char smem[];
+  const uint32_t base = smem_u32(smem), bars = base + CF::kBars;
+  const auto bar = [&](int i) { return bars + (uint32_t)i * 8; };
+  const auto full = [&](int i) { return bar(i); };
+  const auto empty = [&](int i) { return bar(CF::kRing + i); };
+  const auto b_q = [&](int x) { return bar(2 * CF::kRing + x); };           // the queries are there
+  const auto b_q_free = [&](int x) { return bar(2 * CF::kRing + 2 + x); };  // and were used
+  const auto b_s = [&](int x) { return bar(2 * CF::kRing + 4 + x); };       // S is there, O has all before
+  const auto b_p = [&](int x, int half) { return bar(2 * CF::kRing + 6 + 2 * x + half); };  // P is there
+  const auto b_o = [&](int x) { return bar(2 * CF::kRing + 10 + x); };      // O is complete
+  const auto b_o_free = [&](int x) { return bar(2 * CF::kRing + 12 + x); }; // and was read
+  const uint32_t b_end = bar(2 * CF::kRing + 14), b_raw = bar(2 * CF::kRing + 15);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + CF::kNumBars * 8);
+  volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
+
+  const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid / 32, 0), lane = tid % 32;
+  if (tid == 0) {
+    for (int i = 0; i < CF::kNumBars; ++i) la_init(bar(i), 1);
+    for (int x = 0; x < 2; ++x) {
+      for (int half = 0; half < 2; ++half) la_init(b_p(x, half), 4);
+      la_init(b_o_free(x), 4);
+    }
+    fence_mbar_init();
+    *dead = 0;
+  }
+  if (warp == kWtMmaWarp) tmem_alloc(tmem_at, 512);
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  const uint32_t tmem = __shfl_sync(kFullMask, *tmem_at, 0);
+  WtItem w;
+
+  if (warp >= kWtLoadWarp) {
+    regs_give<CF::kAuxRegs>();
+    if (warp == kWtLoadWarp) {
+      // ---- loader
+      LaRing<CF::kRing> ring;
+      bool gone = false;  // a place was not free in time: no further copies
+      uint32_t raw = 0, queries[2] = {0, 0};
+      for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+        if (!wt_item(w, a, item)) continue;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (w.to(x) == w.from(x)) continue;
+          if (!gone && queries[x] > 0) gone = !la_wait(b_q_free(x), (queries[x] - 1) & 1, dead);
+          if (gone) continue;
+          if (lane == 0) wt_load<DP>(base + CF::kQ + x * CF::kTile, &maps.q, b_q(x), w.from(x), w.h, w.b);
+          __syncwarp();
+          ++queries[x];
+        }
+        for (int i = 0; i < w.keys.count && !gone; ++i) {
+          const int c0 = w.keys.at(i) * kWtRows;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!gone && ring.used()) gone = !la_wait(empty(ring.i), ring.empty(), dead);
+            if (gone) continue;
+            const uint32_t to = base + CF::kKv + ring.i * CF::kTile;
+            // TMA clips at the tensor's end, not at a row's length
+            const bool ragged = kv && c0 + kWtRows > w.len && w.len < a.seqlen;
+            if (lane == 0)
+              wt_load<DP>(to, kv ? &maps.v : &maps.k, ragged ? b_raw : full(ring.i), c0, w.h / a.share, w.b);
+            __syncwarp();
+            if (ragged) {
+              la_wait_own(b_raw, raw);
+              raw ^= 1;
+              wt_clear<DP>(smem + CF::kKv + ring.i * CF::kTile, w.len - c0, lane);
+              if (lane == 0) la_arrive(full(ring.i));
+            }
+            ring.next();
+          }
+        }
+      }
+      // the last copies land before the end, also where those that they are for have given up
+#pragma unroll 1
+      for (int i = 0; i < CF::kRing; ++i) {
+        const uint32_t fills = ring.turn + (i < ring.i ? 1 : 0);
+        if (fills > 0) la_wait_own(full(i), (fills - 1) & 1);
+      }
+      for (int x = 0; x < 2; ++x)
+        if (queries[x] > 0) la_wait_own(b_q(x), (queries[x] - 1) & 1);
+    } else if (warp == kWtMmaWarp) {
+      // ---- products
+      const bool leader = elect_one();
+      constexpr int kUnits = kWtBlock >> 4;
+      LaRing<CF::kRing> ring;
+      int done[2] = {0, 0}, items[2] = {0, 0};  // tiles of P taken, items begun
+      for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+        if (!wt_item(w, a, item)) continue;
+        int v_at = 0;
+        uint32_t v_full = 0;
+        bool first[2] = {true, true};  // O's first product: it does not add
+        bool asked[2] = {false, false};
+        for (int i = -1; i < w.keys.count; ++i) {
+          int k_at = 0;
+          const bool more = i + 1 < w.keys.count;
+          if (more) {
+            k_at = ring.i;
+            la_wait(full(k_at), ring.full(), dead);
+          }
+          if (i >= 0) la_wait(full(v_at), v_full, dead);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (i >= 0 && w.needs(x, i, a)) {
+              const uint32_t v = tile_desc(base + CF::kKv + v_at * CF::kTile, kWtBlock);
+              const int steps = wa_columns(i, w.keys, a.sinks) / 16;
+              if (first[x] && items[x] > 1) la_wait(b_o_free(x), items[x] & 1, dead);
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                la_wait(b_p(x, half), done[x] & 1, dead);
+                tc5_fence_after();
+                const int to = steps < half * 4 + 4 ? steps : half * 4 + 4;
+                if (leader) {
+#pragma unroll 1
+                  for (int s = half * 4; s < to; ++s)
+                    mma_ts(tmem + CF::cO + x * DP, tmem + CF::cS + x * kWtRows + s * 8, v + s * (16 * kTileRow >> 4),
+                           mma_idesc(128, DP, false, true), !first[x] || s > 0);
+                }
+                __syncwarp();
+              }
+              first[x] = false;
+              ++done[x];
+              if (i == w.last(x)) {
+                if (leader) mma_commit(b_o(x));
+                __syncwarp();
+              }
+            }
+            if (more && w.needs(x, i + 1, a)) {
+              if (!asked[x]) {
+                la_wait(b_q(x), items[x] & 1, dead);
+                asked[x] = true;
+                ++items[x];
+              }
+              tc5_fence_after();
+              if (leader) {
+                const uint32_t q = tile_desc(base + CF::kQ + x * CF::kTile, 0);
+                const uint32_t k = tile_desc(base + CF::kKv + k_at * CF::kTile, 0);
+                const uint32_t idesc = mma_idesc(128, wa_columns(i + 1, w.keys, a.sinks), false, false);
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s) {
+                  const int off = (s / 4) * kUnits + (s % 4) * 2;
+                  mma_ss(tmem + CF::cS + x * kWtRows, q + off, k + off, idesc, s > 0);
+                }
+                mma_commit(b_s(x));
+                if (i + 1 == w.last(x)) mma_commit(b_q_free(x));
+              }
+              __syncwarp();
+            }
+          }
+          if (i >= 0 && leader) mma_commit(empty(v_at));
+          if (more) {
+            if (leader) mma_commit(empty(k_at));
+            ring.next();
+            v_at = ring.i, v_full = ring.full();
+            ring.next();
+          }
+          __syncwarp();
+        }
+      }
+      if (leader) mma_commit(b_end);
+      __syncwarp();
+      la_wait_own(b_end, 0);
+    }
+  } else {
+    // ---- softmax: a row a thread
+    regs_take<CF::kSoftmaxRegs>();
+    const int x = warp / 4, quad = warp % 4;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_at = tmem + lanes + CF::cS + x * kWtRows, o_at = tmem + lanes + CF::cO + x * DP;
+    const float by = a.scale * kLog2e, room = 8.f / by;
+    const int64_t bh_all = (int64_t)a.batch * a.heads;
+    int n = 0, items = 0;  // tiles and items so far
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+      if (!wt_item(w, a, item) || w.to(x) == w.from(x)) continue;
+      const int from = w.from(x), to = w.to(x), row = from + quad * 32 + lane;
+      float top = -CUDART_INF_F, sum = 0.f;
+      bool begun = false;
+      // one tile of 32 CHUNKS columns
+      const auto tile = [&](auto chunks, int c0) {
+        constexpr int CHUNKS = decltype(chunks)::value;
+        la_wait(b_s(x), n & 1, dead);
+        tc5_fence_after();
+        uint32_t s[CHUNKS][32];
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) tmem_ld32(s[c], s_at + 32 * c);
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) tmem_wait_ld(s[c]);
+        if (CHUNKS < 4 || !wa_all_seen(from, to, c0, c0 + kWtRows, a.window, a.sinks)) {
+          // columns of this row: up to `upto`, from `near` on or below `far`, as bits
+          const int upto = row - c0, far = a.sinks - c0;
+          const int64_t first = (int64_t)row - a.window + 1 - c0;
+          const int near = first > 0 ? (int)(first < kWtRows ? first : kWtRows) : 0;
+#pragma unroll
+          for (int c = 0; c < CHUNKS; ++c) {
+            const auto below = [&](int k) { return k <= 32 * c ? 0u : k >= 32 * c + 32 ? ~0u : (1u << (k - 32 * c)) - 1; };
+            const uint32_t seen = below(upto + 1) & (~below(near) | below(far));
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(seen & 1u << j)) s[c][j] = 0xff800000u;  // minus infinity
+          }
+        }
+        float m[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            m[j / 2 % 4] = fmaxf(fmaxf(m[j / 2 % 4], __uint_as_float(s[c][j])), __uint_as_float(s[c][j + 1]));
+        const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        float fade = 1.f;
+        if (most > top + room) fade = ex2_approx((top - most) * by), top = most;  // (from -inf: 0)
+        if (begun && __any_sync(kFullMask, fade != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 16) {
+            uint32_t o[16];
+            tmem_ld(o, o_at + c);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fade);
+            tmem_st16(o_at + c, o);
+          }
+        }
+        begun = true;
+        const float off = top == -CUDART_INF_F ? 0.f : -top * by;  // nothing seen yet: exponents from 0
+        const uint64_t by2 = pair(by, by), off2 = pair(off, off);
+        uint64_t add[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c < CHUNKS) {
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint64_t e = fma2(pair(s[c % CHUNKS][2 * j], s[c % CHUNKS][2 * j + 1]), by2, off2);
+              const float p0 = ex2_approx(pair_lo(e)), p1 = ex2_approx(pair_hi(e));
+              add[j % 2] = add2(add[j % 2], pair(p0, p1));
+              p[j] = to_bf16x2(p0, p1);
+            }
+            tmem_st16(s_at + 16 * c, p);
+          }
+          if (c % 2 == 1) {
+            tmem_wait_st();
+            tc5_fence_before();
+            __syncwarp();
+            if (lane == 0) la_arrive(b_p(x, c / 2));
+          }
+        }
+        const uint64_t both = add2(add[0], add[1]);
+        sum = fmaf(sum, fade, pair_lo(both) + pair_hi(both));
+        ++n;
+      };
+#pragma unroll 1
+      for (int i = 0; i < w.keys.count; ++i) {
+        if (!w.needs(x, i, a)) continue;
+        const int c0 = w.keys.at(i) * kWtRows;
+        if (wa_columns(i, w.keys, a.sinks) <= 32) tile(WtWidth<1>{}, c0);
+        else tile(WtWidth<4>{}, c0);
+      }
+      // O through a place of this warp's own, 64 columns at a time, whole rows at once
+      la_wait(b_o(x), items & 1, dead);
+      ++items;
+      tc5_fence_after();
+      const float inv = 1.f / sum;
+      char* mine = smem + CF::kOut + warp * CF::kStage;
+#pragma unroll
+      for (int half = 0; half < DP / 64; ++half) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o, o_at + half * 64 + c);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint4 y;
+            y.x = to_bf16x2(__uint_as_float(o[8 * u]) * inv, __uint_as_float(o[8 * u + 1]) * inv);
+            y.y = to_bf16x2(__uint_as_float(o[8 * u + 2]) * inv, __uint_as_float(o[8 * u + 3]) * inv);
+            y.z = to_bf16x2(__uint_as_float(o[8 * u + 4]) * inv, __uint_as_float(o[8 * u + 5]) * inv);
+            y.w = to_bf16x2(__uint_as_float(o[8 * u + 6]) * inv, __uint_as_float(o[8 * u + 7]) * inv);
+            *reinterpret_cast<uint4*>(mine + tile_unit(lane, c / 8 + u)) = y;
+          }
+        }
+        if (half == DP / 64 - 1) tc5_fence_before();
+        __syncwarp();
+        if (half == DP / 64 - 1 && lane == 0) la_arrive(b_o_free(x));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = e * 4 + lane / 8, col = half * 64 + lane % 8 * 8, t = from + quad * 32 + r;
+          const int64_t at = (((int64_t)w.b * a.seqlen + t) * a.heads + w.h) * a.d + col;
+          if (t < to && col < a.d && in_range(at, 8, bh_all * a.seqlen * a.d))
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+                *reinterpret_cast<const uint4*>(mine + tile_unit(r, lane % 8));
+        }
+        __syncwarp();
+      }
+      const int64_t l = ((int64_t)w.b * a.heads + w.h) * a.seqlen + row;
+      if (a.lse && row < to && in_range(l, bh_all * a.seqlen)) a.lse[l] = (top * by + log2f(sum)) * kLn2;
+    }
+  }
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  if (warp == kWtMmaWarp) tmem_free(tmem, 512);
+}
+
+}  // namespace ssscan

@@ -10,9 +10,11 @@
 #include <cstdint>
 
 #include "ss_winattn.h"
+#include "heads_host.cuh"
 #include "host_common.cuh"
 #include "rotate.cuh"
 #include "winattn_fma.cuh"
+#include "winattn_fwd.cuh"
 #include "winattn_step.cuh"
 
 namespace ssscan {
@@ -129,6 +131,22 @@ ss_status wa_fma_fwd(const WaArgs& a, cudaStream_t stream) {
   return wa_launched();
 }
 
+// bf16 rows of whole 16-byte units whose maps TMA takes.
+bool wa_map(CUtensorMap* m, const LaTensor& x, const WaShape& s) {
+  return la_vec(x, s.d, 2) && la_map(m, x, s.batch, s.seqlen, s.heads / x.share, s.d, kWtRows);
+}
+
+template <int DP>
+ss_status wa_tc_fwd(WaArgs a, const WaMaps& maps, cudaStream_t stream) {
+  using CF = WtFwdCfg<DP>;
+  struct Tag : CF {};
+  if (once_per_device<Tag>([] { return wa_set_smem(winattn_fwd_kernel<DP>, CF::kSmem); }) != 1) return SS_ERR_CUDA;
+  a.items = (int)wa_grid((a.seqlen + 2 * kWtRows - 1) / (2 * kWtRows), (int64_t)a.batch * a.heads);
+  const int sms = device_sms() > 0 ? device_sms() : 148, grid = a.items < sms ? a.items : sms;
+  winattn_fwd_kernel<DP><<<grid, CF::kThreads, CF::kSmem, stream>>>(a, maps);
+  return wa_launched();
+}
+
 // The grid of every launch fits (64 tokens the smallest tile of any).
 ss_status wa_check_grid(const WaShape& s) {
   return wa_grid((s.seqlen + kWfTile - 1) / kWfTile + 128, s.batch * s.heads) ? SS_OK : SS_ERR_INVALID_ARG;
@@ -147,6 +165,9 @@ ss_status winattn_fwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   WaArgs a = wa_base(s, q, k, v, scale, lengths);
   a.out = o;
   a.lse = lse;
+  WaMaps maps;
+  if (s.dtype == SS_BF16 && aligned(o, 16) && wa_map(&maps.q, a.q, s) && wa_map(&maps.k, a.k, s) && wa_map(&maps.v, a.v, s))
+    return s.d <= 64 ? wa_tc_fwd<64>(a, maps, stream) : wa_tc_fwd<128>(a, maps, stream);
   if (s.dtype == SS_BF16)
     return s.d <= 64 ? wa_fma_fwd<__nv_bfloat16, 64>(a, stream) : wa_fma_fwd<__nv_bfloat16, 128>(a, stream);
   return s.d <= 64 ? wa_fma_fwd<float, 64>(a, stream) : wa_fma_fwd<float, 128>(a, stream);
