@@ -15,8 +15,9 @@
 // is rounded to bf16 once, 2^-9 of each term on average, random in sign, next to the output's
 // own rounding.
 //
-// Roles: two warpgroups of softmax, a warp that loads (TMA, 128 x 64 blocks), one that issues
-// products.  S of the next tile is issued behind P V of this one, so that what a warpgroup
+// Roles: two warpgroups of softmax, a warp that loads (TMA, 128 x 64 blocks), one each that
+// issues A's and B's products (one warp for both was busy waiting for one of them while the
+// other's were due: 4200 cycles a pair of tiles).  S of the next tile is issued behind P V of this one, so that what a warpgroup
 // waits for (its next S) also tells that its last O is complete and may be scaled.  A block
 // stays on its SM and goes on with the next queries while the last O is written out.
 #pragma once
@@ -149,7 +150,7 @@ __device__ __forceinline__ bool wt_item(WtItem& w, const WaArgs& a, int n) {
   w.b = bh / a.heads;
   w.h = bh - w.b * a.heads;
   w.r0 = (a.items / bh_all - 1 - n / bh_all) * 2 * kWtRows;
-  w.len = wa_length(a.lengths, w.b, a.seqlen);
+  w.len = __shfl_sync(kFullMask, wa_length(a.lengths, w.b, a.seqlen), 0);  // known as one value for a warp
   if (w.r0 >= w.len) return false;
   w.end = w.len - w.r0 > 2 * kWtRows ? w.r0 + 2 * kWtRows : w.len;
   w.mid = w.end - w.r0 > kWtRows ? w.r0 + kWtRows : w.end;
@@ -183,6 +184,8 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
       for (int half = 0; half < 2; ++half) la_init(b_p(x, half), 4);
       la_init(b_o_free(x), 4);
     }
+    for (int i = 0; i < CF::kRing; ++i) la_init(empty(i), 2);
+    la_init(b_end, 2);
     fence_mbar_init();
     *dead = 0;
   }
@@ -241,61 +244,56 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
       }
       for (int x = 0; x < 2; ++x)
         if (queries[x] > 0) la_wait_own(b_q(x), (queries[x] - 1) & 1);
-    } else if (warp == kWtMmaWarp) {
-      // ---- products
+    } else if (warp <= kWtMmaWarp + 1) {
+      // ---- products, a warp for A and one for B
+      const int x = warp - kWtMmaWarp;
       const bool leader = elect_one();
       constexpr int kUnits = kWtBlock >> 4;
+      const uint32_t q = tile_desc(base + CF::kQ + x * CF::kTile, 0);
       LaRing<CF::kRing> ring;
-      int done[2] = {0, 0}, items[2] = {0, 0};  // tiles of P taken, items begun
+      int done = 0, items = 0;  // tiles of P taken, items so far
       for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
         if (!wt_item(w, a, item)) continue;
+        const bool mine = w.to(x) > w.from(x);
+        if (mine) la_wait(b_q(x), items & 1, dead);
         int v_at = 0;
         uint32_t v_full = 0;
-        bool first[2] = {true, true};  // O's first product: it does not add
-        bool asked[2] = {false, false};
+        bool add = false;  // O's first product does not
         for (int i = -1; i < w.keys.count; ++i) {
-          int k_at = 0;
           const bool more = i + 1 < w.keys.count;
-          if (more) {
-            k_at = ring.i;
-            la_wait(full(k_at), ring.full(), dead);
-          }
-          if (i >= 0) la_wait(full(v_at), v_full, dead);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (i >= 0 && w.needs(x, i, a)) {
+          const int k_at = ring.i;
+          const uint32_t k_full = ring.full();
+          if (more) la_wait(full(k_at), k_full, dead);
+          if (i >= 0) {
+            la_wait(full(v_at), v_full, dead);
+            if (w.needs(x, i, a)) {
               const uint32_t v = tile_desc(base + CF::kKv + v_at * CF::kTile, kWtBlock);
               const int steps = wa_columns(i, w.keys, a.sinks) / 16;
-              if (first[x] && items[x] > 1) la_wait(b_o_free(x), items[x] & 1, dead);
-#pragma unroll 1
+              if (!add && items > 0) la_wait(b_o_free(x), (items - 1) & 1, dead);
+#pragma unroll
               for (int half = 0; half < 2; ++half) {
-                la_wait(b_p(x, half), done[x] & 1, dead);
+                la_wait(b_p(x, half), done & 1, dead);
                 tc5_fence_after();
-                const int to = steps < half * 4 + 4 ? steps : half * 4 + 4;
                 if (leader) {
-#pragma unroll 1
-                  for (int s = half * 4; s < to; ++s)
-                    mma_ts(tmem + CF::cO + x * DP, tmem + CF::cS + x * kWtRows + s * 8, v + s * (16 * kTileRow >> 4),
-                           mma_idesc(128, DP, false, true), !first[x] || s > 0);
+#pragma unroll
+                  for (int s = half * 4; s < half * 4 + 4; ++s)
+                    if (s < steps)
+                      mma_ts(tmem + CF::cO + x * DP, tmem + CF::cS + x * kWtRows + s * 8, v + s * (16 * kTileRow >> 4),
+                             mma_idesc(128, DP, false, true), add || s > 0);
                 }
                 __syncwarp();
               }
-              first[x] = false;
-              ++done[x];
-              if (i == w.last(x)) {
-                if (leader) mma_commit(b_o(x));
-                __syncwarp();
-              }
+              add = true;
+              ++done;
+              if (leader && i == w.last(x)) mma_commit(b_o(x));
             }
-            if (more && w.needs(x, i + 1, a)) {
-              if (!asked[x]) {
-                la_wait(b_q(x), items[x] & 1, dead);
-                asked[x] = true;
-                ++items[x];
-              }
-              tc5_fence_after();
-              if (leader) {
-                const uint32_t q = tile_desc(base + CF::kQ + x * CF::kTile, 0);
+            if (leader) mma_commit(empty(v_at));
+            __syncwarp();
+          }
+          if (more) {
+            tc5_fence_after();
+            if (leader) {
+              if (w.needs(x, i + 1, a)) {
                 const uint32_t k = tile_desc(base + CF::kKv + k_at * CF::kTile, 0);
                 const uint32_t idesc = mma_idesc(128, wa_columns(i + 1, w.keys, a.sinks), false, false);
 #pragma unroll
@@ -306,18 +304,15 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
                 mma_commit(b_s(x));
                 if (i + 1 == w.last(x)) mma_commit(b_q_free(x));
               }
-              __syncwarp();
+              mma_commit(empty(k_at));
             }
-          }
-          if (i >= 0 && leader) mma_commit(empty(v_at));
-          if (more) {
-            if (leader) mma_commit(empty(k_at));
+            __syncwarp();
             ring.next();
             v_at = ring.i, v_full = ring.full();
             ring.next();
           }
-          __syncwarp();
         }
+        if (mine) ++items;
       }
       if (leader) mma_commit(b_end);
       __syncwarp();
@@ -332,8 +327,15 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
     const float by = a.scale * kLog2e, room = 8.f / by;
     const int64_t bh_all = (int64_t)a.batch * a.heads;
     int n = 0, items = 0;  // tiles and items so far
+    // A and B take turns at their exponentials, for every tile of either: left alone they
+    // fall into step, and the tensor core waits while both are at it and works while both wait.
+    const auto turn = [](int x, bool begin) {
+      if (begin) asm volatile("bar.sync %0, 256;\n" ::"r"(1 + x) : "memory");
+      else asm volatile("bar.arrive %0, 256;\n" ::"r"(2 - x) : "memory");
+    };
+    if (x == 1) turn(1, false);  // A begins
     for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
-      if (!wt_item(w, a, item) || w.to(x) == w.from(x)) continue;
+      if (!wt_item(w, a, item)) continue;
       const int from = w.from(x), to = w.to(x), row = from + quad * 32 + lane;
       float top = -CUDART_INF_F, sum = 0.f;
       bool begun = false;
@@ -382,6 +384,7 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
           }
         }
         begun = true;
+        turn(x, true);
         const float off = top == -CUDART_INF_F ? 0.f : -top * by;  // nothing seen yet: exponents from 0
         const uint64_t by2 = pair(by, by), off2 = pair(off, off);
         uint64_t add[2] = {0, 0};
@@ -405,17 +408,23 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
             if (lane == 0) la_arrive(b_p(x, c / 2));
           }
         }
+        turn(x, false);
         const uint64_t both = add2(add[0], add[1]);
         sum = fmaf(sum, fade, pair_lo(both) + pair_hi(both));
         ++n;
       };
 #pragma unroll 1
       for (int i = 0; i < w.keys.count; ++i) {
-        if (!w.needs(x, i, a)) continue;
+        if (!w.needs(x, i, a)) {
+          turn(x, true);
+          turn(x, false);
+          continue;
+        }
         const int c0 = w.keys.at(i) * kWtRows;
         if (wa_columns(i, w.keys, a.sinks) <= 32) tile(WtWidth<1>{}, c0);
         else tile(WtWidth<4>{}, c0);
       }
+      if (to == from) continue;
       // O through a place of this warp's own, 64 columns at a time, whole rows at once
       la_wait(b_o(x), items & 1, dead);
       ++items;
@@ -455,6 +464,7 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
       const int64_t l = ((int64_t)w.b * a.heads + w.h) * a.seqlen + row;
       if (a.lse && row < to && in_range(l, bh_all * a.seqlen)) a.lse[l] = (top * by + log2f(sum)) * kLn2;
     }
+    if (x == 0) turn(0, true);  // B's last
   }
   tc5_fence_before();
   __syncthreads();
