@@ -1,0 +1,649 @@
+// winattn_bwd.cuh -- the window attention's gradients on the tensor cores (bf16, rows of
+// whole 16-byte units).
+//
+// With P = exp(scale S - lse) from the saved normaliser and dS = P . (dO V^T - delta), delta =
+// do . o of each query:
+//
+//   dV = P^T dO,    dK = scale dS^T Q,    dQ = scale dS K.
+//
+// Two kernels, each working out S = Q K^T and dO V^T of its own: one whose blocks stay at 128
+// keys and walk the queries that see them (dK, dV), one whose blocks stay at 128 queries and
+// walk their keys (dQ).  A sum is then held in tensor memory from its first term to its last,
+// in a fixed order; one kernel for all three would make seven products into five, but would
+// add dQ up in memory, in whatever order the blocks come.  P and dS are rounded to bf16 once,
+// as operands (from tensor memory) of the next product.
+//
+// In the first kernel everything is transposed, keys in the lanes, so that P^T and dS^T are
+// operands as they come.  The softmax's warps turn S of one tile into P while the tensor core
+// has dK and dP of the tiles before and behind, and dP into dS while it has dV and the next
+// S.
+#pragma once
+
+#include "winattn_fma.cuh"
+#include "winattn_fwd.cuh"
+
+namespace ssscan {
+
+// 64 columns of 32 rows from tensor memory, times `by`, as bf16 through a warp's place in
+// shared memory to whole rows: row r is token t0 + r, written where that is below `end`
+// (`out` has `left` elements).
+template <int COLS>
+__device__ __forceinline__ void wt_put_rows(char* place, uint32_t tmem_from, __nv_bfloat16* out, int64_t left,
+                                            int64_t row_stride, int t0, int end, int col0, int d, float by, int lane) {
+#pragma unroll
+  for (int c = 0; c < COLS; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(o, tmem_from + c);
+    tmem_wait_ld(o);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint4 y;
+      y.x = to_bf16x2(__uint_as_float(o[8 * u]) * by, __uint_as_float(o[8 * u + 1]) * by);
+      y.y = to_bf16x2(__uint_as_float(o[8 * u + 2]) * by, __uint_as_float(o[8 * u + 3]) * by);
+      y.z = to_bf16x2(__uint_as_float(o[8 * u + 4]) * by, __uint_as_float(o[8 * u + 5]) * by);
+      y.w = to_bf16x2(__uint_as_float(o[8 * u + 6]) * by, __uint_as_float(o[8 * u + 7]) * by);
+      *reinterpret_cast<uint4*>(place + tile_unit(lane, c / 8 + u)) = y;
+    }
+  }
+  __syncwarp();
+  constexpr int UNITS = COLS / 8, ROWS = 32 / UNITS;
+#pragma unroll
+  for (int e = 0; e < 32 / ROWS; ++e) {
+    const int r = e * ROWS + lane / UNITS, col = col0 + lane % UNITS * 8;
+    if (t0 + r < end && col < d && in_range((int64_t)(t0 + r) * row_stride + col, 8, left))
+      *reinterpret_cast<uint4*>(out + (int64_t)(t0 + r) * row_stride + col) =
+          *reinterpret_cast<const uint4*>(place + tile_unit(r, lane % UNITS));
+  }
+  __syncwarp();
+}
+
+// Bits from `lo` on below `hi` of the columns c .. c + 31.
+__device__ __forceinline__ uint32_t wt_bits(int lo, int hi, int c) {
+  const auto below = [&](int k) { return k <= c ? 0u : k >= c + 32 ? ~0u : (1u << (k - c)) - 1; };
+  return below(hi) & ~below(lo);
+}
+
+// ---- dK and dV
+
+template <int DP>
+struct WtKvCfg {
+  static constexpr int kTile = DP / 64 * (int)kWtBlock;
+  static constexpr int kRing = DP == 64 ? 3 : 2;  // places for queries, and as many for do
+  static constexpr int kK = 0, kV = kTile, kQ = 2 * kTile, kG = kQ + kRing * kTile, kStat = kG + kRing * kTile;
+  static constexpr int kStatBytes = 2 * kWtRows * 4;  // lse and delta of a tile's queries
+  static constexpr int kBars = kStat + 2 * kStatBytes;
+  static constexpr int kNumBars = 4 * kRing + 12;
+  static constexpr int kSmem = kBars + kNumBars * 8 + 16;
+  static constexpr int cS = 0, cP = 128, cDv = 256, cDk = 256 + DP;
+  static constexpr int kThreads = 384;
+  static_assert(kSmem <= 232448 && 2 * kRing * kTile >= 8 * 32 * (int)kTileRow, "shared memory");
+};
+constexpr int kWtStatWarp = 10;
+
+template <int DP>
+__global__ void __launch_bounds__(WtKvCfg<DP>::kThreads, 1)
+winattn_dkv_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMaps maps) {
+  using CF = WtKvCfg<DP>;
+  extern __shared__ __align__(1024) char smem[];
+  const uint32_t base = smem_u32(smem), bars = base + CF::kBars;
+  const auto bar = [&](int i) { return bars + (uint32_t)i * 8; };
+  const auto full_q = [&](int i) { return bar(i); };
+  const auto empty_q = [&](int i) { return bar(CF::kRing + i); };
+  const auto full_g = [&](int i) { return bar(2 * CF::kRing + i); };
+  const auto empty_g = [&](int i) { return bar(3 * CF::kRing + i); };
+  const auto full_st = [&](int i) { return bar(4 * CF::kRing + i); };
+  const auto empty_st = [&](int i) { return bar(4 * CF::kRing + 2 + i); };
+  const uint32_t b_kv = bar(4 * CF::kRing + 4), b_s = bar(4 * CF::kRing + 5), b_p = bar(4 * CF::kRing + 6),
+                 b_dp = bar(4 * CF::kRing + 7), b_ds = bar(4 * CF::kRing + 8), b_end = bar(4 * CF::kRing + 9),
+                 b_raw = bar(4 * CF::kRing + 10);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + CF::kNumBars * 8);
+  volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
+
+  const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid / 32, 0), lane = tid % 32;
+  const int kv_heads = a.heads / a.share, bh_all = a.batch * kv_heads;
+  const int bh = blockIdx.x % bh_all, b = bh / kv_heads, hk = bh - b * kv_heads;
+  const int len = __shfl_sync(kFullMask, wa_length(a.lengths, b, a.seqlen), 0);
+  const WaKeyBlock<kWtRows> w(a, blockIdx.x / bh_all, len);
+  const int c0 = w.tile * kWtRows;
+  if (c0 >= len) return;
+  const int per = w.to > w.from ? w.to - w.from : 0, count = per * a.share;  // tiles of queries, head by head
+  const auto head = [&](int i) { return hk * a.share + i / per; };
+  const auto rows = [&](int i) { return (w.from + i % per) * kWtRows; };
+
+  if (tid == 0) {
+    for (int i = 0; i < CF::kNumBars; ++i) la_init(bar(i), 1);
+    for (int i = 0; i < 2; ++i) la_init(empty_st(i), 8);
+    la_init(b_p, 8);
+    la_init(b_ds, 8);
+    fence_mbar_init();
+    *dead = 0;
+  }
+  if (warp == kWtMmaWarp) tmem_alloc(tmem_at, 512);
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  const uint32_t tmem = __shfl_sync(kFullMask, *tmem_at, 0);
+
+  if (warp == kWtLoadWarp) {
+    // ---- loader
+    if (lane == 0 && count > 0) {
+      la_expect(b_kv, 2 * CF::kTile);
+#pragma unroll
+      for (int j = 0; j < DP / 64; ++j) {
+        tma_load_block(base + CF::kK + j * kWtBlock, &maps.k, b_kv, j * 64, c0, hk, b);
+        tma_load_block(base + CF::kV + j * kWtBlock, &maps.v, b_kv, j * 64, c0, hk, b);
+      }
+    }
+    LaRing<CF::kRing> ring;
+    bool gone = false;  // a place was not free in time: no further copies
+    bool odd = false;   // (and the queries of the last place came without their do)
+    uint32_t raw = 0;
+    for (int i = 0; i < count && !gone; ++i) {
+      const int r0 = rows(i), h = head(i);
+      // TMA clips at the tensor's end, not at a row's length
+      const bool ragged = r0 + kWtRows > len && len < a.seqlen;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (!gone && ring.used()) gone = !la_wait(g ? empty_g(ring.i) : empty_q(ring.i), ring.empty(), dead);
+        if (gone) continue;
+        const int at = (g ? CF::kG : CF::kQ) + ring.i * CF::kTile;
+        const uint32_t full = g ? full_g(ring.i) : full_q(ring.i);
+        if (lane == 0) wt_load<DP>(base + at, g ? &maps.g : &maps.q, ragged ? b_raw : full, r0, h, b);
+        __syncwarp();
+        if (ragged) {
+          la_wait_own(b_raw, raw);
+          raw ^= 1;
+          wt_clear<DP>(smem + at, len - r0, lane);
+          if (lane == 0) la_arrive(full);
+        }
+        odd = g == 0;
+      }
+      if (!gone) ring.next();
+    }
+    // the last copies land before the end, also where those that they are for have given up
+#pragma unroll 1
+    for (int i = 0; i < CF::kRing; ++i) {
+      const uint32_t fills = ring.turn + (i < ring.i ? 1 : 0);
+      if (fills > 0) la_wait_own(full_q(i), (fills - 1) & 1), la_wait_own(full_g(i), (fills - 1) & 1);
+    }
+    if (odd) la_wait_own(full_q(ring.i), ring.full());
+    if (count > 0) la_wait_own(b_kv, 0);
+  } else if (warp == kWtMmaWarp) {
+    // ---- products
+    const bool leader = elect_one();
+    constexpr int kUnits = kWtBlock >> 4;
+    const uint32_t k = tile_desc(base + CF::kK, 0), v = tile_desc(base + CF::kV, 0);
+    constexpr uint32_t kScores = mma_idesc(128, kWtRows, false, false), kSums = mma_idesc(128, DP, false, true);
+    LaRing<CF::kRing> ring;
+    // S^T = K Q^T or dP^T = V dO^T
+    const auto scores = [&](uint32_t to, uint32_t x, int at) {
+      const uint32_t y = tile_desc(base + at, 0);
+#pragma unroll
+      for (int s = 0; s < DP / 16; ++s) {
+        const int off = (s / 4) * kUnits + (s % 4) * 2;
+        mma_ss(tmem + to, x + off, y + off, kScores, s > 0);
+      }
+    };
+    // dV += P^T dO or dK += dS^T Q: the operand's two halves lie 64 columns apart
+    const auto sums = [&](uint32_t to, uint32_t x, int at, bool add) {
+      const uint32_t y = tile_desc(base + at, kWtBlock);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        mma_ts(tmem + to, tmem + x + (s / 4) * 64 + (s % 4) * 8, y + s * (16 * kTileRow >> 4), kSums, add || s > 0);
+    };
+    if (count > 0) {
+      la_wait(b_kv, 0, dead);
+      la_wait(full_q(0), 0, dead);
+      if (leader) scores(CF::cS, k, CF::kQ), mma_commit(b_s);
+      __syncwarp();
+      la_wait(full_g(0), 0, dead);
+      if (leader) scores(CF::cP, v, CF::kG), mma_commit(b_dp);
+      __syncwarp();
+    }
+    for (int i = 0; i < count; ++i) {
+      const bool more = i + 1 < count;
+      const int at = ring.i;
+      ring.next();
+      if (more) la_wait(full_q(ring.i), ring.full(), dead);
+      la_wait(b_p, i & 1, dead);
+      tc5_fence_after();
+      if (leader) {
+        sums(CF::cDv, CF::cS, CF::kG + at * CF::kTile, i > 0);
+        mma_commit(empty_g(at));
+        if (more) scores(CF::cS, k, CF::kQ + ring.i * CF::kTile), mma_commit(b_s);
+      }
+      __syncwarp();
+      if (more) la_wait(full_g(ring.i), ring.full(), dead);
+      la_wait(b_ds, i & 1, dead);
+      tc5_fence_after();
+      if (leader) {
+        sums(CF::cDk, CF::cP, CF::kQ + at * CF::kTile, i > 0);
+        mma_commit(empty_q(at));
+        if (more) scores(CF::cP, v, CF::kG + ring.i * CF::kTile), mma_commit(b_dp);
+      }
+      __syncwarp();
+    }
+    if (leader) mma_commit(b_end);
+    __syncwarp();
+    la_wait_own(b_end, 0);
+  } else if (warp == kWtStatWarp) {
+    // ---- the queries' normalisers (base 2) and deltas
+    for (int i = 0; i < count; ++i) {
+      if (i >= 2) la_wait(empty_st(i % 2), (i / 2 - 1) & 1, dead);
+      float* st = reinterpret_cast<float*>(smem + CF::kStat + (i % 2) * CF::kStatBytes);
+      const int64_t row = ((int64_t)b * a.heads + head(i)) * a.seqlen;
+      const int r0 = rows(i);
+#pragma unroll
+      for (int j = lane; j < kWtRows; j += 32) {
+        const bool real = r0 + j < len && in_range(row + r0 + j, (int64_t)a.batch * a.heads * a.seqlen);
+        st[j] = real ? -a.lse[row + r0 + j] * kLog2e : 0.f;
+        st[kWtRows + j] = real ? -a.delta[row + r0 + j] : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) la_arrive(full_st(i % 2));
+    }
+  } else if (warp < kWtLoadWarp) {
+    // ---- P and dS: a key a thread, the two warpgroups 64 queries each
+    const int side = warp / 4, quad = warp % 4, key = c0 + quad * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_at = tmem + lanes + CF::cS + side * 64, p_at = tmem + lanes + CF::cP + side * 64;
+    const float by = a.scale * kLog2e;
+    const uint64_t by2 = pair(by, by);
+    // the queries that see this key
+    const int64_t behind = key < a.sinks ? (int64_t)len : key + a.window;
+    const int upto = (int)(behind < len ? behind : len);
+    for (int i = 0; i < count; ++i) {
+      const int r0 = rows(i);
+      const float* st = reinterpret_cast<const float*>(smem + CF::kStat + (i % 2) * CF::kStatBytes) + side * 64;
+      la_wait(full_st(i % 2), (i / 2) & 1, dead);
+      la_wait(b_s, i & 1, dead);
+      tc5_fence_after();
+      uint32_t s[2][32];
+      tmem_ld32(s[0], s_at);
+      tmem_ld32(s[1], s_at + 32);
+      tmem_wait_ld(s[0]);
+      tmem_wait_ld(s[1]);
+      const bool all = r0 + kWtRows <= len && wa_all_seen(r0, r0 + kWtRows, c0, c0 + kWtRows, a.window, a.sinks);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const ulonglong2 lse = *reinterpret_cast<const ulonglong2*>(st + 32 * c + 2 * j);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t z = fma2(pair(s[c][2 * (j + e)], s[c][2 * (j + e) + 1]), by2, e ? lse.y : lse.x);
+            s[c][2 * (j + e)] = __float_as_uint(ex2_approx(pair_lo(z)));
+            s[c][2 * (j + e) + 1] = __float_as_uint(ex2_approx(pair_hi(z)));
+          }
+        }
+        if (!all) {
+          const uint32_t seen = wt_bits(key - r0, upto - r0, side * 64 + 32 * c);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!(seen & 1u << j)) s[c][j] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) p[j] = to_bf16x2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1]));
+        tmem_st16(s_at + 16 * c, p);
+      }
+      tmem_wait_st();
+      tc5_fence_before();
+      __syncwarp();
+      if (lane == 0) la_arrive(b_p);
+      la_wait(b_dp, i & 1, dead);
+      tc5_fence_after();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t dp[32], ds[16];
+        tmem_ld32(dp, p_at + 32 * c);
+        tmem_wait_ld(dp);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const ulonglong2 delta = *reinterpret_cast<const ulonglong2*>(st + kWtRows + 32 * c + 2 * j);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int k = 2 * (j + e);
+            const uint64_t z = mul2(pair(s[c][k], s[c][k + 1]), add2(pair(dp[k], dp[k + 1]), e ? delta.y : delta.x));
+            ds[j + e] = to_bf16x2(pair_lo(z), pair_hi(z));
+          }
+        }
+        tmem_st16(p_at + 16 * c, ds);
+      }
+      tmem_wait_st();
+      tc5_fence_before();
+      __syncwarp();
+      if (lane == 0) la_arrive(b_ds), la_arrive(empty_st(i % 2));
+    }
+    // one warpgroup writes dV, the other dK, through the places of the queries
+    if (count > 0) la_wait(b_end, 0, dead);
+    tc5_fence_after();
+    const uint32_t from = tmem + lanes + (side ? CF::cDk : CF::cDv);
+    const float scale = side ? a.scale : 1.f;
+    if (w.partial) {
+      float* to = a.part + wa_part<kWtRows>(a, bh, w.tile, w.piece) + (side ? 0 : kWtRows * a.d) + (int64_t)(key - c0) * a.d;
+#pragma unroll 1
+      for (int c = 0; c < DP; c += 16) {
+        uint32_t o[16] = {};
+        if (count > 0) {
+          tmem_ld(o, from + c);
+          tmem_wait_ld(o);
+        }
+        if (key < len)
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            if (c + j < a.d)
+              *reinterpret_cast<float4*>(to + c + j) =
+                  make_float4(__uint_as_float(o[j]) * scale, __uint_as_float(o[j + 1]) * scale,
+                              __uint_as_float(o[j + 2]) * scale, __uint_as_float(o[j + 3]) * scale);
+      }
+    } else {
+      const int64_t at = ((int64_t)b * a.seqlen * kv_heads + hk) * a.d;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(side ? a.dk : a.dv) + at;
+#pragma unroll
+      for (int c = 0; c < DP; c += 64)
+        wt_put_rows<64>(smem + CF::kQ + warp * 32 * kTileRow, from + c, out, (int64_t)bh_all * a.seqlen * a.d - at,
+                        (int64_t)kv_heads * a.d, key - lane, len, c, a.d, scale, lane);
+    }
+  }
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  if (warp == kWtMmaWarp) tmem_free(tmem, 512);
+}
+
+// ---- dQ
+
+template <int DP>
+struct WtDqCfg {
+  static constexpr int kTile = DP / 64 * (int)kWtBlock;
+  static constexpr int kRing = DP == 64 ? 4 : 2;  // places for keys, and as many for values
+  static constexpr int kQ = 0, kG = kTile, kK = 2 * kTile, kV = kK + kRing * kTile, kOut = kV + kRing * kTile;
+  static constexpr int kStage = 32 * (int)kTileRow;
+  static constexpr int kBars = kOut + 8 * kStage;
+  static constexpr int kNumBars = 4 * kRing + 10;
+  static constexpr int kSmem = kBars + kNumBars * 8 + 16;
+  static constexpr int cS = 0, cP = 256, cDq = 384;  // S in two places
+  static constexpr int kThreads = 384;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+// 128 queries of a head at a time, item `n`, long rows first; false where the row has ended before.
+struct WtRowItem {
+  int b, h, r0, end, len;
+  WaKeyTiles<kWtRows> keys;
+};
+__device__ __forceinline__ bool wt_row_item(WtRowItem& w, const WaArgs& a, int n) {
+  const int bh_all = a.batch * a.heads, bh = n % bh_all;
+  w.b = bh / a.heads;
+  w.h = bh - w.b * a.heads;
+  w.r0 = (a.items / bh_all - 1 - n / bh_all) * kWtRows;
+  w.len = __shfl_sync(kFullMask, wa_length(a.lengths, w.b, a.seqlen), 0);
+  if (w.r0 >= w.len) return false;
+  w.end = w.len - w.r0 > kWtRows ? w.r0 + kWtRows : w.len;
+  w.keys = WaKeyTiles<kWtRows>(w.r0, w.end, a.window, a.sinks);
+  return true;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(WtDqCfg<DP>::kThreads, 1)
+winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMaps maps) {
+  using CF = WtDqCfg<DP>;
+  extern __shared__ __align__(1024) char smem[];
+  const uint32_t base = smem_u32(smem), bars = base + CF::kBars;
+  const auto bar = [&](int i) { return bars + (uint32_t)i * 8; };
+  const auto full_k = [&](int i) { return bar(i); };
+  const auto empty_k = [&](int i) { return bar(CF::kRing + i); };
+  const auto full_v = [&](int i) { return bar(2 * CF::kRing + i); };
+  const auto empty_v = [&](int i) { return bar(3 * CF::kRing + i); };
+  const uint32_t b_q = bar(4 * CF::kRing), b_q_free = bar(4 * CF::kRing + 1);  // queries and do are there, were used
+  const uint32_t b_dp = bar(4 * CF::kRing + 2), b_dp_free = bar(4 * CF::kRing + 3);  // S and dP are there, were read
+  const uint32_t b_ds = bar(4 * CF::kRing + 4);
+  const uint32_t b_o = bar(4 * CF::kRing + 5), b_o_free = bar(4 * CF::kRing + 6);  // dQ is complete, was read
+  const uint32_t b_end = bar(4 * CF::kRing + 7), b_raw = bar(4 * CF::kRing + 8);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + CF::kNumBars * 8);
+  volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
+
+  const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid / 32, 0), lane = tid % 32;
+  if (tid == 0) {
+    for (int i = 0; i < CF::kNumBars; ++i) la_init(bar(i), 1);
+    la_init(b_dp_free, 8);
+    la_init(b_ds, 8);
+    la_init(b_o_free, 8);
+    fence_mbar_init();
+    *dead = 0;
+  }
+  if (warp == kWtMmaWarp) tmem_alloc(tmem_at, 512);
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  const uint32_t tmem = __shfl_sync(kFullMask, *tmem_at, 0);
+  WtRowItem w;
+
+  if (warp == kWtLoadWarp) {
+    // ---- loader
+    LaRing<CF::kRing> ring;
+    bool gone = false;  // a place was not free in time: no further copies
+    uint32_t raw = 0, items = 0;
+    for (int item = blockIdx.x; item < a.items && !gone; item += gridDim.x) {
+      if (!wt_row_item(w, a, item)) continue;
+      if (items > 0) gone = !la_wait(b_q_free, (items - 1) & 1, dead);
+      if (gone) break;
+      if (lane == 0) {
+        la_expect(b_q, 2 * CF::kTile);
+#pragma unroll
+        for (int j = 0; j < DP / 64; ++j) {
+          tma_load_block(base + CF::kQ + j * kWtBlock, &maps.q, b_q, j * 64, w.r0, w.h, w.b);
+          tma_load_block(base + CF::kG + j * kWtBlock, &maps.g, b_q, j * 64, w.r0, w.h, w.b);
+        }
+      }
+      __syncwarp();
+      ++items;
+      for (int i = 0; i < w.keys.count; ++i) {
+        const int c0 = w.keys.at(i) * kWtRows;
+        if (ring.used()) {
+          gone = !la_wait(empty_k(ring.i), ring.empty(), dead);
+          if (!gone) gone = !la_wait(empty_v(ring.i), ring.empty(), dead);
+        }
+        if (gone) break;
+        // TMA clips at the tensor's end, not at a row's length; zeros of dS do not take a NaN
+        // out of dS K
+        const bool ragged = c0 + kWtRows > w.len && w.len < a.seqlen;
+        if (lane == 0) {
+          wt_load<DP>(base + CF::kK + ring.i * CF::kTile, &maps.k, ragged ? b_raw : full_k(ring.i), c0, w.h / a.share, w.b);
+          wt_load<DP>(base + CF::kV + ring.i * CF::kTile, &maps.v, full_v(ring.i), c0, w.h / a.share, w.b);
+        }
+        __syncwarp();
+        if (ragged) {
+          la_wait_own(b_raw, raw);
+          raw ^= 1;
+          wt_clear<DP>(smem + CF::kK + ring.i * CF::kTile, w.len - c0, lane);
+          if (lane == 0) la_arrive(full_k(ring.i));
+        }
+        ring.next();
+      }
+    }
+    // the last copies land before the end, also where those that they are for have given up
+#pragma unroll 1
+    for (int i = 0; i < CF::kRing; ++i) {
+      const uint32_t fills = ring.turn + (i < ring.i ? 1 : 0);
+      if (fills > 0) la_wait_own(full_k(i), (fills - 1) & 1), la_wait_own(full_v(i), (fills - 1) & 1);
+    }
+    if (items > 0) la_wait_own(b_q, (items - 1) & 1);
+  } else if (warp == kWtMmaWarp) {
+    // ---- products
+    const bool leader = elect_one();
+    constexpr int kUnits = kWtBlock >> 4;
+    const uint32_t q = tile_desc(base + CF::kQ, 0), g = tile_desc(base + CF::kG, 0);
+    LaRing<CF::kRing> ring;
+    int n = 0, items = 0;  // tiles and items so far
+    // S = Q K^T and dP = dO V^T of tile i, the n-th
+    const auto scores = [&](int i, int n, int at) {
+      const uint32_t idesc = mma_idesc(128, wa_columns(i, w.keys, a.sinks), false, false);
+      const uint32_t k = tile_desc(base + CF::kK + at * CF::kTile, 0), v = tile_desc(base + CF::kV + at * CF::kTile, 0);
+#pragma unroll
+      for (int s = 0; s < DP / 16; ++s) {
+        const int off = (s / 4) * kUnits + (s % 4) * 2;
+        mma_ss(tmem + CF::cS + (n & 1) * 128, q + off, k + off, idesc, s > 0);
+      }
+#pragma unroll
+      for (int s = 0; s < DP / 16; ++s) {
+        const int off = (s / 4) * kUnits + (s % 4) * 2;
+        mma_ss(tmem + CF::cP, g + off, v + off, idesc, s > 0);
+      }
+      mma_commit(b_dp);
+      mma_commit(empty_v(at));
+    };
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+      if (!wt_row_item(w, a, item)) continue;
+      la_wait(b_q, items & 1, dead);
+      int k_at = 0;
+      for (int i = -1; i < w.keys.count; ++i) {
+        const bool more = i + 1 < w.keys.count;
+        const int next = ring.i;
+        if (more) {
+          la_wait(full_k(next), ring.full(), dead);
+          la_wait(full_v(next), ring.full(), dead);
+          if (n > 0) la_wait(b_dp_free, (n - 1) & 1, dead);  // the last tile's, this item's or not
+          tc5_fence_after();
+          if (leader) {
+            scores(i + 1, n, next);
+            if (i + 2 == w.keys.count) mma_commit(b_q_free);
+          }
+          __syncwarp();
+        }
+        if (i >= 0) {
+          const int t = n - 1;  // of all tiles
+          if (i == 0 && items > 0) la_wait(b_o_free, (items - 1) & 1, dead);
+          la_wait(b_ds, t & 1, dead);
+          tc5_fence_after();
+          if (leader) {
+            const uint32_t k = tile_desc(base + CF::kK + k_at * CF::kTile, kWtBlock);
+            const int steps = wa_columns(i, w.keys, a.sinks) / 16;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              if (s < steps)
+                mma_ts(tmem + CF::cDq, tmem + CF::cS + (t & 1) * 128 + (s / 4) * 64 + (s % 4) * 8, k + s * (16 * kTileRow >> 4),
+                       mma_idesc(128, DP, false, true), i > 0 || s > 0);
+            mma_commit(empty_k(k_at));
+            if (!more) mma_commit(b_o);
+          }
+          __syncwarp();
+        }
+        if (more) {
+          k_at = next;
+          ring.next();
+          ++n;
+        }
+      }
+      ++items;
+    }
+    if (leader) mma_commit(b_end);
+    __syncwarp();
+    la_wait_own(b_end, 0);
+  } else if (warp < kWtLoadWarp) {
+    // ---- dS: a query a thread, the two warpgroups 64 keys each
+    const int side = warp / 4, quad = warp % 4;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t p_at = tmem + lanes + CF::cP + side * 64;
+    const float by = a.scale * kLog2e;
+    const uint64_t by2 = pair(by, by);
+    int n = 0, items = 0;
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+      if (!wt_row_item(w, a, item)) continue;
+      const int row = w.r0 + quad * 32 + lane;
+      const int64_t at = ((int64_t)w.b * a.heads + w.h) * a.seqlen + row;
+      const bool real = row < w.end && in_range(at, (int64_t)a.batch * a.heads * a.seqlen);
+      const float lse = real ? -a.lse[at] * kLog2e : 0.f, delta = real ? -a.delta[at] : 0.f;
+      const uint64_t lse2 = pair(lse, lse), delta2 = pair(delta, delta);
+#pragma unroll 1
+      for (int i = 0; i < w.keys.count; ++i, ++n) {
+        const int c0 = w.keys.at(i) * kWtRows;
+        const int cols = wa_columns(i, w.keys, a.sinks) - side * 64;  // of this warpgroup, 64 or more: all its own
+        const uint32_t s_at = tmem + lanes + CF::cS + (n & 1) * 128 + side * 64;
+        la_wait(b_dp, n & 1, dead);
+        tc5_fence_after();
+        uint32_t s[2][32], dp[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (cols > 32 * c) tmem_ld32(s[c], s_at + 32 * c), tmem_ld32(dp[c], p_at + 32 * c);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (cols > 32 * c) tmem_wait_ld(s[c]), tmem_wait_ld(dp[c]);
+        tc5_fence_before();
+        __syncwarp();
+        if (lane == 0) la_arrive(b_dp_free);
+        const bool all = wa_all_seen(w.r0, w.end, c0, c0 + kWtRows, a.window, a.sinks);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (cols <= 32 * c) continue;
+          uint32_t ds[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t z = fma2(pair(s[c][2 * j], s[c][2 * j + 1]), by2, lse2);
+            const uint64_t y = mul2(pair(ex2_approx(pair_lo(z)), ex2_approx(pair_hi(z))),
+                                    add2(pair(dp[c][2 * j], dp[c][2 * j + 1]), delta2));
+            s[c][2 * j] = (uint32_t)y, s[c][2 * j + 1] = (uint32_t)(y >> 32);
+          }
+          if (!all) {
+            const int64_t first = (int64_t)row - a.window + 1 - c0;
+            const int near = first > 0 ? (int)(first < kWtRows ? first : kWtRows) : 0, c32 = side * 64 + 32 * c;
+            const uint32_t seen = wt_bits(near, row + 1 - c0, c32) | (wt_bits(0, a.sinks - c0, c32) & wt_bits(0, row + 1 - c0, c32));
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(seen & 1u << j)) s[c][j] = 0;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) ds[j] = to_bf16x2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1]));
+          tmem_st16(s_at + 16 * c, ds);
+        }
+        tmem_wait_st();
+        tc5_fence_before();
+        __syncwarp();
+        if (lane == 0) la_arrive(b_ds);
+      }
+      la_wait(b_o, items & 1, dead);
+      ++items;
+      tc5_fence_after();
+      const int64_t first = ((int64_t)w.b * a.seqlen * a.heads + w.h) * a.d;
+      wt_put_rows<DP / 2>(smem + CF::kOut + warp * CF::kStage, tmem + lanes + CF::cDq + side * (DP / 2),
+                          static_cast<__nv_bfloat16*>(a.out) + first,
+                          (int64_t)a.batch * a.heads * a.seqlen * a.d - first, (int64_t)a.heads * a.d, w.r0 + quad * 32, w.end, side * (DP / 2), a.d, a.scale, lane);
+      tc5_fence_before();
+      __syncwarp();
+      if (lane == 0) la_arrive(b_o_free);
+    }
+  }
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  if (warp == kWtMmaWarp) tmem_free(tmem, 512);
+}
+
+// delta = do . o of every row, 16-byte units, d / 8 lanes (made up to 8 or 16) a row.
+template <int LANES>
+__global__ void __launch_bounds__(256) winattn_delta16_kernel(const __grid_constant__ WaArgs a) {
+  const int64_t row = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES, all = (int64_t)a.batch * a.heads * a.seqlen;
+  const int u = threadIdx.x % LANES;
+  float sum = 0.f;
+  const int h = (int)(row % a.heads);
+  const int64_t bt = row / a.heads, t = bt % a.seqlen, b = bt / a.seqlen;
+  const bool real = row < all && t < wa_length(a.lengths, b, a.seqlen);
+  if (real && 8 * u < a.d) {
+    const char *o = la_row(a.o, b, t, h, 2) + 16 * u, *g = la_row(a.g, b, t, h, 2) + 16 * u;
+    if (la_inside(a.o, o, 8, 2) && la_inside(a.g, g, 8, 2)) {
+      const uint4 x = *reinterpret_cast<const uint4*>(o), y = *reinterpret_cast<const uint4*>(g);
+      uint64_t z = mul2(from_bf16x2(x.x), from_bf16x2(y.x));
+      z = fma2(from_bf16x2(x.y), from_bf16x2(y.y), z);
+      z = fma2(from_bf16x2(x.z), from_bf16x2(y.z), z);
+      z = fma2(from_bf16x2(x.w), from_bf16x2(y.w), z);
+      sum = pair_lo(z) + pair_hi(z);
+    }
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
+  const int64_t at = (b * a.heads + h) * a.seqlen + t;
+  if (real && u == 0 && in_range(at, all)) a.delta[at] = sum;
+}
+
+}  // namespace ssscan

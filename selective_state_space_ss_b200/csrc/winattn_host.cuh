@@ -13,6 +13,7 @@
 #include "heads_host.cuh"
 #include "host_common.cuh"
 #include "rotate.cuh"
+#include "winattn_bwd.cuh"
 #include "winattn_fma.cuh"
 #include "winattn_fwd.cuh"
 #include "winattn_step.cuh"
@@ -218,13 +219,39 @@ ss_status wa_check_bwd_shape(const WaShape& s) {
   return wa_check_grid(s);
 }
 
-// Tokens of a tile of the backward pass.
-int wa_bwd_tile(const WaShape&) { return kWfTile; }
+template <int DP>
+ss_status wa_tc_bwd(WaArgs a, const WaMaps& maps, void* dq, cudaStream_t stream) {
+  using KV = WtKvCfg<DP>;
+  using DQ = WtDqCfg<DP>;
+  struct Tag : KV {};
+  if (once_per_device<Tag>([] {
+        return wa_set_smem(winattn_dkv_kernel<DP>, KV::kSmem) && wa_set_smem(winattn_dq_kernel<DP>, DQ::kSmem);
+      }) != 1)
+    return SS_ERR_CUDA;
+  constexpr int LANES = DP / 8;
+  const int64_t all = (int64_t)a.batch * a.heads * a.seqlen;
+  winattn_delta16_kernel<LANES><<<(unsigned)((all + 256 / LANES - 1) / (256 / LANES)), 256, 0, stream>>>(a);
+  ss_status st = wa_launched();
+  if (st != SS_OK) return st;
+  const int64_t tiles = (a.seqlen + kWtRows - 1) / kWtRows;
+  const int sms = device_sms() > 0 ? device_sms() : 148;
+  a.out = dq;
+  a.items = (int)wa_grid(tiles, (int64_t)a.batch * a.heads);
+  winattn_dq_kernel<DP><<<a.items < sms ? a.items : sms, DQ::kThreads, DQ::kSmem, stream>>>(a, maps);
+  st = wa_launched();
+  if (st != SS_OK) return st;
+  const unsigned grid = wa_grid(tiles + a.sink_tiles * a.pieces, (int64_t)a.batch * (a.heads / a.share));
+  winattn_dkv_kernel<DP><<<grid, KV::kThreads, KV::kSmem, stream>>>(a, maps);
+  st = wa_launched();
+  return st != SS_OK ? st : wa_sinks<__nv_bfloat16, kWtRows>(a, stream);
+}
 
+// The same workspace does for either tile: which one applies depends on addresses and strides.
 size_t winattn_bwd_bytes(const WaShape& given) {
   if (wa_check_bwd_shape(given) != SS_OK) return (size_t)-1;
   const WaShape s = wa_normal(given, given.seqlen);
-  return wa_bwd_ws(s, wa_split(s, wa_bwd_tile(s)), wa_bwd_tile(s)).bytes;
+  const size_t one = wa_bwd_ws(s, wa_split(s, kWfTile), kWfTile).bytes, two = wa_bwd_ws(s, wa_split(s, kWtRows), kWtRows).bytes;
+  return one > two ? one : two;
 }
 
 ss_status winattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads* v, const ss_heads* o,
@@ -240,19 +267,23 @@ ss_status winattn_bwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads*
   if (!lse || !aligned(lse, 4) || !aligned(lengths, 4)) return SS_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return SS_ERR_INVALID_ARG;
   const WaShape s = wa_normal(given, given.seqlen);
-  const int tile = wa_bwd_tile(s);
-  const WaSplit split = wa_split(s, tile);
-  const WaBwdWs w = wa_bwd_ws(s, split, tile);
-  if (!ws || ws_bytes < w.bytes || !aligned(ws, 256)) return SS_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < winattn_bwd_bytes(given) || !aligned(ws, 256)) return SS_ERR_INVALID_ARG;
   WaArgs a = wa_base(s, q, k, v, scale, lengths);
   a.o = wa_tensor(*o, s.batch, s.seqlen, s.heads, s.d, 1);
   a.g = wa_tensor(*g, s.batch, s.seqlen, s.heads, s.d, 1);
   a.lse = const_cast<float*>(lse);
+  WaMaps maps;
+  const bool tensor = s.dtype == SS_BF16 && aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16) && la_vec(a.o, s.d, 2) &&
+                      wa_map(&maps.q, a.q, s) && wa_map(&maps.k, a.k, s) && wa_map(&maps.v, a.v, s) && wa_map(&maps.g, a.g, s);
+  const int tile = tensor ? kWtRows : kWfTile;
+  const WaSplit split = wa_split(s, tile);
+  const WaBwdWs w = wa_bwd_ws(s, split, tile);
   a.delta = static_cast<float*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part);
   a.sink_tiles = split.sink_tiles, a.pieces = split.pieces, a.piece_tiles = split.piece_tiles;
   a.dk = dk;
   a.dv = dv;
+  if (tensor) return s.d <= 64 ? wa_tc_bwd<64>(a, maps, dq, stream) : wa_tc_bwd<128>(a, maps, dq, stream);
   if (s.dtype == SS_BF16)
     return s.d <= 64 ? wa_fma_bwd<__nv_bfloat16, 64>(a, dq, stream) : wa_fma_bwd<__nv_bfloat16, 128>(a, dq, stream);
   return s.d <= 64 ? wa_fma_bwd<float, 64>(a, dq, stream) : wa_fma_bwd<float, 128>(a, dq, stream);

@@ -19,6 +19,8 @@ the tensor core (which may truncate).
                e32 sum|do||o|;  ds: p (a + D) (1 + g + u) + |ds| (g + u + 4 e32);
                dq: scale sum_j (ds's)|k| + n e32 sum|ds||k|, dk alike over t, dv: sum_t
                p|do| (g + u + (n + 64) e32)
+  underflow    powers of two, and operands, below 2^-126 may come out as zero: that much of
+               every p and of every ds, absolutely
   the end      half a step of the output's type, of the value and of the bound
 """
 from __future__ import annotations
@@ -28,6 +30,7 @@ import math
 import torch
 
 E32 = 2.0 ** -23
+TINY = 2.0 ** -126
 
 
 def half_step(dtype):
@@ -65,7 +68,7 @@ def attention(q, k, v, window, sinks=0, scale=None, lengths=None, do=None):
             top = s.amax(-1)
             e = scale * (d + 8) * E32 * (Q.abs() @ K.abs().T) + 4 * E32 * (s.abs() + top.abs()[:, None]) + 2.0 ** -21
             e = e.masked_fill(~seen, 0).amax(-1, keepdim=True)
-            bo = (p @ V.abs()) * (2 * e + u + (count + 64) * E32)
+            bo = (p @ V.abs()) * (2 * e + u + (count + 64) * E32) + 2 * TINY * (seen.double() @ V.abs())
             bl = e[:, 0] + (count + 64) * E32 + 4 * E32 * (lse.abs() + 1)
             out["o"][0][b, :n, h], out["o"][1][b, :n, h] = o, bo
             out["lse"][0][b, h, :n], out["lse"][1][b, h, :n] = lse, bl
@@ -78,11 +81,11 @@ def attention(q, k, v, window, sinks=0, scale=None, lengths=None, do=None):
             rounded = bo + half_step(dtype) * (o.abs() + bo)
             a = (d + 8) * E32 * (G.abs() @ V.abs().T)
             D = (G.abs() * rounded).sum(-1, keepdim=True) + (d + 8) * E32 * (G.abs() * o.abs()).sum(-1, keepdim=True)
-            eds = p * (a + D) * (1 + g + u) + ds.abs() * (g + u + 4 * E32)
+            eds = p * (a + D) * (1 + g + u) + ds.abs() * (g + u + 4 * E32) + TINY * (dp.abs() + delta.abs() + a + D + 1) * seen
             for name, at, value, bound in (
                     ("dq", h, scale * ds @ K, scale * (eds @ K.abs() + count * E32 * (ds.abs() @ K.abs()))),
                     ("dk", h // share, scale * ds.T @ Q, scale * (eds.T @ Q.abs() + n * share * E32 * (ds.abs().T @ Q.abs()))),
-                    ("dv", h // share, p.T @ G, (p * (g + u + (n * share + 64) * E32)).T @ G.abs())):
+                    ("dv", h // share, p.T @ G, (p * (g + u + (n * share + 64) * E32) + TINY * seen).T @ G.abs())):
                 out[name][0][b, :n, at] += value
                 out[name][1][b, :n, at] += bound
     return out
