@@ -307,22 +307,41 @@ WaPages wa_pages(const ss_pages& p, int kv_heads, int d) {
   return r;
 }
 
-template <typename T, int DP>
-ss_status wa_step_fma(const WaStepArgs& a, int parts, cudaStream_t stream) {
-  constexpr int kSmem = WsFmaCfg<DP>::kFloats * 4;
-  struct Tag : WsFmaCfg<DP> { T x; };
-  if (once_per_device<Tag>([] { return wa_set_smem(winattn_step_fma_kernel<T, DP>, kSmem); }) != 1) return SS_ERR_CUDA;
+// A kernel whose grid's x axis is one cluster.
+template <typename K>
+ss_status wa_step_launch(K kernel, const WaStepArgs& a, int parts, int threads, int smem, cudaStream_t stream) {
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)parts, (unsigned)a.row_tiles, (unsigned)(a.batch * (a.heads / a.share)));
-  c.blockDim = dim3(kWsThreads);
-  c.dynamicSmemBytes = kSmem;
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
   c.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim = {(unsigned)parts, 1, 1};
   c.attrs = at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, winattn_step_fma_kernel<T, DP>, a) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+  return cudaLaunchKernelEx(&c, kernel, a) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+template <typename T, int DP>
+ss_status wa_step_fma(const WaStepArgs& a, int parts, cudaStream_t stream) {
+  constexpr int kSmem = WsFmaCfg<DP>::kFloats * 4;
+  struct Tag : WsFmaCfg<DP> { T x; };
+  if (once_per_device<Tag>([] { return wa_set_smem(winattn_step_fma_kernel<T, DP>, kSmem); }) != 1) return SS_ERR_CUDA;
+  return wa_step_launch(winattn_step_fma_kernel<T, DP>, a, parts < 8 ? parts : 8, kWsThreads, kSmem, stream);
+}
+
+template <int DP, int WARPS, int STAGES>
+ss_status wa_step_mma(const WaStepArgs& a, int parts, cudaStream_t stream) {
+  using CF = WsCfg<DP, WARPS, STAGES>;
+  struct Tag : CF {};
+  if (once_per_device<Tag>([] {
+        return wa_set_smem(winattn_step_kernel<DP, WARPS, STAGES>, CF::kSmem) &&
+               cudaFuncSetAttribute(winattn_step_kernel<DP, WARPS, STAGES>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                   cudaSuccess;
+      }) != 1)
+    return SS_ERR_CUDA;
+  return wa_step_launch(winattn_step_kernel<DP, WARPS, STAGES>, a, parts, CF::kThreads, CF::kSmem, stream);
 }
 
 ss_status winattn_step_impl(const ss_heads* q, const ss_pages* pages, const int32_t* lengths, float scale, void* o,
@@ -350,11 +369,19 @@ ss_status winattn_step_impl(const ss_heads* q, const ss_pages* pages, const int3
   a.batch = (int)s.batch;
   a.scale = scale;
   a.row_tiles = (int)((s.seqlen * a.share + kWsRows - 1) / kWsRows);
-  // a walk is cut while blocks are fewer than SMs twice over and its parts have two chunks or more
+  // A walk is cut while blocks are fewer than SMs twice over and its parts have 64 tokens or
+  // more, and further, for blocks that end at different times, while its parts have 1024.
   const int64_t seen = s.window + s.sinks + s.seqlen - 1, chunks = ((seen < room ? seen : room) + kWsChunk - 1) / kWsChunk;
   const int64_t blocks = s.batch * s.kv_heads * a.row_tiles, sms = device_sms() > 0 ? device_sms() : 148;
   int parts = 1;
-  while (parts < 8 && blocks * parts < 2 * sms && chunks >= 4 * parts) parts *= 2;
+  while (parts < 16 && ((blocks * parts < 2 * sms && chunks >= 2 * parts) || (blocks * parts < 8 * sms && chunks >= 32 * parts)))
+    parts *= 2;
+  if (s.dtype == SS_BF16 && la_vec(a.q, s.d, 2) && la_vec(a.pages.k, s.d, 2) && la_vec(a.pages.v, s.d, 2)) {
+    // few blocks: an SM each and twice the warps
+    const bool few = blocks * parts <= sms;
+    if (s.d <= 64) return few ? wa_step_mma<64, 8, 4>(a, parts, stream) : wa_step_mma<64, 4, 4>(a, parts, stream);
+    return few ? wa_step_mma<128, 8, 3>(a, parts, stream) : wa_step_mma<128, 4, 3>(a, parts, stream);
+  }
   if (s.dtype == SS_BF16)
     return s.d <= 64 ? wa_step_fma<__nv_bfloat16, 64>(a, parts, stream) : wa_step_fma<__nv_bfloat16, 128>(a, parts, stream);
   return s.d <= 64 ? wa_step_fma<float, 64>(a, parts, stream) : wa_step_fma<float, 128>(a, parts, stream);

@@ -11,6 +11,7 @@
 #include <cooperative_groups.h>
 
 #include "rotate.cuh"
+#include "tc5.cuh"
 #include "winattn_common.cuh"
 
 namespace ssscan {
@@ -181,6 +182,263 @@ __global__ void __launch_bounds__(kWsThreads) winattn_step_fma_kernel(const __gr
     const int64_t to = (((int64_t)b * a.tokens + token(r)) * a.heads + head(r)) * a.d + c;
     if (in_range(to, (int64_t)a.batch * a.tokens * a.heads * a.d))
       rot_set(static_cast<T*>(a.out)[to], total > 0.f ? o / total : 0.f);
+  }
+  cluster.sync();  // a block's shared memory stays until all have read it
+}
+
+// ---- bf16 rows of whole 16-byte units
+
+__device__ __forceinline__ void ws_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four 8 x 8 blocks from shared memory: a thread gets two neighbours of row lane / 4 of each.
+__device__ __forceinline__ void load_blocks(uint32_t row_addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(row_addr)
+               : "memory");
+}
+
+// Every warp has a ring of STAGES places of its own for 16 tokens' keys and values, filled by
+// asynchronous copies, and a softmax of its own: no warp waits for another before the end,
+// where the warps' and then the blocks' parts are joined.  The products are 16 rows wide (one
+// group's queries, made up with zeros) on the plain tensor path: they have nothing to do next
+// to the copies, 32 bytes a clock of an SM.
+template <int DP, int WARPS, int STAGES>
+struct WsCfg {
+  static constexpr int kWarps = WARPS, kThreads = 32 * WARPS, kTokens = 16;
+  static constexpr int kRowBytes = DP * 2, kTile = kTokens * kRowBytes, kStage = 2 * kTile, kRing = STAGES * kStage;
+  static constexpr int kQ = kWarps * kRing, kOk = kQ + kWsRows * kRowBytes;
+  static constexpr int kSmem = kOk + kWarps * STAGES * 4;
+  // the end: every warp's sums, maxima and normalisers in the places of its ring
+  static_assert(kRing >= kWsRows * (DP + 4) * 4 + 2 * kWsRows * 4, "a warp's part");
+};
+template <int DP>
+__device__ __forceinline__ uint32_t ws_unit(int row, int unit) {
+  return row * (DP * 2) + ((unit ^ (row & 7)) << 4);
+}
+
+template <int DP, int WARPS, int STAGES>
+__global__ void __launch_bounds__(32 * WARPS) winattn_step_kernel(const __grid_constant__ WaStepArgs a) {
+  namespace cg = cooperative_groups;
+  using CF = WsCfg<DP, WARPS, STAGES>;
+  constexpr int UNITS = DP / 8, KS = DP / 16;  // 16-byte units of a row, MMA steps
+  extern __shared__ __align__(16) char ws_bytes[];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, kv_heads = a.heads / a.share;
+  const int b = blockIdx.z / kv_heads, hk = blockIdx.z % kv_heads;
+  const int row0 = blockIdx.y * kWsRows, all_rows = a.tokens * a.share;
+  const int rows = all_rows - row0 < kWsRows ? all_rows - row0 : kWsRows;
+  const int len = wa_length(a.lengths, b, a.pages.max_pages * a.pages.page_size);
+  const auto token = [&](int r) { return (row0 + r) / a.share; };
+  const auto head = [&](int r) { return hk * a.share + (row0 + r) % a.share; };
+  const int last = len - a.tokens + token(rows - 1) + 1;  // behind the block's newest query
+  const WaVisible seen(len - a.tokens + token(0), last, a.window, a.sinks);
+  char* ring = ws_bytes + warp * CF::kRing;
+  uint32_t* oks = reinterpret_cast<uint32_t*>(ws_bytes + CF::kOk) + warp * STAGES;
+
+  // queries into shared memory, then into registers
+  for (int u = tid; u < kWsRows * UNITS; u += CF::kThreads) {
+    const int r = u / UNITS, c = u % UNITS;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < rows && 8 * c < a.d) {
+      const char* from = la_row(a.q, b, token(r), head(r), 2) + 16 * c;
+      if (la_inside(a.q, from, 8, 2)) x = *reinterpret_cast<const uint4*>(from);
+    }
+    *reinterpret_cast<uint4*>(ws_bytes + CF::kQ + ws_unit<DP>(r, c)) = x;
+  }
+
+  // this warp's steps of 16 tokens: the warps of all parts take them in turn
+  const int steps = (seen.count + CF::kTokens - 1) / CF::kTokens, stride = parts * CF::kWarps;
+  const int first = part * CF::kWarps + warp;
+  const int count = steps > first ? (steps - first + stride - 1) / stride : 0;
+  // The token that lanes 0 to 15 (and 16 to 31) see to in step n, -1 for none, and the entry of
+  // the page table that it lies in, asked for a step before it is used.
+  const auto token_of = [&](int n) {
+    const int i = (first + n * stride) * CF::kTokens + lane % CF::kTokens;
+    return n < count && i < seen.count ? seen.at(i) : -1;
+  };
+  const uint32_t page_size = (uint32_t)a.pages.page_size;
+  const int* table = a.pages.table + (int64_t)b * a.pages.max_pages;
+  const auto entry_of = [&](int t) { return t >= 0 ? table[(uint32_t)t / page_size] : -1; };
+  const char *k_base = static_cast<const char*>(a.pages.k.ptr) + (int64_t)hk * a.pages.k.sh * 2;
+  const char *v_base = static_cast<const char*>(a.pages.v.ptr) + (int64_t)hk * a.pages.v.sh * 2;
+  const bool alike = a.pages.k.sb == a.pages.v.sb && a.pages.k.st == a.pages.v.st;
+  const int unit = lane % UNITS;
+  const auto fill = [&](int n, int t, int page) {  // step n into its place of the ring
+    const int stage = n % STAGES;
+    const uint32_t to = smem_u32(ring) + stage * CF::kStage;
+    const bool is = t >= 0 && (uint32_t)page < (uint32_t)a.pages.num_pages;
+    const uint32_t ok = __ballot_sync(kFullMask, is) & 0xffffu;
+    if (lane == 0) oks[stage] = ok;
+    const int64_t at = (uint32_t)t % page_size;
+    const int64_t k_of = (page * a.pages.k.sb + at * a.pages.k.st) * 2, v_of = (page * a.pages.v.sb + at * a.pages.v.st) * 2;
+#pragma unroll
+    for (int j = 0; j < CF::kTokens; j += 32 / UNITS) {
+      const int row = j + lane / UNITS;
+      const char* k = k_base + __shfl_sync(kFullMask, k_of, row) + unit * 16;
+      const char* v = v_base + unit * 16;
+      if (alike) v += k - (k_base + unit * 16);
+      else v += __shfl_sync(kFullMask, v_of, row);
+      bool in = (ok >> row & 1) && unit * 8 < a.d;
+      if (in) in = la_inside(a.pages.k, k, 8, 2) && la_inside(a.pages.v, v, 8, 2);
+      // tokens that are none are zeros: a product of zero with what lies there might not be
+      const uint32_t bytes = in ? 16 : 0, dst = to + ws_unit<DP>(row, unit);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(in ? k : k_base), "r"(bytes) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst + CF::kTile), "l"(in ? v : v_base), "r"(bytes)
+                   : "memory");
+    }
+  };
+  int t_next[STAGES], entry_next[STAGES];  // the first steps' entries all at once
+#pragma unroll
+  for (int n = 0; n < STAGES; ++n) t_next[n] = token_of(n), entry_next[n] = entry_of(t_next[n]);
+#pragma unroll
+  for (int n = 0; n < STAGES - 1; ++n) {
+    if (n < count) fill(n, t_next[n], entry_next[n]);
+    cp_async_commit();
+  }
+  int t = t_next[STAGES - 1], entry = entry_next[STAGES - 1];
+  __syncthreads();  // the queries
+  uint32_t q[KS][4];
+#pragma unroll
+  for (int s = 0; s < KS; ++s)
+    load_blocks(smem_u32(ws_bytes + CF::kQ) + ws_unit<DP>(lane % 16, 2 * s + lane / 16), q[s]);
+
+  // rows lane / 4 and 8 further down; columns 2 (lane % 4) and the next of each block of 8
+  const float by = a.scale * kLog2e, room = 8.f / by;
+  float acc[DP / 8][4] = {}, top[2] = {-CUDART_INF_F, -CUDART_INF_F}, sum[2] = {0.f, 0.f};
+  int at_row[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) at_row[y] = lane / 4 + 8 * y < rows ? len - a.tokens + token(lane / 4 + 8 * y) : -1;
+#pragma unroll 1
+  for (int n = 0; n < count; ++n) {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
+    __syncwarp();
+    if (n + STAGES - 1 < count) fill(n + STAGES - 1, t, entry);
+    cp_async_commit();
+    t = token_of(n + STAGES), entry = entry_of(t);
+    const int stage = n % STAGES;
+    const uint32_t k_at = smem_u32(ring) + stage * CF::kStage, v_at = k_at + CF::kTile, ok = oks[stage];
+    float s[2][4] = {}, s2[2][4] = {};  // (two sums each: the products wait for one another)
+#pragma unroll
+    for (int c = 0; c < KS; ++c) {
+      uint32_t x[4];  // tokens 0 - 7 and 8 - 15, 16 values each
+      load_blocks(k_at + ws_unit<DP>(lane % 8 + lane / 16 * 8, 2 * c + lane / 8 % 2), x);
+      ws_mma(c % 2 ? s2[0] : s[0], q[c], x[0], x[1]);
+      ws_mma(c % 2 ? s2[1] : s[1], q[c], x[2], x[3]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[0][e] += s2[0][e], s[1][e] += s2[1][e];
+    if (ok != 0xffffu || a.tokens > 1) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = 8 * y + 2 * (lane % 4) + e % 2, i = (first + n * stride) * CF::kTokens + col;
+          if (!(ok >> col & 1) || !wa_sees(at_row[e / 2], seen.at(i), a.window, a.sinks)) s[y][e] = -CUDART_INF_F;
+        }
+    }
+    float most[2], fade[2] = {1.f, 1.f};
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      most[y] = fmaxf(fmaxf(s[0][2 * y], s[0][2 * y + 1]), fmaxf(s[1][2 * y], s[1][2 * y + 1]));
+      most[y] = fmaxf(most[y], __shfl_xor_sync(kFullMask, most[y], 1));
+      most[y] = fmaxf(most[y], __shfl_xor_sync(kFullMask, most[y], 2));
+      if (most[y] > top[y] + room) fade[y] = ex2_approx((top[y] - most[y]) * by), top[y] = most[y];
+    }
+    if (__any_sync(kFullMask, fade[0] != 1.f || fade[1] != 1.f)) {
+#pragma unroll
+      for (int c = 0; c < DP / 8; ++c) acc[c][0] *= fade[0], acc[c][1] *= fade[0], acc[c][2] *= fade[1], acc[c][3] *= fade[1];
+      sum[0] *= fade[0], sum[1] *= fade[1];
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const float off = top[y] == -CUDART_INF_F ? 0.f : -top[y] * by;
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int e = 2 * y; e < 2 * y + 2; ++e) {
+          s[z][e] = ex2_approx(fmaf(s[z][e], by, off));
+          sum[y] += s[z][e];
+        }
+    }
+    const uint32_t p[4] = {to_bf16x2(s[0][0], s[0][1]), to_bf16x2(s[0][2], s[0][3]), to_bf16x2(s[1][0], s[1][1]),
+                           to_bf16x2(s[1][2], s[1][3])};
+#pragma unroll
+    for (int c = 0; c < DP / 16; ++c) {
+      uint32_t x[4];  // 16 columns of all 16 tokens
+      load_blocks_t(v_at + ws_unit<DP>(lane % 16, 2 * c + lane / 16), x);
+      ws_mma(acc[2 * c], p, x[0], x[1]);
+      ws_mma(acc[2 * c + 1], p, x[2], x[3]);
+    }
+    __syncwarp();  // before the place is filled again
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  // every warp's part into its ring's place: sums, maxima (base 2) and normalisers of 16 rows
+  constexpr int ROW = DP + 4;
+  const auto part_of = [&](int w) { return reinterpret_cast<float*>(ws_bytes + w * CF::kRing); };
+  float* mine = part_of(warp);
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    sum[y] += __shfl_xor_sync(kFullMask, sum[y], 1);
+    sum[y] += __shfl_xor_sync(kFullMask, sum[y], 2);
+    const int r = lane / 4 + 8 * y;
+    if (lane % 4 == 0) mine[kWsRows * ROW + r] = top[y] * by, mine[kWsRows * ROW + kWsRows + r] = sum[y];
+#pragma unroll
+    for (int c = 0; c < DP / 8; ++c)
+      *reinterpret_cast<float2*>(mine + r * ROW + 8 * c + 2 * (lane % 4)) = make_float2(acc[c][2 * y], acc[c][2 * y + 1]);
+  }
+  __syncthreads();
+  // the warps' joined into the first's place
+  const auto joined = [&](const auto& from, int n, int r, int c, float& most, float& total) {
+    most = -CUDART_INF_F;
+    for (int x = 0; x < n; ++x) most = fmaxf(most, from(x)[kWsRows * ROW + r]);
+    float o = 0.f;
+    total = 0.f;
+    if (most != -CUDART_INF_F)
+      for (int x = 0; x < n; ++x) {
+        const float* y = from(x);
+        const float f = ex2_approx(y[kWsRows * ROW + r] - most);
+        total = fmaf(f, y[kWsRows * ROW + kWsRows + r], total);
+        o = fmaf(f, y[r * ROW + c], o);
+      }
+    return o;
+  };
+  float *whole = part_of(0), o[kWsRows * DP / CF::kThreads], m[kWsRows * DP / CF::kThreads], l[kWsRows * DP / CF::kThreads];
+#pragma unroll
+  for (int i = 0; i < kWsRows * DP / CF::kThreads; ++i) {
+    const int e = i * CF::kThreads + tid;
+    o[i] = joined(part_of, CF::kWarps, e / DP, e % DP, m[i], l[i]);
+  }
+  __syncthreads();
+  const auto put = [&](int r, int c, float x, float total) {
+    const int64_t to = (((int64_t)b * a.tokens + token(r)) * a.heads + head(r)) * a.d + c;
+    if (r < rows && c < a.d && in_range(to, (int64_t)a.batch * a.tokens * a.heads * a.d))
+      static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(total > 0.f ? x / total : 0.f);
+  };
+  if (parts == 1) {
+#pragma unroll
+    for (int i = 0; i < kWsRows * DP / CF::kThreads; ++i) put((i * CF::kThreads + tid) / DP, (i * CF::kThreads + tid) % DP, o[i], l[i]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kWsRows * DP / CF::kThreads; ++i) {
+    const int e = i * CF::kThreads + tid, r = e / DP, c = e % DP;
+    whole[r * ROW + c] = o[i];
+    if (c == 0) whole[kWsRows * ROW + r] = m[i], whole[kWsRows * ROW + kWsRows + r] = l[i];
+  }
+  cluster.sync();
+  // the blocks' joined, each block a share of the values
+  const auto whole_of = [&](int x) { return cluster.map_shared_rank(whole, x); };
+  for (int e = part * CF::kThreads + tid; e < rows * DP; e += parts * CF::kThreads) {
+    float most, total;
+    const float x = joined(whole_of, parts, e / DP, e % DP, most, total);
+    put(e / DP, e % DP, x, total);
   }
   cluster.sync();  // a block's shared memory stays until all have read it
 }
