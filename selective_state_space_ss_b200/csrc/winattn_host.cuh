@@ -331,17 +331,23 @@ ss_status wa_step_fma(const WaStepArgs& a, int parts, cudaStream_t stream) {
   return wa_step_launch(winattn_step_fma_kernel<T, DP>, a, parts < 8 ? parts : 8, kWsThreads, kSmem, stream);
 }
 
-template <int DP, int WARPS, int STAGES>
-ss_status wa_step_mma(const WaStepArgs& a, int parts, cudaStream_t stream) {
+template <int DP, int WARPS, int STAGES, bool WHOLE>
+ss_status wa_step_mma_as(const WaStepArgs& a, int parts, cudaStream_t stream) {
   using CF = WsCfg<DP, WARPS, STAGES>;
-  struct Tag : CF {};
+  struct Tag : CF { char whole[1 + WHOLE]; };
   if (once_per_device<Tag>([] {
-        return wa_set_smem(winattn_step_kernel<DP, WARPS, STAGES>, CF::kSmem) &&
-               cudaFuncSetAttribute(winattn_step_kernel<DP, WARPS, STAGES>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+        return wa_set_smem(winattn_step_kernel<DP, WARPS, STAGES, WHOLE>, CF::kSmem) &&
+               cudaFuncSetAttribute(winattn_step_kernel<DP, WARPS, STAGES, WHOLE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
                    cudaSuccess;
       }) != 1)
     return SS_ERR_CUDA;
-  return wa_step_launch(winattn_step_kernel<DP, WARPS, STAGES>, a, parts, CF::kThreads, CF::kSmem, stream);
+  return wa_step_launch(winattn_step_kernel<DP, WARPS, STAGES, WHOLE>, a, parts, CF::kThreads, CF::kSmem, stream);
+}
+
+template <int DP, int WARPS, int STAGES>
+ss_status wa_step_mma(const WaStepArgs& a, int parts, cudaStream_t stream) {
+  return a.pages.page_size % 16 == 0 ? wa_step_mma_as<DP, WARPS, STAGES, true>(a, parts, stream)
+                                     : wa_step_mma_as<DP, WARPS, STAGES, false>(a, parts, stream);
 }
 
 ss_status winattn_step_impl(const ss_heads* q, const ss_pages* pages, const int32_t* lengths, float scale, void* o,
@@ -369,15 +375,17 @@ ss_status winattn_step_impl(const ss_heads* q, const ss_pages* pages, const int3
   a.batch = (int)s.batch;
   a.scale = scale;
   a.row_tiles = (int)((s.seqlen * a.share + kWsRows - 1) / kWsRows);
-  // A walk is cut while blocks are fewer than SMs twice over and its parts have 64 tokens or
-  // more, and further, for blocks that end at different times, while its parts have 1024.
+  // Blocks cost 6 us or more to begin and join, so there is one wave of them: a walk is cut
+  // (into parts of 64 tokens or more) only as far as SMs are left.  Batch 64 of 8 groups, 4112
+  // tokens of 128: 162 us uncut, 184, 206, 250 in 2, 4, 8 parts; one row of 4 groups, 65001
+  // tokens: 40 us in 16 parts, 73, 137, 268, 527 in 8, 4, 2 and 1.
   const int64_t seen = s.window + s.sinks + s.seqlen - 1, chunks = ((seen < room ? seen : room) + kWsChunk - 1) / kWsChunk;
   const int64_t blocks = s.batch * s.kv_heads * a.row_tiles, sms = device_sms() > 0 ? device_sms() : 148;
   int parts = 1;
-  while (parts < 16 && ((blocks * parts < 2 * sms && chunks >= 2 * parts) || (blocks * parts < 8 * sms && chunks >= 32 * parts)))
-    parts *= 2;
+  while (parts < 16 && 2 * blocks * parts <= sms && chunks >= 2 * parts) parts *= 2;
   if (s.dtype == SS_BF16 && la_vec(a.q, s.d, 2) && la_vec(a.pages.k, s.d, 2) && la_vec(a.pages.v, s.d, 2)) {
-    // few blocks: an SM each and twice the warps
+    // few blocks: an SM each and twice the warps (16 rows of 8 groups, 1028 tokens: 16 us, 21
+    // with four; with more blocks than SMs 4 to 10% slower)
     const bool few = blocks * parts <= sms;
     if (s.d <= 64) return few ? wa_step_mma<64, 8, 4>(a, parts, stream) : wa_step_mma<64, 4, 4>(a, parts, stream);
     return few ? wa_step_mma<128, 8, 3>(a, parts, stream) : wa_step_mma<128, 4, 3>(a, parts, stream);

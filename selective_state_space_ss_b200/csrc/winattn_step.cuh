@@ -202,11 +202,13 @@ __device__ __forceinline__ void load_blocks(uint32_t row_addr, uint32_t (&r)[4])
                : "memory");
 }
 
-// Every warp has a ring of STAGES places of its own for 16 tokens' keys and values, filled by
-// asynchronous copies, and a softmax of its own: no warp waits for another before the end,
-// where the warps' and then the blocks' parts are joined.  The products are 16 rows wide (one
-// group's queries, made up with zeros) on the plain tensor path: they have nothing to do next
-// to the copies, 32 bytes a clock of an SM.
+// Every warp has a ring of STAGES places of its own for 16 tokens' keys and values (numbers
+// 16 n to 16 n + 15 of the sequence), filled by asynchronous copies, and a softmax of its own:
+// no warp waits for another before the end, where the warps' and then the blocks' parts are
+// joined.  The products are 16 rows wide (one group's queries, made up with zeros) on the plain
+// tensor path: what they take is little next to the copies.  WHOLE: pages of a multiple of 16
+// tokens, so that a place comes out of one page, with one look at the table and little address
+// work (bulk copies of a row each, one a lane, took 1.5 times as long).
 template <int DP, int WARPS, int STAGES>
 struct WsCfg {
   static constexpr int kWarps = WARPS, kThreads = 32 * WARPS, kTokens = 16;
@@ -221,7 +223,7 @@ __device__ __forceinline__ uint32_t ws_unit(int row, int unit) {
   return row * (DP * 2) + ((unit ^ (row & 7)) << 4);
 }
 
-template <int DP, int WARPS, int STAGES>
+template <int DP, int WARPS, int STAGES, bool WHOLE>
 __global__ void __launch_bounds__(32 * WARPS) winattn_step_kernel(const __grid_constant__ WaStepArgs a) {
   namespace cg = cooperative_groups;
   using CF = WsCfg<DP, WARPS, STAGES>;
@@ -237,7 +239,9 @@ __global__ void __launch_bounds__(32 * WARPS) winattn_step_kernel(const __grid_c
   const auto token = [&](int r) { return (row0 + r) / a.share; };
   const auto head = [&](int r) { return hk * a.share + (row0 + r) % a.share; };
   const int last = len - a.tokens + token(rows - 1) + 1;  // behind the block's newest query
-  const WaVisible seen(len - a.tokens + token(0), last, a.window, a.sinks);
+  const int p0 = len - a.tokens + token(0) > 0 ? len - a.tokens + token(0) : 0;
+  const WaKeyTiles<CF::kTokens> tiles(p0, last, a.window, a.sinks);
+  const WaVisible seen(p0, last, a.window, a.sinks);
   char* ring = ws_bytes + warp * CF::kRing;
   uint32_t* oks = reinterpret_cast<uint32_t*>(ws_bytes + CF::kOk) + warp * STAGES;
 
@@ -253,55 +257,85 @@ __global__ void __launch_bounds__(32 * WARPS) winattn_step_kernel(const __grid_c
   }
 
   // this warp's steps of 16 tokens: the warps of all parts take them in turn
-  const int steps = (seen.count + CF::kTokens - 1) / CF::kTokens, stride = parts * CF::kWarps;
+  const int steps = last > 0 ? tiles.count : 0, stride = parts * CF::kWarps;
   const int first = part * CF::kWarps + warp;
   const int count = steps > first ? (steps - first + stride - 1) / stride : 0;
-  // The token that lanes 0 to 15 (and 16 to 31) see to in step n, -1 for none, and the entry of
-  // the page table that it lies in, asked for a step before it is used.
-  const auto token_of = [&](int n) {
-    const int i = (first + n * stride) * CF::kTokens + lane % CF::kTokens;
-    return n < count && i < seen.count ? seen.at(i) : -1;
-  };
+  const auto tile_of = [&](int n) { return tiles.at(first + n * stride) * CF::kTokens; };  // its first token
+  // the entry of the page table that a step's tokens lie in, asked for a step before it is used
   const uint32_t page_size = (uint32_t)a.pages.page_size;
   const int* table = a.pages.table + (int64_t)b * a.pages.max_pages;
-  const auto entry_of = [&](int t) { return t >= 0 ? table[(uint32_t)t / page_size] : -1; };
+  const auto entry_of = [&](int n) {
+    if (n >= count) return -1;
+    const int t = tile_of(n) + (WHOLE ? 0 : lane % CF::kTokens);
+    return t < last ? table[(uint32_t)t / page_size] : -1;
+  };
   const char *k_base = static_cast<const char*>(a.pages.k.ptr) + (int64_t)hk * a.pages.k.sh * 2;
   const char *v_base = static_cast<const char*>(a.pages.v.ptr) + (int64_t)hk * a.pages.v.sh * 2;
-  const bool alike = a.pages.k.sb == a.pages.v.sb && a.pages.k.st == a.pages.v.st;
   const int unit = lane % UNITS;
-  const auto fill = [&](int n, int t, int page) {  // step n into its place of the ring
-    const int stage = n % STAGES;
+  const uint32_t unit_bytes = unit * 8 < a.d ? 16 : 0;
+  const auto copy = [&](uint32_t to, const char* from, uint32_t bytes) {  // zeros where bytes is 0
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+  };
+  // step n into its place of the ring
+  const auto fill = [&](int n, int entry) {
+    const int stage = n % STAGES, t0 = tile_of(n), row = lane / UNITS;
     const uint32_t to = smem_u32(ring) + stage * CF::kStage;
-    const bool is = t >= 0 && (uint32_t)page < (uint32_t)a.pages.num_pages;
-    const uint32_t ok = __ballot_sync(kFullMask, is) & 0xffffu;
+    const auto below = [&](int k) { return k <= t0 ? 0u : k >= t0 + CF::kTokens ? 0xffffu : (1u << (k - t0)) - 1; };
+    uint32_t ok = below(last) & (~below(seen.first) | below(a.sinks));  // tokens that any of the queries sees
+    const bool in_page = (uint32_t)entry < (uint32_t)a.pages.num_pages;
+    ok &= WHOLE ? (in_page ? 0xffffu : 0u) : __ballot_sync(kFullMask, in_page);
     if (lane == 0) oks[stage] = ok;
-    const int64_t at = (uint32_t)t % page_size;
-    const int64_t k_of = (page * a.pages.k.sb + at * a.pages.k.st) * 2, v_of = (page * a.pages.v.sb + at * a.pages.v.st) * 2;
+    // tokens that are none are zeros: a product of zero with what lies there might not be
+    if (WHOLE) {
+      const int64_t at = (uint32_t)t0 % page_size + row;
+      const char* k = k_base + (entry * a.pages.k.sb + at * a.pages.k.st) * 2 + unit * 16;
+      const char* v = v_base + (entry * a.pages.v.sb + at * a.pages.v.st) * 2 + unit * 16;
+      const int64_t k_step = a.pages.k.st * (2 * (32 / UNITS)), v_step = a.pages.v.st * (2 * (32 / UNITS));
+#ifndef SS_BOUNDS_CHECK
+      if (ok == 0xffffu) {
 #pragma unroll
-    for (int j = 0; j < CF::kTokens; j += 32 / UNITS) {
-      const int row = j + lane / UNITS;
-      const char* k = k_base + __shfl_sync(kFullMask, k_of, row) + unit * 16;
-      const char* v = v_base + unit * 16;
-      if (alike) v += k - (k_base + unit * 16);
-      else v += __shfl_sync(kFullMask, v_of, row);
-      bool in = (ok >> row & 1) && unit * 8 < a.d;
-      if (in) in = la_inside(a.pages.k, k, 8, 2) && la_inside(a.pages.v, v, 8, 2);
-      // tokens that are none are zeros: a product of zero with what lies there might not be
-      const uint32_t bytes = in ? 16 : 0, dst = to + ws_unit<DP>(row, unit);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(in ? k : k_base), "r"(bytes) : "memory");
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst + CF::kTile), "l"(in ? v : v_base), "r"(bytes)
-                   : "memory");
+        for (int j = 0; j < CF::kTokens; j += 32 / UNITS) {
+          const uint32_t dst = to + ws_unit<DP>(j + row, unit);
+          copy(dst, k, unit_bytes);
+          copy(dst + CF::kTile, v, unit_bytes);
+          k += k_step, v += v_step;
+        }
+        return;
+      }
+#endif
+#pragma unroll
+      for (int j = 0; j < CF::kTokens; j += 32 / UNITS) {
+        bool in = (ok >> (j + row) & 1) && unit_bytes > 0;
+        if (in) in = la_inside(a.pages.k, k, 8, 2) && la_inside(a.pages.v, v, 8, 2);
+        const uint32_t dst = to + ws_unit<DP>(j + row, unit);
+        copy(dst, in ? k : k_base, in ? 16 : 0);
+        copy(dst + CF::kTile, in ? v : v_base, in ? 16 : 0);
+        k += k_step, v += v_step;
+      }
+    } else {
+      const int64_t at = (uint32_t)(t0 + lane % CF::kTokens) % page_size;
+      const int64_t k_of = (entry * a.pages.k.sb + at * a.pages.k.st) * 2, v_of = (entry * a.pages.v.sb + at * a.pages.v.st) * 2;
+#pragma unroll
+      for (int j = 0; j < CF::kTokens; j += 32 / UNITS) {
+        const char* k = k_base + __shfl_sync(kFullMask, k_of, j + row) + unit * 16;
+        const char* v = v_base + __shfl_sync(kFullMask, v_of, j + row) + unit * 16;
+        bool in = (ok >> (j + row) & 1) && unit_bytes > 0;
+        if (in) in = la_inside(a.pages.k, k, 8, 2) && la_inside(a.pages.v, v, 8, 2);
+        const uint32_t dst = to + ws_unit<DP>(j + row, unit);
+        copy(dst, in ? k : k_base, in ? 16 : 0);
+        copy(dst + CF::kTile, in ? v : v_base, in ? 16 : 0);
+      }
     }
   };
-  int t_next[STAGES], entry_next[STAGES];  // the first steps' entries all at once
+  int entries[STAGES];  // the first steps' all at once
 #pragma unroll
-  for (int n = 0; n < STAGES; ++n) t_next[n] = token_of(n), entry_next[n] = entry_of(t_next[n]);
+  for (int n = 0; n < STAGES; ++n) entries[n] = entry_of(n);
 #pragma unroll
   for (int n = 0; n < STAGES - 1; ++n) {
-    if (n < count) fill(n, t_next[n], entry_next[n]);
+    if (n < count) fill(n, entries[n]);
     cp_async_commit();
   }
-  int t = t_next[STAGES - 1], entry = entry_next[STAGES - 1];
+  int entry = entries[STAGES - 1];
   __syncthreads();  // the queries
   uint32_t q[KS][4];
 #pragma unroll
@@ -318,9 +352,9 @@ __global__ void __launch_bounds__(32 * WARPS) winattn_step_kernel(const __grid_c
   for (int n = 0; n < count; ++n) {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
     __syncwarp();
-    if (n + STAGES - 1 < count) fill(n + STAGES - 1, t, entry);
+    if (n + STAGES - 1 < count) fill(n + STAGES - 1, entry);
     cp_async_commit();
-    t = token_of(n + STAGES), entry = entry_of(t);
+    entry = entry_of(n + STAGES);
     const int stage = n % STAGES;
     const uint32_t k_at = smem_u32(ring) + stage * CF::kStage, v_at = k_at + CF::kTile, ok = oks[stage];
     float s[2][4] = {}, s2[2][4] = {};  // (two sums each: the products wait for one another)
@@ -338,8 +372,8 @@ __global__ void __launch_bounds__(32 * WARPS) winattn_step_kernel(const __grid_c
       for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int col = 8 * y + 2 * (lane % 4) + e % 2, i = (first + n * stride) * CF::kTokens + col;
-          if (!(ok >> col & 1) || !wa_sees(at_row[e / 2], seen.at(i), a.window, a.sinks)) s[y][e] = -CUDART_INF_F;
+          const int col = 8 * y + 2 * (lane % 4) + e % 2;
+          if (!(ok >> col & 1) || !wa_sees(at_row[e / 2], tile_of(n) + col, a.window, a.sinks)) s[y][e] = -CUDART_INF_F;
         }
     }
     float most[2], fade[2] = {1.f, 1.f};
@@ -388,6 +422,7 @@ __global__ void __launch_bounds__(32 * WARPS) winattn_step_kernel(const __grid_c
     sum[y] += __shfl_xor_sync(kFullMask, sum[y], 1);
     sum[y] += __shfl_xor_sync(kFullMask, sum[y], 2);
     const int r = lane / 4 + 8 * y;
+    if (r >= rows) continue;  // (rows made up with zeros)
     if (lane % 4 == 0) mine[kWsRows * ROW + r] = top[y] * by, mine[kWsRows * ROW + kWsRows + r] = sum[y];
 #pragma unroll
     for (int c = 0; c < DP / 8; ++c)
@@ -413,7 +448,7 @@ __global__ void __launch_bounds__(32 * WARPS) winattn_step_kernel(const __grid_c
 #pragma unroll
   for (int i = 0; i < kWsRows * DP / CF::kThreads; ++i) {
     const int e = i * CF::kThreads + tid;
-    o[i] = joined(part_of, CF::kWarps, e / DP, e % DP, m[i], l[i]);
+    if (e / DP < rows) o[i] = joined(part_of, CF::kWarps, e / DP, e % DP, m[i], l[i]);
   }
   __syncthreads();
   const auto put = [&](int r, int c, float x, float total) {
@@ -429,6 +464,7 @@ __global__ void __launch_bounds__(32 * WARPS) winattn_step_kernel(const __grid_c
 #pragma unroll
   for (int i = 0; i < kWsRows * DP / CF::kThreads; ++i) {
     const int e = i * CF::kThreads + tid, r = e / DP, c = e % DP;
+    if (r >= rows) continue;
     whole[r * ROW + c] = o[i];
     if (c == 0) whole[kWsRows * ROW + r] = m[i], whole[kWsRows * ROW + kWsRows + r] = l[i];
   }
