@@ -5,10 +5,13 @@
 //
 //   (x, y) -> (x cos a - y sin a, x sin a + y cos a).
 //
-// The angle is a product of a 32-bit integer and a float, exact in a double; it is brought
-// into +-pi there (fp32 has lost all of it at a position of 2^24), and its sine and cosine
-// are rounded to fp32 once.  A block works them out for a few tokens and then goes over all
-// their heads: bound by memory, each value read once and written once.
+// The angle is a product of a 32-bit integer and a float, exact in a double, and its sine and
+// cosine are worked out there (fp32 has lost all of it at a position of 2^24) and rounded to
+// fp32 once.  A block works them out for a few tokens and then goes over all
+// their heads: bound by memory, each value read once and written once.  Batch 8, 2048 tokens, 40
+// heads on 8 of 128 into pages (470 MB): 84 us, 5.6 TB/s, 85% of the copy rate; 24 on 8 of 64
+// rotated (134 MB): 28 us, 73%.  What else it does is to hide: five blocks an SM and one row
+// under way a thread (two took 84 and 29 us with more registers, four 88 and 30).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -19,7 +22,7 @@
 
 namespace ssscan {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 256, kRotTokens = 16;  // of a block
 
 // The cache, as the kernels have it.
 struct WaPages {
@@ -67,15 +70,71 @@ __device__ __forceinline__ void rot_store(T* to, const RotUnit<T, VEC>& u) {
 __device__ __forceinline__ void rot_set(float& to, float x) { to = x; }
 __device__ __forceinline__ void rot_set(__nv_bfloat16& to, float x) { to = __float2bfloat16_rn(x); }
 
-__device__ __forceinline__ void rot_turn(float& x, float& y, float c, float s) {
-  const float x0 = x;
-  x = fmaf(x0, c, -y * s);
-  y = fmaf(x0, s, y * c);
+// Two values of a unit as floats, and back, rounded once.
+template <typename T, int VEC>
+__device__ __forceinline__ float2 rot_get2(const RotUnit<T, VEC>& u, int j) {
+  return make_float2(to_f32(u.x[j]), to_f32(u.x[j + 1]));
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void rot_set2(RotUnit<T, VEC>& u, int j, float2 x) {
+  if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(u.x + j) = __float22bfloat162_rn(x);
+  else u.x[j] = x.x, u.x[j + 1] = x.y;
 }
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_constant__ RotArgs a) {
-  extern __shared__ float rot_smem[];  // [block_tokens][half] cosines, then sines
+// Row e of a block: head h of the queries, the keys or the values of its token t.
+struct RotRow {
+  int t, h;
+  bool is_q, is_v;
+  __device__ __forceinline__ RotRow(const RotArgs& a, int e, int rows) {
+    t = (unsigned)e / (unsigned)rows;
+    const int r = e - t * rows;
+    is_q = r < a.heads;
+    is_v = r >= a.heads + a.kv_heads;
+    h = is_q ? r : is_v ? r - a.heads - a.kv_heads : r - a.heads;
+  }
+  __device__ __forceinline__ const LaTensor& of(const RotArgs& a) const { return is_q ? a.q : is_v ? a.v : a.k; }
+};
+
+// The pairs of an item turned, `left` of them and those behind.
+template <typename T, int VEC, bool INTER>
+__device__ __forceinline__ void rot_turn(RotUnit<T, VEC>& y0, RotUnit<T, VEC>& y1, const float* c, const float* s, int left) {
+  if constexpr (VEC == 1) {
+    // the two units are the pair
+    const float p = to_f32(y0.x[0]), q = to_f32(y1.x[0]);
+    rot_set(y0.x[0], fmaf(p, c[0], -q * s[0])), rot_set(y1.x[0], fmaf(p, s[0], q * c[0]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) {
+      const float4 c4 = *reinterpret_cast<const float4*>(c + j), s4 = *reinterpret_cast<const float4*>(s + j);
+      const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+      if constexpr (!INTER) {
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const float2 p = rot_get2(y0, j + k), q = rot_get2(y1, j + k);
+          rot_set2(y0, j + k, make_float2(fmaf(p.x, cs[k], -q.x * sn[k]), fmaf(p.y, cs[k + 1], -q.y * sn[k + 1])));
+          rot_set2(y1, j + k, make_float2(fmaf(p.x, sn[k], q.x * cs[k]), fmaf(p.y, sn[k + 1], q.y * cs[k + 1])));
+        }
+      } else {
+        // pair j of the item: values 2 j and 2 j + 1 of its two units, some of them behind the last pair
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (j + k >= left) continue;
+          RotUnit<T, VEC>& y = 2 * (j + k) < VEC ? y0 : y1;
+          const float2 p = rot_get2(y, 2 * (j + k) % VEC);
+          rot_set2(y, 2 * (j + k) % VEC, make_float2(fmaf(p.x, cs[k], -p.y * sn[k]), fmaf(p.x, sn[k], p.y * cs[k])));
+        }
+      }
+    }
+  }
+}
+
+// An item is two units of a row and the VEC pairs i VEC .. i VEC + VEC - 1: unit i of each half
+// of what is rotated, or (interleaved, and what is not rotated) neighbours 2 i and 2 i + 1.  A
+// thread keeps its item and goes from row to row with it.
+template <typename T, int VEC, bool INTER>
+__global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const __grid_constant__ RotArgs a) {
+  extern __shared__ __align__(16) float rot_smem[];  // [block_tokens][half] cosines, then sines (half made up to VEC)
+  __shared__ int64_t places[2][kRotTokens];          // the tokens' places in the pools, in elements; -1: none
   const int64_t b = blockIdx.x / a.blocks;
   const int t0 = (int)(blockIdx.x % a.blocks) * a.block_tokens;
   int end = a.tokens;
@@ -86,90 +145,60 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_consta
   const int start = a.starts ? a.starts[b] : 0;
   const int n = end - t0 < a.block_tokens ? end - t0 : a.block_tokens;
   if (n <= 0) return;
-  float *cosines = rot_smem, *sines = rot_smem + a.block_tokens * a.half;
-  for (int i = threadIdx.x; i < n * a.half; i += kRotThreads) {
-    const int t = i / a.half;
-    const double x = (double)((int64_t)start + t0 + t) * (double)a.inv_freq[i - t * a.half];
-    // x - 2 pi k, 2 pi in two doubles
-    const double k = rint(x * 0.15915494309189535);
-    double c, s;
-    sincos(fma(k, -2.4492935982947064e-16, fma(k, -6.283185307179586, x)), &s, &c);
-    cosines[i] = (float)c;
-    sines[i] = a.inverse ? -(float)s : (float)s;
+  const int width = (a.half + VEC - 1) / VEC * VEC;
+  float *cosines = rot_smem, *sines = rot_smem + a.block_tokens * width;
+  for (int e = threadIdx.x; e < n * width; e += kRotThreads) {
+    const int t = e / width, i = e - t * width;
+    if (i >= a.half) continue;
+    double c, s;  // in half turns; a double keeps 2^-52 of the angle
+    sincospi((double)((int64_t)start + t0 + t) * (double)a.inv_freq[i] * 0.3183098861837907, &s, &c);
+    cosines[e] = (float)c;
+    sines[e] = a.inverse ? -(float)s : (float)s;
+  }
+  if (a.pages.table && threadIdx.x < n) {
+    const int64_t pos = (int64_t)start + t0 + threadIdx.x, page = start < 0 ? -1 : wa_page_of(a.pages, b, pos);
+    const int64_t at = page < 0 ? 0 : pos % a.pages.page_size;
+    places[0][threadIdx.x] = page < 0 ? -1 : page * a.pages.k.sb + at * a.pages.k.st;
+    places[1][threadIdx.x] = page < 0 ? -1 : page * a.pages.v.sb + at * a.pages.v.st;
   }
   __syncthreads();
-  const int units = a.d / VEC, items = (units + 1) / 2;  // an item: two units
-  const int half_units = a.interleaved ? 0 : a.half / VEC;
-  const int rows = a.heads + (a.v.ptr ? 2 : 1) * a.kv_heads;
-  const int64_t bt0 = b * a.tokens + t0;
-  for (int e = threadIdx.x; e < n * rows * items; e += kRotThreads) {
-    const int r = e / items, i = e - r * items, t = r / rows, h = r - t * rows;
-    const bool is_q = h < a.heads, is_v = h >= a.heads + a.kv_heads;
-    const int hx = is_q ? h : is_v ? h - a.heads - a.kv_heads : h - a.heads;
-    const LaTensor& x = is_q ? a.q : is_v ? a.v : a.k;
-    // the units of this item: a pair of the two halves, or neighbours
-    const bool halves = !is_v && i < half_units;
-    const int first = halves ? i : 2 * i;
-    const int c0 = first * VEC, c1 = halves ? c0 + a.half : c0 + VEC;
-    const T* from = reinterpret_cast<const T*>(la_row(x, b, t0 + t, hx, sizeof(T)));
-    RotUnit<T, VEC> y0, y1;
-    const bool two = c1 < a.d;
-    if (!la_inside(x, reinterpret_cast<const char*>(from + c0), VEC, sizeof(T)) ||
-        (two && !la_inside(x, reinterpret_cast<const char*>(from + c1), VEC, sizeof(T))))
-      continue;
-    rot_load<T, VEC>(y0, from + c0);
-    if (two) rot_load<T, VEC>(y1, from + c1);
-    const float *c = cosines + t * a.half, *s = sines + t * a.half;
-    if (halves) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float p = to_f32(y0.x[j]), q = to_f32(y1.x[j]);
-        rot_turn(p, q, c[c0 + j], s[c0 + j]);
-        rot_set(y0.x[j], p), rot_set(y1.x[j], q);
+  const int units = a.d / VEC, items = (units + 1) / 2;
+  const int lanes = items < kRotThreads ? kRotThreads / items : 1;  // rows at once
+  const int row0 = lanes > 1 ? threadIdx.x / items : 0;
+  if (row0 >= lanes) return;
+  const int rows = a.heads + (a.v.ptr ? 2 : 1) * a.kv_heads, total = n * rows;  // rows of a token, of the block
+  const int64_t all = a.batch * a.tokens, bt0 = b * a.tokens + t0;
+  for (int i = threadIdx.x - row0 * items; i < items; i += kRotThreads) {
+    const bool turned = i * VEC < a.half, halves = !INTER && turned;
+    for (int e = row0; e < total; e += lanes) {
+      const RotRow w(a, e, rows);
+      const bool pairs = halves && !w.is_v;
+      const int c0 = (pairs ? i : 2 * i) * VEC, c1 = pairs ? c0 + a.half : c0 + VEC;
+      const bool two = c1 < a.d;
+      const T* from = reinterpret_cast<const T*>(la_row(w.of(a), b, t0 + w.t, w.h, sizeof(T)));
+      RotUnit<T, VEC> y0, y1;
+      if (la_inside(w.of(a), reinterpret_cast<const char*>(from + c0), VEC, sizeof(T))) rot_load<T, VEC>(y0, from + c0);
+      if (two && la_inside(w.of(a), reinterpret_cast<const char*>(from + c1), VEC, sizeof(T))) rot_load<T, VEC>(y1, from + c1);
+      if (turned && !w.is_v) {
+        const int at = w.t * width + i * VEC;
+        rot_turn<T, VEC, INTER>(y0, y1, cosines + at, sines + at, a.half - i * VEC);
       }
-    } else if (a.interleaved && !is_v) {
-      if constexpr (VEC == 1) {
-        // one value a unit: the two units of the item are the pair
-        if (two && c1 < 2 * a.half) {
-          float p = to_f32(y0.x[0]), q = to_f32(y1.x[0]);
-          rot_turn(p, q, c[c0 / 2], s[c0 / 2]);
-          rot_set(y0.x[0], p), rot_set(y1.x[0], q);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; j += 2) {
-          if (c0 + j < 2 * a.half) {
-            float p = to_f32(y0.x[j]), q = to_f32(y0.x[j + 1]);
-            rot_turn(p, q, c[(c0 + j) / 2], s[(c0 + j) / 2]);
-            rot_set(y0.x[j], p), rot_set(y0.x[j + 1], q);
-          }
-          if (two && c1 + j < 2 * a.half) {
-            float p = to_f32(y1.x[j]), q = to_f32(y1.x[j + 1]);
-            rot_turn(p, q, c[(c1 + j) / 2], s[(c1 + j) / 2]);
-            rot_set(y1.x[j], p), rot_set(y1.x[j + 1], q);
-          }
-        }
+      const auto put = [&](T* to) {
+        rot_store<T, VEC>(to + c0, y0);
+        if (two) rot_store<T, VEC>(to + c1, y1);
+      };
+      if (w.is_q) {
+        const int64_t at = ((bt0 + w.t) * a.heads + w.h) * a.d;
+        if (in_range(at, a.d, all * a.heads * a.d)) put(static_cast<T*>(a.q_out) + at);
+        continue;
       }
-    }
-    const auto put = [&](T* to) {
-      rot_store<T, VEC>(to + c0, y0);
-      if (two) rot_store<T, VEC>(to + c1, y1);
-    };
-    const int64_t bt = bt0 + t, all = a.batch * a.tokens;
-    if (is_q) {
-      const int64_t at = (bt * a.heads + hx) * a.d;
-      if (in_range(at, a.d, all * a.heads * a.d)) put(static_cast<T*>(a.q_out) + at);
-      continue;
-    }
-    if (!is_v && a.k_out) {
-      const int64_t at = (bt * a.kv_heads + hx) * a.d;
-      if (in_range(at, a.d, all * a.kv_heads * a.d)) put(static_cast<T*>(a.k_out) + at);
-    }
-    if (a.pages.table && start >= 0) {
-      const int64_t pos = (int64_t)start + t0 + t, page = wa_page_of(a.pages, b, pos);
-      const LaTensor& to = is_v ? a.pages.v : a.pages.k;
-      if (page >= 0) {
-        const char* at = la_row(to, page, pos % a.pages.page_size, hx, sizeof(T));
+      if (!w.is_v && a.k_out) {
+        const int64_t at = ((bt0 + w.t) * a.kv_heads + w.h) * a.d;
+        if (in_range(at, a.d, all * a.kv_heads * a.d)) put(static_cast<T*>(a.k_out) + at);
+      }
+      if (a.pages.table && places[w.is_v][w.t] >= 0) {
+        const LaTensor& to = w.is_v ? a.pages.v : a.pages.k;
+        const char* at = static_cast<const char*>(to.ptr) + (places[w.is_v][w.t] + (int64_t)w.h * to.sh) * (int64_t)sizeof(T);
         if (la_inside(to, at, a.d, sizeof(T))) put(reinterpret_cast<T*>(const_cast<char*>(at)));
       }
     }
