@@ -24,37 +24,47 @@
 
 namespace ssscan {
 
-// 64 columns of 32 rows from tensor memory, times `by`, as bf16 through a warp's place in
-// shared memory to whole rows: row r is token t0 + r, written where that is below `end`
-// (`out` has `left` elements).
-template <int COLS>
+// COLS columns of 32 rows from tensor memory, times `by`, as bf16 through a warp's place in
+// shared memory, STEP columns at a time, so that a row's 32 bytes or more go out together: row r
+// is token t0 + r, written where that is below `end` (`out` has `left` elements).  STEP 0:
+// without that place, every thread its own row, 16 bytes at a time.
+template <int COLS, int STEP>
 __device__ __forceinline__ void wt_put_rows(char* place, uint32_t tmem_from, __nv_bfloat16* out, int64_t left,
                                             int64_t row_stride, int t0, int end, int col0, int d, float by, int lane) {
+  constexpr int WIDE = STEP == 0 ? COLS : STEP, UNITS = WIDE / 8, ROWS = STEP > 0 ? 32 / UNITS : 1, kRow = STEP * 2;
 #pragma unroll
-  for (int c = 0; c < COLS; c += 32) {
-    uint32_t o[32];
-    tmem_ld32(o, tmem_from + c);
-    tmem_wait_ld(o);
+  for (int c = 0; c < COLS; c += WIDE) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      uint4 y;
-      y.x = to_bf16x2(__uint_as_float(o[8 * u]) * by, __uint_as_float(o[8 * u + 1]) * by);
-      y.y = to_bf16x2(__uint_as_float(o[8 * u + 2]) * by, __uint_as_float(o[8 * u + 3]) * by);
-      y.z = to_bf16x2(__uint_as_float(o[8 * u + 4]) * by, __uint_as_float(o[8 * u + 5]) * by);
-      y.w = to_bf16x2(__uint_as_float(o[8 * u + 6]) * by, __uint_as_float(o[8 * u + 7]) * by);
-      *reinterpret_cast<uint4*>(place + tile_unit(lane, c / 8 + u)) = y;
+    for (int i = 0; i < WIDE; i += 16) {
+      uint32_t o[16];
+      tmem_ld(o, tmem_from + c + i);
+      tmem_wait_ld(o);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint4 y;
+        y.x = to_bf16x2(__uint_as_float(o[8 * u]) * by, __uint_as_float(o[8 * u + 1]) * by);
+        y.y = to_bf16x2(__uint_as_float(o[8 * u + 2]) * by, __uint_as_float(o[8 * u + 3]) * by);
+        y.z = to_bf16x2(__uint_as_float(o[8 * u + 4]) * by, __uint_as_float(o[8 * u + 5]) * by);
+        y.w = to_bf16x2(__uint_as_float(o[8 * u + 6]) * by, __uint_as_float(o[8 * u + 7]) * by);
+        if constexpr (STEP > 0) {
+          *reinterpret_cast<uint4*>(place + lane * kRow + (((i / 8 + u) ^ lane) % UNITS) * 16) = y;
+        } else {
+          const int64_t at = (int64_t)(t0 + lane) * row_stride + col0 + i + 8 * u;
+          if (t0 + lane < end && col0 + i + 8 * u < d && in_range(at, 8, left)) *reinterpret_cast<uint4*>(out + at) = y;
+        }
+      }
     }
-  }
-  __syncwarp();
-  constexpr int UNITS = COLS / 8, ROWS = 32 / UNITS;
+    if (STEP == 0) continue;
+    __syncwarp();
 #pragma unroll
-  for (int e = 0; e < 32 / ROWS; ++e) {
-    const int r = e * ROWS + lane / UNITS, col = col0 + lane % UNITS * 8;
-    if (t0 + r < end && col < d && in_range((int64_t)(t0 + r) * row_stride + col, 8, left))
-      *reinterpret_cast<uint4*>(out + (int64_t)(t0 + r) * row_stride + col) =
-          *reinterpret_cast<const uint4*>(place + tile_unit(r, lane % UNITS));
+    for (int e = 0; e < UNITS; ++e) {
+      const int r = e * ROWS + lane / UNITS, u = lane % UNITS, col = col0 + c + u * 8;
+      if (t0 + r < end && col < d && in_range((int64_t)(t0 + r) * row_stride + col, 8, left))
+        *reinterpret_cast<uint4*>(out + (int64_t)(t0 + r) * row_stride + col) =
+            *reinterpret_cast<const uint4*>(place + r * kRow + ((u ^ r) % UNITS) * 16);
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 // Bits from `lo` on below `hi` of the columns c .. c + 31.
@@ -68,15 +78,17 @@ __device__ __forceinline__ uint32_t wt_bits(int lo, int hi, int c) {
 template <int DP>
 struct WtKvCfg {
   static constexpr int kTile = DP / 64 * (int)kWtBlock;
-  static constexpr int kRing = DP == 64 ? 3 : 2;  // places for queries, and as many for do
-  static constexpr int kK = 0, kV = kTile, kQ = 2 * kTile, kG = kQ + kRing * kTile, kStat = kG + kRing * kTile;
+  // Places for queries and for do.  A query tile is held longer: from the next tile's S, issued
+  // ahead, to its dK (with two places it was waited for).
+  static constexpr int RQ = DP == 64 ? 4 : 3, RG = DP == 64 ? 4 : 2;
+  static constexpr int kK = 0, kV = kTile, kQ = 2 * kTile, kG = kQ + RQ * kTile, kStat = kG + RG * kTile;
   static constexpr int kStatBytes = 2 * kWtRows * 4;  // lse and delta of a tile's queries
   static constexpr int kBars = kStat + 2 * kStatBytes;
-  static constexpr int kNumBars = 4 * kRing + 12;
+  static constexpr int kNumBars = 2 * (RQ + RG) + 12;
   static constexpr int kSmem = kBars + kNumBars * 8 + 16;
   static constexpr int cS = 0, cP = 128, cDv = 256, cDk = 256 + DP;
   static constexpr int kThreads = 384;
-  static_assert(kSmem <= 232448 && 2 * kRing * kTile >= 8 * 32 * (int)kTileRow, "shared memory");
+  static_assert(kSmem <= 232448 && RQ * kTile >= 8 * 32 * (int)kTileRow, "shared memory");
 };
 constexpr int kWtStatWarp = 10;
 
@@ -88,14 +100,14 @@ winattn_dkv_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
   const uint32_t base = smem_u32(smem), bars = base + CF::kBars;
   const auto bar = [&](int i) { return bars + (uint32_t)i * 8; };
   const auto full_q = [&](int i) { return bar(i); };
-  const auto empty_q = [&](int i) { return bar(CF::kRing + i); };
-  const auto full_g = [&](int i) { return bar(2 * CF::kRing + i); };
-  const auto empty_g = [&](int i) { return bar(3 * CF::kRing + i); };
-  const auto full_st = [&](int i) { return bar(4 * CF::kRing + i); };
-  const auto empty_st = [&](int i) { return bar(4 * CF::kRing + 2 + i); };
-  const uint32_t b_kv = bar(4 * CF::kRing + 4), b_s = bar(4 * CF::kRing + 5), b_p = bar(4 * CF::kRing + 6),
-                 b_dp = bar(4 * CF::kRing + 7), b_ds = bar(4 * CF::kRing + 8), b_end = bar(4 * CF::kRing + 9),
-                 b_raw = bar(4 * CF::kRing + 10);
+  const auto empty_q = [&](int i) { return bar(CF::RQ + i); };
+  const auto full_g = [&](int i) { return bar(2 * CF::RQ + i); };
+  const auto empty_g = [&](int i) { return bar(2 * CF::RQ + CF::RG + i); };
+  constexpr int kRest = 2 * (CF::RQ + CF::RG);
+  const auto full_st = [&](int i) { return bar(kRest + i); };
+  const auto empty_st = [&](int i) { return bar(kRest + 2 + i); };
+  const uint32_t b_kv = bar(kRest + 4), b_s = bar(kRest + 5), b_p = bar(kRest + 6), b_dp = bar(kRest + 7),
+                 b_ds = bar(kRest + 8), b_end = bar(kRest + 9), b_raw = bar(kRest + 10);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + CF::kNumBars * 8);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
 
@@ -134,21 +146,19 @@ winattn_dkv_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
         tma_load_block(base + CF::kV + j * kWtBlock, &maps.v, b_kv, j * 64, c0, hk, b);
       }
     }
-    LaRing<CF::kRing> ring;
+    LaRing<CF::RQ> rq;
+    LaRing<CF::RG> rg;
     bool gone = false;  // a place was not free in time: no further copies
-    bool odd = false;   // (and the queries of the last place came without their do)
     uint32_t raw = 0;
     for (int i = 0; i < count && !gone; ++i) {
       const int r0 = rows(i), h = head(i);
       // TMA clips at the tensor's end, not at a row's length
       const bool ragged = r0 + kWtRows > len && len < a.seqlen;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (!gone && ring.used()) gone = !la_wait(g ? empty_g(ring.i) : empty_q(ring.i), ring.empty(), dead);
-        if (gone) continue;
-        const int at = (g ? CF::kG : CF::kQ) + ring.i * CF::kTile;
-        const uint32_t full = g ? full_g(ring.i) : full_q(ring.i);
-        if (lane == 0) wt_load<DP>(base + at, g ? &maps.g : &maps.q, ragged ? b_raw : full, r0, h, b);
+      const auto tile = [&](auto& ring, int at, const CUtensorMap* map, uint32_t full, uint32_t empty) {
+        if (!gone && ring.used()) gone = !la_wait(empty, ring.empty(), dead);
+        if (gone) return;
+        at += ring.i * CF::kTile;
+        if (lane == 0) wt_load<DP>(base + at, map, ragged ? b_raw : full, r0, h, b);
         __syncwarp();
         if (ragged) {
           la_wait_own(b_raw, raw);
@@ -156,17 +166,21 @@ winattn_dkv_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
           wt_clear<DP>(smem + at, len - r0, lane);
           if (lane == 0) la_arrive(full);
         }
-        odd = g == 0;
-      }
-      if (!gone) ring.next();
+        ring.next();
+      };
+      tile(rq, CF::kQ, &maps.q, full_q(rq.i), empty_q(rq.i));
+      tile(rg, CF::kG, &maps.g, full_g(rg.i), empty_g(rg.i));
     }
     // the last copies land before the end, also where those that they are for have given up
+    const auto land = [&](auto& ring, int count, const auto& full) {
 #pragma unroll 1
-    for (int i = 0; i < CF::kRing; ++i) {
-      const uint32_t fills = ring.turn + (i < ring.i ? 1 : 0);
-      if (fills > 0) la_wait_own(full_q(i), (fills - 1) & 1), la_wait_own(full_g(i), (fills - 1) & 1);
-    }
-    if (odd) la_wait_own(full_q(ring.i), ring.full());
+      for (int i = 0; i < count; ++i) {
+        const uint32_t fills = ring.turn + (i < ring.i ? 1 : 0);
+        if (fills > 0) la_wait_own(full(i), (fills - 1) & 1);
+      }
+    };
+    land(rq, CF::RQ, full_q);
+    land(rg, CF::RG, full_g);
     if (count > 0) la_wait_own(b_kv, 0);
   } else if (warp == kWtMmaWarp) {
     // ---- products
@@ -174,7 +188,8 @@ winattn_dkv_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
     constexpr int kUnits = kWtBlock >> 4;
     const uint32_t k = tile_desc(base + CF::kK, 0), v = tile_desc(base + CF::kV, 0);
     constexpr uint32_t kScores = mma_idesc(128, kWtRows, false, false), kSums = mma_idesc(128, DP, false, true);
-    LaRing<CF::kRing> ring;
+    LaRing<CF::RQ> rq;
+    LaRing<CF::RG> rg;
     // S^T = K Q^T or dP^T = V dO^T
     const auto scores = [&](uint32_t to, uint32_t x, int at) {
       const uint32_t y = tile_desc(base + at, 0);
@@ -202,24 +217,24 @@ winattn_dkv_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
     }
     for (int i = 0; i < count; ++i) {
       const bool more = i + 1 < count;
-      const int at = ring.i;
-      ring.next();
-      if (more) la_wait(full_q(ring.i), ring.full(), dead);
+      const int q_at = rq.i, g_at = rg.i;
+      rq.next(), rg.next();
+      if (more) la_wait(full_q(rq.i), rq.full(), dead);
       la_wait(b_p, i & 1, dead);
       tc5_fence_after();
       if (leader) {
-        sums(CF::cDv, CF::cS, CF::kG + at * CF::kTile, i > 0);
-        mma_commit(empty_g(at));
-        if (more) scores(CF::cS, k, CF::kQ + ring.i * CF::kTile), mma_commit(b_s);
+        sums(CF::cDv, CF::cS, CF::kG + g_at * CF::kTile, i > 0);
+        mma_commit(empty_g(g_at));
+        if (more) scores(CF::cS, k, CF::kQ + rq.i * CF::kTile), mma_commit(b_s);
       }
       __syncwarp();
-      if (more) la_wait(full_g(ring.i), ring.full(), dead);
+      if (more) la_wait(full_g(rg.i), rg.full(), dead);
       la_wait(b_ds, i & 1, dead);
       tc5_fence_after();
       if (leader) {
-        sums(CF::cDk, CF::cP, CF::kQ + at * CF::kTile, i > 0);
-        mma_commit(empty_q(at));
-        if (more) scores(CF::cP, v, CF::kG + ring.i * CF::kTile), mma_commit(b_dp);
+        sums(CF::cDk, CF::cP, CF::kQ + q_at * CF::kTile, i > 0);
+        mma_commit(empty_q(q_at));
+        if (more) scores(CF::cP, v, CF::kG + rg.i * CF::kTile), mma_commit(b_dp);
       }
       __syncwarp();
     }
@@ -342,7 +357,7 @@ winattn_dkv_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(side ? a.dk : a.dv) + at;
 #pragma unroll
       for (int c = 0; c < DP; c += 64)
-        wt_put_rows<64>(smem + CF::kQ + warp * 32 * kTileRow, from + c, out, (int64_t)bh_all * a.seqlen * a.d - at,
+        wt_put_rows<64, 64>(smem + CF::kQ + warp * 32 * kTileRow, from + c, out, (int64_t)bh_all * a.seqlen * a.d - at,
                         (int64_t)kv_heads * a.d, key - lane, len, c, a.d, scale, lane);
     }
   }
@@ -357,11 +372,13 @@ winattn_dkv_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
 template <int DP>
 struct WtDqCfg {
   static constexpr int kTile = DP / 64 * (int)kWtBlock;
-  static constexpr int kRing = DP == 64 ? 4 : 2;  // places for keys, and as many for values
-  static constexpr int kQ = 0, kG = kTile, kK = 2 * kTile, kV = kK + kRing * kTile, kOut = kV + kRing * kTile;
-  static constexpr int kStage = 32 * (int)kTileRow;
+  // Places for keys and for values: keys are held longer, from S to dQ (with two places they
+  // were waited for, half of the time).
+  static constexpr int RK = DP == 64 ? 4 : 3, RV = DP == 64 ? 4 : 2;
+  static constexpr int kQ = 0, kG = kTile, kK = 2 * kTile, kV = kK + RK * kTile, kOut = kV + RV * kTile;
+  static constexpr int kOutCols = DP == 64 ? 32 : 0, kStage = 32 * kOutCols * 2;  // written out at a time, where there is room
   static constexpr int kBars = kOut + 8 * kStage;
-  static constexpr int kNumBars = 4 * kRing + 10;
+  static constexpr int kNumBars = 2 * (RK + RV) + 10;
   static constexpr int kSmem = kBars + kNumBars * 8 + 16;
   static constexpr int cS = 0, cP = 256, cDq = 384;  // S in two places
   static constexpr int kThreads = 384;
@@ -393,14 +410,15 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
   const uint32_t base = smem_u32(smem), bars = base + CF::kBars;
   const auto bar = [&](int i) { return bars + (uint32_t)i * 8; };
   const auto full_k = [&](int i) { return bar(i); };
-  const auto empty_k = [&](int i) { return bar(CF::kRing + i); };
-  const auto full_v = [&](int i) { return bar(2 * CF::kRing + i); };
-  const auto empty_v = [&](int i) { return bar(3 * CF::kRing + i); };
-  const uint32_t b_q = bar(4 * CF::kRing), b_q_free = bar(4 * CF::kRing + 1);  // queries and do are there, were used
-  const uint32_t b_dp = bar(4 * CF::kRing + 2), b_dp_free = bar(4 * CF::kRing + 3);  // S and dP are there, were read
-  const uint32_t b_ds = bar(4 * CF::kRing + 4);
-  const uint32_t b_o = bar(4 * CF::kRing + 5), b_o_free = bar(4 * CF::kRing + 6);  // dQ is complete, was read
-  const uint32_t b_end = bar(4 * CF::kRing + 7), b_raw = bar(4 * CF::kRing + 8);
+  const auto empty_k = [&](int i) { return bar(CF::RK + i); };
+  const auto full_v = [&](int i) { return bar(2 * CF::RK + i); };
+  const auto empty_v = [&](int i) { return bar(2 * CF::RK + CF::RV + i); };
+  constexpr int kRest = 2 * (CF::RK + CF::RV);
+  const uint32_t b_q = bar(kRest), b_q_free = bar(kRest + 1);  // queries and do are there, were used
+  const uint32_t b_dp = bar(kRest + 2), b_dp_free = bar(kRest + 3);  // S and dP are there, were read
+  const uint32_t b_ds = bar(kRest + 4);
+  const uint32_t b_o = bar(kRest + 5), b_o_free = bar(kRest + 6);  // dQ is complete, was read
+  const uint32_t b_end = bar(kRest + 7), b_raw = bar(kRest + 8);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + CF::kNumBars * 8);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
 
@@ -422,7 +440,8 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
 
   if (warp == kWtLoadWarp) {
     // ---- loader
-    LaRing<CF::kRing> ring;
+    LaRing<CF::RK> rk;
+    LaRing<CF::RV> rv;
     bool gone = false;  // a place was not free in time: no further copies
     uint32_t raw = 0, items = 0;
     for (int item = blockIdx.x; item < a.items && !gone; item += gridDim.x) {
@@ -441,46 +460,50 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
       ++items;
       for (int i = 0; i < w.keys.count; ++i) {
         const int c0 = w.keys.at(i) * kWtRows;
-        if (ring.used()) {
-          gone = !la_wait(empty_k(ring.i), ring.empty(), dead);
-          if (!gone) gone = !la_wait(empty_v(ring.i), ring.empty(), dead);
-        }
+        if (rk.used()) gone = !la_wait(empty_k(rk.i), rk.empty(), dead);
+        if (!gone && rv.used()) gone = !la_wait(empty_v(rv.i), rv.empty(), dead);
         if (gone) break;
         // TMA clips at the tensor's end, not at a row's length; zeros of dS do not take a NaN
         // out of dS K
         const bool ragged = c0 + kWtRows > w.len && w.len < a.seqlen;
+        const int k_to = CF::kK + rk.i * CF::kTile;
         if (lane == 0) {
-          wt_load<DP>(base + CF::kK + ring.i * CF::kTile, &maps.k, ragged ? b_raw : full_k(ring.i), c0, w.h / a.share, w.b);
-          wt_load<DP>(base + CF::kV + ring.i * CF::kTile, &maps.v, full_v(ring.i), c0, w.h / a.share, w.b);
+          wt_load<DP>(base + k_to, &maps.k, ragged ? b_raw : full_k(rk.i), c0, w.h / a.share, w.b);
+          wt_load<DP>(base + CF::kV + rv.i * CF::kTile, &maps.v, full_v(rv.i), c0, w.h / a.share, w.b);
         }
         __syncwarp();
         if (ragged) {
           la_wait_own(b_raw, raw);
           raw ^= 1;
-          wt_clear<DP>(smem + CF::kK + ring.i * CF::kTile, w.len - c0, lane);
-          if (lane == 0) la_arrive(full_k(ring.i));
+          wt_clear<DP>(smem + k_to, w.len - c0, lane);
+          if (lane == 0) la_arrive(full_k(rk.i));
         }
-        ring.next();
+        rk.next(), rv.next();
       }
     }
     // the last copies land before the end, also where those that they are for have given up
+    const auto land = [&](auto& ring, int count, const auto& full) {
 #pragma unroll 1
-    for (int i = 0; i < CF::kRing; ++i) {
-      const uint32_t fills = ring.turn + (i < ring.i ? 1 : 0);
-      if (fills > 0) la_wait_own(full_k(i), (fills - 1) & 1), la_wait_own(full_v(i), (fills - 1) & 1);
-    }
+      for (int i = 0; i < count; ++i) {
+        const uint32_t fills = ring.turn + (i < ring.i ? 1 : 0);
+        if (fills > 0) la_wait_own(full(i), (fills - 1) & 1);
+      }
+    };
+    land(rk, CF::RK, full_k);
+    land(rv, CF::RV, full_v);
     if (items > 0) la_wait_own(b_q, (items - 1) & 1);
   } else if (warp == kWtMmaWarp) {
     // ---- products
     const bool leader = elect_one();
     constexpr int kUnits = kWtBlock >> 4;
     const uint32_t q = tile_desc(base + CF::kQ, 0), g = tile_desc(base + CF::kG, 0);
-    LaRing<CF::kRing> ring;
+    LaRing<CF::RK> rk;
+    LaRing<CF::RV> rv;
     int n = 0, items = 0;  // tiles and items so far
     // S = Q K^T and dP = dO V^T of tile i, the n-th
-    const auto scores = [&](int i, int n, int at) {
+    const auto scores = [&](int i, int n, int k_at, int v_at) {
       const uint32_t idesc = mma_idesc(128, wa_columns(i, w.keys, a.sinks), false, false);
-      const uint32_t k = tile_desc(base + CF::kK + at * CF::kTile, 0), v = tile_desc(base + CF::kV + at * CF::kTile, 0);
+      const uint32_t k = tile_desc(base + CF::kK + k_at * CF::kTile, 0), v = tile_desc(base + CF::kV + v_at * CF::kTile, 0);
 #pragma unroll
       for (int s = 0; s < DP / 16; ++s) {
         const int off = (s / 4) * kUnits + (s % 4) * 2;
@@ -492,7 +515,7 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
         mma_ss(tmem + CF::cP, g + off, v + off, idesc, s > 0);
       }
       mma_commit(b_dp);
-      mma_commit(empty_v(at));
+      mma_commit(empty_v(v_at));
     };
     for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
       if (!wt_row_item(w, a, item)) continue;
@@ -500,14 +523,14 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
       int k_at = 0;
       for (int i = -1; i < w.keys.count; ++i) {
         const bool more = i + 1 < w.keys.count;
-        const int next = ring.i;
+        const int next = rk.i;
         if (more) {
-          la_wait(full_k(next), ring.full(), dead);
-          la_wait(full_v(next), ring.full(), dead);
+          la_wait(full_k(next), rk.full(), dead);
+          la_wait(full_v(rv.i), rv.full(), dead);
           if (n > 0) la_wait(b_dp_free, (n - 1) & 1, dead);  // the last tile's, this item's or not
           tc5_fence_after();
           if (leader) {
-            scores(i + 1, n, next);
+            scores(i + 1, n, next, rv.i);
             if (i + 2 == w.keys.count) mma_commit(b_q_free);
           }
           __syncwarp();
@@ -532,7 +555,7 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
         }
         if (more) {
           k_at = next;
-          ring.next();
+          rk.next(), rv.next();
           ++n;
         }
       }
@@ -548,14 +571,24 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
     const uint32_t p_at = tmem + lanes + CF::cP + side * 64;
     const float by = a.scale * kLog2e;
     const uint64_t by2 = pair(by, by);
-    int n = 0, items = 0;
-    for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
-      if (!wt_row_item(w, a, item)) continue;
+    int n = 0, items = 0, item = blockIdx.x;
+    float lse = 0.f, delta = 0.f;  // of the item at hand, asked for before the one before it is written out
+    const auto begin = [&]() {  // the next item that there is
+      for (; item < a.items; item += gridDim.x)
+        if (wt_row_item(w, a, item)) {
+          const int row = w.r0 + quad * 32 + lane;
+          const int64_t at = ((int64_t)w.b * a.heads + w.h) * a.seqlen + row;
+          const bool real = row < w.end && in_range(at, (int64_t)a.batch * a.heads * a.seqlen);
+          lse = real ? a.lse[at] : 0.f, delta = real ? a.delta[at] : 0.f;
+          item += gridDim.x;
+          return true;
+        }
+      return false;
+    };
+    bool more = begin();
+    while (more) {
       const int row = w.r0 + quad * 32 + lane;
-      const int64_t at = ((int64_t)w.b * a.heads + w.h) * a.seqlen + row;
-      const bool real = row < w.end && in_range(at, (int64_t)a.batch * a.heads * a.seqlen);
-      const float lse = real ? -a.lse[at] * kLog2e : 0.f, delta = real ? -a.delta[at] : 0.f;
-      const uint64_t lse2 = pair(lse, lse), delta2 = pair(delta, delta);
+      const uint64_t lse2 = pair(-lse * kLog2e, -lse * kLog2e), delta2 = pair(-delta, -delta);
 #pragma unroll 1
       for (int i = 0; i < w.keys.count; ++i, ++n) {
         const int c0 = w.keys.at(i) * kWtRows;
@@ -602,13 +635,16 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
         __syncwarp();
         if (lane == 0) la_arrive(b_ds);
       }
+      const WtRowItem done = w;
+      more = begin();
       la_wait(b_o, items & 1, dead);
       ++items;
       tc5_fence_after();
-      const int64_t first = ((int64_t)w.b * a.seqlen * a.heads + w.h) * a.d;
-      wt_put_rows<DP / 2>(smem + CF::kOut + warp * CF::kStage, tmem + lanes + CF::cDq + side * (DP / 2),
-                          static_cast<__nv_bfloat16*>(a.out) + first,
-                          (int64_t)a.batch * a.heads * a.seqlen * a.d - first, (int64_t)a.heads * a.d, w.r0 + quad * 32, w.end, side * (DP / 2), a.d, a.scale, lane);
+      const int64_t first = ((int64_t)done.b * a.seqlen * a.heads + done.h) * a.d;
+      wt_put_rows<DP / 2, CF::kOutCols>(smem + CF::kOut + warp * CF::kStage, tmem + lanes + CF::cDq + side * (DP / 2),
+                                        static_cast<__nv_bfloat16*>(a.out) + first,
+                                        (int64_t)a.batch * a.heads * a.seqlen * a.d - first, (int64_t)a.heads * a.d,
+                                        done.r0 + quad * 32, done.end, side * (DP / 2), a.d, a.scale, lane);
       tc5_fence_before();
       __syncwarp();
       if (lane == 0) la_arrive(b_o_free);
