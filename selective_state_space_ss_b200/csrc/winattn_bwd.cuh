@@ -416,9 +416,11 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
   constexpr int kRest = 2 * (CF::RK + CF::RV);
   const uint32_t b_q = bar(kRest), b_q_free = bar(kRest + 1);  // queries and do are there, were used
   const uint32_t b_dp = bar(kRest + 2), b_dp_free = bar(kRest + 3);  // S and dP are there, were read
-  const uint32_t b_ds = bar(kRest + 4);
-  const uint32_t b_o = bar(kRest + 5), b_o_free = bar(kRest + 6);  // dQ is complete, was read
-  const uint32_t b_end = bar(kRest + 7), b_raw = bar(kRest + 8);
+  // dS is there, of even and of odd tiles: the next tile's scores are issued before this one's
+  // dS is waited for, and a barrier that completes twice unseen looks as if it had not
+  const auto b_ds = [&](int n) { return bar(kRest + 4 + (n & 1)); };
+  const uint32_t b_o = bar(kRest + 6), b_o_free = bar(kRest + 7);  // dQ is complete, was read
+  const uint32_t b_end = bar(kRest + 8), b_raw = bar(kRest + 9);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + CF::kNumBars * 8);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
 
@@ -426,7 +428,8 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
   if (tid == 0) {
     for (int i = 0; i < CF::kNumBars; ++i) la_init(bar(i), 1);
     la_init(b_dp_free, 8);
-    la_init(b_ds, 8);
+    la_init(b_ds(0), 8);
+    la_init(b_ds(1), 8);
     la_init(b_o_free, 8);
     fence_mbar_init();
     *dead = 0;
@@ -538,7 +541,7 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
         if (i >= 0) {
           const int t = n - 1;  // of all tiles
           if (i == 0 && items > 0) la_wait(b_o_free, (items - 1) & 1, dead);
-          la_wait(b_ds, t & 1, dead);
+          la_wait(b_ds(t), (t / 2) & 1, dead);
           tc5_fence_after();
           if (leader) {
             const uint32_t k = tile_desc(base + CF::kK + k_at * CF::kTile, kWtBlock);
@@ -633,7 +636,7 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
         tmem_wait_st();
         tc5_fence_before();
         __syncwarp();
-        if (lane == 0) la_arrive(b_ds);
+        if (lane == 0) la_arrive(b_ds(n));
       }
       const WtRowItem done = w;
       more = begin();

@@ -17,9 +17,9 @@
 //
 // Roles: two warpgroups of softmax, a warp that loads (TMA, 128 x 64 blocks), one each that
 // issues A's and B's products (one warp for both was busy waiting for one of them while the
-// other's were due: 4200 cycles a pair of tiles).  S of the next tile is issued behind P V of this one, so that what a warpgroup
-// waits for (its next S) also tells that its last O is complete and may be scaled.  A block
-// stays on its SM and goes on with the next queries while the last O is written out.
+// other's were due: 4200 cycles a pair of tiles).  Where P is in S's place (heads wider than 64)
+// S of the next tile is issued behind P V of this one, so that what a warpgroup waits for (its
+// next S) also tells that its last O is complete and may be scaled.  A block stays on its SM and goes on with the next queries while the last O is written out.
 #pragma once
 
 #include <cuda.h>
@@ -118,9 +118,12 @@ struct WtFwdCfg {
   static constexpr int kRing = DP == 64 ? 8 : 4;  // places for tiles of K and V in turn
   static constexpr int kStage = 32 * (int)kTileRow;  // a softmax warp's 32 rows of 64 output columns
   static constexpr int kQ = 0, kKv = 2 * kTile, kOut = kKv + kRing * kTile, kBars = kOut + 8 * kStage;
-  static constexpr int kNumBars = 2 * kRing + 16;
+  static constexpr int kNumBars = 2 * kRing + 20;
   static constexpr int kSmem = kBars + kNumBars * 8 + 16;
-  static constexpr int cS = 0, cO = 2 * kWtRows;  // tensor memory: S (and P) of A and B, then O
+  // Tensor memory: S of A and B, then O, then (where there is room) P, which is in S's place
+  // otherwise.  With a place of its own the next S is formed while this one's P is.
+  static constexpr bool kApart = DP == 64;
+  static constexpr int cS = 0, cO = 2 * kWtRows, cP = kApart ? cO + 2 * DP : cS, kPStep = kApart ? 64 : kWtRows;
   static constexpr int kThreads = 384;
   // Registers a thread: 2 x 208 + 88 = 3 x 168 at launch.
   static constexpr int kSoftmaxRegs = 208, kAuxRegs = 88;
@@ -173,7 +176,9 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
   const auto b_p = [&](int x, int half) { return bar(2 * CF::kRing + 6 + 2 * x + half); };  // P is there
   const auto b_o = [&](int x) { return bar(2 * CF::kRing + 10 + x); };      // O is complete
   const auto b_o_free = [&](int x) { return bar(2 * CF::kRing + 12 + x); }; // and was read
-  const uint32_t b_end = bar(2 * CF::kRing + 14), b_raw = bar(2 * CF::kRing + 15);
+  const auto b_s_free = [&](int x) { return bar(2 * CF::kRing + 14 + x); }; // (P apart) S was read
+  const auto b_pv = [&](int x) { return bar(2 * CF::kRing + 16 + x); };     // (P apart) P was used
+  const uint32_t b_end = bar(2 * CF::kRing + 18), b_raw = bar(2 * CF::kRing + 19);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + CF::kBars + CF::kNumBars * 8);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
 
@@ -183,6 +188,7 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
     for (int x = 0; x < 2; ++x) {
       for (int half = 0; half < 2; ++half) la_init(b_p(x, half), 4);
       la_init(b_o_free(x), 4);
+      la_init(b_s_free(x), 4);
     }
     for (int i = 0; i < CF::kRing; ++i) la_init(empty(i), 2);
     la_init(b_end, 2);
@@ -251,7 +257,7 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
       constexpr int kUnits = kWtBlock >> 4;
       const uint32_t q = tile_desc(base + CF::kQ + x * CF::kTile, 0);
       LaRing<CF::kRing> ring;
-      int done = 0, items = 0;  // tiles of P taken, items so far
+      int scored = 0, done = 0, items = 0;  // tiles of S formed, of P taken, items so far
       for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
         if (!wt_item(w, a, item)) continue;
         const bool mine = w.to(x) > w.from(x);
@@ -259,11 +265,32 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
         int v_at = 0;
         uint32_t v_full = 0;
         bool add = false;  // O's first product does not
+        const auto scores = [&](int i, int k_at) {  // of tile i, and its keys given back
+          const bool needed = w.needs(x, i, a);
+          if (CF::kApart && needed && scored > 0) la_wait(b_s_free(x), (scored - 1) & 1, dead);
+          if (needed) ++scored;
+          tc5_fence_after();
+          if (leader) {
+            if (needed) {
+              const uint32_t k = tile_desc(base + CF::kKv + k_at * CF::kTile, 0);
+              const uint32_t idesc = mma_idesc(128, wa_columns(i, w.keys, a.sinks), false, false);
+#pragma unroll
+              for (int s = 0; s < DP / 16; ++s) {
+                const int off = (s / 4) * kUnits + (s % 4) * 2;
+                mma_ss(tmem + CF::cS + x * kWtRows, q + off, k + off, idesc, s > 0);
+              }
+              mma_commit(b_s(x));
+              if (i == w.last(x)) mma_commit(b_q_free(x));
+            }
+            mma_commit(empty(k_at));
+          }
+          __syncwarp();
+        };
         for (int i = -1; i < w.keys.count; ++i) {
           const bool more = i + 1 < w.keys.count;
           const int k_at = ring.i;
-          const uint32_t k_full = ring.full();
-          if (more) la_wait(full(k_at), k_full, dead);
+          if (more) la_wait(full(k_at), ring.full(), dead);
+          if (CF::kApart && more) scores(i + 1, k_at);
           if (i >= 0) {
             la_wait(full(v_at), v_full, dead);
             if (w.needs(x, i, a)) {
@@ -278,35 +305,21 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
 #pragma unroll
                   for (int s = half * 4; s < half * 4 + 4; ++s)
                     if (s < steps)
-                      mma_ts(tmem + CF::cO + x * DP, tmem + CF::cS + x * kWtRows + s * 8, v + s * (16 * kTileRow >> 4),
-                             mma_idesc(128, DP, false, true), add || s > 0);
+                      mma_ts(tmem + CF::cO + x * DP, tmem + CF::cP + x * CF::kPStep + s * 8,
+                             v + s * (16 * kTileRow >> 4), mma_idesc(128, DP, false, true), add || s > 0);
                 }
                 __syncwarp();
               }
               add = true;
               ++done;
+              if (CF::kApart && leader) mma_commit(b_pv(x));
               if (leader && i == w.last(x)) mma_commit(b_o(x));
             }
             if (leader) mma_commit(empty(v_at));
             __syncwarp();
           }
           if (more) {
-            tc5_fence_after();
-            if (leader) {
-              if (w.needs(x, i + 1, a)) {
-                const uint32_t k = tile_desc(base + CF::kKv + k_at * CF::kTile, 0);
-                const uint32_t idesc = mma_idesc(128, wa_columns(i + 1, w.keys, a.sinks), false, false);
-#pragma unroll
-                for (int s = 0; s < DP / 16; ++s) {
-                  const int off = (s / 4) * kUnits + (s % 4) * 2;
-                  mma_ss(tmem + CF::cS + x * kWtRows, q + off, k + off, idesc, s > 0);
-                }
-                mma_commit(b_s(x));
-                if (i + 1 == w.last(x)) mma_commit(b_q_free(x));
-              }
-              mma_commit(empty(k_at));
-            }
-            __syncwarp();
+            if (!CF::kApart) scores(i + 1, k_at);
             ring.next();
             v_at = ring.i, v_full = ring.full();
             ring.next();
@@ -324,6 +337,7 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
     const int x = warp / 4, quad = warp % 4;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t s_at = tmem + lanes + CF::cS + x * kWtRows, o_at = tmem + lanes + CF::cO + x * DP;
+    const uint32_t p_at = tmem + lanes + CF::cP + x * CF::kPStep;
     const float by = a.scale * kLog2e, room = 8.f / by;
     const int64_t bh_all = (int64_t)a.batch * a.heads;
     int n = 0, items = 0;  // tiles and items so far
@@ -349,6 +363,11 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
         for (int c = 0; c < CHUNKS; ++c) tmem_ld32(s[c], s_at + 32 * c);
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) tmem_wait_ld(s[c]);
+        if (CF::kApart) {
+          tc5_fence_before();
+          __syncwarp();
+          if (lane == 0) la_arrive(b_s_free(x));
+        }
         if (CHUNKS < 4 || !wa_all_seen(from, to, c0, c0 + kWtRows, a.window, a.sinks)) {
           // columns of this row: up to `upto`, from `near` on or below `far`, as bits
           const int upto = row - c0, far = a.sinks - c0;
@@ -370,6 +389,10 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
           for (int j = 0; j < 32; j += 2)
             m[j / 2 % 4] = fmaxf(fmaxf(m[j / 2 % 4], __uint_as_float(s[c][j])), __uint_as_float(s[c][j + 1]));
         const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        if (CF::kApart && n > 0) {  // O has all before, P's place is free
+          la_wait(b_pv(x), (n - 1) & 1, dead);
+          tc5_fence_after();
+        }
         float fade = 1.f;
         if (most > top + room) fade = ex2_approx((top - most) * by), top = most;  // (from -inf: 0)
         if (begun && __any_sync(kFullMask, fade != 1.f)) {
@@ -399,7 +422,7 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
               add[j % 2] = add2(add[j % 2], pair(p0, p1));
               p[j] = to_bf16x2(p0, p1);
             }
-            tmem_st16(s_at + 16 * c, p);
+            tmem_st16(p_at + 16 * c, p);
           }
           if (c % 2 == 1) {
             tmem_wait_st();
