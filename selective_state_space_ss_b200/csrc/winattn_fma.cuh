@@ -9,6 +9,7 @@
 // works the probabilities out again from the saved normaliser.
 #pragma once
 
+#include "tc5.cuh"
 #include "winattn_common.cuh"
 
 namespace ssscan {
@@ -23,63 +24,77 @@ struct WfCfg {
   static constexpr int kFwd = 2 * kTile + kScores, kDq = 4 * kTile + kScores, kDkv = 4 * kTile + 2 * kScores;
 };
 
-// A tile of 64 tokens from t0 on into fp32 rows; what is behind `len` or d is zero.
+// A tile of 64 tokens from t0 on as fp32 rows, first in a thread's registers; what is behind
+// `len` or d is zero.
 template <typename T, int DP>
-__device__ __forceinline__ void wf_load(float* to, const LaTensor& x, int64_t b, int h, int t0, int len, int d) {
-  constexpr int kRow = WfCfg<DP>::kRow;
-  const bool vec = sizeof(T) == 4 && d % 4 == 0 && reinterpret_cast<uintptr_t>(x.ptr) % 16 == 0 && x.sb % 4 == 0 &&
-                   x.st % 4 == 0 && x.sh % 4 == 0;
-  for (int u = threadIdx.x; u < kWfTile * (DP / 4); u += kWfThreads) {
-    const int row = u / (DP / 4), col = u % (DP / 4) * 4;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (t0 + row < len && col < d) {
+struct WfTile {
+  float4 y[DP / 16];
+  __device__ __forceinline__ void fetch(const LaTensor& x, int64_t b, int h, int t0, int len, int d) {
+    const bool vec = sizeof(T) == 4 && d % 4 == 0 && reinterpret_cast<uintptr_t>(x.ptr) % 16 == 0 && x.sb % 4 == 0 &&
+                     x.st % 4 == 0 && x.sh % 4 == 0;
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const int u = i * kWfThreads + threadIdx.x, row = u / (DP / 4), col = u % (DP / 4) * 4;
+      y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t0 + row >= len || col >= d) continue;
       const char* from = la_row(x, b, t0 + row, h, sizeof(T)) + col * sizeof(T);
-      if (la_inside(x, from, d - col < 4 ? d - col : 4, sizeof(T))) {
-        const T* p = reinterpret_cast<const T*>(from);
-        if (vec) {
-          y = *reinterpret_cast<const float4*>(from);
-        } else {
-          y.x = to_f32(p[0]);
-          if (col + 1 < d) y.y = to_f32(p[1]);
-          if (col + 2 < d) y.z = to_f32(p[2]);
-          if (col + 3 < d) y.w = to_f32(p[3]);
-        }
+      if (!la_inside(x, from, d - col < 4 ? d - col : 4, sizeof(T))) continue;
+      const T* p = reinterpret_cast<const T*>(from);
+      if (vec) {
+        y[i] = *reinterpret_cast<const float4*>(from);
+      } else {
+        y[i].x = to_f32(p[0]);
+        if (col + 1 < d) y[i].y = to_f32(p[1]);
+        if (col + 2 < d) y[i].z = to_f32(p[2]);
+        if (col + 3 < d) y[i].w = to_f32(p[3]);
       }
     }
-    *reinterpret_cast<float4*>(to + row * kRow + col) = y;
   }
+  __device__ __forceinline__ void put(float* to) const {
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const int u = i * kWfThreads + threadIdx.x;
+      *reinterpret_cast<float4*>(to + u / (DP / 4) * WfCfg<DP>::kRow + u % (DP / 4) * 4) = y[i];
+    }
+  }
+};
+template <typename T, int DP>
+__device__ __forceinline__ void wf_load(float* to, const LaTensor& x, int64_t b, int h, int t0, int len, int d) {
+  WfTile<T, DP> tile;
+  tile.fetch(x, b, h, t0, len, d);
+  tile.put(to);
 }
 
-// s[i][j] = <a row 4 ty + i, b row tx + 16 j>
+// s[i][j] = <a row 4 ty + i, b row tx + 16 j>, even and odd values summed apart, two at a time
 template <int DP>
 __device__ __forceinline__ void wf_scores(float (&s)[4][4], const float* a, const float* b, int ty, int tx) {
   constexpr int kRow = WfCfg<DP>::kRow;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+  uint64_t sum[4][4] = {};
 #pragma unroll 4
   for (int k = 0; k < DP; k += 4) {
-    float4 x[4], y[4];
+    ulonglong2 x[4], y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (4 * ty + i) * kRow + k);
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(a + (4 * ty + i) * kRow + k);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * kRow + k);
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * j) * kRow + k);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
-        s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
-        s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
-        s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
-      }
+      for (int j = 0; j < 4; ++j) sum[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, sum[i][j]));
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = pair_lo(sum[i][j]) + pair_hi(sum[i][j]);
 }
 
-// acc[i] += sum_j w[4 ty + i][j] x row j (TRANSPOSED: w[j][4 ty + i]), columns 4 tx + 64 c
+// A thread's sums: rows 4 ty + i, columns 4 tx + 64 c and the three behind, in pairs
+template <int DP>
+using WfSums = uint64_t[4][DP / 32];
+
+// acc[i] += sum_j w[4 ty + i][j] x row j (TRANSPOSED: w[j][4 ty + i])
 template <int DP, bool TRANSPOSED>
-__device__ __forceinline__ void wf_accumulate(float (&acc)[4][DP / 16], const float* w, const float* x, int ty, int tx) {
+__device__ __forceinline__ void wf_accumulate(WfSums<DP>& acc, const float* w, const float* x, int ty, int tx) {
   constexpr int kRow = WfCfg<DP>::kRow, kW = WfCfg<DP>::kScoreRow;
 #pragma unroll 2
   for (int j = 0; j < kWfTile; j += 4) {
@@ -94,13 +109,12 @@ __device__ __forceinline__ void wf_accumulate(float (&acc)[4][DP / 16], const fl
     for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int c = 0; c < DP / 64; ++c) {
-        const float4 y = *reinterpret_cast<const float4*>(x + (j + k) * kRow + 4 * tx + 64 * c);
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(x + (j + k) * kRow + 4 * tx + 64 * c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          acc[i][4 * c] = fmaf(p[i][k], y.x, acc[i][4 * c]);
-          acc[i][4 * c + 1] = fmaf(p[i][k], y.y, acc[i][4 * c + 1]);
-          acc[i][4 * c + 2] = fmaf(p[i][k], y.z, acc[i][4 * c + 2]);
-          acc[i][4 * c + 3] = fmaf(p[i][k], y.w, acc[i][4 * c + 3]);
+          const uint64_t q = pair(p[i][k], p[i][k]);
+          acc[i][2 * c] = fma2(q, y.x, acc[i][2 * c]);
+          acc[i][2 * c + 1] = fma2(q, y.y, acc[i][2 * c + 1]);
         }
       }
   }
@@ -115,12 +129,13 @@ __device__ __forceinline__ __nv_bfloat16 wf_round<__nv_bfloat16>(float x) { retu
 
 // Row r of [.., heads, d] output from this thread's columns.
 template <typename T, int DP>
-__device__ __forceinline__ void wf_store(T* row, const float (&acc)[DP / 16], float by, int d, int tx) {
+__device__ __forceinline__ void wf_store(T* row, const uint64_t (&acc)[DP / 32], float by, int d, int tx) {
 #pragma unroll
-  for (int c = 0; c < DP / 64; ++c)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (4 * tx + 64 * c + e < d) row[4 * tx + 64 * c + e] = wf_round<T>(acc[4 * c + e] * by);
+  for (int c = 0; c < DP / 32; ++c) {
+    const int at = 4 * tx + 64 * (c / 2) + 2 * (c % 2);
+    if (at < d) row[at] = wf_round<T>(pair_lo(acc[c]) * by);
+    if (at + 1 < d) row[at + 1] = wf_round<T>(pair_hi(acc[c]) * by);
+  }
 }
 
 __device__ __forceinline__ float wf_max16(float x) {
@@ -147,15 +162,19 @@ __global__ void __launch_bounds__(kWfThreads) winattn_fma_fwd_kernel(const __gri
   const int r1 = r0 + kWfTile < len ? r0 + kWfTile : len;
   wf_load<T, DP>(q, a.q, b, h, r0, len, a.d);
   const float by = a.scale * kLog2e;  // exponents are of base 2
-  float acc[4][DP / 16] = {}, top[4], sum[4];
+  WfSums<DP> acc = {};
+  float top[4], sum[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) top[i] = -CUDART_INF_F, sum[i] = 0.f;
   const WaKeyTiles<kWfTile> keys(r0, r1, a.window, a.sinks);
+  WfTile<T, DP> next;  // the values, or the next keys, on their way while the products before them run
+  next.fetch(a.k, b, h, keys.at(0) * kWfTile, len, a.d);
   for (int n = 0; n < keys.count; ++n) {
     const int c0 = keys.at(n) * kWfTile;
     __syncthreads();
-    wf_load<T, DP>(kv, a.k, b, h, c0, len, a.d);
+    next.put(kv);
     __syncthreads();
+    next.fetch(a.v, b, h, c0, len, a.d);
     float s[4][4];
     wf_scores<DP>(s, q, kv, ty, tx);
     const bool all = wa_all_seen(r0, r1, c0, c0 + kWfTile, a.window, a.sinks);
@@ -181,11 +200,12 @@ __global__ void __launch_bounds__(kWfThreads) winattn_fma_fwd_kernel(const __gri
       top[i] = most;
       sum[i] = sum[i] * fade + wf_sum16(add);
 #pragma unroll
-      for (int c = 0; c < DP / 16; ++c) acc[i][c] *= fade;
+      for (int c = 0; c < DP / 32; ++c) acc[i][c] = mul2(acc[i][c], pair(fade, fade));
     }
     __syncthreads();
-    wf_load<T, DP>(kv, a.v, b, h, c0, len, a.d);
+    next.put(kv);
     __syncthreads();
+    if (n + 1 < keys.count) next.fetch(a.k, b, h, keys.at(n + 1) * kWfTile, len, a.d);
     wf_accumulate<DP, false>(acc, p, kv, ty, tx);
   }
 #pragma unroll
@@ -237,7 +257,7 @@ __global__ void __launch_bounds__(kWfThreads) winattn_fma_dq_kernel(const __grid
   const int r1 = r0 + kWfTile < len ? r0 + kWfTile : len;
   wf_load<T, DP>(q, a.q, b, h, r0, len, a.d);
   wf_load<T, DP>(g, a.g, b, h, r0, len, a.d);
-  float acc[4][DP / 16] = {};
+  WfSums<DP> acc = {};
   const WaKeyTiles<kWfTile> keys(r0, r1, a.window, a.sinks);
   for (int n = 0; n < keys.count; ++n) {
     const int c0 = keys.at(n) * kWfTile;
@@ -311,7 +331,7 @@ __global__ void __launch_bounds__(kWfThreads) winattn_fma_dkv_kernel(const __gri
   if (c0 >= len) return;
   wf_load<T, DP>(k, a.k, b, hk * a.share, c0, len, a.d);
   wf_load<T, DP>(v, a.v, b, hk * a.share, c0, len, a.d);
-  float dk[4][DP / 16] = {}, dv[4][DP / 16] = {};
+  WfSums<DP> dk = {}, dv = {};
   for (int h = hk * a.share; h < (hk + 1) * a.share; ++h)
     for (int n = w.from; n < w.to; ++n) {
       const int r0 = n * kWfTile;
