@@ -60,7 +60,7 @@ extern "C" {
  *  lse_out       [batch, heads, seqlen] float32, nullable; ss_winattn_bwd takes it
  *  1 <= d <= 128 (others: SS_ERR_UNSUPPORTED); heads a multiple of kv_heads and at
  *                most 65536, batch * heads at most 2^24, seqlen below 2^31 - 1024,
- *                and at most 2^31 - 1 blocks of 64 tokens of all rows and heads
+ *                and batch * heads * seqlen at most 2^33
  *
  * No workspace.
  */

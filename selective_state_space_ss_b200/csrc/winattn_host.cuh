@@ -35,8 +35,8 @@ constexpr int64_t kWaMostTokens = INT_MAX - 1024;
 ss_status wa_check_shape(const WaShape& s, int most_d) {
   if (s.batch < 1 || s.seqlen < 1 || s.heads < 1 || s.kv_heads < 1 || s.d < 1) return SS_ERR_INVALID_ARG;
   if (s.heads % s.kv_heads != 0 || s.seqlen > kWaMostTokens || s.batch > (1 << 24) || s.heads > 65536 ||
-      s.batch * s.heads > (1 << 24))
-    return SS_ERR_INVALID_ARG;
+      s.batch * s.heads > (1 << 24) || s.batch * s.heads * s.seqlen > (INT64_C(1) << 33))
+    return SS_ERR_INVALID_ARG;  // (the last so that every launch's blocks fit a grid)
   if (s.window < 1 || s.sinks < 0) return SS_ERR_INVALID_ARG;
   if (s.d > most_d) return SS_ERR_UNSUPPORTED;
   if (s.dtype != SS_F32 && s.dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
@@ -71,8 +71,9 @@ bool wa_set_smem(K kernel, int bytes) {
 
 ss_status wa_launched() { return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA; }
 
-// Blocks of `tile` tokens of every row and head; 0 where they are more than a grid has.
-unsigned wa_grid(int64_t tiles, int64_t bh) { return tiles * bh > INT_MAX ? 0 : (unsigned)(tiles * bh); }
+// Blocks of so many tiles of every row and head: at most 2^27 + 2^24 of each kind and 64 pieces
+// more, with what wa_check_shape lets through.
+unsigned wa_grid(int64_t tiles, int64_t bh) { return (unsigned)(tiles * bh); }
 
 // The keys' gradients of the tiles that hold sinks, cut into pieces (WaQueryTiles): every
 // piece about as long as what a tile meets through its window, but not more than 64 pieces
@@ -148,16 +149,10 @@ ss_status wa_tc_fwd(WaArgs a, const WaMaps& maps, cudaStream_t stream) {
   return wa_launched();
 }
 
-// The grid of every launch fits (64 tokens the smallest tile of any).
-ss_status wa_check_grid(const WaShape& s) {
-  return wa_grid((s.seqlen + kWfTile - 1) / kWfTile + 128, s.batch * s.heads) ? SS_OK : SS_ERR_INVALID_ARG;
-}
-
 ss_status winattn_fwd_impl(const ss_heads* q, const ss_heads* k, const ss_heads* v, float scale,
                            const int32_t* lengths, void* o, float* lse, const WaShape& given, cudaStream_t stream) {
-  ss_status st = wa_check_shape(given, 128);
-  if (st == SS_OK) st = wa_check_grid(given);
-  if (st != SS_OK) return st;
+  const ss_status shape = wa_check_shape(given, 128);
+  if (shape != SS_OK) return shape;
   const int es = given.es();
   if (!wa_check_heads(q, es) || !wa_check_heads(k, es) || !wa_check_heads(v, es) || !o) return SS_ERR_INVALID_ARG;
   if (!aligned(o, es) || !aligned(lse, 4) || !aligned(lengths, 4)) return SS_ERR_INVALID_ARG;
@@ -193,20 +188,15 @@ template <typename T, int DP>
 ss_status wa_fma_bwd(WaArgs a, void* dq, cudaStream_t stream) {
   using CF = WfCfg<DP>;
   struct Tag : CF { T x; };
-  if (once_per_device<Tag>([] {
-        return wa_set_smem(winattn_fma_dq_kernel<T, DP>, CF::kDq * 4) &&
-               wa_set_smem(winattn_fma_dkv_kernel<T, DP>, CF::kDkv * 4);
-      }) != 1)
-    return SS_ERR_CUDA;
+  constexpr int kSmem = (CF::kDq > CF::kDkv ? CF::kDq : CF::kDkv) * 4;
+  if (once_per_device<Tag>([] { return wa_set_smem(winattn_fma_bwd_kernel<T, DP>, kSmem); }) != 1) return SS_ERR_CUDA;
   ss_status st = wa_delta<T>(a, stream);
   if (st != SS_OK) return st;
   const int64_t tiles = (a.seqlen + kWfTile - 1) / kWfTile;
   a.out = dq;
-  winattn_fma_dq_kernel<T, DP><<<wa_grid(tiles, (int64_t)a.batch * a.heads), kWfThreads, CF::kDq * 4, stream>>>(a);
-  st = wa_launched();
-  if (st != SS_OK) return st;
-  const unsigned grid = wa_grid(tiles + a.sink_tiles * a.pieces, (int64_t)a.batch * (a.heads / a.share));
-  winattn_fma_dkv_kernel<T, DP><<<grid, kWfThreads, CF::kDkv * 4, stream>>>(a);
+  a.items = (int)wa_grid(tiles + a.sink_tiles * a.pieces, (int64_t)a.batch * (a.heads / a.share));
+  const unsigned blocks = a.items + wa_grid(tiles, (int64_t)a.batch * a.heads);
+  winattn_fma_bwd_kernel<T, DP><<<blocks, kWfThreads, kSmem, stream>>>(a);
   st = wa_launched();
   return st != SS_OK ? st : wa_sinks<T, kWfTile>(a, stream);
 }
@@ -215,8 +205,7 @@ ss_status wa_check_bwd_shape(const WaShape& s) {
   const ss_status st = wa_check_shape(s, 128);
   if (st != SS_OK) return st;
   if (s.batch * s.kv_heads > 65535) return SS_ERR_INVALID_ARG;  // the sinks' sums have a grid row each
-  if ((s.batch * s.heads * s.seqlen + 7) / 8 > INT_MAX) return SS_ERR_INVALID_ARG;
-  return wa_check_grid(s);
+  return SS_OK;
 }
 
 template <int DP>

@@ -71,7 +71,8 @@ def _rotate(lib, **over):
 ALL = [_fwd, _bwd, _step, _append, _rotate]
 SIZES = [(dict(batch=0), BAD), (dict(L=0), BAD), (dict(heads=0), BAD), (dict(hk=0), BAD), (dict(hk=3), BAD),
          (dict(heads=2, hk=4), BAD), (dict(d=0), BAD), (dict(dt=2), NO), (dict(batch=1 << 24), BAD), (dict(batch=1 << 40), BAD),
-         (dict(L=1 << 31), BAD), (dict(L=(1 << 31) - 1024), BAD), (dict(heads=65537, hk=1), BAD)]
+         (dict(L=1 << 31), BAD), (dict(L=(1 << 31) - 1024), BAD), (dict(heads=65537, hk=1), BAD),
+         (dict(L=1 << 30, heads=8), BAD)]
 
 
 @pytest.mark.parametrize("over,status", SIZES)
