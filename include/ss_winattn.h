@@ -81,7 +81,8 @@ ss_status ss_winattn_fwd(const ss_heads* q, const ss_heads* k, const ss_heads* v
  *   dk_j  = scale sum_t ds_tj q_t                (and over the heads that share j)
  *
  * dq [batch, seqlen, heads, d], dk_out, dv_out [batch, seqlen, kv_heads, d]:
- * in_dtype, contiguous, required; nothing is written behind a row's length.
+ * in_dtype, contiguous, required; nothing is written behind a row's length.  Sizes as
+ * ss_winattn_fwd, and batch * kv_heads at most 65535.
  * workspace: ss_winattn_bwd_workspace_bytes(...) bytes, 256-byte aligned.  Contents on
  * entry do not matter; calls in flight at once, replays of captured ones among them,
  * must not share one.

@@ -41,6 +41,7 @@ SS_NOALLOC_SCRATCH_BYTES = 4 << 20
 (SS_DEBUG_CLEAR, SS_DEBUG_FORCE_WORKERS, SS_DEBUG_SKIP_PUBLISH, SS_DEBUG_SPIN_LIMIT,
  SS_DEBUG_STEP_SIMPLE, SS_DEBUG_FORCE_SEGMENTS, SS_DEBUG_LINATTN_SPIN_LIMIT, SS_DEBUG_LINATTN_SKIP_PUBLISH,
  SS_DEBUG_LINATTN_SKIP_LOAD) = range(9)
+SS_DEBUG_WINATTN_SKIP_LOAD = 16
 # pointwise functions ss_debug_pointwise evaluates (include/ss_scan_debug.h)
 (SS_PW_SOFTPLUS, SS_PW_SILU, SS_PW_SOFTPLUS2, SS_PW_SILU2, SS_PW_EXP2_NEG_FMA, SS_PW_RCP_1_2,
  SS_PW_EX2) = range(7)

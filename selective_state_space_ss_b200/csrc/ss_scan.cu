@@ -23,6 +23,7 @@ bool take_linattn_error_word(unsigned int* word);
 void set_linattn_debug(int what, long long value);
 // ss_winattn.cu's
 bool take_winattn_error_word(unsigned int* word);
+void set_winattn_debug(int what, long long value);
 }
 
 // Scratch of ss_scan_fwd_noalloc: one file-scope device array, held by every
@@ -267,8 +268,10 @@ ss_status ss_debug_inject(int what, long long value) {
     case SS_DEBUG_LINATTN_SKIP_LOAD:
       set_linattn_debug(what, value);
       return SS_OK;
+    case SS_DEBUG_WINATTN_SKIP_LOAD: set_winattn_debug(what, value); return SS_OK;
     case SS_DEBUG_CLEAR:
       set_linattn_debug(what, 0);
+      set_winattn_debug(what, 0);
       g_dbg_segments.store(0);
       g_dbg_step_simple.store(0);
       g_dbg_workers.store(0);

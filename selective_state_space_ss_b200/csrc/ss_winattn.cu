@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "ss_scan_debug.h"
 #include "ss_winattn.h"
 #include "winattn_host.cuh"
 
@@ -19,6 +20,11 @@ bool take_winattn_error_word(unsigned int* word) {
   if (*word == 0) return true;
   const unsigned int zero = 0;
   return cudaMemcpyToSymbol(g_error_word, &zero, sizeof zero) == cudaSuccess;
+}
+
+// ss_debug_inject's settings of this unit.
+void set_winattn_debug(int what, long long value) {
+  g_dbg_wa_skip_load.store(what == SS_DEBUG_WINATTN_SKIP_LOAD ? value : -1);
 }
 
 }  // namespace ssscan

@@ -169,7 +169,7 @@ winattn_dkv_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
         ring.next();
       };
       tile(rq, CF::kQ, &maps.q, full_q(rq.i), empty_q(rq.i));
-      tile(rg, CF::kG, &maps.g, full_g(rg.i), empty_g(rg.i));
+      if (r0 / kWtRows != a.skip_load) tile(rg, CF::kG, &maps.g, full_g(rg.i), empty_g(rg.i));
     }
     // the last copies land before the end, also where those that they are for have given up
     const auto land = [&](auto& ring, int count, const auto& full) {
@@ -470,9 +470,10 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
         // out of dS K
         const bool ragged = c0 + kWtRows > w.len && w.len < a.seqlen;
         const int k_to = CF::kK + rk.i * CF::kTile;
+        const bool skip = c0 / kWtRows == a.skip_load;
         if (lane == 0) {
           wt_load<DP>(base + k_to, &maps.k, ragged ? b_raw : full_k(rk.i), c0, w.h / a.share, w.b);
-          wt_load<DP>(base + CF::kV + rv.i * CF::kTile, &maps.v, full_v(rv.i), c0, w.h / a.share, w.b);
+          if (!skip) wt_load<DP>(base + CF::kV + rv.i * CF::kTile, &maps.v, full_v(rv.i), c0, w.h / a.share, w.b);
         }
         __syncwarp();
         if (ragged) {
@@ -481,7 +482,8 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
           wt_clear<DP>(smem + k_to, w.len - c0, lane);
           if (lane == 0) la_arrive(full_k(rk.i));
         }
-        rk.next(), rv.next();
+        rk.next();
+        if (!skip) rv.next();
       }
     }
     // the last copies land before the end, also where those that they are for have given up

@@ -20,7 +20,8 @@ struct WaArgs {
   int64_t window;
   int sinks, seqlen, heads, share, d, batch;  // share: heads that read one head of keys
   float scale;
-  int items;           // tensor cores: 256 queries of a head each, shared by the blocks
+  int items;           // what the blocks share: tiles of queries of a head (forward, dQ), keys' blocks (fp32 gradients)
+  int skip_load;       // test hook: a tile that is never loaded (-1: none)
   // backward
   LaTensor o, g;       // the forward's result and its gradient
   float* delta;        // [batch, heads, seqlen]: do . o

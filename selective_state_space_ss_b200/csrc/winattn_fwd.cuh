@@ -224,6 +224,7 @@ winattn_fwd_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaM
           const int c0 = w.keys.at(i) * kWtRows;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
+            if (kv && c0 / kWtRows == a.skip_load) continue;
             if (!gone && ring.used()) gone = !la_wait(empty(ring.i), ring.empty(), dead);
             if (gone) continue;
             const uint32_t to = base + CF::kKv + ring.i * CF::kTile;

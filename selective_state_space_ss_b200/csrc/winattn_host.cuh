@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -77,7 +78,8 @@ unsigned wa_grid(int64_t tiles, int64_t bh) { return (unsigned)(tiles * bh); }
 
 // The keys' gradients of the tiles that hold sinks, cut into pieces (WaQueryTiles): every
 // piece about as long as what a tile meets through its window, but not more than 64 pieces
-// of all of them (their sums take workspace).
+// of all of them (their sums take workspace).  Where more tiles than that hold sinks there are
+// blocks enough without.
 struct WaSplit {
   int sink_tiles = 0, pieces = 0, piece_tiles = 0;
 };
@@ -85,8 +87,8 @@ WaSplit wa_split(const WaShape& s, int tile) {
   WaSplit r;
   const int64_t all = (s.seqlen + tile - 1) / tile, near = (s.window + tile - 2) / tile + 1;
   if (s.sinks == 0 || all <= 2 * near) return r;
-  const int64_t tiles = (s.sinks + tile - 1) / tile;
-  const int64_t most = 64 / tiles > 1 ? 64 / tiles : 1;
+  const int64_t tiles = (s.sinks + tile - 1) / tile, most = 64 / tiles;
+  if (most == 0) return r;
   int64_t each = near > 8 ? near : 8;
   if (each * most < all) each = (all + most - 1) / most;
   r.sink_tiles = (int)(tiles < all ? tiles : all);
@@ -105,6 +107,9 @@ WaBwdWs wa_bwd_ws(const WaShape& s, const WaSplit& split, int tile) {
   return w;
 }
 
+// Test hook (ss_scan_debug.h): consumed by the next forward or backward call.
+std::atomic<long long> g_dbg_wa_skip_load{-1};
+
 WaArgs wa_base(const WaShape& s, const ss_heads* q, const ss_heads* k, const ss_heads* v, float scale,
                const int32_t* lengths) {
   WaArgs a = {};
@@ -120,6 +125,7 @@ WaArgs wa_base(const WaShape& s, const ss_heads* q, const ss_heads* k, const ss_
   a.d = s.d;
   a.batch = (int)s.batch;
   a.scale = scale;
+  a.skip_load = (int)g_dbg_wa_skip_load.exchange(-1);
   return a;
 }
 

@@ -165,3 +165,9 @@ def test_the_binding_runs_on_cuda_tensors_only(lib):
                  lambda: N.ss_kv_append(x, x, pages, pages, table, n)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_the_waits_hook_is_known(lib):
+    assert lib.ss_debug_inject(N.SS_DEBUG_WINATTN_SKIP_LOAD, 3) == N.SS_OK
+    assert lib.ss_debug_inject(N.SS_DEBUG_CLEAR, 0) == N.SS_OK
+    assert lib.ss_debug_inject(N.SS_DEBUG_WINATTN_SKIP_LOAD + 1, 0) == BAD
