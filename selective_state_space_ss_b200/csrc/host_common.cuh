@@ -1,7 +1,7 @@
 // host_common.cuh -- host helpers shared by every entry point: alignment,
 // per-device lookups done once, and the scan's test-hook settings
-// (host code of both translation units of libssscan.so; the scan's hooks are set and
-// read in ss_scan.cu alone, the other unit's 40 bytes of them never)
+// (host code of all translation units of libssscan.so; the scan's hooks are set and
+// read in ss_scan.cu alone, the other units' 40 bytes of them never)
 #pragma once
 
 #include <cuda_runtime.h>

@@ -46,7 +46,7 @@ namespace ssscan {
 
 // Device error word: a kernel that gives up a bounded wait sets a bit here
 // instead of trapping; ss_last_device_error reads and clears it.  (Each of the
-// library's two translation units has one of its own; both are read.)
+// library's translation units has one of its own; all are read.)
 __device__ unsigned int g_error_word = 0;
 constexpr unsigned kErrTmaWait = 1u;     // a TMA completion wait timed out
 constexpr unsigned kErrLookback = 2u;    // an inter-CTA carry wait timed out

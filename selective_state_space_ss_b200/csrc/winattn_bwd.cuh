@@ -379,17 +379,20 @@ struct WtDqCfg {
   static constexpr int kOutCols = DP == 64 ? 32 : 0, kStage = 32 * kOutCols * 2;  // written out at a time, where there is room
   static constexpr int kBars = kOut + 8 * kStage;
   static constexpr int kNumBars = 2 * (RK + RV) + 10;
-  static constexpr int kSmem = kBars + kNumBars * 8 + 16;
+  static constexpr int kSmem = kBars + kNumBars * 8 + 16 + kWtRows * 4;
   static constexpr int cS = 0, cP = 256, cDq = 384;  // S in two places
   static constexpr int kThreads = 384;
   static_assert(kSmem <= 232448, "shared memory");
 };
+
+constexpr int kWtExact = 2;  // tiles of keys (below)
 
 // 128 queries of a head at a time, item `n`, long rows first; false where the row has ended before.
 struct WtRowItem {
   int b, h, r0, end, len;
   WaKeyTiles<kWtRows> keys;
 };
+template <bool DELTA = false>
 __device__ __forceinline__ bool wt_row_item(WtRowItem& w, const WaArgs& a, int n) {
   const int bh_all = a.batch * a.heads, bh = n % bh_all;
   w.b = bh / a.heads;
@@ -399,10 +402,15 @@ __device__ __forceinline__ bool wt_row_item(WtRowItem& w, const WaArgs& a, int n
   if (w.r0 >= w.len) return false;
   w.end = w.len - w.r0 > kWtRows ? w.r0 + kWtRows : w.len;
   w.keys = WaKeyTiles<kWtRows>(w.r0, w.end, a.window, a.sinks);
-  return true;
+  return !DELTA || w.keys.count - w.keys.sink <= kWtExact;
 }
 
-template <int DP>
+// DELTA: no dQ, but delta of the tiles whose window has up to kWtExact tiles of keys (the first
+// two of a row, all with windows of up to 129), as sum_j p_j (do . v_j), which is do . o with the o that this P gives.  The given o is rounded to bf16, an
+// error of all of a row's dS alike: where a row sees many keys it vanishes in dQ next to what
+// the rounding of dS leaves, but of few keys dS itself may be small differences (windows of 1 to
+// 3: dq and dk up to 3.9e-3 off in norm, 2.4e-3 with this; plain rounding 1.7e-3).
+template <int DP, bool DELTA>
 __global__ void __launch_bounds__(WtDqCfg<DP>::kThreads, 1)
 winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMaps maps) {
   using CF = WtDqCfg<DP>;
@@ -448,7 +456,7 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
     bool gone = false;  // a place was not free in time: no further copies
     uint32_t raw = 0, items = 0;
     for (int item = blockIdx.x; item < a.items && !gone; item += gridDim.x) {
-      if (!wt_row_item(w, a, item)) continue;
+      if (!wt_row_item<DELTA>(w, a, item)) continue;
       if (items > 0) gone = !la_wait(b_q_free, (items - 1) & 1, dead);
       if (gone) break;
       if (lane == 0) {
@@ -521,9 +529,10 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
       }
       mma_commit(b_dp);
       mma_commit(empty_v(v_at));
+      if (DELTA) mma_commit(empty_k(k_at));
     };
     for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
-      if (!wt_row_item(w, a, item)) continue;
+      if (!wt_row_item<DELTA>(w, a, item)) continue;
       la_wait(b_q, items & 1, dead);
       int k_at = 0;
       for (int i = -1; i < w.keys.count; ++i) {
@@ -540,7 +549,7 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
           }
           __syncwarp();
         }
-        if (i >= 0) {
+        if (!DELTA && i >= 0) {
           const int t = n - 1;  // of all tiles
           if (i == 0 && items > 0) la_wait(b_o_free, (items - 1) & 1, dead);
           la_wait(b_ds(t), (t / 2) & 1, dead);
@@ -580,11 +589,11 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
     float lse = 0.f, delta = 0.f;  // of the item at hand, asked for before the one before it is written out
     const auto begin = [&]() {  // the next item that there is
       for (; item < a.items; item += gridDim.x)
-        if (wt_row_item(w, a, item)) {
+        if (wt_row_item<DELTA>(w, a, item)) {
           const int row = w.r0 + quad * 32 + lane;
           const int64_t at = ((int64_t)w.b * a.heads + w.h) * a.seqlen + row;
           const bool real = row < w.end && in_range(at, (int64_t)a.batch * a.heads * a.seqlen);
-          lse = real ? a.lse[at] : 0.f, delta = real ? a.delta[at] : 0.f;
+          lse = real ? a.lse[at] : 0.f, delta = real && !DELTA ? a.delta[at] : 0.f;
           item += gridDim.x;
           return true;
         }
@@ -594,6 +603,7 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
     while (more) {
       const int row = w.r0 + quad * 32 + lane;
       const uint64_t lse2 = pair(-lse * kLog2e, -lse * kLog2e), delta2 = pair(-delta, -delta);
+      float total = 0.f;
 #pragma unroll 1
       for (int i = 0; i < w.keys.count; ++i, ++n) {
         const int c0 = w.keys.at(i) * kWtRows;
@@ -615,7 +625,6 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if (cols <= 32 * c) continue;
-          uint32_t ds[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const uint64_t z = fma2(pair(s[c][2 * j], s[c][2 * j + 1]), by2, lse2);
@@ -631,14 +640,33 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
             for (int j = 0; j < 32; ++j)
               if (!(seen & 1u << j)) s[c][j] = 0;
           }
+          if constexpr (DELTA) {
+            uint64_t add = 0;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) ds[j] = to_bf16x2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1]));
-          tmem_st16(s_at + 16 * c, ds);
+            for (int j = 0; j < 16; ++j) add = add2(add, pair(s[c][2 * j], s[c][2 * j + 1]));
+            total += pair_lo(add) + pair_hi(add);
+          } else {
+            uint32_t ds[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) ds[j] = to_bf16x2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1]));
+            tmem_st16(s_at + 16 * c, ds);
+          }
         }
+        if (DELTA) continue;
         tmem_wait_st();
         tc5_fence_before();
         __syncwarp();
         if (lane == 0) la_arrive(b_ds(n));
+      }
+      if constexpr (DELTA) {  // the two halves' sums
+        float* other = reinterpret_cast<float*>(smem + CF::kBars + CF::kNumBars * 8 + 16) + quad * 32 + lane;
+        if (side) *other = total;
+        asm volatile("bar.sync 1, 256;\n" ::: "memory");
+        const int64_t at = ((int64_t)w.b * a.heads + w.h) * a.seqlen + row;
+        if (!side && row < w.end && in_range(at, (int64_t)a.batch * a.heads * a.seqlen)) a.delta[at] = total + *other;
+        asm volatile("bar.sync 1, 256;\n" ::: "memory");
+        more = begin();
+        continue;
       }
       const WtRowItem done = w;
       more = begin();

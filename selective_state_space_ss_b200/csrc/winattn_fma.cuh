@@ -219,14 +219,16 @@ __global__ void __launch_bounds__(kWfThreads) winattn_fma_fwd_kernel(const __gri
   }
 }
 
-// p = exp(s - lse) of a tile's scores, and ds = p (dp - delta); both zero where nothing is seen.
+// p = exp(s - lse) of a tile's scores, and ds = p (dp - delta) (DELTA: p dp); both zero where
+// nothing is seen.
+template <bool DELTA = false>
 __device__ __forceinline__ void wf_probabilities(float (&s)[4][4], float (&dp)[4][4], const WaArgs& a, int64_t bh, int r0,
                                                  int c0, int len, int ty, int tx) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = r0 + 4 * ty + i;
     const bool real = t < len && in_range(bh * a.seqlen + t, (int64_t)a.batch * a.heads * a.seqlen);
-    const float lse = real ? a.lse[bh * a.seqlen + t] * kLog2e : 0.f, delta = real ? a.delta[bh * a.seqlen + t] : 0.f;
+    const float lse = real ? a.lse[bh * a.seqlen + t] * kLog2e : 0.f, delta = real && !DELTA ? a.delta[bh * a.seqlen + t] : 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool seen = real && wa_sees(t, c0 + tx + 16 * j, a.window, a.sinks);
@@ -244,8 +246,9 @@ __device__ __forceinline__ void wf_put_scores(float* to, const float (&s)[4][4],
     for (int j = 0; j < 4; ++j) to[(4 * ty + i) * WfCfg<DP>::kScoreRow + tx + 16 * j] = s[i][j];
 }
 
-// dQ of block `block`'s 64 queries.
-template <typename T, int DP>
+// dQ of block `block`'s 64 queries; DELTA: their sums p (do . v) instead, which are do . o with
+// an o that is not rounded.
+template <typename T, int DP, bool DELTA = false>
 __device__ __forceinline__ void wf_dq(const WaArgs& a, int block, int blocks) {
   using CF = WfCfg<DP>;
   extern __shared__ __align__(16) float wf_smem[];
@@ -259,6 +262,7 @@ __device__ __forceinline__ void wf_dq(const WaArgs& a, int block, int blocks) {
   wf_load<T, DP>(q, a.q, b, h, r0, len, a.d);
   wf_load<T, DP>(g, a.g, b, h, r0, len, a.d);
   WfSums<DP> acc = {};
+  float delta[4] = {};
   const WaKeyTiles<kWfTile> keys(r0, r1, a.window, a.sinks);
   for (int n = 0; n < keys.count; ++n) {
     const int c0 = keys.at(n) * kWfTile;
@@ -269,17 +273,27 @@ __device__ __forceinline__ void wf_dq(const WaArgs& a, int block, int blocks) {
     float s[4][4], dp[4][4];
     wf_scores<DP>(s, q, k, ty, tx);
     wf_scores<DP>(dp, g, v, ty, tx);
-    wf_probabilities(s, dp, a, bh, r0, c0, len, ty, tx);
-    wf_put_scores<DP>(ds, dp, ty, tx);
-    __syncthreads();
-    wf_accumulate<DP, false>(acc, ds, k, ty, tx);
+    wf_probabilities<DELTA>(s, dp, a, bh, r0, c0, len, ty, tx);
+    if constexpr (DELTA) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) delta[i] += wf_sum16(dp[i][0] + dp[i][1] + dp[i][2] + dp[i][3]);
+    } else {
+      wf_put_scores<DP>(ds, dp, ty, tx);
+      __syncthreads();
+      wf_accumulate<DP, false>(acc, ds, k, ty, tx);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = r0 + 4 * ty + i;
-    const int64_t at = (((int64_t)b * a.seqlen + t) * a.heads + h) * a.d;
-    if (t < len && in_range(at, a.d, (int64_t)bh_all * a.seqlen * a.d))
-      wf_store<T, DP>(static_cast<T*>(a.out) + at, acc[i], a.scale, a.d, tx);
+    if constexpr (DELTA) {
+      const int64_t l = (int64_t)bh * a.seqlen + t;
+      if (tx == 0 && t < len && in_range(l, (int64_t)bh_all * a.seqlen)) a.delta[l] = delta[i];
+    } else {
+      const int64_t at = (((int64_t)b * a.seqlen + t) * a.heads + h) * a.d;
+      if (t < len && in_range(at, a.d, (int64_t)bh_all * a.seqlen * a.d))
+        wf_store<T, DP>(static_cast<T*>(a.out) + at, acc[i], a.scale, a.d, tx);
+    }
   }
 }
 
@@ -374,6 +388,11 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kWfThreads) winattn_fma_bwd_kernel(const __grid_constant__ WaArgs a) {
   if ((int)blockIdx.x < a.items) wf_dkv<T, DP>(a, blockIdx.x);
   else wf_dq<T, DP>(a, blockIdx.x - a.items, gridDim.x - a.items);
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kWfThreads) winattn_fma_delta_kernel(const __grid_constant__ WaArgs a) {
+  wf_dq<T, DP, true>(a, blockIdx.x, gridDim.x);
 }
 
 // delta = do . o of every row, a warp each.

@@ -195,11 +195,20 @@ ss_status wa_fma_bwd(WaArgs a, void* dq, cudaStream_t stream) {
   using CF = WfCfg<DP>;
   struct Tag : CF { T x; };
   constexpr int kSmem = (CF::kDq > CF::kDkv ? CF::kDq : CF::kDkv) * 4;
-  if (once_per_device<Tag>([] { return wa_set_smem(winattn_fma_bwd_kernel<T, DP>, kSmem); }) != 1) return SS_ERR_CUDA;
-  ss_status st = wa_delta<T>(a, stream);
-  if (st != SS_OK) return st;
+  if (once_per_device<Tag>([] {
+        return wa_set_smem(winattn_fma_bwd_kernel<T, DP>, kSmem) && wa_set_smem(winattn_fma_delta_kernel<T, DP>, kSmem);
+      }) != 1)
+    return SS_ERR_CUDA;
   const int64_t tiles = (a.seqlen + kWfTile - 1) / kWfTile;
   a.out = dq;
+  ss_status st;
+  if constexpr (sizeof(T) == 4) {
+    st = wa_delta<T>(a, stream);
+  } else {  // (winattn_dq_kernel says why)
+    winattn_fma_delta_kernel<T, DP><<<wa_grid(tiles, (int64_t)a.batch * a.heads), kWfThreads, kSmem, stream>>>(a);
+    st = wa_launched();
+  }
+  if (st != SS_OK) return st;
   a.items = (int)wa_grid(tiles + a.sink_tiles * a.pieces, (int64_t)a.batch * (a.heads / a.share));
   const unsigned blocks = a.items + wa_grid(tiles, (int64_t)a.batch * a.heads);
   winattn_fma_bwd_kernel<T, DP><<<blocks, kWfThreads, kSmem, stream>>>(a);
@@ -220,7 +229,8 @@ ss_status wa_tc_bwd(WaArgs a, const WaMaps& maps, void* dq, cudaStream_t stream)
   using DQ = WtDqCfg<DP>;
   struct Tag : KV {};
   if (once_per_device<Tag>([] {
-        return wa_set_smem(winattn_dkv_kernel<DP>, KV::kSmem) && wa_set_smem(winattn_dq_kernel<DP>, DQ::kSmem);
+        return wa_set_smem(winattn_dkv_kernel<DP>, KV::kSmem) && wa_set_smem(winattn_dq_kernel<DP, false>, DQ::kSmem) &&
+               wa_set_smem(winattn_dq_kernel<DP, true>, DQ::kSmem);
       }) != 1)
     return SS_ERR_CUDA;
   constexpr int LANES = DP / 8;
@@ -232,7 +242,11 @@ ss_status wa_tc_bwd(WaArgs a, const WaMaps& maps, void* dq, cudaStream_t stream)
   const int sms = device_sms() > 0 ? device_sms() : 148;
   a.out = dq;
   a.items = (int)wa_grid(tiles, (int64_t)a.batch * a.heads);
-  winattn_dq_kernel<DP><<<a.items < sms ? a.items : sms, DQ::kThreads, DQ::kSmem, stream>>>(a, maps);
+  const int blocks = a.items < sms ? a.items : sms;
+  winattn_dq_kernel<DP, true><<<blocks, DQ::kThreads, DQ::kSmem, stream>>>(a, maps);
+  st = wa_launched();
+  if (st != SS_OK) return st;
+  winattn_dq_kernel<DP, false><<<blocks, DQ::kThreads, DQ::kSmem, stream>>>(a, maps);
   st = wa_launched();
   if (st != SS_OK) return st;
   const unsigned grid = wa_grid(tiles + a.sink_tiles * a.pieces, (int64_t)a.batch * (a.heads / a.share));
