@@ -27,7 +27,8 @@
  *
  * Softmax statistics and all sums are fp32, in a fixed order: the same call gives the
  * same bits.  For bfloat16 operands the probabilities, and in the backward pass their
- * gradients, are rounded to bfloat16 as operands of the next product.
+ * gradients, are rounded to bfloat16 as operands of the next product (results 1.4 times
+ * as far from the exact ones, in norm, as their own rounding alone leaves them).
  *
  * Values of tokens that a row holds must be finite: a NaN or an infinity among them
  * may spread over its row's and its heads' results, to tokens that do not see it as

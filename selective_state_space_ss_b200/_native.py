@@ -820,7 +820,8 @@ def _winattn_operands(what, q, k, v):
 
 def _count(name, n):
     """A window or a number of sinks as the C ABI takes it."""
-    n = int(n)
+    if type(n) is not int:
+        n = int(n)
     if not 0 <= n < 1 << 62:
         raise ValueError(f"{name}: {n} is out of range")
     return n

@@ -5,8 +5,12 @@
 // A block takes 64 queries (or, for the keys' gradients, 64 keys) of one head and walks
 // the tiles of 64 keys (queries) that they meet; every product is a 64 x 64 x d or
 // 64 x d x 64 one in registers, 4 x 4 or 4 x d/16 values a thread, from tiles in shared
-// memory.  The forward keeps the running maximum and sum of the softmax; the backward
-// works the probabilities out again from the saved normaliser.
+// memory, two values at a time (fma.rn.f32x2).  The forward keeps the running maximum and sum of
+// the softmax; the backward works the probabilities out again from the saved normaliser.
+//
+// Bound by shared memory's wavefronts and issue, each about half of what there is, and by the
+// last wave of few blocks: ragged B6 L1000, 8 heads of 64 on 4, window 256: 95 us; gradients of B2
+// L1024, 8 heads of 64, window 256: 145 us (16 TFLOP/s of fp32).
 #pragma once
 
 #include "tc5.cuh"

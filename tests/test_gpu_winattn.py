@@ -193,3 +193,20 @@ def test_refusals():
                 lambda: ss.ss_winattn_fwd(q[:, :, :3], k, v, 5), lambda: ss.ss_winattn_bwd(q, k, v, o, lse, do, 0)):
         with pytest.raises(ss.SSError):
             bad()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 queries' values: the end of the row against 64 bits."""
+    L, heads, kv, d, window = 1 << 17, 130, 2, 128, 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, do = (torch.randn(1, L, heads, d, device="cuda", generator=gen, dtype=BF16) for _ in range(2))
+    k, v = (torch.randn(1, L, kv, d, device="cuda", generator=gen, dtype=BF16) for _ in range(2))
+    assert q.numel() > 1 << 31
+    o, lse = ss.ss_winattn_fwd(q, k, v, window)
+    g = ss.ss_winattn_bwd(q, k, v, o, lse, do, window)
+    assert ss.ss_last_device_error() == ss.SS_OK
+    end = slice(L - 256, L)
+    ref = P.attention(q[:, end], k[:, end], v[:, end], window, do=do[:, end])
+    for name, x in {"o": o, **g}.items():  # from the first token on whose window lies in the piece
+        P.check(name, x[:, end][:, window:], *(y[:, window:] for y in ref[name]))
+    P.check("lse", lse[..., end][..., window:], *(y[..., window:] for y in ref["lse"]))
