@@ -20,8 +20,8 @@
 // What bounds it (B4 L8192, 40 heads of 128 on 8, window 2048: 3.0 TFLOP in five products; 3.9
 // ms, 0.77 PFLOP/s, 0.46 of the measured rate, 1.08 of that for the seven that are formed): a
 // tile of either kernel is a chain of hand-overs between products and softmax.  With two places
-// for keys and queries instead of three 4.5 ms.  B8 L2048, 24 heads of 64 on 8, window 512: 0.385
-// ms (fp32 arithmetic 6.0), dQ's 160 us and the keys' 197; per tile 1800 to 2100 and 3000 cycles
+// for keys and queries instead of three 4.5 ms.  B8 L2048, 24 heads of 64 on 8, window 512: 0.373
+// ms (fp32 arithmetic 6.0), dQ's 158 us and the keys' 198; per tile 1800 to 2100 and 3000 cycles
 // next to 1024 of the special-function unit, 20% of dQ's time and of the keys' between items.
 // Tiles halved, with barriers of their own for each half and the second half a half step behind
 // the first: the same time with 64-wide heads, 12% more with 128 (64-wide score products).
@@ -697,30 +697,38 @@ winattn_dq_kernel(const __grid_constant__ WaArgs a, const __grid_constant__ WaMa
   if (warp == kWtMmaWarp) tmem_free(tmem, 512);
 }
 
-// delta = do . o of every row, 16-byte units, d / 8 lanes (made up to 8 or 16) a row.
+// delta = do . o of every row, 16-byte units, d / 8 lanes (made up to 8 or 16) a row; a block
+// has kDeltaRows rows of one batch row's [seqlen, heads].
+constexpr int kDeltaRows = 64;
 template <int LANES>
 __global__ void __launch_bounds__(256) winattn_delta16_kernel(const __grid_constant__ WaArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES, all = (int64_t)a.batch * a.heads * a.seqlen;
-  const int u = threadIdx.x % LANES;
-  float sum = 0.f;
-  const int h = (int)(row % a.heads);
-  const int64_t bt = row / a.heads, t = bt % a.seqlen, b = bt / a.seqlen;
-  const bool real = row < all && t < wa_length(a.lengths, b, a.seqlen);
-  if (real && 8 * u < a.d) {
-    const char *o = la_row(a.o, b, t, h, 2) + 16 * u, *g = la_row(a.g, b, t, h, 2) + 16 * u;
-    if (la_inside(a.o, o, 8, 2) && la_inside(a.g, g, 8, 2)) {
-      const uint4 x = *reinterpret_cast<const uint4*>(o), y = *reinterpret_cast<const uint4*>(g);
-      uint64_t z = mul2(from_bf16x2(x.x), from_bf16x2(y.x));
-      z = fma2(from_bf16x2(x.y), from_bf16x2(y.y), z);
-      z = fma2(from_bf16x2(x.z), from_bf16x2(y.z), z);
-      z = fma2(from_bf16x2(x.w), from_bf16x2(y.w), z);
-      sum = pair_lo(z) + pair_hi(z);
-    }
-  }
+  const int64_t rows = (int64_t)a.seqlen * a.heads, blocks = (rows + kDeltaRows - 1) / kDeltaRows;
+  const int64_t b = blockIdx.x / blocks, first = (blockIdx.x - b * blocks) * kDeltaRows;
+  const int64_t t0 = first / a.heads;  // and the block's other rows from there, in 32 bits
+  const unsigned h0 = (unsigned)(first - t0 * a.heads);
+  const int len = wa_length(a.lengths, b, a.seqlen), u = threadIdx.x % LANES;
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
-  const int64_t at = (b * a.heads + h) * a.seqlen + t;
-  if (real && u == 0 && in_range(at, all)) a.delta[at] = sum;
+  for (int i = 0; i < kDeltaRows; i += 256 / LANES) {
+    const unsigned at = h0 + i + threadIdx.x / LANES, up = at / (unsigned)a.heads;
+    const int h = (int)(at - up * a.heads);
+    const int64_t t = t0 + up;
+    float sum = 0.f;
+    if (t < len && 8 * u < a.d) {
+      const char *o = la_row(a.o, b, t, h, 2) + 16 * u, *g = la_row(a.g, b, t, h, 2) + 16 * u;
+      if (la_inside(a.o, o, 8, 2) && la_inside(a.g, g, 8, 2)) {
+        const uint4 x = *reinterpret_cast<const uint4*>(o), y = *reinterpret_cast<const uint4*>(g);
+        uint64_t z = mul2(from_bf16x2(x.x), from_bf16x2(y.x));
+        z = fma2(from_bf16x2(x.y), from_bf16x2(y.y), z);
+        z = fma2(from_bf16x2(x.z), from_bf16x2(y.z), z);
+        z = fma2(from_bf16x2(x.w), from_bf16x2(y.w), z);
+        sum = pair_lo(z) + pair_hi(z);
+      }
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
+    const int64_t to = (b * a.heads + h) * a.seqlen + t;
+    if (t < len && u == 0 && in_range(to, (int64_t)a.batch * a.heads * a.seqlen)) a.delta[to] = sum;
+  }
 }
 
 }  // namespace ssscan

@@ -419,21 +419,31 @@ __global__ void __launch_bounds__(256) winattn_delta_kernel(const __grid_constan
   if (lane == 0 && in_range(at, all)) a.delta[at] = sum;
 }
 
-// The sinks' partial gradients added up, N tokens a tile.
-template <typename T, int N>
+// The sinks' partial gradients added up, N tokens a tile, VEC values of a row a thread.
+template <typename T, int N, int VEC>
 __global__ void __launch_bounds__(256) winattn_sinks_kernel(const __grid_constant__ WaArgs a) {
   const int kv_heads = a.heads / a.share;
   const int64_t bh = blockIdx.y, b = bh / kv_heads, hk = bh % kv_heads;
-  const int i = blockIdx.x * 256 + threadIdx.x;  // of [sink_tiles, 2, N, d]
-  if (i >= a.sink_tiles * 2 * N * a.d) return;
-  const int tile = i / (2 * N * a.d), rest = i % (2 * N * a.d), j = rest % (N * a.d) / a.d, c = rest % a.d;
-  const int64_t t = (int64_t)tile * N + j;
+  const unsigned i = (blockIdx.x * 256 + threadIdx.x) * VEC, tile_values = 2 * N * a.d;  // of [sink_tiles, 2, N, d]
+  if (i >= a.sink_tiles * tile_values) return;
+  const unsigned tile = i / tile_values, rest = i - tile * tile_values, row = rest / (unsigned)a.d;
+  const int64_t t = (int64_t)tile * N + row % N;
   if (t >= wa_length(a.lengths, b, a.seqlen)) return;
-  float sum = 0.f;
-  for (int piece = 0; piece <= a.pieces; ++piece) sum += a.part[wa_part<N>(a, bh, tile, piece) + rest];
-  const int64_t at = ((b * a.seqlen + t) * kv_heads + hk) * a.d + c;
-  if (in_range(at, (int64_t)a.batch * kv_heads * a.seqlen * a.d))
-    static_cast<T*>(rest < N * a.d ? a.dk : a.dv)[at] = wf_round<T>(sum);
+  const float* part = a.part + wa_part<N>(a, bh, tile, 0) + rest;
+  float sum[VEC] = {};
+  for (int piece = 0; piece <= a.pieces; ++piece, part += tile_values) {
+    if constexpr (VEC == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(part);
+      sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+    } else {
+      sum[0] += *part;
+    }
+  }
+  const int64_t at = ((b * a.seqlen + t) * kv_heads + hk) * a.d + (rest - row * a.d);
+  if (!in_range(at, VEC, (int64_t)a.batch * kv_heads * a.seqlen * a.d)) return;
+  T* to = static_cast<T*>(row < N ? a.dk : a.dv) + at;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) to[e] = wf_round<T>(sum[e]);
 }
 
 }  // namespace ssscan

@@ -185,8 +185,11 @@ ss_status wa_delta(const WaArgs& a, cudaStream_t stream) {
 template <typename T, int N>
 ss_status wa_sinks(const WaArgs& a, cudaStream_t stream) {
   if (a.pieces == 0) return SS_OK;
-  const int64_t n = (int64_t)a.sink_tiles * 2 * N * a.d;
-  winattn_sinks_kernel<T, N><<<dim3((unsigned)((n + 255) / 256), (unsigned)(a.batch * (a.heads / a.share))), 256, 0, stream>>>(a);
+  const int vec = a.d % 4 == 0 ? 4 : 1;
+  const int64_t n = (int64_t)a.sink_tiles * 2 * N * a.d / vec;
+  const dim3 grid((unsigned)((n + 255) / 256), (unsigned)(a.batch * (a.heads / a.share)));
+  if (vec == 4) winattn_sinks_kernel<T, N, 4><<<grid, 256, 0, stream>>>(a);
+  else winattn_sinks_kernel<T, N, 1><<<grid, 256, 0, stream>>>(a);
   return wa_launched();
 }
 
@@ -233,20 +236,22 @@ ss_status wa_tc_bwd(WaArgs a, const WaMaps& maps, void* dq, cudaStream_t stream)
                wa_set_smem(winattn_dq_kernel<DP, true>, DQ::kSmem);
       }) != 1)
     return SS_ERR_CUDA;
-  constexpr int LANES = DP / 8;
-  const int64_t all = (int64_t)a.batch * a.heads * a.seqlen;
-  winattn_delta16_kernel<LANES><<<(unsigned)((all + 256 / LANES - 1) / (256 / LANES)), 256, 0, stream>>>(a);
+  const int64_t delta = a.batch * (((int64_t)a.heads * a.seqlen + kDeltaRows - 1) / kDeltaRows);
+  winattn_delta16_kernel<DP / 8><<<(unsigned)delta, 256, 0, stream>>>(a);
   ss_status st = wa_launched();
   if (st != SS_OK) return st;
   const int64_t tiles = (a.seqlen + kWtRows - 1) / kWtRows;
   const int sms = device_sms() > 0 ? device_sms() : 148;
   a.out = dq;
-  a.items = (int)wa_grid(tiles, (int64_t)a.batch * a.heads);
-  const int blocks = a.items < sms ? a.items : sms;
-  winattn_dq_kernel<DP, true><<<blocks, DQ::kThreads, DQ::kSmem, stream>>>(a, maps);
+  const auto blocks = [&] { return a.items < sms ? a.items : sms; };
+  // delta of the tiles that see few keys: with windows of more than a tile the first two of each row
+  const int64_t few = a.window > kWtRows + 1 && tiles > kWtExact ? kWtExact : tiles;
+  a.items = (int)wa_grid(few, (int64_t)a.batch * a.heads);
+  winattn_dq_kernel<DP, true><<<blocks(), DQ::kThreads, DQ::kSmem, stream>>>(a, maps);
   st = wa_launched();
   if (st != SS_OK) return st;
-  winattn_dq_kernel<DP, false><<<blocks, DQ::kThreads, DQ::kSmem, stream>>>(a, maps);
+  a.items = (int)wa_grid(tiles, (int64_t)a.batch * a.heads);
+  winattn_dq_kernel<DP, false><<<blocks(), DQ::kThreads, DQ::kSmem, stream>>>(a, maps);
   st = wa_launched();
   if (st != SS_OK) return st;
   const unsigned grid = wa_grid(tiles + a.sink_tiles * a.pieces, (int64_t)a.batch * (a.heads / a.share));
