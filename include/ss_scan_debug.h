@@ -3,9 +3,10 @@
  *
  * Each setting is picked up by the NEXT ss_scan_fwd (SS_DEBUG_STEP_SIMPLE:
  * ss_scan_step; SS_DEBUG_LINATTN_...: ss_linattn_fwd or ss_linattn_bwd;
- * SS_DEBUG_WINATTN_...: ss_winattn_fwd or ss_winattn_bwd) call in the process and then cleared (ss_scan_workspace_bytes honours a pending worker count, so a
- * test can size the workspace for it).  They exist so that tests can drive the
- * load-balanced schedule and its bounded carry waits on small problems:
+ * SS_DEBUG_WINATTN_...: ss_winattn_fwd or ss_winattn_bwd) call in the process and
+ * then cleared (ss_scan_workspace_bytes honours a pending worker count, so a test can
+ * size the workspace for it).  They exist so that tests can drive the load-balanced
+ * schedule and its bounded carry waits on small problems:
  *
  *   SS_DEBUG_FORCE_WORKERS  value = number of CTAs that share the work (>= 1;
  *                           capped at the number of channel groups), so ranges
